@@ -20,6 +20,9 @@
  *   verify_mss       VerifyStochastic: multi-step speculative sampling (Algorithm 2)
  *   verify_naive     naive sampling, the comparison verifier of sec. 4.3 / 6.6
  *   kv_commit        keep only the accepted path's K/V (sec. 4.2, last paragraph)
+ *   tree_qk_norm_rope, kv8_append, kv8_read, tree_attention_kv8, kv8_commit
+ *                    head norms with rotation, and the same step over a cache
+ *                    held in 8 bits (e4m3 codes, one fp32 scale per row and head)
  *
  * Conventions shared by every call
  *  - All array arguments are DEVICE pointers owned by the caller, unless the
@@ -367,6 +370,108 @@ ts_status tree_attention_paged(void *out, const void *q, const ts_paged_kv *kv, 
 ts_status kv_commit_paged(const ts_paged_kv *kv, const int32_t *prefix_len, int32_t *new_prefix_len,
                           const int32_t *out_path, const int32_t *out_count, const ts_tree *t, int H, int d,
                           uint32_t *status, cudaStream_t stream);
+
+/*
+ * tree_qk_norm_rope -- the query and key heads of a pass made ready for the
+ * cache and the attention: every head's vector x (d values) is normed by its
+ * root mean square and rotated to its node's position, in one pass.
+ *   y = x / sqrt(mean(x^2) + eps) * weight            (norm != 0; weight NULL: 1)
+ *   angle_j = pos * inv_freq[j],  j < rot_dim / 2     (rot_dim 0: no rotation)
+ *   (a, b) -> (a cos - b sin, b cos + a sin) on the pairs (j, j + rot_dim/2),
+ *   or (2j, 2j+1) when interleaved; values from rot_dim on are not rotated.
+ * pos is t->pos of the node (tree_build with prefix_len fills it: prefix length
+ * + depth). Angles are formed in fp64, everything else in fp32; the result is
+ * rounded once, to dtype.
+ *   q [B][n_max] rows of Hq heads, q_stride elements from one node to the next
+ *   (>= Hq * d, a multiple of 16 bytes; q may be a slice of a wider projection
+ *   output); likewise k with Hk heads. q_out [B][n_max][Hq][d] and
+ *   k_out [B][n_max][Hk][d] are contiguous; q_out may be q where q_stride is
+ *   Hq * d, likewise k_out. Hk = 0 leaves k out, Hq = 0 leaves q out.
+ * Input ids v >= n_nodes[b] keep their rows of the outputs. rot_dim is a
+ * multiple of 16, at most d. Squares are summed in fp32: |x| up to 1e18.
+ * Non-finite values give non-finite heads; no status bit is set.
+ */
+typedef struct ts_qk_rope {
+    const float *inv_freq;             /* [rot_dim / 2] (NULL: rot_dim must be 0) */
+    const float *q_weight, *k_weight;  /* [d], NULL: ones */
+    float eps;                         /* >= 0 */
+    int32_t norm, rot_dim, interleaved;
+} ts_qk_rope;
+ts_status tree_qk_norm_rope(void *q_out, void *k_out, const void *q, const void *k, int Hq, int Hk, int d,
+                            long long q_stride, long long k_stride, const ts_qk_rope *rope, const ts_tree *t,
+                            ts_dtype dtype, uint32_t *status, cudaStream_t stream);
+
+/*
+ * A KV cache in 8 bits: e4m3 codes and one fp32 scale per row and head; a row's
+ * values are code * scale. Dense (block_table NULL): codes [B][H][L_max][d],
+ * scales [B][H][L_max]. Paged: codes [num_pages][H][TS_PAGE_KEYS][d], scales
+ * [num_pages][H][TS_PAGE_KEYS], rows found through block_table [B][max_pages]
+ * as in ts_paged_kv; L_max is then not read. H counts the key/value heads. Host struct of device pointers
+ * owned by the caller; codes 16-byte aligned.
+ */
+typedef struct ts_kv8 {
+    uint8_t *k, *v;
+    float *k_scale, *v_scale;
+    const int32_t *block_table;
+    int32_t B, H, d, L_max;
+    int32_t num_pages, max_pages;
+} ts_kv8;
+
+/*
+ * kv8_append -- kv_append into an 8-bit cache: node v of request b goes to row
+ * prefix_len[b] + dfs_of[v]. For each row and head, of K and of V,
+ *   scale = max(max|x| / 448, 2^-100),  code = e4m3(x * (1 / scale))
+ * with the division and the product in fp32 and the code rounded to nearest
+ * even. With rope != NULL the keys are first normed and rotated as in
+ * tree_qk_norm_rope (in fp32, not rounded in between), and the queries
+ * q [B][n_max] (Hq heads) are normed and rotated into q_out in the same pass
+ * (Hq = 0: no queries). k_new and v_new: rows of kv->H heads, k_stride / v_stride elements
+ * from one node to the next, as for tree_qk_norm_rope; dtype of q, k_new, v_new, q_out.
+ * A row with a non-finite value gets codes 0 and scale NaN, so that only nodes
+ * that attend to it see it (TS_STATUS_NONFINITE). A request whose rows pass the
+ * cache's end, or with a page id outside the table's range, is skipped, its
+ * queries included (TS_STATUS_INDEX).
+ */
+ts_status kv8_append(const ts_kv8 *kv, const void *k_new, const void *v_new, long long k_stride, long long v_stride,
+                     const ts_qk_rope *rope, void *q_out, const void *q, int Hq, long long q_stride,
+                     const int32_t *prefix_len, const ts_tree *t, ts_dtype dtype, uint32_t *status,
+                     cudaStream_t stream);
+
+/*
+ * kv8_read -- cache rows back as values: for j in 0 .. row_end[b] - row_begin[b] - 1,
+ *   k_out[b][h][j][:] = code * scale of cache row row_begin[b] + j, likewise V,
+ * rounded once to dtype. k_out, v_out [B][H][L_out][d]; rows from the count on
+ * are left as they were. row_begin NULL: 0. A request whose range is not within
+ * 0 <= row_begin <= row_end <= the cache's rows, or longer than L_out, is
+ * skipped; a row on a page outside the table's range is left out (TS_STATUS_INDEX).
+ */
+ts_status kv8_read(void *k_out, void *v_out, const ts_kv8 *kv, const int32_t *row_begin, const int32_t *row_end,
+                   int L_out, ts_dtype dtype, uint32_t *status, cudaStream_t stream);
+
+/*
+ * tree_attention_kv8 -- tree_attention over an 8-bit cache, with grouped query
+ * heads: query head h reads key/value head h / (Hq / kv->H). q, out
+ * [B][n_max][Hq][d] bf16, Hq a multiple of kv->H. The softmax and all sums are
+ * fp32. Node rows v >= n_nodes[b] are left as they were, as are all rows of a
+ * request whose keys pass the cache's end (TS_STATUS_INDEX). Rows of the cache from prefix_len[b] +
+ * n_nodes[b] on may hold anything. A page id outside [0, num_pages) reads as
+ * zeros and sets TS_STATUS_INDEX. t must be as tree_build fills it (n_nodes,
+ * perm and sub_end are read). scale <= 0 selects 1/sqrt(d). ws: at least
+ * treespec_kv8_workspace_size(...) bytes, zero-filled before its first use
+ * (treespec_workspace_init); calls leave what must be zero so. Calls that share
+ * one ws must not overlap on the GPU, two captured graphs that hold them included.
+ */
+ts_status tree_attention_kv8(void *out, const void *q, const ts_kv8 *kv, int Hq, const int32_t *prefix_len,
+                             const ts_tree *t, float scale, void *ws, size_t ws_bytes, uint32_t *status,
+                             cudaStream_t stream);
+
+/* kv_commit for an 8-bit cache: codes and scales of the accepted path's rows move. */
+ts_status kv8_commit(const ts_kv8 *kv, const int32_t *prefix_len, int32_t *new_prefix_len, const int32_t *out_path,
+                     const int32_t *out_count, const ts_tree *t, uint32_t *status, cudaStream_t stream);
+
+/* Bytes of workspace tree_attention_kv8 needs on the current device (0 for sizes it would reject);
+ * L_max = the dense cache's rows or max_pages * TS_PAGE_KEYS. */
+size_t treespec_kv8_workspace_size(int B, int Hq, int Hkv, int n_max, int d, int L_max);
 
 /* Bytes of workspace an op needs for these sizes on the current device (0 if none). */
 size_t treespec_workspace_size(ts_op op, int B, int H, int n_max, int d, int L_max, int V);

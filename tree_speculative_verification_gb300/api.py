@@ -28,7 +28,8 @@ EXPORTS = ("tree_build", "tree_build_chains", "kv_append", "tree_attention", "ve
            "kv_commit", "treespec_workspace_size", "treespec_workspace_init", "treespec_last_error",
            "treespec_version", "tree_attention_noalloc", "treespec_attention_kernel", "verify_naive",
            "tree_expand_topk", "kv_append_paged", "tree_attention_paged", "kv_commit_paged", "tree_build_append",
-           "tree_attention_append")
+           "tree_attention_append", "tree_qk_norm_rope", "kv8_append", "kv8_read", "tree_attention_kv8", "kv8_commit",
+           "treespec_kv8_workspace_size")
 #: bytes of the scratch array compiled into the library (TS_NOALLOC_SCRATCH_BYTES)
 NOALLOC_SCRATCH_BYTES = 8 << 20
 
@@ -48,6 +49,16 @@ class ts_paged_kv(C.Structure):
                 ("num_pages", C.c_int32), ("max_pages", C.c_int32)]
 
 
+class ts_qk_rope(C.Structure):
+    _fields_ = [("inv_freq", C.c_void_p), ("q_weight", C.c_void_p), ("k_weight", C.c_void_p), ("eps", C.c_float),
+                ("norm", C.c_int32), ("rot_dim", C.c_int32), ("interleaved", C.c_int32)]
+
+
+class ts_kv8(C.Structure):
+    _fields_ = [(name, C.c_void_p) for name in ("k", "v", "k_scale", "v_scale", "block_table")] + [
+        (name, C.c_int32) for name in ("B", "H", "d", "L_max", "num_pages", "max_pages")]
+
+
 _lib = None
 
 
@@ -62,7 +73,7 @@ def load_library(path: str | None = None):
                             "(python -m tree_speculative_verification_gb300.build)")
     lib = C.CDLL(path)
     P, I, F, Z = C.c_void_p, C.c_int, C.c_float, C.c_size_t
-    T = C.POINTER(ts_tree)
+    T, KV, R, S = C.POINTER(ts_tree), C.POINTER(ts_kv8), C.POINTER(ts_qk_rope), C.c_longlong
     sig = {
         "tree_build": [T, P, P, P, P, I, P, P, P],
         "tree_build_chains": [T, P, P, I, I, P, P, P, P, P, P],
@@ -80,6 +91,11 @@ def load_library(path: str | None = None):
         "kv_commit": [P, P, P, P, P, P, T, I, I, I, I, P, P],
         "treespec_workspace_init": [P, Z, P],
         "tree_attention_noalloc": [P, P, P, P, P, T, I, I, I, I, F, P, P],
+        "tree_qk_norm_rope": [P, P, P, P, I, I, I, S, S, R, T, I, P, P],
+        "kv8_append": [KV, P, P, S, S, R, P, P, I, S, P, T, I, P, P],
+        "kv8_read": [P, P, KV, P, P, I, I, P, P],
+        "tree_attention_kv8": [P, P, KV, I, P, T, F, P, Z, P, P],
+        "kv8_commit": [KV, P, P, P, P, T, P, P],
     }
     for name, args in sig.items():
         fn = getattr(lib, name)
@@ -87,6 +103,8 @@ def load_library(path: str | None = None):
         fn.restype = C.c_int
     lib.treespec_workspace_size.argtypes = [I, I, I, I, I, I, I]
     lib.treespec_workspace_size.restype = C.c_size_t
+    lib.treespec_kv8_workspace_size.argtypes = [I, I, I, I, I, I]
+    lib.treespec_kv8_workspace_size.restype = C.c_size_t
     lib.treespec_attention_kernel.argtypes = [I, I, I, I, I, I]
     lib.treespec_attention_kernel.restype = C.c_char_p
     lib.treespec_last_error.restype = C.c_char_p
@@ -239,7 +257,8 @@ def tree_attention_append(out, q, k_cache, v_cache, k_new, v_new, prefix_len, tr
     _check(lib.tree_attention_append(_ptr(out), _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(k_new), _ptr(v_new),
                                      _ptr(_i32(prefix_len, "prefix_len")), tree.c, H, d, L_max, _dtype(k_cache),
                                      float(scale), _ptr(ws), nbytes, _ptr(status), _stream(stream)),
-           "tree_attention_append")
+           "tree_attention_append", "tree_qk_norm_rope", "kv8_append", "kv8_read", "tree_attention_kv8", "kv8_commit",
+           "treespec_kv8_workspace_size")
 
 
 def tree_attention_noalloc(out, q, k_cache, v_cache, prefix_len, tree: Tree, scale: float = 0.0, status=None,
@@ -336,6 +355,213 @@ def kv_commit_paged(kv: PagedKV, prefix_len, new_prefix_len, out_path, out_count
                                           _ptr(_i32(new_prefix_len, "new_prefix_len")), _ptr(out_path),
                                           _ptr(out_count), tree.c, kv.H, kv.d, _ptr(status), _stream(stream)),
            "kv_commit_paged")
+
+
+# -- head norms with rotation, and the 8-bit KV cache -----------------------------
+def _need(cond, msg):
+    if not cond:
+        raise TreespecError(msg)
+
+
+def _int_array(t, n, name, device):
+    """Pointer of an int32 tensor of at least n entries on `device`."""
+    _need(t.dtype == torch.int32 and t.numel() >= n and t.is_contiguous() and t.device == device,
+          f"{name} must be a contiguous int32 tensor of {n} entries on {device}")
+    return t.data_ptr()
+
+
+def _status_ptr(status, device):
+    return None if status is None else _int_array(status, 1, "status", device)
+
+
+def _node_rows(t, tree, H, d, name, dtype, device):
+    """(pointer, elements from one node to the next) of node rows [B][n_max][H][d]: heads contiguous, nodes and
+    requests a constant stride apart (a slice of a wider projection output)."""
+    _need(t.dtype == dtype and t.device == device, f"{name} must be {dtype} on {device}")
+    B, n = tree.B, tree.n_max
+    _need(tuple(t.shape) == (B, n, H, d), f"{name} has shape {tuple(t.shape)}, not {(B, n, H, d)}")
+    sb, sn, sh, sd = t.stride()
+    if n == 1:
+        sn = sb if B > 1 else H * d
+    _need(sd == 1 and (H == 1 or sh == d) and (B == 1 or sb == n * sn),
+          f"{name}: heads must be contiguous, nodes and requests a constant stride apart")
+    return t.data_ptr(), sn
+
+
+def _out_rows(t, tree, H, d, name, dtype, device):
+    _need(t.dtype == dtype and t.device == device and tuple(t.shape) == (tree.B, tree.n_max, H, d)
+          and t.is_contiguous(), f"{name} must be a contiguous {dtype} tensor {(tree.B, tree.n_max, H, d)} on {device}")
+    return t.data_ptr()
+
+
+def _run(fn, what, device, stream, *args):
+    """Call an entry point on the current stream of the tensors' device (or the given one)."""
+    if stream is None and device.index == torch.cuda.current_device():
+        _check(fn(*args, torch.cuda.current_stream(device).cuda_stream), what)
+        return
+    with torch.cuda.device(device):
+        _check(fn(*args, (stream or torch.cuda.current_stream(device)).cuda_stream), what)
+
+
+class QKRope:
+    """Norm and rotation of query and key heads (the ts_qk_rope of the C ABI). inv_freq: fp32 [rot_dim / 2] (None: no
+    rotation); q_weight, k_weight: fp32 [d] norm weights (None: ones); norm=False rotates only."""
+
+    def __init__(self, inv_freq=None, q_weight=None, k_weight=None, eps: float = 1e-6, norm: bool = True,
+                 interleaved: bool = False):
+        given = [x for x in (inv_freq, q_weight, k_weight) if x is not None]
+        for x in given:
+            _need(x.dtype == torch.float32 and x.is_contiguous() and x.dim() == 1 and x.is_cuda
+                  and x.device == given[0].device, "inv_freq and weights must be contiguous fp32 vectors on one CUDA device")
+        self.inv_freq, self.q_weight, self.k_weight = inv_freq, q_weight, k_weight
+        self.device = given[0].device if given else None
+        self.rot_dim = 0 if inv_freq is None else 2 * inv_freq.numel()
+        p = lambda x: None if x is None else x.data_ptr()
+        self._c = ts_qk_rope(p(inv_freq), p(q_weight), p(k_weight), float(eps), int(bool(norm)), self.rot_dim,
+                             int(bool(interleaved)))
+        self._ref = C.byref(self._c)
+
+    def _for(self, d, device):
+        _need(self.device is None or self.device == device, f"the rotation's tensors are on {self.device}, not {device}")
+        for w in (self.q_weight, self.k_weight):
+            _need(w is None or w.numel() == d, f"norm weights must have head_dim {d} entries")
+        return self._ref
+
+    @staticmethod
+    def frequencies(rot_dim: int, theta: float = 10000.0, device="cuda"):
+        """theta^(-2j / rot_dim), j = 0 .. rot_dim / 2 - 1, in fp32."""
+        return (theta ** (-torch.arange(0, rot_dim, 2, dtype=torch.float64) / rot_dim)).float().to(device)
+
+
+def tree_qk_norm_rope(q_out, k_out, q, k, rope: QKRope, tree: Tree, status=None, stream=None):
+    """Norm every head of q and k [B][n_max][H][d] and rotate it to its node's position (tree.pos); q or k may be
+    None with its output. Outputs are contiguous, and may be the inputs where those are."""
+    x = q if q is not None else k
+    _need(x is not None and x.is_cuda and x.dim() == 4, "q or k [B][n_max][H][d] on a CUDA device is needed")
+    dev, d, dt = x.device, x.shape[3], _dtype(x)
+    _need(tree.n_nodes.device == dev, f"the tree is on {tree.n_nodes.device}, not {dev}")
+    qp = kp = qo = ko = None
+    Hq = Hk = qs = ks = 0
+    if q is not None:
+        Hq = q.shape[2]
+        (qp, qs), qo = _node_rows(q, tree, Hq, d, "q", x.dtype, dev), _out_rows(q_out, tree, Hq, d, "q_out", x.dtype, dev)
+    if k is not None:
+        Hk = k.shape[2]
+        (kp, ks), ko = _node_rows(k, tree, Hk, d, "k", x.dtype, dev), _out_rows(k_out, tree, Hk, d, "k_out", x.dtype, dev)
+    _run(load_library().tree_qk_norm_rope, "tree_qk_norm_rope", dev, stream, qo, ko, qp, kp, Hq, Hk, d, qs, ks,
+         rope._for(d, dev), tree.c, dt, _status_ptr(status, dev))
+
+
+class KV8:
+    """An 8-bit KV cache (the ts_kv8 of the C ABI): e4m3 codes and one fp32 scale per row and head. Dense: k, v
+    [B][H][L_max][d] torch.float8_e4m3fn, k_scale, v_scale [B][H][L_max]; with block_table [B][max_pages] int32 paged:
+    k, v [num_pages][H][PAGE_KEYS][d], scales [num_pages][H][PAGE_KEYS]."""
+
+    def __init__(self, k, v, k_scale, v_scale, block_table=None):
+        _need(k.dim() == 4 and k.dtype == torch.float8_e4m3fn and v.dtype == k.dtype and v.shape == k.shape,
+              "k and v must be two float8_e4m3fn tensors of one shape [B or pages][H][rows][d]")
+        _need(k_scale.dtype == torch.float32 and v_scale.dtype == torch.float32 and k_scale.shape == k.shape[:3]
+              and v_scale.shape == k.shape[:3], "scales must be fp32 of the codes' shape without head_dim")
+        for x in (k, v, k_scale, v_scale):
+            _need(x.is_cuda and x.is_contiguous() and x.device == k.device,
+                  "cache tensors must be contiguous on one CUDA device")
+        self.k, self.v, self.k_scale, self.v_scale, self.block_table = k, v, k_scale, v_scale, block_table
+        self.H, self.d, self.device = k.shape[1], k.shape[3], k.device
+        pages = 0
+        if block_table is not None:
+            _need(k.shape[2] == PAGE_KEYS, f"a page holds {PAGE_KEYS} keys")
+            _need(block_table.dim() == 2, "block_table must be [B][max_pages]")
+            _int_array(block_table, 1, "block_table", k.device)
+            self.B, pages = block_table.shape
+            self.L_max = pages * PAGE_KEYS
+        else:
+            self.B, self.L_max = k.shape[0], k.shape[2]
+        self._c = ts_kv8(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
+                         None if block_table is None else block_table.data_ptr(), self.B, self.H, self.d,
+                         self.L_max if block_table is None else 0, 0 if block_table is None else k.shape[0], pages)
+        self._ref = C.byref(self._c)
+
+    @classmethod
+    def dense(cls, B: int, H: int, L_max: int, d: int, device="cuda"):
+        """A dense cache of zeros."""
+        z = lambda *s, t=torch.float8_e4m3fn: torch.zeros(s, dtype=t, device=device)
+        return cls(z(B, H, L_max, d), z(B, H, L_max, d), z(B, H, L_max, t=torch.float32), z(B, H, L_max, t=torch.float32))
+
+    @classmethod
+    def paged(cls, num_pages: int, H: int, d: int, block_table):
+        """A paged cache of zeros on the block table's device."""
+        z = lambda *s, t=torch.float8_e4m3fn: torch.zeros(s, dtype=t, device=block_table.device)
+        s = (num_pages, H, PAGE_KEYS)
+        return cls(z(*s, d), z(*s, d), z(*s, t=torch.float32), z(*s, t=torch.float32), block_table)
+
+    def _with(self, tree: Tree):
+        _need(tree.B == self.B, f"cache of {self.B} requests, tree of {tree.B}")
+        _need(tree.n_nodes.device == self.device, f"the tree is on {tree.n_nodes.device}, the cache on {self.device}")
+        return self._ref
+
+
+def kv8_append(kv: KV8, k_new, v_new, prefix_len, tree: Tree, rope: QKRope | None = None, q=None, q_out=None,
+               status=None, stream=None):
+    """Quantise the pass's K/V [B][n_max][H][d] into the cache rows P + dfs; with rope the keys are normed and rotated
+    on the way, and the queries q, if given, into q_out."""
+    ref, dev, d = kv._with(tree), kv.device, kv.d
+    dt = _dtype(k_new)
+    kp, ks = _node_rows(k_new, tree, kv.H, d, "k_new", k_new.dtype, dev)
+    vp, vs = _node_rows(v_new, tree, kv.H, d, "v_new", k_new.dtype, dev)
+    qp = qo = r = None
+    Hq = qs = 0
+    if q is not None:
+        _need(rope is not None, "queries are only taken with rope")
+        Hq = q.shape[2]
+        qp, qs = _node_rows(q, tree, Hq, d, "q", k_new.dtype, dev)
+        _need(q_out is not None, "q_out is needed with q")
+        qo = _out_rows(q_out, tree, Hq, d, "q_out", k_new.dtype, dev)
+    if rope is not None:
+        r = rope._for(d, dev)
+    _run(load_library().kv8_append, "kv8_append", dev, stream, ref, kp, vp, ks, vs, r, qo, qp, Hq, qs,
+         _int_array(prefix_len, tree.B, "prefix_len", dev), tree.c, dt, _status_ptr(status, dev))
+
+
+def kv8_read(k_out, v_out, kv: KV8, row_end, row_begin=None, status=None, stream=None):
+    """Cache rows row_begin[b] .. row_end[b] - 1 as values into rows 0 .. of k_out, v_out [B][H][L_out][d] (bfloat16
+    or float32)."""
+    dev = kv.device
+    shape = (kv.B, kv.H, k_out.shape[2] if k_out.dim() == 4 else 0, kv.d)
+    for x in (k_out, v_out):
+        _need(tuple(x.shape) == shape and x.dtype == k_out.dtype and x.device == dev and x.is_contiguous(),
+              f"k_out and v_out must be contiguous tensors {shape} of one dtype on {dev}")
+    begin = None if row_begin is None else _int_array(row_begin, kv.B, "row_begin", dev)
+    _run(load_library().kv8_read, "kv8_read", dev, stream, k_out.data_ptr(), v_out.data_ptr(), kv._ref, begin,
+         _int_array(row_end, kv.B, "row_end", dev), shape[2], _dtype(k_out), _status_ptr(status, dev))
+
+
+def kv8_workspace(B: int, Hq: int, Hkv: int, n_max: int, d: int, L_max: int, device="cuda"):
+    """A zero-filled workspace of the size tree_attention_kv8 needs (L_max: KV8.L_max)."""
+    with torch.cuda.device(device):
+        need = int(load_library().treespec_kv8_workspace_size(B, Hq, Hkv, n_max, d, L_max))
+    return torch.zeros(max(256, need), dtype=torch.uint8, device=device)
+
+
+def tree_attention_kv8(out, q, kv: KV8, prefix_len, tree: Tree, scale: float = 0.0, ws=None, status=None, stream=None):
+    """tree_attention over an 8-bit cache; q, out [B][n_max][Hq][d] bfloat16, Hq a multiple of kv.H."""
+    ref, dev = kv._with(tree), kv.device
+    _need(q.dim() == 4, "q must be [B][n_max][Hq][d]")
+    Hq = q.shape[2]
+    op = _out_rows(out, tree, Hq, kv.d, "out", torch.bfloat16, dev)
+    qp = _out_rows(q, tree, Hq, kv.d, "q", torch.bfloat16, dev)
+    _need(ws is not None and ws.device == dev and ws.is_contiguous(), f"a workspace (kv8_workspace) on {dev} is needed")
+    _run(load_library().tree_attention_kv8, "tree_attention_kv8", dev, stream, op, qp, ref, Hq,
+         _int_array(prefix_len, tree.B, "prefix_len", dev), tree.c, float(scale), ws.data_ptr(),
+         ws.numel() * ws.element_size(), _status_ptr(status, dev))
+
+
+def kv8_commit(kv: KV8, prefix_len, new_prefix_len, out_path, out_count, tree: Tree, status=None, stream=None):
+    """kv_commit over an 8-bit cache."""
+    ref, dev, B = kv._with(tree), kv.device, tree.B
+    _run(load_library().kv8_commit, "kv8_commit", dev, stream, ref, _int_array(prefix_len, B, "prefix_len", dev),
+         _int_array(new_prefix_len, B, "new_prefix_len", dev),
+         _int_array(out_path, B * (tree.n_max + 1), "out_path", dev), _int_array(out_count, B, "out_count", dev),
+         tree.c, _status_ptr(status, dev))
 
 
 def version() -> str:
