@@ -165,6 +165,8 @@ ts_status tree_attention_kv8(void *out, const void *q, const ts_kv8 *kv, int Hq,
         return set_error(TS_ERR_INVALID_ARG, "%s: q and out must be 16-byte aligned", who);
     if (Hq < 1 || Hq > 65535 || Hq % kv->H != 0)
         return set_error(TS_ERR_INVALID_ARG, "%s: Hq=%d is not a multiple of the cache's H=%d", who, Hq, kv->H);
+    if ((long long)t->B * Hq * t->n_max >= (1LL << 31))
+        return set_error(TS_ERR_INVALID_ARG, "%s: %lld query rows (2^31 or more)", who, (long long)t->B * Hq * t->n_max);
     if (!(scale > 0.f)) scale = 1.0f / sqrtf((float)kv->d);
     if (!(scale < INFINITY)) return set_error(TS_ERR_INVALID_ARG, "%s: scale is not finite", who);
     const size_t need = ts::kv8_attention_ws_bytes(t->B, Hq, kv->H, t->n_max, kv->d, ts::kv8_rows(*kv));
@@ -192,7 +194,7 @@ ts_status kv8_commit(const ts_kv8 *kv, const int32_t *prefix_len, int32_t *new_p
 
 size_t treespec_kv8_workspace_size(int B, int Hq, int Hkv, int n_max, int d, int L_max) {
     if (B < 1 || B > 65535 || Hkv < 1 || Hkv > 65535 || Hq < 1 || Hq > 65535 || Hq % Hkv != 0 || n_max < 1 ||
-        n_max > TS_MAX_NODES || (d != 64 && d != 128) || L_max < n_max)
+        n_max > TS_MAX_NODES || (d != 64 && d != 128) || L_max < n_max || (long long)B * Hq * n_max >= (1LL << 31))
         return 0;
     return ts::kv8_attention_ws_bytes(B, Hq, Hkv, n_max, d, L_max);
 }

@@ -1,106 +1,1020 @@
-// attn_kv8.cu -- tree attention over the 8-bit KV cache.
+// attn_kv8.cu -- tree attention over the 8-bit KV cache, on tcgen05.
 //
-// TreeAttention(u) = Attention(S_u) (SpecInfer, arXiv 2305.09781, Def. 4.1) with
-// keys and values code * scale, and grouped query heads.
+// TreeAttention(u) = Attention(S_u) for every node u of the token tree
+// (SpecInfer, arXiv 2305.09781, Def. 4.1, Eq. 1-4; the mask of sec. 4.2), with
+// K and V held as e4m3 codes times one fp32 scale per (row, head), and G query
+// heads to a key/value head. The R = n * G query rows of a (request, key/value
+// head) share its keys; they are taken RP at a time (RP = 16, 32, 48 or 64).
+//
+// The cache's codes go to the tensor cores as they are. Both products are
+// transposed, so that keys, then value dims, are the 128 rows of the MMA and a
+// tile costs in proportion to the query rows there are:
+//   S^T [128 keys x 2 RP]  = K [128 x d] * [Qh | Ql]^T        (e4m3 * e4m3)
+//   O^T [d x 3 RP]        += V^T [d x 128 keys] * [P0 | P1 | P2]^T (e4m3 * e5m2)
+// What is not in 8 bits is split into several 8-bit numbers, each a column
+// block of its own, so K and V are read from shared memory once a tile:
+//   a query row, scaled by a power of two to a largest value in [128, 256), is
+//   qh + ql with qh = e4m3(q), ql = e4m3(q - qh): bf16's eight bits exactly for
+//   values down to 2^-10 of the row's largest, 2^-18 of it absolutely below;
+//   a probability p (held as 2^11 at the running maximum) is rounded to fp16,
+//   whose upper byte is an e5m2 number: p0 = upper byte of p, p1 = of p - p0,
+//   p2 = of the rest, rounded. Nine bits, down to 2^-28 of the largest (an e4m3
+//   pair would lose weights below 2^-19, which a long cache with one dominant
+//   key has by the thousand).
+// Softmax: S * key scale * query scale is the exponent; the value scale times a
+// common reference is multiplied into p before it is split. Sums, maxima, O: fp32.
+//
+// Bound by HBM: (P + n) * 2 * (d + 4) bytes a (request, head), and a tile of 128
+// keys (32 KB at d = 128) has to pass an SM in 0.73 us at the measured copy peak.
+//
+// One CTA per SM takes units (request, head, RP query rows, range of tiles) from
+// a queue in the workspace, longest first; ranges are cut only as far as the
+// launch needs to fill the SMs, the last CTA of a cut item joining the parts.
+//   warp 0      TMA producer and queue: K and V tiles into a ring of stages; the
+//               tile's scales and, for tree keys, subtree ends by cp.async on the
+//               same mbarrier
+//   warp 1      MMA issuer: S(g + 1) is issued before O += P(g) V(g)
+//   warps 2-9   softmax: two groups of four warps take half the columns each, lane
+//               = key. The running maximum of a column is raised only when a score
+//               passes it by 2^4 (one vote per tile and group), so the common tile
+//               has no reduction over keys. Tree node j is seen by the rows of its
+//               subtree, one interval of rows.
+//   warps 10-11 the next unit's query rows, split, into the other Q buffer
+// Every wait is bounded; a wait that gives up sets TS_STATUS_TIMEOUT, the others
+// follow by their own limits or the group's vote, and TMEM is freed.
+#include <cuda.h>
 #include <math.h>
 
+#include "attn_common.cuh"
 #include "kv8.cuh"
 
 namespace ts {
 namespace {
 
+// ---------------------------------------------------------------- PTX ---
+__device__ __forceinline__ uint64_t smem_desc8(uint32_t addr, uint32_t lbo, uint32_t sbo, uint64_t layout) {
+    return (uint64_t)((addr >> 4) & 0x3FFFu) | (uint64_t)((lbo >> 4) & 0x3FFFu) << 16 |
+           (uint64_t)((sbo >> 4) & 0x3FFFu) << 32 | (uint64_t)1 << 46 | layout << 61;
+}
+constexpr uint64_t kSwz128 = 2, kSwz64 = 4;
+
+// kind::f8f6f4 instruction descriptor: fp32 accumulate, A e4m3, B e4m3 or e5m2.
+constexpr uint32_t idesc_f8(int M, int N, bool b_e5m2, bool a_mn, bool b_mn) {
+    return (1u << 4) | ((b_e5m2 ? 1u : 0u) << 10) | ((a_mn ? 1u : 0u) << 15) | ((b_mn ? 1u : 0u) << 16) |
+           ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+
+__device__ __forceinline__ void tc_mma_f8(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accum) {
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n"
+        ::"r"(d_tmem), "l"(a), "l"(b), "r"(idesc), "r"(accum)
+        : "memory");
+}
+
+__device__ __forceinline__ void tc_ld8(uint32_t taddr, float *v) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7])
+                 : "r"(taddr));
+}
+__device__ __forceinline__ void tc_st8(uint32_t taddr, const float *v) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "f"(v[0]),
+                 "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
+                 : "memory");
+}
+
+// Maximum over the warp, NaN left out.
+__device__ __forceinline__ float warp_max(float v) {
+    float r;
+    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+    return r;
+}
+
+// Barrier of `threads` threads that also tells whether any of them votes.
+__device__ __forceinline__ bool bar_any(int id, int threads, bool vote) {
+    uint32_t r;
+    asm volatile(
+        "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n barrier.cta.red.or.pred q, %2, %3, p;\n selp.u32 %0, 1, 0, q;\n}\n"
+        : "=r"(r)
+        : "r"((uint32_t)vote), "r"(id), "r"(threads)
+        : "memory");
+    return r != 0;
+}
+__device__ __forceinline__ void bar_sync(int id, int threads) {
+    asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+
+// 4-byte asynchronous copy to shared memory; zeros where !valid.
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void *src, bool valid) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(valid ? 4 : 0) : "memory");
+}
+// One arrival of this thread once its copies so far have landed.
+__device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
+
+__device__ __forceinline__ uint32_t half2_of(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+__device__ __forceinline__ uint32_t hsub2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
+// ------------------------------------------------------------ arguments ---
 struct Attn8Args {
     __nv_bfloat16 *out;
     const __nv_bfloat16 *q;
-    const uint8_t *k8, *v8;
     const float *k_scale, *v_scale;
     const int32_t *prefix_len;
     ts_tree t;
-    int Hq, H, G, rows;
+    int Hq, H, G, rows;   // rows: L_max of the cache
     float scale_log2;
     PagedArgs pg;
     uint32_t *status;
+    unsigned *queue;      // [0] next unit, [1] CTAs finished
+    unsigned *joins;      // [slots][2] parts done, by the item's first slot and column group
+    float2 *part_ml;      // [slots][RP] (maximum, sum)
+    float *part_o;        // [slots][RP][D]
+    int slots;
 };
 
-constexpr int kWarps = 8;
+constexpr int kTileKeys = 128;
+constexpr int kReqCache = 256;     // requests planned in shared memory
+constexpr int kMaxCuts = 32;       // parts of one item (a lane each when they are joined)
+constexpr int kMinCut = 3;         // tiles of a part at least
+constexpr int kCutsPerSm = 2;      // units per SM that cutting aims at
+constexpr int kRing = 4;           // published units
 
-// A warp per (node, query head): 32 keys at a time, lane j the score of key j,
-// then the lanes share the value dims. Simple, and right for every size.
-template <int D>
-__global__ void __launch_bounds__(kWarps * 32) k_attn_kv8_rows(Attn8Args a) {
-    constexpr int DPL = D / 32;
-    __shared__ float q_s[kWarps][D];
-    const int b = blockIdx.z, h = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+template <int D_, int RP_>
+struct Cfg8 {
+    static constexpr int D = D_, RP = RP_, CG = RP / 2;
+    static constexpr int SM_WARPS = 8, THREADS = 32 * (2 + SM_WARPS + 2);
+    static constexpr int OP_BYTES = kTileKeys * D;             // codes of one operand tile
+    static constexpr int STAGE_BYTES = 2 * OP_BYTES;
+    static constexpr int P_ATOMS = (3 * RP + 63) / 64, P_ATOM = kTileKeys * 64, P_BYTES = P_ATOMS * P_ATOM;
+    static constexpr int Q_BYTES = 2 * RP * D;
+    static constexpr int SIDE = 3 * kTileKeys * 4;             // a stage's key scales, value scales, subtree ends
+    // fixed part, behind the stages
+    static constexpr int FIX_P = 0, FIX_Q = FIX_P + P_BYTES, FIX_MX = FIX_Q + 2 * Q_BYTES;
+    static constexpr int FIX_LS = FIX_MX + 2 * 4 * 32 * 4;     // column maxima [2 groups][4 warps][32]
+    static constexpr int FIX_F = FIX_LS + 4 * 64 * 4;          // column sums [4 warps][64], then factors [64]
+    static constexpr int FIX_QS = FIX_F + 64 * 4;              // query scales [kRing][64], output rows [kRing][64]
+    static constexpr int FIX_QROW = FIX_QS + kRing * 64 * 4;
+    static constexpr int FIX_REQ = FIX_QROW + kRing * 64 * 4;  // (n, P) by request, then order, first unit, first slot
+    static constexpr int FIX_ORDER = FIX_REQ + kReqCache * 8, FIX_UNIT = FIX_ORDER + kReqCache * 4;
+    static constexpr int FIX_SLOT = FIX_UNIT + kReqCache * 4;
+    static constexpr int FIX_INFO = FIX_SLOT + kReqCache * 4;  // units [kRing][12]
+    static constexpr int FIX_MISC = FIX_INFO + kRing * 12 * 4; // 0 TMEM base, 1 timeout, 2 units, 3 tiles a part, 4-5 last
+    static constexpr int FIX_BAR = FIX_MISC + 64;
+    static constexpr int FIX_END = FIX_BAR + 64 * 8;
+    static constexpr int LIMIT = 232448 - 2 * 1024;            // the base and the fixed part are 1024-byte aligned
+    static constexpr int FIT = (LIMIT - FIX_END) / (STAGE_BYTES + SIDE);
+    static constexpr int STAGES = FIT < 8 ? FIT : 8;
+    static constexpr int OFF_SIDE = STAGES * STAGE_BYTES;
+    static constexpr int OFF_FIX = (OFF_SIDE + STAGES * SIDE + 1023) / 1024 * 1024;
+    static constexpr int SMEM = OFF_FIX + FIX_END + 1024;
+    static constexpr uint32_t S_COL = 0, O_COL = 4 * RP;       // two score buffers of 2 RP columns, O of 3 RP
+    static constexpr uint32_t TMEM_COLS = 7 * RP <= 128 ? 128 : 7 * RP <= 256 ? 256 : 512;
+    static_assert(STAGES >= 3 && SMEM <= 232448 && STAGE_BYTES % 1024 == 0 && FIX_Q % 1024 == 0 && Q_BYTES % 1024 == 0,
+                  "shared memory and the alignment of swizzled tiles");
+};
+
+struct Unit8 {
+    int b, h, row0, n, P, j0, j1, parts, part, slot;   // tiles [j0, j1); slot: of the item's first part
+};
+
+template <int N>
+__device__ __forceinline__ void reduce_scatter(float *v, int lane) {
+    // sums of N columns over the warp: column lane / (32 / N) ends in v[0]
+#pragma unroll
+    for (int w = 16, n = N; w; w >>= 1) {
+        if (n > 1) {
+            n >>= 1;
+#pragma unroll
+            for (int i = 0; i < n; ++i) {
+                const float keep = lane & w ? v[i + n] : v[i], send = lane & w ? v[i] : v[i + n];
+                v[i] = keep + __shfl_xor_sync(~0u, send, w);
+            }
+        } else {
+            v[0] += __shfl_xor_sync(~0u, v[0], w);
+        }
+    }
+}
+
+template <int D, int RP>
+__global__ void __launch_bounds__(Cfg8<D, RP>::THREADS, 1)
+    k_attn_kv8(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v, Attn8Args a) {
+    using C = Cfg8<D, RP>;
+    extern __shared__ unsigned char smem_raw[];
+    unsigned char *sm = (unsigned char *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+    unsigned char *fix = sm + C::OFF_FIX;
+    const uint32_t sm_base = smem_u32(sm), fix_base = sm_base + C::OFF_FIX;
+    volatile int *misc = (volatile int *)(fix + C::FIX_MISC);
+    int2 *req_s = (int2 *)(fix + C::FIX_REQ);
+    int *order_s = (int *)(fix + C::FIX_ORDER), *unit_s = (int *)(fix + C::FIX_UNIT), *slot_s = (int *)(fix + C::FIX_SLOT);
+    volatile int *info_s = (volatile int *)(fix + C::FIX_INFO);
+    const float *qs_s = (const float *)(fix + C::FIX_QS);
+    const int *qrow_s = (const int *)(fix + C::FIX_QROW);
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int B = a.t.B, n_max = a.t.n_max;
     pdl_wait();
     pdl_trigger();
-    const int n = a.t.n_nodes[b], P = a.prefix_len[b];
-    const int r = blockIdx.x * kWarps + warp, i = r / a.G, hq = h * a.G + r % a.G;
-    if (n <= 0 || i >= n) return;
-    if (n > a.t.n_max || P < 0 || P > a.rows - n) {
-        if (lane == 0 && h == 0 && r == 0) flag(a.status, TS_STATUS_INDEX);
-        return;
+
+    const uint32_t full = fix_base + C::FIX_BAR, empty = full + 8 * C::STAGES, sfull = empty + 8 * C::STAGES;
+    const uint32_t pfull = sfull + 16, pvdone = pfull + 8, qready = pvdone + 8, qfree = qready + 16, ofree = qfree + 16;
+    const uint32_t fin = ofree + 8, iready = fin + 8, ifree = iready + 8 * kRing;
+
+    if (warp == 0) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32((void *)misc)),
+                     "r"(C::TMEM_COLS)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
-    const int v = a.t.perm[(size_t)b * a.t.n_max + i];
-    if (v < 0 || v >= a.t.n_max) return;
-    const size_t at = (((size_t)b * a.t.n_max + v) * a.Hq + hq) * D;
-    for (int e = lane; e < D; e += 32) q_s[warp][e] = __bfloat162float(a.q[at + e]) * a.scale_log2;
-    __syncwarp();
-    float m = -INFINITY, l = 0.f, o[DPL] = {};
-    const int L = P + n;
-    for (int j0 = 0; j0 < L; j0 += 32) {
-        const int j = j0 + lane;
-        bool see = j < P;
-        if (!see && j < L) see = j - P <= i && i < a.t.sub_end[(size_t)b * a.t.n_max + j - P];
-        long long row = -1;
-        if (j < L) row = cache_row(a.pg, b, h, a.H, a.rows, j);
-        if (j < L && row < 0) flag(a.status, TS_STATUS_INDEX);
-        float s = 0.f;
-        if (row >= 0 && see) {
-            const uint16_t *k = reinterpret_cast<const uint16_t *>(a.k8 + (size_t)row * D);
-            for (int e = 0; e < D / 2; ++e) {
-                const float2 f = fp8x2_to_float2(k[e]);
-                s = fmaf(q_s[warp][2 * e], f.x, s);
-                s = fmaf(q_s[warp][2 * e + 1], f.y, s);
-            }
-            s *= a.k_scale[row];
+    if (tid == 32) {
+        for (int s = 0; s < C::STAGES; ++s) {
+            mbar_init(full + 8 * s, 1 + 32);   // the TMA's bytes, and the producer's lanes' copies
+            mbar_init(empty + 8 * s, 1);
         }
-        if (!see) s = -INFINITY;
-        float mx = s;
-        for (int o2 = 16; o2; o2 >>= 1) mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, o2));
-        const float mn = fmaxf(m, mx), alpha = mn > -INFINITY ? exp2f(m - mn) : 1.f;
-        const float p = see ? exp2f(s - mn) : 0.f;
-        m = mn;
-        l = l * alpha + p;
-        for (int e = 0; e < DPL; ++e) o[e] *= alpha;
-        const float pv = see && row >= 0 ? p * a.v_scale[row] : 0.f;
-        for (int k = 0; k < 32 && j0 + k < L; ++k) {
-            const long long rk = __shfl_sync(~0u, row, k);
-            const float pk = __shfl_sync(~0u, pv, k);
-            const bool sk = __shfl_sync(~0u, (int)see, k);
-            if (rk < 0 || !sk) continue;
-            const uint8_t *vp = a.v8 + (size_t)rk * D + lane * DPL;
-            for (int e = 0; e < DPL; e += 2) {
-                const float2 f = fp8x2_to_float2(*reinterpret_cast<const uint16_t *>(vp + e));
-                o[e] = fmaf(pk, f.x, o[e]);
-                o[e + 1] = fmaf(pk, f.y, o[e + 1]);
+        for (int x = 0; x < 2; ++x) {
+            mbar_init(sfull + 8 * x, 1);
+            mbar_init(qready + 8 * x, 2);
+            mbar_init(qfree + 8 * x, 1);
+        }
+        mbar_init(pfull, C::SM_WARPS);
+        mbar_init(pvdone, 1);
+        mbar_init(ofree, C::SM_WARPS);
+        mbar_init(fin, 1);
+        for (int r = 0; r < kRing; ++r) {
+            mbar_init(iready + 8 * r, 1);
+            mbar_init(ifree + 8 * r, 1 + C::SM_WARPS + 2);
+        }
+        misc[1] = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+
+    // ---- the plan, the same in every CTA: how many tiles a part has, and each
+    // request's first unit and first slot of the workspace
+    const bool planned = B <= kReqCache;
+    const int blocks_max = (n_max * a.G + RP - 1) / RP;
+    auto blocks_of = [&](int n) { return (n * a.G + RP - 1) / RP; };
+    auto tiles_of = [&](int n, int P) -> int {   // 0 for a request that is empty or does not fit
+        return n > 0 && n <= n_max && P >= 0 && P <= a.rows - n ? (P + n + kTileKeys - 1) / kTileKeys : 0;
+    };
+    auto parts_of = [&](int tiles, int per) {
+        const int p = (tiles + per - 1) / per;
+        return p < kMaxCuts ? p : kMaxCuts;
+    };
+    for (int b = tid; planned && b < B; b += C::THREADS) req_s[b] = make_int2(a.t.n_nodes[b], a.prefix_len[b]);
+    __syncthreads();
+    if (planned && warp == 0) {
+        long long work = 0;   // tiles over all items
+        for (int b = lane; b < B; b += 32) work += (long long)tiles_of(req_s[b].x, req_s[b].y) * blocks_of(req_s[b].x);
+#pragma unroll
+        for (int o = 16; o; o >>= 1) work += __shfl_xor_sync(~0u, work, o);
+        const long long aim = (long long)gridDim.x * kCutsPerSm;
+        long long per = (work * a.H + aim - 1) / aim;
+        if (per < kMinCut) per = kMinCut;
+        if (per > (1 << 24)) per = 1 << 24;
+        if (lane == 0) misc[3] = (int)per;
+    }
+    __syncthreads();
+    const int per = planned ? misc[3] : 1 << 24;
+    for (int b = tid; planned && b < B; b += C::THREADS) {   // rank by the length of the request's parts
+        auto key = [&](int o) {
+            const int tl = tiles_of(req_s[o].x, req_s[o].y);
+            return tl ? (tl + parts_of(tl, per) - 1) / parts_of(tl, per) : 0;
+        };
+        const int mine = key(b);
+        int rank = 0;
+        for (int o = 0; o < B; ++o) {
+            const int ko = key(o);
+            rank += ko > mine || (ko == mine && o < b);
+        }
+        order_s[rank] = b;
+    }
+    __syncthreads();
+    if (planned && warp == 0) {   // exclusive sums of units and of slots, in that order
+        int units = 0, slots = 0;
+        for (int r0 = 0; r0 < B; r0 += 32) {
+            int u = 0, s = 0;
+            if (r0 + lane < B) {
+                const int2 rq = req_s[order_s[r0 + lane]];
+                const int tl = tiles_of(rq.x, rq.y);
+                if (tl) {
+                    const int pt = parts_of(tl, per);
+                    u = a.H * blocks_of(rq.x) * pt;
+                    s = pt > 1 ? u : 0;
+                }
             }
+            int cu = u, cs = s;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int tu = __shfl_up_sync(~0u, cu, o), ts_ = __shfl_up_sync(~0u, cs, o);
+                if (lane >= o) {
+                    cu += tu;
+                    cs += ts_;
+                }
+            }
+            if (r0 + lane < B) {
+                unit_s[r0 + lane] = units + cu - u;
+                slot_s[r0 + lane] = slots + cs - s;
+            }
+            units += __shfl_sync(~0u, cu, 31);
+            slots += __shfl_sync(~0u, cs, 31);
+        }
+        if (lane == 0) misc[2] = units;
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = (uint32_t)misc[0];
+    const int units = planned ? misc[2] : B * a.H * blocks_max;
+    if (blockIdx.x == 0)   // requests that do not fit
+        for (int b = tid; b < B; b += C::THREADS) {
+            const int n = a.t.n_nodes[b];
+            if (n > 0 && !tiles_of(n, a.prefix_len[b])) flag(a.status, TS_STATUS_INDEX);
+        }
+
+    // unit q of the queue; false for one that is empty (requests beyond the planned ones)
+    auto decode = [&](int q, Unit8 &u) -> bool {
+        int rest, first = 0;
+        u.slot = 0;
+        u.parts = 1;
+        if (planned) {
+            int lo = 0, hi = B - 1;   // the last request whose first unit is at most q
+            while (lo < hi) {
+                const int mid = (lo + hi + 1) >> 1;
+                if (unit_s[mid] <= q) lo = mid;
+                else hi = mid - 1;
+            }
+            u.b = order_s[lo];
+            first = unit_s[lo];
+            u.slot = slot_s[lo];
+            u.n = req_s[u.b].x;
+            u.P = req_s[u.b].y;
+        } else {
+            u.b = q / (a.H * blocks_max);
+            first = u.b * a.H * blocks_max;
+            u.n = a.t.n_nodes[u.b];
+            u.P = a.prefix_len[u.b];
+        }
+        rest = q - first;
+        const int tl = tiles_of(u.n, u.P), blocks = planned ? blocks_of(u.n) : blocks_max;
+        if (planned) u.parts = parts_of(tl, per);
+        // row blocks of the same keys follow one another: the second finds them in L2
+        const int blk = rest % blocks, item = rest / blocks;
+        u.h = item % a.H;
+        u.part = item / a.H;
+        u.row0 = blk * RP;
+        if (!tl || blk >= blocks_of(u.n)) return false;
+        u.j0 = (int)((long long)tl * u.part / u.parts);
+        u.j1 = (int)((long long)tl * (u.part + 1) / u.parts);
+        if (u.parts > 1) u.slot += (u.h * blocks + blk) * u.parts;
+        return true;
+    };
+    auto read_unit = [&](int r) -> Unit8 {
+        const volatile int *i = info_s + r * 12;
+        return Unit8{i[0], i[1], i[2], i[3], i[4], i[5], i[6], i[7], i[8], i[9]};
+    };
+
+    if (warp == 0) {   // ------------------------------------------------ producer and queue
+        int g = 0;
+        bool ok = true;
+        auto next = [&]() -> int { return lane == 0 ? (int)atomicAdd(a.queue, 1u) : 0; };
+        int q = __shfl_sync(~0u, next(), 0), k = 0;
+        Unit8 u;
+        for (;;) {
+            while (q < units && !decode(q, u)) q = __shfl_sync(~0u, next(), 0);
+            const int r = k % kRing;
+            if (k >= kRing && !mbar_wait_warp(ifree + 8 * r, (uint32_t)(k / kRing - 1) & 1u)) {
+                ok = false;
+                break;
+            }
+            if (lane == 0) {
+                volatile int *i = info_s + r * 12;
+                i[0] = q < units ? u.b : -1;
+                i[1] = u.h; i[2] = u.row0; i[3] = u.n; i[4] = u.P; i[5] = u.j0; i[6] = u.j1;
+                i[7] = u.parts; i[8] = u.part; i[9] = u.slot;
+                mbar_arrive(iready + 8 * r);
+            }
+            if (q >= units) break;
+            const int qn = next();   // in flight over this unit's loads
+            const int L = u.P + u.n;
+            const int strip = (u.b * a.H + u.h) * a.rows;   // dense: the cache row of key 0
+            for (int j = u.j0; j < u.j1; ++j, ++g) {
+                const int st = g % C::STAGES, key0 = j * kTileKeys;
+                const bool two = key0 + 64 < L;
+                int row0 = strip + key0, row1 = row0 + 64;
+                bool has0 = true, has1 = true;
+                if (a.pg.bt) {   // a page's 64 rows of this head; zeros (a row far outside) for a page that is none
+                    const int32_t *bt = a.pg.bt + (size_t)u.b * a.pg.max_pages + key0 / TS_PAGE_KEYS;
+                    const int p0 = __ldg(bt), p1 = two ? __ldg(bt + 1) : 0;
+                    has0 = p0 >= 0 && p0 < a.pg.num_pages;
+                    has1 = p1 >= 0 && p1 < a.pg.num_pages;
+                    if (lane == 0 && !(has0 && has1)) flag(a.status, TS_STATUS_INDEX);
+                    row0 = has0 ? (p0 * a.H + u.h) * TS_PAGE_KEYS : 0x7fffff00;
+                    row1 = has1 ? (p1 * a.H + u.h) * TS_PAGE_KEYS : 0x7fffff00;
+                }
+                if (g >= C::STAGES && !mbar_wait_warp(empty + 8 * st, (uint32_t)(g / C::STAGES - 1) & 1u)) {
+                    ok = false;
+                    break;
+                }
+                const uint32_t kd = sm_base + st * C::STAGE_BYTES, vd = kd + C::OP_BYTES, fb = full + 8 * st;
+                if (lane == 0) {
+                    if (a.pg.bt) {
+                        mbar_expect_tx(fb, (two ? 4 : 2) * 64 * D);
+                        tma_load_2d(kd, &map_k, 0, row0, fb);
+                        tma_load_2d(vd, &map_v, 0, row0, fb);
+                        if (two) {
+                            tma_load_2d(kd + 64 * D, &map_k, 0, row1, fb);
+                            tma_load_2d(vd + 64 * D, &map_v, 0, row1, fb);
+                        }
+                    } else {
+                        mbar_expect_tx(fb, C::STAGE_BYTES);
+                        tma_load_2d(kd, &map_k, 0, row0, fb);
+                        tma_load_2d(vd, &map_v, 0, row0, fb);
+                    }
+                }
+                const uint32_t side = sm_base + C::OFF_SIDE + st * C::SIDE + lane * 4;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int key = key0 + i * 32 + lane;
+                    const bool in = key < L && (i < 2 ? has0 : has1);
+                    const size_t row = in ? (size_t)((i < 2 ? row0 : row1) + (i & 1) * 32 + lane) : 0;
+                    cp_async4(side + i * 128, a.k_scale + row, in);
+                    cp_async4(side + 512 + i * 128, a.v_scale + row, in);
+                }
+                if (key0 + kTileKeys > u.P) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int node = key0 + i * 32 + lane - u.P;
+                        const bool in = node >= 0 && node < u.n;
+                        cp_async4(side + 1024 + i * 128, a.t.sub_end + (in ? (size_t)u.b * n_max + node : 0), in);
+                    }
+                }
+                cp_async_arrive(fb);
+            }
+            if (!ok) break;
+            q = __shfl_sync(~0u, qn, 0);
+            ++k;
+        }
+        if (!ok) {   // leave no copy in flight
+            if (lane == 0) misc[1] = 1;
+            for (int i = g > C::STAGES ? g - C::STAGES : 0; i < g; ++i)
+                mbar_wait_warp(full + 8 * (i % C::STAGES), (uint32_t)(i / C::STAGES) & 1u);
+        }
+    } else if (warp == 1) {   // ----------------------------------------- MMA issuer
+        if (lane == 0) {
+            constexpr uint32_t idesc_s = idesc_f8(128, 2 * RP, false, false, false);
+            constexpr uint32_t idesc_o = idesc_f8(128, 3 * RP, true, true, true);
+            constexpr uint64_t swz = D == 128 ? kSwz128 : kSwz64;
+            bool ok = true;
+            auto issue_s = [&](int g, int qb) -> bool {
+                const int st = g % C::STAGES, x = g & 1;
+                if (!mbar_wait_bounded(full + 8 * st, (uint32_t)(g / C::STAGES) & 1u)) return false;
+                tc_fence_after();
+                const uint32_t kb = sm_base + st * C::STAGE_BYTES, qd = fix_base + C::FIX_Q + qb * C::Q_BYTES;
+#pragma unroll
+                for (int kk = 0; kk < D / 32; ++kk)
+                    tc_mma_f8(tmem + C::S_COL + x * 2 * RP, smem_desc8(kb + kk * 32, 16, 8 * D, swz),
+                              smem_desc8(qd + kk * 32, 16, 8 * D, swz), idesc_s, kk > 0);
+                tc_commit(sfull + 8 * x);
+                return true;
+            };
+            // the first tile of unit k starts O afresh, once unit k - 1's has been read out of it
+            auto issue_o = [&](int g, bool first, int k) -> bool {
+                const int st = g % C::STAGES;
+                if (first && k >= 1 && !mbar_wait_bounded(ofree, (uint32_t)(k - 1) & 1u)) return false;
+                if (!mbar_wait_bounded(pfull, (uint32_t)g & 1u)) return false;
+                tc_fence_after();
+                const uint32_t vb = sm_base + st * C::STAGE_BYTES + C::OP_BYTES, pd = fix_base + C::FIX_P;
+                // V^T: dims contiguous; d = 64 repeats its 64 rows (stride 0) to the MMA's 128
+#pragma unroll
+                for (int kk = 0; kk < kTileKeys / 32; ++kk)
+                    tc_mma_f8(tmem + C::O_COL, smem_desc8(vb + kk * 32 * D, 0, 8 * D, swz),
+                              smem_desc8(pd + kk * 32 * 64, C::P_ATOM, 512, kSwz64), idesc_o, !first || kk > 0);
+                tc_commit(empty + 8 * st);
+                tc_commit(pvdone);
+                return true;
+            };
+            int g = 0, pend = -1, pend_k = 0;
+            bool pend_first = false;
+            for (int k = 0; ok; ++k) {
+                const int r = k % kRing;
+                if (!mbar_wait_bounded(iready + 8 * r, (uint32_t)(k / kRing) & 1u)) { ok = false; break; }
+                const Unit8 u = read_unit(r);
+                mbar_arrive(ifree + 8 * r);
+                if (u.b < 0) break;
+                if (!mbar_wait_bounded(qready + 8 * (k & 1), (uint32_t)(k >> 1) & 1u)) { ok = false; break; }
+                for (int j = u.j0; j < u.j1 && ok; ++j, ++g) {
+                    // score buffer g & 1 was read before O(g - 2) was issued
+                    if (!issue_s(g, k & 1)) { ok = false; break; }
+                    if (j == u.j1 - 1) tc_commit(qfree + 8 * (k & 1));
+                    if (pend >= 0 && !issue_o(pend, pend_first, pend_k)) { ok = false; break; }
+                    pend = g;
+                    pend_first = j == u.j0;
+                    pend_k = k;
+                }
+            }
+            if (ok && pend >= 0) ok = issue_o(pend, pend_first, pend_k);
+            if (!ok) misc[1] = 1;
+            tc_commit(fin);
+            if (!mbar_wait_bounded(fin, 0)) misc[1] = 1;
+        }
+        __syncwarp();
+    } else if (warp >= 2 + C::SM_WARPS) {   // --------------------------- query rows
+        constexpr int EPL = D / 32, AHEAD = 8;   // values a lane holds of a row; rows in flight
+        const int w = warp - (2 + C::SM_WARPS);
+        float *qs_w = (float *)(fix + C::FIX_QS);
+        int *qrow_w = (int *)(fix + C::FIX_QROW);
+        bool ok = true;
+        for (int k = 0;; ++k) {
+            const int r = k % kRing;
+            if (!mbar_wait_warp(iready + 8 * r, (uint32_t)(k / kRing) & 1u)) { ok = false; break; }
+            const Unit8 u = read_unit(r);
+            if (u.b < 0) break;
+            // rows w * RP/2 .. of the block; lane i looks up row i's place in q and out
+            constexpr int MINE = RP / 2;
+            int place = -1;
+            if (lane < MINE) {
+                const int rho = u.row0 + w * MINE + lane, i = rho / a.G;
+                if (i < u.n) {
+                    const int v = a.t.perm[(size_t)u.b * n_max + i];
+                    if (v >= 0 && v < n_max) place = v * a.Hq + u.h * a.G + (rho - i * a.G);
+                }
+                qrow_w[r * 64 + w * MINE + lane] = place;
+            }
+            if (k >= 2 && !mbar_wait_warp(qfree + 8 * (k & 1), (uint32_t)(k / 2 - 1) & 1u)) { ok = false; break; }
+            unsigned char *qd = fix + C::FIX_Q + (k & 1) * C::Q_BYTES;
+            const __nv_bfloat16 *qb = a.q + (size_t)u.b * n_max * a.Hq * D;
+#pragma unroll 1
+            for (int c0 = 0; c0 < MINE; c0 += AHEAD) {
+                uint2 raw[AHEAD];
+#pragma unroll
+                for (int i = 0; i < AHEAD; ++i) {
+                    const int pl = __shfl_sync(~0u, place, c0 + i);
+                    raw[i] = make_uint2(0u, 0u);
+                    if (pl >= 0) {
+                        const __nv_bfloat16 *p = qb + (size_t)pl * D + lane * EPL;
+                        if constexpr (EPL == 4) raw[i] = __ldg(reinterpret_cast<const uint2 *>(p));
+                        else raw[i].x = __ldg(reinterpret_cast<const uint32_t *>(p));
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < AHEAD; ++i) {
+                    float x[4] = {__uint_as_float(raw[i].x << 16), __uint_as_float(raw[i].x & 0xffff0000u),
+                                  __uint_as_float(raw[i].y << 16), __uint_as_float(raw[i].y & 0xffff0000u)};
+                    uint32_t top = 0;   // |values| order as their bits do, infinities and NaN on top
+#pragma unroll
+                    for (int e = 0; e < EPL; ++e) top = max(top, __float_as_uint(x[e]) & 0x7fffffffu);
+                    top = __reduce_max_sync(~0u, top);
+                    // 2^(exponent - 7), within the normal numbers whose reciprocal is one too
+                    int ex = (int)(top >> 23) - 7;
+                    ex = ex < 4 ? 4 : ex;
+                    const float sc = __uint_as_float((uint32_t)ex << 23), inv = __uint_as_float((uint32_t)(254 - ex) << 23);
+                    uint32_t hi = 0, lo = 0;
+#pragma unroll
+                    for (int e = 0; e < EPL; e += 2) {
+                        const float y0 = x[e] * inv, y1 = x[e + 1] * inv;
+                        const uint16_t h2 = __nv_cvt_float2_to_fp8x2(make_float2(y0, y1), __NV_SATFINITE, __NV_E4M3);
+                        const float2 f = fp8x2_to_float2(h2);
+                        const uint16_t l2 = __nv_cvt_float2_to_fp8x2(make_float2(y0 - f.x, y1 - f.y), __NV_SATFINITE, __NV_E4M3);
+                        hi |= (uint32_t)h2 << (e * 8);
+                        lo |= (uint32_t)l2 << (e * 8);
+                    }
+                    const int c = w * MINE + c0 + i;
+                    // 16-byte chunks of a row are permuted as the MMA's descriptor says
+                    auto at = [&](int row) {
+                        return D == 128 ? row * 128 + (((lane >> 2) ^ (row & 7)) << 4) + (lane & 3) * 4
+                                        : row * 64 + (((lane >> 3) ^ ((row >> 1) & 3)) << 4) + (lane & 7) * 2;
+                    };
+                    if constexpr (EPL == 4) {
+                        *(uint32_t *)(qd + at(c)) = hi;
+                        *(uint32_t *)(qd + at(RP + c)) = lo;
+                    } else {
+                        *(uint16_t *)(qd + at(c)) = (uint16_t)hi;
+                        *(uint16_t *)(qd + at(RP + c)) = (uint16_t)lo;
+                    }
+                    if (lane == 0) qs_w[r * 64 + c] = top >= 0x7f800000u ? __int_as_float(0x7fc00000) : sc;
+                }
+            }
+            fence_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(qready + 8 * (k & 1));
+                mbar_arrive(ifree + 8 * r);
+            }
+        }
+        if (!ok && lane == 0) misc[1] = 1;
+    } else {   // -------------------------------------------------------- softmax
+        constexpr int CG = C::CG;
+        constexpr float kBase = 11.f, kOver = 4.f;   // p = 2^kBase at the running maximum, raised beyond 2^kOver of it
+        const int grp = (warp - 2) >> 2, quarter = warp & 3, cb = grp * CG;
+        const int bar = 1 + grp, gt = (warp - 2 - 4 * grp) * 32 + lane;   // thread of the group
+        const uint32_t tl = tmem + ((uint32_t)(quarter * 32) << 16);
+        const int kslot = quarter * 32 + lane;   // this lane's key of a tile, and its dim of O
+        float *mx_s = (float *)(fix + C::FIX_MX) + grp * 4 * 32, *ls_s = (float *)(fix + C::FIX_LS);
+        float *f_s = (float *)(fix + C::FIX_F) + cb;
+        bool ok = true;
+        int g = 0;
+        for (int k = 0;; ++k) {
+            const int r = k % kRing;
+            if (!mbar_wait_warp(iready + 8 * r, (uint32_t)(k / kRing) & 1u)) ok = false;
+            if (bar_any(bar, 128, !ok)) {   // all of the group go on, or none
+                ok = false;
+                break;
+            }
+            const Unit8 u = read_unit(r);
+            if (u.b < 0) break;
+            const int L = u.P + u.n;
+            float m[CG], l[CG], qs[CG];   // maximum less kBase, negated; sums of this lane's keys; query scales
+            float ref = 0.f, iref = 0.f;  // the value scales' reference
+#pragma unroll
+            for (int c = 0; c < CG; ++c) {
+                m[c] = 1e30f;
+                l[c] = 0.f;
+            }
+            bool gone = false;
+            for (int j = u.j0; j < u.j1; ++j, ++g) {
+                const int x = g & 1, st = g % C::STAGES, key = j * kTileKeys + kslot;
+                if (ok && !mbar_wait_warp(sfull + 8 * x, (uint32_t)(g >> 1) & 1u)) ok = false;
+                if (ok && !mbar_wait_warp(full + 8 * st, (uint32_t)(g / C::STAGES) & 1u)) ok = false;
+                tc_fence_after();
+                if (j == u.j0) {   // the scales were there before the first scores
+#pragma unroll
+                    for (int c = 0; c < CG; c += 4) {
+                        const float4 v = *(const float4 *)(qs_s + r * 64 + cb + c);
+                        qs[c] = v.x; qs[c + 1] = v.y; qs[c + 2] = v.z; qs[c + 3] = v.w;
+                    }
+                }
+                const float *side = (const float *)(sm + C::OFF_SIDE + st * C::SIDE);
+                const float ks = side[kslot] * a.scale_log2, vs = side[128 + kslot];
+                float t[CG];
+                {
+                    float lo[CG];
+                    const uint32_t sb = tl + C::S_COL + x * 2 * RP + cb;
+#pragma unroll
+                    for (int c = 0; c < CG; c += 8) {
+                        tc_ld8(sb + c, t + c);
+                        tc_ld8(sb + RP + c, lo + c);
+                    }
+                    tc_wait_ld();
+#pragma unroll
+                    for (int c = 0; c < CG; ++c) t[c] = (t[c] + lo[c]) * ks;
+                }
+                if (j * kTileKeys + kTileKeys > u.P) {   // tree keys, or keys past the end
+                    int from = 0, to = 0;                // the rows that see this lane's key
+                    if (key < u.P) {
+                        to = 0x7fffffff;
+                        from = -to;
+                    } else if (key < L) {
+                        from = (key - u.P) * a.G - u.row0 - cb;
+                        to = ((const int *)side)[256 + kslot] * a.G - u.row0 - cb;
+                    }
+#pragma unroll
+                    for (int c = 0; c < CG; ++c)
+                        if (!(c >= from && c < to)) t[c] = -INFINITY;
+                }
+                float top = -INFINITY;
+#pragma unroll
+                for (int c = 0; c < CG; ++c) top = fmaxf(top, fmaf(t[c], qs[c], m[c]));
+                if (bar_any(bar, 128, j == u.j0 || top > kBase + kOver || vs > ref || !ok)) {
+                    // new maxima: of each column over the tile, taken where the old one is passed by 2^kOver
+                    float mine = 0.f;
+#pragma unroll
+                    for (int c = 0; c < CG; ++c) {
+                        const float w = warp_max(t[c] * qs[c]);
+                        if (lane == c) mine = w;
+                    }
+                    if (lane < CG) mx_s[quarter * 32 + lane] = mine;
+                    const float vtop = warp_max(vs);
+                    if (lane == 0) ls_s[quarter * 64 + cb] = vtop;
+                    if (bar_any(bar, 128, !ok)) {
+                        ok = false;
+                        gone = true;
+                        break;
+                    }
+                    float nref = fmaxf(fmaxf(ls_s[cb], ls_s[64 + cb]), fmaxf(ls_s[128 + cb], ls_s[192 + cb]));
+                    // a half more than the largest scale so far, so that few tiles raise it
+                    nref = nref > ref ? nref * 1.5f : ref;
+                    const float rr = nref > 0.f ? ref / nref : 1.f;
+                    ref = nref;
+                    iref = ref > 0.f ? 1.f / ref : 0.f;
+                    float al[CG];
+#pragma unroll
+                    for (int c = 0; c < CG; ++c) {
+                        const float top4 = fmaxf(fmaxf(mx_s[c], mx_s[32 + c]), fmaxf(mx_s[64 + c], mx_s[96 + c]));
+                        const float nm = kBase - top4;   // = -(maximum - kBase)
+                        al[c] = 1.f;
+                        if (top4 + m[c] > kBase + kOver) {
+                            al[c] = ex2(nm - m[c]);      // 2^(old - new)
+                            m[c] = nm;
+                        }
+                        l[c] *= al[c];
+                        al[c] *= rr;
+                    }
+                    if (j > u.j0) {   // O so far, once the product before this one has landed in it
+                        if (ok && !mbar_wait_warp(pvdone, (uint32_t)(g - 1) & 1u)) ok = false;
+                        tc_fence_after();
+                        if (ok && quarter * 32 < D) {
+#pragma unroll
+                            for (int i = 0; i < 3; ++i)
+#pragma unroll
+                                for (int c = 0; c < CG; c += 8) {
+                                    float o[8];
+                                    const uint32_t oc = tl + C::O_COL + i * RP + cb + c;
+                                    tc_ld8(oc, o);
+                                    tc_wait_ld();
+#pragma unroll
+                                    for (int e = 0; e < 8; ++e) o[e] *= al[c + e];
+                                    tc_st8(oc, o);
+                                }
+                            tc_wait_st();
+                        }
+                    }
+                    bar_sync(bar, 128);   // the exchange may be written again
+                }
+                const float rv = vs * iref;
+                uint32_t w0[CG / 4], w1[CG / 4], w2[CG / 4];   // the three parts, four columns a word
+#pragma unroll
+                for (int c = 0; c < CG; c += 4) {
+                    uint32_t h[2], a1[2], a2[2];
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const int cc = c + 2 * e;
+                        const float p0 = ex2(fmaf(t[cc], qs[cc], m[cc])), p1 = ex2(fmaf(t[cc + 1], qs[cc + 1], m[cc + 1]));
+                        l[cc] += p0;
+                        l[cc + 1] += p1;
+                        h[e] = half2_of(p0 * rv, p1 * rv);
+                    }
+                    if (j * kTileKeys + kTileKeys > u.P) {   // a masked weight is zero whatever the row's scale is
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const int cc = c + 2 * e;
+                            if (t[cc] == -INFINITY) h[e] &= 0xffff0000u;
+                            if (t[cc + 1] == -INFINITY) h[e] &= 0xffffu;
+                        }
+                    }
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        a1[e] = hsub2(h[e], h[e] & 0xff00ff00u);
+                        a2[e] = hsub2(a1[e], a1[e] & 0xff00ff00u) + 0x00800080u;   // half a step: rounded
+                    }
+                    w0[c / 4] = __byte_perm(h[0], h[1], 0x7531);
+                    w1[c / 4] = __byte_perm(a1[0], a1[1], 0x7531);
+                    w2[c / 4] = __byte_perm(a2[0], a2[1], 0x7531);
+                }
+                // P's one buffer is free once the product before this one has read it
+                if (ok && j > u.j0 && !mbar_wait_warp(pvdone, (uint32_t)(g - 1) & 1u)) ok = false;
+                if (ok) {
+                    unsigned char *pd = fix + C::FIX_P + kslot * 64;
+                    const int flip = (kslot >> 1) & 3;
+                    auto put = [&](const uint32_t (&w)[CG / 4], int term) {
+                        constexpr int STEP = CG % 16 == 0 ? 16 : 8;
+#pragma unroll
+                        for (int c = 0; c < CG; c += STEP) {
+                            const int col = term * RP + cb + c;
+                            unsigned char *p = pd + (col >> 6) * C::P_ATOM + ((((col >> 4) & 3) ^ flip) << 4) + (col & 15);
+                            if constexpr (STEP == 16) *(uint4 *)p = make_uint4(w[c / 4], w[c / 4 + 1], w[c / 4 + 2], w[c / 4 + 3]);
+                            else *(uint2 *)p = make_uint2(w[c / 4], w[c / 4 + 1]);
+                        }
+                    };
+                    put(w0, 0);
+                    put(w1, 1);
+                    put(w2, 2);
+                }
+                if (j * kTileKeys + kTileKeys > L && ok) {
+                    // V's rows past the last key may hold anything: zeros (whose weights are zero too)
+                    unsigned char *vt = sm + st * C::STAGE_BYTES + C::OP_BYTES;
+                    const int r0 = (L - j * kTileKeys) * (D / 16);
+                    for (int i = r0 + tid - 64; i < kTileKeys * (D / 16); i += 32 * C::SM_WARPS)
+                        *(uint4 *)(vt + i * 16) = make_uint4(0u, 0u, 0u, 0u);
+                }
+                fence_async_smem();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(pfull);
+            }
+            if (gone) break;
+
+            // ---- the unit's output
+#pragma unroll
+            for (int c = 0; c < CG / 16 * 16; c += 16) {
+                reduce_scatter<16>(l + c, lane);
+                if (!(lane & 1)) ls_s[quarter * 64 + cb + c + (lane >> 1)] = l[c];
+            }
+            if constexpr (CG % 16 != 0) {
+                constexpr int c = CG / 16 * 16;
+                reduce_scatter<8>(l + c, lane);
+                if (!(lane & 3)) ls_s[quarter * 64 + cb + c + (lane >> 2)] = l[c];
+            }
+            bar_sync(bar, 128);
+            float lsum = 0.f;
+            if (gt < CG) {
+                const int c = cb + gt;
+                lsum = (ls_s[c] + ls_s[64 + c]) + (ls_s[128 + c] + ls_s[192 + c]);
+                // a part keeps its own maximum and sum; a whole unit is divided by its sum here
+                f_s[gt] = u.parts > 1 ? ref : ref / lsum;
+            }
+            if (u.parts > 1) {
+                float mm = 0.f;
+#pragma unroll
+                for (int c = 0; c < CG; ++c)
+                    if (gt == c) mm = -m[c];
+                if (gt < CG) a.part_ml[(size_t)(u.slot + u.part) * RP + cb + gt] = make_float2(mm, lsum);
+            }
+            if (ok && !mbar_wait_warp(pvdone, (uint32_t)(g - 1) & 1u)) ok = false;
+            tc_fence_after();
+            bar_sync(bar, 128);
+            __nv_bfloat16 *ob = a.out + (size_t)u.b * n_max * a.Hq * D;
+            const int *rows = qrow_s + r * 64 + cb;
+#pragma unroll
+            for (int c = 0; c < CG; c += 8) {
+                float o[3][8];
+                if (ok && quarter * 32 < D) {
+#pragma unroll
+                    for (int i = 0; i < 3; ++i) tc_ld8(tl + C::O_COL + i * RP + cb + c, o[i]);
+                    tc_wait_ld();
+                }
+                if (c + 8 >= CG) {   // O is read out
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(ofree);
+                }
+                if (!ok || quarter * 32 >= D) continue;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) o[0][e] = ((o[0][e] + o[1][e]) + o[2][e]) * f_s[c + e];
+                if (u.parts > 1) {
+                    float *po = a.part_o + ((size_t)(u.slot + u.part) * RP + cb + c) * D + kslot;
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) po[e * D] = o[0][e];
+                } else {
+                    // two columns at a time: even lanes store dims (d, d + 1) of the first, odd lanes of the second
+#pragma unroll
+                    for (int e = 0; e < 8; e += 2) {
+                        const float keep = lane & 1 ? o[0][e + 1] : o[0][e], send = lane & 1 ? o[0][e] : o[0][e + 1];
+                        const float got = __shfl_xor_sync(~0u, send, 1);
+                        const int row = rows[c + e + (lane & 1)];
+                        const __nv_bfloat162 v = lane & 1 ? __floats2bfloat162_rn(got, keep) : __floats2bfloat162_rn(keep, got);
+                        if (row >= 0) *(__nv_bfloat162 *)(ob + (size_t)row * D + (kslot & ~1)) = v;
+                    }
+                }
+            }
+            if (u.parts > 1) {   // the last part of the item to finish joins them, for this group's columns
+                __threadfence();
+                bar_sync(bar, 128);
+                if (gt == 0) {
+                    unsigned *cnt = a.joins + (size_t)u.slot * 2 + grp;
+                    const bool last = ok && atomicAdd(cnt, 1u) == (unsigned)u.parts - 1;
+                    if (last) *cnt = 0u;
+                    misc[4 + grp] = last;
+                }
+                bar_sync(bar, 128);
+                if (misc[4 + grp]) {
+                    __threadfence();
+                    constexpr int EPL = D / 32;
+                    for (int c = warp & 3; c < CG; c += 4) {   // a warp a column, lane = part, then lane = dims
+                        const int row = rows[c];
+                        if (row < 0) continue;
+                        float2 ml = make_float2(-INFINITY, 0.f);
+                        if (lane < u.parts) ml = __ldcg(a.part_ml + (size_t)(u.slot + lane) * RP + cb + c);
+                        const float mx = warp_max(ml.x);
+                        const float wt = lane < u.parts ? ex2(ml.x - mx) : 0.f;
+                        float ls = wt * ml.y;
+#pragma unroll
+                        for (int o = 16; o; o >>= 1) ls += __shfl_xor_sync(~0u, ls, o);
+                        float acc[EPL] = {};
+                        const float *po = a.part_o + ((size_t)u.slot * RP + cb + c) * D + lane * EPL;
+#pragma unroll 8
+                        for (int s = 0; s < u.parts; ++s) {
+                            const float ws = __shfl_sync(~0u, wt, s);
+                            float v[EPL];
+                            if constexpr (EPL == 4) {
+                                const float4 f = __ldcg((const float4 *)(po + (size_t)s * RP * D));
+                                v[0] = f.x; v[1] = f.y; v[2] = f.z; v[3] = f.w;
+                            } else {
+                                const float2 f = __ldcg((const float2 *)(po + (size_t)s * RP * D));
+                                v[0] = f.x; v[1] = f.y;
+                            }
+#pragma unroll
+                            for (int e = 0; e < EPL; ++e) acc[e] = fmaf(ws, v[e], acc[e]);
+                        }
+                        const float inv = 1.f / ls;
+#pragma unroll
+                        for (int e = 0; e < EPL; e += 2)
+                            *(__nv_bfloat162 *)(ob + (size_t)row * D + lane * EPL + e) =
+                                __floats2bfloat162_rn(acc[e] * inv, acc[e + 1] * inv);
+                    }
+                }
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(ifree + 8 * r);
+        }
+        if (!ok) misc[1] = 1;
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 0)
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(C::TMEM_COLS) : "memory");
+    if (tid == 0) {
+        if (misc[1]) flag(a.status, TS_STATUS_TIMEOUT);
+        // the last CTA returns the queue to zero: every CTA counted here has stopped taking units
+        __threadfence();
+        if (atomicAdd(a.queue + 1, 1u) == gridDim.x - 1) {
+            a.queue[0] = 0u;
+            a.queue[1] = 0u;
         }
     }
-    for (int o2 = 16; o2; o2 >>= 1) l += __shfl_xor_sync(~0u, l, o2);
-    for (int e = 0; e < DPL; ++e) a.out[at + lane * DPL + e] = __float2bfloat16(o[e] / l);
+}
+
+// ------------------------------------------------------------------ plan ---
+struct Plan8 {
+    int rp, blocks, slots;
+    size_t ml, o, bytes;   // offsets of the parts, all bytes
+};
+
+// RP: the rows there can be, cut into equal blocks of at most 64, rounded up
+// to 16. Slots: an item with T tiles is cut into ceil(T / per) parts, and
+// per >= all tiles / (kCutsPerSm * SMs), so the parts of the cut items (each
+// longer than per) number less than 2 * kCutsPerSm * SMs.
+Plan8 plan8(int B, int Hkv, int G, int n_max, int d) {
+    Plan8 p;
+    const long long rows = (long long)n_max * G;
+    p.blocks = (int)((rows + 63) / 64);
+    p.rp = (int)(((rows + p.blocks - 1) / p.blocks + 15) / 16 * 16);
+    p.blocks = (int)((rows + p.rp - 1) / p.rp);
+    p.slots = B <= kReqCache ? 2 * kCutsPerSm * num_sms() : 0;
+    size_t at = 256 + ((size_t)p.slots * 2 * sizeof(unsigned) + 255) / 256 * 256;
+    p.ml = at;
+    at += (size_t)p.slots * p.rp * sizeof(float2);
+    p.o = (at + 255) / 256 * 256;
+    p.bytes = p.o + (size_t)p.slots * p.rp * d * sizeof(float);
+    return p;
+}
+
+// Rows of d codes; boxes of box_rows whole rows, swizzled by the row's width.
+bool make_map8(CUtensorMap *map, const void *base, int d, long long rows, int box_rows) {
+    EncodeTiledFn enc = encode_fn();
+    if (!enc) return false;
+    cuuint64_t dims[2] = {(cuuint64_t)d, (cuuint64_t)rows}, strides[1] = {(cuuint64_t)d};
+    cuuint32_t box[2] = {(cuuint32_t)d, (cuuint32_t)box_rows}, estr[2] = {1, 1};
+    return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(base), dims, strides, box, estr,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, d == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int D, int RP>
+cudaError_t launch8(const CUtensorMap &mk, const CUtensorMap &mv, const Attn8Args &a, int grid, cudaStream_t s) {
+    using C = Cfg8<D, RP>;
+    cudaError_t e = cudaFuncSetAttribute(k_attn_kv8<D, RP>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+    if (e != cudaSuccess) return e;
+    return launch(k_attn_kv8<D, RP>, dim3(grid), dim3(C::THREADS), C::SMEM, s, mk, mv, a);
 }
 
 }  // namespace
 
-size_t kv8_attention_ws_bytes(int, int, int, int, int, int) { return 256; }
+size_t kv8_attention_ws_bytes(int B, int Hq, int Hkv, int n_max, int d, int) {
+    return plan8(B, Hkv, Hq / Hkv, n_max, d).bytes;
+}
 
 cudaError_t launch_attn_kv8(void *out, const void *q, const ts_kv8 &kv, int Hq, const int32_t *prefix_len,
-                            const ts_tree &t, float scale, void *, uint32_t *status, cudaStream_t s, const char **) {
-    Attn8Args a = {(__nv_bfloat16 *)out, (const __nv_bfloat16 *)q, kv.k, kv.v, kv.k_scale, kv.v_scale, prefix_len, t,
-                   Hq, kv.H, Hq / kv.H, kv8_rows(kv), scale * 1.4426950408889634f, kv8_pages(kv), status};
-    const dim3 grid((t.n_max * a.G + kWarps - 1) / kWarps, kv.H, t.B), block(kWarps * 32);
-    return kv.d == 128 ? launch(k_attn_kv8_rows<128>, grid, block, 0, s, a)
-                       : launch(k_attn_kv8_rows<64>, grid, block, 0, s, a);
+                            const ts_tree &t, float scale, void *ws, uint32_t *status, cudaStream_t s,
+                            const char **why) {
+    const int G = Hq / kv.H;
+    const Plan8 p = plan8(t.B, kv.H, G, t.n_max, kv.d);
+    const bool paged = kv.block_table != nullptr;
+    const long long rows = paged ? (long long)kv.num_pages * kv.H * TS_PAGE_KEYS : (long long)kv.B * kv.H * kv.L_max;
+    CUtensorMap mk, mv;
+    if (!make_map8(&mk, kv.k, kv.d, rows, paged ? TS_PAGE_KEYS : kTileKeys) ||
+        !make_map8(&mv, kv.v, kv.d, rows, paged ? TS_PAGE_KEYS : kTileKeys)) {
+        *why = "cuTensorMapEncodeTiled failed for the 8-bit cache";
+        return cudaErrorInvalidValue;
+    }
+    unsigned char *w = (unsigned char *)ws;
+    Attn8Args a = {(__nv_bfloat16 *)out, (const __nv_bfloat16 *)q, kv.k_scale, kv.v_scale, prefix_len, t, Hq, kv.H, G,
+                   kv8_rows(kv), scale * 1.4426950408889634f, kv8_pages(kv), status, (unsigned *)w,
+                   (unsigned *)(w + 256), (float2 *)(w + p.ml), (float *)(w + p.o), p.slots};
+    // no more CTAs than there can be units
+    const long long tiles = (a.rows + kTileKeys - 1) / kTileKeys, cuts = (tiles + kMinCut - 1) / kMinCut;
+    const long long units = (long long)t.B * kv.H * p.blocks * (p.slots ? (cuts < kMaxCuts ? cuts : kMaxCuts) : 1);
+    const int grid = (int)(units < num_sms() ? units : num_sms());
+    if (kv.d == 128) switch (p.rp) {
+        case 16: return launch8<128, 16>(mk, mv, a, grid, s);
+        case 32: return launch8<128, 32>(mk, mv, a, grid, s);
+        case 48: return launch8<128, 48>(mk, mv, a, grid, s);
+        default: return launch8<128, 64>(mk, mv, a, grid, s);
+    }
+    switch (p.rp) {
+        case 16: return launch8<64, 16>(mk, mv, a, grid, s);
+        case 32: return launch8<64, 32>(mk, mv, a, grid, s);
+        case 48: return launch8<64, 48>(mk, mv, a, grid, s);
+        default: return launch8<64, 64>(mk, mv, a, grid, s);
+    }
 }
 
 }  // namespace ts
