@@ -76,9 +76,14 @@ __device__ __forceinline__ void tc_ld8(uint32_t taddr, float *v) {
                  : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7])
                  : "r"(taddr));
 }
-__device__ __forceinline__ void tc_st8(uint32_t taddr, const float *v) {
-    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "f"(v[0]),
-                 "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
+__device__ __forceinline__ void tc_ld4(uint32_t taddr, float *v) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0,%1,%2,%3}, [%4];"
+                 : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3])
+                 : "r"(taddr));
+}
+__device__ __forceinline__ void tc_st4(uint32_t taddr, const float *v) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1,%2,%3,%4};" ::"r"(taddr), "f"(v[0]), "f"(v[1]),
+                 "f"(v[2]), "f"(v[3])
                  : "memory");
 }
 
@@ -612,7 +617,9 @@ __global__ void __launch_bounds__(Cfg8<D, RP>::THREADS, 1)
         if (!ok && lane == 0) misc[1] = 1;
     } else {   // -------------------------------------------------------- softmax
         constexpr int CG = C::CG;
-        constexpr float kBase = 11.f, kOver = 4.f;   // p = 2^kBase at the running maximum, raised beyond 2^kOver of it
+        // p is 2^kBase at the running maximum, which is raised once a score passes it by 2^kOver: fp16 (and e5m2) hold
+        // both ends, and what is 2^-24 of the maximum still has a bit
+        constexpr float kBase = 7.f, kOver = 8.f;
         const int grp = (warp - 2) >> 2, quarter = warp & 3, cb = grp * CG;
         const int bar = 1 + grp, gt = (warp - 2 - 4 * grp) * 32 + lane;   // thread of the group
         const uint32_t tl = tmem + ((uint32_t)(quarter * 32) << 16);
@@ -631,12 +638,12 @@ __global__ void __launch_bounds__(Cfg8<D, RP>::THREADS, 1)
             const Unit8 u = read_unit(r);
             if (u.b < 0) break;
             const int L = u.P + u.n;
-            float m[CG], l[CG], qs[CG];   // maximum less kBase, negated; sums of this lane's keys; query scales
-            float ref = 0.f, iref = 0.f;  // the value scales' reference
+            float2 m[CG / 2], l[CG / 2], qs[CG / 2];   // kBase - maximum; sums over this lane's keys; query scales
+            float ref = 0.f, iref = 0.f;               // the value scales' reference and its reciprocal
 #pragma unroll
-            for (int c = 0; c < CG; ++c) {
-                m[c] = 1e30f;
-                l[c] = 0.f;
+            for (int c = 0; c < CG / 2; ++c) {
+                m[c] = make_float2(1e30f, 1e30f);
+                l[c] = make_float2(0.f, 0.f);
             }
             bool gone = false;
             for (int j = u.j0; j < u.j1; ++j, ++g) {
@@ -648,49 +655,80 @@ __global__ void __launch_bounds__(Cfg8<D, RP>::THREADS, 1)
 #pragma unroll
                     for (int c = 0; c < CG; c += 4) {
                         const float4 v = *(const float4 *)(qs_s + r * 64 + cb + c);
-                        qs[c] = v.x; qs[c + 1] = v.y; qs[c + 2] = v.z; qs[c + 3] = v.w;
+                        qs[c / 2] = make_float2(v.x, v.y);
+                        qs[c / 2 + 1] = make_float2(v.z, v.w);
                     }
                 }
                 const float *side = (const float *)(sm + C::OFF_SIDE + st * C::SIDE);
-                const float ks = side[kslot] * a.scale_log2, vs = side[128 + kslot];
-                float t[CG];
-                {
-                    float lo[CG];
-                    const uint32_t sb = tl + C::S_COL + x * 2 * RP + cb;
-#pragma unroll
-                    for (int c = 0; c < CG; c += 8) {
-                        tc_ld8(sb + c, t + c);
-                        tc_ld8(sb + RP + c, lo + c);
-                    }
-                    tc_wait_ld();
-#pragma unroll
-                    for (int c = 0; c < CG; ++c) t[c] = (t[c] + lo[c]) * ks;
+                float ks = side[kslot] * a.scale_log2, vs = side[128 + kslot];
+                if (!(vs <= 3.402823466e38f)) {   // a poisoned value row: NaN to every row that sees it
+                    ks = __int_as_float(0x7fc00000);
+                    vs = 0.f;
                 }
-                if (j * kTileKeys + kTileKeys > u.P) {   // tree keys, or keys past the end
-                    int from = 0, to = 0;                // the rows that see this lane's key
-                    if (key < u.P) {
-                        to = 0x7fffffff;
-                        from = -to;
-                    } else if (key < L) {
+                const bool edge = j * kTileKeys + kTileKeys > u.P;   // tree keys, or keys past the end
+                int from = -0x7fffffff, to = 0x7fffffff;             // the columns that see this lane's key
+                if (edge && key >= u.P) {
+                    from = to = 0;
+                    if (key < L) {
                         from = (key - u.P) * a.G - u.row0 - cb;
                         to = ((const int *)side)[256 + kslot] * a.G - u.row0 - cb;
                     }
-#pragma unroll
-                    for (int c = 0; c < CG; ++c)
-                        if (!(c >= from && c < to)) t[c] = -INFINITY;
                 }
-                float top = -INFINITY;
+                // eight columns' exponents before the maximum is taken off
+                auto scores = [&](int c, float2 (&y)[4]) {
+                    float hi[8], lo[8];
+                    const uint32_t sb = tl + C::S_COL + x * 2 * RP + cb + c;
+                    tc_ld8(sb, hi);
+                    tc_ld8(sb + RP, lo);
+                    tc_wait_ld();
 #pragma unroll
-                for (int c = 0; c < CG; ++c) top = fmaxf(top, fmaf(t[c], qs[c], m[c]));
-                if (bar_any(bar, 128, j == u.j0 || top > kBase + kOver || vs > ref || !ok)) {
-                    // new maxima: of each column over the tile, taken where the old one is passed by 2^kOver
-                    float mine = 0.f;
+                    for (int e = 0; e < 4; ++e)
+                        y[e] = __fmul2_rn(__fadd2_rn(make_float2(hi[2 * e], hi[2 * e + 1]), make_float2(lo[2 * e], lo[2 * e + 1])),
+                                          make_float2(ks, ks));
+                    if (edge) {
 #pragma unroll
-                    for (int c = 0; c < CG; ++c) {
-                        const float w = warp_max(t[c] * qs[c]);
-                        if (lane == c) mine = w;
+                        for (int e = 0; e < 4; ++e) {
+                            if (!(c + 2 * e >= from && c + 2 * e < to)) y[e].x = -INFINITY;
+                            if (!(c + 2 * e + 1 >= from && c + 2 * e + 1 < to)) y[e].y = -INFINITY;
+                        }
                     }
-                    if (lane < CG) mx_s[quarter * 32 + lane] = mine;
+                };
+                float2 p[CG / 2];   // exponents, then probabilities
+                auto exponents = [&]() -> float {
+                    float top = -INFINITY, top2 = -INFINITY;
+#pragma unroll
+                    for (int c = 0; c < CG; c += 8) {
+                        float2 y[4];
+                        scores(c, y);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            p[c / 2 + e] = __ffma2_rn(y[e], qs[c / 2 + e], m[c / 2 + e]);
+                            top = fmaxf(top, p[c / 2 + e].x);
+                            top2 = fmaxf(top2, p[c / 2 + e].y);
+                        }
+                    }
+                    return fmaxf(top, top2);
+                };
+                bool raise = j == u.j0;
+                if (!raise) {
+                    const float top = exponents();
+                    raise = bar_any(bar, 128, top > kBase + kOver || vs > ref || !ok);
+                }
+                if (raise) {
+                    // new maxima: of each column over the tile, taken where the old one is passed by 2^kOver
+#pragma unroll 1
+                    for (int c = 0; c < CG; c += 8) {
+                        float2 y[4];
+                        scores(c, y);
+                        const float4 q0 = *(const float4 *)(qs_s + r * 64 + cb + c), q1 = *(const float4 *)(qs_s + r * 64 + cb + c + 4);
+                        const float w[8] = {warp_max(y[0].x * q0.x), warp_max(y[0].y * q0.y), warp_max(y[1].x * q0.z),
+                                            warp_max(y[1].y * q0.w), warp_max(y[2].x * q1.x), warp_max(y[2].y * q1.y),
+                                            warp_max(y[3].x * q1.z), warp_max(y[3].y * q1.w)};
+                        if (lane == 0) {
+                            *(float4 *)(mx_s + quarter * 32 + c) = make_float4(w[0], w[1], w[2], w[3]);
+                            *(float4 *)(mx_s + quarter * 32 + c + 4) = make_float4(w[4], w[5], w[6], w[7]);
+                        }
+                    }
                     const float vtop = warp_max(vs);
                     if (lane == 0) ls_s[quarter * 64 + cb] = vtop;
                     if (bar_any(bar, 128, !ok)) {
@@ -704,88 +742,86 @@ __global__ void __launch_bounds__(Cfg8<D, RP>::THREADS, 1)
                     const float rr = nref > 0.f ? ref / nref : 1.f;
                     ref = nref;
                     iref = ref > 0.f ? 1.f / ref : 0.f;
-                    float al[CG];
-#pragma unroll
-                    for (int c = 0; c < CG; ++c) {
-                        const float top4 = fmaxf(fmaxf(mx_s[c], mx_s[32 + c]), fmaxf(mx_s[64 + c], mx_s[96 + c]));
-                        const float nm = kBase - top4;   // = -(maximum - kBase)
-                        al[c] = 1.f;
-                        if (top4 + m[c] > kBase + kOver) {
-                            al[c] = ex2(nm - m[c]);      // 2^(old - new)
-                            m[c] = nm;
-                        }
-                        l[c] *= al[c];
-                        al[c] *= rr;
-                    }
-                    if (j > u.j0) {   // O so far, once the product before this one has landed in it
+                    // O so far is rescaled once the product before this one has landed in it
+                    if (j > u.j0) {
                         if (ok && !mbar_wait_warp(pvdone, (uint32_t)(g - 1) & 1u)) ok = false;
                         tc_fence_after();
-                        if (ok && quarter * 32 < D) {
+                    }
+                    const bool scale_o = j > u.j0 && ok && quarter * 32 < D;
 #pragma unroll
-                            for (int i = 0; i < 3; ++i)
+                    for (int c = 0; c < CG; c += 4) {
+                        float t4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY}, al[4];
 #pragma unroll
-                                for (int c = 0; c < CG; c += 8) {
-                                    float o[8];
-                                    const uint32_t oc = tl + C::O_COL + i * RP + cb + c;
-                                    tc_ld8(oc, o);
-                                    tc_wait_ld();
+                        for (int w = 0; w < 4; ++w) {
+                            const float4 v = *(const float4 *)(mx_s + w * 32 + c);
+                            t4[0] = fmaxf(t4[0], v.x);
+                            t4[1] = fmaxf(t4[1], v.y);
+                            t4[2] = fmaxf(t4[2], v.z);
+                            t4[3] = fmaxf(t4[3], v.w);
+                        }
 #pragma unroll
-                                    for (int e = 0; e < 8; ++e) o[e] *= al[c + e];
-                                    tc_st8(oc, o);
-                                }
-                            tc_wait_st();
+                        for (int e = 0; e < 4; ++e) {
+                            float &me = e & 1 ? m[(c + e) / 2].y : m[(c + e) / 2].x;
+                            float &le = e & 1 ? l[(c + e) / 2].y : l[(c + e) / 2].x;
+                            const float nm = kBase - t4[e];
+                            al[e] = 1.f;
+                            if (t4[e] + me > kBase + kOver) {
+                                al[e] = ex2(nm - me);   // 2^(old maximum - new)
+                                me = nm;
+                            }
+                            le *= al[e];
+                            al[e] *= rr;
+                        }
+                        if (scale_o) {
+                            float o[12];
+#pragma unroll
+                            for (int i = 0; i < 3; ++i) tc_ld4(tl + C::O_COL + i * RP + cb + c, o + 4 * i);
+                            tc_wait_ld();
+#pragma unroll
+                            for (int i = 0; i < 12; ++i) o[i] *= al[i & 3];
+#pragma unroll
+                            for (int i = 0; i < 3; ++i) tc_st4(tl + C::O_COL + i * RP + cb + c, o + 4 * i);
                         }
                     }
+                    if (scale_o) tc_wait_st();
                     bar_sync(bar, 128);   // the exchange may be written again
-                }
-                const float rv = vs * iref;
-                uint32_t w0[CG / 4], w1[CG / 4], w2[CG / 4];   // the three parts, four columns a word
-#pragma unroll
-                for (int c = 0; c < CG; c += 4) {
-                    uint32_t h[2], a1[2], a2[2];
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const int cc = c + 2 * e;
-                        const float p0 = ex2(fmaf(t[cc], qs[cc], m[cc])), p1 = ex2(fmaf(t[cc + 1], qs[cc + 1], m[cc + 1]));
-                        l[cc] += p0;
-                        l[cc + 1] += p1;
-                        h[e] = half2_of(p0 * rv, p1 * rv);
-                    }
-                    if (j * kTileKeys + kTileKeys > u.P) {   // a masked weight is zero whatever the row's scale is
-#pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            const int cc = c + 2 * e;
-                            if (t[cc] == -INFINITY) h[e] &= 0xffff0000u;
-                            if (t[cc + 1] == -INFINITY) h[e] &= 0xffffu;
-                        }
-                    }
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        a1[e] = hsub2(h[e], h[e] & 0xff00ff00u);
-                        a2[e] = hsub2(a1[e], a1[e] & 0xff00ff00u) + 0x00800080u;   // half a step: rounded
-                    }
-                    w0[c / 4] = __byte_perm(h[0], h[1], 0x7531);
-                    w1[c / 4] = __byte_perm(a1[0], a1[1], 0x7531);
-                    w2[c / 4] = __byte_perm(a2[0], a2[1], 0x7531);
+                    exponents();
                 }
                 // P's one buffer is free once the product before this one has read it
                 if (ok && j > u.j0 && !mbar_wait_warp(pvdone, (uint32_t)(g - 1) & 1u)) ok = false;
-                if (ok) {
-                    unsigned char *pd = fix + C::FIX_P + kslot * 64;
-                    const int flip = (kslot >> 1) & 3;
-                    auto put = [&](const uint32_t (&w)[CG / 4], int term) {
-                        constexpr int STEP = CG % 16 == 0 ? 16 : 8;
+                const float2 rv = make_float2(vs * iref, vs * iref);
+                unsigned char *pd = fix + C::FIX_P + kslot * 64;
+                const int flip = (kslot >> 1) & 3;
+                constexpr int STEP = CG % 16 == 0 ? 16 : 8;
 #pragma unroll
-                        for (int c = 0; c < CG; c += STEP) {
-                            const int col = term * RP + cb + c;
-                            unsigned char *p = pd + (col >> 6) * C::P_ATOM + ((((col >> 4) & 3) ^ flip) << 4) + (col & 15);
-                            if constexpr (STEP == 16) *(uint4 *)p = make_uint4(w[c / 4], w[c / 4 + 1], w[c / 4 + 2], w[c / 4 + 3]);
-                            else *(uint2 *)p = make_uint2(w[c / 4], w[c / 4 + 1]);
+                for (int c = 0; c < CG; c += STEP) {
+                    uint32_t w[3][STEP / 4];   // the three parts, four columns a word
+#pragma unroll
+                    for (int i = 0; i < STEP / 4; ++i) {
+                        uint32_t h[2], a1[2], a2[2];
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const int cc = c / 2 + 2 * i + e;
+                            const float2 pe = make_float2(ex2(p[cc].x), ex2(p[cc].y));
+                            l[cc] = __fadd2_rn(l[cc], pe);
+                            const float2 pr = __fmul2_rn(pe, rv);
+                            h[e] = half2_of(pr.x, pr.y);
+                            a1[e] = hsub2(h[e], h[e] & 0xff00ff00u);
+                            a2[e] = hsub2(a1[e], a1[e] & 0xff00ff00u) + 0x00800080u;   // half a step: rounded
                         }
-                    };
-                    put(w0, 0);
-                    put(w1, 1);
-                    put(w2, 2);
+                        w[0][i] = __byte_perm(h[0], h[1], 0x7531);
+                        w[1][i] = __byte_perm(a1[0], a1[1], 0x7531);
+                        w[2][i] = __byte_perm(a2[0], a2[1], 0x7531);
+                    }
+                    if (ok) {
+#pragma unroll
+                        for (int t = 0; t < 3; ++t) {
+                            const int col = t * RP + cb + c;
+                            unsigned char *d = pd + (col >> 6) * C::P_ATOM + ((((col >> 4) & 3) ^ flip) << 4) + (col & 15);
+                            if constexpr (STEP == 16) *(uint4 *)d = make_uint4(w[t][0], w[t][1], w[t][2], w[t][3]);
+                            else *(uint2 *)d = make_uint2(w[t][0], w[t][1]);
+                        }
+                    }
                 }
                 if (j * kTileKeys + kTileKeys > L && ok) {
                     // V's rows past the last key may hold anything: zeros (whose weights are zero too)
@@ -803,14 +839,15 @@ __global__ void __launch_bounds__(Cfg8<D, RP>::THREADS, 1)
 
             // ---- the unit's output
 #pragma unroll
-            for (int c = 0; c < CG / 16 * 16; c += 16) {
-                reduce_scatter<16>(l + c, lane);
-                if (!(lane & 1)) ls_s[quarter * 64 + cb + c + (lane >> 1)] = l[c];
-            }
-            if constexpr (CG % 16 != 0) {
-                constexpr int c = CG / 16 * 16;
-                reduce_scatter<8>(l + c, lane);
-                if (!(lane & 3)) ls_s[quarter * 64 + cb + c + (lane >> 2)] = l[c];
+            for (int c = 0; c < CG; c += 8) {
+                float v[8];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    v[2 * e] = l[c / 2 + e].x;
+                    v[2 * e + 1] = l[c / 2 + e].y;
+                }
+                reduce_scatter<8>(v, lane);
+                if (!(lane & 3)) ls_s[quarter * 64 + cb + c + (lane >> 2)] = v[0];
             }
             bar_sync(bar, 128);
             float lsum = 0.f;
@@ -824,7 +861,7 @@ __global__ void __launch_bounds__(Cfg8<D, RP>::THREADS, 1)
                 float mm = 0.f;
 #pragma unroll
                 for (int c = 0; c < CG; ++c)
-                    if (gt == c) mm = -m[c];
+                    if (gt == c) mm = -(c & 1 ? m[c / 2].y : m[c / 2].x);
                 if (gt < CG) a.part_ml[(size_t)(u.slot + u.part) * RP + cb + gt] = make_float2(mm, lsum);
             }
             if (ok && !mbar_wait_warp(pvdone, (uint32_t)(g - 1) & 1u)) ok = false;
