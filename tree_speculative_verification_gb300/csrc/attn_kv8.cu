@@ -33,13 +33,12 @@
 //   warp 0      TMA producer and queue: K and V tiles into a ring of stages; the
 //               tile's scales and, for tree keys, subtree ends by cp.async on the
 //               same mbarrier
-//   warp 1      MMA issuer: S(g + 1) is issued before O += P(g) V(g)
-//   warps 2-9   softmax: two groups of four warps take half the columns each, lane
-//               = key. The running maximum of a column is raised only when a score
+//   warps 1, 2  issue the scores, up to two tiles ahead, and O += P V
+//   warp 3      the next unit's query rows, split, into the other Q buffer
+//   softmax     groups of four warps, 16 columns (8 of RP = 16) a group, lane = key. The running maximum of a column is raised only when a score
 //               passes it by 2^4 (one vote per tile and group), so the common tile
 //               has no reduction over keys. Tree node j is seen by the rows of its
 //               subtree, one interval of rows.
-//   warps 10-11 the next unit's query rows, split, into the other Q buffer
 // Every wait is bounded; a wait that gives up sets TS_STATUS_TIMEOUT, the others
 // follow by their own limits or the group's vote, and TMEM is freed.
 #include <cuda.h>
@@ -87,6 +86,12 @@ __device__ __forceinline__ void tc_st4(uint32_t taddr, const float *v) {
                  : "memory");
 }
 
+template <int N>
+__device__ __forceinline__ void tc_ldn(uint32_t taddr, float (&v)[N]) {
+    if constexpr (N == 16) tc_ld16(taddr, v);
+    else tc_ld8(taddr, v);
+}
+
 // Maximum over the warp, NaN left out.
 __device__ __forceinline__ float warp_max(float v) {
     float r;
@@ -112,9 +117,57 @@ __device__ __forceinline__ void bar_sync(int id, int threads) {
 __device__ __forceinline__ void cp_async4(uint32_t dst, const void *src, bool valid) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(valid ? 4 : 0) : "memory");
 }
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool valid) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(valid ? 16 : 0) : "memory");
+}
 // One arrival of this thread once its copies so far have landed.
 __device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
     asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
+
+// Bounded wait for a phase: try_wait suspends the thread in hardware for up to a microsecond a try, and the tries are
+// limited (a second or so at most; every wait here is for warps of the same CTA).
+__device__ __forceinline__ bool wait1(uint32_t bar, uint32_t phase) {
+    for (int i = 0; i < 1 << 20; ++i) {
+        uint32_t ok;
+        asm volatile(
+            "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n selp.u32 %0, 1, 0, p;\n}\n"
+            : "=r"(ok)
+            : "r"(bar), "r"(phase), "r"(1000)
+            : "memory");
+        if (ok) return true;
+    }
+    return false;
+}
+// The same by a whole warp, one verdict for every lane.
+__device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t phase) { return __all_sync(~0u, wait1(bar, phase)); }
+
+// Shared memory by its 32-bit address.
+__device__ __forceinline__ float4 lds4(uint32_t a) {
+    float4 v;
+    asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(a) : "memory");
+    return v;
+}
+__device__ __forceinline__ float lds1(uint32_t a) {
+    float v;
+    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
+    return v;
+}
+__device__ __forceinline__ int ldsi(uint32_t a) {
+    int v;
+    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+    return v;
+}
+__device__ __forceinline__ void sts1(uint32_t a, float v) { asm volatile("st.shared.f32 [%0], %1;" ::"r"(a), "f"(v) : "memory"); }
+__device__ __forceinline__ void stsi(uint32_t a, int v) { asm volatile("st.shared.b32 [%0], %1;" ::"r"(a), "r"(v) : "memory"); }
+__device__ __forceinline__ void sts4(uint32_t a, float4 v) {
+    asm volatile("st.shared.v4.f32 [%0], {%1,%2,%3,%4};" ::"r"(a), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w) : "memory");
+}
+__device__ __forceinline__ void sts4u(uint32_t a, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
+    asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
+}
+__device__ __forceinline__ void sts2u(uint32_t a, uint32_t x, uint32_t y) {
+    asm volatile("st.shared.v2.b32 [%0], {%1,%2};" ::"r"(a), "r"(x), "r"(y) : "memory");
 }
 
 __device__ __forceinline__ uint32_t half2_of(float lo, float hi) {
@@ -140,7 +193,7 @@ struct Attn8Args {
     PagedArgs pg;
     uint32_t *status;
     unsigned *queue;      // [0] next unit, [1] CTAs finished
-    unsigned *joins;      // [slots][2] parts done, by the item's first slot and column group
+    unsigned *joins;      // [slots][4] parts done, by the item's first slot and column group
     float2 *part_ml;      // [slots][RP] (maximum, sum)
     float *part_o;        // [slots][RP][D]
     int slots;
@@ -152,35 +205,39 @@ constexpr int kMaxCuts = 32;       // parts of one item (a lane each when they a
 constexpr int kMinCut = 3;         // tiles of a part at least
 constexpr int kCutsPerSm = 2;      // units per SM that cutting aims at
 constexpr int kRing = 4;           // published units
+constexpr int kClaimAhead = 6;
 
 template <int D_, int RP_>
 struct Cfg8 {
-    static constexpr int D = D_, RP = RP_, CG = RP / 2;
-    static constexpr int SM_WARPS = 8, THREADS = 32 * (2 + SM_WARPS + 2);
+    static constexpr int D = D_, RP = RP_, CG = RP == 16 ? 8 : 16, GROUPS = RP / CG;   // columns of a softmax group
+    static constexpr int SM_WARPS = 4 * GROUPS, THREADS = 32 * (4 + SM_WARPS);
     static constexpr int OP_BYTES = kTileKeys * D;             // codes of one operand tile
     static constexpr int STAGE_BYTES = 2 * OP_BYTES;
     static constexpr int P_ATOMS = (3 * RP + 63) / 64, P_ATOM = kTileKeys * 64, P_BYTES = P_ATOMS * P_ATOM;
     static constexpr int Q_BYTES = 2 * RP * D;
     static constexpr int SIDE = 3 * kTileKeys * 4;             // a stage's key scales, value scales, subtree ends
     // fixed part, behind the stages
-    static constexpr int FIX_P = 0, FIX_Q = FIX_P + P_BYTES, FIX_MX = FIX_Q + 2 * Q_BYTES;
-    static constexpr int FIX_LS = FIX_MX + 2 * 4 * 32 * 4;     // column maxima [2 groups][4 warps][32]
+    static constexpr int FIX_P = 0, FIX_Q = FIX_P + 2 * P_BYTES, FIX_MX = FIX_Q + 2 * Q_BYTES;
+    static constexpr int FIX_LS = FIX_MX + 4 * RP * 4;         // column maxima [groups][4 warps][CG]
     static constexpr int FIX_F = FIX_LS + 4 * 64 * 4;          // column sums [4 warps][64], then factors [64]
-    static constexpr int FIX_QS = FIX_F + 64 * 4;              // query scales [kRing][64], output rows [kRing][64]
+    static constexpr int FIX_V = FIX_F + 64 * 4;               // largest value scales [groups][4 warps]
+    static constexpr int FIX_QS = FIX_V + 64;                  // query scales [kRing][64], output rows [kRing][64]
     static constexpr int FIX_QROW = FIX_QS + kRing * 64 * 4;
     static constexpr int FIX_REQ = FIX_QROW + kRing * 64 * 4;  // (n, P) by request, then order, first unit, first slot
     static constexpr int FIX_ORDER = FIX_REQ + kReqCache * 8, FIX_UNIT = FIX_ORDER + kReqCache * 4;
     static constexpr int FIX_SLOT = FIX_UNIT + kReqCache * 4;
     static constexpr int FIX_INFO = FIX_SLOT + kReqCache * 4;  // units [kRing][12]
-    static constexpr int FIX_MISC = FIX_INFO + kRing * 12 * 4; // 0 TMEM base, 1 timeout, 2 units, 3 tiles a part, 4-5 last
+    static constexpr int FIX_MISC = FIX_INFO + kRing * 12 * 4; // 0 TMEM base, 1 timeout, 2 units, 3 tiles a part, 4-7 last
     static constexpr int FIX_BAR = FIX_MISC + 64;
     static constexpr int FIX_END = FIX_BAR + 64 * 8;
-    static constexpr int LIMIT = 232448 - 2 * 1024;            // the base and the fixed part are 1024-byte aligned
-    static constexpr int FIT = (LIMIT - FIX_END) / (STAGE_BYTES + SIDE);
-    static constexpr int STAGES = FIT < 8 ? FIT : 8;
-    static constexpr int OFF_SIDE = STAGES * STAGE_BYTES;
-    static constexpr int OFF_FIX = (OFF_SIDE + STAGES * SIDE + 1023) / 1024 * 1024;
-    static constexpr int SMEM = OFF_FIX + FIX_END + 1024;
+    static constexpr int off_fix(int stages) { return (stages * (STAGE_BYTES + SIDE) + 1023) / 1024 * 1024; }
+    static constexpr int fit() {
+        int n = 8;
+        while (off_fix(n) + FIX_END + 1024 > 232448) --n;
+        return n;
+    }
+    static constexpr int STAGES = fit();
+    static constexpr int OFF_SIDE = STAGES * STAGE_BYTES, OFF_FIX = off_fix(STAGES), SMEM = OFF_FIX + FIX_END + 1024;
     static constexpr uint32_t S_COL = 0, O_COL = 4 * RP;       // two score buffers of 2 RP columns, O of 3 RP
     static constexpr uint32_t TMEM_COLS = 7 * RP <= 128 ? 128 : 7 * RP <= 256 ? 256 : 512;
     static_assert(STAGES >= 3 && SMEM <= 232448 && STAGE_BYTES % 1024 == 0 && FIX_Q % 1024 == 0 && Q_BYTES % 1024 == 0,
@@ -191,22 +248,19 @@ struct Unit8 {
     int b, h, row0, n, P, j0, j1, parts, part, slot;   // tiles [j0, j1); slot: of the item's first part
 };
 
-template <int N>
+// Sums of N columns over the warp: column lane / (32 / N) ends in v[0].
+template <int N, int W = 16>
 __device__ __forceinline__ void reduce_scatter(float *v, int lane) {
-    // sums of N columns over the warp: column lane / (32 / N) ends in v[0]
+    if constexpr (N > 1) {
 #pragma unroll
-    for (int w = 16, n = N; w; w >>= 1) {
-        if (n > 1) {
-            n >>= 1;
-#pragma unroll
-            for (int i = 0; i < n; ++i) {
-                const float keep = lane & w ? v[i + n] : v[i], send = lane & w ? v[i] : v[i + n];
-                v[i] = keep + __shfl_xor_sync(~0u, send, w);
-            }
-        } else {
-            v[0] += __shfl_xor_sync(~0u, v[0], w);
+        for (int i = 0; i < N / 2; ++i) {
+            const float keep = lane & W ? v[i + N / 2] : v[i], send = lane & W ? v[i] : v[i + N / 2];
+            v[i] = keep + __shfl_xor_sync(~0u, send, W);
         }
+    } else {
+        v[0] += __shfl_xor_sync(~0u, v[0], W);
     }
+    if constexpr (W > 1) reduce_scatter<(N > 1 ? N / 2 : 1), W / 2>(v, lane);
 }
 
 template <int D, int RP>
@@ -220,9 +274,6 @@ __global__ void __launch_bounds__(Cfg8<D, RP>::THREADS, 1)
     volatile int *misc = (volatile int *)(fix + C::FIX_MISC);
     int2 *req_s = (int2 *)(fix + C::FIX_REQ);
     int *order_s = (int *)(fix + C::FIX_ORDER), *unit_s = (int *)(fix + C::FIX_UNIT), *slot_s = (int *)(fix + C::FIX_SLOT);
-    volatile int *info_s = (volatile int *)(fix + C::FIX_INFO);
-    const float *qs_s = (const float *)(fix + C::FIX_QS);
-    const int *qrow_s = (const int *)(fix + C::FIX_QROW);
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int B = a.t.B, n_max = a.t.n_max;
@@ -230,8 +281,8 @@ __global__ void __launch_bounds__(Cfg8<D, RP>::THREADS, 1)
     pdl_trigger();
 
     const uint32_t full = fix_base + C::FIX_BAR, empty = full + 8 * C::STAGES, sfull = empty + 8 * C::STAGES;
-    const uint32_t pfull = sfull + 16, pvdone = pfull + 8, qready = pvdone + 8, qfree = qready + 16, ofree = qfree + 16;
-    const uint32_t fin = ofree + 8, iready = fin + 8, ifree = iready + 8 * kRing;
+    const uint32_t pfull = sfull + 16, pvdone = pfull + 16, qready = pvdone + 16, qfree = qready + 16;
+    const uint32_t fin = qfree + 16, iready = fin + 16, ifree = iready + 8 * kRing;
 
     if (warp == 0) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32((void *)misc)),
@@ -245,17 +296,16 @@ __global__ void __launch_bounds__(Cfg8<D, RP>::THREADS, 1)
             mbar_init(empty + 8 * s, 1);
         }
         for (int x = 0; x < 2; ++x) {
-            mbar_init(sfull + 8 * x, 1);
-            mbar_init(qready + 8 * x, 2);
+            mbar_init(sfull + 8 * x, 2);   // the scores, and the issuer's sight of the stage (scales by cp.async)
+            mbar_init(pfull + 8 * x, C::SM_WARPS);
+            mbar_init(pvdone + 8 * x, 1);
+            mbar_init(qready + 8 * x, 1);
             mbar_init(qfree + 8 * x, 1);
+            mbar_init(fin + 8 * x, 1);
         }
-        mbar_init(pfull, C::SM_WARPS);
-        mbar_init(pvdone, 1);
-        mbar_init(ofree, C::SM_WARPS);
-        mbar_init(fin, 1);
         for (int r = 0; r < kRing; ++r) {
             mbar_init(iready + 8 * r, 1);
-            mbar_init(ifree + 8 * r, 1 + C::SM_WARPS + 2);
+            mbar_init(ifree + 8 * r, 3 + C::SM_WARPS);
         }
         misc[1] = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -382,35 +432,49 @@ __global__ void __launch_bounds__(Cfg8<D, RP>::THREADS, 1)
         return true;
     };
     auto read_unit = [&](int r) -> Unit8 {
-        const volatile int *i = info_s + r * 12;
-        return Unit8{i[0], i[1], i[2], i[3], i[4], i[5], i[6], i[7], i[8], i[9]};
+        const uint32_t i = fix_base + C::FIX_INFO + r * 48;
+        return Unit8{ldsi(i), ldsi(i + 4), ldsi(i + 8), ldsi(i + 12), ldsi(i + 16), ldsi(i + 20), ldsi(i + 24), ldsi(i + 28),
+                     ldsi(i + 32), ldsi(i + 36)};
     };
 
+    constexpr uint64_t swz = D == 128 ? kSwz128 : kSwz64;
     if (warp == 0) {   // ------------------------------------------------ producer and queue
-        int g = 0;
+        int g = 0, k = 0;
         bool ok = true;
         auto next = [&]() -> int { return lane == 0 ? (int)atomicAdd(a.queue, 1u) : 0; };
-        int q = __shfl_sync(~0u, next(), 0), k = 0;
-        Unit8 u;
-        for (;;) {
+        // the unit of queue place q, or of the first one after it that is not empty, into ring slot k
+        auto publish = [&](int q, Unit8 &u) -> bool {
             while (q < units && !decode(q, u)) q = __shfl_sync(~0u, next(), 0);
             const int r = k % kRing;
-            if (k >= kRing && !mbar_wait_warp(ifree + 8 * r, (uint32_t)(k / kRing - 1) & 1u)) {
+            if (k >= kRing && !wait_warp(ifree + 8 * r, (uint32_t)(k / kRing - 1) & 1u)) {
                 ok = false;
-                break;
+                return false;
             }
             if (lane == 0) {
-                volatile int *i = info_s + r * 12;
-                i[0] = q < units ? u.b : -1;
-                i[1] = u.h; i[2] = u.row0; i[3] = u.n; i[4] = u.P; i[5] = u.j0; i[6] = u.j1;
-                i[7] = u.parts; i[8] = u.part; i[9] = u.slot;
+                const uint32_t i = fix_base + C::FIX_INFO + r * 48;
+                const int v[10] = {q < units ? u.b : -1, u.h, u.row0, u.n, u.P, u.j0, u.j1, u.parts, u.part, u.slot};
+#pragma unroll
+                for (int e = 0; e < 10; ++e) stsi(i + 4 * e, v[e]);
                 mbar_arrive(iready + 8 * r);
             }
-            if (q >= units) break;
-            const int qn = next();   // in flight over this unit's loads
+            ++k;
+            return q < units;
+        };
+        Unit8 u = {}, un = {};
+        bool more = publish(__shfl_sync(~0u, next(), 0), u);
+        while (more) {
+            // the next unit is taken kClaimAhead tiles before this one's last load, late enough that CTAs share the
+            // last units evenly, early enough that its query rows are staged in time
+            const int claim = u.j1 - kClaimAhead > u.j0 ? u.j1 - kClaimAhead : u.j0;
+            int qn = 0;
             const int L = u.P + u.n;
             const int strip = (u.b * a.H + u.h) * a.rows;   // dense: the cache row of key 0
             for (int j = u.j0; j < u.j1; ++j, ++g) {
+                if (j == claim) qn = next();
+                if (j == claim + 1) {
+                    more = publish(__shfl_sync(~0u, qn, 0), un);
+                    if (!ok) break;
+                }
                 const int st = g % C::STAGES, key0 = j * kTileKeys;
                 const bool two = key0 + 64 < L;
                 int row0 = strip + key0, row1 = row0 + 64;
@@ -424,7 +488,7 @@ __global__ void __launch_bounds__(Cfg8<D, RP>::THREADS, 1)
                     row0 = has0 ? (p0 * a.H + u.h) * TS_PAGE_KEYS : 0x7fffff00;
                     row1 = has1 ? (p1 * a.H + u.h) * TS_PAGE_KEYS : 0x7fffff00;
                 }
-                if (g >= C::STAGES && !mbar_wait_warp(empty + 8 * st, (uint32_t)(g / C::STAGES - 1) & 1u)) {
+                if (g >= C::STAGES && !wait_warp(empty + 8 * st, (uint32_t)(g / C::STAGES - 1) & 1u)) {
                     ok = false;
                     break;
                 }
@@ -463,148 +527,175 @@ __global__ void __launch_bounds__(Cfg8<D, RP>::THREADS, 1)
                 }
                 cp_async_arrive(fb);
             }
+            if (ok && claim + 1 >= u.j1) more = publish(__shfl_sync(~0u, qn, 0), un);
             if (!ok) break;
-            q = __shfl_sync(~0u, qn, 0);
-            ++k;
+            u = un;
         }
         if (!ok) {   // leave no copy in flight
             if (lane == 0) misc[1] = 1;
             for (int i = g > C::STAGES ? g - C::STAGES : 0; i < g; ++i)
-                mbar_wait_warp(full + 8 * (i % C::STAGES), (uint32_t)(i / C::STAGES) & 1u);
+                wait_warp(full + 8 * (i % C::STAGES), (uint32_t)(i / C::STAGES) & 1u);
         }
     } else if (warp == 1) {   // ----------------------------------------- MMA issuer
         if (lane == 0) {
             constexpr uint32_t idesc_s = idesc_f8(128, 2 * RP, false, false, false);
-            constexpr uint32_t idesc_o = idesc_f8(128, 3 * RP, true, true, true);
-            constexpr uint64_t swz = D == 128 ? kSwz128 : kSwz64;
             bool ok = true;
-            auto issue_s = [&](int g, int qb) -> bool {
-                const int st = g % C::STAGES, x = g & 1;
-                if (!mbar_wait_bounded(full + 8 * st, (uint32_t)(g / C::STAGES) & 1u)) return false;
-                tc_fence_after();
-                const uint32_t kb = sm_base + st * C::STAGE_BYTES, qd = fix_base + C::FIX_Q + qb * C::Q_BYTES;
-#pragma unroll
-                for (int kk = 0; kk < D / 32; ++kk)
-                    tc_mma_f8(tmem + C::S_COL + x * 2 * RP, smem_desc8(kb + kk * 32, 16, 8 * D, swz),
-                              smem_desc8(qd + kk * 32, 16, 8 * D, swz), idesc_s, kk > 0);
-                tc_commit(sfull + 8 * x);
-                return true;
-            };
-            // the first tile of unit k starts O afresh, once unit k - 1's has been read out of it
-            auto issue_o = [&](int g, bool first, int k) -> bool {
-                const int st = g % C::STAGES;
-                if (first && k >= 1 && !mbar_wait_bounded(ofree, (uint32_t)(k - 1) & 1u)) return false;
-                if (!mbar_wait_bounded(pfull, (uint32_t)g & 1u)) return false;
-                tc_fence_after();
-                const uint32_t vb = sm_base + st * C::STAGE_BYTES + C::OP_BYTES, pd = fix_base + C::FIX_P;
-                // V^T: dims contiguous; d = 64 repeats its 64 rows (stride 0) to the MMA's 128
-#pragma unroll
-                for (int kk = 0; kk < kTileKeys / 32; ++kk)
-                    tc_mma_f8(tmem + C::O_COL, smem_desc8(vb + kk * 32 * D, 0, 8 * D, swz),
-                              smem_desc8(pd + kk * 32 * 64, C::P_ATOM, 512, kSwz64), idesc_o, !first || kk > 0);
-                tc_commit(empty + 8 * st);
-                tc_commit(pvdone);
-                return true;
-            };
-            int g = 0, pend = -1, pend_k = 0;
-            bool pend_first = false;
+            int g = 0;
             for (int k = 0; ok; ++k) {
                 const int r = k % kRing;
-                if (!mbar_wait_bounded(iready + 8 * r, (uint32_t)(k / kRing) & 1u)) { ok = false; break; }
+                if (!wait1(iready + 8 * r, (uint32_t)(k / kRing) & 1u)) { ok = false; break; }
                 const Unit8 u = read_unit(r);
                 mbar_arrive(ifree + 8 * r);
                 if (u.b < 0) break;
-                if (!mbar_wait_bounded(qready + 8 * (k & 1), (uint32_t)(k >> 1) & 1u)) { ok = false; break; }
-                for (int j = u.j0; j < u.j1 && ok; ++j, ++g) {
-                    // score buffer g & 1 was read before O(g - 2) was issued
-                    if (!issue_s(g, k & 1)) { ok = false; break; }
-                    if (j == u.j1 - 1) tc_commit(qfree + 8 * (k & 1));
-                    if (pend >= 0 && !issue_o(pend, pend_first, pend_k)) { ok = false; break; }
-                    pend = g;
-                    pend_first = j == u.j0;
-                    pend_k = k;
+                if (!wait1(qready + 8 * (k & 1), (uint32_t)(k >> 1) & 1u)) { ok = false; break; }
+                for (int j = u.j0; j < u.j1; ++j, ++g) {
+                    const int st = g % C::STAGES, x = g & 1;
+                    // the product of tile g - 2 is done: S(g - 2) was read and P(g - 2) is free, for who waits for S(g)
+                    if ((g >= 2 && !wait1(pvdone + 8 * x, (uint32_t)((g - 2) >> 1) & 1u)) ||
+                        !wait1(full + 8 * st, (uint32_t)(g / C::STAGES) & 1u)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t kb = sm_base + st * C::STAGE_BYTES, qd = fix_base + C::FIX_Q + (k & 1) * C::Q_BYTES;
+#pragma unroll
+                    for (int kk = 0; kk < D / 32; ++kk)
+                        tc_mma_f8(tmem + C::S_COL + x * 2 * RP, smem_desc8(kb + kk * 32, 16, 8 * D, swz),
+                                  smem_desc8(qd + kk * 32, 16, 8 * D, swz), idesc_s, kk > 0);
+                    tc_commit(sfull + 8 * x);
+                    mbar_arrive(sfull + 8 * x);
                 }
+                if (ok) tc_commit(qfree + 8 * (k & 1));   // the unit's query rows may be overwritten
             }
-            if (ok && pend >= 0) ok = issue_o(pend, pend_first, pend_k);
             if (!ok) misc[1] = 1;
             tc_commit(fin);
-            if (!mbar_wait_bounded(fin, 0)) misc[1] = 1;
+            if (!wait1(fin, 0)) misc[1] = 1;
         }
         __syncwarp();
-    } else if (warp >= 2 + C::SM_WARPS) {   // --------------------------- query rows
-        constexpr int EPL = D / 32, AHEAD = 8;   // values a lane holds of a row; rows in flight
-        const int w = warp - (2 + C::SM_WARPS);
-        float *qs_w = (float *)(fix + C::FIX_QS);
-        int *qrow_w = (int *)(fix + C::FIX_QROW);
+    } else if (warp == 2) {   // ----------------------------------------- O += P V
+        // a thread of its own: a product waits for its tile's probabilities only, never for the next tile's load
+        if (lane == 0) {
+            constexpr uint32_t idesc_o = idesc_f8(128, 3 * RP, true, true, true);
+            bool ok = true;
+            int g = 0;
+            for (int k = 0; ok; ++k) {
+                const int r = k % kRing;
+                if (!wait1(iready + 8 * r, (uint32_t)(k / kRing) & 1u)) { ok = false; break; }
+                const Unit8 u = read_unit(r);
+                mbar_arrive(ifree + 8 * r);
+                if (u.b < 0) break;
+                for (int j = u.j0; j < u.j1; ++j, ++g) {
+                    const int st = g % C::STAGES, x = g & 1;
+                    if (!wait1(full + 8 * st, (uint32_t)(g / C::STAGES) & 1u) ||
+                        !wait1(pfull + 8 * x, (uint32_t)(g >> 1) & 1u)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t vb = sm_base + st * C::STAGE_BYTES + C::OP_BYTES, pd = fix_base + C::FIX_P + x * C::P_BYTES;
+                    // a unit's first product starts O afresh: each softmax warp wrote its P after it had read out O.
+                    // V^T: dims contiguous; d = 64 repeats its 64 rows (stride 0) to the MMA's 128
+#pragma unroll
+                    for (int kk = 0; kk < kTileKeys / 32; ++kk)
+                        tc_mma_f8(tmem + C::O_COL, smem_desc8(vb + kk * 32 * D, 0, 8 * D, swz),
+                                  smem_desc8(pd + kk * 32 * 64, C::P_ATOM, 512, kSwz64), idesc_o, j > u.j0 || kk > 0);
+                    tc_commit(empty + 8 * st);
+                    tc_commit(pvdone + 8 * x);
+                }
+            }
+            if (!ok) misc[1] = 1;
+            tc_commit(fin + 8);
+            if (!wait1(fin + 8, 0)) misc[1] = 1;
+        }
+        __syncwarp();
+    } else if (warp == 3) {   // ----------------------------------------- query rows
+        // A raw row of 2 * d bytes and its two parts of d bytes take the same room: each half of the row is copied
+        // to where a part will be, and half a warp turns a row into its parts in place.
+        constexpr int EPL = D / 16;   // values a lane holds of a row
+        const int sub = lane & 15, odd = lane >> 4;
         bool ok = true;
         for (int k = 0;; ++k) {
             const int r = k % kRing;
-            if (!mbar_wait_warp(iready + 8 * r, (uint32_t)(k / kRing) & 1u)) { ok = false; break; }
+            if (!wait_warp(iready + 8 * r, (uint32_t)(k / kRing) & 1u)) { ok = false; break; }
             const Unit8 u = read_unit(r);
             if (u.b < 0) break;
-            // rows w * RP/2 .. of the block; lane i looks up row i's place in q and out
-            constexpr int MINE = RP / 2;
-            int place = -1;
-            if (lane < MINE) {
-                const int rho = u.row0 + w * MINE + lane, i = rho / a.G;
-                if (i < u.n) {
-                    const int v = a.t.perm[(size_t)u.b * n_max + i];
-                    if (v >= 0 && v < n_max) place = v * a.Hq + u.h * a.G + (rho - i * a.G);
-                }
-                qrow_w[r * 64 + w * MINE + lane] = place;
-            }
-            if (k >= 2 && !mbar_wait_warp(qfree + 8 * (k & 1), (uint32_t)(k / 2 - 1) & 1u)) { ok = false; break; }
-            unsigned char *qd = fix + C::FIX_Q + (k & 1) * C::Q_BYTES;
-            const __nv_bfloat16 *qb = a.q + (size_t)u.b * n_max * a.Hq * D;
-#pragma unroll 1
-            for (int c0 = 0; c0 < MINE; c0 += AHEAD) {
-                uint2 raw[AHEAD];
+            // lane i looks up the places of rows i and 32 + i of the block in q and out
+            int place[2] = {-1, -1};
 #pragma unroll
-                for (int i = 0; i < AHEAD; ++i) {
-                    const int pl = __shfl_sync(~0u, place, c0 + i);
-                    raw[i] = make_uint2(0u, 0u);
-                    if (pl >= 0) {
-                        const __nv_bfloat16 *p = qb + (size_t)pl * D + lane * EPL;
-                        if constexpr (EPL == 4) raw[i] = __ldg(reinterpret_cast<const uint2 *>(p));
-                        else raw[i].x = __ldg(reinterpret_cast<const uint32_t *>(p));
+            for (int h = 0; h < 2; ++h) {
+                const int c = h * 32 + lane;
+                if (c < RP) {
+                    const int rho = u.row0 + c, i = rho / a.G;
+                    if (i < u.n) {
+                        const int v = a.t.perm[(size_t)u.b * n_max + i];
+                        if (v >= 0 && v < n_max) place[h] = v * a.Hq + u.h * a.G + (rho - i * a.G);
                     }
+                    stsi(fix_base + C::FIX_QROW + (r * 64 + c) * 4, place[h]);
                 }
-#pragma unroll
-                for (int i = 0; i < AHEAD; ++i) {
-                    float x[4] = {__uint_as_float(raw[i].x << 16), __uint_as_float(raw[i].x & 0xffff0000u),
-                                  __uint_as_float(raw[i].y << 16), __uint_as_float(raw[i].y & 0xffff0000u)};
+            }
+            if (k >= 2 && !wait_warp(qfree + 8 * (k & 1), (uint32_t)(k / 2 - 1) & 1u)) { ok = false; break; }
+            const uint32_t qd = fix_base + C::FIX_Q + (k & 1) * C::Q_BYTES;
+            const __nv_bfloat16 *qb = a.q + (size_t)u.b * n_max * a.Hq * D;
+            constexpr int VPR = D / 8;   // 16-byte pieces of a raw row
+#pragma unroll 4
+            for (int i = lane; i < RP * VPR; i += 32) {
+                const int c = i / VPR, v = i % VPR;
+                const int lo = __shfl_sync(~0u, place[0], c & 31), hi = __shfl_sync(~0u, place[1], c & 31);
+                const int pl = c < 32 ? lo : hi;
+                cp_async16(qd + ((v >= VPR / 2 ? RP : 0) + c) * D + (v % (VPR / 2)) * 16,
+                           qb + (size_t)(pl < 0 ? 0 : pl) * D + v * 8, pl >= 0);
+            }
+            asm volatile("cp.async.wait_all;" ::: "memory");
+            __syncwarp();
+#pragma unroll 4
+            for (int c0 = 0; c0 < RP; c0 += 2) {
+                {
+                    const int c = c0 + odd;
+                    uint32_t w[4] = {0u, 0u, 0u, 0u};
+                    const uint32_t src = qd + ((sub >= 8 ? RP : 0) + c) * D + (sub & 7) * (2 * EPL);
+                    if constexpr (EPL == 8)
+                        asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(src) : "memory");
+                    else
+                        asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(src) : "memory");
                     uint32_t top = 0;   // |values| order as their bits do, infinities and NaN on top
 #pragma unroll
-                    for (int e = 0; e < EPL; ++e) top = max(top, __float_as_uint(x[e]) & 0x7fffffffu);
-                    top = __reduce_max_sync(~0u, top);
+                    for (int e = 0; e < EPL / 2; ++e) top = max(top, max(w[e] & 0x7fff0000u, (w[e] << 16) & 0x7fff0000u));
+#pragma unroll
+                    for (int o = 8; o; o >>= 1) top = max(top, __shfl_xor_sync(~0u, top, o));
                     // 2^(exponent - 7), within the normal numbers whose reciprocal is one too
                     int ex = (int)(top >> 23) - 7;
                     ex = ex < 4 ? 4 : ex;
-                    const float sc = __uint_as_float((uint32_t)ex << 23), inv = __uint_as_float((uint32_t)(254 - ex) << 23);
-                    uint32_t hi = 0, lo = 0;
+                    const float inv = __uint_as_float((uint32_t)(254 - ex) << 23);
+                    uint32_t hi[EPL / 4], lo[EPL / 4];
 #pragma unroll
-                    for (int e = 0; e < EPL; e += 2) {
-                        const float y0 = x[e] * inv, y1 = x[e + 1] * inv;
-                        const uint16_t h2 = __nv_cvt_float2_to_fp8x2(make_float2(y0, y1), __NV_SATFINITE, __NV_E4M3);
-                        const float2 f = fp8x2_to_float2(h2);
-                        const uint16_t l2 = __nv_cvt_float2_to_fp8x2(make_float2(y0 - f.x, y1 - f.y), __NV_SATFINITE, __NV_E4M3);
-                        hi |= (uint32_t)h2 << (e * 8);
-                        lo |= (uint32_t)l2 << (e * 8);
+                    for (int e = 0; e < EPL / 4; ++e) {
+                        uint32_t h2[2], l2[2];
+#pragma unroll
+                        for (int f = 0; f < 2; ++f) {
+                            const uint32_t v = w[2 * e + f];
+                            const float2 y = __fmul2_rn(make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u)),
+                                                        make_float2(inv, inv));
+                            h2[f] = __nv_cvt_float2_to_fp8x2(y, __NV_SATFINITE, __NV_E4M3);
+                            const float2 b = fp8x2_to_float2((uint16_t)h2[f]);
+                            l2[f] = __nv_cvt_float2_to_fp8x2(make_float2(y.x - b.x, y.y - b.y), __NV_SATFINITE, __NV_E4M3);
+                        }
+                        hi[e] = h2[0] | h2[1] << 16;
+                        lo[e] = l2[0] | l2[1] << 16;
                     }
-                    const int c = w * MINE + c0 + i;
                     // 16-byte chunks of a row are permuted as the MMA's descriptor says
                     auto at = [&](int row) {
-                        return D == 128 ? row * 128 + (((lane >> 2) ^ (row & 7)) << 4) + (lane & 3) * 4
-                                        : row * 64 + (((lane >> 3) ^ ((row >> 1) & 3)) << 4) + (lane & 7) * 2;
+                        return D == 128 ? row * 128 + (((sub >> 1) ^ (row & 7)) << 4) + (sub & 1) * 8
+                                        : row * 64 + (((sub >> 2) ^ ((row >> 1) & 3)) << 4) + (sub & 3) * 4;
                     };
-                    if constexpr (EPL == 4) {
-                        *(uint32_t *)(qd + at(c)) = hi;
-                        *(uint32_t *)(qd + at(RP + c)) = lo;
+                    if constexpr (EPL == 8) {
+                        sts2u(qd + at(c), hi[0], hi[1]);
+                        sts2u(qd + at(RP + c), lo[0], lo[1]);
                     } else {
-                        *(uint16_t *)(qd + at(c)) = (uint16_t)hi;
-                        *(uint16_t *)(qd + at(RP + c)) = (uint16_t)lo;
+                        stsi(qd + at(c), (int)hi[0]);
+                        stsi(qd + at(RP + c), (int)lo[0]);
                     }
-                    if (lane == 0) qs_w[r * 64 + c] = top >= 0x7f800000u ? __int_as_float(0x7fc00000) : sc;
+                    if (sub == 0)
+                        stsi(fix_base + C::FIX_QS + (r * 64 + c) * 4, top >= 0x7f800000u ? 0x7fc00000 : (int)((uint32_t)ex << 23));
                 }
             }
             fence_async_smem();
@@ -620,17 +711,17 @@ __global__ void __launch_bounds__(Cfg8<D, RP>::THREADS, 1)
         // p is 2^kBase at the running maximum, which is raised once a score passes it by 2^kOver: fp16 (and e5m2) hold
         // both ends, and what is 2^-24 of the maximum still has a bit
         constexpr float kBase = 7.f, kOver = 8.f;
-        const int grp = (warp - 2) >> 2, quarter = warp & 3, cb = grp * CG;
-        const int bar = 1 + grp, gt = (warp - 2 - 4 * grp) * 32 + lane;   // thread of the group
+        const int grp = (warp - 4) >> 2, quarter = warp & 3, cb = grp * CG;
+        const int bar = 1 + grp, gt = quarter * 32 + lane;   // thread of the group
         const uint32_t tl = tmem + ((uint32_t)(quarter * 32) << 16);
         const int kslot = quarter * 32 + lane;   // this lane's key of a tile, and its dim of O
-        float *mx_s = (float *)(fix + C::FIX_MX) + grp * 4 * 32, *ls_s = (float *)(fix + C::FIX_LS);
-        float *f_s = (float *)(fix + C::FIX_F) + cb;
+        const uint32_t mx_s = fix_base + C::FIX_MX + grp * 16 * CG, ls_s = fix_base + C::FIX_LS;
+        const uint32_t f_s = fix_base + C::FIX_F + cb * 4, v_s = fix_base + C::FIX_V + grp * 16;
         bool ok = true;
         int g = 0;
         for (int k = 0;; ++k) {
             const int r = k % kRing;
-            if (!mbar_wait_warp(iready + 8 * r, (uint32_t)(k / kRing) & 1u)) ok = false;
+            if (!wait_warp(iready + 8 * r, (uint32_t)(k / kRing) & 1u)) ok = false;
             if (bar_any(bar, 128, !ok)) {   // all of the group go on, or none
                 ok = false;
                 break;
@@ -638,159 +729,140 @@ __global__ void __launch_bounds__(Cfg8<D, RP>::THREADS, 1)
             const Unit8 u = read_unit(r);
             if (u.b < 0) break;
             const int L = u.P + u.n;
-            float2 m[CG / 2], l[CG / 2], qs[CG / 2];   // kBase - maximum; sums over this lane's keys; query scales
+            float2 m[CG / 2], l[CG / 2];   // kBase - maximum; sums over this lane's keys
             float ref = 0.f, iref = 0.f;               // the value scales' reference and its reciprocal
 #pragma unroll
             for (int c = 0; c < CG / 2; ++c) {
                 m[c] = make_float2(1e30f, 1e30f);
                 l[c] = make_float2(0.f, 0.f);
             }
+            const uint32_t qs = fix_base + C::FIX_QS + (r * 64 + cb) * 4;   // query scales, there before the first scores
             bool gone = false;
             for (int j = u.j0; j < u.j1; ++j, ++g) {
                 const int x = g & 1, st = g % C::STAGES, key = j * kTileKeys + kslot;
-                if (ok && !mbar_wait_warp(sfull + 8 * x, (uint32_t)(g >> 1) & 1u)) ok = false;
-                if (ok && !mbar_wait_warp(full + 8 * st, (uint32_t)(g / C::STAGES) & 1u)) ok = false;
+                if (ok && !wait_warp(sfull + 8 * x, (uint32_t)(g >> 1) & 1u)) ok = false;
                 tc_fence_after();
-                if (j == u.j0) {   // the scales were there before the first scores
-#pragma unroll
-                    for (int c = 0; c < CG; c += 4) {
-                        const float4 v = *(const float4 *)(qs_s + r * 64 + cb + c);
-                        qs[c / 2] = make_float2(v.x, v.y);
-                        qs[c / 2 + 1] = make_float2(v.z, v.w);
-                    }
-                }
-                const float *side = (const float *)(sm + C::OFF_SIDE + st * C::SIDE);
-                float ks = side[kslot] * a.scale_log2, vs = side[128 + kslot];
+                const uint32_t side = sm_base + C::OFF_SIDE + st * C::SIDE + kslot * 4;
+                float ks = lds1(side) * a.scale_log2, vs = lds1(side + 512);
                 if (!(vs <= 3.402823466e38f)) {   // a poisoned value row: NaN to every row that sees it
                     ks = __int_as_float(0x7fc00000);
                     vs = 0.f;
                 }
-                const bool edge = j * kTileKeys + kTileKeys > u.P;   // tree keys, or keys past the end
-                int from = -0x7fffffff, to = 0x7fffffff;             // the columns that see this lane's key
-                if (edge && key >= u.P) {
-                    from = to = 0;
-                    if (key < L) {
-                        from = (key - u.P) * a.G - u.row0 - cb;
-                        to = ((const int *)side)[256 + kslot] * a.G - u.row0 - cb;
-                    }
-                }
-                // eight columns' exponents before the maximum is taken off
-                auto scores = [&](int c, float2 (&y)[4]) {
-                    float hi[8], lo[8];
-                    const uint32_t sb = tl + C::S_COL + x * 2 * RP + cb + c;
-                    tc_ld8(sb, hi);
-                    tc_ld8(sb + RP, lo);
+                // y: the columns' exponents before the maximum is taken off
+                float2 y[CG / 2];
+                {
+                    float hi[CG], lo[CG];
+                    const uint32_t sb = tl + C::S_COL + x * 2 * RP + cb;
+                    tc_ldn<CG>(sb, hi);
+                    tc_ldn<CG>(sb + RP, lo);
                     tc_wait_ld();
 #pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        y[e] = __fmul2_rn(__fadd2_rn(make_float2(hi[2 * e], hi[2 * e + 1]), make_float2(lo[2 * e], lo[2 * e + 1])),
-                                          make_float2(ks, ks));
-                    if (edge) {
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            if (!(c + 2 * e >= from && c + 2 * e < to)) y[e].x = -INFINITY;
-                            if (!(c + 2 * e + 1 >= from && c + 2 * e + 1 < to)) y[e].y = -INFINITY;
+                    for (int c = 0; c < CG / 4; ++c) {
+                        const float4 v = lds4(qs + 16 * c);
+                        const float2 k2 = make_float2(ks, ks);
+                        y[2 * c] = __fmul2_rn(__fadd2_rn(make_float2(hi[4 * c], hi[4 * c + 1]), make_float2(lo[4 * c], lo[4 * c + 1])),
+                                              __fmul2_rn(k2, make_float2(v.x, v.y)));
+                        y[2 * c + 1] = __fmul2_rn(__fadd2_rn(make_float2(hi[4 * c + 2], hi[4 * c + 3]), make_float2(lo[4 * c + 2], lo[4 * c + 3])),
+                                                  __fmul2_rn(k2, make_float2(v.z, v.w)));
+                    }
+                }
+                if (j * kTileKeys + kTileKeys > u.P) {   // tree keys, or keys past the end
+                    int from = -0x7fffffff, to = 0x7fffffff;   // the columns that see this lane's key
+                    if (key >= u.P) {
+                        from = to = 0;
+                        if (key < L) {
+                            from = (key - u.P) * a.G - u.row0 - cb;
+                            to = ldsi(side + 1024) * a.G - u.row0 - cb;
                         }
                     }
-                };
-                float2 p[CG / 2];   // exponents, then probabilities
-                auto exponents = [&]() -> float {
-                    float top = -INFINITY, top2 = -INFINITY;
 #pragma unroll
-                    for (int c = 0; c < CG; c += 8) {
-                        float2 y[4];
-                        scores(c, y);
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            p[c / 2 + e] = __ffma2_rn(y[e], qs[c / 2 + e], m[c / 2 + e]);
-                            top = fmaxf(top, p[c / 2 + e].x);
-                            top2 = fmaxf(top2, p[c / 2 + e].y);
-                        }
+                    for (int c = 0; c < CG / 2; ++c) {
+                        if (!(2 * c >= from && 2 * c < to)) y[c].x = -INFINITY;
+                        if (!(2 * c + 1 >= from && 2 * c + 1 < to)) y[c].y = -INFINITY;
                     }
-                    return fmaxf(top, top2);
-                };
+                }
                 bool raise = j == u.j0;
                 if (!raise) {
-                    const float top = exponents();
-                    raise = bar_any(bar, 128, top > kBase + kOver || vs > ref || !ok);
+                    float2 d = __fadd2_rn(y[0], m[0]);
+                    float top = d.x, top2 = d.y;
+#pragma unroll
+                    for (int c = 1; c < CG / 2; ++c) {
+                        d = __fadd2_rn(y[c], m[c]);
+                        top = fmaxf(top, d.x);
+                        top2 = fmaxf(top2, d.y);
+                    }
+                    raise = bar_any(bar, 128, fmaxf(top, top2) > kBase + kOver || vs > ref || !ok);
                 }
                 if (raise) {
                     // new maxima: of each column over the tile, taken where the old one is passed by 2^kOver
-#pragma unroll 1
-                    for (int c = 0; c < CG; c += 8) {
-                        float2 y[4];
-                        scores(c, y);
-                        const float4 q0 = *(const float4 *)(qs_s + r * 64 + cb + c), q1 = *(const float4 *)(qs_s + r * 64 + cb + c + 4);
-                        const float w[8] = {warp_max(y[0].x * q0.x), warp_max(y[0].y * q0.y), warp_max(y[1].x * q0.z),
-                                            warp_max(y[1].y * q0.w), warp_max(y[2].x * q1.x), warp_max(y[2].y * q1.y),
-                                            warp_max(y[3].x * q1.z), warp_max(y[3].y * q1.w)};
-                        if (lane == 0) {
-                            *(float4 *)(mx_s + quarter * 32 + c) = make_float4(w[0], w[1], w[2], w[3]);
-                            *(float4 *)(mx_s + quarter * 32 + c + 4) = make_float4(w[4], w[5], w[6], w[7]);
-                        }
+#pragma unroll
+                    for (int c = 0; c < CG; c += 4) {
+                        const float4 w = make_float4(warp_max(y[c / 2].x), warp_max(y[c / 2].y), warp_max(y[c / 2 + 1].x),
+                                                     warp_max(y[c / 2 + 1].y));
+                        if (lane == 0) sts4(mx_s + (quarter * CG + c) * 4, w);
                     }
                     const float vtop = warp_max(vs);
-                    if (lane == 0) ls_s[quarter * 64 + cb] = vtop;
+                    if (lane == 0) sts1(v_s + quarter * 4, vtop);
                     if (bar_any(bar, 128, !ok)) {
                         ok = false;
                         gone = true;
                         break;
                     }
-                    float nref = fmaxf(fmaxf(ls_s[cb], ls_s[64 + cb]), fmaxf(ls_s[128 + cb], ls_s[192 + cb]));
+                    const float4 v4 = lds4(v_s);
+                    float nref = fmaxf(fmaxf(v4.x, v4.y), fmaxf(v4.z, v4.w));
                     // a half more than the largest scale so far, so that few tiles raise it
                     nref = nref > ref ? nref * 1.5f : ref;
                     const float rr = nref > 0.f ? ref / nref : 1.f;
                     ref = nref;
                     iref = ref > 0.f ? 1.f / ref : 0.f;
-                    // O so far is rescaled once the product before this one has landed in it
-                    if (j > u.j0) {
-                        if (ok && !mbar_wait_warp(pvdone, (uint32_t)(g - 1) & 1u)) ok = false;
+                    const bool later = j > u.j0;   // O so far is rescaled once the product before this one has landed in it
+                    if (later) {
+                        if (ok && !wait_warp(pvdone + 8 * ((g - 1) & 1), (uint32_t)((g - 1) >> 1) & 1u)) ok = false;
                         tc_fence_after();
                     }
-                    const bool scale_o = j > u.j0 && ok && quarter * 32 < D;
 #pragma unroll
                     for (int c = 0; c < CG; c += 4) {
-                        float t4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY}, al[4];
-#pragma unroll
-                        for (int w = 0; w < 4; ++w) {
-                            const float4 v = *(const float4 *)(mx_s + w * 32 + c);
-                            t4[0] = fmaxf(t4[0], v.x);
-                            t4[1] = fmaxf(t4[1], v.y);
-                            t4[2] = fmaxf(t4[2], v.z);
-                            t4[3] = fmaxf(t4[3], v.w);
+                        float t4[4], al[4];
+                        {
+                            const float4 v0 = lds4(mx_s + c * 4), v1 = lds4(mx_s + (CG + c) * 4);
+                            const float4 v2 = lds4(mx_s + (2 * CG + c) * 4), v3 = lds4(mx_s + (3 * CG + c) * 4);
+                            t4[0] = fmaxf(fmaxf(v0.x, v1.x), fmaxf(v2.x, v3.x));
+                            t4[1] = fmaxf(fmaxf(v0.y, v1.y), fmaxf(v2.y, v3.y));
+                            t4[2] = fmaxf(fmaxf(v0.z, v1.z), fmaxf(v2.z, v3.z));
+                            t4[3] = fmaxf(fmaxf(v0.w, v1.w), fmaxf(v2.w, v3.w));
                         }
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
                             float &me = e & 1 ? m[(c + e) / 2].y : m[(c + e) / 2].x;
-                            float &le = e & 1 ? l[(c + e) / 2].y : l[(c + e) / 2].x;
-                            const float nm = kBase - t4[e];
-                            al[e] = 1.f;
-                            if (t4[e] + me > kBase + kOver) {
-                                al[e] = ex2(nm - me);   // 2^(old maximum - new)
-                                me = nm;
-                            }
-                            le *= al[e];
-                            al[e] *= rr;
+                            const float nm = t4[e] + me > kBase + kOver ? kBase - t4[e] : me;
+                            al[e] = nm - me;   // log2 of old maximum over new
+                            me = nm;
                         }
-                        if (scale_o) {
-                            float o[12];
+                        if (later) {
 #pragma unroll
-                            for (int i = 0; i < 3; ++i) tc_ld4(tl + C::O_COL + i * RP + cb + c, o + 4 * i);
-                            tc_wait_ld();
+                            for (int e = 0; e < 4; ++e) {
+                                al[e] = ex2(al[e]);
+                                float &le = e & 1 ? l[(c + e) / 2].y : l[(c + e) / 2].x;
+                                le *= al[e];
+                                al[e] *= rr;
+                            }
+                            if (ok && quarter * 32 < D) {
+                                float o[12];
 #pragma unroll
-                            for (int i = 0; i < 12; ++i) o[i] *= al[i & 3];
+                                for (int i = 0; i < 3; ++i) tc_ld4(tl + C::O_COL + i * RP + cb + c, o + 4 * i);
+                                tc_wait_ld();
 #pragma unroll
-                            for (int i = 0; i < 3; ++i) tc_st4(tl + C::O_COL + i * RP + cb + c, o + 4 * i);
+                                for (int i = 0; i < 12; ++i) o[i] *= al[i & 3];
+#pragma unroll
+                                for (int i = 0; i < 3; ++i) tc_st4(tl + C::O_COL + i * RP + cb + c, o + 4 * i);
+                            }
                         }
                     }
-                    if (scale_o) tc_wait_st();
-                    bar_sync(bar, 128);   // the exchange may be written again
-                    exponents();
+                    if (later) tc_wait_st();   // the exchange is written again only after another vote
                 }
-                // P's one buffer is free once the product before this one has read it
-                if (ok && j > u.j0 && !mbar_wait_warp(pvdone, (uint32_t)(g - 1) & 1u)) ok = false;
+                // P buffer x is free: S(g) was issued once the product that read P(g - 2) had finished
                 const float2 rv = make_float2(vs * iref, vs * iref);
-                unsigned char *pd = fix + C::FIX_P + kslot * 64;
+                const uint32_t pd = fix_base + C::FIX_P + x * C::P_BYTES + kslot * 64;
                 const int flip = (kslot >> 1) & 3;
                 constexpr int STEP = CG % 16 == 0 ? 16 : 8;
 #pragma unroll
@@ -802,7 +874,8 @@ __global__ void __launch_bounds__(Cfg8<D, RP>::THREADS, 1)
 #pragma unroll
                         for (int e = 0; e < 2; ++e) {
                             const int cc = c / 2 + 2 * i + e;
-                            const float2 pe = make_float2(ex2(p[cc].x), ex2(p[cc].y));
+                            const float2 d = __fadd2_rn(y[cc], m[cc]);
+                            const float2 pe = make_float2(ex2(d.x), ex2(d.y));
                             l[cc] = __fadd2_rn(l[cc], pe);
                             const float2 pr = __fmul2_rn(pe, rv);
                             h[e] = half2_of(pr.x, pr.y);
@@ -817,45 +890,42 @@ __global__ void __launch_bounds__(Cfg8<D, RP>::THREADS, 1)
 #pragma unroll
                         for (int t = 0; t < 3; ++t) {
                             const int col = t * RP + cb + c;
-                            unsigned char *d = pd + (col >> 6) * C::P_ATOM + ((((col >> 4) & 3) ^ flip) << 4) + (col & 15);
-                            if constexpr (STEP == 16) *(uint4 *)d = make_uint4(w[t][0], w[t][1], w[t][2], w[t][3]);
-                            else *(uint2 *)d = make_uint2(w[t][0], w[t][1]);
+                            const uint32_t d = pd + (col >> 6) * C::P_ATOM + ((((col >> 4) & 3) ^ flip) << 4) + (col & 15);
+                            if constexpr (STEP == 16) sts4u(d, w[t][0], w[t][1], w[t][2], w[t][3]);
+                            else sts2u(d, w[t][0], w[t][1]);
                         }
                     }
                 }
                 if (j * kTileKeys + kTileKeys > L && ok) {
                     // V's rows past the last key may hold anything: zeros (whose weights are zero too)
-                    unsigned char *vt = sm + st * C::STAGE_BYTES + C::OP_BYTES;
+                    const uint32_t vt = sm_base + st * C::STAGE_BYTES + C::OP_BYTES;
                     const int r0 = (L - j * kTileKeys) * (D / 16);
-                    for (int i = r0 + tid - 64; i < kTileKeys * (D / 16); i += 32 * C::SM_WARPS)
-                        *(uint4 *)(vt + i * 16) = make_uint4(0u, 0u, 0u, 0u);
+                    for (int i = r0 + tid - 128; i < kTileKeys * (D / 16); i += 32 * C::SM_WARPS)
+                        sts4u(vt + i * 16, 0u, 0u, 0u, 0u);
                 }
                 fence_async_smem();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(pfull);
+                if (lane == 0) mbar_arrive(pfull + 8 * x);
             }
             if (gone) break;
 
             // ---- the unit's output
+            float v[CG];
 #pragma unroll
-            for (int c = 0; c < CG; c += 8) {
-                float v[8];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    v[2 * e] = l[c / 2 + e].x;
-                    v[2 * e + 1] = l[c / 2 + e].y;
-                }
-                reduce_scatter<8>(v, lane);
-                if (!(lane & 3)) ls_s[quarter * 64 + cb + c + (lane >> 2)] = v[0];
+            for (int c = 0; c < CG / 2; ++c) {
+                v[2 * c] = l[c].x;
+                v[2 * c + 1] = l[c].y;
             }
+            reduce_scatter<CG>(v, lane);
+            if (lane % (32 / CG) == 0) sts1(ls_s + (quarter * 64 + cb + lane / (32 / CG)) * 4, v[0]);
             bar_sync(bar, 128);
             float lsum = 0.f;
             if (gt < CG) {
-                const int c = cb + gt;
-                lsum = (ls_s[c] + ls_s[64 + c]) + (ls_s[128 + c] + ls_s[192 + c]);
+                const uint32_t c = ls_s + (cb + gt) * 4;
+                lsum = (lds1(c) + lds1(c + 256)) + (lds1(c + 512) + lds1(c + 768));
                 // a part keeps its own maximum and sum; a whole unit is divided by its sum here
-                f_s[gt] = u.parts > 1 ? ref : ref / lsum;
+                sts1(f_s + gt * 4, u.parts > 1 ? ref : ref / lsum);
             }
             if (u.parts > 1) {
                 float mm = 0.f;
@@ -864,11 +934,11 @@ __global__ void __launch_bounds__(Cfg8<D, RP>::THREADS, 1)
                     if (gt == c) mm = -(c & 1 ? m[c / 2].y : m[c / 2].x);
                 if (gt < CG) a.part_ml[(size_t)(u.slot + u.part) * RP + cb + gt] = make_float2(mm, lsum);
             }
-            if (ok && !mbar_wait_warp(pvdone, (uint32_t)(g - 1) & 1u)) ok = false;
+            if (ok && !wait_warp(pvdone + 8 * ((g - 1) & 1), (uint32_t)((g - 1) >> 1) & 1u)) ok = false;
             tc_fence_after();
             bar_sync(bar, 128);
             __nv_bfloat16 *ob = a.out + (size_t)u.b * n_max * a.Hq * D;
-            const int *rows = qrow_s + r * 64 + cb;
+            const uint32_t rows = fix_base + C::FIX_QROW + (r * 64 + cb) * 4;
 #pragma unroll
             for (int c = 0; c < CG; c += 8) {
                 float o[3][8];
@@ -877,14 +947,15 @@ __global__ void __launch_bounds__(Cfg8<D, RP>::THREADS, 1)
                     for (int i = 0; i < 3; ++i) tc_ld8(tl + C::O_COL + i * RP + cb + c, o[i]);
                     tc_wait_ld();
                 }
-                if (c + 8 >= CG) {   // O is read out
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(ofree);
-                }
                 if (!ok || quarter * 32 >= D) continue;
 #pragma unroll
-                for (int e = 0; e < 8; ++e) o[0][e] = ((o[0][e] + o[1][e]) + o[2][e]) * f_s[c + e];
+                for (int e = 0; e < 8; e += 4) {
+                    const float4 f = lds4(f_s + (c + e) * 4);
+                    o[0][e] = ((o[0][e] + o[1][e]) + o[2][e]) * f.x;
+                    o[0][e + 1] = ((o[0][e + 1] + o[1][e + 1]) + o[2][e + 1]) * f.y;
+                    o[0][e + 2] = ((o[0][e + 2] + o[1][e + 2]) + o[2][e + 2]) * f.z;
+                    o[0][e + 3] = ((o[0][e + 3] + o[1][e + 3]) + o[2][e + 3]) * f.w;
+                }
                 if (u.parts > 1) {
                     float *po = a.part_o + ((size_t)(u.slot + u.part) * RP + cb + c) * D + kslot;
 #pragma unroll
@@ -895,7 +966,7 @@ __global__ void __launch_bounds__(Cfg8<D, RP>::THREADS, 1)
                     for (int e = 0; e < 8; e += 2) {
                         const float keep = lane & 1 ? o[0][e + 1] : o[0][e], send = lane & 1 ? o[0][e] : o[0][e + 1];
                         const float got = __shfl_xor_sync(~0u, send, 1);
-                        const int row = rows[c + e + (lane & 1)];
+                        const int row = ldsi(rows + (c + e + (lane & 1)) * 4);
                         const __nv_bfloat162 v = lane & 1 ? __floats2bfloat162_rn(got, keep) : __floats2bfloat162_rn(keep, got);
                         if (row >= 0) *(__nv_bfloat162 *)(ob + (size_t)row * D + (kslot & ~1)) = v;
                     }
@@ -905,7 +976,7 @@ __global__ void __launch_bounds__(Cfg8<D, RP>::THREADS, 1)
                 __threadfence();
                 bar_sync(bar, 128);
                 if (gt == 0) {
-                    unsigned *cnt = a.joins + (size_t)u.slot * 2 + grp;
+                    unsigned *cnt = a.joins + (size_t)u.slot * 4 + grp;
                     const bool last = ok && atomicAdd(cnt, 1u) == (unsigned)u.parts - 1;
                     if (last) *cnt = 0u;
                     misc[4 + grp] = last;
@@ -915,7 +986,7 @@ __global__ void __launch_bounds__(Cfg8<D, RP>::THREADS, 1)
                     __threadfence();
                     constexpr int EPL = D / 32;
                     for (int c = warp & 3; c < CG; c += 4) {   // a warp a column, lane = part, then lane = dims
-                        const int row = rows[c];
+                        const int row = ldsi(rows + c * 4);
                         if (row < 0) continue;
                         float2 ml = make_float2(-INFINITY, 0.f);
                         if (lane < u.parts) ml = __ldcg(a.part_ml + (size_t)(u.slot + lane) * RP + cb + c);
@@ -986,7 +1057,7 @@ Plan8 plan8(int B, int Hkv, int G, int n_max, int d) {
     p.rp = (int)(((rows + p.blocks - 1) / p.blocks + 15) / 16 * 16);
     p.blocks = (int)((rows + p.rp - 1) / p.rp);
     p.slots = B <= kReqCache ? 2 * kCutsPerSm * num_sms() : 0;
-    size_t at = 256 + ((size_t)p.slots * 2 * sizeof(unsigned) + 255) / 256 * 256;
+    size_t at = 256 + ((size_t)p.slots * 4 * sizeof(unsigned) + 255) / 256 * 256;
     p.ml = at;
     at += (size_t)p.slots * p.rp * sizeof(float2);
     p.o = (at + 255) / 256 * 256;
