@@ -4,15 +4,14 @@
 // (SpecInfer, arXiv 2305.09781, Def. 4.1, Eq. 1-4; the mask of sec. 4.2), with
 // K and V held as e4m3 codes times one fp32 scale per (row, head), and G query
 // heads to a key/value head. The R = n * G query rows of a (request, key/value
-// head) share its keys; they are taken RP at a time (RP = 16, 32, 48 or 64).
+// head) share its keys; they are taken RP at a time (RP = 16, 32 or 48).
 //
 // The cache's codes go to the tensor cores as they are. Both products are
 // transposed, so that keys, then value dims, are the 128 rows of the MMA and a
 // tile costs in proportion to the query rows there are:
-//   S^T [128 keys x 2 RP]  = K [128 x d] * [Qh | Ql]^T        (e4m3 * e4m3)
+//   S^T [128 keys x RP]    = K [128 x d] * Qh^T + K * Ql^T            (e4m3 * e4m3)
 //   O^T [d x 3 RP]        += V^T [d x 128 keys] * [P0 | P1 | P2]^T (e4m3 * e5m2)
-// What is not in 8 bits is split into several 8-bit numbers, each a column
-// block of its own, so K and V are read from shared memory once a tile:
+// What is not in 8 bits is split into several 8-bit numbers:
 //   a query row, scaled by a power of two to a largest value in [128, 256), is
 //   qh + ql with qh = e4m3(q), ql = e4m3(q - qh): bf16's eight bits exactly for
 //   values down to 2^-10 of the row's largest, 2^-18 of it absolutely below;
@@ -125,15 +124,16 @@ __device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
     asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
 }
 
-// Bounded wait for a phase: try_wait suspends the thread in hardware for up to a microsecond a try, and the tries are
-// limited (a second or so at most; every wait here is for warps of the same CTA).
+// Bounded wait for a phase: try_wait suspends the thread in hardware for up to 20 us a try, and the tries are
+// limited (some seconds at most; every wait here is for warps of the same CTA).
 __device__ __forceinline__ bool wait1(uint32_t bar, uint32_t phase) {
+#pragma unroll 1
     for (int i = 0; i < 1 << 20; ++i) {
         uint32_t ok;
         asm volatile(
             "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n selp.u32 %0, 1, 0, p;\n}\n"
             : "=r"(ok)
-            : "r"(bar), "r"(phase), "r"(1000)
+            : "r"(bar), "r"(phase), "r"(20000)
             : "memory");
         if (ok) return true;
     }
@@ -160,9 +160,6 @@ __device__ __forceinline__ int ldsi(uint32_t a) {
 }
 __device__ __forceinline__ void sts1(uint32_t a, float v) { asm volatile("st.shared.f32 [%0], %1;" ::"r"(a), "f"(v) : "memory"); }
 __device__ __forceinline__ void stsi(uint32_t a, int v) { asm volatile("st.shared.b32 [%0], %1;" ::"r"(a), "r"(v) : "memory"); }
-__device__ __forceinline__ void sts4(uint32_t a, float4 v) {
-    asm volatile("st.shared.v4.f32 [%0], {%1,%2,%3,%4};" ::"r"(a), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w) : "memory");
-}
 __device__ __forceinline__ void sts4u(uint32_t a, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
     asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
 }
@@ -181,6 +178,16 @@ __device__ __forceinline__ uint32_t hsub2(uint32_t a, uint32_t b) {
     return r;
 }
 
+__device__ __forceinline__ uint32_t half2_to_fp8x2(uint32_t h) {
+    __half2_raw r;
+    r.x = (unsigned short)h;
+    r.y = (unsigned short)(h >> 16);
+    return __nv_cvt_halfraw2_to_fp8x2(r, __NV_SATFINITE, __NV_E4M3);
+}
+__device__ __forceinline__ uint32_t fp8x2_to_half2(uint32_t c) {
+    const __half2_raw r = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)c, __NV_E4M3);
+    return (uint32_t)r.x | (uint32_t)r.y << 16;
+}
 // ------------------------------------------------------------ arguments ---
 struct Attn8Args {
     __nv_bfloat16 *out;
@@ -205,7 +212,7 @@ constexpr int kMaxCuts = 32;       // parts of one item (a lane each when they a
 constexpr int kMinCut = 3;         // tiles of a part at least
 constexpr int kCutsPerSm = 2;      // units per SM that cutting aims at
 constexpr int kRing = 4;           // published units
-constexpr int kClaimAhead = 6;
+constexpr int kClaimAhead = 6;     // tiles
 
 template <int D_, int RP_>
 struct Cfg8 {
@@ -220,12 +227,14 @@ struct Cfg8 {
     static constexpr int FIX_P = 0, FIX_Q = FIX_P + 2 * P_BYTES, FIX_MX = FIX_Q + 2 * Q_BYTES;
     static constexpr int FIX_LS = FIX_MX + 4 * RP * 4;         // column maxima [groups][4 warps][CG]
     static constexpr int FIX_F = FIX_LS + 4 * 64 * 4;          // column sums [4 warps][64], then factors [64]
-    static constexpr int FIX_V = FIX_F + 64 * 4;               // largest value scales [groups][4 warps]
+    static constexpr int FIX_F2 = FIX_F + 64 * 4;              // factors of O where a maximum is raised [64]
+    static constexpr int FIX_V = FIX_F2 + 64 * 4;              // largest value scales [groups][4 warps]
     static constexpr int FIX_QS = FIX_V + 64;                  // query scales [kRing][64], output rows [kRing][64]
     static constexpr int FIX_QROW = FIX_QS + kRing * 64 * 4;
-    static constexpr int FIX_REQ = FIX_QROW + kRing * 64 * 4;  // (n, P) by request, then order, first unit, first slot
-    static constexpr int FIX_ORDER = FIX_REQ + kReqCache * 8, FIX_UNIT = FIX_ORDER + kReqCache * 4;
-    static constexpr int FIX_SLOT = FIX_UNIT + kReqCache * 4;
+    static constexpr int FIX_REQ = FIX_QROW + kRing * 64 * 4;  // requests: n, P, tiles, parts
+    static constexpr int FIX_KEY = FIX_REQ + kReqCache * 16;   // tiles of a part
+    static constexpr int FIX_ORDER = FIX_KEY + kReqCache * 4;  // by rank: request, first unit, first slot
+    static constexpr int FIX_UNIT = FIX_ORDER + kReqCache * 4, FIX_SLOT = FIX_UNIT + kReqCache * 4;
     static constexpr int FIX_INFO = FIX_SLOT + kReqCache * 4;  // units [kRing][12]
     static constexpr int FIX_MISC = FIX_INFO + kRing * 12 * 4; // 0 TMEM base, 1 timeout, 2 units, 3 tiles a part, 4-7 last
     static constexpr int FIX_BAR = FIX_MISC + 64;
@@ -238,9 +247,9 @@ struct Cfg8 {
     }
     static constexpr int STAGES = fit();
     static constexpr int OFF_SIDE = STAGES * STAGE_BYTES, OFF_FIX = off_fix(STAGES), SMEM = OFF_FIX + FIX_END + 1024;
-    static constexpr uint32_t S_COL = 0, O_COL = 4 * RP;       // two score buffers of 2 RP columns, O of 3 RP
-    static constexpr uint32_t TMEM_COLS = 7 * RP <= 128 ? 128 : 7 * RP <= 256 ? 256 : 512;
-    static_assert(STAGES >= 3 && SMEM <= 232448 && STAGE_BYTES % 1024 == 0 && FIX_Q % 1024 == 0 && Q_BYTES % 1024 == 0,
+    static constexpr uint32_t S_COL = 0, O_COL = 2 * RP;       // two score buffers of RP columns, two O of 3 RP
+    static constexpr uint32_t TMEM_COLS = 8 * RP <= 128 ? 128 : 8 * RP <= 256 ? 256 : 512;
+    static_assert(STAGES >= 4 && SMEM <= 232448 && STAGE_BYTES % 1024 == 0 && FIX_Q % 1024 == 0 && Q_BYTES % 1024 == 0,
                   "shared memory and the alignment of swizzled tiles");
 };
 
@@ -248,19 +257,21 @@ struct Unit8 {
     int b, h, row0, n, P, j0, j1, parts, part, slot;   // tiles [j0, j1); slot: of the item's first part
 };
 
-// Sums of N columns over the warp: column lane / (32 / N) ends in v[0].
-template <int N, int W = 16>
+// Sums (or maxima) of N columns over the warp: column lane / (32 / N) ends in v[0].
+template <int N, bool MAX = false, int W = 16>
 __device__ __forceinline__ void reduce_scatter(float *v, int lane) {
     if constexpr (N > 1) {
 #pragma unroll
         for (int i = 0; i < N / 2; ++i) {
             const float keep = lane & W ? v[i + N / 2] : v[i], send = lane & W ? v[i] : v[i + N / 2];
-            v[i] = keep + __shfl_xor_sync(~0u, send, W);
+            const float got = __shfl_xor_sync(~0u, send, W);
+            v[i] = MAX ? fmaxf(keep, got) : keep + got;
         }
     } else {
-        v[0] += __shfl_xor_sync(~0u, v[0], W);
+        const float got = __shfl_xor_sync(~0u, v[0], W);
+        v[0] = MAX ? fmaxf(v[0], got) : v[0] + got;
     }
-    if constexpr (W > 1) reduce_scatter<(N > 1 ? N / 2 : 1), W / 2>(v, lane);
+    if constexpr (W > 1) reduce_scatter<(N > 1 ? N / 2 : 1), MAX, W / 2>(v, lane);
 }
 
 template <int D, int RP>
@@ -272,8 +283,9 @@ __global__ void __launch_bounds__(Cfg8<D, RP>::THREADS, 1)
     unsigned char *fix = sm + C::OFF_FIX;
     const uint32_t sm_base = smem_u32(sm), fix_base = sm_base + C::OFF_FIX;
     volatile int *misc = (volatile int *)(fix + C::FIX_MISC);
-    int2 *req_s = (int2 *)(fix + C::FIX_REQ);
-    int *order_s = (int *)(fix + C::FIX_ORDER), *unit_s = (int *)(fix + C::FIX_UNIT), *slot_s = (int *)(fix + C::FIX_SLOT);
+    int4 *req_s = (int4 *)(fix + C::FIX_REQ);
+    int *key_s = (int *)(fix + C::FIX_KEY), *order_s = (int *)(fix + C::FIX_ORDER);
+    int *unit_s = (int *)(fix + C::FIX_UNIT), *slot_s = (int *)(fix + C::FIX_SLOT);
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int B = a.t.B, n_max = a.t.n_max;
@@ -281,28 +293,32 @@ __global__ void __launch_bounds__(Cfg8<D, RP>::THREADS, 1)
     pdl_trigger();
 
     const uint32_t full = fix_base + C::FIX_BAR, empty = full + 8 * C::STAGES, sfull = empty + 8 * C::STAGES;
-    const uint32_t pfull = sfull + 16, pvdone = pfull + 16, qready = pvdone + 16, qfree = qready + 16;
+    const uint32_t pvdone = sfull + 16, pfull = pvdone + 16, qraw = pfull + 16, qready = qraw + 16, qfree = qready + 16;
     const uint32_t fin = qfree + 16, iready = fin + 16, ifree = iready + 8 * kRing;
 
-    if (warp == 0) {
+    if (warp == 2) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32((void *)misc)),
                      "r"(C::TMEM_COLS)
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
     if (tid == 32) {
+#pragma unroll 1
         for (int s = 0; s < C::STAGES; ++s) {
             mbar_init(full + 8 * s, 1 + 32);   // the TMA's bytes, and the producer's lanes' copies
             mbar_init(empty + 8 * s, 1);
         }
+#pragma unroll 1
         for (int x = 0; x < 2; ++x) {
             mbar_init(sfull + 8 * x, 2);   // the scores, and the issuer's sight of the stage (scales by cp.async)
-            mbar_init(pfull + 8 * x, C::SM_WARPS);
             mbar_init(pvdone + 8 * x, 1);
-            mbar_init(qready + 8 * x, 1);
+            mbar_init(pfull + 8 * x, C::SM_WARPS);
+            mbar_init(qraw + 8 * x, 1 + 32);
+            mbar_init(qready + 8 * x, C::SM_WARPS);
             mbar_init(qfree + 8 * x, 1);
             mbar_init(fin + 8 * x, 1);
         }
+#pragma unroll 1
         for (int r = 0; r < kRing; ++r) {
             mbar_init(iready + 8 * r, 1);
             mbar_init(ifree + 8 * r, 3 + C::SM_WARPS);
@@ -319,34 +335,42 @@ __global__ void __launch_bounds__(Cfg8<D, RP>::THREADS, 1)
     auto tiles_of = [&](int n, int P) -> int {   // 0 for a request that is empty or does not fit
         return n > 0 && n <= n_max && P >= 0 && P <= a.rows - n ? (P + n + kTileKeys - 1) / kTileKeys : 0;
     };
-    auto parts_of = [&](int tiles, int per) {
-        const int p = (tiles + per - 1) / per;
-        return p < kMaxCuts ? p : kMaxCuts;
-    };
-    for (int b = tid; planned && b < B; b += C::THREADS) req_s[b] = make_int2(a.t.n_nodes[b], a.prefix_len[b]);
+#pragma unroll 1
+    for (int b = tid; b < B; b += C::THREADS) {
+        const int n = a.t.n_nodes[b], P = a.prefix_len[b], tl = tiles_of(n, P);
+        if (planned) req_s[b] = make_int4(n, P, tl, 1);
+        if (blockIdx.x == 0 && n > 0 && !tl) flag(a.status, TS_STATUS_INDEX);
+    }
     __syncthreads();
     if (planned && warp == 0) {
         long long work = 0;   // tiles over all items
-        for (int b = lane; b < B; b += 32) work += (long long)tiles_of(req_s[b].x, req_s[b].y) * blocks_of(req_s[b].x);
+#pragma unroll 1
+        for (int b = lane; b < B; b += 32) work += (long long)req_s[b].z * blocks_of(req_s[b].x);
 #pragma unroll
         for (int o = 16; o; o >>= 1) work += __shfl_xor_sync(~0u, work, o);
-        const long long aim = (long long)gridDim.x * kCutsPerSm;
-        long long per = (work * a.H + aim - 1) / aim;
-        if (per < kMinCut) per = kMinCut;
-        if (per > (1 << 24)) per = 1 << 24;
-        if (lane == 0) misc[3] = (int)per;
+        // rounded up, so that the parts of cut items, fewer than 2 * work / per, fit the slots
+        const float each = __fdiv_ru(__fmul_ru(__ll2float_ru(work), (float)a.H), (float)((int)gridDim.x * kCutsPerSm));
+        const int per = max(kMinCut, (int)ceilf(fminf(each, 16777216.f)));
+#pragma unroll 1
+        for (int b = lane; b < B; b += 32) {
+            const int tl = req_s[b].z;
+            if (tl > per) {
+                const int parts = min((tl + per - 1) / per, kMaxCuts);
+                req_s[b].w = parts;
+                key_s[b] = (tl + parts - 1) / parts;
+            } else {
+                key_s[b] = tl;
+            }
+        }
     }
     __syncthreads();
-    const int per = planned ? misc[3] : 1 << 24;
+#pragma unroll 1
     for (int b = tid; planned && b < B; b += C::THREADS) {   // rank by the length of the request's parts
-        auto key = [&](int o) {
-            const int tl = tiles_of(req_s[o].x, req_s[o].y);
-            return tl ? (tl + parts_of(tl, per) - 1) / parts_of(tl, per) : 0;
-        };
-        const int mine = key(b);
+        const int mine = key_s[b];
         int rank = 0;
+#pragma unroll 4
         for (int o = 0; o < B; ++o) {
-            const int ko = key(o);
+            const int ko = key_s[o];
             rank += ko > mine || (ko == mine && o < b);
         }
         order_s[rank] = b;
@@ -354,16 +378,13 @@ __global__ void __launch_bounds__(Cfg8<D, RP>::THREADS, 1)
     __syncthreads();
     if (planned && warp == 0) {   // exclusive sums of units and of slots, in that order
         int units = 0, slots = 0;
+#pragma unroll 1
         for (int r0 = 0; r0 < B; r0 += 32) {
             int u = 0, s = 0;
             if (r0 + lane < B) {
-                const int2 rq = req_s[order_s[r0 + lane]];
-                const int tl = tiles_of(rq.x, rq.y);
-                if (tl) {
-                    const int pt = parts_of(tl, per);
-                    u = a.H * blocks_of(rq.x) * pt;
-                    s = pt > 1 ? u : 0;
-                }
+                const int4 rq = req_s[order_s[r0 + lane]];
+                if (rq.z) u = a.H * blocks_of(rq.x) * rq.w;
+                if (rq.w > 1) s = u;
             }
             int cu = u, cs = s;
 #pragma unroll
@@ -388,19 +409,15 @@ __global__ void __launch_bounds__(Cfg8<D, RP>::THREADS, 1)
     tc_fence_after();
     const uint32_t tmem = (uint32_t)misc[0];
     const int units = planned ? misc[2] : B * a.H * blocks_max;
-    if (blockIdx.x == 0)   // requests that do not fit
-        for (int b = tid; b < B; b += C::THREADS) {
-            const int n = a.t.n_nodes[b];
-            if (n > 0 && !tiles_of(n, a.prefix_len[b])) flag(a.status, TS_STATUS_INDEX);
-        }
 
     // unit q of the queue; false for one that is empty (requests beyond the planned ones)
     auto decode = [&](int q, Unit8 &u) -> bool {
-        int rest, first = 0;
+        int first, tl;
         u.slot = 0;
         u.parts = 1;
         if (planned) {
             int lo = 0, hi = B - 1;   // the last request whose first unit is at most q
+#pragma unroll 1
             while (lo < hi) {
                 const int mid = (lo + hi + 1) >> 1;
                 if (unit_s[mid] <= q) lo = mid;
@@ -409,32 +426,35 @@ __global__ void __launch_bounds__(Cfg8<D, RP>::THREADS, 1)
             u.b = order_s[lo];
             first = unit_s[lo];
             u.slot = slot_s[lo];
-            u.n = req_s[u.b].x;
-            u.P = req_s[u.b].y;
+            const int4 rq = req_s[u.b];
+            u.n = rq.x;
+            u.P = rq.y;
+            tl = rq.z;
+            u.parts = rq.w;
         } else {
             u.b = q / (a.H * blocks_max);
             first = u.b * a.H * blocks_max;
             u.n = a.t.n_nodes[u.b];
             u.P = a.prefix_len[u.b];
+            tl = tiles_of(u.n, u.P);
         }
-        rest = q - first;
-        const int tl = tiles_of(u.n, u.P), blocks = planned ? blocks_of(u.n) : blocks_max;
-        if (planned) u.parts = parts_of(tl, per);
+        const int blocks = planned ? blocks_of(u.n) : blocks_max;
         // row blocks of the same keys follow one another: the second finds them in L2
-        const int blk = rest % blocks, item = rest / blocks;
-        u.h = item % a.H;
+        const int rest = q - first, item = rest / blocks, blk = rest - item * blocks;
         u.part = item / a.H;
+        u.h = item - u.part * a.H;
         u.row0 = blk * RP;
         if (!tl || blk >= blocks_of(u.n)) return false;
-        u.j0 = (int)((long long)tl * u.part / u.parts);
-        u.j1 = (int)((long long)tl * (u.part + 1) / u.parts);
+        u.j0 = tl * u.part / u.parts;   // tl < 2^24, parts <= 32
+        u.j1 = tl * (u.part + 1) / u.parts;
         if (u.parts > 1) u.slot += (u.h * blocks + blk) * u.parts;
         return true;
     };
     auto read_unit = [&](int r) -> Unit8 {
         const uint32_t i = fix_base + C::FIX_INFO + r * 48;
-        return Unit8{ldsi(i), ldsi(i + 4), ldsi(i + 8), ldsi(i + 12), ldsi(i + 16), ldsi(i + 20), ldsi(i + 24), ldsi(i + 28),
-                     ldsi(i + 32), ldsi(i + 36)};
+        const float4 v = lds4(i), w = lds4(i + 16), x = lds4(i + 32);
+        return Unit8{__float_as_int(v.x), __float_as_int(v.y), __float_as_int(v.z), __float_as_int(v.w), __float_as_int(w.x),
+                     __float_as_int(w.y), __float_as_int(w.z), __float_as_int(w.w), __float_as_int(x.x), __float_as_int(x.y)};
     };
 
     constexpr uint64_t swz = D == 128 ? kSwz128 : kSwz64;
@@ -460,21 +480,24 @@ __global__ void __launch_bounds__(Cfg8<D, RP>::THREADS, 1)
             ++k;
             return q < units;
         };
-        Unit8 u = {}, un = {};
-        bool more = publish(__shfl_sync(~0u, next(), 0), u);
+        Unit8 u = {}, un = {};   // the first unit follows one without tiles
+        bool more = true;
+#pragma unroll 1
         while (more) {
             // the next unit is taken kClaimAhead tiles before this one's last load, late enough that CTAs share the
             // last units evenly, early enough that its query rows are staged in time
-            const int claim = u.j1 - kClaimAhead > u.j0 ? u.j1 - kClaimAhead : u.j0;
+            const int claim = max(u.j1 - kClaimAhead, u.j0);
             int qn = 0;
             const int L = u.P + u.n;
             const int strip = (u.b * a.H + u.h) * a.rows;   // dense: the cache row of key 0
-            for (int j = u.j0; j < u.j1; ++j, ++g) {
+#pragma unroll 1
+            for (int j = u.j0;; ++j, ++g) {
                 if (j == claim) qn = next();
-                if (j == claim + 1) {
+                if (j == min(claim + 1, u.j1)) {
                     more = publish(__shfl_sync(~0u, qn, 0), un);
                     if (!ok) break;
                 }
+                if (j == u.j1) break;
                 const int st = g % C::STAGES, key0 = j * kTileKeys;
                 const bool two = key0 + 64 < L;
                 int row0 = strip + key0, row1 = row0 + 64;
@@ -527,18 +550,18 @@ __global__ void __launch_bounds__(Cfg8<D, RP>::THREADS, 1)
                 }
                 cp_async_arrive(fb);
             }
-            if (ok && claim + 1 >= u.j1) more = publish(__shfl_sync(~0u, qn, 0), un);
             if (!ok) break;
             u = un;
         }
         if (!ok) {   // leave no copy in flight
             if (lane == 0) misc[1] = 1;
+#pragma unroll 1
             for (int i = g > C::STAGES ? g - C::STAGES : 0; i < g; ++i)
                 wait_warp(full + 8 * (i % C::STAGES), (uint32_t)(i / C::STAGES) & 1u);
         }
     } else if (warp == 1) {   // ----------------------------------------- MMA issuer
         if (lane == 0) {
-            constexpr uint32_t idesc_s = idesc_f8(128, 2 * RP, false, false, false);
+            constexpr uint32_t idesc_s = idesc_f8(128, RP, false, false, false);
             bool ok = true;
             int g = 0;
             for (int k = 0; ok; ++k) {
@@ -548,6 +571,7 @@ __global__ void __launch_bounds__(Cfg8<D, RP>::THREADS, 1)
                 mbar_arrive(ifree + 8 * r);
                 if (u.b < 0) break;
                 if (!wait1(qready + 8 * (k & 1), (uint32_t)(k >> 1) & 1u)) { ok = false; break; }
+#pragma unroll 1
                 for (int j = u.j0; j < u.j1; ++j, ++g) {
                     const int st = g % C::STAGES, x = g & 1;
                     // the product of tile g - 2 is done: S(g - 2) was read and P(g - 2) is free, for who waits for S(g)
@@ -559,9 +583,9 @@ __global__ void __launch_bounds__(Cfg8<D, RP>::THREADS, 1)
                     tc_fence_after();
                     const uint32_t kb = sm_base + st * C::STAGE_BYTES, qd = fix_base + C::FIX_Q + (k & 1) * C::Q_BYTES;
 #pragma unroll
-                    for (int kk = 0; kk < D / 32; ++kk)
-                        tc_mma_f8(tmem + C::S_COL + x * 2 * RP, smem_desc8(kb + kk * 32, 16, 8 * D, swz),
-                                  smem_desc8(qd + kk * 32, 16, 8 * D, swz), idesc_s, kk > 0);
+                    for (int kk = 0; kk < 2 * (D / 32); ++kk)   // with the rows' upper, then their lower parts
+                        tc_mma_f8(tmem + C::S_COL + x * RP, smem_desc8(kb + kk % (D / 32) * 32, 16, 8 * D, swz),
+                                  smem_desc8(qd + kk / (D / 32) * RP * D + kk % (D / 32) * 32, 16, 8 * D, swz), idesc_s, kk > 0);
                     tc_commit(sfull + 8 * x);
                     mbar_arrive(sfull + 8 * x);
                 }
@@ -584,6 +608,7 @@ __global__ void __launch_bounds__(Cfg8<D, RP>::THREADS, 1)
                 const Unit8 u = read_unit(r);
                 mbar_arrive(ifree + 8 * r);
                 if (u.b < 0) break;
+#pragma unroll 1
                 for (int j = u.j0; j < u.j1; ++j, ++g) {
                     const int st = g % C::STAGES, x = g & 1;
                     if (!wait1(full + 8 * st, (uint32_t)(g / C::STAGES) & 1u) ||
@@ -593,11 +618,12 @@ __global__ void __launch_bounds__(Cfg8<D, RP>::THREADS, 1)
                     }
                     tc_fence_after();
                     const uint32_t vb = sm_base + st * C::STAGE_BYTES + C::OP_BYTES, pd = fix_base + C::FIX_P + x * C::P_BYTES;
-                    // a unit's first product starts O afresh: each softmax warp wrote its P after it had read out O.
+                    // a unit's first product starts its O afresh: each softmax warp wrote the P of it after it had read
+                    // out the O of two units before, the same buffer.
                     // V^T: dims contiguous; d = 64 repeats its 64 rows (stride 0) to the MMA's 128
 #pragma unroll
                     for (int kk = 0; kk < kTileKeys / 32; ++kk)
-                        tc_mma_f8(tmem + C::O_COL, smem_desc8(vb + kk * 32 * D, 0, 8 * D, swz),
+                        tc_mma_f8(tmem + C::O_COL + (k & 1) * 3 * RP, smem_desc8(vb + kk * 32 * D, 0, 8 * D, swz),
                                   smem_desc8(pd + kk * 32 * 64, C::P_ATOM, 512, kSwz64), idesc_o, j > u.j0 || kk > 0);
                     tc_commit(empty + 8 * st);
                     tc_commit(pvdone + 8 * x);
@@ -610,9 +636,7 @@ __global__ void __launch_bounds__(Cfg8<D, RP>::THREADS, 1)
         __syncwarp();
     } else if (warp == 3) {   // ----------------------------------------- query rows
         // A raw row of 2 * d bytes and its two parts of d bytes take the same room: each half of the row is copied
-        // to where a part will be, and half a warp turns a row into its parts in place.
-        constexpr int EPL = D / 16;   // values a lane holds of a row
-        const int sub = lane & 15, odd = lane >> 4;
+        // to where a part will be; the softmax warps turn rows into parts in place.
         bool ok = true;
         for (int k = 0;; ++k) {
             const int r = k % kRing;
@@ -645,67 +669,15 @@ __global__ void __launch_bounds__(Cfg8<D, RP>::THREADS, 1)
                 cp_async16(qd + ((v >= VPR / 2 ? RP : 0) + c) * D + (v % (VPR / 2)) * 16,
                            qb + (size_t)(pl < 0 ? 0 : pl) * D + v * 8, pl >= 0);
             }
-            asm volatile("cp.async.wait_all;" ::: "memory");
-            __syncwarp();
-#pragma unroll 4
-            for (int c0 = 0; c0 < RP; c0 += 2) {
-                {
-                    const int c = c0 + odd;
-                    uint32_t w[4] = {0u, 0u, 0u, 0u};
-                    const uint32_t src = qd + ((sub >= 8 ? RP : 0) + c) * D + (sub & 7) * (2 * EPL);
-                    if constexpr (EPL == 8)
-                        asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(src) : "memory");
-                    else
-                        asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(src) : "memory");
-                    uint32_t top = 0;   // |values| order as their bits do, infinities and NaN on top
-#pragma unroll
-                    for (int e = 0; e < EPL / 2; ++e) top = max(top, max(w[e] & 0x7fff0000u, (w[e] << 16) & 0x7fff0000u));
-#pragma unroll
-                    for (int o = 8; o; o >>= 1) top = max(top, __shfl_xor_sync(~0u, top, o));
-                    // 2^(exponent - 7), within the normal numbers whose reciprocal is one too
-                    int ex = (int)(top >> 23) - 7;
-                    ex = ex < 4 ? 4 : ex;
-                    const float inv = __uint_as_float((uint32_t)(254 - ex) << 23);
-                    uint32_t hi[EPL / 4], lo[EPL / 4];
-#pragma unroll
-                    for (int e = 0; e < EPL / 4; ++e) {
-                        uint32_t h2[2], l2[2];
-#pragma unroll
-                        for (int f = 0; f < 2; ++f) {
-                            const uint32_t v = w[2 * e + f];
-                            const float2 y = __fmul2_rn(make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u)),
-                                                        make_float2(inv, inv));
-                            h2[f] = __nv_cvt_float2_to_fp8x2(y, __NV_SATFINITE, __NV_E4M3);
-                            const float2 b = fp8x2_to_float2((uint16_t)h2[f]);
-                            l2[f] = __nv_cvt_float2_to_fp8x2(make_float2(y.x - b.x, y.y - b.y), __NV_SATFINITE, __NV_E4M3);
-                        }
-                        hi[e] = h2[0] | h2[1] << 16;
-                        lo[e] = l2[0] | l2[1] << 16;
-                    }
-                    // 16-byte chunks of a row are permuted as the MMA's descriptor says
-                    auto at = [&](int row) {
-                        return D == 128 ? row * 128 + (((sub >> 1) ^ (row & 7)) << 4) + (sub & 1) * 8
-                                        : row * 64 + (((sub >> 2) ^ ((row >> 1) & 3)) << 4) + (sub & 3) * 4;
-                    };
-                    if constexpr (EPL == 8) {
-                        sts2u(qd + at(c), hi[0], hi[1]);
-                        sts2u(qd + at(RP + c), lo[0], lo[1]);
-                    } else {
-                        stsi(qd + at(c), (int)hi[0]);
-                        stsi(qd + at(RP + c), (int)lo[0]);
-                    }
-                    if (sub == 0)
-                        stsi(fix_base + C::FIX_QS + (r * 64 + c) * 4, top >= 0x7f800000u ? 0x7fc00000 : (int)((uint32_t)ex << 23));
-                }
-            }
-            fence_async_smem();
+            cp_async_arrive(qraw + 8 * (k & 1));
             __syncwarp();
             if (lane == 0) {
-                mbar_arrive(qready + 8 * (k & 1));
+                mbar_arrive(qraw + 8 * (k & 1));   // hands on the rows' places
                 mbar_arrive(ifree + 8 * r);
             }
         }
         if (!ok && lane == 0) misc[1] = 1;
+        asm volatile("cp.async.wait_all;" ::: "memory");
     } else {   // -------------------------------------------------------- softmax
         constexpr int CG = C::CG;
         // p is 2^kBase at the running maximum, which is raised once a score passes it by 2^kOver: fp16 (and e5m2) hold
@@ -717,8 +689,70 @@ __global__ void __launch_bounds__(Cfg8<D, RP>::THREADS, 1)
         const int kslot = quarter * 32 + lane;   // this lane's key of a tile, and its dim of O
         const uint32_t mx_s = fix_base + C::FIX_MX + grp * 16 * CG, ls_s = fix_base + C::FIX_LS;
         const uint32_t f_s = fix_base + C::FIX_F + cb * 4, v_s = fix_base + C::FIX_V + grp * 16;
+        const uint32_t f2_s = fix_base + C::FIX_F2 + cb * 4;
         bool ok = true;
         int g = 0;
+        // this warp's share of a unit's query rows, half a warp a row, once the raw rows are there
+        auto convert = [&](int unit) {
+            const uint32_t qd = fix_base + C::FIX_Q + (unit & 1) * C::Q_BYTES;
+            constexpr int EPL = D / 16, ROWS = RP / C::SM_WARPS;   // values a lane holds of a row; rows of a warp
+            const int sub = lane & 15, odd = lane >> 4;
+#pragma unroll
+            for (int c0 = (warp - 4) * ROWS; c0 < (warp - 3) * ROWS; c0 += 2) {
+            const int c = c0 + odd;
+            uint32_t w[4] = {0u, 0u, 0u, 0u};
+            const uint32_t src = qd + ((sub >= 8 ? RP : 0) + c) * D + (sub & 7) * (2 * EPL);
+            if constexpr (EPL == 8)
+                asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(src) : "memory");
+            else
+                asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(src) : "memory");
+            uint32_t top = 0;   // two |values| at a time, which order as their bits do, infinities and NaN on top
+#pragma unroll
+            for (int e = 0; e < EPL / 2; ++e) top = __vmaxu2(top, w[e] & 0x7fff7fffu);
+#pragma unroll
+            for (int o = 8; o; o >>= 1) top = __vmaxu2(top, __shfl_xor_sync(~0u, top, o));
+            top = max(top >> 16, top & 0xffffu);
+            // 2^(exponent - 7), within the normal numbers whose reciprocal is one too
+            int ex = (int)(top >> 7) - 7;
+            ex = ex < 4 ? 4 : ex;
+            const float inv = __uint_as_float((uint32_t)(254 - ex) << 23);
+            uint32_t hi[EPL / 4], lo[EPL / 4];
+#pragma unroll
+            for (int e = 0; e < EPL / 4; ++e) {
+                uint32_t h2[2], l2[2];
+#pragma unroll
+                for (int f = 0; f < 2; ++f) {   // fp16 holds the scaled values and every difference here
+                    const uint32_t v = w[2 * e + f];
+                    const float2 y = __fmul2_rn(make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u)),
+                                                make_float2(inv, inv));
+                    const uint32_t y16 = half2_of(y.x, y.y);
+                    h2[f] = half2_to_fp8x2(y16);
+                    l2[f] = half2_to_fp8x2(hsub2(y16, fp8x2_to_half2(h2[f])));
+                }
+                hi[e] = h2[0] | h2[1] << 16;
+                lo[e] = l2[0] | l2[1] << 16;
+            }
+            // 16-byte chunks of a row are permuted as the MMA's descriptor says
+            auto at = [&](int row) {
+                return D == 128 ? row * 128 + (((sub >> 1) ^ (row & 7)) << 4) + (sub & 1) * 8
+                                : row * 64 + (((sub >> 2) ^ ((row >> 1) & 3)) << 4) + (sub & 3) * 4;
+            };
+            if constexpr (EPL == 8) {
+                sts2u(qd + at(c), hi[0], hi[1]);
+                sts2u(qd + at(RP + c), lo[0], lo[1]);
+            } else {
+                stsi(qd + at(c), (int)hi[0]);
+                stsi(qd + at(RP + c), (int)lo[0]);
+            }
+            if (sub == 0)
+                stsi(fix_base + C::FIX_QS + (unit % kRing * 64 + c) * 4, top >= 0x7f80u ? 0x7fc00000 : (int)((uint32_t)ex << 23));
+            }
+            fence_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(qready + 8 * (unit & 1));
+        };
+        int done_parts = 1;       // of the unit before
+        float done_ref = 0.f, done_m = 0.f;   // done_m: of column gt
         for (int k = 0;; ++k) {
             const int r = k % kRing;
             if (!wait_warp(iready + 8 * r, (uint32_t)(k / kRing) & 1u)) ok = false;
@@ -727,52 +761,138 @@ __global__ void __launch_bounds__(Cfg8<D, RP>::THREADS, 1)
                 break;
             }
             const Unit8 u = read_unit(r);
-            if (u.b < 0) break;
+            const bool more = u.b >= 0;
+            if (more) {
+                if (!wait_warp(qraw + 8 * (k & 1), (uint32_t)(k >> 1) & 1u)) ok = false;
+                convert(k);
+            }
+            // the unit before is written out after this one's first tile (or at the end): its last product and this
+            // unit's first do not wait for that
+            bool pending = k > 0;
+            const int dr = (k - 1) % kRing;
+            if (pending && gt < CG) {   // the sums are all there since the barrier
+                const uint32_t c = ls_s + (cb + gt) * 4;
+                const float lsum = (lds1(c) + lds1(c + 256)) + (lds1(c + 512) + lds1(c + 768));
+                // a part keeps its own maximum and sum; a whole unit is divided by its sum
+                sts1(f_s + gt * 4, done_parts > 1 ? done_ref : done_ref / lsum);
+                if (done_parts > 1) {
+                    const Unit8 done = read_unit(dr);
+                    a.part_ml[(size_t)(done.slot + done.part) * RP + cb + gt] = make_float2(done_m, lsum);
+                }
+            }
+            if (!more) {
+                if (!pending) break;
+                bar_sync(bar, 128);
+            }
+            const uint32_t oc = tl + C::O_COL + (k & 1) * 3 * RP + cb;   // this unit's O
             const int L = u.P + u.n;
             float2 m[CG / 2], l[CG / 2];   // kBase - maximum; sums over this lane's keys
-            float ref = 0.f, iref = 0.f;               // the value scales' reference and its reciprocal
+            float ref = 0.f, iref = 0.f;   // the value scales' reference and its reciprocal
 #pragma unroll
             for (int c = 0; c < CG / 2; ++c) {
                 m[c] = make_float2(1e30f, 1e30f);
                 l[c] = make_float2(0.f, 0.f);
             }
             const uint32_t qs = fix_base + C::FIX_QS + (r * 64 + cb) * 4;   // query scales, there before the first scores
-            bool gone = false;
-            for (int j = u.j0; j < u.j1; ++j, ++g) {
-                const int x = g & 1, st = g % C::STAGES, key = j * kTileKeys + kslot;
+            int j = u.j0;
+            // y: the columns' exponents before the maximum is taken off; vs: the key's value scale
+            auto scores = [&](float2 (&y)[CG / 2], float &vs) {
+                const int x = g & 1;
                 if (ok && !wait_warp(sfull + 8 * x, (uint32_t)(g >> 1) & 1u)) ok = false;
                 tc_fence_after();
-                const uint32_t side = sm_base + C::OFF_SIDE + st * C::SIDE + kslot * 4;
-                float ks = lds1(side) * a.scale_log2, vs = lds1(side + 512);
+                const uint32_t side = sm_base + C::OFF_SIDE + g % C::STAGES * C::SIDE + kslot * 4;
+                float s[CG];
+                tc_ldn<CG>(tl + C::S_COL + x * RP + cb, s);
+                float ks = lds1(side) * a.scale_log2;
+                vs = lds1(side + 512);
                 if (!(vs <= 3.402823466e38f)) {   // a poisoned value row: NaN to every row that sees it
                     ks = __int_as_float(0x7fc00000);
                     vs = 0.f;
                 }
-                // y: the columns' exponents before the maximum is taken off
-                float2 y[CG / 2];
-                {
-                    float hi[CG], lo[CG];
-                    const uint32_t sb = tl + C::S_COL + x * 2 * RP + cb;
-                    tc_ldn<CG>(sb, hi);
-                    tc_ldn<CG>(sb + RP, lo);
-                    tc_wait_ld();
+                tc_wait_ld();
 #pragma unroll
-                    for (int c = 0; c < CG / 4; ++c) {
-                        const float4 v = lds4(qs + 16 * c);
-                        const float2 k2 = make_float2(ks, ks);
-                        y[2 * c] = __fmul2_rn(__fadd2_rn(make_float2(hi[4 * c], hi[4 * c + 1]), make_float2(lo[4 * c], lo[4 * c + 1])),
-                                              __fmul2_rn(k2, make_float2(v.x, v.y)));
-                        y[2 * c + 1] = __fmul2_rn(__fadd2_rn(make_float2(hi[4 * c + 2], hi[4 * c + 3]), make_float2(lo[4 * c + 2], lo[4 * c + 3])),
-                                                  __fmul2_rn(k2, make_float2(v.z, v.w)));
+                for (int c = 0; c < CG / 4; ++c) {
+                    const float4 v = lds4(qs + 16 * c);
+                    y[2 * c] = __fmul2_rn(__fmul2_rn(make_float2(s[4 * c], s[4 * c + 1]), make_float2(v.x, v.y)), make_float2(ks, ks));
+                    y[2 * c + 1] = __fmul2_rn(__fmul2_rn(make_float2(s[4 * c + 2], s[4 * c + 3]), make_float2(v.z, v.w)), make_float2(ks, ks));
+                }
+            };
+            auto above = [&](const float2 (&y)[CG / 2]) -> float {   // the furthest score above its column's maximum
+                float top = -INFINITY, top2 = -INFINITY;
+#pragma unroll
+                for (int c = 0; c < CG / 2; ++c) {
+                    const float2 d = __fadd2_rn(y[c], m[c]);
+                    top = fmaxf(top, d.x);
+                    top2 = fmaxf(top2, d.y);
+                }
+                return fmaxf(top, top2);
+            };
+            auto write_p = [&](const float2 (&y)[CG / 2], float vs) {
+                const float2 rv = make_float2(vs * iref, vs * iref);
+                const uint32_t pd = fix_base + C::FIX_P + (g & 1) * C::P_BYTES + kslot * 64;
+                const int flip = (kslot >> 1) & 3;
+                constexpr int STEP = CG % 16 == 0 ? 16 : 8;
+#pragma unroll
+                for (int c = 0; c < CG; c += STEP) {
+                    uint32_t w[3][STEP / 4];   // the three parts, four columns a word
+#pragma unroll
+                    for (int i = 0; i < STEP / 4; ++i) {
+                        uint32_t h[2], a1[2], a2[2];
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const int cc = c / 2 + 2 * i + e;
+                            const float2 d = __fadd2_rn(y[cc], m[cc]);
+                            const float2 pe = make_float2(ex2(d.x), ex2(d.y));
+                            l[cc] = __fadd2_rn(l[cc], pe);
+                            const float2 pr = __fmul2_rn(pe, rv);
+                            h[e] = half2_of(pr.x, pr.y);
+                            a1[e] = hsub2(h[e], h[e] & 0xff00ff00u);
+                            a2[e] = hsub2(a1[e], a1[e] & 0xff00ff00u) + 0x00800080u;   // half a step: rounded
+                        }
+                        w[0][i] = __byte_perm(h[0], h[1], 0x7531);
+                        w[1][i] = __byte_perm(a1[0], a1[1], 0x7531);
+                        w[2][i] = __byte_perm(a2[0], a2[1], 0x7531);
+                    }
+                    if (ok) {
+#pragma unroll
+                        for (int e = 0; e < 3; ++e) {
+                            const int col = e * RP + cb + c;
+                            const uint32_t d = pd + (col >> 6) * C::P_ATOM + ((((col >> 4) & 3) ^ flip) << 4) + (col & 15);
+                            if constexpr (STEP == 16) sts4u(d, w[e][0], w[e][1], w[e][2], w[e][3]);
+                            else sts2u(d, w[e][0], w[e][1]);
+                        }
                     }
                 }
+            };
+            auto hand_over = [&]() {
+                fence_async_smem();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(pfull + 8 * (g & 1));
+            };
+            // the common tile: every key seen by every row, no maximum raised; false with nothing done otherwise
+            auto plain_tile = [&]() -> bool {
+                float2 y[CG / 2];
+                float vs;
+                scores(y, vs);
+                if (bar_any(bar, 128, above(y) > kBase + kOver || vs > ref || !ok)) return false;
+                write_p(y, vs);
+                hand_over();
+                return true;
+            };
+            // any one tile; false: a wait has failed
+            auto any_tile = [&](bool raise) -> bool {
+                const int st = g % C::STAGES, key = j * kTileKeys + kslot;
+                float2 y[CG / 2];
+                float vs;
+                scores(y, vs);
                 if (j * kTileKeys + kTileKeys > u.P) {   // tree keys, or keys past the end
                     int from = -0x7fffffff, to = 0x7fffffff;   // the columns that see this lane's key
                     if (key >= u.P) {
                         from = to = 0;
                         if (key < L) {
                             from = (key - u.P) * a.G - u.row0 - cb;
-                            to = ldsi(side + 1024) * a.G - u.row0 - cb;
+                            to = ldsi(sm_base + C::OFF_SIDE + st * C::SIDE + kslot * 4 + 1024) * a.G - u.row0 - cb;
                         }
                     }
 #pragma unroll
@@ -781,40 +901,30 @@ __global__ void __launch_bounds__(Cfg8<D, RP>::THREADS, 1)
                         if (!(2 * c + 1 >= from && 2 * c + 1 < to)) y[c].y = -INFINITY;
                     }
                 }
-                bool raise = j == u.j0;
-                if (!raise) {
-                    float2 d = __fadd2_rn(y[0], m[0]);
-                    float top = d.x, top2 = d.y;
-#pragma unroll
-                    for (int c = 1; c < CG / 2; ++c) {
-                        d = __fadd2_rn(y[c], m[c]);
-                        top = fmaxf(top, d.x);
-                        top2 = fmaxf(top2, d.y);
-                    }
-                    raise = bar_any(bar, 128, fmaxf(top, top2) > kBase + kOver || vs > ref || !ok);
-                }
+                if (!raise) raise = bar_any(bar, 128, above(y) > kBase + kOver || vs > ref || !ok);
                 if (raise) {
                     // new maxima: of each column over the tile, taken where the old one is passed by 2^kOver
+                    float t[CG];
 #pragma unroll
-                    for (int c = 0; c < CG; c += 4) {
-                        const float4 w = make_float4(warp_max(y[c / 2].x), warp_max(y[c / 2].y), warp_max(y[c / 2 + 1].x),
-                                                     warp_max(y[c / 2 + 1].y));
-                        if (lane == 0) sts4(mx_s + (quarter * CG + c) * 4, w);
+                    for (int c = 0; c < CG / 2; ++c) {
+                        t[2 * c] = y[c].x;
+                        t[2 * c + 1] = y[c].y;
                     }
+                    reduce_scatter<CG, true>(t, lane);
+                    if (lane % (32 / CG) == 0) sts1(mx_s + (quarter * CG + lane / (32 / CG)) * 4, t[0]);
                     const float vtop = warp_max(vs);
                     if (lane == 0) sts1(v_s + quarter * 4, vtop);
                     if (bar_any(bar, 128, !ok)) {
                         ok = false;
-                        gone = true;
-                        break;
+                        return false;
                     }
                     const float4 v4 = lds4(v_s);
                     float nref = fmaxf(fmaxf(v4.x, v4.y), fmaxf(v4.z, v4.w));
                     // a half more than the largest scale so far, so that few tiles raise it
                     nref = nref > ref ? nref * 1.5f : ref;
-                    const float rr = nref > 0.f ? ref / nref : 1.f;
+                    iref = nref > 0.f ? __frcp_rn(nref) : 0.f;
+                    const float rr = nref > 0.f ? ref * iref : 1.f;
                     ref = nref;
-                    iref = ref > 0.f ? 1.f / ref : 0.f;
                     const bool later = j > u.j0;   // O so far is rescaled once the product before this one has landed in it
                     if (later) {
                         if (ok && !wait_warp(pvdone + 8 * ((g - 1) & 1), (uint32_t)((g - 1) >> 1) & 1u)) ok = false;
@@ -844,73 +954,157 @@ __global__ void __launch_bounds__(Cfg8<D, RP>::THREADS, 1)
                                 al[e] = ex2(al[e]);
                                 float &le = e & 1 ? l[(c + e) / 2].y : l[(c + e) / 2].x;
                                 le *= al[e];
-                                al[e] *= rr;
+                                if (gt == c + e) sts1(f2_s + (c + e) * 4, al[e] * rr);
                             }
-                            if (ok && quarter * 32 < D) {
-                                float o[12];
-#pragma unroll
-                                for (int i = 0; i < 3; ++i) tc_ld4(tl + C::O_COL + i * RP + cb + c, o + 4 * i);
+                        }
+                    }
+                    if (later) {
+                        bar_sync(bar, 128);
+                        if (ok && quarter * 32 < D) {
+#pragma unroll 1
+                            for (int c = 0; c < 3 * CG; c += 4) {
+                                float o[4];
+                                const uint32_t at = oc + c / CG * RP + c % CG;
+                                const float4 f = lds4(f2_s + c % CG * 4);
+                                tc_ld4(at, o);
                                 tc_wait_ld();
-#pragma unroll
-                                for (int i = 0; i < 12; ++i) o[i] *= al[i & 3];
-#pragma unroll
-                                for (int i = 0; i < 3; ++i) tc_st4(tl + C::O_COL + i * RP + cb + c, o + 4 * i);
+                                o[0] *= f.x;
+                                o[1] *= f.y;
+                                o[2] *= f.z;
+                                o[3] *= f.w;
+                                tc_st4(at, o);
                             }
-                        }
-                    }
-                    if (later) tc_wait_st();   // the exchange is written again only after another vote
-                }
-                // P buffer x is free: S(g) was issued once the product that read P(g - 2) had finished
-                const float2 rv = make_float2(vs * iref, vs * iref);
-                const uint32_t pd = fix_base + C::FIX_P + x * C::P_BYTES + kslot * 64;
-                const int flip = (kslot >> 1) & 3;
-                constexpr int STEP = CG % 16 == 0 ? 16 : 8;
-#pragma unroll
-                for (int c = 0; c < CG; c += STEP) {
-                    uint32_t w[3][STEP / 4];   // the three parts, four columns a word
-#pragma unroll
-                    for (int i = 0; i < STEP / 4; ++i) {
-                        uint32_t h[2], a1[2], a2[2];
-#pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            const int cc = c / 2 + 2 * i + e;
-                            const float2 d = __fadd2_rn(y[cc], m[cc]);
-                            const float2 pe = make_float2(ex2(d.x), ex2(d.y));
-                            l[cc] = __fadd2_rn(l[cc], pe);
-                            const float2 pr = __fmul2_rn(pe, rv);
-                            h[e] = half2_of(pr.x, pr.y);
-                            a1[e] = hsub2(h[e], h[e] & 0xff00ff00u);
-                            a2[e] = hsub2(a1[e], a1[e] & 0xff00ff00u) + 0x00800080u;   // half a step: rounded
-                        }
-                        w[0][i] = __byte_perm(h[0], h[1], 0x7531);
-                        w[1][i] = __byte_perm(a1[0], a1[1], 0x7531);
-                        w[2][i] = __byte_perm(a2[0], a2[1], 0x7531);
-                    }
-                    if (ok) {
-#pragma unroll
-                        for (int t = 0; t < 3; ++t) {
-                            const int col = t * RP + cb + c;
-                            const uint32_t d = pd + (col >> 6) * C::P_ATOM + ((((col >> 4) & 3) ^ flip) << 4) + (col & 15);
-                            if constexpr (STEP == 16) sts4u(d, w[t][0], w[t][1], w[t][2], w[t][3]);
-                            else sts2u(d, w[t][0], w[t][1]);
+                            tc_wait_st();
                         }
                     }
                 }
+                write_p(y, vs);
                 if (j * kTileKeys + kTileKeys > L && ok) {
                     // V's rows past the last key may hold anything: zeros (whose weights are zero too)
                     const uint32_t vt = sm_base + st * C::STAGE_BYTES + C::OP_BYTES;
                     const int r0 = (L - j * kTileKeys) * (D / 16);
+#pragma unroll 1
                     for (int i = r0 + tid - 128; i < kTileKeys * (D / 16); i += 32 * C::SM_WARPS)
                         sts4u(vt + i * 16, 0u, 0u, 0u, 0u);
                 }
-                fence_async_smem();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(pfull + 8 * x);
-            }
+                hand_over();
+                return true;
+            };
+            const int plain_end = min(u.j1, u.P / kTileKeys);   // tiles before the first with tree keys
+            bool gone = false;
+            do {
+                if (more) {
+                    bool raise = j == u.j0;
+                    if (!raise) {
+#pragma unroll 1
+                        while (j < plain_end && plain_tile()) {
+                            ++j;
+                            ++g;
+                        }
+                        raise = j < plain_end;
+                        if (j == u.j1) break;
+                    }
+                    if (!any_tile(raise)) {
+                        gone = true;
+                        break;
+                    }
+                    ++j;
+                    ++g;
+                }
+                if (pending) {
+                    pending = false;
+                    const Unit8 done = read_unit(dr);
+                    const int pg = more ? g - 2 : g - 1;   // its last tile
+                    if (ok && !wait_warp(pvdone + 8 * (pg & 1), (uint32_t)(pg >> 1) & 1u)) ok = false;
+                    tc_fence_after();
+                    __nv_bfloat16 *ob = a.out + (size_t)done.b * n_max * a.Hq * D;
+                    const uint32_t rows = fix_base + C::FIX_QROW + (dr * 64 + cb) * 4;
+        #pragma unroll 1
+                    for (int c = 0; c < CG; c += 8) {
+                        float o[3][8];
+                        if (ok && quarter * 32 < D) {
+        #pragma unroll
+                            for (int i = 0; i < 3; ++i) tc_ld8(tl + C::O_COL + (~k & 1) * 3 * RP + i * RP + cb + c, o[i]);
+                            tc_wait_ld();
+                        }
+                        if (!ok || quarter * 32 >= D) continue;
+        #pragma unroll
+                        for (int e = 0; e < 8; e += 4) {
+                            const float4 f = lds4(f_s + (c + e) * 4);
+                            o[0][e] = ((o[0][e] + o[1][e]) + o[2][e]) * f.x;
+                            o[0][e + 1] = ((o[0][e + 1] + o[1][e + 1]) + o[2][e + 1]) * f.y;
+                            o[0][e + 2] = ((o[0][e + 2] + o[1][e + 2]) + o[2][e + 2]) * f.z;
+                            o[0][e + 3] = ((o[0][e + 3] + o[1][e + 3]) + o[2][e + 3]) * f.w;
+                        }
+                        if (done.parts > 1) {
+                            float *po = a.part_o + ((size_t)(done.slot + done.part) * RP + cb + c) * D + kslot;
+        #pragma unroll
+                            for (int e = 0; e < 8; ++e) po[e * D] = o[0][e];
+                        } else {
+                            // two columns at a time: even lanes store dims (d, d + 1) of the first, odd lanes of the second
+        #pragma unroll
+                            for (int e = 0; e < 8; e += 2) {
+                                const float keep = lane & 1 ? o[0][e + 1] : o[0][e], send = lane & 1 ? o[0][e] : o[0][e + 1];
+                                const float got = __shfl_xor_sync(~0u, send, 1);
+                                const int row = ldsi(rows + (c + e + (lane & 1)) * 4);
+                                const __nv_bfloat162 v = lane & 1 ? __floats2bfloat162_rn(got, keep) : __floats2bfloat162_rn(keep, got);
+                                if (row >= 0) *(__nv_bfloat162 *)(ob + (size_t)row * D + (kslot & ~1)) = v;
+                            }
+                        }
+                    }
+                    if (done.parts > 1) {   // the last part of the item to finish joins them, for this group's columns
+                        __threadfence();
+                        bar_sync(bar, 128);
+                        if (gt == 0) {
+                            unsigned *cnt = a.joins + (size_t)done.slot * 4 + grp;
+                            const bool last = ok && atomicAdd(cnt, 1u) == (unsigned)done.parts - 1;
+                            if (last) *cnt = 0u;
+                            misc[4 + grp] = last;
+                        }
+                        bar_sync(bar, 128);
+                        if (misc[4 + grp]) {
+                            __threadfence();
+                            constexpr int EPL = D / 32;
+                            for (int c = warp & 3; c < CG; c += 4) {   // a warp a column, lane = part, then lane = dims
+                                const int row = ldsi(rows + c * 4);
+                                if (row < 0) continue;
+                                float2 ml = make_float2(-INFINITY, 0.f);
+                                if (lane < done.parts) ml = __ldcg(a.part_ml + (size_t)(done.slot + lane) * RP + cb + c);
+                                const float mx = warp_max(ml.x);
+                                const float wt = lane < done.parts ? ex2(ml.x - mx) : 0.f;
+                                float ls = wt * ml.y;
+        #pragma unroll
+                                for (int o = 16; o; o >>= 1) ls += __shfl_xor_sync(~0u, ls, o);
+                                float acc[EPL] = {};
+                                const float *po = a.part_o + ((size_t)done.slot * RP + cb + c) * D + lane * EPL;
+        #pragma unroll 8
+                                for (int s = 0; s < done.parts; ++s) {
+                                    const float ws = __shfl_sync(~0u, wt, s);
+                                    float v[EPL];
+                                    if constexpr (EPL == 4) {
+                                        const float4 f = __ldcg((const float4 *)(po + (size_t)s * RP * D));
+                                        v[0] = f.x; v[1] = f.y; v[2] = f.z; v[3] = f.w;
+                                    } else {
+                                        const float2 f = __ldcg((const float2 *)(po + (size_t)s * RP * D));
+                                        v[0] = f.x; v[1] = f.y;
+                                    }
+        #pragma unroll
+                                    for (int e = 0; e < EPL; ++e) acc[e] = fmaf(ws, v[e], acc[e]);
+                                }
+                                const float inv = 1.f / ls;
+        #pragma unroll
+                                for (int e = 0; e < EPL; e += 2)
+                                    *(__nv_bfloat162 *)(ob + (size_t)row * D + lane * EPL + e) =
+                                        __floats2bfloat162_rn(acc[e] * inv, acc[e + 1] * inv);
+                            }
+                        }
+                    }
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(ifree + 8 * dr);
+                }
+            } while (more && j < u.j1);
+            if (!more) break;
             if (gone) break;
-
-            // ---- the unit's output
             float v[CG];
 #pragma unroll
             for (int c = 0; c < CG / 2; ++c) {
@@ -919,115 +1113,20 @@ __global__ void __launch_bounds__(Cfg8<D, RP>::THREADS, 1)
             }
             reduce_scatter<CG>(v, lane);
             if (lane % (32 / CG) == 0) sts1(ls_s + (quarter * 64 + cb + lane / (32 / CG)) * 4, v[0]);
-            bar_sync(bar, 128);
-            float lsum = 0.f;
-            if (gt < CG) {
-                const uint32_t c = ls_s + (cb + gt) * 4;
-                lsum = (lds1(c) + lds1(c + 256)) + (lds1(c + 512) + lds1(c + 768));
-                // a part keeps its own maximum and sum; a whole unit is divided by its sum here
-                sts1(f_s + gt * 4, u.parts > 1 ? ref : ref / lsum);
-            }
             if (u.parts > 1) {
-                float mm = 0.f;
 #pragma unroll
                 for (int c = 0; c < CG; ++c)
-                    if (gt == c) mm = -(c & 1 ? m[c / 2].y : m[c / 2].x);
-                if (gt < CG) a.part_ml[(size_t)(u.slot + u.part) * RP + cb + gt] = make_float2(mm, lsum);
+                    if (gt == c) done_m = -(c & 1 ? m[c / 2].y : m[c / 2].x);
             }
-            if (ok && !wait_warp(pvdone + 8 * ((g - 1) & 1), (uint32_t)((g - 1) >> 1) & 1u)) ok = false;
-            tc_fence_after();
-            bar_sync(bar, 128);
-            __nv_bfloat16 *ob = a.out + (size_t)u.b * n_max * a.Hq * D;
-            const uint32_t rows = fix_base + C::FIX_QROW + (r * 64 + cb) * 4;
-#pragma unroll
-            for (int c = 0; c < CG; c += 8) {
-                float o[3][8];
-                if (ok && quarter * 32 < D) {
-#pragma unroll
-                    for (int i = 0; i < 3; ++i) tc_ld8(tl + C::O_COL + i * RP + cb + c, o[i]);
-                    tc_wait_ld();
-                }
-                if (!ok || quarter * 32 >= D) continue;
-#pragma unroll
-                for (int e = 0; e < 8; e += 4) {
-                    const float4 f = lds4(f_s + (c + e) * 4);
-                    o[0][e] = ((o[0][e] + o[1][e]) + o[2][e]) * f.x;
-                    o[0][e + 1] = ((o[0][e + 1] + o[1][e + 1]) + o[2][e + 1]) * f.y;
-                    o[0][e + 2] = ((o[0][e + 2] + o[1][e + 2]) + o[2][e + 2]) * f.z;
-                    o[0][e + 3] = ((o[0][e + 3] + o[1][e + 3]) + o[2][e + 3]) * f.w;
-                }
-                if (u.parts > 1) {
-                    float *po = a.part_o + ((size_t)(u.slot + u.part) * RP + cb + c) * D + kslot;
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) po[e * D] = o[0][e];
-                } else {
-                    // two columns at a time: even lanes store dims (d, d + 1) of the first, odd lanes of the second
-#pragma unroll
-                    for (int e = 0; e < 8; e += 2) {
-                        const float keep = lane & 1 ? o[0][e + 1] : o[0][e], send = lane & 1 ? o[0][e] : o[0][e + 1];
-                        const float got = __shfl_xor_sync(~0u, send, 1);
-                        const int row = ldsi(rows + (c + e + (lane & 1)) * 4);
-                        const __nv_bfloat162 v = lane & 1 ? __floats2bfloat162_rn(got, keep) : __floats2bfloat162_rn(keep, got);
-                        if (row >= 0) *(__nv_bfloat162 *)(ob + (size_t)row * D + (kslot & ~1)) = v;
-                    }
-                }
-            }
-            if (u.parts > 1) {   // the last part of the item to finish joins them, for this group's columns
-                __threadfence();
-                bar_sync(bar, 128);
-                if (gt == 0) {
-                    unsigned *cnt = a.joins + (size_t)u.slot * 4 + grp;
-                    const bool last = ok && atomicAdd(cnt, 1u) == (unsigned)u.parts - 1;
-                    if (last) *cnt = 0u;
-                    misc[4 + grp] = last;
-                }
-                bar_sync(bar, 128);
-                if (misc[4 + grp]) {
-                    __threadfence();
-                    constexpr int EPL = D / 32;
-                    for (int c = warp & 3; c < CG; c += 4) {   // a warp a column, lane = part, then lane = dims
-                        const int row = ldsi(rows + c * 4);
-                        if (row < 0) continue;
-                        float2 ml = make_float2(-INFINITY, 0.f);
-                        if (lane < u.parts) ml = __ldcg(a.part_ml + (size_t)(u.slot + lane) * RP + cb + c);
-                        const float mx = warp_max(ml.x);
-                        const float wt = lane < u.parts ? ex2(ml.x - mx) : 0.f;
-                        float ls = wt * ml.y;
-#pragma unroll
-                        for (int o = 16; o; o >>= 1) ls += __shfl_xor_sync(~0u, ls, o);
-                        float acc[EPL] = {};
-                        const float *po = a.part_o + ((size_t)u.slot * RP + cb + c) * D + lane * EPL;
-#pragma unroll 8
-                        for (int s = 0; s < u.parts; ++s) {
-                            const float ws = __shfl_sync(~0u, wt, s);
-                            float v[EPL];
-                            if constexpr (EPL == 4) {
-                                const float4 f = __ldcg((const float4 *)(po + (size_t)s * RP * D));
-                                v[0] = f.x; v[1] = f.y; v[2] = f.z; v[3] = f.w;
-                            } else {
-                                const float2 f = __ldcg((const float2 *)(po + (size_t)s * RP * D));
-                                v[0] = f.x; v[1] = f.y;
-                            }
-#pragma unroll
-                            for (int e = 0; e < EPL; ++e) acc[e] = fmaf(ws, v[e], acc[e]);
-                        }
-                        const float inv = 1.f / ls;
-#pragma unroll
-                        for (int e = 0; e < EPL; e += 2)
-                            *(__nv_bfloat162 *)(ob + (size_t)row * D + lane * EPL + e) =
-                                __floats2bfloat162_rn(acc[e] * inv, acc[e + 1] * inv);
-                    }
-                }
-            }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(ifree + 8 * r);
+            done_parts = u.parts;
+            done_ref = ref;
         }
         if (!ok) misc[1] = 1;
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (warp == 0)
+    if (warp == 2)
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(C::TMEM_COLS) : "memory");
     if (tid == 0) {
         if (misc[1]) flag(a.status, TS_STATUS_TIMEOUT);
@@ -1046,14 +1145,14 @@ struct Plan8 {
     size_t ml, o, bytes;   // offsets of the parts, all bytes
 };
 
-// RP: the rows there can be, cut into equal blocks of at most 64, rounded up
+// RP: the rows there can be, cut into equal blocks of at most 48, rounded up
 // to 16. Slots: an item with T tiles is cut into ceil(T / per) parts, and
 // per >= all tiles / (kCutsPerSm * SMs), so the parts of the cut items (each
 // longer than per) number less than 2 * kCutsPerSm * SMs.
 Plan8 plan8(int B, int Hkv, int G, int n_max, int d) {
     Plan8 p;
     const long long rows = (long long)n_max * G;
-    p.blocks = (int)((rows + 63) / 64);
+    p.blocks = (int)((rows + 47) / 48);
     p.rp = (int)(((rows + p.blocks - 1) / p.blocks + 15) / 16 * 16);
     p.blocks = (int)((rows + p.rp - 1) / p.rp);
     p.slots = B <= kReqCache ? 2 * kCutsPerSm * num_sms() : 0;
@@ -1114,14 +1213,12 @@ cudaError_t launch_attn_kv8(void *out, const void *q, const ts_kv8 &kv, int Hq, 
     if (kv.d == 128) switch (p.rp) {
         case 16: return launch8<128, 16>(mk, mv, a, grid, s);
         case 32: return launch8<128, 32>(mk, mv, a, grid, s);
-        case 48: return launch8<128, 48>(mk, mv, a, grid, s);
-        default: return launch8<128, 64>(mk, mv, a, grid, s);
+        default: return launch8<128, 48>(mk, mv, a, grid, s);
     }
     switch (p.rp) {
         case 16: return launch8<64, 16>(mk, mv, a, grid, s);
         case 32: return launch8<64, 32>(mk, mv, a, grid, s);
-        case 48: return launch8<64, 48>(mk, mv, a, grid, s);
-        default: return launch8<64, 64>(mk, mv, a, grid, s);
+        default: return launch8<64, 48>(mk, mv, a, grid, s);
     }
 }
 
