@@ -228,7 +228,8 @@ struct Cfg8 {
     static constexpr int FIX_LS = FIX_MX + 4 * RP * 4;         // column maxima [groups][4 warps][CG]
     static constexpr int FIX_F = FIX_LS + 4 * 64 * 4;          // column sums [4 warps][64], then factors [64]
     static constexpr int FIX_F2 = FIX_F + 64 * 4;              // factors of O where a maximum is raised [64]
-    static constexpr int FIX_V = FIX_F2 + 64 * 4;              // largest value scales [groups][4 warps]
+    static constexpr int FIX_M = FIX_F2 + 64 * 4;              // kBase - maximum [64]
+    static constexpr int FIX_V = FIX_M + 64 * 4;               // largest value scales [groups][4 warps]
     static constexpr int FIX_QS = FIX_V + 64;                  // query scales [kRing][64], output rows [kRing][64]
     static constexpr int FIX_QROW = FIX_QS + kRing * 64 * 4;
     static constexpr int FIX_REQ = FIX_QROW + kRing * 64 * 4;  // requests: n, P, tiles, parts
@@ -272,6 +273,47 @@ __device__ __forceinline__ void reduce_scatter(float *v, int lane) {
         v[0] = MAX ? fmaxf(v[0], got) : v[0] + got;
     }
     if constexpr (W > 1) reduce_scatter<(N > 1 ? N / 2 : 1), MAX, W / 2>(v, lane);
+}
+
+// The parts of a cut item into its output rows, one group's columns: a warp a column, lane = part for the weights, then
+// lane = dims. Out of line: it runs once an item, and the loops around its call are better short.
+template <int D, int RP, int CG>
+__device__ __noinline__ void join_parts(const float2 *part_ml, const float *part_o, int parts, uint32_t rows,
+                                        __nv_bfloat16 *out) {
+    constexpr int EPL = D / 32;
+    const int lane = threadIdx.x & 31;
+    __threadfence();
+    for (int c = (threadIdx.x >> 5) & 3; c < CG; c += 4) {
+        const int row = ldsi(rows + c * 4);
+        if (row < 0) continue;
+        float2 ml = make_float2(-INFINITY, 0.f);
+        if (lane < parts) ml = __ldcg(part_ml + (size_t)lane * RP + c);
+        const float mx = warp_max(ml.x);
+        const float wt = lane < parts ? ex2(ml.x - mx) : 0.f;
+        float ls = wt * ml.y;
+#pragma unroll
+        for (int o = 16; o; o >>= 1) ls += __shfl_xor_sync(~0u, ls, o);
+        float acc[EPL] = {};
+        const float *po = part_o + (size_t)c * D + lane * EPL;
+#pragma unroll 8
+        for (int s = 0; s < parts; ++s) {
+            const float ws = __shfl_sync(~0u, wt, s);
+            float v[EPL];
+            if constexpr (EPL == 4) {
+                const float4 f = __ldcg((const float4 *)(po + (size_t)s * RP * D));
+                v[0] = f.x; v[1] = f.y; v[2] = f.z; v[3] = f.w;
+            } else {
+                const float2 f = __ldcg((const float2 *)(po + (size_t)s * RP * D));
+                v[0] = f.x; v[1] = f.y;
+            }
+#pragma unroll
+            for (int e = 0; e < EPL; ++e) acc[e] = fmaf(ws, v[e], acc[e]);
+        }
+        const float inv = 1.f / ls;
+#pragma unroll
+        for (int e = 0; e < EPL; e += 2)
+            *(__nv_bfloat162 *)(out + (size_t)row * D + lane * EPL + e) = __floats2bfloat162_rn(acc[e] * inv, acc[e + 1] * inv);
+    }
 }
 
 template <int D, int RP>
@@ -534,9 +576,8 @@ __global__ void __launch_bounds__(Cfg8<D, RP>::THREADS, 1)
                 const uint32_t side = sm_base + C::OFF_SIDE + st * C::SIDE + lane * 4;
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const int key = key0 + i * 32 + lane;
-                    const bool in = key < L && (i < 2 ? has0 : has1);
-                    const size_t row = in ? (size_t)((i < 2 ? row0 : row1) + (i & 1) * 32 + lane) : 0;
+                    const bool in = key0 + i * 32 + lane < L && (i < 2 ? has0 : has1);
+                    const int row = in ? (i < 2 ? row0 : row1) + (i & 1) * 32 + lane : 0;
                     cp_async4(side + i * 128, a.k_scale + row, in);
                     cp_async4(side + 512 + i * 128, a.v_scale + row, in);
                 }
@@ -689,7 +730,7 @@ __global__ void __launch_bounds__(Cfg8<D, RP>::THREADS, 1)
         const int kslot = quarter * 32 + lane;   // this lane's key of a tile, and its dim of O
         const uint32_t mx_s = fix_base + C::FIX_MX + grp * 16 * CG, ls_s = fix_base + C::FIX_LS;
         const uint32_t f_s = fix_base + C::FIX_F + cb * 4, v_s = fix_base + C::FIX_V + grp * 16;
-        const uint32_t f2_s = fix_base + C::FIX_F2 + cb * 4;
+        const uint32_t f2_s = fix_base + C::FIX_F2 + cb * 4, m_s = fix_base + C::FIX_M + cb * 4;
         bool ok = true;
         int g = 0;
         // this warp's share of a unit's query rows, half a warp a row, once the raw rows are there
@@ -697,7 +738,7 @@ __global__ void __launch_bounds__(Cfg8<D, RP>::THREADS, 1)
             const uint32_t qd = fix_base + C::FIX_Q + (unit & 1) * C::Q_BYTES;
             constexpr int EPL = D / 16, ROWS = RP / C::SM_WARPS;   // values a lane holds of a row; rows of a warp
             const int sub = lane & 15, odd = lane >> 4;
-#pragma unroll
+#pragma unroll 1
             for (int c0 = (warp - 4) * ROWS; c0 < (warp - 3) * ROWS; c0 += 2) {
             const int c = c0 + odd;
             uint32_t w[4] = {0u, 0u, 0u, 0u};
@@ -784,6 +825,7 @@ __global__ void __launch_bounds__(Cfg8<D, RP>::THREADS, 1)
                 if (!pending) break;
                 bar_sync(bar, 128);
             }
+            if (gt < CG) sts1(m_s + gt * 4, 1e30f);
             const uint32_t oc = tl + C::O_COL + (k & 1) * 3 * RP + cb;   // this unit's O
             const int L = u.P + u.n;
             float2 m[CG / 2], l[CG / 2];   // kBase - maximum; sums over this lane's keys
@@ -926,40 +968,28 @@ __global__ void __launch_bounds__(Cfg8<D, RP>::THREADS, 1)
                     const float rr = nref > 0.f ? ref * iref : 1.f;
                     ref = nref;
                     const bool later = j > u.j0;   // O so far is rescaled once the product before this one has landed in it
+                    if (gt < CG) {
+                        const uint32_t c = mx_s + gt * 4;
+                        const float top = fmaxf(fmaxf(lds1(c), lds1(c + 4 * CG)), fmaxf(lds1(c + 8 * CG), lds1(c + 12 * CG)));
+                        const float old = lds1(m_s + gt * 4), nm = top + old > kBase + kOver ? kBase - top : old;
+                        sts1(m_s + gt * 4, nm);
+                        sts1(f2_s + gt * 4, ex2(nm - old));   // 2^(old maximum - new)
+                    }
+                    bar_sync(bar, 128);
+#pragma unroll
+                    for (int c = 0; c < CG / 4; ++c) {
+                        const float4 v = lds4(m_s + 16 * c);
+                        m[2 * c] = make_float2(v.x, v.y);
+                        m[2 * c + 1] = make_float2(v.z, v.w);
+                        if (later) {
+                            const float4 f = lds4(f2_s + 16 * c);
+                            l[2 * c] = __fmul2_rn(l[2 * c], make_float2(f.x, f.y));
+                            l[2 * c + 1] = __fmul2_rn(l[2 * c + 1], make_float2(f.z, f.w));
+                        }
+                    }
                     if (later) {
                         if (ok && !wait_warp(pvdone + 8 * ((g - 1) & 1), (uint32_t)((g - 1) >> 1) & 1u)) ok = false;
                         tc_fence_after();
-                    }
-#pragma unroll
-                    for (int c = 0; c < CG; c += 4) {
-                        float t4[4], al[4];
-                        {
-                            const float4 v0 = lds4(mx_s + c * 4), v1 = lds4(mx_s + (CG + c) * 4);
-                            const float4 v2 = lds4(mx_s + (2 * CG + c) * 4), v3 = lds4(mx_s + (3 * CG + c) * 4);
-                            t4[0] = fmaxf(fmaxf(v0.x, v1.x), fmaxf(v2.x, v3.x));
-                            t4[1] = fmaxf(fmaxf(v0.y, v1.y), fmaxf(v2.y, v3.y));
-                            t4[2] = fmaxf(fmaxf(v0.z, v1.z), fmaxf(v2.z, v3.z));
-                            t4[3] = fmaxf(fmaxf(v0.w, v1.w), fmaxf(v2.w, v3.w));
-                        }
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            float &me = e & 1 ? m[(c + e) / 2].y : m[(c + e) / 2].x;
-                            const float nm = t4[e] + me > kBase + kOver ? kBase - t4[e] : me;
-                            al[e] = nm - me;   // log2 of old maximum over new
-                            me = nm;
-                        }
-                        if (later) {
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                al[e] = ex2(al[e]);
-                                float &le = e & 1 ? l[(c + e) / 2].y : l[(c + e) / 2].x;
-                                le *= al[e];
-                                if (gt == c + e) sts1(f2_s + (c + e) * 4, al[e] * rr);
-                            }
-                        }
-                    }
-                    if (later) {
-                        bar_sync(bar, 128);
                         if (ok && quarter * 32 < D) {
 #pragma unroll 1
                             for (int c = 0; c < 3 * CG; c += 4) {
@@ -968,10 +998,10 @@ __global__ void __launch_bounds__(Cfg8<D, RP>::THREADS, 1)
                                 const float4 f = lds4(f2_s + c % CG * 4);
                                 tc_ld4(at, o);
                                 tc_wait_ld();
-                                o[0] *= f.x;
-                                o[1] *= f.y;
-                                o[2] *= f.z;
-                                o[3] *= f.w;
+                                o[0] *= f.x * rr;
+                                o[1] *= f.y * rr;
+                                o[2] *= f.z * rr;
+                                o[3] *= f.w * rr;
                                 tc_st4(at, o);
                             }
                             tc_wait_st();
@@ -1062,42 +1092,9 @@ __global__ void __launch_bounds__(Cfg8<D, RP>::THREADS, 1)
                             misc[4 + grp] = last;
                         }
                         bar_sync(bar, 128);
-                        if (misc[4 + grp]) {
-                            __threadfence();
-                            constexpr int EPL = D / 32;
-                            for (int c = warp & 3; c < CG; c += 4) {   // a warp a column, lane = part, then lane = dims
-                                const int row = ldsi(rows + c * 4);
-                                if (row < 0) continue;
-                                float2 ml = make_float2(-INFINITY, 0.f);
-                                if (lane < done.parts) ml = __ldcg(a.part_ml + (size_t)(done.slot + lane) * RP + cb + c);
-                                const float mx = warp_max(ml.x);
-                                const float wt = lane < done.parts ? ex2(ml.x - mx) : 0.f;
-                                float ls = wt * ml.y;
-        #pragma unroll
-                                for (int o = 16; o; o >>= 1) ls += __shfl_xor_sync(~0u, ls, o);
-                                float acc[EPL] = {};
-                                const float *po = a.part_o + ((size_t)done.slot * RP + cb + c) * D + lane * EPL;
-        #pragma unroll 8
-                                for (int s = 0; s < done.parts; ++s) {
-                                    const float ws = __shfl_sync(~0u, wt, s);
-                                    float v[EPL];
-                                    if constexpr (EPL == 4) {
-                                        const float4 f = __ldcg((const float4 *)(po + (size_t)s * RP * D));
-                                        v[0] = f.x; v[1] = f.y; v[2] = f.z; v[3] = f.w;
-                                    } else {
-                                        const float2 f = __ldcg((const float2 *)(po + (size_t)s * RP * D));
-                                        v[0] = f.x; v[1] = f.y;
-                                    }
-        #pragma unroll
-                                    for (int e = 0; e < EPL; ++e) acc[e] = fmaf(ws, v[e], acc[e]);
-                                }
-                                const float inv = 1.f / ls;
-        #pragma unroll
-                                for (int e = 0; e < EPL; e += 2)
-                                    *(__nv_bfloat162 *)(ob + (size_t)row * D + lane * EPL + e) =
-                                        __floats2bfloat162_rn(acc[e] * inv, acc[e + 1] * inv);
-                            }
-                        }
+                        if (misc[4 + grp])
+                            join_parts<D, RP, CG>(a.part_ml + (size_t)done.slot * RP + cb, a.part_o + ((size_t)done.slot * RP + cb) * D,
+                                                  done.parts, rows, ob);
                     }
                     __syncwarp();
                     if (lane == 0) mbar_arrive(ifree + 8 * dr);
@@ -1113,11 +1110,7 @@ __global__ void __launch_bounds__(Cfg8<D, RP>::THREADS, 1)
             }
             reduce_scatter<CG>(v, lane);
             if (lane % (32 / CG) == 0) sts1(ls_s + (quarter * 64 + cb + lane / (32 / CG)) * 4, v[0]);
-            if (u.parts > 1) {
-#pragma unroll
-                for (int c = 0; c < CG; ++c)
-                    if (gt == c) done_m = -(c & 1 ? m[c / 2].y : m[c / 2].x);
-            }
+            if (gt < CG) done_m = -lds1(m_s + gt * 4);
             done_parts = u.parts;
             done_ref = ref;
         }
