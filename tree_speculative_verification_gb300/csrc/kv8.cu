@@ -56,9 +56,9 @@ __device__ __forceinline__ float max_nan(float a, float b) {
 
 // ---- norm, rotation, quantised append ---------------------------------------
 struct RowArgs {
-    const uint4 *q, *k, *v;              // node rows, *_stride 16-byte vectors apart
+    const void *q, *k, *v;               // node rows, *_stride values apart
     long long q_stride, k_stride, v_stride;
-    uint4 *q_out, *k_out;                // contiguous [B][n_max][H][d]; k_out without the cache
+    void *q_out, *k_out;                 // contiguous [B][n_max][H][d]; k_out without the cache
     int Hq, Hk, Hv;                      // heads handled here (0 leaves a projection out)
     const float *inv_freq, *q_weight, *k_weight;
     float eps;
@@ -74,25 +74,70 @@ struct RowArgs {
     int rows_per_cta;
 };
 
-constexpr int kRowThreads = 256;
+constexpr int kRowThreads = 128, kRowsAhead = 4;
+
+// Two values of a row as one 4-byte (bf16) or 8-byte (fp32) piece.
+template <typename T>
+struct Two;
+template <>
+struct Two<__nv_bfloat16> {
+    using U = uint32_t;
+    static __device__ __forceinline__ float2 get(U u) { return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u)); }
+    static __device__ __forceinline__ U put(float2 x) {
+        const __nv_bfloat162 p = __floats2bfloat162_rn(x.x, x.y);
+        return *reinterpret_cast<const U *>(&p);
+    }
+};
+template <>
+struct Two<float> {
+    using U = uint2;
+    static __device__ __forceinline__ float2 get(U u) { return make_float2(__uint_as_float(u.x), __uint_as_float(u.y)); }
+    static __device__ __forceinline__ U put(float2 x) { return make_uint2(__float_as_uint(x.x), __float_as_uint(x.y)); }
+};
+
+// Values t (as they lie: the lane's first piece, then its second) as H rotation pairs (x, y), two pairs a vector, and back.
+template <int H, bool INTER>
+__device__ __forceinline__ void pairs(const float2 (&t)[H], float2 (&x)[H / 2], float2 (&y)[H / 2]) {
+#pragma unroll
+    for (int e = 0; e < H / 2; ++e) {
+        x[e] = INTER ? make_float2(t[2 * e].x, t[2 * e + 1].x) : t[e];
+        y[e] = INTER ? make_float2(t[2 * e].y, t[2 * e + 1].y) : t[H / 2 + e];
+    }
+}
+template <int H, bool INTER>
+__device__ __forceinline__ void unpairs(const float2 (&x)[H / 2], const float2 (&y)[H / 2], float2 (&t)[H]) {
+#pragma unroll
+    for (int e = 0; e < H / 2; ++e) {
+        t[INTER ? 2 * e : e] = INTER ? make_float2(x[e].x, y[e].x) : x[e];
+        t[INTER ? 2 * e + 1 : H / 2 + e] = INTER ? make_float2(x[e].y, y[e].y) : y[e];
+    }
+}
 
 // One CTA per (node, group of its heads). A row (one head's d values) is held
-// by LPR = d / E lanes, E values of 16 bytes each, the same E positions of
-// every row a lane meets, so the angles' cosines and sines and the norm weights
-// stay in registers over the CTA's rows. The d / 2 angles are formed once per
-// CTA: position times frequency and its remainder by 2 pi in fp64 (four
-// operations an angle; an fp32 product at position 131072 is off by up to 4e-3),
-// then sincosf of the fp32 remainder. Sums over a row are shuffles among its
-// lanes. Memory bound: each element is read once and written once; kRowsAhead
-// rows per lane group are loaded before any of them is worked on.
-template <typename T, int D, bool APPEND>
+// by LPR lanes, E = d / LPR values each in two pieces of 8 bytes: the first
+// members of E / 2 rotation pairs and the second ones (interleaved pairs: 16
+// bytes in a row), so a rotation needs no other lane; a row's only shuffles
+// are those of its sum of squares (and, quantised, of its largest value). The
+// lane's cosines, sines and norm weights stay in registers over the CTA's rows.
+// The angles are formed once per CTA: position times frequency and its remainder
+// by 2 pi in fp64 (an fp32 product at position 131072 is off by up to 4e-3),
+// then sincosf of the fp32 remainder. Memory bound: each value is read once and
+// written once; kRowsAhead rows a lane group are in flight.
+template <typename T, int D, bool APPEND, bool INTER>
 __global__ void __launch_bounds__(kRowThreads) k_head_rows(RowArgs a) {
-    constexpr int E = Vec<T>::E, LPR = D / E, RPC = kRowThreads / LPR, AHEAD = 2;
+    constexpr int E = 16 / (int)sizeof(T), LPR = D / E, RPC = kRowThreads / LPR, RW = 32 / LPR, H = E / 2;
+    using U = typename Two<T>::U;
     __shared__ float2 cs_s[D / 2];
     __shared__ int bad_s;
     const int n_max = a.t.n_max, b = blockIdx.x / n_max, v = blockIdx.x - b * n_max;
     const int tid = threadIdx.x, sub = tid % LPR, slot = tid / LPR;
-    const int e0 = sub * E;
+    const int half = a.rot_dim >> 1;
+    // this lane's pairs p0 .. p0 + H - 1: pair p is (p, p + half), or behind the rotated part (unrotated) the
+    // same with that part's halves
+    const int p0 = sub * H;
+    const bool turned = p0 < half;
+    const int e0 = INTER ? 2 * p0 : turned ? p0 : p0 + half;
+    const int e1 = INTER ? e0 + H : turned ? p0 + half : p0 + D / 2;
     pdl_wait();
     pdl_trigger();
     const int n = a.t.n_nodes[b];
@@ -106,17 +151,19 @@ __global__ void __launch_bounds__(kRowThreads) k_head_rows(RowArgs a) {
     const int rows = a.Hq + a.Hk + a.Hv;
     const int r_begin = blockIdx.y * a.rows_per_cta, r_end = min(rows, r_begin + a.rows_per_cta);
     const size_t node = (size_t)b * n_max + v;
-    auto src = [&](int r) -> const uint4 * {
-        if (r < a.Hq) return a.q + node * a.q_stride + (size_t)r * LPR + sub;
-        r -= a.Hq;
-        if (r < a.Hk) return a.k + node * a.k_stride + (size_t)r * LPR + sub;
-        return a.v + node * a.v_stride + (size_t)(r - a.Hk) * LPR + sub;
+    const T *qb = (const T *)a.q + node * a.q_stride, *kb = (const T *)a.k + node * a.k_stride, *vb = (const T *)a.v + node * a.v_stride;
+    struct Raw {
+        uint2 lo, hi;
+    };
+    auto load = [&](int r) -> Raw {
+        const T *x = r < a.Hq ? qb + (size_t)r * D : r < a.Hq + a.Hk ? kb + (size_t)(r - a.Hq) * D : vb + (size_t)(r - a.Hq - a.Hk) * D;
+        return Raw{__ldcs(reinterpret_cast<const uint2 *>(x + e0)), __ldcs(reinterpret_cast<const uint2 *>(x + e1))};
     };
     // the first rows' loads are in flight while the angles are formed
-    uint4 u[AHEAD];
+    Raw u[kRowsAhead] = {};
 #pragma unroll
-    for (int i = 0; i < AHEAD; ++i)
-        if (r_begin + slot + i * RPC < r_end) u[i] = __ldcs(src(r_begin + slot + i * RPC));
+    for (int i = 0; i < kRowsAhead; ++i)
+        if (r_begin + slot + i * RPC < r_end) u[i] = load(r_begin + slot + i * RPC);
     if (APPEND) {
         if (tid == 0) bad_s = 0;
         __syncthreads();
@@ -126,7 +173,6 @@ __global__ void __launch_bounds__(kRowThreads) k_head_rows(RowArgs a) {
             if (page < 0 || page >= a.pg.num_pages) bad_s = 1;
         }
     }
-    const int half = a.rot_dim >> 1;
     if (tid < half) {
         constexpr double kTwoPi = 6.283185307179586476925;
         const double ang = (double)a.t.pos[(size_t)b * n_max + dfs] * (double)a.inv_freq[tid];
@@ -140,107 +186,131 @@ __global__ void __launch_bounds__(kRowThreads) k_head_rows(RowArgs a) {
         if (v == 0 && blockIdx.y == 0 && tid == 0) flag(a.status, TS_STATUS_INDEX);
         return;
     }
-    // y[e] = x[e] * ca[e] + partner * sa[e]; the partner of position p is p +- rot_dim/2
-    // (the same slot of another lane) or, interleaved, the pair's other value
-    float ca[E], sa[E];
-    const bool turned = e0 < a.rot_dim;
-    int partner = tid & 31;
-#pragma unroll
-    for (int e = 0; e < E; ++e) {
-        ca[e] = 1.f;
-        sa[e] = 0.f;
-        if (turned) {
-            const int p = e0 + e;
-            const bool low = a.interleaved ? !(p & 1) : p < half;
-            const float2 cs = cs_s[a.interleaved ? p >> 1 : (low ? p : p - half)];
-            ca[e] = cs.x;
-            sa[e] = low ? -cs.y : cs.y;
-        }
-    }
-    if (turned && !a.interleaved) partner += (e0 < half ? half : -half) / E;
-    const unsigned group = LPR == 32 ? 0xffffffffu : ((1u << LPR) - 1u) << ((tid & 31) / LPR * LPR);
-
     long long row0 = 0, hs = 0;
     if (APPEND) {   // cache row of head 0; head h is h * hs rows further
         row0 = cache_row(a.pg, b, 0, a.Hv, a.L_max, P + dfs);
         hs = a.pg.bt ? TS_PAGE_KEYS : a.L_max;
     }
-    for (int base = r_begin + slot; base < r_end; base += AHEAD * RPC) {
+    // weights and rotation of the lane's pairs (p, q), two pairs a vector:
+    // p -> inv * (p * pc - q * qs), q -> inv * (q * qc + p * ps)
+    float2 pc[H / 2], qs[H / 2], qc[H / 2], ps[H / 2];
+    int kind = -1;
+    // the rows of a warp's lane groups go together (none of them leaves early), so every shuffle is the whole warp's
+    for (int base = r_begin + slot, first = r_begin + slot / RW * RW; first < r_end; base += kRowsAhead * RPC, first += kRowsAhead * RPC) {
 #pragma unroll
-        for (int i = 0; i < AHEAD; ++i) {
-            const int r = base + i * RPC;
-            if (r >= r_end) break;
-            const bool is_q = r < a.Hq, is_v = r >= a.Hq + a.Hk;
-            float x[E];
-            Vec<T>::unpack(u[i], x);
-            if (!is_v) {
-                if (a.norm) {
-                    float ss = 0.f;
-#pragma unroll
-                    for (int e = 0; e < E; ++e) ss = fmaf(x[e], x[e], ss);
-#pragma unroll
-                    for (int o = LPR / 2; o; o >>= 1) ss += __shfl_xor_sync(group, ss, o);
-                    const float inv = rsqrtf(ss * (1.f / D) + a.eps);
-                    const float *w = is_q ? a.q_weight : a.k_weight;
-#pragma unroll
-                    for (int e = 0; e < E; ++e) x[e] = x[e] * inv * (w ? __ldg(w + e0 + e) : 1.f);
+        for (int i = 0; i < kRowsAhead; ++i) {
+            const int r = base + i * RPC, f = first + i * RPC;   // this group's row, the warp's first
+            if (f >= r_end) break;
+            const int is = r < a.Hq ? 0 : r < a.Hq + a.Hk ? 1 : 2;   // query, key, value
+            const int h = is == 0 ? r : is == 1 ? r - a.Hq : r - a.Hq - a.Hk;
+            float2 x[H / 2], y[H / 2];   // first and second members
+            {
+                float2 t[H];
+                if constexpr (sizeof(T) == 2) {
+                    t[0] = Two<T>::get(u[i].lo.x);
+                    t[1] = Two<T>::get(u[i].lo.y);
+                    t[2] = Two<T>::get(u[i].hi.x);
+                    t[3] = Two<T>::get(u[i].hi.y);
+                } else {
+                    t[0] = Two<T>::get(u[i].lo);
+                    t[1] = Two<T>::get(u[i].hi);
                 }
-                if (half) {
-                    float y[E];
-                    if (a.interleaved) {
+                pairs<H, INTER>(t, x, y);
+            }
+            const int nr = r + kRowsAhead * RPC;   // this group's next row
+            if (nr < r_end) u[i] = load(nr);
+            if (is != kind) {
+                kind = is;
+                const float *wp = is == 0 ? a.q_weight : is == 1 ? a.k_weight : nullptr;
+                float w[4][H];
 #pragma unroll
-                        for (int e = 0; e < E; ++e) y[e] = x[e ^ 1];
-                    } else {
+                for (int e = 0; e < H; ++e) {
+                    const float2 c = turned && is < 2 ? cs_s[p0 + e] : make_float2(1.f, 0.f);
+                    const float wx = wp ? __ldg(wp + (INTER ? e0 + 2 * e : e0 + e)) : 1.f;
+                    const float wy = wp ? __ldg(wp + (INTER ? e0 + 2 * e + 1 : e1 + e)) : 1.f;
+                    w[0][e] = wx * c.x;
+                    w[1][e] = -wy * c.y;
+                    w[2][e] = wy * c.x;
+                    w[3][e] = wx * c.y;
+                }
 #pragma unroll
-                        for (int e = 0; e < E; ++e) y[e] = __shfl_sync(group, x[e], partner);
-                    }
-                    if (turned) {
-#pragma unroll
-                        for (int e = 0; e < E; ++e) x[e] = x[e] * ca[e] + y[e] * sa[e];
-                    }
+                for (int e = 0; e < H / 2; ++e) {
+                    pc[e] = make_float2(w[0][2 * e], w[0][2 * e + 1]);
+                    qs[e] = make_float2(w[1][2 * e], w[1][2 * e + 1]);
+                    qc[e] = make_float2(w[2][2 * e], w[2][2 * e + 1]);
+                    ps[e] = make_float2(w[3][2 * e], w[3][2 * e + 1]);
                 }
             }
-            if (is_q || !APPEND) {
-                const int h = is_q ? r : r - a.Hq;
-                uint4 *o = is_q ? a.q_out + (node * a.Hq + h) * LPR : a.k_out + (node * a.Hk + h) * LPR;
-                o[sub] = Vec<T>::pack(x);
+            float inv = 1.f;
+            if (a.norm && f < a.Hq + a.Hk) {   // not for a warp of value rows
+                float2 s2 = make_float2(0.f, 0.f);
+#pragma unroll
+                for (int e = 0; e < H / 2; ++e) s2 = __ffma2_rn(y[e], y[e], __ffma2_rn(x[e], x[e], s2));
+                float ss = s2.x + s2.y;
+#pragma unroll
+                for (int o = LPR / 2; o; o >>= 1) ss += __shfl_xor_sync(~0u, ss, o);
+                if (is < 2) inv = rsqrtf(ss * (1.f / D) + a.eps);
+            }
+            if (is < 2) {
+                const float2 i2 = make_float2(inv, inv);
+#pragma unroll
+                for (int e = 0; e < H / 2; ++e) {
+                    const float2 p = __fmul2_rn(x[e], i2), q = __fmul2_rn(y[e], i2);
+                    x[e] = __ffma2_rn(q, qs[e], __fmul2_rn(p, pc[e]));
+                    y[e] = __ffma2_rn(p, ps[e], __fmul2_rn(q, qc[e]));
+                }
+            }
+            float2 t[H];
+            unpairs<H, INTER>(x, y, t);
+            float top = 0.f;
+            if (APPEND && f + RW > a.Hq) {   // some row of the warp is quantised
+#pragma unroll
+                for (int e = 0; e < H; ++e) top = max_nan(top, max_nan(fabsf(t[e].x), fabsf(t[e].y)));
+#pragma unroll
+                for (int o = LPR / 2; o; o >>= 1) top = max_nan(top, __shfl_xor_sync(~0u, top, o));
+            }
+            if (r >= r_end) continue;
+            if (is == 0 || !APPEND) {
+                T *o = is == 0 ? (T *)a.q_out + (node * a.Hq + h) * D : (T *)a.k_out + (node * a.Hk + h) * D;
+                uint2 lo, hi;
+                if constexpr (sizeof(T) == 2) {
+                    lo = make_uint2(Two<T>::put(t[0]), Two<T>::put(t[1]));
+                    hi = make_uint2(Two<T>::put(t[2]), Two<T>::put(t[3]));
+                } else {
+                    lo = Two<T>::put(t[0]);
+                    hi = Two<T>::put(t[1]);
+                }
+                *reinterpret_cast<uint2 *>(o + e0) = lo;
+                *reinterpret_cast<uint2 *>(o + e1) = hi;
             } else {
-                const int h = is_v ? r - a.Hq - a.Hk : r - a.Hq;
-                float top = 0.f;
-#pragma unroll
-                for (int e = 0; e < E; ++e) top = max_nan(top, fabsf(x[e]));
-#pragma unroll
-                for (int o = LPR / 2; o; o >>= 1) top = max_nan(top, __shfl_xor_sync(group, top, o));
                 const bool fine = top <= 3.402823466e38f;   // false for infinities and NaN
                 const float scale = fmaxf(__fdiv_rn(top, kFp8Max), kScaleMin);
-                const float inv = __fdiv_rn(1.f, scale);
-                uint32_t c[E / 4];
+                const float rs = __frcp_rn(scale);
+                uint32_t c[H];   // two codes each
 #pragma unroll
-                for (int e = 0; e < E; e += 4) {
-                    const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(__fmul_rn(x[e], inv), __fmul_rn(x[e + 1], inv)),
-                                                                 __NV_SATFINITE, __NV_E4M3);
-                    const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(__fmul_rn(x[e + 2], inv), __fmul_rn(x[e + 3], inv)),
-                                                                 __NV_SATFINITE, __NV_E4M3);
-                    c[e / 4] = fine ? lo | hi << 16 : 0u;
-                }
+                for (int e = 0; e < H; ++e)
+                    c[e] = fine ? __nv_cvt_float2_to_fp8x2(__fmul2_rn(t[e], make_float2(rs, rs)), __NV_SATFINITE, __NV_E4M3) : 0u;
                 const size_t row = (size_t)(row0 + h * hs);
-                uint8_t *dst = (is_v ? a.v8 : a.k8) + row * D + e0;
-                if constexpr (E == 8) *reinterpret_cast<uint2 *>(dst) = make_uint2(c[0], c[1]);
-                else *reinterpret_cast<uint32_t *>(dst) = c[0];
+                uint8_t *dst = (is == 2 ? a.v8 : a.k8) + row * D;
+                if constexpr (sizeof(T) == 2) {
+                    *reinterpret_cast<uint32_t *>(dst + e0) = c[0] | c[1] << 16;
+                    *reinterpret_cast<uint32_t *>(dst + e1) = c[2] | c[3] << 16;
+                } else {
+                    *reinterpret_cast<uint16_t *>(dst + e0) = (uint16_t)c[0];
+                    *reinterpret_cast<uint16_t *>(dst + e1) = (uint16_t)c[1];
+                }
                 if (sub == 0) {
-                    (is_v ? a.v_scale : a.k_scale)[row] = fine ? scale : __int_as_float(0x7fc00000);
+                    (is == 2 ? a.v_scale : a.k_scale)[row] = fine ? scale : __int_as_float(0x7fc00000);
                     if (!fine) flag(a.status, TS_STATUS_NONFINITE);
                 }
             }
-            const int nr = r + AHEAD * RPC;   // this slot's next row
-            if (nr < r_end) u[i] = __ldcs(src(nr));
         }
     }
 }
 
 template <typename T, int D, bool APPEND>
 cudaError_t rows_launch(RowArgs &a, cudaStream_t s) {
-    constexpr int RPC = kRowThreads / (D / Vec<T>::E);
+    constexpr int RPC = kRowThreads / (D * (int)sizeof(T) / 16);
     const int rows = a.Hq + a.Hk + a.Hv;
     const long long nodes = (long long)a.t.B * a.t.n_max;
     // heads of a node are split over CTAs only while that gives each SM more to do
@@ -250,7 +320,8 @@ cudaError_t rows_launch(RowArgs &a, cudaStream_t s) {
     if (groups < 1) groups = 1;
     a.rows_per_cta = ((rows + (int)groups - 1) / (int)groups + RPC - 1) / RPC * RPC;
     const dim3 grid((unsigned)nodes, (rows + a.rows_per_cta - 1) / a.rows_per_cta);
-    return launch(k_head_rows<T, D, APPEND>, grid, dim3(kRowThreads), 0, s, a);
+    if (a.interleaved) return launch(k_head_rows<T, D, APPEND, true>, grid, dim3(kRowThreads), 0, s, a);
+    return launch(k_head_rows<T, D, APPEND, false>, grid, dim3(kRowThreads), 0, s, a);
 }
 
 template <bool APPEND>
@@ -425,14 +496,13 @@ __global__ void __launch_bounds__(kCommit8Threads) k_kv8_commit(uint4 *k8, uint4
 cudaError_t launch_qk_norm_rope(void *q_out, void *k_out, const void *q, const void *k, int Hq, int Hk, int d,
                                 long long q_stride, long long k_stride, const ts_qk_rope &rope, const ts_tree &t,
                                 ts_dtype dt, cudaStream_t s) {
-    const int per = 16 / (dt == TS_BF16 ? 2 : 4);
     RowArgs a = {};
-    a.q = (const uint4 *)q;
-    a.k = (const uint4 *)k;
-    a.q_stride = q_stride / per;
-    a.k_stride = k_stride / per;
-    a.q_out = (uint4 *)q_out;
-    a.k_out = (uint4 *)k_out;
+    a.q = q;
+    a.k = k;
+    a.q_stride = q_stride;
+    a.k_stride = k_stride;
+    a.q_out = q_out;
+    a.k_out = k_out;
     a.Hq = Hq;
     a.Hk = Hk;
     set_rope(a, rope);
@@ -444,15 +514,14 @@ cudaError_t launch_kv8_append(const ts_kv8 &kv, const void *k_new, const void *v
                               long long v_stride, const ts_qk_rope *rope, void *q_out, const void *q, int Hq,
                               long long q_stride, const int32_t *prefix_len, const ts_tree &t, ts_dtype dt,
                               uint32_t *status, cudaStream_t s) {
-    const int per = 16 / (dt == TS_BF16 ? 2 : 4);
     RowArgs a = {};
-    a.q = (const uint4 *)q;
-    a.k = (const uint4 *)k_new;
-    a.v = (const uint4 *)v_new;
-    a.q_stride = q_stride / per;
-    a.k_stride = k_stride / per;
-    a.v_stride = v_stride / per;
-    a.q_out = (uint4 *)q_out;
+    a.q = q;
+    a.k = k_new;
+    a.v = v_new;
+    a.q_stride = q_stride;
+    a.k_stride = k_stride;
+    a.v_stride = v_stride;
+    a.q_out = q_out;
     a.Hq = Hq;
     a.Hk = kv.H;
     a.Hv = kv.H;
