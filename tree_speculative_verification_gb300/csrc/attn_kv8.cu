@@ -4,7 +4,7 @@
 // (SpecInfer, arXiv 2305.09781, Def. 4.1, Eq. 1-4; the mask of sec. 4.2), with
 // K and V held as e4m3 codes times one fp32 scale per (row, head), and G query
 // heads to a key/value head. The R = n * G query rows of a (request, key/value
-// head) share its keys; they are taken RP at a time (RP = 16, 32 or 48).
+// head) share its keys; they are taken RP at a time (RP = 16, 32, 48 or 64).
 //
 // The cache's codes go to the tensor cores as they are. Both products are
 // transposed, so that keys, then value dims, are the 128 rows of the MMA and a
@@ -207,12 +207,13 @@ struct Attn8Args {
 };
 
 constexpr int kTileKeys = 128;
-constexpr int kReqCache = 256;     // requests planned in shared memory
+constexpr int kReqCache = 192;     // requests planned in shared memory
 constexpr int kMaxCuts = 32;       // parts of one item (a lane each when they are joined)
 constexpr int kMinCut = 3;         // tiles of a part at least
-constexpr int kCutsPerSm = 2;      // units per SM that cutting aims at
+constexpr int kSlotsPerSm = 12;    // parts of cut items there is room for
+constexpr float kUnitCost = 5.f, kJoinCost = 2.f;   // of a unit beside its tiles, and of joining parts, in tiles
 constexpr int kRing = 4;           // published units
-constexpr int kClaimAhead = 6;     // tiles
+constexpr int kClaimAhead = 8;     // tiles
 
 template <int D_, int RP_>
 struct Cfg8 {
@@ -237,7 +238,7 @@ struct Cfg8 {
     static constexpr int FIX_ORDER = FIX_KEY + kReqCache * 4;  // by rank: request, first unit, first slot
     static constexpr int FIX_UNIT = FIX_ORDER + kReqCache * 4, FIX_SLOT = FIX_UNIT + kReqCache * 4;
     static constexpr int FIX_INFO = FIX_SLOT + kReqCache * 4;  // units [kRing][12]
-    static constexpr int FIX_MISC = FIX_INFO + kRing * 12 * 4; // 0 TMEM base, 1 timeout, 2 units, 3 tiles a part, 4-7 last
+    static constexpr int FIX_MISC = FIX_INFO + kRing * 12 * 4; // 0 TMEM base, 1 timeout, 2 units, 4-7 last
     static constexpr int FIX_BAR = FIX_MISC + 64;
     static constexpr int FIX_END = FIX_BAR + 64 * 8;
     static constexpr int off_fix(int stages) { return (stages * (STAGE_BYTES + SIDE) + 1023) / 1024 * 1024; }
@@ -383,68 +384,88 @@ __global__ void __launch_bounds__(Cfg8<D, RP>::THREADS, 1)
         if (planned) req_s[b] = make_int4(n, P, tl, 1);
         if (blockIdx.x == 0 && n > 0 && !tl) flag(a.status, TS_STATUS_INDEX);
     }
+    int ticket = 0;   // the CTA's first place in the queue
+    if (warp == 0 && lane == 0) ticket = (int)atomicAdd(a.queue, 1u);
     __syncthreads();
     if (planned && warp == 0) {
-        long long work = 0;   // tiles over all items
+        // How far to cut: lane i tries parts of at most 1 / (i + 1) of the longest item. A launch takes as many
+        // rounds over the SMs as it has units, each of a unit's average tiles and cost, and at least its longest
+        // unit. Cut items have to fit the slots.
+        int longest = 0;
 #pragma unroll 1
-        for (int b = lane; b < B; b += 32) work += (long long)req_s[b].z * blocks_of(req_s[b].x);
-#pragma unroll
-        for (int o = 16; o; o >>= 1) work += __shfl_xor_sync(~0u, work, o);
-        // rounded up, so that the parts of cut items, fewer than 2 * work / per, fit the slots
-        const float each = __fdiv_ru(__fmul_ru(__ll2float_ru(work), (float)a.H), (float)((int)gridDim.x * kCutsPerSm));
-        const int per = max(kMinCut, (int)ceilf(fminf(each, 16777216.f)));
+        for (int b = lane; b < B; b += 32) longest = max(longest, req_s[b].z);
+        longest = __reduce_max_sync(~0u, longest);
+        const float per = fmaxf((float)kMinCut, ceilf((float)longest / (lane + 1))), rate = __frcp_rn(per);
+        float work = 0.f, units = 0.f, cut = 0.f;
+#pragma unroll 2
+        for (int b = 0; b < B; ++b) {
+            const int4 rq = req_s[b];
+            const float items = (float)(a.H * blocks_of(rq.x)), parts = fminf(ceilf(rq.z * rate), (float)kMaxCuts);
+            work += items * rq.z;
+            units += items * parts;
+            cut += parts > 1.f ? items * parts : 0.f;
+        }
+        const float each = work / fmaxf(units, 1.f) + kUnitCost, sms = (float)gridDim.x;
+        float cost = fmaxf(per + kUnitCost, ceilf(units / sms) * each) + (cut > 0.f ? kJoinCost : 0.f);
+        if (lane > 0 && cut > (float)a.slots) cost = 3e38f;
+        // the lane of the least cost (they are positive: their bits order as they do), the least cutting of equal ones
+        const uint32_t least = __reduce_min_sync(~0u, __float_as_uint(cost));
+        const int pick = __ffs(__ballot_sync(~0u, __float_as_uint(cost) == least)) - 1;
+        const float pick_rate = __shfl_sync(~0u, rate, pick);
+        int same = 1;   // whether every part is as long as any other
 #pragma unroll 1
         for (int b = lane; b < B; b += 32) {
-            const int tl = req_s[b].z;
-            if (tl > per) {
-                const int parts = min((tl + per - 1) / per, kMaxCuts);
-                req_s[b].w = parts;
-                key_s[b] = (tl + parts - 1) / parts;
-            } else {
-                key_s[b] = tl;
-            }
+            const int tl = req_s[b].z, parts = max(1, (int)fminf(ceilf(tl * pick_rate), (float)kMaxCuts));
+            req_s[b].w = parts;
+            key_s[b] = parts > 1 ? (tl + parts - 1) / parts : tl;
+            same &= tl == longest;
         }
-    }
-    __syncthreads();
+        same = __all_sync(~0u, same);
+        __syncwarp();
+        // requests by the length of their parts, longest first
 #pragma unroll 1
-    for (int b = tid; planned && b < B; b += C::THREADS) {   // rank by the length of the request's parts
-        const int mine = key_s[b];
-        int rank = 0;
+        for (int b = lane; b < B; b += 32) {
+            int rank = 0;
+            if (same) {
+                rank = b;
+            } else {
+                const int mine = key_s[b];
 #pragma unroll 4
-        for (int o = 0; o < B; ++o) {
-            const int ko = key_s[o];
-            rank += ko > mine || (ko == mine && o < b);
+                for (int o = 0; o < B; ++o) {
+                    const int ko = key_s[o];
+                    rank += ko > mine || (ko == mine && o < b);
+                }
+            }
+            order_s[rank] = b;
         }
-        order_s[rank] = b;
-    }
-    __syncthreads();
-    if (planned && warp == 0) {   // exclusive sums of units and of slots, in that order
-        int units = 0, slots = 0;
+        __syncwarp();
+        // exclusive sums of units and of slots, in that order
+        int nu = 0, ns = 0;
 #pragma unroll 1
         for (int r0 = 0; r0 < B; r0 += 32) {
-            int u = 0, s = 0;
+            int u = 0, c = 0;
             if (r0 + lane < B) {
                 const int4 rq = req_s[order_s[r0 + lane]];
                 if (rq.z) u = a.H * blocks_of(rq.x) * rq.w;
-                if (rq.w > 1) s = u;
+                if (rq.w > 1) c = u;
             }
-            int cu = u, cs = s;
+            int cu = u, cc = c;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
-                const int tu = __shfl_up_sync(~0u, cu, o), ts_ = __shfl_up_sync(~0u, cs, o);
+                const int tu = __shfl_up_sync(~0u, cu, o), tc = __shfl_up_sync(~0u, cc, o);
                 if (lane >= o) {
                     cu += tu;
-                    cs += ts_;
+                    cc += tc;
                 }
             }
             if (r0 + lane < B) {
-                unit_s[r0 + lane] = units + cu - u;
-                slot_s[r0 + lane] = slots + cs - s;
+                unit_s[r0 + lane] = nu + cu - u;
+                slot_s[r0 + lane] = ns + cc - c;
             }
-            units += __shfl_sync(~0u, cu, 31);
-            slots += __shfl_sync(~0u, cs, 31);
+            nu += __shfl_sync(~0u, cu, 31);
+            ns += __shfl_sync(~0u, cc, 31);
         }
-        if (lane == 0) misc[2] = units;
+        if (lane == 0) misc[2] = nu;
     }
     tc_fence_before();
     __syncthreads();
@@ -534,7 +555,10 @@ __global__ void __launch_bounds__(Cfg8<D, RP>::THREADS, 1)
             const int strip = (u.b * a.H + u.h) * a.rows;   // dense: the cache row of key 0
 #pragma unroll 1
             for (int j = u.j0;; ++j, ++g) {
-                if (j == claim) qn = next();
+                if (j == claim) {
+                    qn = ticket >= 0 ? ticket : next();
+                    ticket = -1;
+                }
                 if (j == min(claim + 1, u.j1)) {
                     more = publish(__shfl_sync(~0u, qn, 0), un);
                     if (!ok) break;
@@ -733,31 +757,26 @@ __global__ void __launch_bounds__(Cfg8<D, RP>::THREADS, 1)
         const uint32_t f2_s = fix_base + C::FIX_F2 + cb * 4, m_s = fix_base + C::FIX_M + cb * 4;
         bool ok = true;
         int g = 0;
-        // this warp's share of a unit's query rows, half a warp a row, once the raw rows are there
+        // this warp's share of a unit's query rows, all of them at once, once the raw rows are there
         auto convert = [&](int unit) {
             const uint32_t qd = fix_base + C::FIX_Q + (unit & 1) * C::Q_BYTES;
-            constexpr int EPL = D / 16, ROWS = RP / C::SM_WARPS;   // values a lane holds of a row; rows of a warp
-            const int sub = lane & 15, odd = lane >> 4;
-#pragma unroll 1
-            for (int c0 = (warp - 4) * ROWS; c0 < (warp - 3) * ROWS; c0 += 2) {
-            const int c = c0 + odd;
-            uint32_t w[4] = {0u, 0u, 0u, 0u};
-            const uint32_t src = qd + ((sub >= 8 ? RP : 0) + c) * D + (sub & 7) * (2 * EPL);
-            if constexpr (EPL == 8)
-                asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(src) : "memory");
-            else
-                asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(src) : "memory");
+            constexpr int ROWS = RP / C::SM_WARPS, LPR = 32 / ROWS, EPL = D / LPR;   // of a warp; lanes of a row; values of a lane
+            const int sub = lane % LPR, c = (warp - 4) * ROWS + lane / LPR;
+            uint32_t w[EPL / 2];   // two values each
+            const uint32_t src = qd + ((sub >= LPR / 2 ? RP : 0) + c) * D + sub % (LPR / 2) * (2 * EPL);
+#pragma unroll
+            for (int e = 0; e < EPL / 2; e += 2)
+                asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];" : "=r"(w[e]), "=r"(w[e + 1]) : "r"(src + 4 * e) : "memory");
             uint32_t top = 0;   // two |values| at a time, which order as their bits do, infinities and NaN on top
 #pragma unroll
             for (int e = 0; e < EPL / 2; ++e) top = __vmaxu2(top, w[e] & 0x7fff7fffu);
 #pragma unroll
-            for (int o = 8; o; o >>= 1) top = __vmaxu2(top, __shfl_xor_sync(~0u, top, o));
+            for (int o = LPR / 2; o; o >>= 1) top = __vmaxu2(top, __shfl_xor_sync(~0u, top, o));
             top = max(top >> 16, top & 0xffffu);
             // 2^(exponent - 7), within the normal numbers whose reciprocal is one too
             int ex = (int)(top >> 7) - 7;
             ex = ex < 4 ? 4 : ex;
             const float inv = __uint_as_float((uint32_t)(254 - ex) << 23);
-            uint32_t hi[EPL / 4], lo[EPL / 4];
 #pragma unroll
             for (int e = 0; e < EPL / 4; ++e) {
                 uint32_t h2[2], l2[2];
@@ -770,24 +789,17 @@ __global__ void __launch_bounds__(Cfg8<D, RP>::THREADS, 1)
                     h2[f] = half2_to_fp8x2(y16);
                     l2[f] = half2_to_fp8x2(hsub2(y16, fp8x2_to_half2(h2[f])));
                 }
-                hi[e] = h2[0] | h2[1] << 16;
-                lo[e] = l2[0] | l2[1] << 16;
-            }
-            // 16-byte chunks of a row are permuted as the MMA's descriptor says
-            auto at = [&](int row) {
-                return D == 128 ? row * 128 + (((sub >> 1) ^ (row & 7)) << 4) + (sub & 1) * 8
-                                : row * 64 + (((sub >> 2) ^ ((row >> 1) & 3)) << 4) + (sub & 3) * 4;
-            };
-            if constexpr (EPL == 8) {
-                sts2u(qd + at(c), hi[0], hi[1]);
-                sts2u(qd + at(RP + c), lo[0], lo[1]);
-            } else {
-                stsi(qd + at(c), (int)hi[0]);
-                stsi(qd + at(RP + c), (int)lo[0]);
+                // 16-byte chunks of a row are permuted as the MMA's descriptor says
+                const int at = sub * EPL + 4 * e;
+                auto place = [&](int row) {
+                    const int flip = D == 128 ? row & 7 : (row >> 1) & 3;
+                    return qd + row * D + (((at >> 4) ^ flip) << 4) + (at & 15);
+                };
+                stsi(place(c), (int)(h2[0] | h2[1] << 16));
+                stsi(place(RP + c), (int)(l2[0] | l2[1] << 16));
             }
             if (sub == 0)
                 stsi(fix_base + C::FIX_QS + (unit % kRing * 64 + c) * 4, top >= 0x7f80u ? 0x7fc00000 : (int)((uint32_t)ex << 23));
-            }
             fence_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(qready + 8 * (unit & 1));
@@ -1138,17 +1150,16 @@ struct Plan8 {
     size_t ml, o, bytes;   // offsets of the parts, all bytes
 };
 
-// RP: the rows there can be, cut into equal blocks of at most 48, rounded up
-// to 16. Slots: an item with T tiles is cut into ceil(T / per) parts, and
-// per >= all tiles / (kCutsPerSm * SMs), so the parts of the cut items (each
-// longer than per) number less than 2 * kCutsPerSm * SMs.
+// RP: the rows there can be, cut into equal blocks of at most 64, rounded up to
+// 16. Slots: no more than there can be parts.
 Plan8 plan8(int B, int Hkv, int G, int n_max, int d) {
     Plan8 p;
     const long long rows = (long long)n_max * G;
-    p.blocks = (int)((rows + 47) / 48);
+    p.blocks = (int)((rows + 63) / 64);
     p.rp = (int)(((rows + p.blocks - 1) / p.blocks + 15) / 16 * 16);
     p.blocks = (int)((rows + p.rp - 1) / p.rp);
-    p.slots = B <= kReqCache ? 2 * kCutsPerSm * num_sms() : 0;
+    const long long most = (long long)B * Hkv * p.blocks * kMaxCuts;
+    p.slots = B > kReqCache ? 0 : (int)(most < kSlotsPerSm * num_sms() ? most : kSlotsPerSm * num_sms());
     size_t at = 256 + ((size_t)p.slots * 4 * sizeof(unsigned) + 255) / 256 * 256;
     p.ml = at;
     at += (size_t)p.slots * p.rp * sizeof(float2);
@@ -1206,12 +1217,14 @@ cudaError_t launch_attn_kv8(void *out, const void *q, const ts_kv8 &kv, int Hq, 
     if (kv.d == 128) switch (p.rp) {
         case 16: return launch8<128, 16>(mk, mv, a, grid, s);
         case 32: return launch8<128, 32>(mk, mv, a, grid, s);
-        default: return launch8<128, 48>(mk, mv, a, grid, s);
+        case 48: return launch8<128, 48>(mk, mv, a, grid, s);
+        default: return launch8<128, 64>(mk, mv, a, grid, s);
     }
     switch (p.rp) {
         case 16: return launch8<64, 16>(mk, mv, a, grid, s);
         case 32: return launch8<64, 32>(mk, mv, a, grid, s);
-        default: return launch8<64, 48>(mk, mv, a, grid, s);
+        case 48: return launch8<64, 48>(mk, mv, a, grid, s);
+        default: return launch8<64, 64>(mk, mv, a, grid, s);
     }
 }
 
