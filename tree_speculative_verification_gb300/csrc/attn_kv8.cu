@@ -211,7 +211,7 @@ constexpr int kReqCache = 192;     // requests planned in shared memory
 constexpr int kMaxCuts = 32;       // parts of one item (a lane each when they are joined)
 constexpr int kMinCut = 3;         // tiles of a part at least
 constexpr int kSlotsPerSm = 12;    // parts of cut items there is room for
-constexpr float kUnitCost = 5.f, kJoinCost = 2.f;   // of a unit beside its tiles, and of joining parts, in tiles
+constexpr float kUnitCost = 5.f, kJoinCost = 6.f;   // of a unit beside its tiles, and of joining parts, in tiles
 constexpr int kRing = 4;           // published units
 constexpr int kClaimAhead = 8;     // tiles
 
@@ -332,8 +332,6 @@ __global__ void __launch_bounds__(Cfg8<D, RP>::THREADS, 1)
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int B = a.t.B, n_max = a.t.n_max;
-    pdl_wait();
-    pdl_trigger();
 
     const uint32_t full = fix_base + C::FIX_BAR, empty = full + 8 * C::STAGES, sfull = empty + 8 * C::STAGES;
     const uint32_t pvdone = sfull + 16, pfull = pvdone + 16, qraw = pfull + 16, qready = qraw + 16, qfree = qready + 16;
@@ -370,6 +368,9 @@ __global__ void __launch_bounds__(Cfg8<D, RP>::THREADS, 1)
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
 
+    pdl_wait();   // nothing above touches global memory
+    pdl_trigger();
+
     // ---- the plan, the same in every CTA: how many tiles a part has, and each
     // request's first unit and first slot of the workspace
     const bool planned = B <= kReqCache;
@@ -388,13 +389,17 @@ __global__ void __launch_bounds__(Cfg8<D, RP>::THREADS, 1)
     if (warp == 0 && lane == 0) ticket = (int)atomicAdd(a.queue, 1u);
     __syncthreads();
     if (planned && warp == 0) {
-        // How far to cut: lane i tries parts of at most 1 / (i + 1) of the longest item. A launch takes as many
-        // rounds over the SMs as it has units, each of a unit's average tiles and cost, and at least its longest
-        // unit. Cut items have to fit the slots.
-        int longest = 0;
+        // How far to cut: lane i tries parts of at most 1 / (i + 1) of the longest item. Items of one length take
+        // as many rounds over the SMs as they have units; others, handed out longest first, about their sum over
+        // the SMs and half a longest unit. Cut items have to fit the slots.
+        int longest = 0, same = 1;
 #pragma unroll 1
-        for (int b = lane; b < B; b += 32) longest = max(longest, req_s[b].z);
+        for (int b = lane; b < B; b += 32) {
+            longest = max(longest, req_s[b].z);
+            same &= req_s[b].z == req_s[0].z;
+        }
         longest = __reduce_max_sync(~0u, longest);
+        same = __all_sync(~0u, same);
         const float per = fmaxf((float)kMinCut, ceilf((float)longest / (lane + 1))), rate = __frcp_rn(per);
         float work = 0.f, units = 0.f, cut = 0.f;
 #pragma unroll 2
@@ -405,22 +410,20 @@ __global__ void __launch_bounds__(Cfg8<D, RP>::THREADS, 1)
             units += items * parts;
             cut += parts > 1.f ? items * parts : 0.f;
         }
-        const float each = work / fmaxf(units, 1.f) + kUnitCost, sms = (float)gridDim.x;
-        float cost = fmaxf(per + kUnitCost, ceilf(units / sms) * each) + (cut > 0.f ? kJoinCost : 0.f);
+        const float all = work + units * kUnitCost, sms = (float)gridDim.x;
+        float cost = fmaxf(per + kUnitCost, same ? ceilf(units / sms) * all / fmaxf(units, 1.f) : all / sms + 0.5f * per) +
+                     (cut > 0.f ? kJoinCost : 0.f);
         if (lane > 0 && cut > (float)a.slots) cost = 3e38f;
         // the lane of the least cost (they are positive: their bits order as they do), the least cutting of equal ones
         const uint32_t least = __reduce_min_sync(~0u, __float_as_uint(cost));
         const int pick = __ffs(__ballot_sync(~0u, __float_as_uint(cost) == least)) - 1;
         const float pick_rate = __shfl_sync(~0u, rate, pick);
-        int same = 1;   // whether every part is as long as any other
 #pragma unroll 1
         for (int b = lane; b < B; b += 32) {
             const int tl = req_s[b].z, parts = max(1, (int)fminf(ceilf(tl * pick_rate), (float)kMaxCuts));
             req_s[b].w = parts;
             key_s[b] = parts > 1 ? (tl + parts - 1) / parts : tl;
-            same &= tl == longest;
         }
-        same = __all_sync(~0u, same);
         __syncwarp();
         // requests by the length of their parts, longest first
 #pragma unroll 1
@@ -804,6 +807,7 @@ __global__ void __launch_bounds__(Cfg8<D, RP>::THREADS, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive(qready + 8 * (unit & 1));
         };
+        bool converted = false;   // this unit's rows, during the unit before
         int done_parts = 1;       // of the unit before
         float done_ref = 0.f, done_m = 0.f;   // done_m: of column gt
         for (int k = 0;; ++k) {
@@ -815,13 +819,14 @@ __global__ void __launch_bounds__(Cfg8<D, RP>::THREADS, 1)
             }
             const Unit8 u = read_unit(r);
             const bool more = u.b >= 0;
-            if (more) {
+            if (more && !converted) {
                 if (!wait_warp(qraw + 8 * (k & 1), (uint32_t)(k >> 1) & 1u)) ok = false;
                 convert(k);
             }
             // the unit before is written out after this one's first tile (or at the end): its last product and this
             // unit's first do not wait for that
             bool pending = k > 0;
+            converted = false;
             const int dr = (k - 1) % kRing;
             if (pending && gt < CG) {   // the sums are all there since the barrier
                 const uint32_t c = ls_s + (cb + gt) * 4;
@@ -1044,6 +1049,16 @@ __global__ void __launch_bounds__(Cfg8<D, RP>::THREADS, 1)
                             ++g;
                         }
                         raise = j < plain_end;
+                        // the next unit's query rows before the last tile, if they are there by then (the registers of
+                        // 64-row blocks have no room for it here)
+                        const int nr = (k + 1) % kRing;
+                        if (RP < 64 && !converted && !raise &&
+                            __all_sync(~0u, mbar_test(iready + 8 * nr, (uint32_t)((k + 1) / kRing) & 1u)) &&
+                            ldsi(fix_base + C::FIX_INFO + nr * 48) >= 0 &&
+                            __all_sync(~0u, mbar_test(qraw + 8 * ((k + 1) & 1), (uint32_t)((k + 1) >> 1) & 1u))) {
+                            convert(k + 1);
+                            converted = true;
+                        }
                         if (j == u.j1) break;
                     }
                     if (!any_tile(raise)) {
