@@ -200,14 +200,14 @@ struct Attn8Args {
     PagedArgs pg;
     uint32_t *status;
     unsigned *queue;      // [0] next unit, [1] CTAs finished
-    unsigned *joins;      // [slots][4] parts done, by the item's first slot and column group
+    unsigned *joins;      // [slots] parts done, by the item's first slot
     float2 *part_ml;      // [slots][RP] (maximum, sum)
     float *part_o;        // [slots][RP][D]
     int slots;
 };
 
 constexpr int kTileKeys = 128;
-constexpr int kReqCache = 192;     // requests planned in shared memory
+constexpr int kReqCache = 128;     // requests planned in shared memory
 constexpr int kMaxCuts = 32;       // parts of one item (a lane each when they are joined)
 constexpr int kMinCut = 3;         // tiles of a part at least
 constexpr int kSlotsPerSm = 12;    // parts of cut items there is room for
@@ -218,7 +218,13 @@ constexpr int kClaimAhead = 8;     // tiles
 template <int D_, int RP_>
 struct Cfg8 {
     static constexpr int D = D_, RP = RP_, CG = RP == 16 ? 8 : 16, GROUPS = RP / CG;   // columns of a softmax group
-    static constexpr int SM_WARPS = 4 * GROUPS, THREADS = 32 * (4 + SM_WARPS);
+    static constexpr int SM_WARPS = 4 * GROUPS, THREADS = 32 * (4 + SM_WARPS + 4);
+    // Registers a thread: LAUNCH x THREADS at launch, handed from the eight other warps to the softmax's where they
+    // need more. The sums: 48: 640 x 96 = 61440 >= 256 x 56 + 384 x 120 = 60416; 64: 768 x 80 = 61440 = 256 x 48 + 512 x 96.
+    static constexpr int LAUNCH_REGS = RP == 64 ? 80 : RP == 48 ? 96 : 128;
+    static constexpr int SM_REGS = RP == 64 ? 96 : RP == 48 ? 120 : 128;
+    static constexpr int OTHER_REGS = RP == 64 ? 48 : RP == 48 ? 56 : 128;
+    static_assert(32 * SM_WARPS * SM_REGS + 256 * OTHER_REGS <= THREADS * LAUNCH_REGS, "a split of the launch's registers");
     static constexpr int OP_BYTES = kTileKeys * D;             // codes of one operand tile
     static constexpr int STAGE_BYTES = 2 * OP_BYTES;
     static constexpr int P_ATOMS = (3 * RP + 63) / 64, P_ATOM = kTileKeys * 64, P_BYTES = P_ATOMS * P_ATOM;
@@ -226,19 +232,19 @@ struct Cfg8 {
     static constexpr int SIDE = 3 * kTileKeys * 4;             // a stage's key scales, value scales, subtree ends
     // fixed part, behind the stages
     static constexpr int FIX_P = 0, FIX_Q = FIX_P + 2 * P_BYTES, FIX_MX = FIX_Q + 2 * Q_BYTES;
-    static constexpr int FIX_LS = FIX_MX + 4 * RP * 4;         // column maxima [groups][4 warps][CG]
-    static constexpr int FIX_F = FIX_LS + 4 * 64 * 4;          // column sums [4 warps][64], then factors [64]
-    static constexpr int FIX_F2 = FIX_F + 64 * 4;              // factors of O where a maximum is raised [64]
+    static constexpr int FIX_F2 = FIX_MX + 4 * RP * 4;         // column maxima [groups][4 warps][CG]; factors of O [64]
     static constexpr int FIX_M = FIX_F2 + 64 * 4;              // kBase - maximum [64]
     static constexpr int FIX_V = FIX_M + 64 * 4;               // largest value scales [groups][4 warps]
-    static constexpr int FIX_QS = FIX_V + 64;                  // query scales [kRing][64], output rows [kRing][64]
+    // by unit parity: column sums [4 warps][64], maxima [64], value references [64] (a group's in its first column)
+    static constexpr int FIX_SUM = FIX_V + 64, SUM_BYTES = 6 * 64 * 4;
+    static constexpr int FIX_QS = FIX_SUM + 2 * SUM_BYTES;     // query scales [kRing][64], output rows [kRing][64]
     static constexpr int FIX_QROW = FIX_QS + kRing * 64 * 4;
     static constexpr int FIX_REQ = FIX_QROW + kRing * 64 * 4;  // requests: n, P, tiles, parts
     static constexpr int FIX_KEY = FIX_REQ + kReqCache * 16;   // tiles of a part
     static constexpr int FIX_ORDER = FIX_KEY + kReqCache * 4;  // by rank: request, first unit, first slot
     static constexpr int FIX_UNIT = FIX_ORDER + kReqCache * 4, FIX_SLOT = FIX_UNIT + kReqCache * 4;
     static constexpr int FIX_INFO = FIX_SLOT + kReqCache * 4;  // units [kRing][12]
-    static constexpr int FIX_MISC = FIX_INFO + kRing * 12 * 4; // 0 TMEM base, 1 timeout, 2 units, 4-7 last
+    static constexpr int FIX_MISC = FIX_INFO + kRing * 12 * 4; // 0 TMEM base, 1 timeout, 2 units, 3 last
     static constexpr int FIX_BAR = FIX_MISC + 64;
     static constexpr int FIX_END = FIX_BAR + 64 * 8;
     static constexpr int off_fix(int stages) { return (stages * (STAGE_BYTES + SIDE) + 1023) / 1024 * 1024; }
@@ -276,15 +282,16 @@ __device__ __forceinline__ void reduce_scatter(float *v, int lane) {
     if constexpr (W > 1) reduce_scatter<(N > 1 ? N / 2 : 1), MAX, W / 2>(v, lane);
 }
 
-// The parts of a cut item into its output rows, one group's columns: a warp a column, lane = part for the weights, then
-// lane = dims. Out of line: it runs once an item, and the loops around its call are better short.
-template <int D, int RP, int CG>
-__device__ __noinline__ void join_parts(const float2 *part_ml, const float *part_o, int parts, uint32_t rows,
+// The parts of a cut item into its output rows: a warp a column, lane = part for the weights, then
+// lane = dims.
+template <int D, int RP>
+__device__ __forceinline__ void join_parts(const float2 *part_ml, const float *part_o, int parts, uint32_t rows,
                                         __nv_bfloat16 *out) {
     constexpr int EPL = D / 32;
     const int lane = threadIdx.x & 31;
     __threadfence();
-    for (int c = (threadIdx.x >> 5) & 3; c < CG; c += 4) {
+#pragma unroll 1
+    for (int c = (threadIdx.x >> 5) & 3; c < RP; c += 4) {
         const int row = ldsi(rows + c * 4);
         if (row < 0) continue;
         float2 ml = make_float2(-INFINITY, 0.f);
@@ -296,7 +303,7 @@ __device__ __noinline__ void join_parts(const float2 *part_ml, const float *part
         for (int o = 16; o; o >>= 1) ls += __shfl_xor_sync(~0u, ls, o);
         float acc[EPL] = {};
         const float *po = part_o + (size_t)c * D + lane * EPL;
-#pragma unroll 8
+#pragma unroll 4
         for (int s = 0; s < parts; ++s) {
             const float ws = __shfl_sync(~0u, wt, s);
             float v[EPL];
@@ -317,6 +324,12 @@ __device__ __noinline__ void join_parts(const float2 *part_ml, const float *part
     }
 }
 
+template <bool MORE, int N>
+__device__ __forceinline__ void take_registers() {
+    if constexpr (MORE) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+    else asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
 template <int D, int RP>
 __global__ void __launch_bounds__(Cfg8<D, RP>::THREADS, 1)
     k_attn_kv8(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v, Attn8Args a) {
@@ -335,7 +348,7 @@ __global__ void __launch_bounds__(Cfg8<D, RP>::THREADS, 1)
 
     const uint32_t full = fix_base + C::FIX_BAR, empty = full + 8 * C::STAGES, sfull = empty + 8 * C::STAGES;
     const uint32_t pvdone = sfull + 16, pfull = pvdone + 16, qraw = pfull + 16, qready = qraw + 16, qfree = qready + 16;
-    const uint32_t fin = qfree + 16, iready = fin + 16, ifree = iready + 8 * kRing;
+    const uint32_t fin = qfree + 16, sumfull = fin + 16, odone = sumfull + 16, ofree = odone + 16, iready = ofree + 16, ifree = iready + 8 * kRing;
 
     if (warp == 2) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32((void *)misc)),
@@ -355,14 +368,17 @@ __global__ void __launch_bounds__(Cfg8<D, RP>::THREADS, 1)
             mbar_init(pvdone + 8 * x, 1);
             mbar_init(pfull + 8 * x, C::SM_WARPS);
             mbar_init(qraw + 8 * x, 1 + 32);
-            mbar_init(qready + 8 * x, C::SM_WARPS);
+            mbar_init(qready + 8 * x, 4);
+            mbar_init(sumfull + 8 * x, C::SM_WARPS);
+            mbar_init(odone + 8 * x, 1);
+            mbar_init(ofree + 8 * x, 4);
             mbar_init(qfree + 8 * x, 1);
             mbar_init(fin + 8 * x, 1);
         }
 #pragma unroll 1
         for (int r = 0; r < kRing; ++r) {
             mbar_init(iready + 8 * r, 1);
-            mbar_init(ifree + 8 * r, 3 + C::SM_WARPS);
+            mbar_init(ifree + 8 * r, 3 + C::SM_WARPS + 4);
         }
         misc[1] = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -524,6 +540,8 @@ __global__ void __launch_bounds__(Cfg8<D, RP>::THREADS, 1)
     };
 
     constexpr uint64_t swz = D == 128 ? kSwz128 : kSwz64;
+    if (warp < 4) {
+        if constexpr (C::SM_REGS > C::LAUNCH_REGS) take_registers<false, C::OTHER_REGS>();
     if (warp == 0) {   // ------------------------------------------------ producer and queue
         int g = 0, k = 0;
         bool ok = true;
@@ -676,6 +694,7 @@ __global__ void __launch_bounds__(Cfg8<D, RP>::THREADS, 1)
                 const Unit8 u = read_unit(r);
                 mbar_arrive(ifree + 8 * r);
                 if (u.b < 0) break;
+                if (k >= 2 && !wait1(ofree + 8 * (k & 1), (uint32_t)(k / 2 - 1) & 1u)) { ok = false; break; }
 #pragma unroll 1
                 for (int j = u.j0; j < u.j1; ++j, ++g) {
                     const int st = g % C::STAGES, x = g & 1;
@@ -686,8 +705,7 @@ __global__ void __launch_bounds__(Cfg8<D, RP>::THREADS, 1)
                     }
                     tc_fence_after();
                     const uint32_t vb = sm_base + st * C::STAGE_BYTES + C::OP_BYTES, pd = fix_base + C::FIX_P + x * C::P_BYTES;
-                    // a unit's first product starts its O afresh: each softmax warp wrote the P of it after it had read
-                    // out the O of two units before, the same buffer.
+                    // a unit's first product starts its O afresh; the buffer's last one has been read out.
                     // V^T: dims contiguous; d = 64 repeats its 64 rows (stride 0) to the MMA's 128
 #pragma unroll
                     for (int kk = 0; kk < kTileKeys / 32; ++kk)
@@ -696,6 +714,7 @@ __global__ void __launch_bounds__(Cfg8<D, RP>::THREADS, 1)
                     tc_commit(empty + 8 * st);
                     tc_commit(pvdone + 8 * x);
                 }
+                if (ok) tc_commit(odone + 8 * (k & 1));
             }
             if (!ok) misc[1] = 1;
             tc_commit(fin + 8);
@@ -746,7 +765,9 @@ __global__ void __launch_bounds__(Cfg8<D, RP>::THREADS, 1)
         }
         if (!ok && lane == 0) misc[1] = 1;
         asm volatile("cp.async.wait_all;" ::: "memory");
-    } else {   // -------------------------------------------------------- softmax
+    }
+    } else if (warp < 4 + C::SM_WARPS) {   // ---------------------------- softmax
+        if constexpr (C::SM_REGS > C::LAUNCH_REGS) take_registers<true, C::SM_REGS>();
         constexpr int CG = C::CG;
         // p is 2^kBase at the running maximum, which is raised once a score passes it by 2^kOver: fp16 (and e5m2) hold
         // both ends, and what is 2^-24 of the maximum still has a bit
@@ -755,94 +776,20 @@ __global__ void __launch_bounds__(Cfg8<D, RP>::THREADS, 1)
         const int bar = 1 + grp, gt = quarter * 32 + lane;   // thread of the group
         const uint32_t tl = tmem + ((uint32_t)(quarter * 32) << 16);
         const int kslot = quarter * 32 + lane;   // this lane's key of a tile, and its dim of O
-        const uint32_t mx_s = fix_base + C::FIX_MX + grp * 16 * CG, ls_s = fix_base + C::FIX_LS;
-        const uint32_t f_s = fix_base + C::FIX_F + cb * 4, v_s = fix_base + C::FIX_V + grp * 16;
+        const uint32_t mx_s = fix_base + C::FIX_MX + grp * 16 * CG, v_s = fix_base + C::FIX_V + grp * 16;
         const uint32_t f2_s = fix_base + C::FIX_F2 + cb * 4, m_s = fix_base + C::FIX_M + cb * 4;
         bool ok = true;
         int g = 0;
-        // this warp's share of a unit's query rows, all of them at once, once the raw rows are there
-        auto convert = [&](int unit) {
-            const uint32_t qd = fix_base + C::FIX_Q + (unit & 1) * C::Q_BYTES;
-            constexpr int ROWS = RP / C::SM_WARPS, LPR = 32 / ROWS, EPL = D / LPR;   // of a warp; lanes of a row; values of a lane
-            const int sub = lane % LPR, c = (warp - 4) * ROWS + lane / LPR;
-            uint32_t w[EPL / 2];   // two values each
-            const uint32_t src = qd + ((sub >= LPR / 2 ? RP : 0) + c) * D + sub % (LPR / 2) * (2 * EPL);
-#pragma unroll
-            for (int e = 0; e < EPL / 2; e += 2)
-                asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];" : "=r"(w[e]), "=r"(w[e + 1]) : "r"(src + 4 * e) : "memory");
-            uint32_t top = 0;   // two |values| at a time, which order as their bits do, infinities and NaN on top
-#pragma unroll
-            for (int e = 0; e < EPL / 2; ++e) top = __vmaxu2(top, w[e] & 0x7fff7fffu);
-#pragma unroll
-            for (int o = LPR / 2; o; o >>= 1) top = __vmaxu2(top, __shfl_xor_sync(~0u, top, o));
-            top = max(top >> 16, top & 0xffffu);
-            // 2^(exponent - 7), within the normal numbers whose reciprocal is one too
-            int ex = (int)(top >> 7) - 7;
-            ex = ex < 4 ? 4 : ex;
-            const float inv = __uint_as_float((uint32_t)(254 - ex) << 23);
-#pragma unroll
-            for (int e = 0; e < EPL / 4; ++e) {
-                uint32_t h2[2], l2[2];
-#pragma unroll
-                for (int f = 0; f < 2; ++f) {   // fp16 holds the scaled values and every difference here
-                    const uint32_t v = w[2 * e + f];
-                    const float2 y = __fmul2_rn(make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u)),
-                                                make_float2(inv, inv));
-                    const uint32_t y16 = half2_of(y.x, y.y);
-                    h2[f] = half2_to_fp8x2(y16);
-                    l2[f] = half2_to_fp8x2(hsub2(y16, fp8x2_to_half2(h2[f])));
-                }
-                // 16-byte chunks of a row are permuted as the MMA's descriptor says
-                const int at = sub * EPL + 4 * e;
-                auto place = [&](int row) {
-                    const int flip = D == 128 ? row & 7 : (row >> 1) & 3;
-                    return qd + row * D + (((at >> 4) ^ flip) << 4) + (at & 15);
-                };
-                stsi(place(c), (int)(h2[0] | h2[1] << 16));
-                stsi(place(RP + c), (int)(l2[0] | l2[1] << 16));
-            }
-            if (sub == 0)
-                stsi(fix_base + C::FIX_QS + (unit % kRing * 64 + c) * 4, top >= 0x7f80u ? 0x7fc00000 : (int)((uint32_t)ex << 23));
-            fence_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(qready + 8 * (unit & 1));
-        };
-        bool converted = false;   // this unit's rows, during the unit before
-        int done_parts = 1;       // of the unit before
-        float done_ref = 0.f, done_m = 0.f;   // done_m: of column gt
         for (int k = 0;; ++k) {
             const int r = k % kRing;
             if (!wait_warp(iready + 8 * r, (uint32_t)(k / kRing) & 1u)) ok = false;
+            if (gt < CG) sts1(m_s + gt * 4, 1e30f);
             if (bar_any(bar, 128, !ok)) {   // all of the group go on, or none
                 ok = false;
                 break;
             }
             const Unit8 u = read_unit(r);
-            const bool more = u.b >= 0;
-            if (more && !converted) {
-                if (!wait_warp(qraw + 8 * (k & 1), (uint32_t)(k >> 1) & 1u)) ok = false;
-                convert(k);
-            }
-            // the unit before is written out after this one's first tile (or at the end): its last product and this
-            // unit's first do not wait for that
-            bool pending = k > 0;
-            converted = false;
-            const int dr = (k - 1) % kRing;
-            if (pending && gt < CG) {   // the sums are all there since the barrier
-                const uint32_t c = ls_s + (cb + gt) * 4;
-                const float lsum = (lds1(c) + lds1(c + 256)) + (lds1(c + 512) + lds1(c + 768));
-                // a part keeps its own maximum and sum; a whole unit is divided by its sum
-                sts1(f_s + gt * 4, done_parts > 1 ? done_ref : done_ref / lsum);
-                if (done_parts > 1) {
-                    const Unit8 done = read_unit(dr);
-                    a.part_ml[(size_t)(done.slot + done.part) * RP + cb + gt] = make_float2(done_m, lsum);
-                }
-            }
-            if (!more) {
-                if (!pending) break;
-                bar_sync(bar, 128);
-            }
-            if (gt < CG) sts1(m_s + gt * 4, 1e30f);
+            if (u.b < 0) break;
             const uint32_t oc = tl + C::O_COL + (k & 1) * 3 * RP + cb;   // this unit's O
             const int L = u.P + u.n;
             float2 m[CG / 2], l[CG / 2];   // kBase - maximum; sums over this lane's keys
@@ -1039,96 +986,26 @@ __global__ void __launch_bounds__(Cfg8<D, RP>::THREADS, 1)
             };
             const int plain_end = min(u.j1, u.P / kTileKeys);   // tiles before the first with tree keys
             bool gone = false;
-            do {
-                if (more) {
-                    bool raise = j == u.j0;
-                    if (!raise) {
+            while (j < u.j1) {
+                bool raise = j == u.j0;
+                if (!raise) {
 #pragma unroll 1
-                        while (j < plain_end && plain_tile()) {
-                            ++j;
-                            ++g;
-                        }
-                        raise = j < plain_end;
-                        // the next unit's query rows before the last tile, if they are there by then (the registers of
-                        // 64-row blocks have no room for it here)
-                        const int nr = (k + 1) % kRing;
-                        if (RP < 64 && !converted && !raise &&
-                            __all_sync(~0u, mbar_test(iready + 8 * nr, (uint32_t)((k + 1) / kRing) & 1u)) &&
-                            ldsi(fix_base + C::FIX_INFO + nr * 48) >= 0 &&
-                            __all_sync(~0u, mbar_test(qraw + 8 * ((k + 1) & 1), (uint32_t)((k + 1) >> 1) & 1u))) {
-                            convert(k + 1);
-                            converted = true;
-                        }
-                        if (j == u.j1) break;
+                    while (j < plain_end && plain_tile()) {
+                        ++j;
+                        ++g;
                     }
-                    if (!any_tile(raise)) {
-                        gone = true;
-                        break;
-                    }
-                    ++j;
-                    ++g;
+                    if (j == u.j1) break;
+                    raise = j < plain_end;
                 }
-                if (pending) {
-                    pending = false;
-                    const Unit8 done = read_unit(dr);
-                    const int pg = more ? g - 2 : g - 1;   // its last tile
-                    if (ok && !wait_warp(pvdone + 8 * (pg & 1), (uint32_t)(pg >> 1) & 1u)) ok = false;
-                    tc_fence_after();
-                    __nv_bfloat16 *ob = a.out + (size_t)done.b * n_max * a.Hq * D;
-                    const uint32_t rows = fix_base + C::FIX_QROW + (dr * 64 + cb) * 4;
-        #pragma unroll 1
-                    for (int c = 0; c < CG; c += 8) {
-                        float o[3][8];
-                        if (ok && quarter * 32 < D) {
-        #pragma unroll
-                            for (int i = 0; i < 3; ++i) tc_ld8(tl + C::O_COL + (~k & 1) * 3 * RP + i * RP + cb + c, o[i]);
-                            tc_wait_ld();
-                        }
-                        if (!ok || quarter * 32 >= D) continue;
-        #pragma unroll
-                        for (int e = 0; e < 8; e += 4) {
-                            const float4 f = lds4(f_s + (c + e) * 4);
-                            o[0][e] = ((o[0][e] + o[1][e]) + o[2][e]) * f.x;
-                            o[0][e + 1] = ((o[0][e + 1] + o[1][e + 1]) + o[2][e + 1]) * f.y;
-                            o[0][e + 2] = ((o[0][e + 2] + o[1][e + 2]) + o[2][e + 2]) * f.z;
-                            o[0][e + 3] = ((o[0][e + 3] + o[1][e + 3]) + o[2][e + 3]) * f.w;
-                        }
-                        if (done.parts > 1) {
-                            float *po = a.part_o + ((size_t)(done.slot + done.part) * RP + cb + c) * D + kslot;
-        #pragma unroll
-                            for (int e = 0; e < 8; ++e) po[e * D] = o[0][e];
-                        } else {
-                            // two columns at a time: even lanes store dims (d, d + 1) of the first, odd lanes of the second
-        #pragma unroll
-                            for (int e = 0; e < 8; e += 2) {
-                                const float keep = lane & 1 ? o[0][e + 1] : o[0][e], send = lane & 1 ? o[0][e] : o[0][e + 1];
-                                const float got = __shfl_xor_sync(~0u, send, 1);
-                                const int row = ldsi(rows + (c + e + (lane & 1)) * 4);
-                                const __nv_bfloat162 v = lane & 1 ? __floats2bfloat162_rn(got, keep) : __floats2bfloat162_rn(keep, got);
-                                if (row >= 0) *(__nv_bfloat162 *)(ob + (size_t)row * D + (kslot & ~1)) = v;
-                            }
-                        }
-                    }
-                    if (done.parts > 1) {   // the last part of the item to finish joins them, for this group's columns
-                        __threadfence();
-                        bar_sync(bar, 128);
-                        if (gt == 0) {
-                            unsigned *cnt = a.joins + (size_t)done.slot * 4 + grp;
-                            const bool last = ok && atomicAdd(cnt, 1u) == (unsigned)done.parts - 1;
-                            if (last) *cnt = 0u;
-                            misc[4 + grp] = last;
-                        }
-                        bar_sync(bar, 128);
-                        if (misc[4 + grp])
-                            join_parts<D, RP, CG>(a.part_ml + (size_t)done.slot * RP + cb, a.part_o + ((size_t)done.slot * RP + cb) * D,
-                                                  done.parts, rows, ob);
-                    }
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(ifree + 8 * dr);
+                if (!any_tile(raise)) {
+                    gone = true;
+                    break;
                 }
-            } while (more && j < u.j1);
-            if (!more) break;
+                ++j;
+                ++g;
+            }
             if (gone) break;
+            // the unit's sums, maxima and reference to the output warps, once those of two units before are read
             float v[CG];
 #pragma unroll
             for (int c = 0; c < CG / 2; ++c) {
@@ -1136,12 +1013,163 @@ __global__ void __launch_bounds__(Cfg8<D, RP>::THREADS, 1)
                 v[2 * c + 1] = l[c].y;
             }
             reduce_scatter<CG>(v, lane);
-            if (lane % (32 / CG) == 0) sts1(ls_s + (quarter * 64 + cb + lane / (32 / CG)) * 4, v[0]);
-            if (gt < CG) done_m = -lds1(m_s + gt * 4);
-            done_parts = u.parts;
-            done_ref = ref;
+            if (k >= 2 && !wait_warp(ofree + 8 * (k & 1), (uint32_t)(k / 2 - 1) & 1u)) ok = false;
+            const uint32_t sum = fix_base + C::FIX_SUM + (k & 1) * C::SUM_BYTES;
+            if (lane % (32 / CG) == 0) sts1(sum + (quarter * 64 + cb + lane / (32 / CG)) * 4, v[0]);
+            if (gt < CG) {
+                sts1(sum + (4 * 64 + cb + gt) * 4, -lds1(m_s + gt * 4));
+                sts1(sum + (5 * 64 + cb + gt) * 4, ref);
+            }
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(sumfull + 8 * (k & 1));
+                mbar_arrive(ifree + 8 * r);
+            }
         }
         if (!ok) misc[1] = 1;
+    } else {   // -------------------------------------------------------- query rows, output
+        if constexpr (C::SM_REGS > C::LAUNCH_REGS) take_registers<false, C::OTHER_REGS>();
+        // Unit k's query rows are split here, then unit k - 1 is written out: its last product, its writing and the
+        // next unit's first scores run at the same time.
+        const int quarter = warp & 3, dim = quarter * 32 + lane;
+        bool ok = true;
+        for (int k = 0;; ++k) {
+            const int r = k % kRing;
+            if (!wait_warp(iready + 8 * r, (uint32_t)(k / kRing) & 1u)) ok = false;
+            if (bar_any(15, 128, !ok)) {   // all four warps go on, or none
+                ok = false;
+                break;
+            }
+            const bool more = ldsi(fix_base + C::FIX_INFO + r * 48) >= 0;
+            if (more) {
+                if (!wait_warp(qraw + 8 * (k & 1), (uint32_t)(k >> 1) & 1u)) ok = false;
+                const uint32_t qd = fix_base + C::FIX_Q + (k & 1) * C::Q_BYTES;
+                constexpr int LPR = 8, EPL = D / LPR;   // lanes of a row; values of a lane
+                const int sub = lane % LPR;
+#pragma unroll 1
+                for (int c = quarter * (RP / 4) + lane / LPR; c < (quarter + 1) * (RP / 4); c += 4) {
+                uint32_t w[EPL / 2];   // two values each
+                const uint32_t src = qd + ((sub >= LPR / 2 ? RP : 0) + c) * D + sub % (LPR / 2) * (2 * EPL);
+#pragma unroll
+                for (int e = 0; e < EPL / 2; e += 2)
+                    asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];" : "=r"(w[e]), "=r"(w[e + 1]) : "r"(src + 4 * e) : "memory");
+                uint32_t top = 0;   // two |values| at a time, which order as their bits do, infinities and NaN on top
+#pragma unroll
+                for (int e = 0; e < EPL / 2; ++e) top = __vmaxu2(top, w[e] & 0x7fff7fffu);
+#pragma unroll
+                for (int o = LPR / 2; o; o >>= 1) top = __vmaxu2(top, __shfl_xor_sync(~0u, top, o));
+                top = max(top >> 16, top & 0xffffu);
+                // 2^(exponent - 7), within the normal numbers whose reciprocal is one too
+                int ex = (int)(top >> 7) - 7;
+                ex = ex < 4 ? 4 : ex;
+                const float inv = __uint_as_float((uint32_t)(254 - ex) << 23);
+#pragma unroll
+                for (int e = 0; e < EPL / 4; ++e) {
+                    uint32_t h2[2], l2[2];
+#pragma unroll
+                    for (int f = 0; f < 2; ++f) {   // fp16 holds the scaled values and every difference here
+                        const uint32_t v = w[2 * e + f];
+                        const float2 y = __fmul2_rn(make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u)),
+                                                    make_float2(inv, inv));
+                        const uint32_t y16 = half2_of(y.x, y.y);
+                        h2[f] = half2_to_fp8x2(y16);
+                        l2[f] = half2_to_fp8x2(hsub2(y16, fp8x2_to_half2(h2[f])));
+                    }
+                    // 16-byte chunks of a row are permuted as the MMA's descriptor says
+                    const int at = sub * EPL + 4 * e;
+                    auto place = [&](int row) {
+                        const int flip = D == 128 ? row & 7 : (row >> 1) & 3;
+                        return qd + row * D + (((at >> 4) ^ flip) << 4) + (at & 15);
+                    };
+                    stsi(place(c), (int)(h2[0] | h2[1] << 16));
+                    stsi(place(RP + c), (int)(l2[0] | l2[1] << 16));
+                }
+                if (sub == 0)
+                    stsi(fix_base + C::FIX_QS + (r * 64 + c) * 4, top >= 0x7f80u ? 0x7fc00000 : (int)((uint32_t)ex << 23));
+                }
+                fence_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(qready + 8 * (k & 1));
+            }
+            if (k > 0) {
+                const int par = (k - 1) & 1, dr = (k - 1) % kRing;
+                const Unit8 done = read_unit(dr);
+                if (ok && (!wait_warp(sumfull + 8 * par, (uint32_t)((k - 1) >> 1) & 1u) ||
+                           !wait_warp(odone + 8 * par, (uint32_t)((k - 1) >> 1) & 1u)))
+                    ok = false;
+                if (bar_any(15, 128, !ok)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                // lane c: factor and place of columns c and 32 + c; a part keeps its own maximum and sum, a whole
+                // unit is divided by its sum
+                float f[2] = {0.f, 0.f};
+                int place[2] = {-1, -1};
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int c = h * 32 + lane;
+                    if (c < RP) {
+                        const uint32_t sum = fix_base + C::FIX_SUM + par * C::SUM_BYTES + c * 4;
+                        const float lsum = (lds1(sum) + lds1(sum + 256)) + (lds1(sum + 512) + lds1(sum + 768)), ref = lds1(sum + 1280);
+                        f[h] = done.parts > 1 ? ref : ref / lsum;
+                        place[h] = ldsi(fix_base + C::FIX_QROW + (dr * 64 + c) * 4);
+                        if (done.parts > 1 && quarter == 0)
+                            a.part_ml[(size_t)(done.slot + done.part) * RP + c] = make_float2(lds1(sum + 1024), lsum);
+                    }
+                }
+                __nv_bfloat16 *ob = a.out + (size_t)done.b * n_max * a.Hq * D;
+                const uint32_t oc = tmem + ((uint32_t)(quarter * 32) << 16) + C::O_COL + par * 3 * RP;
+                if (quarter * 32 < D) {
+#pragma unroll 1
+                    for (int c = 0; c < RP; c += 4) {
+                        float o[3][4];
+#pragma unroll
+                        for (int i = 0; i < 3; ++i) tc_ld4(oc + i * RP + c, o[i]);
+                        tc_wait_ld();
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            o[0][e] = ((o[0][e] + o[1][e]) + o[2][e]) * __shfl_sync(~0u, c < 32 ? f[0] : f[1], (c + e) & 31);
+                        if (done.parts > 1) {
+                            float *po = a.part_o + ((size_t)(done.slot + done.part) * RP + c) * D + dim;
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) po[e * D] = o[0][e];
+                        } else {
+                            // two columns at a time: even lanes store dims (d, d + 1) of the first, odd lanes of the second
+#pragma unroll
+                            for (int e = 0; e < 4; e += 2) {
+                                const float keep = lane & 1 ? o[0][e + 1] : o[0][e], send = lane & 1 ? o[0][e] : o[0][e + 1];
+                                const float got = __shfl_xor_sync(~0u, send, 1);
+                                const int row = __shfl_sync(~0u, c < 32 ? place[0] : place[1], (c + e + (lane & 1)) & 31);
+                                const __nv_bfloat162 v = lane & 1 ? __floats2bfloat162_rn(got, keep) : __floats2bfloat162_rn(keep, got);
+                                if (row >= 0) *(__nv_bfloat162 *)(ob + (size_t)row * D + (dim & ~1)) = v;
+                            }
+                        }
+                    }
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(ofree + 8 * par);
+                if (done.parts > 1) {   // the last part of the item to finish joins them
+                    __threadfence();
+                    bar_sync(15, 128);
+                    if (quarter == 0 && lane == 0) {
+                        unsigned *cnt = a.joins + done.slot;
+                        const bool last = atomicAdd(cnt, 1u) == (unsigned)done.parts - 1;
+                        if (last) *cnt = 0u;
+                        misc[3] = last;
+                    }
+                    bar_sync(15, 128);
+                    if (misc[3])
+                        join_parts<D, RP>(a.part_ml + (size_t)done.slot * RP, a.part_o + (size_t)done.slot * RP * D, done.parts,
+                                          fix_base + C::FIX_QROW + dr * 256, ob);
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(ifree + 8 * dr);
+            }
+            if (!more) break;
+        }
+        if (!ok && lane == 0) misc[1] = 1;
     }
     tc_fence_before();
     __syncthreads();
@@ -1175,7 +1203,7 @@ Plan8 plan8(int B, int Hkv, int G, int n_max, int d) {
     p.blocks = (int)((rows + p.rp - 1) / p.rp);
     const long long most = (long long)B * Hkv * p.blocks * kMaxCuts;
     p.slots = B > kReqCache ? 0 : (int)(most < kSlotsPerSm * num_sms() ? most : kSlotsPerSm * num_sms());
-    size_t at = 256 + ((size_t)p.slots * 4 * sizeof(unsigned) + 255) / 256 * 256;
+    size_t at = 256 + ((size_t)p.slots * sizeof(unsigned) + 255) / 256 * 256;
     p.ml = at;
     at += (size_t)p.slots * p.rp * sizeof(float2);
     p.o = (at + 255) / 256 * 256;
@@ -1199,6 +1227,11 @@ cudaError_t launch8(const CUtensorMap &mk, const CUtensorMap &mv, const Attn8Arg
     using C = Cfg8<D, RP>;
     cudaError_t e = cudaFuncSetAttribute(k_attn_kv8<D, RP>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
     if (e != cudaSuccess) return e;
+    if (C::SM_REGS > C::LAUNCH_REGS) {   // the kernel waits for registers that a smaller launch would not have
+        cudaFuncAttributes at;
+        if ((e = cudaFuncGetAttributes(&at, k_attn_kv8<D, RP>)) != cudaSuccess) return e;
+        if (at.numRegs < C::LAUNCH_REGS) return cudaErrorInvalidConfiguration;
+    }
     return launch(k_attn_kv8<D, RP>, dim3(grid), dim3(C::THREADS), C::SMEM, s, mk, mv, a);
 }
 
