@@ -257,8 +257,7 @@ def tree_attention_append(out, q, k_cache, v_cache, k_new, v_new, prefix_len, tr
     _check(lib.tree_attention_append(_ptr(out), _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(k_new), _ptr(v_new),
                                      _ptr(_i32(prefix_len, "prefix_len")), tree.c, H, d, L_max, _dtype(k_cache),
                                      float(scale), _ptr(ws), nbytes, _ptr(status), _stream(stream)),
-           "tree_attention_append", "tree_qk_norm_rope", "kv8_append", "kv8_read", "tree_attention_kv8", "kv8_commit",
-           "treespec_kv8_workspace_size")
+           "tree_attention_append")
 
 
 def tree_attention_noalloc(out, q, k_cache, v_cache, prefix_len, tree: Tree, scale: float = 0.0, status=None,
