@@ -357,15 +357,11 @@ def kv_commit_paged(kv: PagedKV, prefix_len, new_prefix_len, out_path, out_count
 
 
 # -- head norms with rotation, and the 8-bit KV cache -----------------------------
-def _need(cond, msg):
-    if not cond:
-        raise TreespecError(msg)
-
-
+# Checks are written as tests around a raise, so that a call that passes builds no message.
 def _int_array(t, n, name, device):
     """Pointer of an int32 tensor of at least n entries on `device`."""
-    _need(t.dtype == torch.int32 and t.numel() >= n and t.is_contiguous() and t.device == device,
-          f"{name} must be a contiguous int32 tensor of {n} entries on {device}")
+    if t.dtype != torch.int32 or t.numel() < n or t.device != device or not t.is_contiguous():
+        raise TreespecError(f"{name} must be a contiguous int32 tensor of {n} entries on {device}")
     return t.data_ptr()
 
 
@@ -376,30 +372,38 @@ def _status_ptr(status, device):
 def _node_rows(t, tree, H, d, name, dtype, device):
     """(pointer, elements from one node to the next) of node rows [B][n_max][H][d]: heads contiguous, nodes and
     requests a constant stride apart (a slice of a wider projection output)."""
-    _need(t.dtype == dtype and t.device == device, f"{name} must be {dtype} on {device}")
     B, n = tree.B, tree.n_max
-    _need(tuple(t.shape) == (B, n, H, d), f"{name} has shape {tuple(t.shape)}, not {(B, n, H, d)}")
+    if t.dtype != dtype or t.device != device or t.shape != (B, n, H, d):
+        raise TreespecError(f"{name} must be a {dtype} tensor {(B, n, H, d)} on {device}, not {t.dtype} {tuple(t.shape)} "
+                            f"on {t.device}")
     sb, sn, sh, sd = t.stride()
     if n == 1:
         sn = sb if B > 1 else H * d
-    _need(sd == 1 and (H == 1 or sh == d) and (B == 1 or sb == n * sn),
-          f"{name}: heads must be contiguous, nodes and requests a constant stride apart")
+    if sd != 1 or (H > 1 and sh != d) or (B > 1 and sb != n * sn):
+        raise TreespecError(f"{name}: heads must be contiguous, nodes and requests a constant stride apart")
     return t.data_ptr(), sn
 
 
 def _out_rows(t, tree, H, d, name, dtype, device):
-    _need(t.dtype == dtype and t.device == device and tuple(t.shape) == (tree.B, tree.n_max, H, d)
-          and t.is_contiguous(), f"{name} must be a contiguous {dtype} tensor {(tree.B, tree.n_max, H, d)} on {device}")
+    if t.dtype != dtype or t.device != device or t.shape != (tree.B, tree.n_max, H, d) or not t.is_contiguous():
+        raise TreespecError(f"{name} must be a contiguous {dtype} tensor {(tree.B, tree.n_max, H, d)} on {device}")
     return t.data_ptr()
+
+
+def _same_device(tree, device):
+    if tree.n_nodes.device != device:
+        raise TreespecError(f"the tree is on {tree.n_nodes.device}, not {device}")
 
 
 def _run(fn, what, device, stream, *args):
     """Call an entry point on the current stream of the tensors' device (or the given one)."""
-    if stream is None and device.index == torch.cuda.current_device():
-        _check(fn(*args, torch.cuda.current_stream(device).cuda_stream), what)
-        return
-    with torch.cuda.device(device):
-        _check(fn(*args, (stream or torch.cuda.current_stream(device)).cuda_stream), what)
+    if device.index == torch.cuda.current_device():
+        rc = fn(*args, (stream or torch.cuda.current_stream()).cuda_stream)
+    else:
+        with torch.cuda.device(device):
+            rc = fn(*args, (stream or torch.cuda.current_stream()).cuda_stream)
+    if rc != TS_OK:
+        _check(rc, what)
 
 
 class QKRope:
@@ -410,8 +414,9 @@ class QKRope:
                  interleaved: bool = False):
         given = [x for x in (inv_freq, q_weight, k_weight) if x is not None]
         for x in given:
-            _need(x.dtype == torch.float32 and x.is_contiguous() and x.dim() == 1 and x.is_cuda
-                  and x.device == given[0].device, "inv_freq and weights must be contiguous fp32 vectors on one CUDA device")
+            if not (x.dtype == torch.float32 and x.is_contiguous() and x.dim() == 1 and x.is_cuda
+                    and x.device == given[0].device):
+                raise TreespecError("inv_freq and weights must be contiguous fp32 vectors on one CUDA device")
         self.inv_freq, self.q_weight, self.k_weight = inv_freq, q_weight, k_weight
         self.device = given[0].device if given else None
         self.rot_dim = 0 if inv_freq is None else 2 * inv_freq.numel()
@@ -421,9 +426,11 @@ class QKRope:
         self._ref = C.byref(self._c)
 
     def _for(self, d, device):
-        _need(self.device is None or self.device == device, f"the rotation's tensors are on {self.device}, not {device}")
+        if self.device is not None and self.device != device:
+            raise TreespecError(f"the rotation's tensors are on {self.device}, not {device}")
         for w in (self.q_weight, self.k_weight):
-            _need(w is None or w.numel() == d, f"norm weights must have head_dim {d} entries")
+            if w is not None and w.numel() != d:
+                raise TreespecError(f"norm weights must have head_dim {d} entries")
         return self._ref
 
     @staticmethod
@@ -436,9 +443,10 @@ def tree_qk_norm_rope(q_out, k_out, q, k, rope: QKRope, tree: Tree, status=None,
     """Norm every head of q and k [B][n_max][H][d] and rotate it to its node's position (tree.pos); q or k may be
     None with its output. Outputs are contiguous, and may be the inputs where those are."""
     x = q if q is not None else k
-    _need(x is not None and x.is_cuda and x.dim() == 4, "q or k [B][n_max][H][d] on a CUDA device is needed")
+    if x is None or not x.is_cuda or x.dim() != 4:
+        raise TreespecError("q or k [B][n_max][H][d] on a CUDA device is needed")
     dev, d, dt = x.device, x.shape[3], _dtype(x)
-    _need(tree.n_nodes.device == dev, f"the tree is on {tree.n_nodes.device}, not {dev}")
+    _same_device(tree, dev)
     qp = kp = qo = ko = None
     Hq = Hk = qs = ks = 0
     if q is not None:
@@ -457,19 +465,22 @@ class KV8:
     k, v [num_pages][H][PAGE_KEYS][d], scales [num_pages][H][PAGE_KEYS]."""
 
     def __init__(self, k, v, k_scale, v_scale, block_table=None):
-        _need(k.dim() == 4 and k.dtype == torch.float8_e4m3fn and v.dtype == k.dtype and v.shape == k.shape,
-              "k and v must be two float8_e4m3fn tensors of one shape [B or pages][H][rows][d]")
-        _need(k_scale.dtype == torch.float32 and v_scale.dtype == torch.float32 and k_scale.shape == k.shape[:3]
-              and v_scale.shape == k.shape[:3], "scales must be fp32 of the codes' shape without head_dim")
+        if not (k.dim() == 4 and k.dtype == torch.float8_e4m3fn and v.dtype == k.dtype and v.shape == k.shape):
+            raise TreespecError("k and v must be two float8_e4m3fn tensors of one shape [B or pages][H][rows][d]")
+        if not (k_scale.dtype == torch.float32 and v_scale.dtype == torch.float32 and k_scale.shape == k.shape[:3]
+                and v_scale.shape == k.shape[:3]):
+            raise TreespecError("scales must be fp32 of the codes' shape without head_dim")
         for x in (k, v, k_scale, v_scale):
-            _need(x.is_cuda and x.is_contiguous() and x.device == k.device,
-                  "cache tensors must be contiguous on one CUDA device")
+            if not (x.is_cuda and x.is_contiguous() and x.device == k.device):
+                raise TreespecError("cache tensors must be contiguous on one CUDA device")
         self.k, self.v, self.k_scale, self.v_scale, self.block_table = k, v, k_scale, v_scale, block_table
         self.H, self.d, self.device = k.shape[1], k.shape[3], k.device
         pages = 0
         if block_table is not None:
-            _need(k.shape[2] == PAGE_KEYS, f"a page holds {PAGE_KEYS} keys")
-            _need(block_table.dim() == 2, "block_table must be [B][max_pages]")
+            if k.shape[2] != PAGE_KEYS:
+                raise TreespecError(f"a page holds {PAGE_KEYS} keys")
+            if block_table.dim() != 2:
+                raise TreespecError("block_table must be [B][max_pages]")
             _int_array(block_table, 1, "block_table", k.device)
             self.B, pages = block_table.shape
             self.L_max = pages * PAGE_KEYS
@@ -494,8 +505,9 @@ class KV8:
         return cls(z(*s, d), z(*s, d), z(*s, t=torch.float32), z(*s, t=torch.float32), block_table)
 
     def _with(self, tree: Tree):
-        _need(tree.B == self.B, f"cache of {self.B} requests, tree of {tree.B}")
-        _need(tree.n_nodes.device == self.device, f"the tree is on {tree.n_nodes.device}, the cache on {self.device}")
+        if tree.B != self.B:
+            raise TreespecError(f"cache of {self.B} requests, tree of {tree.B}")
+        _same_device(tree, self.device)
         return self._ref
 
 
@@ -510,10 +522,10 @@ def kv8_append(kv: KV8, k_new, v_new, prefix_len, tree: Tree, rope: QKRope | Non
     qp = qo = r = None
     Hq = qs = 0
     if q is not None:
-        _need(rope is not None, "queries are only taken with rope")
+        if rope is None or q_out is None:
+            raise TreespecError("queries are only taken with rope, and need q_out")
         Hq = q.shape[2]
         qp, qs = _node_rows(q, tree, Hq, d, "q", k_new.dtype, dev)
-        _need(q_out is not None, "q_out is needed with q")
         qo = _out_rows(q_out, tree, Hq, d, "q_out", k_new.dtype, dev)
     if rope is not None:
         r = rope._for(d, dev)
@@ -527,8 +539,8 @@ def kv8_read(k_out, v_out, kv: KV8, row_end, row_begin=None, status=None, stream
     dev = kv.device
     shape = (kv.B, kv.H, k_out.shape[2] if k_out.dim() == 4 else 0, kv.d)
     for x in (k_out, v_out):
-        _need(tuple(x.shape) == shape and x.dtype == k_out.dtype and x.device == dev and x.is_contiguous(),
-              f"k_out and v_out must be contiguous tensors {shape} of one dtype on {dev}")
+        if x.shape != shape or x.dtype != k_out.dtype or x.device != dev or not x.is_contiguous():
+            raise TreespecError(f"k_out and v_out must be contiguous tensors {shape} of one dtype on {dev}")
     begin = None if row_begin is None else _int_array(row_begin, kv.B, "row_begin", dev)
     _run(load_library().kv8_read, "kv8_read", dev, stream, k_out.data_ptr(), v_out.data_ptr(), kv._ref, begin,
          _int_array(row_end, kv.B, "row_end", dev), shape[2], _dtype(k_out), _status_ptr(status, dev))
@@ -544,11 +556,13 @@ def kv8_workspace(B: int, Hq: int, Hkv: int, n_max: int, d: int, L_max: int, dev
 def tree_attention_kv8(out, q, kv: KV8, prefix_len, tree: Tree, scale: float = 0.0, ws=None, status=None, stream=None):
     """tree_attention over an 8-bit cache; q, out [B][n_max][Hq][d] bfloat16, Hq a multiple of kv.H."""
     ref, dev = kv._with(tree), kv.device
-    _need(q.dim() == 4, "q must be [B][n_max][Hq][d]")
+    if q.dim() != 4:
+        raise TreespecError("q must be [B][n_max][Hq][d]")
     Hq = q.shape[2]
     op = _out_rows(out, tree, Hq, kv.d, "out", torch.bfloat16, dev)
     qp = _out_rows(q, tree, Hq, kv.d, "q", torch.bfloat16, dev)
-    _need(ws is not None and ws.device == dev and ws.is_contiguous(), f"a workspace (kv8_workspace) on {dev} is needed")
+    if ws is None or ws.device != dev or not ws.is_contiguous():
+        raise TreespecError(f"a workspace (kv8_workspace) on {dev} is needed")
     _run(load_library().tree_attention_kv8, "tree_attention_kv8", dev, stream, op, qp, ref, Hq,
          _int_array(prefix_len, tree.B, "prefix_len", dev), tree.c, float(scale), ws.data_ptr(),
          ws.numel() * ws.element_size(), _status_ptr(status, dev))
