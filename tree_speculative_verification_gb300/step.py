@@ -25,14 +25,21 @@ class DeviceStep:
     """paged: keep the KV cache in pages of api.PAGE_KEYS rows (randomly placed,
     listed per request in a block table) and run the paged calls.
     serial_verify: run verification after the attention on the main stream
-    (the order a verification that also commits would need)."""
+    (the order a verification that also commits would need).
+    kv8: keep the KV cache in 8 bits (dense, or in pages with paged) and run the
+    8-bit calls; rope (an api.QKRope) has the append norm and rotate the query
+    and key heads on the way."""
 
     def __init__(self, w: Workload, device="cuda", attention: bool = True, paged: bool = False,
-                 serial_verify: bool = False, seed: int = 0):
+                 serial_verify: bool = False, seed: int = 0, kv8: bool = False, rope: api.QKRope | None = None):
         self.w = w
         self.device = device
         self.paged = paged
         self.serial_verify = serial_verify
+        self.kv8 = kv8
+        self.rope = rope
+        if rope is not None and not kv8:
+            raise ValueError("the norm and rotation ride in the 8-bit cache's append")
         dev = device
         B, n_max = w.B, w.n_max
         i32 = lambda a: to_device(np.asarray(a, np.int32), dev)
@@ -74,6 +81,15 @@ class DeviceStep:
             self.k_new = to_device(w.k_new, dev, bf)
             self.v_new = to_device(w.v_new, dev, bf)
             self.out = torch.zeros_like(self.q)
+            if kv8:
+                if not bf:
+                    raise ValueError("the attention over an 8-bit cache takes bf16 queries")
+                self.kv = self._cache8(np.random.default_rng(seed))
+                self.k_cache = self.v_cache = None
+                self.q_rot = torch.zeros_like(self.q) if rope is not None else self.q
+                self.ws_attn = api.kv8_workspace(B, w.H, w.H, n_max, w.d, self.kv.L_max, dev)
+                self._fused = False
+                return
             self.ws_attn = api.workspace(api.TS_OP_ATTENTION, B, w.H, n_max, w.d, w.L_max, w.V, device=dev)
             if paged:
                 self.kv = self._pages(np.random.default_rng(seed))
@@ -110,6 +126,21 @@ class DeviceStep:
         dv = self.device
         return api.PagedKV(to_device(kp, dv, True), to_device(vp, dv, True), to_device(bt, dv))
 
+    def _cache8(self, rng):
+        """The prefix cache in 8 bits: each row's codes times its scale are the row to half a step of e4m3."""
+        w, dv = self.w, self.device
+        if self.paged:
+            p = self._pages(rng)
+            k, v, table = p.k_pages, p.v_pages, p.block_table
+        else:
+            k, v, table = to_device(w.k_cache, dv, True), to_device(w.v_cache, dv, True), None
+        parts = []
+        for x in (k, v):
+            x = x.float()
+            scale = torch.clamp_min(x.abs().amax(-1) / 448.0, 2.0 ** -100)
+            parts.append(((x * (1.0 / scale)[..., None]).clamp(-448.0, 448.0).to(torch.float8_e4m3fn), scale))
+        return api.KV8(parts[0][0], parts[1][0], parts[0][1], parts[1][1], table)
+
     # -- the five rows of the hot path ----------------------------------------
     def build(self, stream=None):
         w = self.w
@@ -124,6 +155,11 @@ class DeviceStep:
                            status=self.status, stream=stream)
 
     def append(self, stream=None):
+        if self.kv8:
+            q, q_out = (self.q, self.q_rot) if self.rope is not None else (None, None)
+            api.kv8_append(self.kv, self.k_new, self.v_new, self.prefix_len, self.tree, self.rope, q, q_out,
+                           self.status, stream)
+            return
         if self.paged:
             api.kv_append_paged(self.kv, self.k_new, self.v_new, self.prefix_len, self.tree, self.status, stream)
             return
@@ -131,6 +167,10 @@ class DeviceStep:
                       stream)
 
     def attend(self, stream=None):
+        if self.kv8:
+            api.tree_attention_kv8(self.out, self.q_rot, self.kv, self.prefix_len, self.tree, 0.0, self.ws_attn,
+                                   self.status, stream)
+            return
         if self.paged:
             api.tree_attention_paged(self.out, self.q, self.kv, self.prefix_len, self.tree, 0.0, self.ws_attn,
                                      self.status, stream)
@@ -161,6 +201,9 @@ class DeviceStep:
         kind = kind or self.w.verify
         path, count = ((self.mss_path, self.mss_count) if kind in ("mss", "both", "naive")
                        else (self.out_path, self.out_count))
+        if self.kv8:
+            api.kv8_commit(self.kv, self.prefix_len, self.new_prefix_len, path, count, self.tree, self.status, stream)
+            return
         if self.paged:
             api.kv_commit_paged(self.kv, self.prefix_len, self.new_prefix_len, path, count, self.tree, self.status,
                                 stream)
@@ -247,6 +290,8 @@ class DeviceStep:
         n = 1 + (2 if kind == "both" else 1)
         if self.attention:
             w = self.w
+            if self.kv8:
+                return n + 3
             name = api.attention_kernel(w.B, w.H, w.n_max, w.d, w.L_max,
                                         api.TS_BF16 if w.dtype == "bf16" else api.TS_F32)
             append_rides = self._append_in_attention or (self._fused and kind == "greedy" and not self.serial_verify)
