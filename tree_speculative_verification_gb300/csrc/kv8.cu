@@ -6,6 +6,9 @@
 // row P_b + dfs(v), the accepted path's rows kept after verification.
 #include "kv8.cuh"
 
+#include <algorithm>
+#include <type_traits>
+
 namespace ts {
 namespace {
 
@@ -54,24 +57,32 @@ __device__ __forceinline__ float max_nan(float a, float b) {
     return y;
 }
 
+// Largest magnitude of three, a NaN kept.
+__device__ __forceinline__ float max_abs(float a, float b, float c) {
+    float y;
+    asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+    return y;
+}
+
 // ---- norm, rotation, quantised append ---------------------------------------
 struct RowArgs {
-    const void *q, *k, *v;               // node rows, *_stride values apart
-    long long q_stride, k_stride, v_stride;
-    void *q_out, *k_out;                 // contiguous [B][n_max][H][d]; k_out without the cache
-    int Hq, Hk, Hv;                      // heads handled here (0 leaves a projection out)
-    const float *inv_freq, *q_weight, *k_weight;
+    // by projection: queries, keys, values (0 heads leave one out)
+    const void *src[3];                  // node rows, stride values from one node to the next
+    long long stride[3];
+    int heads[3], groups[3], per_group[3];   // CTAs a node and heads in each, set by rows_launch
+    void *out[2];                        // contiguous [B][n_max][H][d]; keys only without the cache
+    const float *weight[2];
+    const float *inv_freq;
     float eps;
     int norm, rot_dim, interleaved;
     ts_tree t;
-    // append only
-    uint8_t *k8, *v8;
-    float *k_scale, *v_scale;
+    // append only, keys and values
+    uint8_t *codes[2];
+    float *scales[2];
     const int32_t *prefix_len;
     int L_max;
     PagedArgs pg;
     uint32_t *status;
-    int rows_per_cta;
 };
 
 constexpr int kRowThreads = 128, kRowsAhead = 4;
@@ -113,25 +124,27 @@ __device__ __forceinline__ void unpairs(const float2 (&x)[H / 2], const float2 (
     }
 }
 
-// One CTA per (node, group of its heads). A row (one head's d values) is held
-// by LPR lanes, E = d / LPR values each in two pieces of 8 bytes: the first
-// members of E / 2 rotation pairs and the second ones (interleaved pairs: 16
-// bytes in a row), so a rotation needs no other lane; a row's only shuffles
-// are those of its sum of squares (and, quantised, of its largest value). The
-// lane's cosines, sines and norm weights stay in registers over the CTA's rows.
-// The angles are formed once per CTA: position times frequency and its remainder
-// by 2 pi in fp64 (an fp32 product at position 131072 is off by up to 4e-3),
-// then sincosf of the fp32 remainder. Memory bound: each value is read once and
-// written once; kRowsAhead rows a lane group are in flight.
+// One CTA per (node, projection, group of its heads). A row (one head's d
+// values) is held by LPR lanes, E = d / LPR values each in two pieces of 8
+// bytes: the first members of E / 2 rotation pairs and the second ones
+// (interleaved pairs: 16 bytes in a row), so a rotation needs no other lane; a
+// row's only shuffles are those of its sum of squares (and, quantised, of its
+// largest value). The lane's cosines, sines and norm weights stay in registers
+// over the CTA's rows. The angles are formed once per CTA: position times
+// frequency and its remainder by 2 pi in fp64 (an fp32 product at position
+// 131072 is off by up to 4e-3), then sincosf of the fp32 remainder. Each value
+// is read once and written once; kRowsAhead rows a lane group are in flight.
+// What bounds a large call next to memory is issuing: the loop is compiled once
+// for each kind of row (query, key, value), and a CTA runs one of them.
 template <typename T, int D, bool APPEND, bool INTER>
 __global__ void __launch_bounds__(kRowThreads) k_head_rows(RowArgs a) {
     constexpr int E = 16 / (int)sizeof(T), LPR = D / E, RPC = kRowThreads / LPR, RW = 32 / LPR, H = E / 2;
-    using U = typename Two<T>::U;
     __shared__ float2 cs_s[D / 2];
     __shared__ int bad_s;
     const int n_max = a.t.n_max, b = blockIdx.x / n_max, v = blockIdx.x - b * n_max;
     const int tid = threadIdx.x, sub = tid % LPR, slot = tid / LPR;
     const int half = a.rot_dim >> 1;
+    const int kind = (int)blockIdx.y < a.groups[0] ? 0 : (int)blockIdx.y < a.groups[0] + a.groups[1] ? 1 : 2;
     // this lane's pairs p0 .. p0 + H - 1: pair p is (p, p + half), or behind the rotated part (unrotated) the
     // same with that part's halves
     const int p0 = sub * H;
@@ -148,22 +161,23 @@ __global__ void __launch_bounds__(kRowThreads) k_head_rows(RowArgs a) {
         if (v == 0 && blockIdx.y == 0 && tid == 0) flag(a.status, TS_STATUS_INDEX);
         return;
     }
-    const int rows = a.Hq + a.Hk + a.Hv;
-    const int r_begin = blockIdx.y * a.rows_per_cta, r_end = min(rows, r_begin + a.rows_per_cta);
+    const int part = blockIdx.y - (kind == 0 ? 0 : kind == 1 ? a.groups[0] : a.groups[0] + a.groups[1]);
+    const int r_begin = part * a.per_group[kind], r_end = min(a.heads[kind], r_begin + a.per_group[kind]);
     const size_t node = (size_t)b * n_max + v;
-    const T *qb = (const T *)a.q + node * a.q_stride, *kb = (const T *)a.k + node * a.k_stride, *vb = (const T *)a.v + node * a.v_stride;
     struct Raw {
         uint2 lo, hi;
     };
-    auto load = [&](int r) -> Raw {
-        const T *x = r < a.Hq ? qb + (size_t)r * D : r < a.Hq + a.Hk ? kb + (size_t)(r - a.Hq) * D : vb + (size_t)(r - a.Hq - a.Hk) * D;
-        return Raw{__ldcs(reinterpret_cast<const uint2 *>(x + e0)), __ldcs(reinterpret_cast<const uint2 *>(x + e1))};
+    const T *src = (const T *)a.src[kind] + node * a.stride[kind] + (size_t)(r_begin + slot) * D;
+    auto load = [&]() -> Raw {   // the lane group's next row
+        const Raw u{__ldcs(reinterpret_cast<const uint2 *>(src + e0)), __ldcs(reinterpret_cast<const uint2 *>(src + e1))};
+        src += RPC * D;
+        return u;
     };
     // the first rows' loads are in flight while the angles are formed
     Raw u[kRowsAhead] = {};
 #pragma unroll
     for (int i = 0; i < kRowsAhead; ++i)
-        if (r_begin + slot + i * RPC < r_end) u[i] = load(r_begin + slot + i * RPC);
+        if (r_begin + slot + i * RPC < r_end) u[i] = load();
     if (APPEND) {
         if (tid == 0) bad_s = 0;
         __syncthreads();
@@ -173,7 +187,7 @@ __global__ void __launch_bounds__(kRowThreads) k_head_rows(RowArgs a) {
             if (page < 0 || page >= a.pg.num_pages) bad_s = 1;
         }
     }
-    if (tid < half) {
+    if (tid < half && kind < 2) {
         constexpr double kTwoPi = 6.283185307179586476925;
         const double ang = (double)a.t.pos[(size_t)b * n_max + dfs] * (double)a.inv_freq[tid];
         const float r = (float)fma(-kTwoPi, rint(ang * (1.0 / kTwoPi)), ang);
@@ -186,25 +200,51 @@ __global__ void __launch_bounds__(kRowThreads) k_head_rows(RowArgs a) {
         if (v == 0 && blockIdx.y == 0 && tid == 0) flag(a.status, TS_STATUS_INDEX);
         return;
     }
-    long long row0 = 0, hs = 0;
-    if (APPEND) {   // cache row of head 0; head h is h * hs rows further
-        row0 = cache_row(a.pg, b, 0, a.Hv, a.L_max, P + dfs);
-        hs = a.pg.bt ? TS_PAGE_KEYS : a.L_max;
-    }
-    // weights and rotation of the lane's pairs (p, q), two pairs a vector:
-    // p -> inv * (p * pc - q * qs), q -> inv * (q * qc + p * ps)
-    float2 pc[H / 2], qs[H / 2], qc[H / 2], ps[H / 2];
-    int kind = -1;
-    // the rows of a warp's lane groups go together (none of them leaves early), so every shuffle is the whole warp's
-    for (int base = r_begin + slot, first = r_begin + slot / RW * RW; first < r_end; base += kRowsAhead * RPC, first += kRowsAhead * RPC) {
+    auto rows = [&](auto kind_c) {
+        constexpr int KIND = decltype(kind_c)::value;
+        constexpr bool TURN = KIND < 2, QUANT = APPEND && KIND > 0;
+        // weights and rotation of the lane's pairs (p, q), two pairs a vector:
+        // p -> inv * (p * pc + q * qs), q -> inv * (q * qc + p * ps)
+        float2 pc[H / 2], qs[H / 2], qc[H / 2], ps[H / 2];
+        if constexpr (TURN) {
+            const float *wp = a.weight[KIND];
+            float w[4][H];
 #pragma unroll
-        for (int i = 0; i < kRowsAhead; ++i) {
-            const int r = base + i * RPC, f = first + i * RPC;   // this group's row, the warp's first
-            if (f >= r_end) break;
-            const int is = r < a.Hq ? 0 : r < a.Hq + a.Hk ? 1 : 2;   // query, key, value
-            const int h = is == 0 ? r : is == 1 ? r - a.Hq : r - a.Hq - a.Hk;
-            float2 x[H / 2], y[H / 2];   // first and second members
-            {
+            for (int e = 0; e < H; ++e) {
+                const float2 c = turned ? cs_s[p0 + e] : make_float2(1.f, 0.f);
+                const float wx = wp ? __ldg(wp + (INTER ? e0 + 2 * e : e0 + e)) : 1.f;
+                const float wy = wp ? __ldg(wp + (INTER ? e0 + 2 * e + 1 : e1 + e)) : 1.f;
+                w[0][e] = wx * c.x;
+                w[1][e] = -wy * c.y;
+                w[2][e] = wy * c.x;
+                w[3][e] = wx * c.y;
+            }
+#pragma unroll
+            for (int e = 0; e < H / 2; ++e) {
+                pc[e] = make_float2(w[0][2 * e], w[0][2 * e + 1]);
+                qs[e] = make_float2(w[1][2 * e], w[1][2 * e + 1]);
+                qc[e] = make_float2(w[2][2 * e], w[2][2 * e + 1]);
+                ps[e] = make_float2(w[3][2 * e], w[3][2 * e + 1]);
+            }
+        }
+        // where the lane group's first row goes: values, or codes and a scale
+        T *out = nullptr;
+        uint8_t *codes = nullptr;
+        float *scales = nullptr;
+        long long hs = 0;   // cache rows from one head to the next
+        if constexpr (QUANT) {
+            const long long row = cache_row(a.pg, b, r_begin + slot, a.heads[KIND], a.L_max, P + dfs);
+            hs = a.pg.bt ? TS_PAGE_KEYS : a.L_max;
+            codes = a.codes[KIND - 1] + (size_t)row * D;
+            scales = a.scales[KIND - 1] + row;
+        } else {
+            out = (T *)a.out[KIND] + (node * a.heads[KIND] + r_begin + slot) * D;
+        }
+        // the rows of a warp's lane groups go together (none of them leaves early), so every shuffle is the whole warp's
+        for (int r = r_begin + slot, first = r_begin + slot / RW * RW; first < r_end;) {
+#pragma unroll
+            for (int i = 0; i < kRowsAhead; ++i, r += RPC, first += RPC) {   // this group's row, the warp's first
+                if (first >= r_end) break;
                 float2 t[H];
                 if constexpr (sizeof(T) == 2) {
                     t[0] = Two<T>::get(u[i].lo.x);
@@ -215,111 +255,101 @@ __global__ void __launch_bounds__(kRowThreads) k_head_rows(RowArgs a) {
                     t[0] = Two<T>::get(u[i].lo);
                     t[1] = Two<T>::get(u[i].hi);
                 }
-                pairs<H, INTER>(t, x, y);
-            }
-            const int nr = r + kRowsAhead * RPC;   // this group's next row
-            if (nr < r_end) u[i] = load(nr);
-            if (is != kind) {
-                kind = is;
-                const float *wp = is == 0 ? a.q_weight : is == 1 ? a.k_weight : nullptr;
-                float w[4][H];
+                if (r + kRowsAhead * RPC < r_end) u[i] = load();
+                if (TURN && (a.norm || half)) {
+                    float2 x[H / 2], y[H / 2];   // first and second members
+                    pairs<H, INTER>(t, x, y);
+                    if (a.norm) {
+                        float2 s2 = make_float2(0.f, 0.f);
 #pragma unroll
-                for (int e = 0; e < H; ++e) {
-                    const float2 c = turned && is < 2 ? cs_s[p0 + e] : make_float2(1.f, 0.f);
-                    const float wx = wp ? __ldg(wp + (INTER ? e0 + 2 * e : e0 + e)) : 1.f;
-                    const float wy = wp ? __ldg(wp + (INTER ? e0 + 2 * e + 1 : e1 + e)) : 1.f;
-                    w[0][e] = wx * c.x;
-                    w[1][e] = -wy * c.y;
-                    w[2][e] = wy * c.x;
-                    w[3][e] = wx * c.y;
+                        for (int e = 0; e < H / 2; ++e) s2 = __ffma2_rn(y[e], y[e], __ffma2_rn(x[e], x[e], s2));
+                        float ss = s2.x + s2.y;
+#pragma unroll
+                        for (int o = LPR / 2; o; o >>= 1) ss += __shfl_xor_sync(~0u, ss, o);
+                        const float inv = rsqrtf(ss * (1.f / D) + a.eps);
+#pragma unroll
+                        for (int e = 0; e < H / 2; ++e) {
+                            x[e] = __fmul2_rn(x[e], make_float2(inv, inv));
+                            y[e] = __fmul2_rn(y[e], make_float2(inv, inv));
+                        }
+                    }
+#pragma unroll
+                    for (int e = 0; e < H / 2; ++e) {
+                        const float2 p = x[e], q = y[e];
+                        x[e] = __fmul2_rn(p, pc[e]);
+                        y[e] = __fmul2_rn(q, qc[e]);
+                        if (turned) {   // an unrotated pair's members keep apart, an infinity in one of them too
+                            x[e] = __ffma2_rn(q, qs[e], x[e]);
+                            y[e] = __ffma2_rn(p, ps[e], y[e]);
+                        }
+                    }
+                    unpairs<H, INTER>(x, y, t);
                 }
+                if constexpr (QUANT) {
+                    float top = 0.f;
 #pragma unroll
-                for (int e = 0; e < H / 2; ++e) {
-                    pc[e] = make_float2(w[0][2 * e], w[0][2 * e + 1]);
-                    qs[e] = make_float2(w[1][2 * e], w[1][2 * e + 1]);
-                    qc[e] = make_float2(w[2][2 * e], w[2][2 * e + 1]);
-                    ps[e] = make_float2(w[3][2 * e], w[3][2 * e + 1]);
-                }
-            }
-            float inv = 1.f;
-            if (a.norm && f < a.Hq + a.Hk) {   // not for a warp of value rows
-                float2 s2 = make_float2(0.f, 0.f);
+                    for (int e = 0; e < H; ++e) top = max_abs(top, t[e].x, t[e].y);
 #pragma unroll
-                for (int e = 0; e < H / 2; ++e) s2 = __ffma2_rn(y[e], y[e], __ffma2_rn(x[e], x[e], s2));
-                float ss = s2.x + s2.y;
+                    for (int o = LPR / 2; o; o >>= 1) top = max_nan(top, __shfl_xor_sync(~0u, top, o));
+                    if (r < r_end) {
+                        const bool fine = top <= 3.402823466e38f;   // false for infinities and NaN
+                        const float scale = fmaxf(__fdiv_rn(top, kFp8Max), kScaleMin);
+                        const float rs = __frcp_rn(scale);
+                        uint32_t c[H];   // two codes each
 #pragma unroll
-                for (int o = LPR / 2; o; o >>= 1) ss += __shfl_xor_sync(~0u, ss, o);
-                if (is < 2) inv = rsqrtf(ss * (1.f / D) + a.eps);
-            }
-            if (is < 2) {
-                const float2 i2 = make_float2(inv, inv);
-#pragma unroll
-                for (int e = 0; e < H / 2; ++e) {
-                    const float2 p = __fmul2_rn(x[e], i2), q = __fmul2_rn(y[e], i2);
-                    x[e] = __ffma2_rn(q, qs[e], __fmul2_rn(p, pc[e]));
-                    y[e] = __ffma2_rn(p, ps[e], __fmul2_rn(q, qc[e]));
-                }
-            }
-            float2 t[H];
-            unpairs<H, INTER>(x, y, t);
-            float top = 0.f;
-            if (APPEND && f + RW > a.Hq) {   // some row of the warp is quantised
-#pragma unroll
-                for (int e = 0; e < H; ++e) top = max_nan(top, max_nan(fabsf(t[e].x), fabsf(t[e].y)));
-#pragma unroll
-                for (int o = LPR / 2; o; o >>= 1) top = max_nan(top, __shfl_xor_sync(~0u, top, o));
-            }
-            if (r >= r_end) continue;
-            if (is == 0 || !APPEND) {
-                T *o = is == 0 ? (T *)a.q_out + (node * a.Hq + h) * D : (T *)a.k_out + (node * a.Hk + h) * D;
-                uint2 lo, hi;
-                if constexpr (sizeof(T) == 2) {
-                    lo = make_uint2(Two<T>::put(t[0]), Two<T>::put(t[1]));
-                    hi = make_uint2(Two<T>::put(t[2]), Two<T>::put(t[3]));
+                        for (int e = 0; e < H; ++e)
+                            c[e] = __nv_cvt_float2_to_fp8x2(__fmul2_rn(t[e], make_float2(rs, rs)), __NV_SATFINITE, __NV_E4M3);
+                        if constexpr (sizeof(T) == 2) {
+                            *reinterpret_cast<uint32_t *>(codes + e0) = fine ? c[0] | c[1] << 16 : 0u;
+                            *reinterpret_cast<uint32_t *>(codes + e1) = fine ? c[2] | c[3] << 16 : 0u;
+                        } else {
+                            *reinterpret_cast<uint16_t *>(codes + e0) = (uint16_t)(fine ? c[0] : 0u);
+                            *reinterpret_cast<uint16_t *>(codes + e1) = (uint16_t)(fine ? c[1] : 0u);
+                        }
+                        if (sub == 0) {
+                            *scales = fine ? scale : __int_as_float(0x7fc00000);
+                            if (!fine) flag(a.status, TS_STATUS_NONFINITE);
+                        }
+                    }
+                    codes += RPC * hs * D;
+                    scales += RPC * hs;
                 } else {
-                    lo = Two<T>::put(t[0]);
-                    hi = Two<T>::put(t[1]);
-                }
-                *reinterpret_cast<uint2 *>(o + e0) = lo;
-                *reinterpret_cast<uint2 *>(o + e1) = hi;
-            } else {
-                const bool fine = top <= 3.402823466e38f;   // false for infinities and NaN
-                const float scale = fmaxf(__fdiv_rn(top, kFp8Max), kScaleMin);
-                const float rs = __frcp_rn(scale);
-                uint32_t c[H];   // two codes each
-#pragma unroll
-                for (int e = 0; e < H; ++e)
-                    c[e] = fine ? __nv_cvt_float2_to_fp8x2(__fmul2_rn(t[e], make_float2(rs, rs)), __NV_SATFINITE, __NV_E4M3) : 0u;
-                const size_t row = (size_t)(row0 + h * hs);
-                uint8_t *dst = (is == 2 ? a.v8 : a.k8) + row * D;
-                if constexpr (sizeof(T) == 2) {
-                    *reinterpret_cast<uint32_t *>(dst + e0) = c[0] | c[1] << 16;
-                    *reinterpret_cast<uint32_t *>(dst + e1) = c[2] | c[3] << 16;
-                } else {
-                    *reinterpret_cast<uint16_t *>(dst + e0) = (uint16_t)c[0];
-                    *reinterpret_cast<uint16_t *>(dst + e1) = (uint16_t)c[1];
-                }
-                if (sub == 0) {
-                    (is == 2 ? a.v_scale : a.k_scale)[row] = fine ? scale : __int_as_float(0x7fc00000);
-                    if (!fine) flag(a.status, TS_STATUS_NONFINITE);
+                    if (r < r_end) {
+                        uint2 lo, hi;
+                        if constexpr (sizeof(T) == 2) {
+                            lo = make_uint2(Two<T>::put(t[0]), Two<T>::put(t[1]));
+                            hi = make_uint2(Two<T>::put(t[2]), Two<T>::put(t[3]));
+                        } else {
+                            lo = Two<T>::put(t[0]);
+                            hi = Two<T>::put(t[1]);
+                        }
+                        *reinterpret_cast<uint2 *>(out + e0) = lo;
+                        *reinterpret_cast<uint2 *>(out + e1) = hi;
+                    }
+                    out += RPC * D;
                 }
             }
         }
-    }
+    };
+    if (kind == 0) rows(std::integral_constant<int, 0>());
+    else if (kind == 1) rows(std::integral_constant<int, 1>());
+    else if constexpr (APPEND) rows(std::integral_constant<int, 2>());
 }
 
 template <typename T, int D, bool APPEND>
 cudaError_t rows_launch(RowArgs &a, cudaStream_t s) {
     constexpr int RPC = kRowThreads / (D * (int)sizeof(T) / 16);
-    const int rows = a.Hq + a.Hk + a.Hv;
     const long long nodes = (long long)a.t.B * a.t.n_max;
-    // heads of a node are split over CTAs only while that gives each SM more to do
-    long long groups = 2LL * num_sms() / nodes;
-    const int most = (rows + RPC - 1) / RPC;
-    if (groups > most) groups = most;
-    if (groups < 1) groups = 1;
-    a.rows_per_cta = ((rows + (int)groups - 1) / (int)groups + RPC - 1) / RPC * RPC;
-    const dim3 grid((unsigned)nodes, (rows + a.rows_per_cta - 1) / a.rows_per_cta);
+    // a projection's heads are split over CTAs only while that gives each SM more to do
+    int ctas = 0;
+    for (int i = 0; i < 3; ++i) {
+        const int most = (a.heads[i] + RPC - 1) / RPC;
+        int groups = (int)std::max(1LL, std::min<long long>(most, num_sms() / nodes));
+        a.per_group[i] = ((a.heads[i] + groups - 1) / groups + RPC - 1) / RPC * RPC;
+        a.groups[i] = a.heads[i] ? (a.heads[i] + a.per_group[i] - 1) / a.per_group[i] : 0;
+        ctas += a.groups[i];
+    }
+    const dim3 grid((unsigned)nodes, ctas);
     if (a.interleaved) return launch(k_head_rows<T, D, APPEND, true>, grid, dim3(kRowThreads), 0, s, a);
     return launch(k_head_rows<T, D, APPEND, false>, grid, dim3(kRowThreads), 0, s, a);
 }
@@ -333,8 +363,8 @@ cudaError_t rows_dispatch(RowArgs &a, int d, ts_dtype dt, cudaStream_t s) {
 
 void set_rope(RowArgs &a, const ts_qk_rope &r) {
     a.inv_freq = r.inv_freq;
-    a.q_weight = r.q_weight;
-    a.k_weight = r.k_weight;
+    a.weight[0] = r.q_weight;
+    a.weight[1] = r.k_weight;
     a.eps = r.eps;
     a.norm = r.norm != 0;
     a.rot_dim = r.rot_dim;
@@ -497,14 +527,14 @@ cudaError_t launch_qk_norm_rope(void *q_out, void *k_out, const void *q, const v
                                 long long q_stride, long long k_stride, const ts_qk_rope &rope, const ts_tree &t,
                                 ts_dtype dt, cudaStream_t s) {
     RowArgs a = {};
-    a.q = q;
-    a.k = k;
-    a.q_stride = q_stride;
-    a.k_stride = k_stride;
-    a.q_out = q_out;
-    a.k_out = k_out;
-    a.Hq = Hq;
-    a.Hk = Hk;
+    a.src[0] = q;
+    a.src[1] = k;
+    a.stride[0] = q_stride;
+    a.stride[1] = k_stride;
+    a.out[0] = q_out;
+    a.out[1] = k_out;
+    a.heads[0] = Hq;
+    a.heads[1] = Hk;
     set_rope(a, rope);
     a.t = t;
     return rows_dispatch<false>(a, d, dt, s);
@@ -515,22 +545,21 @@ cudaError_t launch_kv8_append(const ts_kv8 &kv, const void *k_new, const void *v
                               long long q_stride, const int32_t *prefix_len, const ts_tree &t, ts_dtype dt,
                               uint32_t *status, cudaStream_t s) {
     RowArgs a = {};
-    a.q = q;
-    a.k = k_new;
-    a.v = v_new;
-    a.q_stride = q_stride;
-    a.k_stride = k_stride;
-    a.v_stride = v_stride;
-    a.q_out = q_out;
-    a.Hq = Hq;
-    a.Hk = kv.H;
-    a.Hv = kv.H;
+    a.src[0] = q;
+    a.src[1] = k_new;
+    a.src[2] = v_new;
+    a.stride[0] = q_stride;
+    a.stride[1] = k_stride;
+    a.stride[2] = v_stride;
+    a.out[0] = q_out;
+    a.heads[0] = Hq;
+    a.heads[1] = a.heads[2] = kv.H;
     if (rope) set_rope(a, *rope);
     a.t = t;
-    a.k8 = kv.k;
-    a.v8 = kv.v;
-    a.k_scale = kv.k_scale;
-    a.v_scale = kv.v_scale;
+    a.codes[0] = kv.k;
+    a.codes[1] = kv.v;
+    a.scales[0] = kv.k_scale;
+    a.scales[1] = kv.v_scale;
     a.prefix_len = prefix_len;
     a.L_max = kv8_rows(kv);
     a.pg = kv8_pages(kv);
