@@ -64,6 +64,11 @@ __device__ __forceinline__ float max_abs(float a, float b, float c) {
     return y;
 }
 
+__device__ __forceinline__ void cp_async16(void *dst, const void *src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
 // ---- norm, rotation, quantised append ---------------------------------------
 struct RowArgs {
     // by projection: queries, keys, values (0 heads leave one out)
@@ -85,7 +90,7 @@ struct RowArgs {
     uint32_t *status;
 };
 
-constexpr int kRowThreads = 128, kRowsAhead = 4;
+constexpr int kRowThreads = 128, kRowPasses = 8;   // rows of a CTA: kRowPasses a lane group, 16 KB
 
 // Two values of a row as one 4-byte (bf16) or 8-byte (fp32) piece.
 template <typename T>
@@ -133,12 +138,16 @@ __device__ __forceinline__ void unpairs(const float2 (&x)[H / 2], const float2 (
 // over the CTA's rows. The angles are formed once per CTA: position times
 // frequency and its remainder by 2 pi in fp64 (an fp32 product at position
 // 131072 is off by up to 4e-3), then sincosf of the fp32 remainder. Each value
-// is read once and written once; kRowsAhead rows a lane group are in flight.
+// is read once and written once, all of a CTA's rows in flight from its start
+// (into shared memory; in registers, four rows a lane group ahead, they cost
+// more occupancy than they hid: 51 us against 46 on an append of 64 x 47 nodes, 56 + 56 heads of 128).
 // What bounds a large call next to memory is issuing: the loop is compiled once
 // for each kind of row (query, key, value), and a CTA runs one of them.
 template <typename T, int D, bool APPEND, bool INTER>
 __global__ void __launch_bounds__(kRowThreads) k_head_rows(RowArgs a) {
     constexpr int E = 16 / (int)sizeof(T), LPR = D / E, RPC = kRowThreads / LPR, RW = 32 / LPR, H = E / 2;
+    constexpr int ROW = D * (int)sizeof(T);   // bytes
+    __shared__ __align__(16) uint8_t rows_s[kRowPasses * RPC * ROW];
     __shared__ float2 cs_s[D / 2];
     __shared__ int bad_s;
     const int n_max = a.t.n_max, b = blockIdx.x / n_max, v = blockIdx.x - b * n_max;
@@ -164,20 +173,11 @@ __global__ void __launch_bounds__(kRowThreads) k_head_rows(RowArgs a) {
     const int part = blockIdx.y - (kind == 0 ? 0 : kind == 1 ? a.groups[0] : a.groups[0] + a.groups[1]);
     const int r_begin = part * a.per_group[kind], r_end = min(a.heads[kind], r_begin + a.per_group[kind]);
     const size_t node = (size_t)b * n_max + v;
-    struct Raw {
-        uint2 lo, hi;
-    };
-    const T *src = (const T *)a.src[kind] + node * a.stride[kind] + (size_t)(r_begin + slot) * D;
-    auto load = [&]() -> Raw {   // the lane group's next row
-        const Raw u{__ldcs(reinterpret_cast<const uint2 *>(src + e0)), __ldcs(reinterpret_cast<const uint2 *>(src + e1))};
-        src += RPC * D;
-        return u;
-    };
-    // the first rows' loads are in flight while the angles are formed
-    Raw u[kRowsAhead] = {};
+    const T *src = (const T *)a.src[kind] + node * a.stride[kind] + (size_t)(r_begin + slot) * D + sub * E;
+    uint8_t *mine = rows_s + slot * ROW;
 #pragma unroll
-    for (int i = 0; i < kRowsAhead; ++i)
-        if (r_begin + slot + i * RPC < r_end) u[i] = load();
+    for (int i = 0; i < kRowPasses; ++i)
+        if (r_begin + slot + i * RPC < r_end) cp_async16(mine + i * RPC * ROW + sub * 16, src + i * RPC * D);
     if (APPEND) {
         if (tid == 0) bad_s = 0;
         __syncthreads();
@@ -195,6 +195,7 @@ __global__ void __launch_bounds__(kRowThreads) k_head_rows(RowArgs a) {
         sincosf(r, &sn, &c);
         cs_s[tid] = make_float2(c, sn);
     }
+    cp_async_wait_all();
     __syncthreads();
     if (APPEND && bad_s) {
         if (v == 0 && blockIdx.y == 0 && tid == 0) flag(a.status, TS_STATUS_INDEX);
@@ -241,21 +242,23 @@ __global__ void __launch_bounds__(kRowThreads) k_head_rows(RowArgs a) {
             out = (T *)a.out[KIND] + (node * a.heads[KIND] + r_begin + slot) * D;
         }
         // the rows of a warp's lane groups go together (none of them leaves early), so every shuffle is the whole warp's
-        for (int r = r_begin + slot, first = r_begin + slot / RW * RW; first < r_end;) {
-#pragma unroll
-            for (int i = 0; i < kRowsAhead; ++i, r += RPC, first += RPC) {   // this group's row, the warp's first
-                if (first >= r_end) break;
+        const T *in = reinterpret_cast<const T *>(mine);
+        // r: this group's row, first: the warp's first
+#pragma unroll 1
+        for (int r = r_begin + slot, first = r_begin + slot / RW * RW; first < r_end; r += RPC, first += RPC) {
+            {
                 float2 t[H];
+                const uint2 lo = *reinterpret_cast<const uint2 *>(in + e0), hi = *reinterpret_cast<const uint2 *>(in + e1);
+                in += RPC * D;
                 if constexpr (sizeof(T) == 2) {
-                    t[0] = Two<T>::get(u[i].lo.x);
-                    t[1] = Two<T>::get(u[i].lo.y);
-                    t[2] = Two<T>::get(u[i].hi.x);
-                    t[3] = Two<T>::get(u[i].hi.y);
+                    t[0] = Two<T>::get(lo.x);
+                    t[1] = Two<T>::get(lo.y);
+                    t[2] = Two<T>::get(hi.x);
+                    t[3] = Two<T>::get(hi.y);
                 } else {
-                    t[0] = Two<T>::get(u[i].lo);
-                    t[1] = Two<T>::get(u[i].hi);
+                    t[0] = Two<T>::get(lo);
+                    t[1] = Two<T>::get(hi);
                 }
-                if (r + kRowsAhead * RPC < r_end) u[i] = load();
                 if (TURN && (a.norm || half)) {
                     float2 x[H / 2], y[H / 2];   // first and second members
                     pairs<H, INTER>(t, x, y);
@@ -344,7 +347,8 @@ cudaError_t rows_launch(RowArgs &a, cudaStream_t s) {
     int ctas = 0;
     for (int i = 0; i < 3; ++i) {
         const int most = (a.heads[i] + RPC - 1) / RPC;
-        int groups = (int)std::max(1LL, std::min<long long>(most, num_sms() / nodes));
+        const int least = (most + kRowPasses - 1) / kRowPasses;
+        const int groups = (int)std::max<long long>(least, std::min<long long>(most, num_sms() / nodes));
         a.per_group[i] = ((a.heads[i] + groups - 1) / groups + RPC - 1) / RPC * RPC;
         a.groups[i] = a.heads[i] ? (a.heads[i] + a.per_group[i] - 1) / a.per_group[i] : 0;
         ctas += a.groups[i];
