@@ -384,6 +384,10 @@ __global__ void __launch_bounds__(Cfg8<D, RP>::THREADS, 1)
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
 
+    if (tid < 2) {
+        const CUtensorMap *map = tid ? &map_v : &map_k;
+        asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
+    }
     pdl_wait();   // nothing above touches global memory
     pdl_trigger();
 
@@ -408,23 +412,32 @@ __global__ void __launch_bounds__(Cfg8<D, RP>::THREADS, 1)
         // How far to cut: lane i tries parts of at most 1 / (i + 1) of the longest item. Items of one length take
         // as many rounds over the SMs as they have units; others, handed out longest first, about their sum over
         // the SMs and half a longest unit. Cut items have to fit the slots.
-        int longest = 0, same = 1;
+        int longest = 0, same = 1;   // same: tiles and row blocks of every request
+        const int4 rq0 = req_s[0];
+        const int blocks0 = blocks_of(rq0.x);
 #pragma unroll 1
         for (int b = lane; b < B; b += 32) {
-            longest = max(longest, req_s[b].z);
-            same &= req_s[b].z == req_s[0].z;
+            const int4 rq = req_s[b];
+            longest = max(longest, rq.z);
+            same &= rq.z == rq0.z && blocks_of(rq.x) == blocks0;
         }
         longest = __reduce_max_sync(~0u, longest);
         same = __all_sync(~0u, same);
         const float per = fmaxf((float)kMinCut, ceilf((float)longest / (lane + 1))), rate = __frcp_rn(per);
+        auto parts_of = [](int tiles, float rate) { return fminf(ceilf(tiles * rate), (float)kMaxCuts); };
         float work = 0.f, units = 0.f, cut = 0.f;
-#pragma unroll 2
-        for (int b = 0; b < B; ++b) {
+#pragma unroll 1
+        for (int b = 0; b < (same ? 1 : B); ++b) {
             const int4 rq = req_s[b];
-            const float items = (float)(a.H * blocks_of(rq.x)), parts = fminf(ceilf(rq.z * rate), (float)kMaxCuts);
+            const float items = (float)(a.H * blocks_of(rq.x)), parts = parts_of(rq.z, rate);
             work += items * rq.z;
             units += items * parts;
             cut += parts > 1.f ? items * parts : 0.f;
+        }
+        if (same) {
+            work *= B;
+            units *= B;
+            cut *= B;
         }
         const float all = work + units * kUnitCost, sms = (float)gridDim.x;
         float cost = fmaxf(per + kUnitCost, same ? ceilf(units / sms) * all / fmaxf(units, 1.f) : all / sms + 0.5f * per) +
@@ -434,55 +447,63 @@ __global__ void __launch_bounds__(Cfg8<D, RP>::THREADS, 1)
         const uint32_t least = __reduce_min_sync(~0u, __float_as_uint(cost));
         const int pick = __ffs(__ballot_sync(~0u, __float_as_uint(cost) == least)) - 1;
         const float pick_rate = __shfl_sync(~0u, rate, pick);
+        int nu = 0, ns = 0;
+        if (same) {
+            const int parts = max(1, (int)parts_of(rq0.z, pick_rate)), u = rq0.z ? a.H * blocks0 * parts : 0;
 #pragma unroll 1
-        for (int b = lane; b < B; b += 32) {
-            const int tl = req_s[b].z, parts = max(1, (int)fminf(ceilf(tl * pick_rate), (float)kMaxCuts));
-            req_s[b].w = parts;
-            key_s[b] = parts > 1 ? (tl + parts - 1) / parts : tl;
-        }
-        __syncwarp();
-        // requests by the length of their parts, longest first
+            for (int b = lane; b < B; b += 32) {
+                req_s[b].w = parts;
+                order_s[b] = b;
+                unit_s[b] = b * u;
+                slot_s[b] = parts > 1 ? b * u : 0;
+            }
+            nu = B * u;
+        } else {
 #pragma unroll 1
-        for (int b = lane; b < B; b += 32) {
-            int rank = 0;
-            if (same) {
-                rank = b;
-            } else {
+            for (int b = lane; b < B; b += 32) {
+                const int tl = req_s[b].z, parts = max(1, (int)parts_of(tl, pick_rate));
+                req_s[b].w = parts;
+                key_s[b] = parts > 1 ? (tl + parts - 1) / parts : tl;
+            }
+            __syncwarp();
+            // requests by the length of their parts, longest first
+#pragma unroll 1
+            for (int b = lane; b < B; b += 32) {
+                int rank = 0;
                 const int mine = key_s[b];
 #pragma unroll 4
                 for (int o = 0; o < B; ++o) {
                     const int ko = key_s[o];
                     rank += ko > mine || (ko == mine && o < b);
                 }
+                order_s[rank] = b;
             }
-            order_s[rank] = b;
-        }
-        __syncwarp();
-        // exclusive sums of units and of slots, in that order
-        int nu = 0, ns = 0;
+            __syncwarp();
+            // exclusive sums of units and of slots, in that order
 #pragma unroll 1
-        for (int r0 = 0; r0 < B; r0 += 32) {
-            int u = 0, c = 0;
-            if (r0 + lane < B) {
-                const int4 rq = req_s[order_s[r0 + lane]];
-                if (rq.z) u = a.H * blocks_of(rq.x) * rq.w;
-                if (rq.w > 1) c = u;
-            }
-            int cu = u, cc = c;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int tu = __shfl_up_sync(~0u, cu, o), tc = __shfl_up_sync(~0u, cc, o);
-                if (lane >= o) {
-                    cu += tu;
-                    cc += tc;
+            for (int r0 = 0; r0 < B; r0 += 32) {
+                int u = 0, c = 0;
+                if (r0 + lane < B) {
+                    const int4 rq = req_s[order_s[r0 + lane]];
+                    if (rq.z) u = a.H * blocks_of(rq.x) * rq.w;
+                    if (rq.w > 1) c = u;
                 }
+                int cu = u, cc = c;
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const int tu = __shfl_up_sync(~0u, cu, o), tc = __shfl_up_sync(~0u, cc, o);
+                    if (lane >= o) {
+                        cu += tu;
+                        cc += tc;
+                    }
+                }
+                if (r0 + lane < B) {
+                    unit_s[r0 + lane] = nu + cu - u;
+                    slot_s[r0 + lane] = ns + cc - c;
+                }
+                nu += __shfl_sync(~0u, cu, 31);
+                ns += __shfl_sync(~0u, cc, 31);
             }
-            if (r0 + lane < B) {
-                unit_s[r0 + lane] = nu + cu - u;
-                slot_s[r0 + lane] = ns + cc - c;
-            }
-            nu += __shfl_sync(~0u, cu, 31);
-            ns += __shfl_sync(~0u, cc, 31);
         }
         if (lane == 0) misc[2] = nu;
     }
@@ -569,8 +590,9 @@ __global__ void __launch_bounds__(Cfg8<D, RP>::THREADS, 1)
 #pragma unroll 1
         while (more) {
             // the next unit is taken kClaimAhead tiles before this one's last load, late enough that CTAs share the
-            // last units evenly, early enough that its query rows are staged in time
-            const int claim = max(u.j1 - kClaimAhead, u.j0);
+            // last units evenly, early enough that its query rows are staged in time; the queue's answer, which
+            // takes up to 2 us while every SM loads, is waited for three loads later
+            const int claim = max(u.j1 - kClaimAhead, u.j0), answer = min(claim + 3, u.j1);
             int qn = 0;
             const int L = u.P + u.n;
             const int strip = (u.b * a.H + u.h) * a.rows;   // dense: the cache row of key 0
@@ -580,7 +602,7 @@ __global__ void __launch_bounds__(Cfg8<D, RP>::THREADS, 1)
                     qn = ticket >= 0 ? ticket : next();
                     ticket = -1;
                 }
-                if (j == min(claim + 1, u.j1)) {
+                if (j == answer) {
                     more = publish(__shfl_sync(~0u, qn, 0), un);
                     if (!ok) break;
                 }
