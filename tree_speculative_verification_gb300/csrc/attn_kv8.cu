@@ -682,8 +682,8 @@ __global__ void __launch_bounds__(Cfg8<D, RP>::THREADS, 1)
 #pragma unroll 1
                 for (int j = u.j0; j < u.j1; ++j, ++g) {
                     const int st = g % C::STAGES, x = g & 1;
-                    // the product of tile g - 2 is done: S(g - 2) was read and P(g - 2) is free, for who waits for S(g)
-                    if ((g >= 2 && !wait1(pvdone + 8 * x, (uint32_t)((g - 2) >> 1) & 1u)) ||
+                    // once the probabilities of tile g - 2 are there S(g - 2) has been read; their product need not be done
+                    if ((g >= 2 && !wait1(pfull + 8 * x, (uint32_t)((g - 2) >> 1) & 1u)) ||
                         !wait1(full + 8 * st, (uint32_t)(g / C::STAGES) & 1u)) {
                         ok = false;
                         break;
@@ -856,6 +856,8 @@ __global__ void __launch_bounds__(Cfg8<D, RP>::THREADS, 1)
                 return fmaxf(top, top2);
             };
             auto write_p = [&](const float2 (&y)[CG / 2], float vs) {
+                // the product of tile g - 2 has read the probabilities there were
+                if (g >= 2 && ok && !wait_warp(pvdone + 8 * (g & 1), (uint32_t)((g - 2) >> 1) & 1u)) ok = false;
                 const float2 rv = make_float2(vs * iref, vs * iref);
                 const uint32_t pd = fix_base + C::FIX_P + (g & 1) * C::P_BYTES + kslot * 64;
                 const int flip = (kslot >> 1) & 3;
