@@ -213,7 +213,7 @@ constexpr int kMinCut = 3;         // tiles of a part at least
 constexpr int kSlotsPerSm = 12;    // parts of cut items there is room for
 constexpr float kUnitCost = 5.f, kJoinCost = 6.f;   // of a unit beside its tiles, and of joining parts, in tiles
 constexpr int kRing = 4;           // published units
-constexpr int kClaimAhead = 8;     // tiles
+constexpr int kClaimAhead = 10;    // tiles
 
 template <int D_, int RP_>
 struct Cfg8 {
@@ -244,7 +244,7 @@ struct Cfg8 {
     static constexpr int FIX_ORDER = FIX_KEY + kReqCache * 4;  // by rank: request, first unit, first slot
     static constexpr int FIX_UNIT = FIX_ORDER + kReqCache * 4, FIX_SLOT = FIX_UNIT + kReqCache * 4;
     static constexpr int FIX_INFO = FIX_SLOT + kReqCache * 4;  // units [kRing][12]
-    static constexpr int FIX_MISC = FIX_INFO + kRing * 12 * 4; // 0 TMEM base, 1 timeout, 2 units, 3 last
+    static constexpr int FIX_MISC = FIX_INFO + kRing * 12 * 4; // 0 TMEM base, 1 timeout, 3 last
     static constexpr int FIX_BAR = FIX_MISC + 64;
     static constexpr int FIX_END = FIX_BAR + 64 * 8;
     static constexpr int off_fix(int stages) { return (stages * (STAGE_BYTES + SIDE) + 1023) / 1024 * 1024; }
@@ -342,6 +342,7 @@ __global__ void __launch_bounds__(Cfg8<D, RP>::THREADS, 1)
     int4 *req_s = (int4 *)(fix + C::FIX_REQ);
     int *key_s = (int *)(fix + C::FIX_KEY), *order_s = (int *)(fix + C::FIX_ORDER);
     int *unit_s = (int *)(fix + C::FIX_UNIT), *slot_s = (int *)(fix + C::FIX_SLOT);
+    float *cost_s = (float *)slot_s;   // until the way of cutting is picked
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int B = a.t.B, n_max = a.t.n_max;
@@ -349,6 +350,7 @@ __global__ void __launch_bounds__(Cfg8<D, RP>::THREADS, 1)
     const uint32_t full = fix_base + C::FIX_BAR, empty = full + 8 * C::STAGES, sfull = empty + 8 * C::STAGES;
     const uint32_t pvdone = sfull + 16, pfull = pvdone + 16, qraw = pfull + 16, qready = qraw + 16, qfree = qready + 16;
     const uint32_t fin = qfree + 16, sumfull = fin + 16, odone = sumfull + 16, ofree = odone + 16, iready = ofree + 16, ifree = iready + 8 * kRing;
+    const uint32_t claimgo = ifree + 8 * kRing;
 
     if (warp == 2) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32((void *)misc)),
@@ -380,6 +382,7 @@ __global__ void __launch_bounds__(Cfg8<D, RP>::THREADS, 1)
             mbar_init(iready + 8 * r, 1);
             mbar_init(ifree + 8 * r, 3 + C::SM_WARPS + 4);
         }
+        mbar_init(claimgo, 1);
         misc[1] = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -394,165 +397,60 @@ __global__ void __launch_bounds__(Cfg8<D, RP>::THREADS, 1)
     // ---- the plan, the same in every CTA: how many tiles a part has, and each
     // request's first unit and first slot of the workspace
     const bool planned = B <= kReqCache;
-    const int blocks_max = (n_max * a.G + RP - 1) / RP;
     auto blocks_of = [&](int n) { return (n * a.G + RP - 1) / RP; };
     auto tiles_of = [&](int n, int P) -> int {   // 0 for a request that is empty or does not fit
         return n > 0 && n <= n_max && P >= 0 && P <= a.rows - n ? (P + n + kTileKeys - 1) / kTileKeys : 0;
     };
+    auto parts_of = [](int tiles, float rate) { return fminf(ceilf(tiles * rate), (float)kMaxCuts); };
+    int ticket = 0;   // the CTA's first place in the queue
+    if (warp == 3 && lane == 0) ticket = (int)atomicAdd(a.queue, 1u);
 #pragma unroll 1
     for (int b = tid; b < B; b += C::THREADS) {
         const int n = a.t.n_nodes[b], P = a.prefix_len[b], tl = tiles_of(n, P);
         if (planned) req_s[b] = make_int4(n, P, tl, 1);
         if (blockIdx.x == 0 && n > 0 && !tl) flag(a.status, TS_STATUS_INDEX);
     }
-    int ticket = 0;   // the CTA's first place in the queue
-    if (warp == 0 && lane == 0) ticket = (int)atomicAdd(a.queue, 1u);
-    __syncthreads();
-    if (planned && warp == 0) {
-        // How far to cut: lane i tries parts of at most 1 / (i + 1) of the longest item. Items of one length take
-        // as many rounds over the SMs as they have units; others, handed out longest first, about their sum over
-        // the SMs and half a longest unit. Cut items have to fit the slots.
-        int longest = 0, same = 1;   // same: tiles and row blocks of every request
-        const int4 rq0 = req_s[0];
-        const int blocks0 = blocks_of(rq0.x);
-#pragma unroll 1
-        for (int b = lane; b < B; b += 32) {
-            const int4 rq = req_s[b];
-            longest = max(longest, rq.z);
-            same &= rq.z == rq0.z && blocks_of(rq.x) == blocks0;
-        }
-        longest = __reduce_max_sync(~0u, longest);
-        same = __all_sync(~0u, same);
-        const float per = fmaxf((float)kMinCut, ceilf((float)longest / (lane + 1))), rate = __frcp_rn(per);
-        auto parts_of = [](int tiles, float rate) { return fminf(ceilf(tiles * rate), (float)kMaxCuts); };
-        float work = 0.f, units = 0.f, cut = 0.f;
-#pragma unroll 1
-        for (int b = 0; b < (same ? 1 : B); ++b) {
-            const int4 rq = req_s[b];
-            const float items = (float)(a.H * blocks_of(rq.x)), parts = parts_of(rq.z, rate);
-            work += items * rq.z;
-            units += items * parts;
-            cut += parts > 1.f ? items * parts : 0.f;
-        }
-        if (same) {
-            work *= B;
-            units *= B;
-            cut *= B;
-        }
-        const float all = work + units * kUnitCost, sms = (float)gridDim.x;
-        float cost = fmaxf(per + kUnitCost, same ? ceilf(units / sms) * all / fmaxf(units, 1.f) : all / sms + 0.5f * per) +
-                     (cut > 0.f ? kJoinCost : 0.f);
-        if (lane > 0 && cut > (float)a.slots) cost = 3e38f;
-        // the lane of the least cost (they are positive: their bits order as they do), the least cutting of equal ones
-        const uint32_t least = __reduce_min_sync(~0u, __float_as_uint(cost));
-        const int pick = __ffs(__ballot_sync(~0u, __float_as_uint(cost) == least)) - 1;
-        const float pick_rate = __shfl_sync(~0u, rate, pick);
-        int nu = 0, ns = 0;
-        if (same) {
-            const int parts = max(1, (int)parts_of(rq0.z, pick_rate)), u = rq0.z ? a.H * blocks0 * parts : 0;
-#pragma unroll 1
-            for (int b = lane; b < B; b += 32) {
-                req_s[b].w = parts;
-                order_s[b] = b;
-                unit_s[b] = b * u;
-                slot_s[b] = parts > 1 ? b * u : 0;
-            }
-            nu = B * u;
-        } else {
-#pragma unroll 1
-            for (int b = lane; b < B; b += 32) {
-                const int tl = req_s[b].z, parts = max(1, (int)parts_of(tl, pick_rate));
-                req_s[b].w = parts;
-                key_s[b] = parts > 1 ? (tl + parts - 1) / parts : tl;
-            }
-            __syncwarp();
-            // requests by the length of their parts, longest first
-#pragma unroll 1
-            for (int b = lane; b < B; b += 32) {
-                int rank = 0;
-                const int mine = key_s[b];
-#pragma unroll 4
-                for (int o = 0; o < B; ++o) {
-                    const int ko = key_s[o];
-                    rank += ko > mine || (ko == mine && o < b);
-                }
-                order_s[rank] = b;
-            }
-            __syncwarp();
-            // exclusive sums of units and of slots, in that order
-#pragma unroll 1
-            for (int r0 = 0; r0 < B; r0 += 32) {
-                int u = 0, c = 0;
-                if (r0 + lane < B) {
-                    const int4 rq = req_s[order_s[r0 + lane]];
-                    if (rq.z) u = a.H * blocks_of(rq.x) * rq.w;
-                    if (rq.w > 1) c = u;
-                }
-                int cu = u, cc = c;
-#pragma unroll
-                for (int o = 1; o < 32; o <<= 1) {
-                    const int tu = __shfl_up_sync(~0u, cu, o), tc = __shfl_up_sync(~0u, cc, o);
-                    if (lane >= o) {
-                        cu += tu;
-                        cc += tc;
-                    }
-                }
-                if (r0 + lane < B) {
-                    unit_s[r0 + lane] = nu + cu - u;
-                    slot_s[r0 + lane] = ns + cc - c;
-                }
-                nu += __shfl_sync(~0u, cu, 31);
-                ns += __shfl_sync(~0u, cc, 31);
-            }
-        }
-        if (lane == 0) misc[2] = nu;
-    }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = (uint32_t)misc[0];
-    const int units = planned ? misc[2] : B * a.H * blocks_max;
-
-    // unit q of the queue; false for one that is empty (requests beyond the planned ones)
-    auto decode = [&](int q, Unit8 &u) -> bool {
-        int first, tl;
-        u.slot = 0;
-        u.parts = 1;
-        if (planned) {
-            int lo = 0, hi = B - 1;   // the last request whose first unit is at most q
+    int longest = 0, same = 1;   // same: tiles and row blocks of every request
+    if (planned) {
+        // How far to cut: parts of at most 1 / (i + 1) of the longest item, a warp trying every i-th (lane = request).
+        // Items of one length take as many rounds over the SMs as they have units; others, handed out longest first,
+        // about their sum over the SMs and half a longest unit. Cut items have to fit the slots.
+        const int4 rq0 = req_s[0];
 #pragma unroll 1
-            while (lo < hi) {
-                const int mid = (lo + hi + 1) >> 1;
-                if (unit_s[mid] <= q) lo = mid;
-                else hi = mid - 1;
-            }
-            u.b = order_s[lo];
-            first = unit_s[lo];
-            u.slot = slot_s[lo];
-            const int4 rq = req_s[u.b];
-            u.n = rq.x;
-            u.P = rq.y;
-            tl = rq.z;
-            u.parts = rq.w;
-        } else {
-            u.b = q / (a.H * blocks_max);
-            first = u.b * a.H * blocks_max;
-            u.n = a.t.n_nodes[u.b];
-            u.P = a.prefix_len[u.b];
-            tl = tiles_of(u.n, u.P);
+        for (int b = lane; b < B; b += 32) {
+            const int4 rq = req_s[b];
+            longest = max(longest, rq.z);
+            same &= rq.z == rq0.z && blocks_of(rq.x) == blocks_of(rq0.x);
         }
-        const int blocks = planned ? blocks_of(u.n) : blocks_max;
-        // row blocks of the same keys follow one another: the second finds them in L2
-        const int rest = q - first, item = rest / blocks, blk = rest - item * blocks;
-        u.part = item / a.H;
-        u.h = item - u.part * a.H;
-        u.row0 = blk * RP;
-        if (!tl || blk >= blocks_of(u.n)) return false;
-        u.j0 = tl * u.part / u.parts;   // tl < 2^24, parts <= 32
-        u.j1 = tl * (u.part + 1) / u.parts;
-        if (u.parts > 1) u.slot += (u.h * blocks + blk) * u.parts;
-        return true;
-    };
+        longest = __reduce_max_sync(~0u, longest);
+        same = __all_sync(~0u, same);
+#pragma unroll 1
+        for (int i = warp; i < 32; i += C::THREADS / 32) {
+            const float per = fmaxf((float)kMinCut, ceilf((float)longest / (i + 1))), rate = __frcp_rn(per);
+            float sum[4] = {0.f, 0.f, 0.f, 0.f};   // tiles, units, units of cut items
+#pragma unroll 1
+            for (int b = lane; b < B; b += 32) {
+                const int4 rq = req_s[b];
+                const float items = (float)(a.H * blocks_of(rq.x)), parts = parts_of(rq.z, rate);
+                sum[0] += items * rq.z;
+                sum[1] += items * parts;
+                sum[2] += parts > 1.f ? items * parts : 0.f;
+            }
+            reduce_scatter<4>(sum, lane);   // in lanes 0, 8, 16
+            const float work = __shfl_sync(~0u, sum[0], 0), units = __shfl_sync(~0u, sum[0], 8), cut = __shfl_sync(~0u, sum[0], 16);
+            const float all = work + units * kUnitCost, sms = (float)gridDim.x;
+            float cost = fmaxf(per + kUnitCost, same ? ceilf(units / sms) * all / fmaxf(units, 1.f) : all / sms + 0.5f * per) +
+                         (cut > 0.f ? kJoinCost : 0.f);
+            if (i > 0 && cut > (float)a.slots) cost = 3e38f;
+            if (lane == 0) cost_s[i] = cost;
+        }
+        __syncthreads();
+    }
+
     auto read_unit = [&](int r) -> Unit8 {
         const uint32_t i = fix_base + C::FIX_INFO + r * 48;
         const float4 v = lds4(i), w = lds4(i + 16), x = lds4(i + 32);
@@ -563,50 +461,26 @@ __global__ void __launch_bounds__(Cfg8<D, RP>::THREADS, 1)
     constexpr uint64_t swz = D == 128 ? kSwz128 : kSwz64;
     if (warp < 4) {
         if constexpr (C::SM_REGS > C::LAUNCH_REGS) take_registers<false, C::OTHER_REGS>();
-    if (warp == 0) {   // ------------------------------------------------ producer and queue
-        int g = 0, k = 0;
+    if (warp == 0) {   // ------------------------------------------------ producer
+        int g = 0;
         bool ok = true;
-        auto next = [&]() -> int { return lane == 0 ? (int)atomicAdd(a.queue, 1u) : 0; };
-        // the unit of queue place q, or of the first one after it that is not empty, into ring slot k
-        auto publish = [&](int q, Unit8 &u) -> bool {
-            while (q < units && !decode(q, u)) q = __shfl_sync(~0u, next(), 0);
-            const int r = k % kRing;
-            if (k >= kRing && !wait_warp(ifree + 8 * r, (uint32_t)(k / kRing - 1) & 1u)) {
-                ok = false;
-                return false;
-            }
-            if (lane == 0) {
-                const uint32_t i = fix_base + C::FIX_INFO + r * 48;
-                const int v[10] = {q < units ? u.b : -1, u.h, u.row0, u.n, u.P, u.j0, u.j1, u.parts, u.part, u.slot};
-#pragma unroll
-                for (int e = 0; e < 10; ++e) stsi(i + 4 * e, v[e]);
-                mbar_arrive(iready + 8 * r);
-            }
-            ++k;
-            return q < units;
-        };
-        Unit8 u = {}, un = {};   // the first unit follows one without tiles
-        bool more = true;
 #pragma unroll 1
-        while (more) {
-            // the next unit is taken kClaimAhead tiles before this one's last load, late enough that CTAs share the
-            // last units evenly, early enough that its query rows are staged in time; the queue's answer, which
-            // takes up to 2 us while every SM loads, is waited for three loads later
-            const int claim = max(u.j1 - kClaimAhead, u.j0), answer = min(claim + 3, u.j1);
-            int qn = 0;
+        for (int k = 0; ok; ++k) {
+            const int r = k % kRing;
+            if (!wait_warp(iready + 8 * r, (uint32_t)(k / kRing) & 1u)) {
+                ok = false;
+                break;
+            }
+            const Unit8 u = read_unit(r);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(ifree + 8 * r);
+            if (u.b < 0) break;
+            const int claim = max(u.j1 - kClaimAhead, u.j0);
             const int L = u.P + u.n;
             const int strip = (u.b * a.H + u.h) * a.rows;   // dense: the cache row of key 0
 #pragma unroll 1
-            for (int j = u.j0;; ++j, ++g) {
-                if (j == claim) {
-                    qn = ticket >= 0 ? ticket : next();
-                    ticket = -1;
-                }
-                if (j == answer) {
-                    more = publish(__shfl_sync(~0u, qn, 0), un);
-                    if (!ok) break;
-                }
-                if (j == u.j1) break;
+            for (int j = u.j0; j < u.j1; ++j, ++g) {
+                if (j == claim && lane == 0) mbar_arrive(claimgo);
                 const int st = g % C::STAGES, key0 = j * kTileKeys;
                 const bool two = key0 + 64 < L;
                 int row0 = strip + key0, row1 = row0 + 64;
@@ -658,8 +532,6 @@ __global__ void __launch_bounds__(Cfg8<D, RP>::THREADS, 1)
                 }
                 cp_async_arrive(fb);
             }
-            if (!ok) break;
-            u = un;
         }
         if (!ok) {   // leave no copy in flight
             if (lane == 0) misc[1] = 1;
@@ -743,15 +615,151 @@ __global__ void __launch_bounds__(Cfg8<D, RP>::THREADS, 1)
             if (!wait1(fin + 8, 0)) misc[1] = 1;
         }
         __syncwarp();
-    } else if (warp == 3) {   // ----------------------------------------- query rows
+    } else if (warp == 3) {   // ----------------------------------------- queue and query rows
+        // ---- the rest of the plan
+        int units = 0;
+        if (planned) {
+            // the way of the least cost (costs are positive: their bits order as they do), the least cutting of equal ones
+            const uint32_t cost = __float_as_uint(cost_s[lane]), least = __reduce_min_sync(~0u, cost);
+            const int pick = __ffs(__ballot_sync(~0u, cost == least)) - 1;
+            const float rate = __frcp_rn(fmaxf((float)kMinCut, ceilf((float)longest / (pick + 1))));
+            if (same) {
+                const int4 rq = req_s[0];
+                const int parts = max(1, (int)parts_of(rq.z, rate)), u = rq.z ? a.H * blocks_of(rq.x) * parts : 0;
+                __syncwarp();
+#pragma unroll 1
+                for (int b = lane; b < B; b += 32) {
+                    req_s[b].w = parts;
+                    order_s[b] = b;
+                    unit_s[b] = b * u;
+                    slot_s[b] = parts > 1 ? b * u : 0;
+                }
+                units = B * u;
+            } else {
+#pragma unroll 1
+                for (int b = lane; b < B; b += 32) {
+                    const int tl = req_s[b].z, parts = max(1, (int)parts_of(tl, rate));
+                    req_s[b].w = parts;
+                    key_s[b] = parts > 1 ? (tl + parts - 1) / parts : tl;
+                }
+                __syncwarp();
+                // requests by the length of their parts, longest first
+#pragma unroll 1
+                for (int b = lane; b < B; b += 32) {
+                    int rank = 0;
+                    const int mine = key_s[b];
+#pragma unroll 4
+                    for (int o = 0; o < B; ++o) {
+                        const int ko = key_s[o];
+                        rank += ko > mine || (ko == mine && o < b);
+                    }
+                    order_s[rank] = b;
+                }
+                __syncwarp();
+                // exclusive sums of units and of slots, in that order
+                int ns = 0;
+#pragma unroll 1
+                for (int r0 = 0; r0 < B; r0 += 32) {
+                    int u = 0, c = 0;
+                    if (r0 + lane < B) {
+                        const int4 rq = req_s[order_s[r0 + lane]];
+                        if (rq.z) u = a.H * blocks_of(rq.x) * rq.w;
+                        if (rq.w > 1) c = u;
+                    }
+                    int cu = u, cc = c;
+#pragma unroll 1
+                    for (int o = 1; o < 32; o <<= 1) {
+                        const int tu = __shfl_up_sync(~0u, cu, o), tc = __shfl_up_sync(~0u, cc, o);
+                        if (lane >= o) {
+                            cu += tu;
+                            cc += tc;
+                        }
+                    }
+                    if (r0 + lane < B) {
+                        unit_s[r0 + lane] = units + cu - u;
+                        slot_s[r0 + lane] = ns + cc - c;
+                    }
+                    units += __shfl_sync(~0u, cu, 31);
+                    ns += __shfl_sync(~0u, cc, 31);
+                }
+            }
+            __syncwarp();
+        } else {
+            units = B * a.H * ((n_max * a.G + RP - 1) / RP);
+        }
+        // unit q of the queue; false for one that is empty (requests beyond the planned ones)
+        auto decode = [&](int q, Unit8 &u) -> bool {
+            int first, tl, blocks;
+            u.slot = 0;
+            u.parts = 1;
+            if (planned) {
+                int lo = 0, hi = B - 1;   // the last request whose first unit is at most q
+#pragma unroll 1
+                while (lo < hi) {
+                    const int mid = (lo + hi + 1) >> 1;
+                    if (unit_s[mid] <= q) lo = mid;
+                    else hi = mid - 1;
+                }
+                u.b = order_s[lo];
+                first = unit_s[lo];
+                u.slot = slot_s[lo];
+                const int4 rq = req_s[u.b];
+                u.n = rq.x;
+                u.P = rq.y;
+                tl = rq.z;
+                u.parts = rq.w;
+                blocks = blocks_of(u.n);
+            } else {
+                blocks = (n_max * a.G + RP - 1) / RP;
+                u.b = q / (a.H * blocks);
+                first = u.b * a.H * blocks;
+                u.n = a.t.n_nodes[u.b];
+                u.P = a.prefix_len[u.b];
+                tl = tiles_of(u.n, u.P);
+            }
+            // row blocks of the same keys follow one another: the second finds them in L2
+            const int rest = q - first, item = blocks > 1 ? rest / blocks : rest, blk = rest - item * blocks;
+            u.part = u.parts > 1 ? item / a.H : 0;
+            u.h = item - u.part * a.H;
+            u.row0 = blk * RP;
+            if (!tl || blk >= blocks_of(u.n)) return false;
+            u.j0 = 0;
+            u.j1 = tl;
+            if (u.parts > 1) {   // parts differ by a tile at most
+                const int len = tl / u.parts, rem = tl - len * u.parts;
+                u.j0 = u.part * len + min(u.part, rem);
+                u.j1 = u.j0 + len + (u.part < rem);
+                u.slot += (u.h * blocks + blk) * u.parts;
+            }
+            return true;
+        };
         // A raw row of 2 * d bytes and its two parts of d bytes take the same room: each half of the row is copied
-        // to where a part will be; the softmax warps turn rows into parts in place.
+        // to where a part will be; the output warps turn rows into parts in place.
         bool ok = true;
         for (int k = 0;; ++k) {
+            // the next unit is taken kClaimAhead tiles before the last load of the one before, late enough that CTAs
+            // share the last units evenly, early enough that its query rows are staged in time
+            int q = ticket;
+            if (k > 0) {
+                if (!wait_warp(claimgo, (uint32_t)(k - 1) & 1u)) { ok = false; break; }
+                if (lane == 0) q = (int)atomicAdd(a.queue, 1u);
+            }
+            q = __shfl_sync(~0u, q, 0);
+            Unit8 u = {};
+            while (q < units && !decode(q, u)) {
+                if (lane == 0) q = (int)atomicAdd(a.queue, 1u);
+                q = __shfl_sync(~0u, q, 0);
+            }
             const int r = k % kRing;
-            if (!wait_warp(iready + 8 * r, (uint32_t)(k / kRing) & 1u)) { ok = false; break; }
-            const Unit8 u = read_unit(r);
-            if (u.b < 0) break;
+            if (k >= kRing && !wait_warp(ifree + 8 * r, (uint32_t)(k / kRing - 1) & 1u)) { ok = false; break; }
+            if (lane == 0) {
+                const uint32_t i = fix_base + C::FIX_INFO + r * 48;
+                const int v[10] = {q < units ? u.b : -1, u.h, u.row0, u.n, u.P, u.j0, u.j1, u.parts, u.part, u.slot};
+#pragma unroll
+                for (int e = 0; e < 10; ++e) stsi(i + 4 * e, v[e]);
+                mbar_arrive(iready + 8 * r);
+            }
+            if (q >= units) break;
             // lane i looks up the places of rows i and 32 + i of the block in q and out
             int place[2] = {-1, -1};
 #pragma unroll
@@ -780,10 +788,7 @@ __global__ void __launch_bounds__(Cfg8<D, RP>::THREADS, 1)
             }
             cp_async_arrive(qraw + 8 * (k & 1));
             __syncwarp();
-            if (lane == 0) {
-                mbar_arrive(qraw + 8 * (k & 1));   // hands on the rows' places
-                mbar_arrive(ifree + 8 * r);
-            }
+            if (lane == 0) mbar_arrive(qraw + 8 * (k & 1));   // hands on the rows' places
         }
         if (!ok && lane == 0) misc[1] = 1;
         asm volatile("cp.async.wait_all;" ::: "memory");
