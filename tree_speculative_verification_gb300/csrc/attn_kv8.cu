@@ -139,8 +139,16 @@ __device__ __forceinline__ bool wait1(uint32_t bar, uint32_t phase) {
     }
     return false;
 }
-// The same by a whole warp, one verdict for every lane.
-__device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t phase) { return __all_sync(~0u, wait1(bar, phase)); }
+// The same by a whole warp, one verdict for every lane; a look first, which most waits in the tile loop need no more
+// than (long-context case: 453 us against 462).
+__device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t phase) {
+    uint32_t ok;
+    asm volatile("{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
+                 : "=r"(ok)
+                 : "r"(bar), "r"(phase)
+                 : "memory");
+    return __all_sync(~0u, ok) || __all_sync(~0u, wait1(bar, phase));
+}
 
 // Shared memory by its 32-bit address.
 __device__ __forceinline__ float4 lds4(uint32_t a) {
@@ -217,7 +225,7 @@ constexpr int kClaimAhead = 10;    // tiles
 
 template <int D_, int RP_>
 struct Cfg8 {
-    static constexpr int D = D_, RP = RP_, CG = RP == 16 ? 8 : 16, GROUPS = RP / CG;   // columns of a softmax group
+    static constexpr int D = D_, RP = RP_, CG = RP <= 32 ? 8 : 16, GROUPS = RP / CG;   // columns of a softmax group
     static constexpr int SM_WARPS = 4 * GROUPS, THREADS = 32 * (4 + SM_WARPS + 4);
     // Registers a thread: LAUNCH x THREADS at launch, handed from the eight other warps to the softmax's where they
     // need more. The sums: 48: 640 x 96 = 61440 >= 256 x 56 + 384 x 120 = 60416; 64: 768 x 80 = 61440 = 256 x 48 + 512 x 96.
@@ -265,21 +273,19 @@ struct Unit8 {
     int b, h, row0, n, P, j0, j1, parts, part, slot;   // tiles [j0, j1); slot: of the item's first part
 };
 
-// Sums (or maxima) of N columns over the warp: column lane / (32 / N) ends in v[0].
-template <int N, bool MAX = false, int W = 16>
+// Sums of N columns over the warp: column lane / (32 / N) ends in v[0].
+template <int N, int W = 16>
 __device__ __forceinline__ void reduce_scatter(float *v, int lane) {
     if constexpr (N > 1) {
 #pragma unroll
         for (int i = 0; i < N / 2; ++i) {
             const float keep = lane & W ? v[i + N / 2] : v[i], send = lane & W ? v[i] : v[i + N / 2];
-            const float got = __shfl_xor_sync(~0u, send, W);
-            v[i] = MAX ? fmaxf(keep, got) : keep + got;
+            v[i] = keep + __shfl_xor_sync(~0u, send, W);
         }
     } else {
-        const float got = __shfl_xor_sync(~0u, v[0], W);
-        v[0] = MAX ? fmaxf(v[0], got) : v[0] + got;
+        v[0] += __shfl_xor_sync(~0u, v[0], W);
     }
-    if constexpr (W > 1) reduce_scatter<(N > 1 ? N / 2 : 1), MAX, W / 2>(v, lane);
+    if constexpr (W > 1) reduce_scatter<(N > 1 ? N / 2 : 1), W / 2>(v, lane);
 }
 
 // The parts of a cut item into its output rows: a warp a column, lane = part for the weights, then
@@ -810,13 +816,11 @@ __global__ void __launch_bounds__(Cfg8<D, RP>::THREADS, 1)
         for (int k = 0;; ++k) {
             const int r = k % kRing;
             if (!wait_warp(iready + 8 * r, (uint32_t)(k / kRing) & 1u)) ok = false;
-            if (gt < CG) sts1(m_s + gt * 4, 1e30f);
-            if (bar_any(bar, 128, !ok)) {   // all of the group go on, or none
-                ok = false;
+            const Unit8 u = read_unit(r);   // all of the group go on, or none: here, or by the vote of the unit's first tile
+            if (!ok || u.b < 0) {
+                if (bar_any(bar, 128, !ok)) ok = false;
                 break;
             }
-            const Unit8 u = read_unit(r);
-            if (u.b < 0) break;
             const uint32_t oc = tl + C::O_COL + (k & 1) * 3 * RP + cb;   // this unit's O
             const int L = u.P + u.n;
             float2 m[CG / 2], l[CG / 2];   // kBase - maximum; sums over this lane's keys
@@ -942,11 +946,15 @@ __global__ void __launch_bounds__(Cfg8<D, RP>::THREADS, 1)
                     float t[CG];
 #pragma unroll
                     for (int c = 0; c < CG / 2; ++c) {
-                        t[2 * c] = y[c].x;
-                        t[2 * c + 1] = y[c].y;
+                        t[2 * c] = warp_max(y[c].x);
+                        t[2 * c + 1] = warp_max(y[c].y);
                     }
-                    reduce_scatter<CG, true>(t, lane);
-                    if (lane % (32 / CG) == 0) sts1(mx_s + (quarter * CG + lane / (32 / CG)) * 4, t[0]);
+                    if (lane == 0) {
+#pragma unroll
+                        for (int c = 0; c < CG; c += 4)
+                            sts4u(mx_s + (quarter * CG + c) * 4, __float_as_uint(t[c]), __float_as_uint(t[c + 1]),
+                                  __float_as_uint(t[c + 2]), __float_as_uint(t[c + 3]));
+                    }
                     const float vtop = warp_max(vs);
                     if (lane == 0) sts1(v_s + quarter * 4, vtop);
                     if (bar_any(bar, 128, !ok)) {
@@ -964,7 +972,7 @@ __global__ void __launch_bounds__(Cfg8<D, RP>::THREADS, 1)
                     if (gt < CG) {
                         const uint32_t c = mx_s + gt * 4;
                         const float top = fmaxf(fmaxf(lds1(c), lds1(c + 4 * CG)), fmaxf(lds1(c + 8 * CG), lds1(c + 12 * CG)));
-                        const float old = lds1(m_s + gt * 4), nm = top + old > kBase + kOver ? kBase - top : old;
+                        const float old = later ? lds1(m_s + gt * 4) : 1e30f, nm = top + old > kBase + kOver ? kBase - top : old;
                         sts1(m_s + gt * 4, nm);
                         sts1(f2_s + gt * 4, ex2(nm - old));   // 2^(old maximum - new)
                     }
@@ -1259,7 +1267,7 @@ cudaError_t launch8(const CUtensorMap &mk, const CUtensorMap &mv, const Attn8Arg
     if (C::SM_REGS > C::LAUNCH_REGS) {   // the kernel waits for registers that a smaller launch would not have
         cudaFuncAttributes at;
         if ((e = cudaFuncGetAttributes(&at, k_attn_kv8<D, RP>)) != cudaSuccess) return e;
-        if (at.numRegs < C::LAUNCH_REGS) return cudaErrorInvalidConfiguration;
+        if ((at.numRegs + 7) / 8 * 8 < C::LAUNCH_REGS) return cudaErrorInvalidConfiguration;   // given out in eights
     }
     return launch(k_attn_kv8<D, RP>, dim3(grid), dim3(C::THREADS), C::SMEM, s, mk, mv, a);
 }
