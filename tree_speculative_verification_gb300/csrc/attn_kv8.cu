@@ -407,7 +407,11 @@ __global__ void __launch_bounds__(Cfg8<D, RP>::THREADS, 1)
     auto tiles_of = [&](int n, int P) -> int {   // 0 for a request that is empty or does not fit
         return n > 0 && n <= n_max && P >= 0 && P <= a.rows - n ? (P + n + kTileKeys - 1) / kTileKeys : 0;
     };
+    // a part's tiles for way i of cutting, and an item's parts by its reciprocal (taken a little low, so that whole
+    // quotients stay so: these are approximate divisions, the same in every CTA)
+    auto part_tiles = [](int longest, int i) { return fmaxf((float)kMinCut, ceilf(__fdividef((float)longest, (float)(i + 1)) * 0.999999f)); };
     auto parts_of = [](int tiles, float rate) { return fminf(ceilf(tiles * rate), (float)kMaxCuts); };
+    auto rate_of = [](float per) { return __fdividef(0.999999f, per); };
     int ticket = 0;   // the CTA's first place in the queue
     if (warp == 3 && lane == 0) ticket = (int)atomicAdd(a.queue, 1u);
 #pragma unroll 1
@@ -422,9 +426,9 @@ __global__ void __launch_bounds__(Cfg8<D, RP>::THREADS, 1)
     const uint32_t tmem = (uint32_t)misc[0];
     int longest = 0, same = 1;   // same: tiles and row blocks of every request
     if (planned) {
-        // How far to cut: parts of at most 1 / (i + 1) of the longest item, a warp trying every i-th (lane = request).
-        // Items of one length take as many rounds over the SMs as they have units; others, handed out longest first,
-        // about their sum over the SMs and half a longest unit. Cut items have to fit the slots.
+        // How far to cut: parts of at most 1 / (i + 1) of the longest item, half a warp for each of 32 ways (lane =
+        // request). Items of one length take as many rounds over the SMs as they have units; others, handed out
+        // longest first, about their sum over the SMs and half a longest unit. Cut items have to fit the slots.
         const int4 rq0 = req_s[0];
 #pragma unroll 1
         for (int b = lane; b < B; b += 32) {
@@ -434,25 +438,30 @@ __global__ void __launch_bounds__(Cfg8<D, RP>::THREADS, 1)
         }
         longest = __reduce_max_sync(~0u, longest);
         same = __all_sync(~0u, same);
+        static_assert(C::THREADS >= 16 * 32, "half a warp a way");
+        const int i = tid >> 4;
+        if (warp < 16) {
+            const float per = part_tiles(longest, i), rate = rate_of(per);
+            float work = 0.f, units = 0.f, cut = 0.f;   // tiles, units, units of cut items
 #pragma unroll 1
-        for (int i = warp; i < 32; i += C::THREADS / 32) {
-            const float per = fmaxf((float)kMinCut, ceilf((float)longest / (i + 1))), rate = __frcp_rn(per);
-            float sum[4] = {0.f, 0.f, 0.f, 0.f};   // tiles, units, units of cut items
-#pragma unroll 1
-            for (int b = lane; b < B; b += 32) {
+            for (int b = lane & 15; b < B; b += 16) {
                 const int4 rq = req_s[b];
                 const float items = (float)(a.H * blocks_of(rq.x)), parts = parts_of(rq.z, rate);
-                sum[0] += items * rq.z;
-                sum[1] += items * parts;
-                sum[2] += parts > 1.f ? items * parts : 0.f;
+                work += items * rq.z;
+                units += items * parts;
+                cut += parts > 1.f ? items * parts : 0.f;
             }
-            reduce_scatter<4>(sum, lane);   // in lanes 0, 8, 16
-            const float work = __shfl_sync(~0u, sum[0], 0), units = __shfl_sync(~0u, sum[0], 8), cut = __shfl_sync(~0u, sum[0], 16);
+#pragma unroll
+            for (int o = 8; o; o >>= 1) {
+                work += __shfl_xor_sync(~0u, work, o);
+                units += __shfl_xor_sync(~0u, units, o);
+                cut += __shfl_xor_sync(~0u, cut, o);
+            }
             const float all = work + units * kUnitCost, sms = (float)gridDim.x;
-            float cost = fmaxf(per + kUnitCost, same ? ceilf(units / sms) * all / fmaxf(units, 1.f) : all / sms + 0.5f * per) +
-                         (cut > 0.f ? kJoinCost : 0.f);
+            float cost = fmaxf(per + kUnitCost, same ? ceilf(__fdividef(units, sms) * 0.999999f) * __fdividef(all, fmaxf(units, 1.f))
+                                                     : __fdividef(all, sms) + 0.5f * per) + (cut > 0.f ? kJoinCost : 0.f);
             if (i > 0 && cut > (float)a.slots) cost = 3e38f;
-            if (lane == 0) cost_s[i] = cost;
+            if ((lane & 15) == 0) cost_s[i] = cost;
         }
         __syncthreads();
     }
@@ -628,7 +637,7 @@ __global__ void __launch_bounds__(Cfg8<D, RP>::THREADS, 1)
             // the way of the least cost (costs are positive: their bits order as they do), the least cutting of equal ones
             const uint32_t cost = __float_as_uint(cost_s[lane]), least = __reduce_min_sync(~0u, cost);
             const int pick = __ffs(__ballot_sync(~0u, cost == least)) - 1;
-            const float rate = __frcp_rn(fmaxf((float)kMinCut, ceilf((float)longest / (pick + 1))));
+            const float rate = rate_of(part_tiles(longest, pick));
             if (same) {
                 const int4 rq = req_s[0];
                 const int parts = max(1, (int)parts_of(rq.z, rate)), u = rq.z ? a.H * blocks_of(rq.x) * parts : 0;
