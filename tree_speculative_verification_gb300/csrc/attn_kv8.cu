@@ -372,7 +372,11 @@ __global__ void __launch_bounds__(Cfg8<D, RP>::THREADS, 1)
         }
 #pragma unroll 1
         for (int x = 0; x < 2; ++x) {
-            mbar_init(sfull + 8 * x, 2);   // the scores, and the issuer's sight of the stage (scales by cp.async)
+            // the scores, the issuer's sight of the stage (scales by cp.async), and the product two tiles before, which
+            // has read the probabilities that this tile's overwrite (with a wait of its own for that, the long-context
+            // case took 452 us instead of 424)
+            mbar_init(sfull + 8 * x, 3);
+            mbar_arrive(sfull + 8 * x);   // there is no such product yet
             mbar_init(pvdone + 8 * x, 1);
             mbar_init(pfull + 8 * x, C::SM_WARPS);
             mbar_init(qraw + 8 * x, 1 + 32);
@@ -622,6 +626,7 @@ __global__ void __launch_bounds__(Cfg8<D, RP>::THREADS, 1)
                                   smem_desc8(pd + kk * 32 * 64, C::P_ATOM, 512, kSwz64), idesc_o, j > u.j0 || kk > 0);
                     tc_commit(empty + 8 * st);
                     tc_commit(pvdone + 8 * x);
+                    tc_commit(sfull + 8 * x);
                 }
                 if (ok) tc_commit(odone + 8 * (k & 1));
             }
@@ -874,8 +879,6 @@ __global__ void __launch_bounds__(Cfg8<D, RP>::THREADS, 1)
                 return fmaxf(top, top2);
             };
             auto write_p = [&](const float2 (&y)[CG / 2], float vs) {
-                // the product of tile g - 2 has read the probabilities there were
-                if (g >= 2 && ok && !wait_warp(pvdone + 8 * (g & 1), (uint32_t)((g - 2) >> 1) & 1u)) ok = false;
                 const float2 rv = make_float2(vs * iref, vs * iref);
                 const uint32_t pd = fix_base + C::FIX_P + (g & 1) * C::P_BYTES + kslot * 64;
                 const int flip = (kslot >> 1) & 3;
