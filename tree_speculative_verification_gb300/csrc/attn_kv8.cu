@@ -849,7 +849,7 @@ __global__ void __launch_bounds__(Cfg8<D, RP>::THREADS, 1)
             // y: the columns' exponents before the maximum is taken off; vs: the key's value scale
             auto scores = [&](float2 (&y)[CG / 2], float &vs) {
                 const int x = g & 1;
-                if (ok && !wait_warp(sfull + 8 * x, (uint32_t)(g >> 1) & 1u)) ok = false;
+                ok &= wait_warp(sfull + 8 * x, (uint32_t)(g >> 1) & 1u);   // a failure ends the unit with the next vote
                 tc_fence_after();
                 const uint32_t side = sm_base + C::OFF_SIDE + g % C::STAGES * C::SIDE + kslot * 4;
                 float s[CG];
@@ -904,14 +904,12 @@ __global__ void __launch_bounds__(Cfg8<D, RP>::THREADS, 1)
                         w[1][i] = __byte_perm(a1[0], a1[1], 0x7531);
                         w[2][i] = __byte_perm(a2[0], a2[1], 0x7531);
                     }
-                    if (ok) {
 #pragma unroll
-                        for (int e = 0; e < 3; ++e) {
-                            const int col = e * RP + cb + c;
-                            const uint32_t d = pd + (col >> 6) * C::P_ATOM + ((((col >> 4) & 3) ^ flip) << 4) + (col & 15);
-                            if constexpr (STEP == 16) sts4u(d, w[e][0], w[e][1], w[e][2], w[e][3]);
-                            else sts2u(d, w[e][0], w[e][1]);
-                        }
+                    for (int e = 0; e < 3; ++e) {
+                        const int col = e * RP + cb + c;
+                        const uint32_t d = pd + (col >> 6) * C::P_ATOM + ((((col >> 4) & 3) ^ flip) << 4) + (col & 15);
+                        if constexpr (STEP == 16) sts4u(d, w[e][0], w[e][1], w[e][2], w[e][3]);
+                        else sts2u(d, w[e][0], w[e][1]);
                     }
                 }
             };
