@@ -4,7 +4,7 @@
 // (SpecInfer, arXiv 2305.09781, Def. 4.1, Eq. 1-4; the mask of sec. 4.2), with
 // K and V held as e4m3 codes times one fp32 scale per (row, head), and G query
 // heads to a key/value head. The R = n * G query rows of a (request, key/value
-// head) share its keys; they are taken RP at a time (RP = 16, 32, 48 or 64).
+// head) share its keys; they are taken in blocks of RP = 16, 32, 48 or 64.
 //
 // The cache's codes go to the tensor cores as they are. Both products are
 // transposed, so that keys, then value dims, are the 128 rows of the MMA and a
@@ -15,31 +15,48 @@
 //   a query row, scaled by a power of two to a largest value in [128, 256), is
 //   qh + ql with qh = e4m3(q), ql = e4m3(q - qh): bf16's eight bits exactly for
 //   values down to 2^-10 of the row's largest, 2^-18 of it absolutely below;
-//   a probability p (held as 2^11 at the running maximum) is rounded to fp16,
-//   whose upper byte is an e5m2 number: p0 = upper byte of p, p1 = of p - p0,
-//   p2 = of the rest, rounded. Nine bits, down to 2^-28 of the largest (an e4m3
-//   pair would lose weights below 2^-19, which a long cache with one dominant
-//   key has by the thousand).
+//   a probability p (2^7 at the reference maximum) is rounded to fp16, whose
+//   upper byte is an e5m2 number: p0 = upper byte of p, p1 = of p - p0, p2 = of
+//   the rest, rounded. Nine bits down to 2^-15 of the weight at the reference,
+//   to 2^-24 of it absolutely below (a pair of e4m3 numbers would end at 2^-18:
+//   a long cache with one dominant key has weights there by the thousand).
 // Softmax: S * key scale * query scale is the exponent; the value scale times a
 // common reference is multiplied into p before it is split. Sums, maxima, O: fp32.
-//
-// Bound by HBM: (P + n) * 2 * (d + 4) bytes a (request, head), and a tile of 128
-// keys (32 KB at d = 128) has to pass an SM in 0.73 us at the measured copy peak.
 //
 // One CTA per SM takes units (request, head, RP query rows, range of tiles) from
 // a queue in the workspace, longest first; ranges are cut only as far as the
 // launch needs to fill the SMs, the last CTA of a cut item joining the parts.
-//   warp 0      TMA producer and queue: K and V tiles into a ring of stages; the
-//               tile's scales and, for tree keys, subtree ends by cp.async on the
-//               same mbarrier
-//   warps 1, 2  issue the scores, up to two tiles ahead, and O += P V
-//   warp 3      the next unit's query rows, split, into the other Q buffer
-//   softmax     groups of four warps, 16 columns (8 of RP = 16) a group, lane = key. The running maximum of a column is raised only when a score
-//               passes it by 2^4 (one vote per tile and group), so the common tile
-//               has no reduction over keys. Tree node j is seen by the rows of its
-//               subtree, one interval of rows.
+//   warp 0      producer: K and V tiles by TMA into a ring of stages; the tile's
+//               scales and, for tree keys, subtree ends by cp.async on the same
+//               mbarrier
+//   warp 1      issues the scores, as soon as a tile's buffer has been read
+//   warp 2      issues O += P V
+//   warp 3      takes units, publishes them in a ring of four, copies the next
+//               unit's query rows into the other Q buffer
+//   softmax     groups of four warps, lane = key, 8 or 16 columns (query rows) a
+//               group. The reference maximum of a column is raised only when a
+//               score passes it by 2^8 (one vote per tile and group), so the
+//               common tile has no reduction over keys. Tree node j is seen by
+//               the rows of its subtree, one interval of rows.
+//   last four   split a unit's query rows in place, then write the unit before
+//               out of its own O buffer while the softmax works on
 // Every wait is bounded; a wait that gives up sets TS_STATUS_TIMEOUT, the others
 // follow by their own limits or the group's vote, and TMEM is freed.
+//
+// Bounds, measured. A tile of 128 keys (33 KB at d = 128) has to pass an SM in
+// 0.74 us at the measured copy peak of 6.8 TB/s, and does with 16 rows a unit
+// (64 requests x 56 heads x 1040 keys: 153 us, 98% of the peak). With more rows
+// the softmax warps' latency bounds it: 32 rows 189 us (83%), 47 rows 215 us
+// (75%), where a tile costs 0.75 us and a unit of 9 tiles some 2 us more (first
+// maxima, masked tile, sums). 64 rows take 0.83 us a tile (4 x 64 heads x 16512
+// keys x 128 nodes: 402 us, 684 TFLOP/s of attention arithmetic). What carried it
+// there: two tiles of scores and two of probabilities in flight; one wait a tile
+// for both; no branch and few instructions in the common tile (its loop has to
+// stay in the instruction cache: a version of twice the code took 1.4 times as
+// long); units switched by other warps than the softmax's. A call of few tiles
+// is bound by its chain: 5 us until the plan is made and the first scores are
+// there, 3 us for the output and the join of cut items (8 requests of one token
+// over 2048 keys: 14.3 us, 5.1 us at the copy peak).
 #include <cuda.h>
 #include <math.h>
 
@@ -166,8 +183,12 @@ __device__ __forceinline__ int ldsi(uint32_t a) {
     asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
     return v;
 }
-__device__ __forceinline__ void sts1(uint32_t a, float v) { asm volatile("st.shared.f32 [%0], %1;" ::"r"(a), "f"(v) : "memory"); }
-__device__ __forceinline__ void stsi(uint32_t a, int v) { asm volatile("st.shared.b32 [%0], %1;" ::"r"(a), "r"(v) : "memory"); }
+__device__ __forceinline__ void sts1(uint32_t a, float v) {
+    asm volatile("st.shared.f32 [%0], %1;" ::"r"(a), "f"(v) : "memory");
+}
+__device__ __forceinline__ void stsi(uint32_t a, int v) {
+    asm volatile("st.shared.b32 [%0], %1;" ::"r"(a), "r"(v) : "memory");
+}
 __device__ __forceinline__ void sts4u(uint32_t a, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
     asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
 }
@@ -227,11 +248,12 @@ template <int D_, int RP_>
 struct Cfg8 {
     static constexpr int D = D_, RP = RP_, CG = RP <= 32 ? 8 : 16, GROUPS = RP / CG;   // columns of a softmax group
     static constexpr int SM_WARPS = 4 * GROUPS, THREADS = 32 * (4 + SM_WARPS + 4);
-    // Registers a thread: LAUNCH x THREADS at launch, handed from the eight other warps to the softmax's where they
-    // need more. The sums: 48: 640 x 96 = 61440 >= 256 x 56 + 384 x 120 = 60416; 64: 768 x 80 = 61440 = 256 x 48 + 512 x 96.
-    static constexpr int LAUNCH_REGS = RP == 64 ? 80 : RP == 48 ? 96 : 128;
-    static constexpr int SM_REGS = RP == 64 ? 96 : RP == 48 ? 120 : 128;
-    static constexpr int OTHER_REGS = RP == 64 ? 48 : RP == 48 ? 56 : 128;
+    // Registers a thread: LAUNCH x THREADS at launch, handed from the eight other warps to the softmax's where 65536 /
+    // THREADS does not do for those. RP = 48: 640 x 96 = 61440 >= 256 x 56 + 384 x 120 = 60416; 64: 768 x 80 = 61440 =
+    // 256 x 48 + 512 x 96.
+    static constexpr int LAUNCH_REGS = RP == 64 ? 80 : RP == 48 ? 96 : 80;
+    static constexpr int SM_REGS = RP == 64 ? 96 : RP == 48 ? 120 : LAUNCH_REGS;
+    static constexpr int OTHER_REGS = RP == 64 ? 48 : RP == 48 ? 56 : LAUNCH_REGS;
     static_assert(32 * SM_WARPS * SM_REGS + 256 * OTHER_REGS <= THREADS * LAUNCH_REGS, "a split of the launch's registers");
     static constexpr int OP_BYTES = kTileKeys * D;             // codes of one operand tile
     static constexpr int STAGE_BYTES = 2 * OP_BYTES;
@@ -355,8 +377,8 @@ __global__ void __launch_bounds__(Cfg8<D, RP>::THREADS, 1)
 
     const uint32_t full = fix_base + C::FIX_BAR, empty = full + 8 * C::STAGES, sfull = empty + 8 * C::STAGES;
     const uint32_t pvdone = sfull + 16, pfull = pvdone + 16, qraw = pfull + 16, qready = qraw + 16, qfree = qready + 16;
-    const uint32_t fin = qfree + 16, sumfull = fin + 16, odone = sumfull + 16, ofree = odone + 16, iready = ofree + 16, ifree = iready + 8 * kRing;
-    const uint32_t claimgo = ifree + 8 * kRing;
+    const uint32_t fin = qfree + 16, sumfull = fin + 16, odone = sumfull + 16, ofree = odone + 16;
+    const uint32_t iready = ofree + 16, ifree = iready + 8 * kRing, claimgo = ifree + 8 * kRing;
 
     if (warp == 2) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32((void *)misc)),
@@ -413,7 +435,9 @@ __global__ void __launch_bounds__(Cfg8<D, RP>::THREADS, 1)
     };
     // a part's tiles for way i of cutting, and an item's parts by its reciprocal (taken a little low, so that whole
     // quotients stay so: these are approximate divisions, the same in every CTA)
-    auto part_tiles = [](int longest, int i) { return fmaxf((float)kMinCut, ceilf(__fdividef((float)longest, (float)(i + 1)) * 0.999999f)); };
+    auto part_tiles = [](int longest, int i) {
+        return fmaxf((float)kMinCut, ceilf(__fdividef((float)longest, (float)(i + 1)) * 0.999999f));
+    };
     auto parts_of = [](int tiles, float rate) { return fminf(ceilf(tiles * rate), (float)kMaxCuts); };
     auto rate_of = [](float per) { return __fdividef(0.999999f, per); };
     int ticket = 0;   // the CTA's first place in the queue
@@ -462,8 +486,9 @@ __global__ void __launch_bounds__(Cfg8<D, RP>::THREADS, 1)
                 cut += __shfl_xor_sync(~0u, cut, o);
             }
             const float all = work + units * kUnitCost, sms = (float)gridDim.x;
-            float cost = fmaxf(per + kUnitCost, same ? ceilf(__fdividef(units, sms) * 0.999999f) * __fdividef(all, fmaxf(units, 1.f))
-                                                     : __fdividef(all, sms) + 0.5f * per) + (cut > 0.f ? kJoinCost : 0.f);
+            const float spread = same ? ceilf(__fdividef(units, sms) * 0.999999f) * __fdividef(all, fmaxf(units, 1.f))
+                                      : __fdividef(all, sms) + 0.5f * per;
+            float cost = fmaxf(per + kUnitCost, spread) + (cut > 0.f ? kJoinCost : 0.f);
             if (i > 0 && cut > (float)a.slots) cost = 3e38f;
             if ((lane & 15) == 0) cost_s[i] = cost;
         }
@@ -480,344 +505,344 @@ __global__ void __launch_bounds__(Cfg8<D, RP>::THREADS, 1)
     constexpr uint64_t swz = D == 128 ? kSwz128 : kSwz64;
     if (warp < 4) {
         if constexpr (C::SM_REGS > C::LAUNCH_REGS) take_registers<false, C::OTHER_REGS>();
-    if (warp == 0) {   // ------------------------------------------------ producer
-        int g = 0;
-        bool ok = true;
+        if (warp == 0) {   // ------------------------------------------------ producer
+            int g = 0;
+            bool ok = true;
 #pragma unroll 1
-        for (int k = 0; ok; ++k) {
-            const int r = k % kRing;
-            if (!wait_warp(iready + 8 * r, (uint32_t)(k / kRing) & 1u)) {
-                ok = false;
-                break;
-            }
-            const Unit8 u = read_unit(r);
-            __syncwarp();
-            if (lane == 0) mbar_arrive(ifree + 8 * r);
-            if (u.b < 0) break;
-            const int claim = max(u.j1 - kClaimAhead, u.j0);
-            const int L = u.P + u.n;
-            const int strip = (u.b * a.H + u.h) * a.rows;   // dense: the cache row of key 0
-#pragma unroll 1
-            for (int j = u.j0; j < u.j1; ++j, ++g) {
-                if (j == claim && lane == 0) mbar_arrive(claimgo);
-                const int st = g % C::STAGES, key0 = j * kTileKeys;
-                const bool two = key0 + 64 < L;
-                int row0 = strip + key0, row1 = row0 + 64;
-                bool has0 = true, has1 = true;
-                if (a.pg.bt) {   // a page's 64 rows of this head; zeros (a row far outside) for a page that is none
-                    const int32_t *bt = a.pg.bt + (size_t)u.b * a.pg.max_pages + key0 / TS_PAGE_KEYS;
-                    const int p0 = __ldg(bt), p1 = two ? __ldg(bt + 1) : 0;
-                    has0 = p0 >= 0 && p0 < a.pg.num_pages;
-                    has1 = p1 >= 0 && p1 < a.pg.num_pages;
-                    if (lane == 0 && !(has0 && has1)) flag(a.status, TS_STATUS_INDEX);
-                    row0 = has0 ? (p0 * a.H + u.h) * TS_PAGE_KEYS : 0x7fffff00;
-                    row1 = has1 ? (p1 * a.H + u.h) * TS_PAGE_KEYS : 0x7fffff00;
-                }
-                if (g >= C::STAGES && !wait_warp(empty + 8 * st, (uint32_t)(g / C::STAGES - 1) & 1u)) {
+            for (int k = 0; ok; ++k) {
+                const int r = k % kRing;
+                if (!wait_warp(iready + 8 * r, (uint32_t)(k / kRing) & 1u)) {
                     ok = false;
                     break;
                 }
-                const uint32_t kd = sm_base + st * C::STAGE_BYTES, vd = kd + C::OP_BYTES, fb = full + 8 * st;
-                if (lane == 0) {
-                    if (a.pg.bt) {
-                        mbar_expect_tx(fb, (two ? 4 : 2) * 64 * D);
-                        tma_load_2d(kd, &map_k, 0, row0, fb);
-                        tma_load_2d(vd, &map_v, 0, row0, fb);
-                        if (two) {
-                            tma_load_2d(kd + 64 * D, &map_k, 0, row1, fb);
-                            tma_load_2d(vd + 64 * D, &map_v, 0, row1, fb);
-                        }
-                    } else {
-                        mbar_expect_tx(fb, C::STAGE_BYTES);
-                        tma_load_2d(kd, &map_k, 0, row0, fb);
-                        tma_load_2d(vd, &map_v, 0, row0, fb);
+                const Unit8 u = read_unit(r);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(ifree + 8 * r);
+                if (u.b < 0) break;
+                const int claim = max(u.j1 - kClaimAhead, u.j0);
+                const int L = u.P + u.n;
+                const int strip = (u.b * a.H + u.h) * a.rows;   // dense: the cache row of key 0
+#pragma unroll 1
+                for (int j = u.j0; j < u.j1; ++j, ++g) {
+                    if (j == claim && lane == 0) mbar_arrive(claimgo);
+                    const int st = g % C::STAGES, key0 = j * kTileKeys;
+                    const bool two = key0 + 64 < L;
+                    int row0 = strip + key0, row1 = row0 + 64;
+                    bool has0 = true, has1 = true;
+                    if (a.pg.bt) {   // a page's 64 rows of this head; zeros (a row far outside) for a page that is none
+                        const int32_t *bt = a.pg.bt + (size_t)u.b * a.pg.max_pages + key0 / TS_PAGE_KEYS;
+                        const int p0 = __ldg(bt), p1 = two ? __ldg(bt + 1) : 0;
+                        has0 = p0 >= 0 && p0 < a.pg.num_pages;
+                        has1 = p1 >= 0 && p1 < a.pg.num_pages;
+                        if (lane == 0 && !(has0 && has1)) flag(a.status, TS_STATUS_INDEX);
+                        row0 = has0 ? (p0 * a.H + u.h) * TS_PAGE_KEYS : 0x7fffff00;
+                        row1 = has1 ? (p1 * a.H + u.h) * TS_PAGE_KEYS : 0x7fffff00;
                     }
-                }
-                const uint32_t side = sm_base + C::OFF_SIDE + st * C::SIDE + lane * 4;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const bool in = key0 + i * 32 + lane < L && (i < 2 ? has0 : has1);
-                    const int row = in ? (i < 2 ? row0 : row1) + (i & 1) * 32 + lane : 0;
-                    cp_async4(side + i * 128, a.k_scale + row, in);
-                    cp_async4(side + 512 + i * 128, a.v_scale + row, in);
-                }
-                if (key0 + kTileKeys > u.P) {
+                    if (g >= C::STAGES && !wait_warp(empty + 8 * st, (uint32_t)(g / C::STAGES - 1) & 1u)) {
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t kd = sm_base + st * C::STAGE_BYTES, vd = kd + C::OP_BYTES, fb = full + 8 * st;
+                    if (lane == 0) {
+                        if (a.pg.bt) {
+                            mbar_expect_tx(fb, (two ? 4 : 2) * 64 * D);
+                            tma_load_2d(kd, &map_k, 0, row0, fb);
+                            tma_load_2d(vd, &map_v, 0, row0, fb);
+                            if (two) {
+                                tma_load_2d(kd + 64 * D, &map_k, 0, row1, fb);
+                                tma_load_2d(vd + 64 * D, &map_v, 0, row1, fb);
+                            }
+                        } else {
+                            mbar_expect_tx(fb, C::STAGE_BYTES);
+                            tma_load_2d(kd, &map_k, 0, row0, fb);
+                            tma_load_2d(vd, &map_v, 0, row0, fb);
+                        }
+                    }
+                    const uint32_t side = sm_base + C::OFF_SIDE + st * C::SIDE + lane * 4;
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        const int node = key0 + i * 32 + lane - u.P;
-                        const bool in = node >= 0 && node < u.n;
-                        cp_async4(side + 1024 + i * 128, a.t.sub_end + (in ? (size_t)u.b * n_max + node : 0), in);
+                        const bool in = key0 + i * 32 + lane < L && (i < 2 ? has0 : has1);
+                        const int row = in ? (i < 2 ? row0 : row1) + (i & 1) * 32 + lane : 0;
+                        cp_async4(side + i * 128, a.k_scale + row, in);
+                        cp_async4(side + 512 + i * 128, a.v_scale + row, in);
                     }
-                }
-                cp_async_arrive(fb);
-            }
-        }
-        if (!ok) {   // leave no copy in flight
-            if (lane == 0) misc[1] = 1;
-#pragma unroll 1
-            for (int i = g > C::STAGES ? g - C::STAGES : 0; i < g; ++i)
-                wait_warp(full + 8 * (i % C::STAGES), (uint32_t)(i / C::STAGES) & 1u);
-        }
-    } else if (warp == 1) {   // ----------------------------------------- MMA issuer
-        if (lane == 0) {
-            constexpr uint32_t idesc_s = idesc_f8(128, RP, false, false, false);
-            bool ok = true;
-            int g = 0;
-            for (int k = 0; ok; ++k) {
-                const int r = k % kRing;
-                if (!wait1(iready + 8 * r, (uint32_t)(k / kRing) & 1u)) { ok = false; break; }
-                const Unit8 u = read_unit(r);
-                mbar_arrive(ifree + 8 * r);
-                if (u.b < 0) break;
-                if (!wait1(qready + 8 * (k & 1), (uint32_t)(k >> 1) & 1u)) { ok = false; break; }
-#pragma unroll 1
-                for (int j = u.j0; j < u.j1; ++j, ++g) {
-                    const int st = g % C::STAGES, x = g & 1;
-                    // once the probabilities of tile g - 2 are there S(g - 2) has been read; their product need not be done
-                    if ((g >= 2 && !wait1(pfull + 8 * x, (uint32_t)((g - 2) >> 1) & 1u)) ||
-                        !wait1(full + 8 * st, (uint32_t)(g / C::STAGES) & 1u)) {
-                        ok = false;
-                        break;
-                    }
-                    tc_fence_after();
-                    const uint32_t kb = sm_base + st * C::STAGE_BYTES, qd = fix_base + C::FIX_Q + (k & 1) * C::Q_BYTES;
+                    if (key0 + kTileKeys > u.P) {
 #pragma unroll
-                    for (int kk = 0; kk < 2 * (D / 32); ++kk)   // with the rows' upper, then their lower parts
-                        tc_mma_f8(tmem + C::S_COL + x * RP, smem_desc8(kb + kk % (D / 32) * 32, 16, 8 * D, swz),
-                                  smem_desc8(qd + kk / (D / 32) * RP * D + kk % (D / 32) * 32, 16, 8 * D, swz), idesc_s, kk > 0);
-                    tc_commit(sfull + 8 * x);
-                    mbar_arrive(sfull + 8 * x);
-                }
-                if (ok) tc_commit(qfree + 8 * (k & 1));   // the unit's query rows may be overwritten
-            }
-            if (!ok) misc[1] = 1;
-            tc_commit(fin);
-            if (!wait1(fin, 0)) misc[1] = 1;
-        }
-        __syncwarp();
-    } else if (warp == 2) {   // ----------------------------------------- O += P V
-        // a thread of its own: a product waits for its tile's probabilities only, never for the next tile's load
-        if (lane == 0) {
-            constexpr uint32_t idesc_o = idesc_f8(128, 3 * RP, true, true, true);
-            bool ok = true;
-            int g = 0;
-            for (int k = 0; ok; ++k) {
-                const int r = k % kRing;
-                if (!wait1(iready + 8 * r, (uint32_t)(k / kRing) & 1u)) { ok = false; break; }
-                const Unit8 u = read_unit(r);
-                mbar_arrive(ifree + 8 * r);
-                if (u.b < 0) break;
-                if (k >= 2 && !wait1(ofree + 8 * (k & 1), (uint32_t)(k / 2 - 1) & 1u)) { ok = false; break; }
-#pragma unroll 1
-                for (int j = u.j0; j < u.j1; ++j, ++g) {
-                    const int st = g % C::STAGES, x = g & 1;
-                    if (!wait1(full + 8 * st, (uint32_t)(g / C::STAGES) & 1u) ||
-                        !wait1(pfull + 8 * x, (uint32_t)(g >> 1) & 1u)) {
-                        ok = false;
-                        break;
-                    }
-                    tc_fence_after();
-                    const uint32_t vb = sm_base + st * C::STAGE_BYTES + C::OP_BYTES, pd = fix_base + C::FIX_P + x * C::P_BYTES;
-                    // a unit's first product starts its O afresh; the buffer's last one has been read out.
-                    // V^T: dims contiguous; d = 64 repeats its 64 rows (stride 0) to the MMA's 128
-#pragma unroll
-                    for (int kk = 0; kk < kTileKeys / 32; ++kk)
-                        tc_mma_f8(tmem + C::O_COL + (k & 1) * 3 * RP, smem_desc8(vb + kk * 32 * D, 0, 8 * D, swz),
-                                  smem_desc8(pd + kk * 32 * 64, C::P_ATOM, 512, kSwz64), idesc_o, j > u.j0 || kk > 0);
-                    tc_commit(empty + 8 * st);
-                    tc_commit(pvdone + 8 * x);
-                    tc_commit(sfull + 8 * x);
-                }
-                if (ok) tc_commit(odone + 8 * (k & 1));
-            }
-            if (!ok) misc[1] = 1;
-            tc_commit(fin + 8);
-            if (!wait1(fin + 8, 0)) misc[1] = 1;
-        }
-        __syncwarp();
-    } else if (warp == 3) {   // ----------------------------------------- queue and query rows
-        // ---- the rest of the plan
-        int units = 0;
-        if (planned) {
-            // the way of the least cost (costs are positive: their bits order as they do), the least cutting of equal ones
-            const uint32_t cost = __float_as_uint(cost_s[lane]), least = __reduce_min_sync(~0u, cost);
-            const int pick = __ffs(__ballot_sync(~0u, cost == least)) - 1;
-            const float rate = rate_of(part_tiles(longest, pick));
-            if (same) {
-                const int4 rq = req_s[0];
-                const int parts = max(1, (int)parts_of(rq.z, rate)), u = rq.z ? a.H * blocks_of(rq.x) * parts : 0;
-                __syncwarp();
-#pragma unroll 1
-                for (int b = lane; b < B; b += 32) {
-                    req_s[b].w = parts;
-                    order_s[b] = b;
-                    unit_s[b] = b * u;
-                    slot_s[b] = parts > 1 ? b * u : 0;
-                }
-                units = B * u;
-            } else {
-#pragma unroll 1
-                for (int b = lane; b < B; b += 32) {
-                    const int tl = req_s[b].z, parts = max(1, (int)parts_of(tl, rate));
-                    req_s[b].w = parts;
-                    key_s[b] = parts > 1 ? (tl + parts - 1) / parts : tl;
-                }
-                __syncwarp();
-                // requests by the length of their parts, longest first
-#pragma unroll 1
-                for (int b = lane; b < B; b += 32) {
-                    int rank = 0;
-                    const int mine = key_s[b];
-#pragma unroll 4
-                    for (int o = 0; o < B; ++o) {
-                        const int ko = key_s[o];
-                        rank += ko > mine || (ko == mine && o < b);
-                    }
-                    order_s[rank] = b;
-                }
-                __syncwarp();
-                // exclusive sums of units and of slots, in that order
-                int ns = 0;
-#pragma unroll 1
-                for (int r0 = 0; r0 < B; r0 += 32) {
-                    int u = 0, c = 0;
-                    if (r0 + lane < B) {
-                        const int4 rq = req_s[order_s[r0 + lane]];
-                        if (rq.z) u = a.H * blocks_of(rq.x) * rq.w;
-                        if (rq.w > 1) c = u;
-                    }
-                    int cu = u, cc = c;
-#pragma unroll 1
-                    for (int o = 1; o < 32; o <<= 1) {
-                        const int tu = __shfl_up_sync(~0u, cu, o), tc = __shfl_up_sync(~0u, cc, o);
-                        if (lane >= o) {
-                            cu += tu;
-                            cc += tc;
+                        for (int i = 0; i < 4; ++i) {
+                            const int node = key0 + i * 32 + lane - u.P;
+                            const bool in = node >= 0 && node < u.n;
+                            cp_async4(side + 1024 + i * 128, a.t.sub_end + (in ? (size_t)u.b * n_max + node : 0), in);
                         }
                     }
-                    if (r0 + lane < B) {
-                        unit_s[r0 + lane] = units + cu - u;
-                        slot_s[r0 + lane] = ns + cc - c;
-                    }
-                    units += __shfl_sync(~0u, cu, 31);
-                    ns += __shfl_sync(~0u, cc, 31);
+                    cp_async_arrive(fb);
                 }
             }
-            __syncwarp();
-        } else {
-            units = B * a.H * ((n_max * a.G + RP - 1) / RP);
-        }
-        // unit q of the queue; false for one that is empty (requests beyond the planned ones)
-        auto decode = [&](int q, Unit8 &u) -> bool {
-            int first, tl, blocks;
-            u.slot = 0;
-            u.parts = 1;
-            if (planned) {
-                int lo = 0, hi = B - 1;   // the last request whose first unit is at most q
+            if (!ok) {   // leave no copy in flight
+                if (lane == 0) misc[1] = 1;
 #pragma unroll 1
-                while (lo < hi) {
-                    const int mid = (lo + hi + 1) >> 1;
-                    if (unit_s[mid] <= q) lo = mid;
-                    else hi = mid - 1;
-                }
-                u.b = order_s[lo];
-                first = unit_s[lo];
-                u.slot = slot_s[lo];
-                const int4 rq = req_s[u.b];
-                u.n = rq.x;
-                u.P = rq.y;
-                tl = rq.z;
-                u.parts = rq.w;
-                blocks = blocks_of(u.n);
-            } else {
-                blocks = (n_max * a.G + RP - 1) / RP;
-                u.b = q / (a.H * blocks);
-                first = u.b * a.H * blocks;
-                u.n = a.t.n_nodes[u.b];
-                u.P = a.prefix_len[u.b];
-                tl = tiles_of(u.n, u.P);
+                for (int i = g > C::STAGES ? g - C::STAGES : 0; i < g; ++i)
+                    wait_warp(full + 8 * (i % C::STAGES), (uint32_t)(i / C::STAGES) & 1u);
             }
-            // row blocks of the same keys follow one another: the second finds them in L2
-            const int rest = q - first, item = blocks > 1 ? rest / blocks : rest, blk = rest - item * blocks;
-            u.part = u.parts > 1 ? item / a.H : 0;
-            u.h = item - u.part * a.H;
-            u.row0 = blk * RP;
-            if (!tl || blk >= blocks_of(u.n)) return false;
-            u.j0 = 0;
-            u.j1 = tl;
-            if (u.parts > 1) {   // parts differ by a tile at most
-                const int len = tl / u.parts, rem = tl - len * u.parts;
-                u.j0 = u.part * len + min(u.part, rem);
-                u.j1 = u.j0 + len + (u.part < rem);
-                u.slot += (u.h * blocks + blk) * u.parts;
-            }
-            return true;
-        };
-        // A raw row of 2 * d bytes and its two parts of d bytes take the same room: each half of the row is copied
-        // to where a part will be; the output warps turn rows into parts in place.
-        bool ok = true;
-        for (int k = 0;; ++k) {
-            // the next unit is taken kClaimAhead tiles before the last load of the one before, late enough that CTAs
-            // share the last units evenly, early enough that its query rows are staged in time
-            int q = ticket;
-            if (k > 0) {
-                if (!wait_warp(claimgo, (uint32_t)(k - 1) & 1u)) { ok = false; break; }
-                if (lane == 0) q = (int)atomicAdd(a.queue, 1u);
-            }
-            q = __shfl_sync(~0u, q, 0);
-            Unit8 u = {};
-            while (q < units && !decode(q, u)) {
-                if (lane == 0) q = (int)atomicAdd(a.queue, 1u);
-                q = __shfl_sync(~0u, q, 0);
-            }
-            const int r = k % kRing;
-            if (k >= kRing && !wait_warp(ifree + 8 * r, (uint32_t)(k / kRing - 1) & 1u)) { ok = false; break; }
+        } else if (warp == 1) {   // ----------------------------------------- MMA issuer
             if (lane == 0) {
-                const uint32_t i = fix_base + C::FIX_INFO + r * 48;
-                const int v[10] = {q < units ? u.b : -1, u.h, u.row0, u.n, u.P, u.j0, u.j1, u.parts, u.part, u.slot};
+                constexpr uint32_t idesc_s = idesc_f8(128, RP, false, false, false);
+                bool ok = true;
+                int g = 0;
+                for (int k = 0; ok; ++k) {
+                    const int r = k % kRing;
+                    if (!wait1(iready + 8 * r, (uint32_t)(k / kRing) & 1u)) { ok = false; break; }
+                    const Unit8 u = read_unit(r);
+                    mbar_arrive(ifree + 8 * r);
+                    if (u.b < 0) break;
+                    if (!wait1(qready + 8 * (k & 1), (uint32_t)(k >> 1) & 1u)) { ok = false; break; }
+#pragma unroll 1
+                    for (int j = u.j0; j < u.j1; ++j, ++g) {
+                        const int st = g % C::STAGES, x = g & 1;
+                        // once the probabilities of tile g - 2 are there S(g - 2) has been read; their product need not be done
+                        if ((g >= 2 && !wait1(pfull + 8 * x, (uint32_t)((g - 2) >> 1) & 1u)) ||
+                            !wait1(full + 8 * st, (uint32_t)(g / C::STAGES) & 1u)) {
+                            ok = false;
+                            break;
+                        }
+                        tc_fence_after();
+                        const uint32_t kb = sm_base + st * C::STAGE_BYTES, qd = fix_base + C::FIX_Q + (k & 1) * C::Q_BYTES;
 #pragma unroll
-                for (int e = 0; e < 10; ++e) stsi(i + 4 * e, v[e]);
-                mbar_arrive(iready + 8 * r);
-            }
-            if (q >= units) break;
-            // lane i looks up the places of rows i and 32 + i of the block in q and out
-            int place[2] = {-1, -1};
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int c = h * 32 + lane;
-                if (c < RP) {
-                    const int rho = u.row0 + c, i = rho / a.G;
-                    if (i < u.n) {
-                        const int v = a.t.perm[(size_t)u.b * n_max + i];
-                        if (v >= 0 && v < n_max) place[h] = v * a.Hq + u.h * a.G + (rho - i * a.G);
+                        for (int kk = 0; kk < 2 * (D / 32); ++kk)   // with the rows' upper, then their lower parts
+                            tc_mma_f8(tmem + C::S_COL + x * RP, smem_desc8(kb + kk % (D / 32) * 32, 16, 8 * D, swz),
+                                      smem_desc8(qd + kk / (D / 32) * RP * D + kk % (D / 32) * 32, 16, 8 * D, swz), idesc_s, kk > 0);
+                        tc_commit(sfull + 8 * x);
+                        mbar_arrive(sfull + 8 * x);
                     }
-                    stsi(fix_base + C::FIX_QROW + (r * 64 + c) * 4, place[h]);
+                    if (ok) tc_commit(qfree + 8 * (k & 1));   // the unit's query rows may be overwritten
                 }
+                if (!ok) misc[1] = 1;
+                tc_commit(fin);
+                if (!wait1(fin, 0)) misc[1] = 1;
             }
-            if (k >= 2 && !wait_warp(qfree + 8 * (k & 1), (uint32_t)(k / 2 - 1) & 1u)) { ok = false; break; }
-            const uint32_t qd = fix_base + C::FIX_Q + (k & 1) * C::Q_BYTES;
-            const __nv_bfloat16 *qb = a.q + (size_t)u.b * n_max * a.Hq * D;
-            constexpr int VPR = D / 8;   // 16-byte pieces of a raw row
-#pragma unroll 4
-            for (int i = lane; i < RP * VPR; i += 32) {
-                const int c = i / VPR, v = i % VPR;
-                const int lo = __shfl_sync(~0u, place[0], c & 31), hi = __shfl_sync(~0u, place[1], c & 31);
-                const int pl = c < 32 ? lo : hi;
-                cp_async16(qd + ((v >= VPR / 2 ? RP : 0) + c) * D + (v % (VPR / 2)) * 16,
-                           qb + (size_t)(pl < 0 ? 0 : pl) * D + v * 8, pl >= 0);
-            }
-            cp_async_arrive(qraw + 8 * (k & 1));
             __syncwarp();
-            if (lane == 0) mbar_arrive(qraw + 8 * (k & 1));   // hands on the rows' places
+        } else if (warp == 2) {   // ----------------------------------------- O += P V
+            // a thread of its own: a product waits for its tile's probabilities only, never for the next tile's load
+            if (lane == 0) {
+                constexpr uint32_t idesc_o = idesc_f8(128, 3 * RP, true, true, true);
+                bool ok = true;
+                int g = 0;
+                for (int k = 0; ok; ++k) {
+                    const int r = k % kRing;
+                    if (!wait1(iready + 8 * r, (uint32_t)(k / kRing) & 1u)) { ok = false; break; }
+                    const Unit8 u = read_unit(r);
+                    mbar_arrive(ifree + 8 * r);
+                    if (u.b < 0) break;
+                    if (k >= 2 && !wait1(ofree + 8 * (k & 1), (uint32_t)(k / 2 - 1) & 1u)) { ok = false; break; }
+#pragma unroll 1
+                    for (int j = u.j0; j < u.j1; ++j, ++g) {
+                        const int st = g % C::STAGES, x = g & 1;
+                        if (!wait1(full + 8 * st, (uint32_t)(g / C::STAGES) & 1u) ||
+                            !wait1(pfull + 8 * x, (uint32_t)(g >> 1) & 1u)) {
+                            ok = false;
+                            break;
+                        }
+                        tc_fence_after();
+                        const uint32_t vb = sm_base + st * C::STAGE_BYTES + C::OP_BYTES, pd = fix_base + C::FIX_P + x * C::P_BYTES;
+                        // a unit's first product starts its O afresh; the buffer's last one has been read out.
+                        // V^T: dims contiguous; d = 64 repeats its 64 rows (stride 0) to the MMA's 128
+#pragma unroll
+                        for (int kk = 0; kk < kTileKeys / 32; ++kk)
+                            tc_mma_f8(tmem + C::O_COL + (k & 1) * 3 * RP, smem_desc8(vb + kk * 32 * D, 0, 8 * D, swz),
+                                      smem_desc8(pd + kk * 32 * 64, C::P_ATOM, 512, kSwz64), idesc_o, j > u.j0 || kk > 0);
+                        tc_commit(empty + 8 * st);
+                        tc_commit(pvdone + 8 * x);
+                        tc_commit(sfull + 8 * x);
+                    }
+                    if (ok) tc_commit(odone + 8 * (k & 1));
+                }
+                if (!ok) misc[1] = 1;
+                tc_commit(fin + 8);
+                if (!wait1(fin + 8, 0)) misc[1] = 1;
+            }
+            __syncwarp();
+        } else if (warp == 3) {   // ----------------------------------------- queue and query rows
+            // ---- the rest of the plan
+            int units = 0;
+            if (planned) {
+                // the way of the least cost (costs are positive: their bits order as they do), the least cutting of equal ones
+                const uint32_t cost = __float_as_uint(cost_s[lane]), least = __reduce_min_sync(~0u, cost);
+                const int pick = __ffs(__ballot_sync(~0u, cost == least)) - 1;
+                const float rate = rate_of(part_tiles(longest, pick));
+                if (same) {
+                    const int4 rq = req_s[0];
+                    const int parts = max(1, (int)parts_of(rq.z, rate)), u = rq.z ? a.H * blocks_of(rq.x) * parts : 0;
+                    __syncwarp();
+#pragma unroll 1
+                    for (int b = lane; b < B; b += 32) {
+                        req_s[b].w = parts;
+                        order_s[b] = b;
+                        unit_s[b] = b * u;
+                        slot_s[b] = parts > 1 ? b * u : 0;
+                    }
+                    units = B * u;
+                } else {
+#pragma unroll 1
+                    for (int b = lane; b < B; b += 32) {
+                        const int tl = req_s[b].z, parts = max(1, (int)parts_of(tl, rate));
+                        req_s[b].w = parts;
+                        key_s[b] = parts > 1 ? (tl + parts - 1) / parts : tl;
+                    }
+                    __syncwarp();
+                    // requests by the length of their parts, longest first
+#pragma unroll 1
+                    for (int b = lane; b < B; b += 32) {
+                        int rank = 0;
+                        const int mine = key_s[b];
+#pragma unroll 4
+                        for (int o = 0; o < B; ++o) {
+                            const int ko = key_s[o];
+                            rank += ko > mine || (ko == mine && o < b);
+                        }
+                        order_s[rank] = b;
+                    }
+                    __syncwarp();
+                    // exclusive sums of units and of slots, in that order
+                    int ns = 0;
+#pragma unroll 1
+                    for (int r0 = 0; r0 < B; r0 += 32) {
+                        int u = 0, c = 0;
+                        if (r0 + lane < B) {
+                            const int4 rq = req_s[order_s[r0 + lane]];
+                            if (rq.z) u = a.H * blocks_of(rq.x) * rq.w;
+                            if (rq.w > 1) c = u;
+                        }
+                        int cu = u, cc = c;
+#pragma unroll 1
+                        for (int o = 1; o < 32; o <<= 1) {
+                            const int tu = __shfl_up_sync(~0u, cu, o), tc = __shfl_up_sync(~0u, cc, o);
+                            if (lane >= o) {
+                                cu += tu;
+                                cc += tc;
+                            }
+                        }
+                        if (r0 + lane < B) {
+                            unit_s[r0 + lane] = units + cu - u;
+                            slot_s[r0 + lane] = ns + cc - c;
+                        }
+                        units += __shfl_sync(~0u, cu, 31);
+                        ns += __shfl_sync(~0u, cc, 31);
+                    }
+                }
+                __syncwarp();
+            } else {
+                units = B * a.H * ((n_max * a.G + RP - 1) / RP);
+            }
+            // unit q of the queue; false for one that is empty (requests beyond the planned ones)
+            auto decode = [&](int q, Unit8 &u) -> bool {
+                int first, tl, blocks;
+                u.slot = 0;
+                u.parts = 1;
+                if (planned) {
+                    int lo = 0, hi = B - 1;   // the last request whose first unit is at most q
+#pragma unroll 1
+                    while (lo < hi) {
+                        const int mid = (lo + hi + 1) >> 1;
+                        if (unit_s[mid] <= q) lo = mid;
+                        else hi = mid - 1;
+                    }
+                    u.b = order_s[lo];
+                    first = unit_s[lo];
+                    u.slot = slot_s[lo];
+                    const int4 rq = req_s[u.b];
+                    u.n = rq.x;
+                    u.P = rq.y;
+                    tl = rq.z;
+                    u.parts = rq.w;
+                    blocks = blocks_of(u.n);
+                } else {
+                    blocks = (n_max * a.G + RP - 1) / RP;
+                    u.b = q / (a.H * blocks);
+                    first = u.b * a.H * blocks;
+                    u.n = a.t.n_nodes[u.b];
+                    u.P = a.prefix_len[u.b];
+                    tl = tiles_of(u.n, u.P);
+                }
+                // row blocks of the same keys follow one another: the second finds them in L2
+                const int rest = q - first, item = blocks > 1 ? rest / blocks : rest, blk = rest - item * blocks;
+                u.part = u.parts > 1 ? item / a.H : 0;
+                u.h = item - u.part * a.H;
+                u.row0 = blk * RP;
+                if (!tl || blk >= blocks_of(u.n)) return false;
+                u.j0 = 0;
+                u.j1 = tl;
+                if (u.parts > 1) {   // parts differ by a tile at most
+                    const int len = tl / u.parts, rem = tl - len * u.parts;
+                    u.j0 = u.part * len + min(u.part, rem);
+                    u.j1 = u.j0 + len + (u.part < rem);
+                    u.slot += (u.h * blocks + blk) * u.parts;
+                }
+                return true;
+            };
+            // A raw row of 2 * d bytes and its two parts of d bytes take the same room: each half of the row is copied
+            // to where a part will be; the output warps turn rows into parts in place.
+            bool ok = true;
+            for (int k = 0;; ++k) {
+                // the next unit is taken kClaimAhead tiles before the last load of the one before, late enough that CTAs
+                // share the last units evenly, early enough that its query rows are staged in time
+                int q = ticket;
+                if (k > 0) {
+                    if (!wait_warp(claimgo, (uint32_t)(k - 1) & 1u)) { ok = false; break; }
+                    if (lane == 0) q = (int)atomicAdd(a.queue, 1u);
+                }
+                q = __shfl_sync(~0u, q, 0);
+                Unit8 u = {};
+                while (q < units && !decode(q, u)) {
+                    if (lane == 0) q = (int)atomicAdd(a.queue, 1u);
+                    q = __shfl_sync(~0u, q, 0);
+                }
+                const int r = k % kRing;
+                if (k >= kRing && !wait_warp(ifree + 8 * r, (uint32_t)(k / kRing - 1) & 1u)) { ok = false; break; }
+                if (lane == 0) {
+                    const uint32_t i = fix_base + C::FIX_INFO + r * 48;
+                    const int v[10] = {q < units ? u.b : -1, u.h, u.row0, u.n, u.P, u.j0, u.j1, u.parts, u.part, u.slot};
+#pragma unroll
+                    for (int e = 0; e < 10; ++e) stsi(i + 4 * e, v[e]);
+                    mbar_arrive(iready + 8 * r);
+                }
+                if (q >= units) break;
+                // lane i looks up the places of rows i and 32 + i of the block in q and out
+                int place[2] = {-1, -1};
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int c = h * 32 + lane;
+                    if (c < RP) {
+                        const int rho = u.row0 + c, i = rho / a.G;
+                        if (i < u.n) {
+                            const int v = a.t.perm[(size_t)u.b * n_max + i];
+                            if (v >= 0 && v < n_max) place[h] = v * a.Hq + u.h * a.G + (rho - i * a.G);
+                        }
+                        stsi(fix_base + C::FIX_QROW + (r * 64 + c) * 4, place[h]);
+                    }
+                }
+                if (k >= 2 && !wait_warp(qfree + 8 * (k & 1), (uint32_t)(k / 2 - 1) & 1u)) { ok = false; break; }
+                const uint32_t qd = fix_base + C::FIX_Q + (k & 1) * C::Q_BYTES;
+                const __nv_bfloat16 *qb = a.q + (size_t)u.b * n_max * a.Hq * D;
+                constexpr int VPR = D / 8;   // 16-byte pieces of a raw row
+#pragma unroll 4
+                for (int i = lane; i < RP * VPR; i += 32) {
+                    const int c = i / VPR, v = i % VPR;
+                    const int lo = __shfl_sync(~0u, place[0], c & 31), hi = __shfl_sync(~0u, place[1], c & 31);
+                    const int pl = c < 32 ? lo : hi;
+                    cp_async16(qd + ((v >= VPR / 2 ? RP : 0) + c) * D + (v % (VPR / 2)) * 16,
+                               qb + (size_t)(pl < 0 ? 0 : pl) * D + v * 8, pl >= 0);
+                }
+                cp_async_arrive(qraw + 8 * (k & 1));
+                __syncwarp();
+                if (lane == 0) mbar_arrive(qraw + 8 * (k & 1));   // hands on the rows' places
+            }
+            if (!ok && lane == 0) misc[1] = 1;
+            asm volatile("cp.async.wait_all;" ::: "memory");
         }
-        if (!ok && lane == 0) misc[1] = 1;
-        asm volatile("cp.async.wait_all;" ::: "memory");
-    }
     } else if (warp < 4 + C::SM_WARPS) {   // ---------------------------- softmax
         if constexpr (C::SM_REGS > C::LAUNCH_REGS) take_registers<true, C::SM_REGS>();
         constexpr int CG = C::CG;
-        // p is 2^kBase at the running maximum, which is raised once a score passes it by 2^kOver: fp16 (and e5m2) hold
-        // both ends, and what is 2^-24 of the maximum still has a bit
+        // p is 2^kBase at the reference maximum, which is raised once a score passes it by 2^kOver: fp16 (and e5m2) hold
+        // both ends, and a weight of 2^-23 of the reference's still has a bit
         constexpr float kBase = 7.f, kOver = 8.f;
         const int grp = (warp - 4) >> 2, quarter = warp & 3, cb = grp * CG;
         const int bar = 1 + grp, gt = quarter * 32 + lane;   // thread of the group
@@ -864,8 +889,9 @@ __global__ void __launch_bounds__(Cfg8<D, RP>::THREADS, 1)
 #pragma unroll
                 for (int c = 0; c < CG / 4; ++c) {
                     const float4 v = lds4(qs + 16 * c);
-                    y[2 * c] = __fmul2_rn(__fmul2_rn(make_float2(s[4 * c], s[4 * c + 1]), make_float2(v.x, v.y)), make_float2(ks, ks));
-                    y[2 * c + 1] = __fmul2_rn(__fmul2_rn(make_float2(s[4 * c + 2], s[4 * c + 3]), make_float2(v.z, v.w)), make_float2(ks, ks));
+                    const float2 k2 = make_float2(ks, ks);
+                    y[2 * c] = __fmul2_rn(__fmul2_rn(make_float2(s[4 * c], s[4 * c + 1]), make_float2(v.x, v.y)), k2);
+                    y[2 * c + 1] = __fmul2_rn(__fmul2_rn(make_float2(s[4 * c + 2], s[4 * c + 3]), make_float2(v.z, v.w)), k2);
                 }
             };
             auto above = [&](const float2 (&y)[CG / 2]) -> float {   // the furthest score above its column's maximum
@@ -1095,44 +1121,46 @@ __global__ void __launch_bounds__(Cfg8<D, RP>::THREADS, 1)
                 const int sub = lane % LPR;
 #pragma unroll 1
                 for (int c = quarter * (RP / 4) + lane / LPR; c < (quarter + 1) * (RP / 4); c += 4) {
-                uint32_t w[EPL / 2];   // two values each
-                const uint32_t src = qd + ((sub >= LPR / 2 ? RP : 0) + c) * D + sub % (LPR / 2) * (2 * EPL);
+                    uint32_t w[EPL / 2];   // two values each
+                    const uint32_t src = qd + ((sub >= LPR / 2 ? RP : 0) + c) * D + sub % (LPR / 2) * (2 * EPL);
 #pragma unroll
-                for (int e = 0; e < EPL / 2; e += 2)
-                    asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];" : "=r"(w[e]), "=r"(w[e + 1]) : "r"(src + 4 * e) : "memory");
-                uint32_t top = 0;   // two |values| at a time, which order as their bits do, infinities and NaN on top
+                    for (int e = 0; e < EPL / 2; e += 2)
+                        asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];" : "=r"(w[e]), "=r"(w[e + 1]) : "r"(src + 4 * e) : "memory");
+                    uint32_t top = 0;   // two |values| at a time, which order as their bits do, infinities and NaN on top
 #pragma unroll
-                for (int e = 0; e < EPL / 2; ++e) top = __vmaxu2(top, w[e] & 0x7fff7fffu);
+                    for (int e = 0; e < EPL / 2; ++e) top = __vmaxu2(top, w[e] & 0x7fff7fffu);
 #pragma unroll
-                for (int o = LPR / 2; o; o >>= 1) top = __vmaxu2(top, __shfl_xor_sync(~0u, top, o));
-                top = max(top >> 16, top & 0xffffu);
-                // 2^(exponent - 7), within the normal numbers whose reciprocal is one too
-                int ex = (int)(top >> 7) - 7;
-                ex = ex < 4 ? 4 : ex;
-                const float inv = __uint_as_float((uint32_t)(254 - ex) << 23);
+                    for (int o = LPR / 2; o; o >>= 1) top = __vmaxu2(top, __shfl_xor_sync(~0u, top, o));
+                    top = max(top >> 16, top & 0xffffu);
+                    // 2^(exponent - 7), within the normal numbers whose reciprocal is one too
+                    int ex = (int)(top >> 7) - 7;
+                    ex = ex < 4 ? 4 : ex;
+                    const float inv = __uint_as_float((uint32_t)(254 - ex) << 23);
 #pragma unroll
-                for (int e = 0; e < EPL / 4; ++e) {
-                    uint32_t h2[2], l2[2];
+                    for (int e = 0; e < EPL / 4; ++e) {
+                        uint32_t h2[2], l2[2];
 #pragma unroll
-                    for (int f = 0; f < 2; ++f) {   // fp16 holds the scaled values and every difference here
-                        const uint32_t v = w[2 * e + f];
-                        const float2 y = __fmul2_rn(make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u)),
-                                                    make_float2(inv, inv));
-                        const uint32_t y16 = half2_of(y.x, y.y);
-                        h2[f] = half2_to_fp8x2(y16);
-                        l2[f] = half2_to_fp8x2(hsub2(y16, fp8x2_to_half2(h2[f])));
+                        for (int f = 0; f < 2; ++f) {   // fp16 holds the scaled values and every difference here
+                            const uint32_t v = w[2 * e + f];
+                            const float2 y = __fmul2_rn(make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u)),
+                                                        make_float2(inv, inv));
+                            const uint32_t y16 = half2_of(y.x, y.y);
+                            h2[f] = half2_to_fp8x2(y16);
+                            l2[f] = half2_to_fp8x2(hsub2(y16, fp8x2_to_half2(h2[f])));
+                        }
+                        // 16-byte chunks of a row are permuted as the MMA's descriptor says
+                        const int at = sub * EPL + 4 * e;
+                        auto place = [&](int row) {
+                            const int flip = D == 128 ? row & 7 : (row >> 1) & 3;
+                            return qd + row * D + (((at >> 4) ^ flip) << 4) + (at & 15);
+                        };
+                        stsi(place(c), (int)(h2[0] | h2[1] << 16));
+                        stsi(place(RP + c), (int)(l2[0] | l2[1] << 16));
                     }
-                    // 16-byte chunks of a row are permuted as the MMA's descriptor says
-                    const int at = sub * EPL + 4 * e;
-                    auto place = [&](int row) {
-                        const int flip = D == 128 ? row & 7 : (row >> 1) & 3;
-                        return qd + row * D + (((at >> 4) ^ flip) << 4) + (at & 15);
-                    };
-                    stsi(place(c), (int)(h2[0] | h2[1] << 16));
-                    stsi(place(RP + c), (int)(l2[0] | l2[1] << 16));
-                }
-                if (sub == 0)
-                    stsi(fix_base + C::FIX_QS + (r * 64 + c) * 4, top >= 0x7f80u ? 0x7fc00000 : (int)((uint32_t)ex << 23));
+                    if (sub == 0) {
+                        const int scale = top >= 0x7f80u ? 0x7fc00000 : (int)((uint32_t)ex << 23);
+                        stsi(fix_base + C::FIX_QS + (r * 64 + c) * 4, scale);
+                    }
                 }
                 fence_async_smem();
                 __syncwarp();

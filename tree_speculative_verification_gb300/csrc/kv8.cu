@@ -65,7 +65,8 @@ __device__ __forceinline__ float max_abs(float a, float b, float c) {
 }
 
 __device__ __forceinline__ void cp_async16(void *dst, const void *src) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src) : "memory");
+    const uint32_t to = (uint32_t)__cvta_generic_to_shared(dst);
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(src) : "memory");
 }
 __device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
@@ -98,7 +99,9 @@ struct Two;
 template <>
 struct Two<__nv_bfloat16> {
     using U = uint32_t;
-    static __device__ __forceinline__ float2 get(U u) { return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u)); }
+    static __device__ __forceinline__ float2 get(U u) {
+        return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
+    }
     static __device__ __forceinline__ U put(float2 x) {
         const __nv_bfloat162 p = __floats2bfloat162_rn(x.x, x.y);
         return *reinterpret_cast<const U *>(&p);
@@ -140,9 +143,13 @@ __device__ __forceinline__ void unpairs(const float2 (&x)[H / 2], const float2 (
 // 131072 is off by up to 4e-3), then sincosf of the fp32 remainder. Each value
 // is read once and written once, all of a CTA's rows in flight from its start
 // (into shared memory; in registers, four rows a lane group ahead, they cost
-// more occupancy than they hid: 51 us against 46 on an append of 64 x 47 nodes, 56 + 56 heads of 128).
-// What bounds a large call next to memory is issuing: the loop is compiled once
-// for each kind of row (query, key, value), and a CTA runs one of them.
+// more occupancy than they hid: 51 us against 46 on an append of 64 x 47 nodes,
+// 56 + 56 heads of 128). What bounds a large call next to memory is issuing
+// (69% of the slots in that append): the loop is compiled once for each kind of
+// row (query, key, value), and a CTA runs one of them; one loop for all kinds
+// took 56 us. Measured there: norm and rotation of q and k 30.5 us (172 MB, 83%
+// of the copy peak), the append with its codes 45.4 us (217 MB, 70%). The
+// divisions are the definition's and cost 1.6 us of that.
 template <typename T, int D, bool APPEND, bool INTER>
 __global__ void __launch_bounds__(kRowThreads) k_head_rows(RowArgs a) {
     constexpr int E = 16 / (int)sizeof(T), LPR = D / E, RPC = kRowThreads / LPR, RW = 32 / LPR, H = E / 2;
@@ -246,91 +253,89 @@ __global__ void __launch_bounds__(kRowThreads) k_head_rows(RowArgs a) {
         // r: this group's row, first: the warp's first
 #pragma unroll 1
         for (int r = r_begin + slot, first = r_begin + slot / RW * RW; first < r_end; r += RPC, first += RPC) {
-            {
-                float2 t[H];
-                const uint2 lo = *reinterpret_cast<const uint2 *>(in + e0), hi = *reinterpret_cast<const uint2 *>(in + e1);
-                in += RPC * D;
-                if constexpr (sizeof(T) == 2) {
-                    t[0] = Two<T>::get(lo.x);
-                    t[1] = Two<T>::get(lo.y);
-                    t[2] = Two<T>::get(hi.x);
-                    t[3] = Two<T>::get(hi.y);
-                } else {
-                    t[0] = Two<T>::get(lo);
-                    t[1] = Two<T>::get(hi);
-                }
-                if (TURN && (a.norm || half)) {
-                    float2 x[H / 2], y[H / 2];   // first and second members
-                    pairs<H, INTER>(t, x, y);
-                    if (a.norm) {
-                        float2 s2 = make_float2(0.f, 0.f);
+            float2 t[H];
+            const uint2 lo = *reinterpret_cast<const uint2 *>(in + e0), hi = *reinterpret_cast<const uint2 *>(in + e1);
+            in += RPC * D;
+            if constexpr (sizeof(T) == 2) {
+                t[0] = Two<T>::get(lo.x);
+                t[1] = Two<T>::get(lo.y);
+                t[2] = Two<T>::get(hi.x);
+                t[3] = Two<T>::get(hi.y);
+            } else {
+                t[0] = Two<T>::get(lo);
+                t[1] = Two<T>::get(hi);
+            }
+            if (TURN && (a.norm || half)) {
+                float2 x[H / 2], y[H / 2];   // first and second members
+                pairs<H, INTER>(t, x, y);
+                if (a.norm) {
+                    float2 s2 = make_float2(0.f, 0.f);
 #pragma unroll
-                        for (int e = 0; e < H / 2; ++e) s2 = __ffma2_rn(y[e], y[e], __ffma2_rn(x[e], x[e], s2));
-                        float ss = s2.x + s2.y;
+                    for (int e = 0; e < H / 2; ++e) s2 = __ffma2_rn(y[e], y[e], __ffma2_rn(x[e], x[e], s2));
+                    float ss = s2.x + s2.y;
 #pragma unroll
-                        for (int o = LPR / 2; o; o >>= 1) ss += __shfl_xor_sync(~0u, ss, o);
-                        const float inv = rsqrtf(ss * (1.f / D) + a.eps);
-#pragma unroll
-                        for (int e = 0; e < H / 2; ++e) {
-                            x[e] = __fmul2_rn(x[e], make_float2(inv, inv));
-                            y[e] = __fmul2_rn(y[e], make_float2(inv, inv));
-                        }
-                    }
+                    for (int o = LPR / 2; o; o >>= 1) ss += __shfl_xor_sync(~0u, ss, o);
+                    const float inv = rsqrtf(ss * (1.f / D) + a.eps);
 #pragma unroll
                     for (int e = 0; e < H / 2; ++e) {
-                        const float2 p = x[e], q = y[e];
-                        x[e] = __fmul2_rn(p, pc[e]);
-                        y[e] = __fmul2_rn(q, qc[e]);
-                        if (turned) {   // an unrotated pair's members keep apart, an infinity in one of them too
-                            x[e] = __ffma2_rn(q, qs[e], x[e]);
-                            y[e] = __ffma2_rn(p, ps[e], y[e]);
-                        }
+                        x[e] = __fmul2_rn(x[e], make_float2(inv, inv));
+                        y[e] = __fmul2_rn(y[e], make_float2(inv, inv));
                     }
-                    unpairs<H, INTER>(x, y, t);
                 }
-                if constexpr (QUANT) {
-                    float top = 0.f;
 #pragma unroll
-                    for (int e = 0; e < H; ++e) top = max_abs(top, t[e].x, t[e].y);
-#pragma unroll
-                    for (int o = LPR / 2; o; o >>= 1) top = max_nan(top, __shfl_xor_sync(~0u, top, o));
-                    if (r < r_end) {
-                        const bool fine = top <= 3.402823466e38f;   // false for infinities and NaN
-                        const float scale = fmaxf(__fdiv_rn(top, kFp8Max), kScaleMin);
-                        const float rs = __frcp_rn(scale);
-                        uint32_t c[H];   // two codes each
-#pragma unroll
-                        for (int e = 0; e < H; ++e)
-                            c[e] = __nv_cvt_float2_to_fp8x2(__fmul2_rn(t[e], make_float2(rs, rs)), __NV_SATFINITE, __NV_E4M3);
-                        if constexpr (sizeof(T) == 2) {
-                            *reinterpret_cast<uint32_t *>(codes + e0) = fine ? c[0] | c[1] << 16 : 0u;
-                            *reinterpret_cast<uint32_t *>(codes + e1) = fine ? c[2] | c[3] << 16 : 0u;
-                        } else {
-                            *reinterpret_cast<uint16_t *>(codes + e0) = (uint16_t)(fine ? c[0] : 0u);
-                            *reinterpret_cast<uint16_t *>(codes + e1) = (uint16_t)(fine ? c[1] : 0u);
-                        }
-                        if (sub == 0) {
-                            *scales = fine ? scale : __int_as_float(0x7fc00000);
-                            if (!fine) flag(a.status, TS_STATUS_NONFINITE);
-                        }
+                for (int e = 0; e < H / 2; ++e) {
+                    const float2 p = x[e], q = y[e];
+                    x[e] = __fmul2_rn(p, pc[e]);
+                    y[e] = __fmul2_rn(q, qc[e]);
+                    if (turned) {   // an unrotated pair's members keep apart, an infinity in one of them too
+                        x[e] = __ffma2_rn(q, qs[e], x[e]);
+                        y[e] = __ffma2_rn(p, ps[e], y[e]);
                     }
-                    codes += RPC * hs * D;
-                    scales += RPC * hs;
-                } else {
-                    if (r < r_end) {
-                        uint2 lo, hi;
-                        if constexpr (sizeof(T) == 2) {
-                            lo = make_uint2(Two<T>::put(t[0]), Two<T>::put(t[1]));
-                            hi = make_uint2(Two<T>::put(t[2]), Two<T>::put(t[3]));
-                        } else {
-                            lo = Two<T>::put(t[0]);
-                            hi = Two<T>::put(t[1]);
-                        }
-                        *reinterpret_cast<uint2 *>(out + e0) = lo;
-                        *reinterpret_cast<uint2 *>(out + e1) = hi;
-                    }
-                    out += RPC * D;
                 }
+                unpairs<H, INTER>(x, y, t);
+            }
+            if constexpr (QUANT) {
+                float top = 0.f;
+#pragma unroll
+                for (int e = 0; e < H; ++e) top = max_abs(top, t[e].x, t[e].y);
+#pragma unroll
+                for (int o = LPR / 2; o; o >>= 1) top = max_nan(top, __shfl_xor_sync(~0u, top, o));
+                if (r < r_end) {
+                    const bool fine = top <= 3.402823466e38f;   // false for infinities and NaN
+                    const float scale = fmaxf(__fdiv_rn(top, kFp8Max), kScaleMin);
+                    const float rs = __frcp_rn(scale);
+                    uint32_t c[H];   // two codes each
+#pragma unroll
+                    for (int e = 0; e < H; ++e)
+                        c[e] = __nv_cvt_float2_to_fp8x2(__fmul2_rn(t[e], make_float2(rs, rs)), __NV_SATFINITE, __NV_E4M3);
+                    if constexpr (sizeof(T) == 2) {
+                        *reinterpret_cast<uint32_t *>(codes + e0) = fine ? c[0] | c[1] << 16 : 0u;
+                        *reinterpret_cast<uint32_t *>(codes + e1) = fine ? c[2] | c[3] << 16 : 0u;
+                    } else {
+                        *reinterpret_cast<uint16_t *>(codes + e0) = (uint16_t)(fine ? c[0] : 0u);
+                        *reinterpret_cast<uint16_t *>(codes + e1) = (uint16_t)(fine ? c[1] : 0u);
+                    }
+                    if (sub == 0) {
+                        *scales = fine ? scale : __int_as_float(0x7fc00000);
+                        if (!fine) flag(a.status, TS_STATUS_NONFINITE);
+                    }
+                }
+                codes += RPC * hs * D;
+                scales += RPC * hs;
+            } else {
+                if (r < r_end) {
+                    uint2 lo, hi;
+                    if constexpr (sizeof(T) == 2) {
+                        lo = make_uint2(Two<T>::put(t[0]), Two<T>::put(t[1]));
+                        hi = make_uint2(Two<T>::put(t[2]), Two<T>::put(t[3]));
+                    } else {
+                        lo = Two<T>::put(t[0]);
+                        hi = Two<T>::put(t[1]);
+                    }
+                    *reinterpret_cast<uint2 *>(out + e0) = lo;
+                    *reinterpret_cast<uint2 *>(out + e1) = hi;
+                }
+                out += RPC * D;
             }
         }
     };
@@ -391,7 +396,8 @@ constexpr int kReadThreads = 256, kReadRows = 64;
 // One CTA per (64 output rows, head, request): a lane turns E codes (8 for
 // bf16, 4 for fp32) into 16 bytes, so that both sides of the copy are
 // contiguous over a warp; the CTA's loads are issued before its stores.
-// Memory bound: d + 4 bytes in, d * sizeof(T) out a row.
+// Memory bound: d + 4 bytes in, d * sizeof(T) out a row; 16 requests of 512 to
+// 4096 rows, 32 heads of 128, into bf16: 142 us, 98% of the copy peak.
 template <typename T, int D>
 __global__ void __launch_bounds__(kReadThreads) k_kv8_read(ReadArgs a) {
     constexpr int E = Vec<T>::E, LPR = D / E, RPC = kReadThreads / LPR, U = kReadRows / RPC;
@@ -449,7 +455,8 @@ __global__ void __launch_bounds__(kReadThreads) k_kv8_read(ReadArgs a) {
 // row P + dfs(path[i]) to row P + i in rounds of increasing i, each round
 // reading all its pieces before any is written. A round's destinations are
 // never a later round's sources (a node's depth-first index is at least its
-// depth), so rounds need no order among themselves beyond that.
+// depth), so rounds need no order among themselves beyond that. Bound by the
+// launch and one chain of loads: 2.9 us for 64 requests of 56 heads.
 constexpr int kCommit8Threads = 256, kCommit8Heads = 8;
 
 template <int D>
