@@ -196,3 +196,35 @@ def test_ragged_lengths_with_joined_parts():
     assert s.status.item() == 0
     assert all(torch.equal(outs[0], x) for x in outs[1:])
     check_attention(s, q, kv, outs[0], torch.full_like(q, 7.0))
+
+
+def test_one_workspace_for_calls_of_several_sizes():
+    """Cut items of few and of many slots, one after another on the workspace of the largest: nothing that one call
+    leaves is taken for another's counters."""
+    cases = [([1] * 8, [2048] * 8, 32, 8, 128), ([3], [700], 2, 1, 64), ([40, 9], [5000, 1200], 8, 2, 128),
+             ([1] * 8, [2048] * 8, 32, 8, 128)]
+    setups = []
+    for i, (n, P, Hq, Hk, d) in enumerate(cases):
+        s = Setup(n, P, seed=30 + i)
+        kv = s.cache(Hk, d)
+        setups.append((s, kv, s.randn(s.B, s.n_max, Hq, d), api.kv8_workspace(s.B, Hq, Hk, s.n_max, d, kv.L_max)))
+    one = torch.zeros(max(w.numel() for *_, w in setups), dtype=torch.uint8, device="cuda")
+    for _ in range(2):
+        for s, kv, q, ws in setups:
+            own, shared = torch.full_like(q, 7.0), torch.full_like(q, 7.0)
+            api.tree_attention_kv8(own, q, kv, s.prefix, s.tree, ws=ws, status=s.status)
+            api.tree_attention_kv8(shared, q, kv, s.prefix, s.tree, ws=one, status=s.status)
+            assert torch.equal(own, shared) and s.status.item() == 0
+            check_attention(s, q, kv, shared, torch.full_like(q, 7.0))
+
+
+def test_every_request_rejected():
+    s = Setup([0, 0], [5, 9], n_max=4, seed=40)
+    kv = api.KV8.dense(2, 2, 64, 128)
+    q = s.randn(2, 4, 4, 128)
+    out = torch.full_like(q, 7.0)
+    ws = api.kv8_workspace(2, 4, 2, 4, 128, 64)
+    for _ in range(2):
+        api.tree_attention_kv8(out, q, kv, s.prefix, s.tree, ws=ws, status=s.status)
+        api.kv8_append(kv, q[:, :, :2].contiguous(), q[:, :, :2].contiguous(), s.prefix, s.tree, status=s.status)
+    assert (out == 7.0).all() and (kv.k.view(torch.uint8) == 0).all() and s.status.item() == 0

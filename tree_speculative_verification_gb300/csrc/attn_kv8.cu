@@ -1269,7 +1269,9 @@ struct Plan8 {
 };
 
 // RP: the rows there can be, cut into equal blocks of at most 64, rounded up to
-// 16. Slots: no more than there can be parts.
+// 16. Slots: no more than there can be parts. The counters (queue, joins) lie
+// ahead of every size's parts, so that one workspace serves calls of any sizes
+// it is large enough for, one after another.
 Plan8 plan8(int B, int Hkv, int G, int n_max, int d) {
     Plan8 p;
     const long long rows = (long long)n_max * G;
@@ -1278,7 +1280,7 @@ Plan8 plan8(int B, int Hkv, int G, int n_max, int d) {
     p.blocks = (int)((rows + p.rp - 1) / p.rp);
     const long long most = (long long)B * Hkv * p.blocks * kMaxCuts;
     p.slots = B > kReqCache ? 0 : (int)(most < kSlotsPerSm * num_sms() ? most : kSlotsPerSm * num_sms());
-    size_t at = 256 + ((size_t)p.slots * sizeof(unsigned) + 255) / 256 * 256;
+    size_t at = 256 + ((size_t)kSlotsPerSm * num_sms() * sizeof(unsigned) + 255) / 256 * 256;
     p.ml = at;
     at += (size_t)p.slots * p.rp * sizeof(float2);
     p.o = (at + 255) / 256 * 256;
