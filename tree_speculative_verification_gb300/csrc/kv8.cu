@@ -351,11 +351,12 @@ cudaError_t rows_launch(RowArgs &a, cudaStream_t s) {
     // a projection's heads are split over CTAs only while that gives each SM more to do
     int ctas = 0;
     for (int i = 0; i < 3; ++i) {
+        if (!a.heads[i]) continue;   // left out: no groups
         const int most = (a.heads[i] + RPC - 1) / RPC;
         const int least = (most + kRowPasses - 1) / kRowPasses;
         const int groups = (int)std::max<long long>(least, std::min<long long>(most, num_sms() / nodes));
         a.per_group[i] = ((a.heads[i] + groups - 1) / groups + RPC - 1) / RPC * RPC;
-        a.groups[i] = a.heads[i] ? (a.heads[i] + a.per_group[i] - 1) / a.per_group[i] : 0;
+        a.groups[i] = (a.heads[i] + a.per_group[i] - 1) / a.per_group[i];
         ctas += a.groups[i];
     }
     const dim3 grid((unsigned)nodes, ctas);
