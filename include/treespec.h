@@ -406,8 +406,9 @@ ts_status tree_qk_norm_rope(void *q_out, void *k_out, const void *q, const void 
  * values are code * scale. Dense (block_table NULL): codes [B][H][L_max][d],
  * scales [B][H][L_max]. Paged: codes [num_pages][H][TS_PAGE_KEYS][d], scales
  * [num_pages][H][TS_PAGE_KEYS], rows found through block_table [B][max_pages]
- * as in ts_paged_kv; L_max is then not read. H counts the key/value heads. Host struct of device pointers
- * owned by the caller; codes 16-byte aligned.
+ * as in ts_paged_kv; L_max is then not read. H counts the key/value heads. Fewer
+ * than 2^31 - 256 (row, head) pairs. Host struct of device pointers owned by the
+ * caller; codes 16-byte aligned.
  */
 typedef struct ts_kv8 {
     uint8_t *k, *v;
@@ -425,8 +426,9 @@ typedef struct ts_kv8 {
  * even. With rope != NULL the keys are first normed and rotated as in
  * tree_qk_norm_rope (in fp32, not rounded in between), and the queries
  * q [B][n_max] (Hq heads) are normed and rotated into q_out in the same pass
- * (Hq = 0: no queries). k_new and v_new: rows of kv->H heads, k_stride / v_stride elements
- * from one node to the next, as for tree_qk_norm_rope; dtype of q, k_new, v_new, q_out.
+ * (Hq = 0: no queries). k_new and v_new: rows of kv->H heads, k_stride / v_stride
+ * elements from one node to the next, as for tree_qk_norm_rope; dtype of q,
+ * k_new, v_new, q_out.
  * A row with a non-finite value gets codes 0 and scale NaN, so that only nodes
  * that attend to it see it (TS_STATUS_NONFINITE). A request whose rows pass the
  * cache's end, or with a page id outside the table's range, is skipped, its
@@ -452,14 +454,17 @@ ts_status kv8_read(void *k_out, void *v_out, const ts_kv8 *kv, const int32_t *ro
  * tree_attention_kv8 -- tree_attention over an 8-bit cache, with grouped query
  * heads: query head h reads key/value head h / (Hq / kv->H). q, out
  * [B][n_max][Hq][d] bf16, Hq a multiple of kv->H. The softmax and all sums are
- * fp32. Node rows v >= n_nodes[b] are left as they were, as are all rows of a
- * request whose keys pass the cache's end (TS_STATUS_INDEX). Rows of the cache from prefix_len[b] +
- * n_nodes[b] on may hold anything. A page id outside [0, num_pages) reads as
- * zeros and sets TS_STATUS_INDEX. t must be as tree_build fills it (n_nodes,
+ * fp32; the weights that meet V keep nine bits. Node rows v >= n_nodes[b] are
+ * left as they were, as are all rows of a request whose keys pass the cache's
+ * end (TS_STATUS_INDEX). Rows of the cache from prefix_len[b] + n_nodes[b] on may
+ * hold anything. A page id outside [0, num_pages) reads as zeros and sets
+ * TS_STATUS_INDEX. t must be as tree_build fills it (n_nodes,
  * perm and sub_end are read). scale <= 0 selects 1/sqrt(d). ws: at least
  * treespec_kv8_workspace_size(...) bytes, zero-filled before its first use
- * (treespec_workspace_init); calls leave what must be zero so. Calls that share
- * one ws must not overlap on the GPU, two captured graphs that hold them included.
+ * (treespec_workspace_init); calls leave what must be zero so (after
+ * TS_STATUS_TIMEOUT it has to be filled again), and may be of several sizes.
+ * Calls that share one ws must not overlap on the GPU, two captured graphs that
+ * hold them included.
  */
 ts_status tree_attention_kv8(void *out, const void *q, const ts_kv8 *kv, int Hq, const int32_t *prefix_len,
                              const ts_tree *t, float scale, void *ws, size_t ws_bytes, uint32_t *status,

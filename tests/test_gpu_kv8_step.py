@@ -228,3 +228,59 @@ def test_every_request_rejected():
         api.tree_attention_kv8(out, q, kv, s.prefix, s.tree, ws=ws, status=s.status)
         api.kv8_append(kv, q[:, :, :2].contiguous(), q[:, :, :2].contiguous(), s.prefix, s.tree, status=s.status)
     assert (out == 7.0).all() and (kv.k.view(torch.uint8) == 0).all() and s.status.item() == 0
+
+
+def test_offsets_past_32_bits():
+    """Two requests of four heads whose second codes lie past 2^32 bytes: append, attention, commit and read there are
+    those of a small cache."""
+    rows, H, d = (1 << 32) // (4 * 128) + 4096, 4, 128
+    s = Setup([20, 20], [300, 300], seed=50)
+    k, v = s.randn(2, 20, H, d), s.randn(2, 20, H, d)
+    q = s.randn(2, 20, 8, d)
+    path = torch.full((2, 21), -1, dtype=torch.int32, device="cuda")
+    path[:, 0], count = 0, torch.ones(2, dtype=torch.int32, device="cuda")
+    far = torch.tensor([rows - 20, rows - 20], dtype=torch.int32, device="cuda")
+    small = s.cache(H, d)
+    got = []
+    for L in (small.L_max, rows):
+        kv = api.KV8.dense(2, H, L, d)
+        for x, y in ((kv.k, small.k), (kv.v, small.v)):
+            x.view(torch.uint8)[:, :, :300] = y.view(torch.uint8)[:, :, :300]
+        kv.k_scale[:, :, :300], kv.v_scale[:, :, :300] = small.k_scale[:, :, :300], small.v_scale[:, :, :300]
+        out, new = torch.zeros_like(q), torch.zeros_like(s.prefix)
+        api.kv8_append(kv, k, v, s.prefix, s.tree, status=s.status)
+        ws = api.kv8_workspace(2, 8, H, 20, d, L)
+        api.tree_attention_kv8(out, q, kv, s.prefix, s.tree, ws=ws, status=s.status)
+        api.kv8_commit(kv, s.prefix, new, path, count, s.tree, status=s.status)
+        ko, vo = (torch.zeros(2, H, 320, d, device="cuda") for _ in "kv")
+        api.kv8_read(ko, vo, kv, s.prefix + 20, status=s.status)
+        got.append([out, new, ko, vo])
+        if L == rows:   # the cache's last rows
+            api.kv8_append(kv, k, v, far, s.tree, status=s.status)
+            kf, vf = (torch.zeros(2, H, 20, d, device="cuda") for _ in "kv")
+            api.kv8_read(kf, vf, kv, far + 20, far, status=s.status)
+            assert torch.equal(kf, ko[:, :, 300:]) and torch.equal(vf, vo[:, :, 300:])
+    assert s.status.item() == 0
+    assert all(torch.equal(a, b) for a, b in zip(*got))
+    assert (got[0][2][:, :, :320] != 0).any(-1).all()
+
+
+def test_two_calls_at_once():
+    """Calls on two streams, each with a workspace of its own, over one cache."""
+    s = Setup([12, 30, 7], [900, 2500, 64], seed=60)
+    kv = s.cache(2, 128)
+    q = [s.randn(3, 30, 8, 128) for _ in range(2)]
+    ws = [api.kv8_workspace(3, 8, 2, 30, 128, kv.L_max) for _ in range(2)]
+    want, streams = [], [torch.cuda.Stream() for _ in range(2)]
+    for i in range(2):
+        want.append(torch.full_like(q[i], 7.0))
+        api.tree_attention_kv8(want[i], q[i], kv, s.prefix, s.tree, ws=ws[i], status=s.status)
+    got = [[torch.full_like(q[i], 7.0) for _ in range(8)] for i in range(2)]
+    torch.cuda.synchronize()
+    for r in range(8):
+        for i in range(2):
+            with torch.cuda.stream(streams[i]):
+                api.tree_attention_kv8(got[i][r], q[i], kv, s.prefix, s.tree, ws=ws[i], status=s.status)
+    torch.cuda.synchronize()
+    assert s.status.item() == 0
+    assert all(torch.equal(x, want[i]) for i in range(2) for x in got[i])
