@@ -357,11 +357,12 @@ def kv_commit_paged(kv: PagedKV, prefix_len, new_prefix_len, out_path, out_count
 
 
 # -- head norms with rotation, and the 8-bit KV cache -----------------------------
-# Checks are written as tests around a raise, so that a call that passes builds no message.
+# A short call's time is the host's, so checks are tests around a raise (a call that passes builds no message), devices
+# are compared by their index, and contiguous rows take no look at strides.
 def _int_array(t, n, name, device):
-    """Pointer of an int32 tensor of at least n entries on `device`."""
-    if t.dtype != torch.int32 or t.numel() < n or t.device != device or not t.is_contiguous():
-        raise TreespecError(f"{name} must be a contiguous int32 tensor of {n} entries on {device}")
+    """Pointer of an int32 tensor of at least n entries on CUDA device number `device`."""
+    if t.dtype is not torch.int32 or t.numel() < n or t.get_device() != device or not t.is_contiguous():
+        raise TreespecError(f"{name} must be a contiguous int32 tensor of {n} entries on CUDA device {device}")
     return t.data_ptr()
 
 
@@ -369,13 +370,15 @@ def _status_ptr(status, device):
     return None if status is None else _int_array(status, 1, "status", device)
 
 
-def _node_rows(t, tree, H, d, name, dtype, device):
-    """(pointer, elements from one node to the next) of node rows [B][n_max][H][d]: heads contiguous, nodes and
-    requests a constant stride apart (a slice of a wider projection output)."""
-    B, n = tree.B, tree.n_max
-    if t.dtype != dtype or t.device != device or t.shape != (B, n, H, d):
-        raise TreespecError(f"{name} must be a {dtype} tensor {(B, n, H, d)} on {device}, not {t.dtype} {tuple(t.shape)} "
-                            f"on {t.device}")
+def _node_rows(t, shape, name, dtype, device):
+    """(pointer, elements from one node to the next) of node rows `shape` = (B, n_max, H, d): heads contiguous, nodes
+    and requests a constant stride apart (a slice of a wider projection output)."""
+    if t.dtype is not dtype or t.get_device() != device or t.shape != shape:
+        raise TreespecError(f"{name} must be a {dtype} tensor {shape} on CUDA device {device}, not {t.dtype} "
+                            f"{tuple(t.shape)} on {t.device}")
+    B, n, H, d = shape
+    if t.is_contiguous():
+        return t.data_ptr(), H * d
     sb, sn, sh, sd = t.stride()
     if n == 1:
         sn = sb if B > 1 else H * d
@@ -384,22 +387,22 @@ def _node_rows(t, tree, H, d, name, dtype, device):
     return t.data_ptr(), sn
 
 
-def _out_rows(t, tree, H, d, name, dtype, device):
-    if t.dtype != dtype or t.device != device or t.shape != (tree.B, tree.n_max, H, d) or not t.is_contiguous():
-        raise TreespecError(f"{name} must be a contiguous {dtype} tensor {(tree.B, tree.n_max, H, d)} on {device}")
+def _out_rows(t, shape, name, dtype, device):
+    if t.dtype is not dtype or t.get_device() != device or t.shape != shape or not t.is_contiguous():
+        raise TreespecError(f"{name} must be a contiguous {dtype} tensor {shape} on CUDA device {device}")
     return t.data_ptr()
 
 
 def _same_device(tree, device):
-    if tree.n_nodes.device != device:
-        raise TreespecError(f"the tree is on {tree.n_nodes.device}, not {device}")
+    if tree.n_nodes.get_device() != device:
+        raise TreespecError(f"the tree is on {tree.n_nodes.device}, not on CUDA device {device}")
 
 
 def _run(fn, what, device, stream, *args):
-    """Call an entry point on the current stream of the tensors' device (or the given one)."""
+    """Call an entry point on the current stream of CUDA device number `device` (or on the given one)."""
     # the stream's handle alone: torch.cuda.current_stream() makes an object of it, a quarter of a short call's time
-    handle = torch._C._cuda_getCurrentRawStream(device.index) if stream is None else stream.cuda_stream
-    if device.index == torch.cuda.current_device():
+    handle = torch._C._cuda_getCurrentRawStream(device) if stream is None else stream.cuda_stream
+    if device == torch._C._cuda_getDevice():
         rc = fn(*args, handle)
     else:
         with torch.cuda.device(device):
@@ -420,7 +423,7 @@ class QKRope:
                     and x.device == given[0].device):
                 raise TreespecError("inv_freq and weights must be contiguous fp32 vectors on one CUDA device")
         self.inv_freq, self.q_weight, self.k_weight = inv_freq, q_weight, k_weight
-        self.device = given[0].device if given else None
+        self.device = given[0].get_device() if given else None
         self.rot_dim = 0 if inv_freq is None else 2 * inv_freq.numel()
         p = lambda x: None if x is None else x.data_ptr()
         self._c = ts_qk_rope(p(inv_freq), p(q_weight), p(k_weight), float(eps), int(bool(norm)), self.rot_dim,
@@ -429,7 +432,7 @@ class QKRope:
 
     def _for(self, d, device):
         if self.device is not None and self.device != device:
-            raise TreespecError(f"the rotation's tensors are on {self.device}, not {device}")
+            raise TreespecError(f"the rotation's tensors are on CUDA device {self.device}, not {device}")
         for w in (self.q_weight, self.k_weight):
             if w is not None and w.numel() != d:
                 raise TreespecError(f"norm weights must have head_dim {d} entries")
@@ -447,16 +450,19 @@ def tree_qk_norm_rope(q_out, k_out, q, k, rope: QKRope, tree: Tree, status=None,
     x = q if q is not None else k
     if x is None or not x.is_cuda or x.dim() != 4:
         raise TreespecError("q or k [B][n_max][H][d] on a CUDA device is needed")
-    dev, d, dt = x.device, x.shape[3], _dtype(x)
+    dev, d, dt, dtype = x.get_device(), x.shape[3], _dtype(x), x.dtype
     _same_device(tree, dev)
+    B, n = tree.B, tree.n_max
     qp = kp = qo = ko = None
     Hq = Hk = qs = ks = 0
     if q is not None:
         Hq = q.shape[2]
-        (qp, qs), qo = _node_rows(q, tree, Hq, d, "q", x.dtype, dev), _out_rows(q_out, tree, Hq, d, "q_out", x.dtype, dev)
+        shape = (B, n, Hq, d)
+        (qp, qs), qo = _node_rows(q, shape, "q", dtype, dev), _out_rows(q_out, shape, "q_out", dtype, dev)
     if k is not None:
         Hk = k.shape[2]
-        (kp, ks), ko = _node_rows(k, tree, Hk, d, "k", x.dtype, dev), _out_rows(k_out, tree, Hk, d, "k_out", x.dtype, dev)
+        shape = (B, n, Hk, d)
+        (kp, ks), ko = _node_rows(k, shape, "k", dtype, dev), _out_rows(k_out, shape, "k_out", dtype, dev)
     _run(load_library().tree_qk_norm_rope, "tree_qk_norm_rope", dev, stream, qo, ko, qp, kp, Hq, Hk, d, qs, ks,
          rope._for(d, dev), tree.c, dt, _status_ptr(status, dev))
 
@@ -476,14 +482,14 @@ class KV8:
             if not (x.is_cuda and x.is_contiguous() and x.device == k.device):
                 raise TreespecError("cache tensors must be contiguous on one CUDA device")
         self.k, self.v, self.k_scale, self.v_scale, self.block_table = k, v, k_scale, v_scale, block_table
-        self.H, self.d, self.device = k.shape[1], k.shape[3], k.device
+        self.H, self.d, self.device = k.shape[1], k.shape[3], k.get_device()
         pages = 0
         if block_table is not None:
             if k.shape[2] != PAGE_KEYS:
                 raise TreespecError(f"a page holds {PAGE_KEYS} keys")
             if block_table.dim() != 2:
                 raise TreespecError("block_table must be [B][max_pages]")
-            _int_array(block_table, 1, "block_table", k.device)
+            _int_array(block_table, 1, "block_table", self.device)
             self.B, pages = block_table.shape
             self.L_max = pages * PAGE_KEYS
         else:
@@ -518,17 +524,18 @@ def kv8_append(kv: KV8, k_new, v_new, prefix_len, tree: Tree, rope: QKRope | Non
     """Quantise the pass's K/V [B][n_max][H][d] into the cache rows P + dfs; with rope the keys are normed and rotated
     on the way, and the queries q, if given, into q_out."""
     ref, dev, d = kv._with(tree), kv.device, kv.d
-    dt = _dtype(k_new)
-    kp, ks = _node_rows(k_new, tree, kv.H, d, "k_new", k_new.dtype, dev)
-    vp, vs = _node_rows(v_new, tree, kv.H, d, "v_new", k_new.dtype, dev)
+    dt, dtype, shape = _dtype(k_new), k_new.dtype, (tree.B, tree.n_max, kv.H, d)
+    kp, ks = _node_rows(k_new, shape, "k_new", dtype, dev)
+    vp, vs = _node_rows(v_new, shape, "v_new", dtype, dev)
     qp = qo = r = None
     Hq = qs = 0
     if q is not None:
         if rope is None or q_out is None:
             raise TreespecError("queries are only taken with rope, and need q_out")
         Hq = q.shape[2]
-        qp, qs = _node_rows(q, tree, Hq, d, "q", k_new.dtype, dev)
-        qo = _out_rows(q_out, tree, Hq, d, "q_out", k_new.dtype, dev)
+        shape = (tree.B, tree.n_max, Hq, d)
+        qp, qs = _node_rows(q, shape, "q", dtype, dev)
+        qo = _out_rows(q_out, shape, "q_out", dtype, dev)
     if rope is not None:
         r = rope._for(d, dev)
     _run(load_library().kv8_append, "kv8_append", dev, stream, ref, kp, vp, ks, vs, r, qo, qp, Hq, qs,
@@ -541,8 +548,8 @@ def kv8_read(k_out, v_out, kv: KV8, row_end, row_begin=None, status=None, stream
     dev = kv.device
     shape = (kv.B, kv.H, k_out.shape[2] if k_out.dim() == 4 else 0, kv.d)
     for x in (k_out, v_out):
-        if x.shape != shape or x.dtype != k_out.dtype or x.device != dev or not x.is_contiguous():
-            raise TreespecError(f"k_out and v_out must be contiguous tensors {shape} of one dtype on {dev}")
+        if x.shape != shape or x.dtype is not k_out.dtype or x.get_device() != dev or not x.is_contiguous():
+            raise TreespecError(f"k_out and v_out must be contiguous tensors {shape} of one dtype on CUDA device {dev}")
     begin = None if row_begin is None else _int_array(row_begin, kv.B, "row_begin", dev)
     _run(load_library().kv8_read, "kv8_read", dev, stream, k_out.data_ptr(), v_out.data_ptr(), kv._ref, begin,
          _int_array(row_end, kv.B, "row_end", dev), shape[2], _dtype(k_out), _status_ptr(status, dev))
@@ -561,10 +568,11 @@ def tree_attention_kv8(out, q, kv: KV8, prefix_len, tree: Tree, scale: float = 0
     if q.dim() != 4:
         raise TreespecError("q must be [B][n_max][Hq][d]")
     Hq = q.shape[2]
-    op = _out_rows(out, tree, Hq, kv.d, "out", torch.bfloat16, dev)
-    qp = _out_rows(q, tree, Hq, kv.d, "q", torch.bfloat16, dev)
-    if ws is None or ws.device != dev or not ws.is_contiguous():
-        raise TreespecError(f"a workspace (kv8_workspace) on {dev} is needed")
+    shape = (tree.B, tree.n_max, Hq, kv.d)
+    op = _out_rows(out, shape, "out", torch.bfloat16, dev)
+    qp = _out_rows(q, shape, "q", torch.bfloat16, dev)
+    if ws is None or ws.get_device() != dev or not ws.is_contiguous():
+        raise TreespecError(f"a workspace (kv8_workspace) on CUDA device {dev} is needed")
     _run(load_library().tree_attention_kv8, "tree_attention_kv8", dev, stream, op, qp, ref, Hq,
          _int_array(prefix_len, tree.B, "prefix_len", dev), tree.c, float(scale), ws.data_ptr(),
          ws.numel() * ws.element_size(), _status_ptr(status, dev))
