@@ -147,8 +147,8 @@ __device__ __forceinline__ void unpairs(const float2 (&x)[H / 2], const float2 (
 // 56 + 56 heads of 128). What bounds a large call next to memory is issuing
 // (69% of the slots in that append): the loop is compiled once for each kind of
 // row (query, key, value), and a CTA runs one of them; one loop for all kinds
-// took 56 us. Measured there: norm and rotation of q and k 30.5 us (172 MB, 83%
-// of the copy peak), the append with its codes 45.4 us (217 MB, 70%). The
+// took 56 us. Measured there: norm and rotation of q and k 30.1 us (172 MB, 84%
+// of the copy peak), the append with its codes 45.3 us (217 MB, 71%). The
 // divisions are the definition's and cost 1.6 us of that.
 template <typename T, int D, bool APPEND, bool INTER>
 __global__ void __launch_bounds__(kRowThreads) k_head_rows(RowArgs a) {
@@ -157,7 +157,7 @@ __global__ void __launch_bounds__(kRowThreads) k_head_rows(RowArgs a) {
     __shared__ __align__(16) uint8_t rows_s[kRowPasses * RPC * ROW];
     __shared__ float2 cs_s[D / 2];
     __shared__ int bad_s;
-    const int n_max = a.t.n_max, b = blockIdx.x / n_max, v = blockIdx.x - b * n_max;
+    const int n_max = a.t.n_max, b = blockIdx.x / n_max, dfs = blockIdx.x - b * n_max;
     const int tid = threadIdx.x, sub = tid % LPR, slot = tid / LPR;
     const int half = a.rot_dim >> 1;
     const int kind = (int)blockIdx.y < a.groups[0] ? 0 : (int)blockIdx.y < a.groups[0] + a.groups[1] ? 1 : 2;
@@ -170,11 +170,12 @@ __global__ void __launch_bounds__(kRowThreads) k_head_rows(RowArgs a) {
     pdl_wait();
     pdl_trigger();
     const int n = a.t.n_nodes[b];
-    const int dfs = a.t.dfs_of[(size_t)b * n_max + v];
+    const int v = a.t.perm[blockIdx.x];   // of nodes past the last, too: no load waits for another
+    const int pos = kind < 2 && half ? a.t.pos[blockIdx.x] : 0;
     const int P = APPEND ? a.prefix_len[b] : 0;
-    if (v >= n || dfs < 0 || dfs >= n_max) return;
+    if (dfs >= n || v < 0 || v >= n_max) return;
     if (APPEND && (P < 0 || P > a.L_max - n)) {
-        if (v == 0 && blockIdx.y == 0 && tid == 0) flag(a.status, TS_STATUS_INDEX);
+        if (dfs == 0 && blockIdx.y == 0 && tid == 0) flag(a.status, TS_STATUS_INDEX);
         return;
     }
     const int part = blockIdx.y - (kind == 0 ? 0 : kind == 1 ? a.groups[0] : a.groups[0] + a.groups[1]);
@@ -196,7 +197,7 @@ __global__ void __launch_bounds__(kRowThreads) k_head_rows(RowArgs a) {
     }
     if (tid < half && kind < 2) {
         constexpr double kTwoPi = 6.283185307179586476925;
-        const double ang = (double)a.t.pos[(size_t)b * n_max + dfs] * (double)a.inv_freq[tid];
+        const double ang = (double)pos * (double)a.inv_freq[tid];
         const float r = (float)fma(-kTwoPi, rint(ang * (1.0 / kTwoPi)), ang);
         float sn, c;
         sincosf(r, &sn, &c);
@@ -205,7 +206,7 @@ __global__ void __launch_bounds__(kRowThreads) k_head_rows(RowArgs a) {
     cp_async_wait_all();
     __syncthreads();
     if (APPEND && bad_s) {
-        if (v == 0 && blockIdx.y == 0 && tid == 0) flag(a.status, TS_STATUS_INDEX);
+        if (dfs == 0 && blockIdx.y == 0 && tid == 0) flag(a.status, TS_STATUS_INDEX);
         return;
     }
     auto rows = [&](auto kind_c) {
