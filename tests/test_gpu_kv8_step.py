@@ -284,3 +284,19 @@ def test_two_calls_at_once():
     torch.cuda.synchronize()
     assert s.status.item() == 0
     assert all(torch.equal(x, want[i]) for i in range(2) for x in got[i])
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_unrotated_values_keep_to_themselves(dtype):
+    """Without the norm, an infinity behind the rotated part stays in its place, and one inside reaches its pair only."""
+    s = Setup([5], [3], seed=70)
+    rope = api.QKRope(api.QKRope.frequencies(64, device="cuda"), norm=False)
+    q = s.randn(1, 5, 3, 128, dtype=dtype)
+    want, got = torch.zeros_like(q), torch.zeros_like(q)
+    api.tree_qk_norm_rope(want, None, q, None, rope, s.tree)
+    q[0, 2, 1, 70], q[0, 3, 0, 7] = float("inf"), float("-inf")
+    api.tree_qk_norm_rope(got, None, q, None, rope, s.tree)
+    assert got[0, 2, 1, 70] == float("inf") and not torch.isfinite(got[0, 3, 0, 7]) and not torch.isfinite(got[0, 3, 0, 39])
+    want[0, 2, 1, 70] = want[0, 3, 0, 7] = want[0, 3, 0, 39] = 0
+    got[0, 2, 1, 70] = got[0, 3, 0, 7] = got[0, 3, 0, 39] = 0
+    assert torch.equal(want, got)
