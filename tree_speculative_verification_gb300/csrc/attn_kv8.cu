@@ -902,7 +902,7 @@ __global__ void __launch_bounds__(Cfg8<D, RP>::THREADS, 1)
         int g = 0;
         for (int k = 0;; ++k) {
             const int r = k % kRing;
-            if (!wait_warp(iready + 8 * r, (uint32_t)(k / kRing) & 1u)) ok = false;
+            ok &= wait_warp(iready + 8 * r, (uint32_t)(k / kRing) & 1u);
             const Unit8 u = read_unit(r);   // all of the group go on, or none: here, or by the vote of the unit's first tile
             if (!ok || u.b < 0) {
                 if (bar_any(bar, 128, !ok)) ok = false;
@@ -1133,8 +1133,8 @@ __global__ void __launch_bounds__(Cfg8<D, RP>::THREADS, 1)
                 v[2 * c] = l[c].x;
                 v[2 * c + 1] = l[c].y;
             }
+            if (k >= 2) ok &= wait_warp(ofree + 8 * (k & 1), (uint32_t)(k / 2 - 1) & 1u);
             reduce_scatter<CG>(v, lane);
-            if (k >= 2 && !wait_warp(ofree + 8 * (k & 1), (uint32_t)(k / 2 - 1) & 1u)) ok = false;
             const uint32_t sum = fix_base + C::FIX_SUM + (k & 1) * C::SUM_BYTES;
             if (lane % (32 / CG) == 0) sts1(sum + (quarter * 64 + cb + lane / (32 / CG)) * 4, v[0]);
             if (gt < CG) {
