@@ -502,9 +502,6 @@ __global__ void __launch_bounds__(Cfg8<D, RP>::THREADS, 1)
     const uint32_t tmem = (uint32_t)misc[0];
     int longest = 0, same = 1;   // same: tiles and row blocks of every request
     if (planned) {
-        // How far to cut: parts of at most 1 / (i + 1) of the longest item, half a warp for each of 32 ways (lane =
-        // request). Items of one length take as many rounds over the SMs as they have units; others, handed out
-        // longest first, about their sum over the SMs and half a longest unit. Cut items have to fit the slots.
         const int4 rq0 = req_s[0];
 #pragma unroll 1
         for (int b = lane; b < B; b += 32) {
@@ -514,6 +511,12 @@ __global__ void __launch_bounds__(Cfg8<D, RP>::THREADS, 1)
         }
         longest = __reduce_max_sync(~0u, longest);
         same = __all_sync(~0u, same);
+    }
+    const bool cuts = longest > kMinCut;   // no item can be cut otherwise
+    if (cuts) {
+        // How far to cut: parts of at most 1 / (i + 1) of the longest item, half a warp for each of 32 ways (lane =
+        // request). Items of one length take as many rounds over the SMs as they have units; others, handed out
+        // longest first, about their sum over the SMs and half a longest unit. Cut items have to fit the slots.
         static_assert(C::THREADS >= 16 * 32, "half a warp a way");
         const int i = tid >> 4;
         if (warp < 16) {
@@ -712,9 +715,13 @@ __global__ void __launch_bounds__(Cfg8<D, RP>::THREADS, 1)
             // ---- the rest of the plan
             int units = 0;
             if (planned) {
-                // the way of the least cost (costs are positive: their bits order as they do), the least cutting of equal ones
-                const uint32_t cost = __float_as_uint(cost_s[lane]), least = __reduce_min_sync(~0u, cost);
-                const int pick = __ffs(__ballot_sync(~0u, cost == least)) - 1;
+                int pick = 0;
+                if (cuts) {
+                    // the way of the least cost (costs are positive: their bits order as they do), the least cutting of
+                    // equal ones
+                    const uint32_t cost = __float_as_uint(cost_s[lane]), least = __reduce_min_sync(~0u, cost);
+                    pick = __ffs(__ballot_sync(~0u, cost == least)) - 1;
+                }
                 const float rate = rate_of(part_tiles(longest, pick));
                 if (same) {
                     const int4 rq = req_s[0];
