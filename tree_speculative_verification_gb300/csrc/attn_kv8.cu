@@ -249,11 +249,12 @@ struct Cfg8 {
     static constexpr int D = D_, RP = RP_, CG = RP <= 32 ? 8 : 16, GROUPS = RP / CG;   // columns of a softmax group
     static constexpr int SM_WARPS = 4 * GROUPS, THREADS = 32 * (4 + SM_WARPS + 4);
     // Registers a thread: LAUNCH x THREADS at launch, handed from the eight other warps to the softmax's where 65536 /
-    // THREADS does not do for those. RP = 48: 640 x 96 = 61440 >= 256 x 56 + 384 x 120 = 60416; 64: 768 x 80 = 61440 =
-    // 256 x 48 + 512 x 96.
+    // THREADS does not do for those. RP = 48: 640 x 96 = 61440 >= 256 x 80 + 384 x 104 = 60416; 64: 768 x 80 = 61440 =
+    // 256 x 64 + 512 x 88. (With 56 and 48 for the others short units, whose output counts, take up to a quarter longer,
+    // long ones 1% less.)
     static constexpr int LAUNCH_REGS = RP == 64 ? 80 : RP == 48 ? 96 : 80;
-    static constexpr int SM_REGS = RP == 64 ? 96 : RP == 48 ? 120 : LAUNCH_REGS;
-    static constexpr int OTHER_REGS = RP == 64 ? 48 : RP == 48 ? 56 : LAUNCH_REGS;
+    static constexpr int SM_REGS = RP == 64 ? 88 : RP == 48 ? 104 : LAUNCH_REGS;
+    static constexpr int OTHER_REGS = RP == 64 ? 64 : RP == 48 ? 80 : LAUNCH_REGS;
     static_assert(32 * SM_WARPS * SM_REGS + 256 * OTHER_REGS <= THREADS * LAUNCH_REGS, "a split of the launch's registers");
     static constexpr int OP_BYTES = kTileKeys * D;             // codes of one operand tile
     static constexpr int STAGE_BYTES = 2 * OP_BYTES;
@@ -354,8 +355,8 @@ __device__ __forceinline__ void join_parts(const float2 *part_ml, const float *p
         }
     } else {
         // every column's maximum and sum first (lane = column, half of the parts), then two columns at a time, whose
-        // loads do not wait for one another (4 x 128 nodes, 64 heads, 16384 keys: 392 us against 403)
-        constexpr int COLS = RP / 4, EPL = D / 16;
+        // loads do not wait for one another (4 x 128 nodes, 64 heads, 16384 keys: 393 us against 403)
+        constexpr int COLS = RP / 4, EPL = D / 16, AHEAD = RP == 64 ? 1 : 4;   // more code costs more than it hides
         const int c0 = ((threadIdx.x >> 5) & 3) * COLS;
         const int mine = c0 + min(lane & 15, COLS - 1);
         float mx = -1e38f, sum = 0.f;
@@ -376,7 +377,7 @@ __device__ __forceinline__ void join_parts(const float2 *part_ml, const float *p
             float acc[EPL] = {};
             const float2 *pm = part_ml + c;
             const float *po = part_o + (size_t)c * D + (lane & 15) * EPL;
-#pragma unroll 4
+#pragma unroll AHEAD
             for (int s = 0; s < parts; ++s, pm += RP, po += (size_t)RP * D) {
                 const float w = ex2(__ldcg(&pm->x) - m);
 #pragma unroll
