@@ -46,10 +46,10 @@
 // Bounds, measured. A tile of 128 keys (33 KB at d = 128) has to pass an SM in
 // 0.74 us at the measured copy peak of 6.8 TB/s, and does with 16 rows a unit
 // (64 requests x 56 heads x 1040 keys: 153 us, 98% of the peak). With more rows
-// the softmax warps' latency bounds it: 32 rows 189 us (83%), 47 rows 211 us
-// (77%), where a tile costs 0.75 us and a unit of 9 tiles some 2 us more (first
+// the softmax warps' latency bounds it: 32 rows 189 us (83%), 47 rows 213 us
+// (76%), where a tile costs 0.75 us and a unit of 9 tiles some 2 us more (first
 // maxima, masked tile, sums). 64 rows take 0.8 us a tile (4 x 64 heads x 16512
-// keys x 128 nodes: 392 us, 701 TFLOP/s of attention arithmetic). What carried it
+// keys x 128 nodes: 393 us, 699 TFLOP/s of attention arithmetic). What carried it
 // there: two tiles of scores and two of probabilities in flight; one wait a tile
 // for both; no branch and few instructions in the common tile (its loop has to
 // stay in the instruction cache: a version of twice the code took 1.4 times as
