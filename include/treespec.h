@@ -454,9 +454,17 @@ ts_status kv8_read(void *k_out, void *v_out, const ts_kv8 *kv, const int32_t *ro
  * tree_attention_kv8 -- tree_attention over an 8-bit cache, with grouped query
  * heads: query head h reads key/value head h / (Hq / kv->H). q, out
  * [B][n_max][Hq][d] bf16, Hq a multiple of kv->H. The softmax and all sums are
- * fp32; the weights that meet V keep nine bits. Node rows v >= n_nodes[b] are
- * left as they were, as are all rows of a request whose keys pass the cache's
- * end (TS_STATUS_INDEX). Rows of the cache from prefix_len[b] + n_nodes[b] on may
+ * fp32. Two roundings to fewer bits:
+ *  - a query row counts as a sum of two e4m3 numbers a value: bf16's eight bits
+ *    for values down to 2^-10 of the row's largest, 2^-18 of it absolutely below;
+ *  - a key's weight in the product with V is its probability times its value
+ *    scale, and keeps nine bits down to 2^-15 of the largest such weight among
+ *    the keys the row sees, 2^-24 of it absolutely below. Rows that it does not
+ *    see, and rows whose weight is small, take nothing from the others, whatever
+ *    their size.
+ * Scales from 2^-100 to 2^100 (values up to 5e32) count exactly in the sums.
+ * Node rows v >= n_nodes[b] are left as they were, as are all rows of a request
+ * whose keys pass the cache's end (TS_STATUS_INDEX). Rows of the cache from prefix_len[b] + n_nodes[b] on may
  * hold anything. A page id outside [0, num_pages) reads as zeros and sets
  * TS_STATUS_INDEX. t must be as tree_build fills it (n_nodes,
  * perm and sub_end are read). scale <= 0 selects 1/sqrt(d). ws: at least

@@ -15,13 +15,19 @@
 //   a query row, scaled by a power of two to a largest value in [128, 256), is
 //   qh + ql with qh = e4m3(q), ql = e4m3(q - qh): bf16's eight bits exactly for
 //   values down to 2^-10 of the row's largest, 2^-18 of it absolutely below;
-//   a probability p (2^7 at the reference maximum) is rounded to fp16, whose
-//   upper byte is an e5m2 number: p0 = upper byte of p, p1 = of p - p0, p2 = of
-//   the rest, rounded. Nine bits down to 2^-15 of the weight at the reference,
-//   to 2^-24 of it absolutely below (a pair of e4m3 numbers would end at 2^-18:
-//   a long cache with one dominant key has weights there by the thousand).
-// Softmax: S * key scale * query scale is the exponent; the value scale times a
-// common reference is multiplied into p before it is split. Sums, maxima, O: fp32.
+//   a weight w = probability * value scale (2^7 at the reference) is rounded to
+//   fp16, whose upper byte is an e5m2 number: w0 = upper byte of w, w1 = of
+//   w - w0, w2 = of the rest, rounded. Nine bits down to 2^-15 of the weight at
+//   the reference, to 2^-24 of it absolutely below (a pair of e4m3 numbers would
+//   end at 2^-18: a long cache with one dominant key has weights there by the
+//   thousand).
+// Softmax: y = S * key scale * query scale is the exponent. What has to fit w's few
+// bits is e^y times the value scale, so the running maximum of a query row is that
+// of y + log2(value scale) over the keys the row sees: a large value that it does
+// not see, or that has no weight, takes no bits from the others. The sums are of
+// the probability alone, which then spans 2^-112 to 2^115 over the scales there
+// are; factors between two references are applied as their root, twice. Sums,
+// maxima, O: fp32.
 //
 // One CTA per SM takes units (request, head, RP query rows, range of tiles) from
 // a queue in the workspace, longest first; ranges are cut only as far as the
@@ -45,18 +51,18 @@
 //
 // Bounds, measured. A tile of 128 keys (33 KB at d = 128) has to pass an SM in
 // 0.74 us at the measured copy peak of 6.8 TB/s, and does with 16 rows a unit
-// (64 requests x 56 heads x 1040 keys: 153 us, 98% of the peak). With more rows
-// the softmax warps' latency bounds it: 32 rows 189 us (83%), 47 rows 213 us
-// (76%), where a tile costs 0.75 us and a unit of 9 tiles some 2 us more (first
-// maxima, masked tile, sums). 64 rows take 0.8 us a tile (4 x 64 heads x 16512
-// keys x 128 nodes: 393 us, 699 TFLOP/s of attention arithmetic). What carried it
+// (64 requests x 56 heads x 1040 keys: 152 us, 98% of the peak). With more rows
+// the softmax warps' latency bounds it: 32 rows 183 us (85%), 47 rows 206 us
+// (79%), and a unit of 9 tiles costs some 2 us beside its tiles (first maxima,
+// masked tile, sums). 64 rows take 0.9 us a tile (4 x 64 heads x 16512 keys x
+// 128 nodes: 395 us, 696 TFLOP/s of attention arithmetic). What carried it
 // there: two tiles of scores and two of probabilities in flight; one wait a tile
 // for both; no branch and few instructions in the common tile (its loop has to
 // stay in the instruction cache: a version of twice the code took 1.4 times as
 // long); units switched by other warps than the softmax's. A call of few tiles
 // is bound by its chain: 5 us until the plan is made and the first scores are
 // there, 3 us for the output and the join of cut items (8 requests of one token
-// over 2048 keys: 14.3 us, 5.1 us at the copy peak).
+// over 2048 keys: 14.7 us, 5.1 us at the copy peak).
 #include <cuda.h>
 #include <math.h>
 
@@ -113,6 +119,13 @@ __device__ __forceinline__ float warp_max(float v) {
     float r;
     asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
     return r;
+}
+
+// log2 of a normal number.
+__device__ __forceinline__ float lg2(float x) {
+    float y;
+    asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
 }
 
 // Barrier of `threads` threads that also tells whether any of them votes.
@@ -263,11 +276,9 @@ struct Cfg8 {
     static constexpr int SIDE = 3 * kTileKeys * 4;             // a stage's key scales, value scales, subtree ends
     // fixed part, behind the stages
     static constexpr int FIX_P = 0, FIX_Q = FIX_P + 2 * P_BYTES, FIX_MX = FIX_Q + 2 * Q_BYTES;
-    static constexpr int FIX_F2 = FIX_MX + 4 * RP * 4;         // column maxima [groups][4 warps][CG]; factors of O [64]
+    static constexpr int FIX_F2 = FIX_MX + 4 * RP * 4;         // column maxima [groups][4 warps][CG]; roots of O's factors [64]
     static constexpr int FIX_M = FIX_F2 + 64 * 4;              // kBase - maximum [64]
-    static constexpr int FIX_V = FIX_M + 64 * 4;               // largest value scales [groups][4 warps]
-    // by unit parity: column sums [4 warps][64], maxima [64], value references [64] (a group's in its first column)
-    static constexpr int FIX_SUM = FIX_V + 64, SUM_BYTES = 6 * 64 * 4;
+    static constexpr int FIX_SUM = FIX_M + 64 * 4, SUM_BYTES = 5 * 64 * 4;   // by unit parity: column sums [4 warps][64], maxima [64]
     static constexpr int FIX_QS = FIX_SUM + 2 * SUM_BYTES;     // query scales [kRing][64], output rows [kRing][64]
     static constexpr int FIX_QROW = FIX_QS + kRing * 64 * 4;
     static constexpr int FIX_REQ = FIX_QROW + kRing * 64 * 4;  // requests: n, P, tiles, parts
@@ -328,8 +339,9 @@ __device__ __forceinline__ void join_parts(const float2 *part_ml, const float *p
             float2 ml = make_float2(-INFINITY, 0.f);
             if (lane < parts) ml = __ldcg(part_ml + (size_t)lane * RP + c);
             const float mx = warp_max(ml.x);
-            const float wt = lane < parts ? ex2(ml.x - mx) : 0.f;
-            float ls = wt * ml.y;
+            // a part of small values may have large sums: its weight, which alone may be below fp32's range, in two steps
+            const float root = lane < parts ? ex2(0.5f * (ml.x - mx)) : 0.f, wt = root * root;
+            float ls = root * ml.y * root;
 #pragma unroll
             for (int o = 16; o; o >>= 1) ls += __shfl_xor_sync(~0u, ls, o);
             float acc[EPL] = {};
@@ -363,12 +375,13 @@ __device__ __forceinline__ void join_parts(const float2 *part_ml, const float *p
 #pragma unroll 4
         for (int s = lane >> 4; s < parts; s += 2) {
             const float2 ml = __ldcg(part_ml + (size_t)s * RP + mine);
-            const float top = fmaxf(mx, ml.x);
-            sum = sum * ex2(mx - top) + ml.y * ex2(ml.x - top);
+            const float top = fmaxf(mx, ml.x), f = ex2(0.5f * (mx - top)), g = ex2(0.5f * (ml.x - top));   // roots: as above
+            sum = f * sum * f + g * ml.y * g;
             mx = top;
         }
         const float mo = __shfl_xor_sync(~0u, mx, 16), so = __shfl_xor_sync(~0u, sum, 16), top = fmaxf(mx, mo);
-        const float inv = 1.f / (lane < 16 ? sum * ex2(mx - top) + so * ex2(mo - top) : so * ex2(mo - top) + sum * ex2(mx - top));
+        const float fm = ex2(0.5f * (mx - top)), fo = ex2(0.5f * (mo - top)), a = fm * sum * fm, b = fo * so * fo;
+        const float inv = 1.f / (a + b);
         mx = top;
 #pragma unroll 1
         for (int i = lane >> 4; i < COLS; i += 2) {
@@ -897,14 +910,14 @@ __global__ void __launch_bounds__(Cfg8<D, RP>::THREADS, 1)
     } else if (warp < 4 + C::SM_WARPS) {   // ---------------------------- softmax
         if constexpr (C::SM_REGS > C::LAUNCH_REGS) take_registers<true, C::SM_REGS>();
         constexpr int CG = C::CG;
-        // p is 2^kBase at the reference maximum, which is raised once a score passes it by 2^kOver: fp16 (and e5m2) hold
+        // w is 2^kBase at the reference, which is raised once a key's y + log2(vs) passes it by 2^kOver: fp16 (and e5m2) hold
         // both ends, and a weight of 2^-23 of the reference's still has a bit
         constexpr float kBase = 7.f, kOver = 8.f;
         const int grp = (warp - 4) >> 2, quarter = warp & 3, cb = grp * CG;
         const int bar = 1 + grp, gt = quarter * 32 + lane;   // thread of the group
         const uint32_t tl = tmem + ((uint32_t)(quarter * 32) << 16);
         const int kslot = quarter * 32 + lane;   // this lane's key of a tile, and its dim of O
-        const uint32_t mx_s = fix_base + C::FIX_MX + grp * 16 * CG, v_s = fix_base + C::FIX_V + grp * 16;
+        const uint32_t mx_s = fix_base + C::FIX_MX + grp * 16 * CG;
         const uint32_t f2_s = fix_base + C::FIX_F2 + cb * 4, m_s = fix_base + C::FIX_M + cb * 4;
         bool ok = true;
         int g = 0;
@@ -918,8 +931,7 @@ __global__ void __launch_bounds__(Cfg8<D, RP>::THREADS, 1)
             }
             const uint32_t oc = tl + C::O_COL + (k & 1) * 3 * RP + cb;   // this unit's O
             const int L = u.P + u.n;
-            float2 m[CG / 2], l[CG / 2];   // kBase - maximum; sums over this lane's keys
-            float ref = 0.f, iref = 0.f;   // the value scales' reference and its reciprocal
+            float2 m[CG / 2], l[CG / 2];   // kBase - reference maximum of exponent + log2(value scale); sums over this lane's keys
 #pragma unroll
             for (int c = 0; c < CG / 2; ++c) {
                 m[c] = make_float2(1e30f, 1e30f);
@@ -927,8 +939,8 @@ __global__ void __launch_bounds__(Cfg8<D, RP>::THREADS, 1)
             }
             const uint32_t qs = fix_base + C::FIX_QS + (r * 64 + cb) * 4;   // query scales, there before the first scores
             int j = u.j0;
-            // y: the columns' exponents before the maximum is taken off; vs: the key's value scale
-            auto scores = [&](float2 (&y)[CG / 2], float &vs) {
+            // y: the columns' exponents before the maximum is taken off; vs: the key's value scale, lv: its log2
+            auto scores = [&](float2 (&y)[CG / 2], float &vs, float &lv) {
                 const int x = g & 1;
                 ok &= wait_warp(sfull + 8 * x, (uint32_t)(g >> 1) & 1u);   // a failure ends the unit with the next vote
                 tc_fence_after();
@@ -941,6 +953,7 @@ __global__ void __launch_bounds__(Cfg8<D, RP>::THREADS, 1)
                     ks = __int_as_float(0x7fc00000);
                     vs = 0.f;
                 }
+                lv = lg2(fmaxf(vs, kScaleMin));
                 tc_wait_ld();
 #pragma unroll
                 for (int c = 0; c < CG / 4; ++c) {
@@ -950,7 +963,7 @@ __global__ void __launch_bounds__(Cfg8<D, RP>::THREADS, 1)
                     y[2 * c + 1] = __fmul2_rn(__fmul2_rn(make_float2(s[4 * c + 2], s[4 * c + 3]), make_float2(v.z, v.w)), k2);
                 }
             };
-            auto above = [&](const float2 (&y)[CG / 2]) -> float {   // the furthest score above its column's maximum
+            auto above = [&](const float2 (&y)[CG / 2], float lv) -> float {   // the furthest above its column's maximum
                 float top = -INFINITY, top2 = -INFINITY;
 #pragma unroll
                 for (int c = 0; c < CG / 2; ++c) {
@@ -958,10 +971,10 @@ __global__ void __launch_bounds__(Cfg8<D, RP>::THREADS, 1)
                     top = fmaxf(top, d.x);
                     top2 = fmaxf(top2, d.y);
                 }
-                return fmaxf(top, top2);
+                return fmaxf(top, top2) + lv;
             };
             auto write_p = [&](const float2 (&y)[CG / 2], float vs) {
-                const float2 rv = make_float2(vs * iref, vs * iref);
+                const float2 rv = make_float2(vs, vs);
                 const uint32_t pd = fix_base + C::FIX_P + (g & 1) * C::P_BYTES + kslot * 64;
                 const int flip = (kslot >> 1) & 3;
                 constexpr int STEP = CG % 16 == 0 ? 16 : 8;
@@ -1004,9 +1017,9 @@ __global__ void __launch_bounds__(Cfg8<D, RP>::THREADS, 1)
             // the common tile: every key seen by every row, no maximum raised; false with nothing done otherwise
             auto plain_tile = [&]() -> bool {
                 float2 y[CG / 2];
-                float vs;
-                scores(y, vs);
-                if (bar_any(bar, 128, above(y) > kBase + kOver || vs > ref || !ok)) return false;
+                float vs, lv;
+                scores(y, vs, lv);
+                if (bar_any(bar, 128, above(y, lv) > kBase + kOver || !ok)) return false;
                 write_p(y, vs);
                 hand_over();
                 return true;
@@ -1015,8 +1028,8 @@ __global__ void __launch_bounds__(Cfg8<D, RP>::THREADS, 1)
             auto any_tile = [&](bool raise) -> bool {
                 const int st = g % C::STAGES, key = j * kTileKeys + kslot;
                 float2 y[CG / 2];
-                float vs;
-                scores(y, vs);
+                float vs, lv;
+                scores(y, vs, lv);
                 if (j * kTileKeys + kTileKeys > u.P) {   // tree keys, or keys past the end
                     int from = -0x7fffffff, to = 0x7fffffff;   // the columns that see this lane's key
                     if (key >= u.P) {
@@ -1032,14 +1045,14 @@ __global__ void __launch_bounds__(Cfg8<D, RP>::THREADS, 1)
                         if (!(2 * c + 1 >= from && 2 * c + 1 < to)) y[c].y = -INFINITY;
                     }
                 }
-                if (!raise) raise = bar_any(bar, 128, above(y) > kBase + kOver || vs > ref || !ok);
+                if (!raise) raise = bar_any(bar, 128, above(y, lv) > kBase + kOver || !ok);
                 if (raise) {
                     // new maxima: of each column over the tile, taken where the old one is passed by 2^kOver
                     float t[CG];
 #pragma unroll
                     for (int c = 0; c < CG / 2; ++c) {
-                        t[2 * c] = warp_max(y[c].x);
-                        t[2 * c + 1] = warp_max(y[c].y);
+                        t[2 * c] = warp_max(y[c].x + lv);
+                        t[2 * c + 1] = warp_max(y[c].y + lv);
                     }
                     if (lane == 0) {
 #pragma unroll
@@ -1047,26 +1060,17 @@ __global__ void __launch_bounds__(Cfg8<D, RP>::THREADS, 1)
                             sts4u(mx_s + (quarter * CG + c) * 4, __float_as_uint(t[c]), __float_as_uint(t[c + 1]),
                                   __float_as_uint(t[c + 2]), __float_as_uint(t[c + 3]));
                     }
-                    const float vtop = warp_max(vs);
-                    if (lane == 0) sts1(v_s + quarter * 4, vtop);
                     if (bar_any(bar, 128, !ok)) {
                         ok = false;
                         return false;
                     }
-                    const float4 v4 = lds4(v_s);
-                    float nref = fmaxf(fmaxf(v4.x, v4.y), fmaxf(v4.z, v4.w));
-                    // a half more than the largest scale so far, so that few tiles raise it
-                    nref = nref > ref ? nref * 1.5f : ref;
-                    iref = nref > 0.f ? __frcp_rn(nref) : 0.f;
-                    const float rr = nref > 0.f ? ref * iref : 1.f;
-                    ref = nref;
                     const bool later = j > u.j0;   // O so far is rescaled once the product before this one has landed in it
                     if (gt < CG) {
                         const uint32_t c = mx_s + gt * 4;
                         const float top = fmaxf(fmaxf(lds1(c), lds1(c + 4 * CG)), fmaxf(lds1(c + 8 * CG), lds1(c + 12 * CG)));
                         const float old = later ? lds1(m_s + gt * 4) : 1e30f, nm = top + old > kBase + kOver ? kBase - top : old;
                         sts1(m_s + gt * 4, nm);
-                        sts1(f2_s + gt * 4, ex2(nm - old));   // 2^(old maximum - new)
+                        sts1(f2_s + gt * 4, ex2(0.5f * (nm - old)));   // root of 2^(old maximum - new): the whole may be below fp32's range
                     }
                     bar_sync(bar, 128);
 #pragma unroll
@@ -1076,8 +1080,8 @@ __global__ void __launch_bounds__(Cfg8<D, RP>::THREADS, 1)
                         m[2 * c + 1] = make_float2(v.z, v.w);
                         if (later) {
                             const float4 f = lds4(f2_s + 16 * c);
-                            l[2 * c] = __fmul2_rn(l[2 * c], make_float2(f.x, f.y));
-                            l[2 * c + 1] = __fmul2_rn(l[2 * c + 1], make_float2(f.z, f.w));
+                            l[2 * c] = __fmul2_rn(__fmul2_rn(l[2 * c], make_float2(f.x, f.y)), make_float2(f.x, f.y));
+                            l[2 * c + 1] = __fmul2_rn(__fmul2_rn(l[2 * c + 1], make_float2(f.z, f.w)), make_float2(f.z, f.w));
                         }
                     }
                     if (later) {
@@ -1091,10 +1095,10 @@ __global__ void __launch_bounds__(Cfg8<D, RP>::THREADS, 1)
                                 const float4 f = lds4(f2_s + c % CG * 4);
                                 tc_ld4(at, o);
                                 tc_wait_ld();
-                                o[0] *= f.x * rr;
-                                o[1] *= f.y * rr;
-                                o[2] *= f.z * rr;
-                                o[3] *= f.w * rr;
+                                o[0] *= f.x * f.x;
+                                o[1] *= f.y * f.y;
+                                o[2] *= f.z * f.z;
+                                o[3] *= f.w * f.w;
                                 tc_st4(at, o);
                             }
                             tc_wait_st();
@@ -1134,7 +1138,7 @@ __global__ void __launch_bounds__(Cfg8<D, RP>::THREADS, 1)
                 ++g;
             }
             if (gone) break;
-            // the unit's sums, maxima and reference to the output warps, once those of two units before are read
+            // the unit's sums and maxima to the output warps, once those of two units before are read
             float v[CG];
 #pragma unroll
             for (int c = 0; c < CG / 2; ++c) {
@@ -1145,10 +1149,7 @@ __global__ void __launch_bounds__(Cfg8<D, RP>::THREADS, 1)
             reduce_scatter<CG>(v, lane);
             const uint32_t sum = fix_base + C::FIX_SUM + (k & 1) * C::SUM_BYTES;
             if (lane % (32 / CG) == 0) sts1(sum + (quarter * 64 + cb + lane / (32 / CG)) * 4, v[0]);
-            if (gt < CG) {
-                sts1(sum + (4 * 64 + cb + gt) * 4, -lds1(m_s + gt * 4));
-                sts1(sum + (5 * 64 + cb + gt) * 4, ref);
-            }
+            if (gt < CG) sts1(sum + (4 * 64 + cb + gt) * 4, -lds1(m_s + gt * 4));
             __syncwarp();
             if (lane == 0) {
                 mbar_arrive(sumfull + 8 * (k & 1));
@@ -1242,8 +1243,8 @@ __global__ void __launch_bounds__(Cfg8<D, RP>::THREADS, 1)
                     const int c = h * 32 + lane;
                     if (c < RP) {
                         const uint32_t sum = fix_base + C::FIX_SUM + par * C::SUM_BYTES + c * 4;
-                        const float lsum = (lds1(sum) + lds1(sum + 256)) + (lds1(sum + 512) + lds1(sum + 768)), ref = lds1(sum + 1280);
-                        f[h] = done.parts > 1 ? ref : ref / lsum;
+                        const float lsum = (lds1(sum) + lds1(sum + 256)) + (lds1(sum + 512) + lds1(sum + 768));
+                        f[h] = done.parts > 1 ? 1.f : 1.f / lsum;
                         place[h] = ldsi(fix_base + C::FIX_QROW + (dr * 64 + c) * 4);
                         if (done.parts > 1 && quarter == 0)
                             a.part_ml[(size_t)(done.slot + done.part) * RP + c] = make_float2(lds1(sum + 1024), lsum);
