@@ -393,7 +393,7 @@ ts_status kv_commit_paged(const ts_paged_kv *kv, const int32_t *prefix_len, int3
  */
 typedef struct ts_qk_rope {
     const float *inv_freq;             /* [rot_dim / 2] (NULL: rot_dim must be 0) */
-    const float *q_weight, *k_weight;  /* [d], NULL: ones */
+    const float *q_weight, *k_weight;  /* [d], NULL: ones; not read without norm */
     float eps;                         /* >= 0 */
     int32_t norm, rot_dim, interleaved;
 } ts_qk_rope;

@@ -374,8 +374,8 @@ cudaError_t rows_dispatch(RowArgs &a, int d, ts_dtype dt, cudaStream_t s) {
 
 void set_rope(RowArgs &a, const ts_qk_rope &r) {
     a.inv_freq = r.inv_freq;
-    a.weight[0] = r.q_weight;
-    a.weight[1] = r.k_weight;
+    a.weight[0] = r.norm ? r.q_weight : nullptr;   // the weights are the norm's
+    a.weight[1] = r.norm ? r.k_weight : nullptr;
     a.eps = r.eps;
     a.norm = r.norm != 0;
     a.rot_dim = r.rot_dim;
