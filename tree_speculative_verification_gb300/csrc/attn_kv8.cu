@@ -46,8 +46,9 @@
 //               the rows of its subtree, one interval of rows.
 //   last four   split a unit's query rows in place, then write the unit before
 //               out of its own O buffer while the softmax works on
-// Every wait is bounded; a wait that gives up sets TS_STATUS_TIMEOUT, the others
-// follow by their own limits or the group's vote, and TMEM is freed.
+// Every wait is bounded, by some 2 s; a wait that gives up sets TS_STATUS_TIMEOUT,
+// the others follow by their own limits or the group's vote (a warp waits in vain
+// three times at most), and TMEM is freed.
 //
 // Bounds, measured. A tile of 128 keys (33 KB at d = 128) has to pass an SM in
 // 0.74 us at the measured copy peak of 6.8 TB/s, and does with 16 rows a unit
@@ -68,6 +69,7 @@
 
 #include "attn_common.cuh"
 #include "kv8.cuh"
+#include "kv8_wait.cuh"
 
 namespace ts {
 namespace {
@@ -152,32 +154,6 @@ __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool v
 // One arrival of this thread once its copies so far have landed.
 __device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
     asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
-}
-
-// Bounded wait for a phase: try_wait suspends the thread in hardware for up to 20 us a try, and the tries are
-// limited (some seconds at most; every wait here is for warps of the same CTA).
-__device__ __forceinline__ bool wait1(uint32_t bar, uint32_t phase) {
-#pragma unroll 1
-    for (int i = 0; i < 1 << 20; ++i) {
-        uint32_t ok;
-        asm volatile(
-            "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n selp.u32 %0, 1, 0, p;\n}\n"
-            : "=r"(ok)
-            : "r"(bar), "r"(phase), "r"(20000)
-            : "memory");
-        if (ok) return true;
-    }
-    return false;
-}
-// The same by a whole warp, one verdict for every lane; a look first, which most waits in the tile loop need no more
-// than (long-context case: 453 us against 462).
-__device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t phase) {
-    uint32_t ok;
-    asm volatile("{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
-                 : "=r"(ok)
-                 : "r"(bar), "r"(phase)
-                 : "memory");
-    return __all_sync(~0u, ok) || __all_sync(~0u, wait1(bar, phase));
 }
 
 // Shared memory by its 32-bit address.
@@ -642,11 +618,11 @@ __global__ void __launch_bounds__(Cfg8<D, RP>::THREADS, 1)
                     cp_async_arrive(fb);
                 }
             }
-            if (!ok) {   // leave no copy in flight
+            if (!ok) {   // leave no copy in flight; one that does not land in a wait's time is the last that is waited for
                 if (lane == 0) misc[1] = 1;
 #pragma unroll 1
                 for (int i = g > C::STAGES ? g - C::STAGES : 0; i < g; ++i)
-                    wait_warp(full + 8 * (i % C::STAGES), (uint32_t)(i / C::STAGES) & 1u);
+                    if (!wait_warp(full + 8 * (i % C::STAGES), (uint32_t)(i / C::STAGES) & 1u)) break;
             }
         } else if (warp == 1) {   // ----------------------------------------- MMA issuer
             if (lane == 0) {
