@@ -168,7 +168,8 @@ ts_status tree_attention_kv8(void *out, const void *q, const ts_kv8 *kv, int Hq,
     if ((long long)t->B * Hq * t->n_max >= (1LL << 31))
         return set_error(TS_ERR_INVALID_ARG, "%s: %lld query rows (2^31 or more)", who, (long long)t->B * Hq * t->n_max);
     if (!(scale > 0.f)) scale = 1.0f / sqrtf((float)kv->d);
-    if (!(scale < INFINITY)) return set_error(TS_ERR_INVALID_ARG, "%s: scale is not finite", who);
+    if (!(scale * ts::kLog2e < INFINITY))   // the kernel's scores are exponents of 2
+        return set_error(TS_ERR_INVALID_ARG, "%s: scale is not finite, or its product with log2(e) is not", who);
     const size_t need = ts::kv8_attention_ws_bytes(t->B, Hq, kv->H, t->n_max, kv->d, ts::kv8_rows(*kv));
     if (!ws || ws_bytes < need)
         return set_error(TS_ERR_INVALID_ARG, "%s: workspace of %zu bytes needed, %zu given", who, need,

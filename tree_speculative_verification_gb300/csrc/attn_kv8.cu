@@ -1366,7 +1366,7 @@ cudaError_t launch_attn_kv8(void *out, const void *q, const ts_kv8 &kv, int Hq, 
     }
     unsigned char *w = (unsigned char *)ws;
     Attn8Args a = {(__nv_bfloat16 *)out, (const __nv_bfloat16 *)q, kv.k_scale, kv.v_scale, prefix_len, t, Hq, kv.H, G,
-                   kv8_rows(kv), scale * 1.4426950408889634f, kv8_pages(kv), status, (unsigned *)w,
+                   kv8_rows(kv), scale * kLog2e, kv8_pages(kv), status, (unsigned *)w,
                    (unsigned *)(w + 256), (float2 *)(w + p.ml), (float *)(w + p.o), p.slots};
     // no more CTAs than there can be units
     const long long tiles = (a.rows + kTileKeys - 1) / kTileKeys, cuts = (tiles + kMinCut - 1) / kMinCut;

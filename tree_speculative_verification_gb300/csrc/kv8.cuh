@@ -11,6 +11,7 @@ namespace ts {
 
 constexpr float kFp8Max = 448.f;                       // largest e4m3 value
 constexpr float kScaleMin = 7.888609052210118e-31f;    // 2^-100: scales stay normal, 1 / scale finite
+constexpr float kLog2e = 1.4426950408889634f;
 
 inline PagedArgs kv8_pages(const ts_kv8 &kv) {
     PagedArgs pg;
