@@ -1333,14 +1333,18 @@ bool make_map8(CUtensorMap *map, const void *base, int d, long long rows, int bo
 }
 
 template <int D, int RP>
-cudaError_t launch8(const CUtensorMap &mk, const CUtensorMap &mv, const Attn8Args &a, int grid, cudaStream_t s) {
+cudaError_t launch8(const CUtensorMap &mk, const CUtensorMap &mv, const Attn8Args &a, int grid, cudaStream_t s,
+                    const char **why) {
     using C = Cfg8<D, RP>;
     cudaError_t e = cudaFuncSetAttribute(k_attn_kv8<D, RP>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
     if (e != cudaSuccess) return e;
     if (C::SM_REGS > C::LAUNCH_REGS) {   // the kernel waits for registers that a smaller launch would not have
         cudaFuncAttributes at;
         if ((e = cudaFuncGetAttributes(&at, k_attn_kv8<D, RP>)) != cudaSuccess) return e;
-        if ((at.numRegs + 7) / 8 * 8 < C::LAUNCH_REGS) return cudaErrorInvalidConfiguration;   // given out in eights
+        if ((at.numRegs + 7) / 8 * 8 < C::LAUNCH_REGS) {   // given out in eights
+            *why = "this build's kernel has fewer registers a thread than its warps hand to one another";
+            return cudaErrorInvalidConfiguration;
+        }
     }
     return launch(k_attn_kv8<D, RP>, dim3(grid), dim3(C::THREADS), C::SMEM, s, mk, mv, a);
 }
@@ -1373,16 +1377,16 @@ cudaError_t launch_attn_kv8(void *out, const void *q, const ts_kv8 &kv, int Hq, 
     const long long units = (long long)t.B * kv.H * p.blocks * (p.slots ? (cuts < kMaxCuts ? cuts : kMaxCuts) : 1);
     const int grid = (int)(units < num_sms() ? units : num_sms());
     if (kv.d == 128) switch (p.rp) {
-        case 16: return launch8<128, 16>(mk, mv, a, grid, s);
-        case 32: return launch8<128, 32>(mk, mv, a, grid, s);
-        case 48: return launch8<128, 48>(mk, mv, a, grid, s);
-        default: return launch8<128, 64>(mk, mv, a, grid, s);
+        case 16: return launch8<128, 16>(mk, mv, a, grid, s, why);
+        case 32: return launch8<128, 32>(mk, mv, a, grid, s, why);
+        case 48: return launch8<128, 48>(mk, mv, a, grid, s, why);
+        default: return launch8<128, 64>(mk, mv, a, grid, s, why);
     }
     switch (p.rp) {
-        case 16: return launch8<64, 16>(mk, mv, a, grid, s);
-        case 32: return launch8<64, 32>(mk, mv, a, grid, s);
-        case 48: return launch8<64, 48>(mk, mv, a, grid, s);
-        default: return launch8<64, 64>(mk, mv, a, grid, s);
+        case 16: return launch8<64, 16>(mk, mv, a, grid, s, why);
+        case 32: return launch8<64, 32>(mk, mv, a, grid, s, why);
+        case 48: return launch8<64, 48>(mk, mv, a, grid, s, why);
+        default: return launch8<64, 64>(mk, mv, a, grid, s, why);
     }
 }
 
