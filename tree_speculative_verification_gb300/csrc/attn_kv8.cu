@@ -237,14 +237,13 @@ template <int D_, int RP_>
 struct Cfg8 {
     static constexpr int D = D_, RP = RP_, CG = RP <= 32 ? 8 : 16, GROUPS = RP / CG;   // columns of a softmax group
     static constexpr int SM_WARPS = 4 * GROUPS, THREADS = 32 * (4 + SM_WARPS + 4);
-    // Registers a thread: LAUNCH x THREADS at launch, handed from the eight other warps to the softmax's where 65536 /
+    // Registers a thread where SPLIT: LAUNCH x THREADS at launch, handed from the eight other warps to the softmax's where 65536 /
     // THREADS does not do for those. RP = 48: 640 x 96 = 61440 >= 256 x 80 + 384 x 104 = 60416; 64: 768 x 80 = 61440 =
     // 256 x 64 + 512 x 88. (With 56 and 48 for the others short units, whose output counts, take up to a quarter longer,
     // long ones 1% less.)
-    static constexpr int LAUNCH_REGS = RP == 64 ? 80 : RP == 48 ? 96 : 80;
-    static constexpr int SM_REGS = RP == 64 ? 88 : RP == 48 ? 104 : LAUNCH_REGS;
-    static constexpr int OTHER_REGS = RP == 64 ? 64 : RP == 48 ? 80 : LAUNCH_REGS;
-    static_assert(32 * SM_WARPS * SM_REGS + 256 * OTHER_REGS <= THREADS * LAUNCH_REGS, "a split of the launch's registers");
+    static constexpr bool SPLIT = RP >= 48;
+    static constexpr int LAUNCH_REGS = RP == 64 ? 80 : 96, SM_REGS = RP == 64 ? 88 : 104, OTHER_REGS = RP == 64 ? 64 : 80;
+    static_assert(!SPLIT || 32 * SM_WARPS * SM_REGS + 256 * OTHER_REGS <= THREADS * LAUNCH_REGS, "a split of the launch's registers");
     static constexpr int OP_BYTES = kTileKeys * D;             // codes of one operand tile
     static constexpr int STAGE_BYTES = 2 * OP_BYTES;
     static constexpr int P_ATOMS = (3 * RP + 63) / 64, P_ATOM = kTileKeys * 64, P_BYTES = P_ATOMS * P_ATOM;
@@ -545,7 +544,7 @@ __global__ void __launch_bounds__(Cfg8<D, RP>::THREADS, 1)
 
     constexpr uint64_t swz = D == 128 ? kSwz128 : kSwz64;
     if (warp < 4) {
-        if constexpr (C::SM_REGS > C::LAUNCH_REGS) take_registers<false, C::OTHER_REGS>();
+        if constexpr (C::SPLIT) take_registers<false, C::OTHER_REGS>();
         if (warp == 0) {   // ------------------------------------------------ producer
             int g = 0;
             bool ok = true;
@@ -884,7 +883,7 @@ __global__ void __launch_bounds__(Cfg8<D, RP>::THREADS, 1)
             asm volatile("cp.async.wait_all;" ::: "memory");
         }
     } else if (warp < 4 + C::SM_WARPS) {   // ---------------------------- softmax
-        if constexpr (C::SM_REGS > C::LAUNCH_REGS) take_registers<true, C::SM_REGS>();
+        if constexpr (C::SPLIT) take_registers<true, C::SM_REGS>();
         constexpr int CG = C::CG;
         // w is 2^kBase at the reference, which is raised once a key's y + log2(vs) passes it by 2^kOver: fp16 (and e5m2) hold
         // both ends, and a weight of 2^-23 of the reference's still has a bit
@@ -1134,7 +1133,7 @@ __global__ void __launch_bounds__(Cfg8<D, RP>::THREADS, 1)
         }
         if (!ok) misc[1] = 1;
     } else {   // -------------------------------------------------------- query rows, output
-        if constexpr (C::SM_REGS > C::LAUNCH_REGS) take_registers<false, C::OTHER_REGS>();
+        if constexpr (C::SPLIT) take_registers<false, C::OTHER_REGS>();
         // Unit k's query rows are split here, then unit k - 1 is written out: its last product, its writing and the
         // next unit's first scores run at the same time.
         const int quarter = warp & 3, dim = quarter * 32 + lane;
@@ -1338,7 +1337,7 @@ cudaError_t launch8(const CUtensorMap &mk, const CUtensorMap &mv, const Attn8Arg
     using C = Cfg8<D, RP>;
     cudaError_t e = cudaFuncSetAttribute(k_attn_kv8<D, RP>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
     if (e != cudaSuccess) return e;
-    if (C::SM_REGS > C::LAUNCH_REGS) {   // the kernel waits for registers that a smaller launch would not have
+    if (C::SPLIT) {   // the kernel waits for registers that a smaller launch would not have
         cudaFuncAttributes at;
         if ((e = cudaFuncGetAttributes(&at, k_attn_kv8<D, RP>)) != cudaSuccess) return e;
         if ((at.numRegs + 7) / 8 * 8 < C::LAUNCH_REGS) {   // given out in eights
