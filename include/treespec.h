@@ -388,8 +388,9 @@ ts_status kv_commit_paged(const ts_paged_kv *kv, const int32_t *prefix_len, int3
  *   k_out [B][n_max][Hk][d] are contiguous; q_out may be q where q_stride is
  *   Hq * d, likewise k_out. Hk = 0 leaves k out, Hq = 0 leaves q out.
  * Input ids v >= n_nodes[b] keep their rows of the outputs. rot_dim is a
- * multiple of 16, at most d. Squares are summed in fp32: |x| up to 1e18.
- * Non-finite values give non-finite heads; no status bit is set.
+ * multiple of 16, at most d. Squares are summed in fp32: |x| up to 1e18, and
+ * where eps is 0 a head's largest from 1e-15. Non-finite values give non-finite
+ * heads; no status bit is set (status is not written).
  */
 typedef struct ts_qk_rope {
     const float *inv_freq;             /* [rot_dim / 2] (NULL: rot_dim must be 0) */
@@ -462,7 +463,8 @@ ts_status kv8_read(void *k_out, void *v_out, const ts_kv8 *kv, const int32_t *ro
  *    the keys the row sees, 2^-24 of it absolutely below. Rows that it does not
  *    see, and rows whose weight is small, take nothing from the others, whatever
  *    their size.
- * Scales from 2^-100 to 2^100 (values up to 5e32) count exactly in the sums.
+ * Value scales from 2^-100 to 2^100 (values up to 5e32) may stand side by side;
+ * an output below 1e-25 may come as zero.
  * Node rows v >= n_nodes[b] are left as they were, as are all rows of a request
  * whose keys pass the cache's end (TS_STATUS_INDEX). Rows of the cache from prefix_len[b] + n_nodes[b] on may
  * hold anything. A page id outside [0, num_pages) reads as zeros and sets

@@ -53,10 +53,10 @@
 // Bounds, measured. A tile of 128 keys (33 KB at d = 128) has to pass an SM in
 // 0.74 us at the measured copy peak of 6.8 TB/s, and does with 16 rows a unit
 // (64 requests x 56 heads x 1040 keys: 152 us, 98% of the peak). With more rows
-// the softmax warps' latency bounds it: 32 rows 183 us (85%), 47 rows 206 us
-// (79%), and a unit of 9 tiles costs some 2 us beside its tiles (first maxima,
-// masked tile, sums). 64 rows take 0.9 us a tile (4 x 64 heads x 16512 keys x
-// 128 nodes: 395 us, 696 TFLOP/s of attention arithmetic). What carried it
+// the softmax warps' latency bounds it: 32 rows 183 us (85%), 47 rows 205 us
+// (79%; 94% over 8192 keys), where a unit of 9 tiles costs some 2 us beside its
+// tiles (first maxima, masked tile, sums). 64 rows take 0.8 us a tile (4 x 64
+// heads x 16512 keys x 128 nodes: 395 us, 696 TFLOP/s of attention arithmetic). What carried it
 // there: two tiles of scores and two of probabilities in flight; one wait a tile
 // for both; no branch and few instructions in the common tile (its loop has to
 // stay in the instruction cache: a version of twice the code took 1.4 times as

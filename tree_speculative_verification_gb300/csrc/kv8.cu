@@ -145,7 +145,7 @@ __device__ __forceinline__ void unpairs(const float2 (&x)[H / 2], const float2 (
 // (into shared memory; in registers, four rows a lane group ahead, they cost
 // more occupancy than they hid: 51 us against 46 on an append of 64 x 47 nodes,
 // 56 + 56 heads of 128). What bounds a large call next to memory is issuing
-// (69% of the slots in that append): the loop is compiled once for each kind of
+// (67% of the slots in that append): the loop is compiled once for each kind of
 // row (query, key, value), and a CTA runs one of them; one loop for all kinds
 // took 56 us. Measured there: norm and rotation of q and k 30.1 us (172 MB, 84%
 // of the copy peak), the append with its codes 45.3 us (217 MB, 71%). The
