@@ -23,6 +23,10 @@
  *   tree_qk_norm_rope, kv8_append, kv8_read, tree_attention_kv8, kv8_commit
  *                    head norms with rotation, and the same step over a cache
  *                    held in 8 bits (e4m3 codes, one fp32 scale per row and head)
+ *   kv_pages_build, kv_append_slots, decode_attention_paged, sample_tokens
+ *                    a decode step on the paged cache: pages to requests and the
+ *                    slots of new rows, rows into their slots, attention of one
+ *                    new token a request, a token from logits
  *
  * Conventions shared by every call
  *  - All array arguments are DEVICE pointers owned by the caller, unless the
@@ -69,6 +73,7 @@ typedef enum { TS_OP_ATTENTION = 0, TS_OP_VERIFY_GREEDY = 1, TS_OP_VERIFY_MSS = 
 #define TS_STATUS_ZERO_RESID 4u  /* residual normaliser <= 0; residual kept unchanged    */
 #define TS_STATUS_INDEX 8u       /* token >= V, row index out of range, prefix+n > L_max  */
 #define TS_STATUS_TIMEOUT 16u    /* a bounded wait inside a kernel gave up               */
+#define TS_STATUS_NO_PAGES 32u   /* the pool has not the pages that a request needs      */
 
 /*
  * The linearised tree. The struct itself is a HOST object holding DEVICE
@@ -487,6 +492,115 @@ ts_status kv8_commit(const ts_kv8 *kv, const int32_t *prefix_len, int32_t *new_p
 /* Bytes of workspace tree_attention_kv8 needs on the current device (0 for sizes it would reject);
  * L_max = the dense cache's rows or max_pages * TS_PAGE_KEYS. */
 size_t treespec_kv8_workspace_size(int B, int Hq, int Hkv, int n_max, int d, int L_max);
+
+/*
+ * A pool of cache pages and who holds them: block_table [B][max_pages], of which
+ * request b holds its first held[b] entries (the others are not read), and the
+ * free pages in a ring of num_pages entries: from entry ring_state[0] on
+ * ring_state[1] of them, past the last entry to the first. ring_state[2] is the
+ * calls' own, 0 between them. Host struct of device pointers owned by the
+ * caller. num_pages < 2^25 (slots are 32-bit).
+ */
+typedef struct ts_page_pool {
+    int32_t *block_table;   /* [B][max_pages] */
+    int32_t *held;          /* [B] */
+    int32_t *ring;          /* [num_pages] */
+    int32_t *ring_state;    /* [3]: first free entry, free pages, 0 */
+    int32_t B, max_pages, num_pages;
+} ts_page_pool;
+
+/*
+ * kv_pages_build -- pages and slots from lengths. Request b gets the pages that
+ * its rows 0 .. row_end[b] - 1 need beyond those it holds, and gives back the
+ * ones it holds beyond those (row_end 0: all); and every new row
+ * row_begin[b] .. row_end[b] - 1 gets its slot, page * TS_PAGE_KEYS + row in the page.
+ *   slot        [max_slots]  the requests' new rows, one request after the other;
+ *                            entries behind the last row are -1 (NULL: no slots,
+ *                            row_begin is not read)
+ *   slot_offset [B + 1]      where a request's slots start, and their number (may be NULL)
+ *   new_held    [B]          pages held after the call; may be pool->held
+ *   new_state   [3]          the ring after the call, its first two entries; may be
+ *                            pool->ring_state. With both apart from the pool's the
+ *                            call can be repeated on the same state.
+ * Pages are handed out in the requests' order from the ring's start, and none
+ * overtakes: where the pool cannot serve a request, that one and all later ones
+ * that need pages get none, keep what they hold, and their slots are -1
+ * (TS_STATUS_NO_PAGES; new_held tells which). Pages given back go behind the free
+ * ones, in the requests' order, and can be handed out from the next call on.
+ * A request with lengths that do not fit (row_begin < 0 or above row_end, more
+ * than max_pages pages, held outside 0 .. max_pages) is left as it is, with slots
+ * -1; so is every request where the ring's state does not fit num_pages, and rows
+ * past max_slots get no slot (TS_STATUS_INDEX).
+ */
+ts_status kv_pages_build(const ts_page_pool *pool, int32_t *new_held, int32_t *new_state, int32_t *slot,
+                         int max_slots, int32_t *slot_offset, const int32_t *row_begin, const int32_t *row_end,
+                         uint32_t *status, cudaStream_t stream);
+
+/*
+ * kv_append_slots -- rows of T tokens into the pages by their slots (as
+ * kv_pages_build gives them): row slot[t] % TS_PAGE_KEYS of page
+ * slot[t] / TS_PAGE_KEYS gets k_new[t] and v_new[t], H heads of d values, bf16,
+ * k_stride / v_stride elements from one token to the next (at least H * d, a
+ * multiple of 16 bytes). A slot of -1 is left out; any other that is not in the
+ * pages too (TS_STATUS_INDEX). Slots are distinct: of a slot that stands twice,
+ * each 16 bytes come from one of its rows, not said which. kv->block_table is not read.
+ */
+ts_status kv_append_slots(const ts_paged_kv *kv, const void *k_new, const void *v_new, long long k_stride,
+                          long long v_stride, const int32_t *slot, int T, int H, int d, uint32_t *status,
+                          cudaStream_t stream);
+
+/*
+ * decode_attention_paged -- attention of one new token a request over its pages:
+ *   out[b][h][:] = softmax_j(scale * q[b][h] . k_j) v_j,  j < kv_len[b],
+ * query head h reading key/value head h / (Hq / Hkv). The token's own row is
+ * among the kv_len[b]. q [B] rows of Hq heads, q_stride elements apart (as for
+ * tree_qk_norm_rope), out [B][Hq][d]; bf16, Hq a multiple of Hkv. Softmax and
+ * sums are fp32. scale <= 0 selects 1/sqrt(d).
+ * kv_len 0 gives zeros. A request with kv_len outside 0 .. max_pages *
+ * TS_PAGE_KEYS keeps its rows of out (TS_STATUS_INDEX); a page id outside
+ * [0, num_pages) reads as zeros (TS_STATUS_INDEX). Rows from kv_len on may hold
+ * anything. ws: at least treespec_decode_workspace_size(...) bytes, zero-filled
+ * before its first use (treespec_workspace_init); calls leave what must be zero
+ * so, and may be of several sizes. Calls that share one ws must not overlap on
+ * the GPU, two captured graphs that hold them included.
+ */
+ts_status decode_attention_paged(void *out, const void *q, long long q_stride, const ts_paged_kv *kv,
+                                 const int32_t *kv_len, int B, int Hq, int Hkv, int d, float scale, void *ws,
+                                 size_t ws_bytes, uint32_t *status, cudaStream_t stream);
+
+/* Bytes of workspace decode_attention_paged needs on the current device (0 for sizes it would reject). */
+size_t treespec_decode_workspace_size(int B, int Hq, int Hkv, int d);
+
+/*
+ * sample_tokens -- a token for each of R rows of logits, from a uniform number.
+ * In a row's order (value falling, id rising) a start is kept, the shortest of
+ *   top_k   the first top_k (0: all)
+ *   min_p   those with exp((x - max) / T) >= min_p, compared as
+ *           x >= max + T ln(min_p) (0 or below: all; above 1 counts as 1)
+ *   top_p   of what these two keep: the fewest whose weights exp((x - max) / T) sum
+ *           to top_p of its sum (1 or above: all)
+ * and at least one token. The token is the first id, ids rising, at which the
+ * running sum of the kept weights is above u times their sum. T = 0 (below
+ * 2^-100) keeps the first of the order.
+ *   logits [R] rows of V values, row_stride elements apart, fp32 or bf16; -inf is
+ *          a token of no weight
+ *   token  [R] (may be NULL, then u may be too), u [R] in [0, 1)
+ *   temperature, top_k, top_p, min_p [R] (each may be NULL: 1, 0, 1, 0)
+ *   probs  [R][V] fp32 (may be NULL): kept weights over their sum, 0 elsewhere; a
+ *          drafter's rows for verify_mss
+ *   kept   [R][V] fp32 (may be NULL; may be the logits where these are fp32, V
+ *          apart): the logits of the kept tokens, TS_DROPPED_LOGIT elsewhere; target
+ *          rows for verify_mss at the same temperature
+ * Weights are counted in units of 2^-40 of the largest, and summed exactly.
+ * A row with NaN or +inf, or with nothing but -inf (TS_STATUS_NONFINITE), or with
+ * u or a setting out of its range (NaN, T negative or infinite, top_k negative;
+ * TS_STATUS_INDEX) gets token -1 and its rows of probs and kept NaN, which a
+ * verifier refuses in turn. V <= 2^18.
+ */
+#define TS_DROPPED_LOGIT (-1e30f)
+ts_status sample_tokens(int32_t *token, float *probs, float *kept, const void *logits, long long row_stride,
+                        ts_dtype dtype, const float *u, const float *temperature, const int32_t *top_k,
+                        const float *top_p, const float *min_p, int R, int V, uint32_t *status, cudaStream_t stream);
 
 /* Bytes of workspace an op needs for these sizes on the current device (0 if none). */
 size_t treespec_workspace_size(ts_op op, int B, int H, int n_max, int d, int L_max, int V);

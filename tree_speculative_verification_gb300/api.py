@@ -20,8 +20,10 @@ TS_OK, TS_ERR_INVALID_ARG, TS_ERR_CUDA, TS_ERR_UNSUPPORTED = 0, 1, 2, 3
 TS_F32, TS_BF16 = 0, 1
 TS_OP_ATTENTION, TS_OP_VERIFY_GREEDY, TS_OP_VERIFY_MSS = 0, 1, 2
 STATUS_BAD_TREE, STATUS_NONFINITE, STATUS_ZERO_RESID, STATUS_INDEX, STATUS_TIMEOUT = 1, 2, 4, 8, 16
+STATUS_NO_PAGES = 32
 MAX_NODES = 256
 PAGE_KEYS = 64   # TS_PAGE_KEYS
+DROPPED_LOGIT = -1e30   # TS_DROPPED_LOGIT
 
 #: every entry point of the C ABI (include/treespec.h)
 EXPORTS = ("tree_build", "tree_build_chains", "kv_append", "tree_attention", "verify_greedy", "verify_mss",
@@ -29,7 +31,8 @@ EXPORTS = ("tree_build", "tree_build_chains", "kv_append", "tree_attention", "ve
            "treespec_version", "tree_attention_noalloc", "treespec_attention_kernel", "verify_naive",
            "tree_expand_topk", "kv_append_paged", "tree_attention_paged", "kv_commit_paged", "tree_build_append",
            "tree_attention_append", "tree_qk_norm_rope", "kv8_append", "kv8_read", "tree_attention_kv8", "kv8_commit",
-           "treespec_kv8_workspace_size")
+           "treespec_kv8_workspace_size", "kv_pages_build", "kv_append_slots", "decode_attention_paged",
+           "treespec_decode_workspace_size", "sample_tokens")
 #: bytes of the scratch array compiled into the library (TS_NOALLOC_SCRATCH_BYTES)
 NOALLOC_SCRATCH_BYTES = 8 << 20
 
@@ -57,6 +60,11 @@ class ts_qk_rope(C.Structure):
 class ts_kv8(C.Structure):
     _fields_ = [(name, C.c_void_p) for name in ("k", "v", "k_scale", "v_scale", "block_table")] + [
         (name, C.c_int32) for name in ("B", "H", "d", "L_max", "num_pages", "max_pages")]
+
+
+class ts_page_pool(C.Structure):
+    _fields_ = [(name, C.c_void_p) for name in ("block_table", "held", "ring", "ring_state")] + [
+        (name, C.c_int32) for name in ("B", "max_pages", "num_pages")]
 
 
 _lib = None
@@ -96,6 +104,10 @@ def load_library(path: str | None = None):
         "kv8_read": [P, P, KV, P, P, I, I, P, P],
         "tree_attention_kv8": [P, P, KV, I, P, T, F, P, Z, P, P],
         "kv8_commit": [KV, P, P, P, P, T, P, P],
+        "kv_pages_build": [C.POINTER(ts_page_pool), P, P, P, I, P, P, P, P, P],
+        "kv_append_slots": [C.POINTER(ts_paged_kv), P, P, S, S, P, I, I, I, P, P],
+        "decode_attention_paged": [P, P, S, C.POINTER(ts_paged_kv), P, I, I, I, I, F, P, Z, P, P],
+        "sample_tokens": [P, P, P, P, S, I, P, P, P, P, P, I, I, P, P],
     }
     for name, args in sig.items():
         fn = getattr(lib, name)
@@ -105,6 +117,8 @@ def load_library(path: str | None = None):
     lib.treespec_workspace_size.restype = C.c_size_t
     lib.treespec_kv8_workspace_size.argtypes = [I, I, I, I, I, I]
     lib.treespec_kv8_workspace_size.restype = C.c_size_t
+    lib.treespec_decode_workspace_size.argtypes = [I, I, I, I]
+    lib.treespec_decode_workspace_size.restype = C.c_size_t
     lib.treespec_attention_kernel.argtypes = [I, I, I, I, I, I]
     lib.treespec_attention_kernel.restype = C.c_char_p
     lib.treespec_last_error.restype = C.c_char_p
@@ -323,7 +337,9 @@ class PagedKV:
         if k_pages.shape[2] != PAGE_KEYS:
             raise TreespecError(f"a page holds {PAGE_KEYS} keys")
         self.k_pages, self.v_pages, self.block_table = k_pages, v_pages, _i32(block_table, "block_table")
-        self.H, self.d = k_pages.shape[1], k_pages.shape[3]
+        self.H, self.d, self.device = k_pages.shape[1], k_pages.shape[3], k_pages.get_device()
+        self._whole = k_pages.is_cuda and all(x.is_contiguous() and x.device == k_pages.device
+                                              for x in (k_pages, v_pages, block_table)) and block_table.dim() == 2
         self._c = ts_paged_kv(k_pages.data_ptr(), v_pages.data_ptr(), block_table.data_ptr(), k_pages.shape[0],
                               block_table.shape[1])
 
@@ -585,6 +601,140 @@ def kv8_commit(kv: KV8, prefix_len, new_prefix_len, out_path, out_count, tree: T
          _int_array(new_prefix_len, B, "new_prefix_len", dev),
          _int_array(out_path, B * (tree.n_max + 1), "out_path", dev), _int_array(out_count, B, "out_count", dev),
          tree.c, _status_ptr(status, dev))
+
+
+# -- a decode step on the paged cache ------------------------------------------------
+class PagePool:
+    """Cache pages and who holds them (the ts_page_pool of the C ABI): block_table [B][max_pages], of which request b
+    holds the first held[b] entries, and the free pages in a ring [num_pages]; state [3] is its first free entry, the
+    number of free pages, and a counter that is 0 between calls. int32 tensors on one CUDA device."""
+
+    def __init__(self, block_table, held, ring, state):
+        if block_table.dim() != 2 or not block_table.is_cuda:
+            raise TreespecError("block_table must be [B][max_pages] on a CUDA device")
+        self.B, self.max_pages = block_table.shape
+        self.device = dev = block_table.get_device()
+        self.num_pages = ring.numel()
+        self.block_table, self.held, self.ring, self.state = block_table, held, ring, state
+        self._c = ts_page_pool(_int_array(block_table, 1, "block_table", dev), _int_array(held, self.B, "held", dev),
+                               _int_array(ring, 1, "ring", dev), _int_array(state, 3, "state", dev), self.B,
+                               self.max_pages, self.num_pages)
+        self._ref = C.byref(self._c)
+
+    @classmethod
+    def empty(cls, B: int, max_pages: int, num_pages: int, device="cuda"):
+        """A pool whose pages are all free."""
+        i32 = lambda *a: torch.tensor(a, dtype=torch.int32, device=device)
+        return cls(torch.full((B, max_pages), -1, dtype=torch.int32, device=device),
+                   torch.zeros(B, dtype=torch.int32, device=device),
+                   torch.arange(num_pages, dtype=torch.int32, device=device), i32(0, num_pages, 0))
+
+
+def kv_pages_build(pool: PagePool, row_end, row_begin=None, slot=None, slot_offset=None, new_held=None, new_state=None,
+                   status=None, stream=None):
+    """Pages for rows 0 .. row_end[b] - 1 of every request, and the slots of rows row_begin[b] .. row_end[b] - 1 into
+    slot (entries behind the last row are -1) with each request's first one in slot_offset [B + 1]. Without new_held and
+    new_state the pool itself is brought up to date; with them it can serve the same call again."""
+    dev, B = pool.device, pool.B
+    sp = so = rb = None
+    n = 0
+    if slot is not None:
+        n = slot.numel()
+        sp = _int_array(slot, 1, "slot", dev)
+        if row_begin is None:
+            raise TreespecError("slots need row_begin")
+        rb = _int_array(row_begin, B, "row_begin", dev)
+        if slot_offset is not None:
+            so = _int_array(slot_offset, B + 1, "slot_offset", dev)
+    elif slot_offset is not None:
+        raise TreespecError("slot_offset without slot")
+    _run(load_library().kv_pages_build, "kv_pages_build", dev, stream, pool._ref,
+         pool._c.held if new_held is None else _int_array(new_held, B, "new_held", dev),
+         pool._c.ring_state if new_state is None else _int_array(new_state, 3, "new_state", dev), sp, n, so, rb,
+         _int_array(row_end, B, "row_end", dev), _status_ptr(status, dev))
+
+
+def _whole_pages(kv: PagedKV):
+    if not kv._whole:
+        raise TreespecError("pages and block table must be contiguous on one CUDA device")
+    return kv.c
+
+
+def _token_rows(t, H, d, name, dtype, device):
+    """(pointer, elements from one token to the next) of rows [T][H][d] whose heads are contiguous."""
+    if t.dtype is not dtype or t.get_device() != device or t.dim() != 3 or t.shape[1] != H or t.shape[2] != d:
+        raise TreespecError(f"{name} must be a {dtype} tensor [T][{H}][{d}] on CUDA device {device}, not {t.dtype} "
+                            f"{tuple(t.shape)} on {t.device}")
+    if t.is_contiguous():
+        return t.data_ptr(), H * d
+    st, sh, sd = t.stride()
+    if (d > 1 and sd != 1) or (H > 1 and sh != d):
+        raise TreespecError(f"{name}: heads must be contiguous")
+    return t.data_ptr(), H * d if t.shape[0] == 1 else st
+
+
+def kv_append_slots(kv: PagedKV, k_new, v_new, slot, status=None, stream=None):
+    """Rows k_new, v_new [T][H][d] into the pages by their slots (-1: left out). H * d apart or more."""
+    ref, dev = _whole_pages(kv), kv.device
+    kp, ks = _token_rows(k_new, kv.H, kv.d, "k_new", torch.bfloat16, dev)
+    vp, vs = _token_rows(v_new, kv.H, kv.d, "v_new", torch.bfloat16, dev)
+    T = k_new.shape[0]
+    if v_new.shape[0] != T:
+        raise TreespecError(f"k_new of {T} tokens, v_new of {v_new.shape[0]}")
+    _run(load_library().kv_append_slots, "kv_append_slots", dev, stream, ref, kp, vp, ks, vs,
+         _int_array(slot, T, "slot", dev), T, kv.H, kv.d, _status_ptr(status, dev))
+
+
+def decode_workspace(B: int, Hq: int, Hkv: int, d: int, device="cuda"):
+    """A zero-filled workspace of the size decode_attention_paged needs."""
+    with torch.cuda.device(device):
+        need = int(load_library().treespec_decode_workspace_size(B, Hq, Hkv, d))
+    return torch.zeros(max(256, need), dtype=torch.uint8, device=device)
+
+
+def decode_attention_paged(out, q, kv: PagedKV, kv_len, scale: float = 0.0, ws=None, status=None, stream=None):
+    """Attention of one new token a request to the first kv_len[b] rows of its pages; q, out [B][Hq][d] bfloat16, Hq a
+    multiple of kv.H, the rows of q Hq * d apart or more."""
+    ref, dev, d, B = _whole_pages(kv), kv.device, kv.d, kv.block_table.shape[0]
+    if q.dim() != 3 or q.shape[0] != B:
+        raise TreespecError(f"q must be [{B}][Hq][{d}]")
+    Hq = q.shape[1]
+    qp, qs = _token_rows(q, Hq, d, "q", torch.bfloat16, dev)
+    op = _out_rows(out, (B, Hq, d), "out", torch.bfloat16, dev)
+    if ws is None or ws.get_device() != dev or not ws.is_contiguous():
+        raise TreespecError(f"a workspace (decode_workspace) on CUDA device {dev} is needed")
+    _run(load_library().decode_attention_paged, "decode_attention_paged", dev, stream, op, qp, qs, ref,
+         _int_array(kv_len, B, "kv_len", dev), B, Hq, kv.H, d, float(scale), ws.data_ptr(),
+         ws.numel() * ws.element_size(), _status_ptr(status, dev))
+
+
+def _f32_array(t, n, name, device):
+    if t is None:
+        return None
+    if t.dtype is not torch.float32 or t.numel() < n or t.get_device() != device or not t.is_contiguous():
+        raise TreespecError(f"{name} must be a contiguous float32 tensor of {n} entries on CUDA device {device}")
+    return t.data_ptr()
+
+
+def sample_tokens(token, logits, u=None, temperature=None, top_k=None, top_p=None, min_p=None, probs=None, kept=None,
+                  status=None, stream=None):
+    """A token for each row of logits [R][V] (bfloat16 or float32, rows V apart or more) from u [R], under each row's
+    temperature, top_k, top_p and min_p [R] (None: 1, all, 1, 0). probs [R][V] float32: the filtered distribution;
+    kept [R][V] float32: the logits of what is kept, DROPPED_LOGIT elsewhere (may be the logits themselves). token may
+    be None where one of these is asked for."""
+    if logits.dim() != 2 or not logits.is_cuda:
+        raise TreespecError("logits must be [R][V] on a CUDA device")
+    R, V = logits.shape
+    dev, stride = logits.get_device(), logits.stride()
+    if stride[1] != 1 and V > 1:
+        raise TreespecError("a row of logits must be contiguous")
+    rows = [None if x is None else _out_rows(x, (R, V), name, torch.float32, dev)
+            for x, name in ((probs, "probs"), (kept, "kept"))]
+    _run(load_library().sample_tokens, "sample_tokens", dev, stream,
+         None if token is None else _int_array(token, R, "token", dev), rows[0], rows[1], logits.data_ptr(),
+         stride[0] if R > 1 else V, _dtype(logits), _f32_array(u, R, "u", dev),
+         _f32_array(temperature, R, "temperature", dev), None if top_k is None else _int_array(top_k, R, "top_k", dev),
+         _f32_array(top_p, R, "top_p", dev), _f32_array(min_p, R, "min_p", dev), R, V, _status_ptr(status, dev))
 
 
 def version() -> str:

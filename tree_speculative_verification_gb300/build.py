@@ -19,7 +19,7 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libtreespec.so")
 SOURCES = ["api.cu", "tree_build.cu", "kv.cu", "attn_f32.cu", "attn_bf16.cu", "attn_tq.cu", "verify.cu", "attn_noalloc.cu",
-           "api_kv8.cu", "kv8.cu", "attn_kv8.cu"]
+           "api_kv8.cu", "kv8.cu", "attn_kv8.cu", "api_decode.cu", "pages.cu", "attn_decode.cu", "sample.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
