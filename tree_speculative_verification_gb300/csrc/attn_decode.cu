@@ -38,16 +38,19 @@ struct DecodeArgs {
     int B, Hq, Hkv, G, blocks;   // query heads a key/value head; blocks of them
     int num_pages, max_pages;
     float scale_log2;
-    unsigned *counters;   // [grid]: parts of the item that starts in a CTA's stretch and ends in a later one's
+    unsigned *counters;   // [2][grid]: parts there are of the item (the group of parts) that starts in a CTA's stretch
     float *parts;         // [grid][2][heads][D + 2]
     uint32_t *status;
 };
 
-__device__ __forceinline__ uint4 ld_stream(const uint4 *p) {
+// 16 bytes that are read once, or zeros where yes is false (no branch: the loads of a step are one run of instructions).
+__device__ __forceinline__ uint4 ld_stream(const uint4 *p, bool yes) {
     uint4 v;
-    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                 : "l"(p));
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.u32 p, %5, 0;\n mov.u32 %0, 0;\n mov.u32 %1, 0;\n mov.u32 %2, 0;\n mov.u32 %3, 0;\n"
+        " @p ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];\n}\n"
+        : "=&r"(v.x), "=&r"(v.y), "=&r"(v.z), "=&r"(v.w)
+        : "l"(p), "r"((uint32_t)yes));
     return v;
 }
 
@@ -74,40 +77,66 @@ __device__ __forceinline__ float guarded(float m) { return m == -INFINITY ? 0.f 
 template <int D, int NT>
 constexpr int kPerSm = D == 64 ? (NT == 1 ? 4 : 3) : (NT == 1 ? 3 : 2);
 
+// A stretch of one item's keys: steps [step0, step1) of 16 keys.
+struct Segment {
+    int b, n, kvh, h0;   // request, its keys, key/value head, first query head of the block
+    int step0, step1;
+    int i0, i1, x1;      // the item's tiles in the line, and where the segment ends
+    const int32_t *bt;
+};
+// An item in several CTAs' stretches, from c0 on: whose rows it is, and what its parts are counted by.
+struct Shared {
+    int b, kvh, h0;
+    int c0, k0;          // the item's first CTA, the group's
+    int n, groups;       // parts to be counted at k0, groups (0: one level)
+};
+
+constexpr int kGroup = 16, kGroupFrom = 33;   // parts are joined in two levels, kGroup at a time, from kGroupFrom on
+constexpr int kMostParts = 64, kMostCtas = kMostParts * kGroup - 1;   // parts, or groups, in one join; CTAs that allows
+
+// Adds one to a counter: what the CTA has written before (behind a barrier) is seen by whoever finds it counted and
+// then sees_counted(). The count is only waited for where it is used.
+__device__ __forceinline__ unsigned count_up(unsigned *p) {
+    unsigned old;
+    asm volatile("atom.add.release.gpu.global.u32 %0, [%1], 1;" : "=r"(old) : "l"(p) : "memory");
+    return old;
+}
+__device__ __forceinline__ void sees_counted() { asm volatile("fence.acq_rel.gpu;" ::: "memory"); }
+
 template <int D, int NT>
 __global__ void __launch_bounds__(kThreads, kPerSm<D, NT>) k_attn_decode(DecodeArgs a) {
     constexpr int HB = 8 * NT;           // query heads of a block
     constexpr int VEC = D / 8;           // 16-byte pieces of a row
     constexpr int KC = D / 32, VC = D / 64;
     constexpr int ROW = D + 4;           // floats between heads in shared memory
+    constexpr int PART = HB * (D + 2);   // floats of a part: O, maxima, sums
     __shared__ float o_s[kWarps][HB][ROW];
-    __shared__ float m_s[kWarps][HB], l_s[kWarps][HB];
-    __shared__ long long sum_s[kWarps], first_s;
-    __shared__ int len_s[kThreads], req_s, last_s;
+    __shared__ float m_s[kWarps][HB], l_s[kWarps][HB], pm_s[kMostParts][HB], pl_s[kMostParts][HB];
+    __shared__ long long sum_s[kWarps];
+    __shared__ int len_s[kThreads], req_s, first_s, items_s[kWarps], last_s;
+    __shared__ Shared shared_s[2];   // of the CTA's first segment, of its last
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
     pdl_wait();
     pdl_trigger();
 
     // ---- the plan: which stretch of the line of tiles is this CTA's
-    auto pages_of = [&](int b, int n) {
-        if (n < 0 || n > (long long)a.max_pages * TS_PAGE_KEYS) {
-            if (blockIdx.x == 0) flag(a.status, TS_STATUS_INDEX);
-            return 0;
-        }
+    auto pages_of = [&](int n) {
+        if (n < 0 || n > (long long)a.max_pages * TS_PAGE_KEYS) return 0;
         return (n + TS_PAGE_KEYS - 1) / TS_PAGE_KEYS;
     };
-    auto block_sum = [&](long long v, long long &before) {   // before: of the threads before this one
+    // sum over the CTA; before: over the threads before this one
+    auto block_sum = [&](long long v, long long &before) {
         long long run = v;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const long long y = __shfl_up_sync(~0u, run, o);
             if (lane >= o) run += y;
         }
-        __syncthreads();
         if (lane == 31) sum_s[warp] = run;
         __syncthreads();
         long long all = 0;
         before = run - v;
+#pragma unroll
         for (int w = 0; w < kWarps; ++w) {
             if (w < warp) before += sum_s[w];
             all += sum_s[w];
@@ -116,78 +145,200 @@ __global__ void __launch_bounds__(kThreads, kPerSm<D, NT>) k_attn_decode(DecodeA
     };
     const int items = a.Hkv * a.blocks;   // of a request
     long long mine = 0, before = 0;
+    int live = 0, mine_first = 0;
     for (int b = tid; b < a.B; b += kThreads) {
-        const int n = a.kv_len[b];
-        if (b < kThreads) len_s[b] = n;
-        mine += pages_of(b, n);
+        const int n = a.kv_len[b], p = pages_of(n);
+        if (b < kThreads) len_s[b] = n, mine_first = p;
+        mine += p;
+        live += p > 0;
+        if (p == 0 && n != 0 && blockIdx.x == 0) flag(a.status, TS_STATUS_INDEX);
     }
     for (int b = blockIdx.x; b < a.B; b += gridDim.x)   // no key: zeros
         if (a.kv_len[b] == 0)
             for (int i = tid; i < a.Hq * VEC; i += kThreads)
                 ((uint4 *)a.out)[(size_t)b * a.Hq * VEC + i] = make_uint4(0, 0, 0, 0);
-    const long long T = block_sum(mine, before) * items;
-    const long long ctas = min((long long)gridDim.x, T), c = blockIdx.x;
-    if (c >= ctas) return;
-    long long x = T * c / ctas;
-    const long long x_end = T * (c + 1) / ctas;
-    for (long long base = 0, done = 0; base < a.B; base += kThreads) {
-        const int b = (int)base + tid, p = b < a.B ? pages_of(b, a.kv_len[b]) : 0;
-        const long long all = block_sum(p, before);
-        if ((done + before) * items <= x && x < (done + before + p) * items) req_s = b, first_s = (done + before) * items;
-        done += all;
-        if (x < done * items) break;
+    live = __reduce_add_sync(~0u, live);
+    if (lane == 0) items_s[warp] = live;
+    const long long all_tiles = block_sum(mine, before) * items;
+    int live_items = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) live_items += items_s[w];
+    if (all_tiles == 0 || all_tiles > INT32_MAX) {
+        if (all_tiles && blockIdx.x == 0 && tid == 0) flag(a.status, TS_STATUS_INDEX);
+        return;
     }
-    __syncthreads();
-    int b = req_s;
-    long long first = first_s;             // the line's tile at which request b starts
-
-    while (x < x_end) {
-        const int n = b < kThreads ? len_s[b] : a.kv_len[b], pages = pages_of(b, n);
-        if (pages == 0 || x >= first + (long long)pages * items) {
-            first += (long long)pages * items;
-            ++b;
-            continue;
+    const int T = (int)all_tiles, c = blockIdx.x;
+    live_items *= items;
+    // As many CTAs as the GPU holds; a whole number of them an item where that leaves no more than a tenth of them out, so
+    // that equal requests are cut alike, no CTA's stretch holds parts of two items, and no item has one part more.
+    int ctas = gridDim.x;
+    if (live_items <= ctas && ctas % live_items <= ctas / 10) ctas -= ctas % live_items;
+    // A part that has to be joined costs 2.5 us, a tile more 1 us: up to three tiles an item are not cut, and no CTA gets
+    // less than two tiles of a longer one.
+    ctas = min(ctas, T <= 3LL * live_items ? live_items : (T + 1) / 2);
+    if (c >= ctas) return;
+    const int q0 = T / ctas, r0 = T - q0 * ctas;
+    auto stretch = [&](int c) { return q0 * c + (unsigned)(r0 * c) / (unsigned)ctas; };   // floor(T c / ctas)
+    int x = stretch(c);
+    const int x_end = stretch(c + 1);
+    if (a.B <= kThreads) {
+        const int lo = (int)before * items;
+        if (lo <= x && x < lo + mine_first * items) req_s = tid, first_s = lo;
+        __syncthreads();
+    } else {
+        int done = 0;
+        for (int base = 0; base < a.B; base += kThreads) {
+            const int b = base + tid, p = b < a.B ? pages_of(a.kv_len[b]) : 0;
+            __syncthreads();
+            const int all = (int)block_sum(p, before), lo = (done + (int)before) * items;
+            if (lo <= x && x < lo + p * items) req_s = b, first_s = lo;
+            done += all;
+            if (x < done * items) break;
         }
-        const int item = (int)((x - first) / pages), kvh = item / a.blocks, h0 = (item - kvh * a.blocks) * HB;
-        const long long i0 = first + (long long)item * pages, i1 = i0 + pages, x1 = min(i1, x_end);
-        const int step0 = (int)(x - i0) * (TS_PAGE_KEYS / 16),
-                  step1 = min((int)(x1 - i0) * (TS_PAGE_KEYS / 16), (n + 15) / 16);
-        const int32_t *bt = a.bt + (size_t)b * a.max_pages;
+        __syncthreads();
+    }
+    int req = req_s, first = first_s;      // a request, and the line's tile at which it starts
+    auto segment = [&](int x) {            // the one that starts at tile x, below x_end
+        Segment z;
+        int n, pages;
+        while (true) {
+            n = req < kThreads ? len_s[req] : a.kv_len[req], pages = pages_of(n);
+            if (x < first + pages * items) break;
+            first += pages * items;
+            ++req;
+        }
+        const int item = (unsigned)(x - first) / (unsigned)pages;
+        z.b = req, z.n = n, z.kvh = a.blocks == 1 ? item : item / a.blocks, z.h0 = (item - z.kvh * a.blocks) * HB;
+        z.i0 = first + item * pages, z.i1 = z.i0 + pages, z.x1 = min(z.i1, x_end);
+        z.step0 = (x - z.i0) * (TS_PAGE_KEYS / 16);
+        z.step1 = min((z.x1 - z.i0) * (TS_PAGE_KEYS / 16), (n + 15) / 16);
+        z.bt = a.bt + (size_t)req * a.max_pages;
+        return z;
+    };
 
-        // ---- a step's loads. Lane (g, t) takes of K rows g and g + 8, pieces t, t + 4, ..; of V rows 2t, 2t + 1, 2t + 8,
-        // 2t + 9, pieces g, g + 8
-        uint4 kr[2][KC], vr[4][VC], qr[NT][KC];
-        const uint4 zero = make_uint4(0, 0, 0, 0);
-        auto page_of = [&](int s) { return s < step1 ? __ldg(bt + (s >> 2)) : 0; };
-        auto rows_at = [&](int page, int s) { return ((size_t)page * a.Hkv + kvh) * TS_PAGE_KEYS + (s & 3) * 16; };
-        auto is_page = [&](int page) {
-            const bool ok = page >= 0 && page < a.num_pages;
-            if (!ok) flag(a.status, TS_STATUS_INDEX);
-            return ok;
-        };
-        auto load_k = [&](int s, int page, bool ok) {
-            const uint4 *p = a.k + rows_at(page, s) * VEC + t;
+    // ---- a step's loads. Lane (g, t) takes of K rows g and g + 8, pieces t, t + 4, ..; of V rows 2t, 2t + 1, 2t + 8,
+    // 2t + 9, pieces g, g + 8
+    uint4 kr[2][KC], vr[4][VC], qr[NT][KC];
+    const uint4 zero = make_uint4(0, 0, 0, 0);
+    // a step to load: its keys' number in all, key/value head, index, page, and whether it is one of the cache's
+    struct Step {
+        int n, kvh, s, page;
+        bool ok;
+    };
+    auto page_of = [&](const Segment &z, int s) { return s < z.step1 ? __ldg(z.bt + (s >> 2)) : 0; };
+    auto step_of = [&](int n, int kvh, int s, int page, bool any) {
+        const bool ok = page >= 0 && page < a.num_pages;
+        if (any && !ok) flag(a.status, TS_STATUS_INDEX);
+        return Step{n, kvh, s, page, any && ok};
+    };
+    auto rows_at = [&](const Step &u) { return ((size_t)u.page * a.Hkv + u.kvh) * TS_PAGE_KEYS + (u.s & 3) * 16; };
+    auto load_k = [&](const Step &u) {
+        const uint4 *p = a.k + rows_at(u) * VEC + t;
 #pragma unroll
-            for (int r = 0; r < 2; ++r)
+        for (int r = 0; r < 2; ++r)
 #pragma unroll
-                for (int i = 0; i < KC; ++i)
-                    kr[r][i] = ok && s * 16 + g + 8 * r < n ? ld_stream(p + (g + 8 * r) * VEC + 4 * i) : zero;
-        };
-        auto load_v = [&](int s, int page, bool ok) {
-            const uint4 *p = a.v + rows_at(page, s) * VEC + g;
+            for (int i = 0; i < KC; ++i)
+                kr[r][i] = ld_stream(p + (g + 8 * r) * VEC + 4 * i, u.ok && u.s * 16 + g + 8 * r < u.n);
+    };
+    auto load_v = [&](const Step &u) {
+        const uint4 *p = a.v + rows_at(u) * VEC + g;
 #pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const int row = 2 * t + (r & 1) + 8 * (r >> 1);
+        for (int r = 0; r < 4; ++r) {
+            const int row = 2 * t + (r & 1) + 8 * (r >> 1);
 #pragma unroll
-                for (int i = 0; i < VC; ++i) vr[r][i] = ok && s * 16 + row < n ? ld_stream(p + row * VEC + 8 * i) : zero;
-            }
-        };
+            for (int i = 0; i < VC; ++i) vr[r][i] = ld_stream(p + row * VEC + 8 * i, u.ok && u.s * 16 + row < u.n);
+        }
+    };
+    auto load_q = [&](const Segment &z) {
 #pragma unroll
         for (int j = 0; j < NT; ++j) {
-            const int h = h0 + 8 * j + g;
-            const uint4 *p = a.q + b * a.q_stride + (size_t)(kvh * a.G + h) * VEC + t;
+            const int h = z.h0 + 8 * j + g;
+            const uint4 *p = a.q + z.b * a.q_stride + (size_t)(z.kvh * a.G + h) * VEC + t;
 #pragma unroll
             for (int i = 0; i < KC; ++i) qr[j][i] = h < a.G ? __ldg(p + 4 * i) : zero;
+        }
+    };
+    // The warps' O, maxima and sums in shared memory as one: the item's rows of out, or a part.
+    auto join_warps = [&](int b, int kvh, int h0, float *part) {
+        __syncthreads();
+        for (int q = tid; q < HB * D / 4; q += kThreads) {
+            const int h = q / (D / 4), dd = q % (D / 4) * 4;
+            if (h0 + h >= a.G) break;
+            float top = -INFINITY, sum = 0.f;
+            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) top = fmaxf(top, m_s[w][h]);
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) {
+                const float f = ex2(m_s[w][h] - guarded(top));
+                const float4 y = *reinterpret_cast<const float4 *>(&o_s[w][h][dd]);
+                sum = fmaf(l_s[w][h], f, sum);
+                acc.x = fmaf(y.x, f, acc.x), acc.y = fmaf(y.y, f, acc.y), acc.z = fmaf(y.z, f, acc.z), acc.w = fmaf(y.w, f, acc.w);
+            }
+            if (part) {
+                *reinterpret_cast<float4 *>(part + h * D + dd) = acc;
+                if (dd == 0) part[HB * D + h] = top, part[HB * (D + 1) + h] = sum;
+            } else {
+                const float f = 1.f / sum;
+                const __nv_bfloat162 r0 = __floats2bfloat162_rn(acc.x * f, acc.y * f), r1 = __floats2bfloat162_rn(acc.z * f, acc.w * f);
+                *reinterpret_cast<uint2 *>(a.out + ((size_t)b * a.Hq + kvh * a.G + h0 + h) * D + dd) =
+                    make_uint2(*reinterpret_cast<const uint32_t *>(&r0), *reinterpret_cast<const uint32_t *>(&r1));
+            }
+        }
+        __syncthreads();
+    };
+
+    // An item in several CTAs' stretches leaves a part of each in the workspace, and the CTA that counts itself last joins
+    // them. Many parts are joined in groups of kGroup first, each by its last CTA, which leaves the sum in its first part's
+    // place; the last group takes what is left over, so that no group has one part only (whose counter another item could
+    // use).
+    auto shared_of = [&](const Segment &w) {
+        Shared sh{w.b, w.kvh, w.h0};
+        const int c1 = (int)(((long long)w.i1 * ctas - 1) / T);
+        sh.c0 = sh.k0 = (int)(((long long)(w.i0 + 1) * ctas - 1) / T);
+        sh.n = c1 - sh.c0 + 1;
+        sh.groups = sh.n >= kGroupFrom ? sh.n / kGroup : 0;
+        if (sh.groups) {
+            const int at = min((c - sh.c0) / kGroup, sh.groups - 1);
+            sh.k0 = sh.c0 + at * kGroup;
+            sh.n = at == sh.groups - 1 ? sh.n - at * kGroup : kGroup;
+        }
+        return sh;
+    };
+    Segment z = segment(x);
+    bool is_shared[2] = {false, false};
+    unsigned counted[2] = {0, 0};
+    load_q(z);
+    int s = z.step0 + warp, page;          // page: of the step after the one whose loads are under way
+    if (s < z.step1) {
+        const Step u = step_of(z.n, z.kvh, s, page_of(z, s), true);
+        page = page_of(z, s + kWarps);
+        load_k(u);
+        load_v(u);
+    }
+    while (true) {
+        const bool starts = x == z.i0, ends = z.x1 == z.i1;
+        if (!(starts && ends)) {
+            is_shared[starts] = true;
+            if (tid == 0) shared_s[starts] = shared_of(z);
+        }
+        // the next segment's first step follows this one's last in the warp's loads
+        const bool more = z.x1 < x_end;
+        Segment nx;
+        int s_nx = 0, page_nx = 0, n_nx = 0, kvh_nx = 0;
+        bool step_nx = false;
+        if (more) {
+            nx = segment(z.x1);
+            n_nx = nx.n, kvh_nx = nx.kvh;
+            s_nx = nx.step0 + warp;
+            step_nx = s_nx < nx.step1;
+            page_nx = page_of(nx, s_nx);
+        }
+        if (s >= z.step1 && step_nx) {     // none of this segment's steps is this warp's
+            const Step u = step_of(nx.n, nx.kvh, s_nx, page_nx, true);
+            page = page_of(nx, s_nx + kWarps);
+            load_k(u);
+            load_v(u);
         }
         float o[NT][VEC / 2][4], m[NT][2], l[NT][2];
 #pragma unroll
@@ -197,14 +348,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm<D, NT>) k_attn_decode(DecodeA
 #pragma unroll
             for (int i = 0; i < VEC / 2; ++i) o[j][i][0] = o[j][i][1] = o[j][i][2] = o[j][i][3] = 0.f;
         }
-        int s = step0 + warp;
-        int page_v = page_of(s), page = page_of(s + kWarps);   // of the step whose V is loaded next; of the one after it
-        bool ok_v = s < step1 && is_page(page_v), ok;
-        if (s < step1) {
-            load_k(s, page_v, ok_v);
-            load_v(s, page_v, ok_v);
-        }
-        for (; s < step1; s += kWarps) {
+        for (; s < z.step1; s += kWarps) {
             float p[NT][4];
 #pragma unroll
             for (int j = 0; j < NT; ++j) {
@@ -216,17 +360,18 @@ __global__ void __launch_bounds__(kThreads, kPerSm<D, NT>) k_attn_decode(DecodeA
                 }
             }
             const int next = s + kWarps;
-            page_v = page;
-            ok = next < step1 && is_page(page);
-            if (next < step1) load_k(next, page, ok);
-            page = page_of(next + kWarps);
+            const bool here = next < z.step1;
+            const Step u = step_of(here ? z.n : n_nx, here ? z.kvh : kvh_nx, here ? next : s_nx, here ? page : page_nx, here || step_nx);
+            load_k(u);
+            if (here) page = page_of(z, next + kWarps);
+            else if (step_nx) page = page_of(nx, s_nx + kWarps);
             // scores as exponents of 2; keys behind the last one have none
             bool raise = false;
 #pragma unroll
             for (int j = 0; j < NT; ++j)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    p[j][e] = s * 16 + g + 8 * (e >> 1) < n ? p[j][e] * a.scale_log2 : -INFINITY;
+                    p[j][e] = s * 16 + g + 8 * (e >> 1) < z.n ? p[j][e] * a.scale_log2 : -INFINITY;
                     raise |= p[j][e] > m[j][e & 1] + kRoom;
                 }
             if (__any_sync(~0u, raise)) {
@@ -279,10 +424,10 @@ __global__ void __launch_bounds__(kThreads, kPerSm<D, NT>) k_attn_decode(DecodeA
                     mma(o[j][i], a0, a1, a2, a3, lo[j][0], lo[j][1]);
                 }
             }
-            if (next < step1) load_v(next, page_v, ok);
+            load_v(u);
         }
+        if (more) load_q(nx);
 
-        // ---- the CTA's warps joined
 #pragma unroll
         for (int j = 0; j < NT; ++j)
 #pragma unroll
@@ -296,78 +441,93 @@ __global__ void __launch_bounds__(kThreads, kPerSm<D, NT>) k_attn_decode(DecodeA
                     *reinterpret_cast<float2 *>(&o_s[warp][h][64 * (i / 4) + 8 * g + 2 * (i % 4)]) =
                         make_float2(o[j][i][e], o[j][i][e + 2]);
             }
-        __syncthreads();
-        const bool whole = x == i0 && x1 == i1;
-        float *part = a.parts + (size_t)(2 * c + (x == i0)) * HB * (D + 2);
-        for (int q = tid; q < HB * D / 4; q += kThreads) {
-            const int h = q / (D / 4), dd = q % (D / 4) * 4;
-            if (h0 + h >= a.G) break;
-            float top = -INFINITY, sum = 0.f;
-            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-            for (int w = 0; w < kWarps; ++w) top = fmaxf(top, m_s[w][h]);
-#pragma unroll
-            for (int w = 0; w < kWarps; ++w) {
-                const float f = ex2(m_s[w][h] - guarded(top));
-                const float4 y = *reinterpret_cast<const float4 *>(&o_s[w][h][dd]);
-                sum = fmaf(l_s[w][h], f, sum);
-                acc.x = fmaf(y.x, f, acc.x), acc.y = fmaf(y.y, f, acc.y), acc.z = fmaf(y.z, f, acc.z), acc.w = fmaf(y.w, f, acc.w);
-            }
-            if (whole) {
-                const float f = 1.f / sum;
-                __nv_bfloat162 r0 = __floats2bfloat162_rn(acc.x * f, acc.y * f), r1 = __floats2bfloat162_rn(acc.z * f, acc.w * f);
-                *reinterpret_cast<uint2 *>(a.out + ((size_t)b * a.Hq + kvh * a.G + h0 + h) * D + dd) =
-                    make_uint2(*reinterpret_cast<uint32_t *>(&r0), *reinterpret_cast<uint32_t *>(&r1));
-            } else {
-                *reinterpret_cast<float4 *>(part + h * D + dd) = acc;
-                if (dd == 0) part[HB * D + h] = top, part[HB * (D + 1) + h] = sum;
-            }
-        }
-        if (!whole) {
-            // ---- the item's CTAs c0 .. c1 joined by the one that comes here last
-            const long long c0 = ((i0 + 1) * ctas - 1) / T, c1 = (i1 * ctas - 1) / T;
-            __threadfence();
-            __syncthreads();
+        join_warps(z.b, z.kvh, z.h0, starts && ends ? nullptr : a.parts + (size_t)(2 * c + starts) * PART);
+        if (!(starts && ends) && tid == 0) counted[starts] = count_up(a.counters + shared_s[starts].k0);
+        if (!more) break;
+        x = z.x1, z = nx, s = s_nx;
+    }
+
+    // ---- parts joined by the CTA that has counted itself last
+    for (int side = 0; side < 2; ++side) {
+        if (!is_shared[side]) continue;
+        const Shared sh = shared_s[side];
+        auto last_of = [&](unsigned *counter, unsigned count, unsigned n) {
             if (tid == 0) {
-                last_s = atomicAdd(a.counters + c0, 1u) == c1 - c0;
-                if (last_s) a.counters[c0] = 0;
-                __threadfence();
+                last_s = count == n - 1;
+                if (last_s) *counter = 0, sees_counted();
             }
             __syncthreads();
-            if (last_s) {
-                for (int q = tid; q < HB * D / 4; q += kThreads) {
-                    const int h = q / (D / 4), dd = q % (D / 4) * 4;
-                    if (h0 + h >= a.G) break;
-                    float top = -INFINITY, sum = 0.f;
-                    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-                    auto part_at = [&](long long k) { return a.parts + (size_t)(2 * k + (k == c0)) * HB * (D + 2); };
-#pragma unroll 8
-                    for (long long k = c0; k <= c1; ++k) top = fmaxf(top, __ldcg(part_at(k) + HB * D + h));
-#pragma unroll 8
-                    for (long long k = c0; k <= c1; ++k) {
-                        const float *y = part_at(k);
-                        const float f = ex2(__ldcg(y + HB * D + h) - guarded(top));
-                        const float4 v = __ldcg(reinterpret_cast<const float4 *>(y + h * D + dd));
-                        sum = fmaf(__ldcg(y + HB * (D + 1) + h), f, sum);
-                        acc.x = fmaf(v.x, f, acc.x), acc.y = fmaf(v.y, f, acc.y), acc.z = fmaf(v.z, f, acc.z), acc.w = fmaf(v.w, f, acc.w);
-                    }
-                    const float f = 1.f / sum;
-                    __nv_bfloat162 r0 = __floats2bfloat162_rn(acc.x * f, acc.y * f), r1 = __floats2bfloat162_rn(acc.z * f, acc.w * f);
-                    *reinterpret_cast<uint2 *>(a.out + ((size_t)b * a.Hq + kvh * a.G + h0 + h) * D + dd) =
-                        make_uint2(*reinterpret_cast<uint32_t *>(&r0), *reinterpret_cast<uint32_t *>(&r1));
+            const bool yes = last_s;
+            __syncthreads();
+            return yes;
+        };
+        // n parts from k0 on, step apart: weights first, then a warp every kWarps-th part
+        auto join_parts = [&](int k0, int n, int step, float *part) {
+            auto part_at = [&](int i) {
+                const int k = k0 + i * step;
+                return a.parts + (size_t)(2 * k + (k == sh.c0)) * PART;
+            };
+            for (int i = tid; i < n * HB; i += kThreads) {
+                const float *y = part_at(i / HB) + HB * D + i % HB;
+                const bool in = sh.h0 + i % HB < a.G;
+                pm_s[i / HB][i % HB] = in ? __ldcg(y) : 0.f;
+                pl_s[i / HB][i % HB] = in ? __ldcg(y + HB) : 0.f;
+            }
+            __syncthreads();
+            if (tid < HB) {
+                float top = -INFINITY, sum = 0.f;
+                for (int i = 0; i < n; ++i) top = fmaxf(top, pm_s[i][tid]);
+                for (int i = 0; i < n; ++i) {
+                    const float f = ex2(pm_s[i][tid] - guarded(top));
+                    sum = fmaf(pl_s[i][tid], f, sum);
+                    pm_s[i][tid] = f;
+                }
+#pragma unroll
+                for (int v = 0; v < kWarps; ++v) m_s[v][tid] = top, l_s[v][tid] = v ? 0.f : sum;
+            }
+            __syncthreads();
+            constexpr int NV = HB * D / 128;   // 16-byte pieces of a part a lane
+            float4 acc[NV];
+#pragma unroll
+            for (int i = 0; i < NV; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 2
+            for (int k = warp; k < n; k += kWarps) {
+                const float4 *y = reinterpret_cast<const float4 *>(part_at(k));
+#pragma unroll
+                for (int i = 0; i < NV; ++i) {
+                    const int q = i * 32 + lane, h = q / (D / 4);
+                    if (sh.h0 + h >= a.G) continue;
+                    const float f = pm_s[k][h];
+                    const float4 v = __ldcg(y + q);
+                    acc[i].x = fmaf(v.x, f, acc[i].x), acc[i].y = fmaf(v.y, f, acc[i].y);
+                    acc[i].z = fmaf(v.z, f, acc[i].z), acc[i].w = fmaf(v.w, f, acc[i].w);
                 }
             }
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                const int q = i * 32 + lane;
+                *reinterpret_cast<float4 *>(&o_s[warp][q / (D / 4)][q % (D / 4) * 4]) = acc[i];
+            }
+            join_warps(sh.b, sh.kvh, sh.h0, part);
+        };
+        if (!last_of(a.counters + sh.k0, counted[side], sh.n)) continue;
+        if (!sh.groups) {
+            join_parts(sh.c0, sh.n, 1, nullptr);
+            continue;
         }
-        __syncthreads();   // shared memory is the next item's
-        x = x1;
+        join_parts(sh.k0, sh.n, 1, a.parts + (size_t)(2 * sh.k0 + (sh.k0 == sh.c0)) * PART);
+        unsigned *const over = a.counters + gridDim.x + sh.c0;
+        unsigned count = 0;
+        if (tid == 0) count = count_up(over);
+        if (last_of(over, count, sh.groups)) join_parts(sh.c0, sh.groups, kGroup, nullptr);
     }
 }
 
 int grid_of(int d, int HB) {
-    return num_sms() * (d == 64 ? (HB == 8 ? kPerSm<64, 1> : kPerSm<64, 2>) : (HB == 8 ? kPerSm<128, 1> : kPerSm<128, 2>));
+    return std::min(kMostCtas, num_sms() * (d == 64 ? (HB == 8 ? kPerSm<64, 1> : kPerSm<64, 2>) : (HB == 8 ? kPerSm<128, 1> : kPerSm<128, 2>)));
 }
 int heads_of(int G) { return G > 8 ? 16 : 8; }
-size_t counter_bytes() { return ((size_t)num_sms() * kPerSm<64, 1> * 4 + 255) / 256 * 256; }   // the largest grid's
+size_t counter_bytes() { return (size_t)(kMostCtas + 1) * 8; }   // any grid's
 
 }  // namespace
 
