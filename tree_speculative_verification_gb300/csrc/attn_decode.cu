@@ -27,7 +27,6 @@
 namespace ts {
 namespace {
 
-constexpr int kWarps = 4, kThreads = 32 * kWarps;
 constexpr float kRoom = 8.f;   // how far (in powers of 2) a score may pass the running maximum before that is raised
 
 struct DecodeArgs {
@@ -73,9 +72,19 @@ __device__ __forceinline__ uint32_t part_of(const uint4 &v, int i) { return i ==
 
 __device__ __forceinline__ float guarded(float m) { return m == -INFINITY ? 0.f : m; }
 
-// CTAs an SM, as the registers allow.
+// As many warps an SM as the registers allow, in CTAs of four, or all in one CTA where there are few items: the more warps
+// share an item, the fewer parts of it are joined through the workspace, but the more of them wait for one another at its
+// end. In fours and in one: one request of 16384 keys, 8 heads 22.0 and 17.5 us; 8 requests of 2048 keys, 8 heads 18.0 and
+// 19.6; 64 requests of 1024 keys, 56 heads 278 and 295.
 template <int D, int NT>
-constexpr int kPerSm = D == 64 ? (NT == 1 ? 4 : 3) : (NT == 1 ? 3 : 2);
+constexpr int kFours = D == 64 ? (NT == 1 ? 4 : 3) : (NT == 1 ? 3 : 2);
+template <int D, int NT, bool ONE>
+constexpr int kWarps = ONE ? 4 * kFours<D, NT> : 4;
+template <int D, int NT, bool ONE>
+constexpr int kPerSm = ONE ? 1 : kFours<D, NT>;
+template <int D, int NT, bool ONE>
+constexpr int kSmem = kWarps<D, NT, ONE> * 8 * NT * (D + 4) * 4;
+constexpr int kFewItems = 48;
 
 // A stretch of one item's keys: steps [step0, step1) of 16 keys.
 struct Segment {
@@ -92,6 +101,7 @@ struct Shared {
 };
 
 constexpr int kGroup = 16, kGroupFrom = 33;   // parts are joined in two levels, kGroup at a time, from kGroupFrom on
+constexpr int kWholeSteps = 4, kLeastSteps = 1;
 constexpr int kMostParts = 64, kMostCtas = kMostParts * kGroup - 1;   // parts, or groups, in one join; CTAs that allows
 
 // Adds one to a counter: what the CTA has written before (behind a barrier) is seen by whoever finds it counted and
@@ -103,17 +113,19 @@ __device__ __forceinline__ unsigned count_up(unsigned *p) {
 }
 __device__ __forceinline__ void sees_counted() { asm volatile("fence.acq_rel.gpu;" ::: "memory"); }
 
-template <int D, int NT>
-__global__ void __launch_bounds__(kThreads, kPerSm<D, NT>) k_attn_decode(DecodeArgs a) {
+template <int D, int NT, bool ONE>
+__global__ void __launch_bounds__(32 * kWarps<D, NT, ONE>, kPerSm<D, NT, ONE>) k_attn_decode(DecodeArgs a) {
+    constexpr int W = kWarps<D, NT, ONE>, kThreads = 32 * W;
     constexpr int HB = 8 * NT;           // query heads of a block
     constexpr int VEC = D / 8;           // 16-byte pieces of a row
     constexpr int KC = D / 32, VC = D / 64;
     constexpr int ROW = D + 4;           // floats between heads in shared memory
     constexpr int PART = HB * (D + 2);   // floats of a part: O, maxima, sums
-    __shared__ float o_s[kWarps][HB][ROW];
-    __shared__ float m_s[kWarps][HB], l_s[kWarps][HB], pm_s[kMostParts][HB], pl_s[kMostParts][HB];
-    __shared__ long long sum_s[kWarps];
-    __shared__ int len_s[kThreads], req_s, first_s, items_s[kWarps], last_s;
+    extern __shared__ float smem[];
+    float(*o_s)[HB][ROW] = reinterpret_cast<float(*)[HB][ROW]>(smem);   // [W]
+    __shared__ float m_s[W][HB], l_s[W][HB], f_s[kMostParts][HB];
+    __shared__ long long sum_s[W];
+    __shared__ int len_s[kThreads], req_s, first_s, items_s[W], last_s;
     __shared__ Shared shared_s[2];   // of the CTA's first segment, of its last
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
     pdl_wait();
@@ -137,7 +149,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm<D, NT>) k_attn_decode(DecodeA
         long long all = 0;
         before = run - v;
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
+        for (int w = 0; w < W; ++w) {
             if (w < warp) before += sum_s[w];
             all += sum_s[w];
         }
@@ -162,20 +174,23 @@ __global__ void __launch_bounds__(kThreads, kPerSm<D, NT>) k_attn_decode(DecodeA
     const long long all_tiles = block_sum(mine, before) * items;
     int live_items = 0;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) live_items += items_s[w];
+    for (int w = 0; w < W; ++w) live_items += items_s[w];
     if (all_tiles == 0 || all_tiles > INT32_MAX) {
         if (all_tiles && blockIdx.x == 0 && tid == 0) flag(a.status, TS_STATUS_INDEX);
         return;
     }
     const int T = (int)all_tiles, c = blockIdx.x;
     live_items *= items;
-    // As many CTAs as the GPU holds; a whole number of them an item where that leaves no more than a tenth of them out, so
-    // that equal requests are cut alike, no CTA's stretch holds parts of two items, and no item has one part more.
+    // As many CTAs as the GPU holds. A part that has to be joined costs 3 us, a step of every warp 0.8 us: items of up to
+    // kWhole tiles are not cut, and none into parts of less than kLeast. Where there are enough CTAs they are a whole number
+    // an item, unless that leaves out more than a tenth of them: equal requests are then cut alike, no CTA's stretch holds
+    // parts of two items, and no item has one part more.
+    constexpr int kWhole = kWholeSteps * W / 4, kLeast = kLeastSteps * W / 4;
     int ctas = gridDim.x;
-    if (live_items <= ctas && ctas % live_items <= ctas / 10) ctas -= ctas % live_items;
-    // A part that has to be joined costs 2.5 us, a tile more 1 us: up to three tiles an item are not cut, and no CTA gets
-    // less than two tiles of a longer one.
-    ctas = min(ctas, T <= 3LL * live_items ? live_items : (T + 1) / 2);
+    if (live_items <= ctas) {
+        const int pages = T / live_items, most = pages <= kWhole ? 1 : pages / kLeast, fit = ctas / live_items;
+        if (most <= fit || ctas % live_items <= ctas / 10) ctas = min(most, fit) * live_items;
+    }
     if (c >= ctas) return;
     const int q0 = T / ctas, r0 = T - q0 * ctas;
     auto stretch = [&](int c) { return q0 * c + (unsigned)(r0 * c) / (unsigned)ctas; };   // floor(T c / ctas)
@@ -267,9 +282,9 @@ __global__ void __launch_bounds__(kThreads, kPerSm<D, NT>) k_attn_decode(DecodeA
             float top = -INFINITY, sum = 0.f;
             float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-            for (int w = 0; w < kWarps; ++w) top = fmaxf(top, m_s[w][h]);
+            for (int w = 0; w < W; ++w) top = fmaxf(top, m_s[w][h]);
 #pragma unroll
-            for (int w = 0; w < kWarps; ++w) {
+            for (int w = 0; w < W; ++w) {
                 const float f = ex2(m_s[w][h] - guarded(top));
                 const float4 y = *reinterpret_cast<const float4 *>(&o_s[w][h][dd]);
                 sum = fmaf(l_s[w][h], f, sum);
@@ -309,10 +324,13 @@ __global__ void __launch_bounds__(kThreads, kPerSm<D, NT>) k_attn_decode(DecodeA
     bool is_shared[2] = {false, false};
     unsigned counted[2] = {0, 0};
     load_q(z);
-    int s = z.step0 + warp, page;          // page: of the step after the one whose loads are under way
+    // steps go round the warps, on from segment to segment: turn is the warp that a segment starts with
+    int turn = 0;
+    auto first_step = [&](const Segment &w) { return w.step0 + warp - turn + (warp < turn ? W : 0); };
+    int s = first_step(z), page;           // page: of the step after the one whose loads are under way
     if (s < z.step1) {
         const Step u = step_of(z.n, z.kvh, s, page_of(z, s), true);
-        page = page_of(z, s + kWarps);
+        page = page_of(z, s + W);
         load_k(u);
         load_v(u);
     }
@@ -330,13 +348,14 @@ __global__ void __launch_bounds__(kThreads, kPerSm<D, NT>) k_attn_decode(DecodeA
         if (more) {
             nx = segment(z.x1);
             n_nx = nx.n, kvh_nx = nx.kvh;
-            s_nx = nx.step0 + warp;
+            turn = (turn + z.step1 - z.step0) % W;
+            s_nx = first_step(nx);
             step_nx = s_nx < nx.step1;
             page_nx = page_of(nx, s_nx);
         }
         if (s >= z.step1 && step_nx) {     // none of this segment's steps is this warp's
             const Step u = step_of(nx.n, nx.kvh, s_nx, page_nx, true);
-            page = page_of(nx, s_nx + kWarps);
+            page = page_of(nx, s_nx + W);
             load_k(u);
             load_v(u);
         }
@@ -348,7 +367,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm<D, NT>) k_attn_decode(DecodeA
 #pragma unroll
             for (int i = 0; i < VEC / 2; ++i) o[j][i][0] = o[j][i][1] = o[j][i][2] = o[j][i][3] = 0.f;
         }
-        for (; s < z.step1; s += kWarps) {
+        for (; s < z.step1; s += W) {
             float p[NT][4];
 #pragma unroll
             for (int j = 0; j < NT; ++j) {
@@ -359,12 +378,12 @@ __global__ void __launch_bounds__(kThreads, kPerSm<D, NT>) k_attn_decode(DecodeA
                     mma(p[j], kr[0][i].z, kr[1][i].z, kr[0][i].w, kr[1][i].w, qr[j][i].z, qr[j][i].w);
                 }
             }
-            const int next = s + kWarps;
+            const int next = s + W;
             const bool here = next < z.step1;
             const Step u = step_of(here ? z.n : n_nx, here ? z.kvh : kvh_nx, here ? next : s_nx, here ? page : page_nx, here || step_nx);
             load_k(u);
-            if (here) page = page_of(z, next + kWarps);
-            else if (step_nx) page = page_of(nx, s_nx + kWarps);
+            if (here) page = page_of(z, next + W);
+            else if (step_nx) page = page_of(nx, s_nx + W);
             // scores as exponents of 2; keys behind the last one have none
             bool raise = false;
 #pragma unroll
@@ -461,46 +480,62 @@ __global__ void __launch_bounds__(kThreads, kPerSm<D, NT>) k_attn_decode(DecodeA
             __syncthreads();
             return yes;
         };
-        // n parts from k0 on, step apart: weights first, then a warp every kWarps-th part
+        // n parts from k0 on, step apart, a warp every W-th; their weights by a warp a head, the first parts' loads under way
         auto join_parts = [&](int k0, int n, int step, float *part) {
+            constexpr int NV = HB * D / 128;   // 16-byte pieces of a part a lane
             auto part_at = [&](int i) {
                 const int k = k0 + i * step;
                 return a.parts + (size_t)(2 * k + (k == sh.c0)) * PART;
             };
-            for (int i = tid; i < n * HB; i += kThreads) {
-                const float *y = part_at(i / HB) + HB * D + i % HB;
-                const bool in = sh.h0 + i % HB < a.G;
-                pm_s[i / HB][i % HB] = in ? __ldcg(y) : 0.f;
-                pl_s[i / HB][i % HB] = in ? __ldcg(y + HB) : 0.f;
-            }
-            __syncthreads();
-            if (tid < HB) {
-                float top = -INFINITY, sum = 0.f;
-                for (int i = 0; i < n; ++i) top = fmaxf(top, pm_s[i][tid]);
-                for (int i = 0; i < n; ++i) {
-                    const float f = ex2(pm_s[i][tid] - guarded(top));
-                    sum = fmaf(pl_s[i][tid], f, sum);
-                    pm_s[i][tid] = f;
-                }
-#pragma unroll
-                for (int v = 0; v < kWarps; ++v) m_s[v][tid] = top, l_s[v][tid] = v ? 0.f : sum;
-            }
-            __syncthreads();
-            constexpr int NV = HB * D / 128;   // 16-byte pieces of a part a lane
-            float4 acc[NV];
-#pragma unroll
-            for (int i = 0; i < NV; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 2
-            for (int k = warp; k < n; k += kWarps) {
-                const float4 *y = reinterpret_cast<const float4 *>(part_at(k));
+            float4 acc[NV], v[NV];
+            auto load = [&](int k) {
 #pragma unroll
                 for (int i = 0; i < NV; ++i) {
-                    const int q = i * 32 + lane, h = q / (D / 4);
-                    if (sh.h0 + h >= a.G) continue;
-                    const float f = pm_s[k][h];
-                    const float4 v = __ldcg(y + q);
-                    acc[i].x = fmaf(v.x, f, acc[i].x), acc[i].y = fmaf(v.y, f, acc[i].y);
-                    acc[i].z = fmaf(v.z, f, acc[i].z), acc[i].w = fmaf(v.w, f, acc[i].w);
+                    const int q = i * 32 + lane;
+                    acc[i] = make_float4(0.f, 0.f, 0.f, 0.f), v[i] = acc[i];
+                    if (k < n && sh.h0 + q / (D / 4) < a.G) v[i] = __ldcg(reinterpret_cast<const float4 *>(part_at(k)) + q);
+                }
+            };
+            load(warp);
+            for (int h = warp; h < HB; h += W) {
+                constexpr int PL = kMostParts / 32;
+                float mk[PL], lk[PL], top = -INFINITY, sum = 0.f;
+#pragma unroll
+                for (int i = 0; i < PL; ++i) {
+                    const int k = lane + 32 * i;
+                    const bool in = k < n && sh.h0 + h < a.G;
+                    const float *y = part_at(k) + HB * D + h;
+                    mk[i] = in ? __ldcg(y) : -INFINITY;
+                    lk[i] = in ? __ldcg(y + HB) : 0.f;
+                    top = fmaxf(top, mk[i]);
+                }
+#pragma unroll
+                for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
+#pragma unroll
+                for (int i = 0; i < PL; ++i) {
+                    const float f = ex2(mk[i] - guarded(top));
+                    sum = fmaf(lk[i], f, sum);
+                    if (lane + 32 * i < n) f_s[lane + 32 * i][h] = f;
+                }
+#pragma unroll
+                for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
+                if (lane < W) m_s[lane][h] = top, l_s[lane][h] = lane ? 0.f : sum;
+            }
+            __syncthreads();
+            for (int k = warp; k < n; k += W) {
+                float4 now[NV];
+#pragma unroll
+                for (int i = 0; i < NV; ++i) now[i] = v[i];
+#pragma unroll
+                for (int i = 0; i < NV; ++i) {
+                    const int q = i * 32 + lane;
+                    if (k + W < n && sh.h0 + q / (D / 4) < a.G) v[i] = __ldcg(reinterpret_cast<const float4 *>(part_at(k + W)) + q);
+                }
+#pragma unroll
+                for (int i = 0; i < NV; ++i) {
+                    const float f = f_s[k][(i * 32 + lane) / (D / 4)];
+                    acc[i].x = fmaf(now[i].x, f, acc[i].x), acc[i].y = fmaf(now[i].y, f, acc[i].y);
+                    acc[i].z = fmaf(now[i].z, f, acc[i].z), acc[i].w = fmaf(now[i].w, f, acc[i].w);
                 }
             }
 #pragma unroll
@@ -523,18 +558,35 @@ __global__ void __launch_bounds__(kThreads, kPerSm<D, NT>) k_attn_decode(DecodeA
     }
 }
 
-int grid_of(int d, int HB) {
-    return std::min(kMostCtas, num_sms() * (d == 64 ? (HB == 8 ? kPerSm<64, 1> : kPerSm<64, 2>) : (HB == 8 ? kPerSm<128, 1> : kPerSm<128, 2>)));
+template <int D, int NT, bool ONE>
+int grid_of() {
+    return std::min(kMostCtas, num_sms() * kPerSm<D, NT, ONE>);
+}
+int most_ctas(int d, int HB) {
+    return d == 64 ? (HB == 8 ? grid_of<64, 1, false>() : grid_of<64, 2, false>())
+                   : (HB == 8 ? grid_of<128, 1, false>() : grid_of<128, 2, false>());
 }
 int heads_of(int G) { return G > 8 ? 16 : 8; }
 size_t counter_bytes() { return (size_t)(kMostCtas + 1) * 8; }   // any grid's
+
+template <int D, int NT, bool ONE>
+cudaError_t launch_as(const DecodeArgs &a, cudaStream_t s) {
+    constexpr auto kern = k_attn_decode<D, NT, ONE>;
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem<D, NT, ONE>);
+    if (e != cudaSuccess) return e;
+    return launch(kern, dim3(grid_of<D, NT, ONE>()), dim3(32 * kWarps<D, NT, ONE>), kSmem<D, NT, ONE>, s, a);
+}
+template <int D, int NT>
+cudaError_t launch_decode(const DecodeArgs &a, cudaStream_t s) {
+    return (long long)a.B * a.Hkv * a.blocks <= kFewItems ? launch_as<D, NT, true>(a, s) : launch_as<D, NT, false>(a, s);
+}
 
 }  // namespace
 
 // Counters first: one workspace serves calls of several sizes.
 size_t decode_ws_bytes(int B, int Hq, int Hkv, int d) {
     const int HB = heads_of(Hq / Hkv);
-    return counter_bytes() + (size_t)grid_of(d, HB) * 2 * HB * (d + 2) * 4;
+    return counter_bytes() + (size_t)most_ctas(d, HB) * 2 * HB * (d + 2) * 4;
 }
 
 cudaError_t launch_attn_decode(void *out, const void *q, long long q_stride, const ts_paged_kv &kv,
@@ -559,9 +611,8 @@ cudaError_t launch_attn_decode(void *out, const void *q, long long q_stride, con
                        (unsigned *)ws,
                        (float *)((char *)ws + counter_bytes()),
                        status};
-    auto go = [&](auto kern) { return launch(kern, dim3(grid_of(d, HB)), dim3(kThreads), 0, s, a); };
-    if (d == 128) return HB == 8 ? go(k_attn_decode<128, 1>) : go(k_attn_decode<128, 2>);
-    return HB == 8 ? go(k_attn_decode<64, 1>) : go(k_attn_decode<64, 2>);
+    if (d == 128) return HB == 8 ? launch_decode<128, 1>(a, s) : launch_decode<128, 2>(a, s);
+    return HB == 8 ? launch_decode<64, 1>(a, s) : launch_decode<64, 2>(a, s);
 }
 
 }  // namespace ts
