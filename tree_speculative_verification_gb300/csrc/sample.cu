@@ -11,15 +11,28 @@
 // wrongly about once in a thousand draws. So weights are whole numbers, the
 // largest 2^40 (weight): their sums are exact, whatever the order, up to 2^18
 // tokens.
+//
+// A row stays on the chip: a cluster of CTAs reads it once, each keeps a segment
+// in shared memory, and the passes over it (maximum, a histogram where a filter
+// needs one, kept weights, output rows) run there.
+#include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <math.h>
 
+#include <algorithm>
+
+#include "attn_common.cuh"
 #include "decode.cuh"
 
 namespace ts {
 namespace {
 
+namespace cg = cooperative_groups;
+
 constexpr int kThreads = 512, kWarps = kThreads / 32;
+constexpr int kGroup = 128;                    // elements of a warp's turn: a sum of weights is kept for each
+constexpr int kMaxSeg = 32896;                 // elements of a segment: 2^18 + 7 over 8 CTAs, in whole groups
+constexpr int kBins = kThreads, kList = 512;   // a thread a bin, a thread a candidate
 constexpr uint32_t kKeyLowest = 0x00800000u;   // key of the lowest finite number
 typedef unsigned long long u64;
 
@@ -32,25 +45,29 @@ __device__ __forceinline__ float value_of(uint32_t k) {
     return __uint_as_float(k & 0x80000000u ? k & 0x7fffffffu : ~k);
 }
 
+// A token's place in the order as one rising number.
+constexpr int kIdBits = 18;
+__device__ __forceinline__ u64 order_of(uint32_t key, int id) { return (u64)(uint32_t)~key << kIdBits | (uint32_t)id; }
+
 // 2^(j / 8) as two floats each.
 __constant__ float kRootHi[8] = {0x1.0000000000000p+0f, 0x1.172b840000000p+0f, 0x1.306fe00000000p+0f, 0x1.4bfdae0000000p+0f,
                                  0x1.6a09e60000000p+0f, 0x1.8ace540000000p+0f, 0x1.ae89fa0000000p+0f, 0x1.d5818e0000000p+0f};
 __constant__ float kRootLo[8] = {0x0.0p+0f, -0x1.c157420000000p-27f, 0x1.4636e20000000p-25f, -0x1.593abc0000000p-25f,
                                  0x1.9fcef40000000p-26f, 0x1.15506e0000000p-27f, -0x1.a94b140000000p-26f, -0x1.822dbc0000000p-27f};
 
-// exp((x - top) / T) in units of 2^-40, to the unit and some 2^-38 of itself.
-// y = (x - top) log2(e) / T as a sum of two floats (the difference and the
-// products by their exact errors), y = n + j / 8 + g, and
-// 2^y = 2^n 2^(j/8) (1 + t + t^2 / 2 + ...), t = g ln 2, |t| < 0.0434: the first
-// two terms as sums of two floats, the rest (below 2^-16) in one.
+// exp((x - top) / T) in units of 2^-40: y = (x - top) log2(e) / T as a sum of two floats (the difference and the products
+// by their exact errors).
+//  - Weights below 2^-8: ex2 and a correction, to some 2^-22 of themselves.
+//  - From 2^-8 on to the unit and some 2^-38 of themselves: y = n + j / 8 + g, and 2^y = 2^n 2^(j/8) (1 + t + t^2 / 2 + ..),
+//    t = g ln 2, |t| < 0.0434: the first two terms as sums of two floats, the rest (below 2^-16) in one.
 struct Weights {
     float top, ch, cl;   // log2(e) / T = ch + cl
-    __device__ __forceinline__ u64 operator()(float x) const {
-        if (x == top) return 1ull << 40;
+    __device__ __forceinline__ void exponent(float x, float &yh, float &yl) const {
         const float dh = x - top, bb = dh - x, dl = (x - (dh - bb)) - (top + bb);
-        const float yh = dh * ch;
-        if (!(yh > -44.f)) return 0;
-        const float yl = fmaf(dh, ch, -yh) + fmaf(dh, cl, dl * ch);
+        yh = dh * ch;
+        yl = fmaf(dh, ch, -yh) + fmaf(dh, cl, dl * ch);
+    }
+    __device__ __noinline__ static u64 heavy(float yh, float yl) {
         const float n8 = rintf(yh * 8.f), f = fmaf(n8, -0.125f, yh);
         const float gh = f + yl, gl = yl - (gh - f);
         const float L = 0.693147182464599609375f, Ll = -1.904654299957767e-09f;   // ln 2
@@ -58,7 +75,7 @@ struct Weights {
         const float hh = 0.5f * th, sh = hh * th, sl = fmaf(hh, th, -sh) + th * tl;
         const float r = th * th * th * fmaf(th, fmaf(th, fmaf(th, 1.f / 720, 1.f / 120), 1.f / 24), 1.f / 6);
         const float ph = th + sh, pl = (sh - (ph - th)) + ((tl + sl) + r);
-        const int m = (int)n8, j = m & 7, n = m >> 3;                             // m = 8 n + j
+        const int m = (int)n8, j = m & 7, n = m >> 3;   // m = 8 n + j
         const float Rh = kRootHi[j], Rl = kRootLo[j];
         const float z = Rh * ph, hi = Rh + z, lo = (z - (hi - Rh)) + (fmaf(Rh, ph, -z) + fmaf(Rh, pl, fmaf(Rl, ph, Rl)));
         // hi in [0.95, 2.1): a whole number of 2^-24; in units of 2^-42, then 2^(n - 40)
@@ -66,204 +83,489 @@ struct Weights {
         const int sft = 2 - n;
         return (u64)((v + (1ll << (sft - 1))) >> sft);
     }
-    // The same as a float, to some 2^-22 of itself.
+    __device__ __forceinline__ u64 operator()(float x) const {
+        float yh, yl;
+        exponent(x, yh, yl);
+        if (x == top) return 1ull << 40;
+        if (yh >= -8.f) return heavy(yh, yl);
+        return yh > -44.f ? __float2uint_rn(ex2(yh) * fmaf(yl, 762123384786.22f, 1099511627776.f)) : 0u;   // 2^40 (1 + yl ln 2)
+    }
+    // The same as a float, to some 2^-21 of itself.
     __device__ __forceinline__ float real(float x) const {
-        const float dh = x - top, bb = dh - x, dl = (x - (dh - bb)) - (top + bb), yh = dh * ch;
-        if (!(yh > -150.f)) return 0.f;
-        return exp2f(yh) * fmaf(fmaf(dh, ch, -yh) + fmaf(dh, cl, dl * ch), 0.693147182f, 1.f);
+        float yh, yl;
+        exponent(x, yh, yl);
+        return yh > -150.f ? exp2f(yh) * fmaf(yl, 0.693147182f, 1.f) : 0.f;
     }
 };
 
-template <typename T>
-__device__ __forceinline__ float load(const void *row, int i) {
-    if constexpr (sizeof(T) == 2) return __bfloat162float(((const __nv_bfloat16 *)row)[i]);
-    else return ((const float *)row)[i];
+// Four elements of a row's segment as floats.
+__device__ __forceinline__ void load4(const float *p, float (&x)[4]) {
+    const float4 v = *reinterpret_cast<const float4 *>(p);
+    x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w;
+}
+__device__ __forceinline__ void load4(const __nv_bfloat16 *p, float (&x)[4]) {
+    const uint2 v = *reinterpret_cast<const uint2 *>(p);
+    x[0] = __uint_as_float(v.x << 16), x[1] = __uint_as_float(v.x & 0xffff0000u);
+    x[2] = __uint_as_float(v.y << 16), x[3] = __uint_as_float(v.y & 0xffff0000u);
 }
 
-template <typename T>
-__device__ __forceinline__ T warp_sum(T v) {
+// The sum over the warp of numbers below 2^43.
+__device__ __forceinline__ u64 warp_sum(u64 v) {
+    const uint32_t lo = __reduce_add_sync(~0u, (uint32_t)v & 0xffffffu), hi = __reduce_add_sync(~0u, (uint32_t)(v >> 24));
+    return ((u64)hi << 24) + lo;
+}
+__device__ __forceinline__ u64 warp_scan(u64 v) {   // inclusive
 #pragma unroll
-    for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(~0u, v, o);
+    for (int o = 1; o < 32; o <<= 1) {
+        const u64 y = __shfl_up_sync(~0u, v, o);
+        if ((threadIdx.x & 31) >= o) v += y;
+    }
     return v;
 }
 
-struct Pair {
-    u64 mass, count;
+struct Shared {
+    uint32_t lo[kBins], hi[kBins];   // the segment's histogram: 64-bit sums in two halves (lo alone: counts)
+    u64 list[kList];                 // the cluster's candidates, in its first CTA: ~key and id, so that order is rising
+    u64 sums[kMaxSeg / kGroup];      // kept weights of each group of the segment
+    u64 part[kWarps];
+    u64 from[3][8];                  // what the cluster's CTAs tell one another, in turn
+    float top[kWarps];
+    u64 cut;                         // the last token kept, as in list
+    int n_list, at;
+    u64 above;
 };
-// Sums over the CTA, for every thread.
-__device__ Pair block_sum(Pair v, Pair *s) {
-    v.mass = warp_sum(v.mass), v.count = warp_sum(v.count);
-    __syncthreads();
-    if ((threadIdx.x & 31) == 0) s[threadIdx.x >> 5] = v;
-    __syncthreads();
-    v = s[0];
-    for (int w = 1; w < kWarps; ++w) v.mass += s[w].mass, v.count += s[w].count;
-    return v;
-}
 
-// A CTA a row. The cut is found by bisection over the values' keys.
+// A cluster a row, segment SL elements. Positions count from the 16-byte boundary at or before the row's first element
+// (lead elements before it); those outside the row hold -inf.
 template <typename T>
-__global__ void __launch_bounds__(kThreads) k_sample(SampleArgs a) {
-    __shared__ Pair part[kWarps];
-    __shared__ float top_s[kWarps];
-    __shared__ int found_s;
-    const int r = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, V = a.V;
+__global__ void __launch_bounds__(kThreads, 2) k_sample(SampleArgs a, int SL) {
+    extern __shared__ uint4 smem[];
+    Shared &sm = *reinterpret_cast<Shared *>(smem);
+    T *const seg = reinterpret_cast<T *>(reinterpret_cast<char *>(smem) + (sizeof(Shared) + 15) / 16 * 16);
+    const cg::cluster_group cluster = cg::this_cluster();
+    const int C = cluster.num_blocks(), rank = cluster.block_rank();
+    const int r = blockIdx.x / C, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, V = a.V;
+    auto sync = [&] {
+        if (C == 1) __syncthreads();
+        else cluster.sync();
+    };
+    if (C > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");   // the cluster's CTAs are there:
     pdl_wait();
     pdl_trigger();
-    const void *row = (const char *)a.logits + (size_t)r * a.stride * sizeof(T);
+    const T *const row = reinterpret_cast<const T *>(a.logits) + (size_t)r * a.stride;
+    const int lead = (int)(((uintptr_t)row & 15) / sizeof(T)), base = rank * SL;
     const float temp = a.temperature ? a.temperature[r] : 1.f, top_p = a.top_p ? a.top_p[r] : 1.f,
                 min_p = a.min_p ? a.min_p[r] : 0.f, u = a.u ? a.u[r] : 0.f;
     const int top_k = a.top_k ? a.top_k[r] : 0;
+
+    // ---- the segment into shared memory; its maximum
+    constexpr int VE = 16 / sizeof(T);
     float top = -INFINITY;
     bool bad = false;
-    for (int i = tid; i < V; i += kThreads) {
-        const float x = load<T>(row, i);
-        bad |= !(x < INFINITY);
-        top = fmaxf(top, x);
-    }
-    for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
-    if (lane == 0) top_s[warp] = top;
-    bad = __syncthreads_or(bad);
-    for (int w = 0; w < kWarps; ++w) top = fmaxf(top, top_s[w]);
-    bad |= top == -INFINITY;
-    const bool wrong = !(temp >= 0.f && temp < INFINITY) || isnan(top_p) || isnan(min_p) || top_k < 0 || !(u >= 0.f && u < 1.f);
-    if (bad || wrong) {
-        if (tid == 0) flag(a.status, (bad ? TS_STATUS_NONFINITE : 0u) | (wrong ? TS_STATUS_INDEX : 0u));
-        if (tid == 0 && a.token) a.token[r] = -1;
-        for (int i = tid; i < V; i += kThreads) {
-            if (a.probs) a.probs[(size_t)r * V + i] = NAN;
-            if (a.kept) a.kept[(size_t)r * V + i] = NAN;
+    {
+        const int nv = SL / VE;
+        for (int v0 = tid; v0 < nv; v0 += 4 * kThreads) {
+            uint4 x[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int v = v0 + k * kThreads, p = base + v * VE - lead;   // p: id of the first of VE
+                T *e = reinterpret_cast<T *>(&x[k]);
+                if (v < nv && p >= 0 && p + VE <= V) x[k] = __ldcs(reinterpret_cast<const uint4 *>(row + p));
+                else
+#pragma unroll
+                    for (int i = 0; i < VE; ++i) e[i] = v < nv && p + i >= 0 && p + i < V ? row[p + i] : (T)(-INFINITY);
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int v = v0 + k * kThreads;
+                if (v < nv) *reinterpret_cast<uint4 *>(seg + v * VE) = x[k];
+#pragma unroll
+                for (int i = 0; i < VE; i += 4) {
+                    float f[4];
+                    load4(reinterpret_cast<const T *>(&x[k]) + i, f);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        bad |= !(f[e] < INFINITY);
+                        top = fmaxf(top, f[e]);
+                    }
+                }
+            }
         }
+    }
+    for (int b = tid; b < kBins; b += kThreads) sm.lo[b] = 0, sm.hi[b] = 0;
+    if (tid == 0) sm.n_list = 0;
+#pragma unroll
+    for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
+    if (lane == 0) sm.top[warp] = top;
+    bad = __syncthreads_or(bad);
+    top = sm.top[lane % kWarps];
+#pragma unroll
+    for (int o = kWarps / 2; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
+    // one word to every CTA of the cluster, and all of theirs
+    auto tell = [&](int turn, u64 word) {
+        if (tid < C) *cluster.map_shared_rank(&sm.from[turn][rank], tid) = word;
+        sync();
+    };
+    if (C > 1) asm volatile("barrier.cluster.wait.aligned;" ::: "memory");             // before anything is written to them
+    tell(0, (u64)__float_as_uint(top) | (u64)bad << 32);
+    bad = false;
+    for (int c = 0; c < C; ++c) {
+        top = fmaxf(top, __uint_as_float((uint32_t)sm.from[0][c]));
+        bad |= sm.from[0][c] >> 32 != 0;
+    }
+    bad |= top == -INFINITY;
+    const bool wrong =
+        !(temp >= 0.f && temp < INFINITY) || isnan(top_p) || isnan(min_p) || top_k < 0 || !(u >= 0.f && u < 1.f);
+    auto out_rows = [&](auto prob, auto kept) {   // the segment's part of the output rows
+        if (!a.probs && !a.kept) return;
+        float *const rows[2] = {a.probs ? a.probs + (size_t)r * V : nullptr, a.kept ? a.kept + (size_t)r * V : nullptr};
+        for (int k = 0; k < 2; ++k) {
+            float *const to = rows[k];
+            if (!to) continue;
+            const bool vec = (((uintptr_t)to - (uintptr_t)lead * 4) & 15) == 0;
+            for (int v = tid; v < SL / 4; v += kThreads) {
+                float x[4], y[4];
+                load4(seg + 4 * v, x);
+                const int p = base + 4 * v - lead;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) y[e] = k ? kept(x[e], p + e) : prob(x[e], p + e);
+                if (vec && p >= 0 && p + 4 <= V) __stcs(reinterpret_cast<float4 *>(to + p), make_float4(y[0], y[1], y[2], y[3]));
+                else
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (p + e >= 0 && p + e < V) to[p + e] = y[e];
+            }
+        }
+    };
+    if (bad || wrong) {
+        if (rank == 0 && tid == 0) {
+            flag(a.status, (bad ? TS_STATUS_NONFINITE : 0u) | (wrong ? TS_STATUS_INDEX : 0u));
+            if (a.token) a.token[r] = -1;
+        }
+        out_rows([](float, int) { return NAN; }, [](float, int) { return NAN; });
+        sync();
         return;
     }
     const bool greedy = temp < 7.888609052210118e-31f;   // 2^-100
     const double c = 1.4426950408889634 / (greedy ? 1.0 : (double)temp);
     const Weights weight{top, (float)c, (float)(c - (double)(float)c)};
-
-    // mass and count of the tokens of key lo or more
-    auto from = [&](uint32_t lo, bool masses) {
-        Pair v{0, 0};
-        for (int i = tid; i < V; i += kThreads) {
-            const float x = load<T>(row, i);
-            if (key_of(x) >= lo) {
-                ++v.count;
-                if (masses) v.mass += weight(x);
-            }
-        }
-        return block_sum(v, part);
-    };
     const uint32_t key_top = key_of(top);
-    uint32_t cut = kKeyLowest;   // key of the last token kept
-    u64 ties = ~0ull;            // tokens kept of that key
+    // tokens of a lower key are not kept: min-p, and -inf
+    uint32_t floor_key = kKeyLowest;
     if (min_p > 0.f && !greedy)
-        cut = max(cut, key_of(__double2float_ru((double)top + (double)temp * log((double)fminf(min_p, 1.f)))));
-    if (greedy) cut = key_top, ties = 1;
-    else if (top_k > 0 && from(cut, false).count > (u64)top_k) {
-        uint32_t lo = cut, hi = key_top + 1;   // count(lo) >= k > count(hi)
-        while (hi - lo > 1) {
-            const uint32_t m = lo + (hi - lo) / 2;
-            if (from(m, false).count >= (u64)top_k) lo = m;
-            else hi = m;
+        floor_key = max(floor_key, key_of(__double2float_ru((double)top + (double)temp * log((double)fminf(min_p, 1.f)))));
+    u64 cut = order_of(floor_key, (1 << kIdBits) - 1);   // kept: order_of(key, id) <= cut
+
+    // every element of the segment, by groups: f(group, x[4], id of x[0])
+    auto groups = [&](auto f) {
+        for (int g = warp; g < SL / kGroup; g += kWarps) {
+            float x[4];
+            load4(seg + g * kGroup + lane * 4, x);
+            f(g, x, base + g * kGroup + lane * 4 - lead);
         }
-        cut = lo, ties = top_k - from(lo + 1, false).count;
-    }
-    Pair above = from(cut + 1, true), all = from(cut, false);
-    u64 wt = cut <= key_top ? weight(value_of(cut)) : 0;
-    ties = min(ties, all.count - above.count);
-    if (top_p < 1.f && !greedy) {
-        const u64 S = above.mass + ties * wt;
-        // a token is kept where the mass before it is below this
-        const u64 P = max(1ull, (u64)ceil((double)fmaxf(top_p, 0.f) * (double)S));
-        if (above.mass >= P) {   // the cut is higher up
-            uint32_t lo = cut, hi = key_top + 1;   // mass(lo) >= P > mass(hi), of whole values
-            ++lo;
-            while (hi - lo > 1) {
-                const uint32_t m = lo + (hi - lo) / 2;
-                if (from(m, true).mass >= P) lo = m;
-                else hi = m;
-            }
-            cut = lo;
-            above = from(cut + 1, true), all = from(cut, false);
-            wt = weight(value_of(cut));
-            ties = all.count - above.count;
-        }
-        ties = min(ties, wt ? (P - above.mass + wt - 1) / wt : ties);
-    }
-    // the id up to which tokens of the cut's key are kept: warps own ranges of ids
-    const int per = (V + kWarps - 1) / kWarps, v0 = min(V, warp * per), v1 = min(V, v0 + per);
-    auto before_warp = [&](u64 mine) {   // what the warps before this one hold
+    };
+    // the CTA's sum, for every thread
+    auto block_sum = [&](u64 v) {
+#pragma unroll
+        for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(~0u, v, o);
         __syncthreads();
-        if (lane == 0) part[warp].mass = mine;
+        if (lane == 0) sm.part[warp] = v;
         __syncthreads();
+        v = sm.part[lane % kWarps];
+#pragma unroll
+        for (int o = kWarps / 2; o; o >>= 1) v += __shfl_xor_sync(~0u, v, o);
+        return v;
+    };
+    // inclusive running sum over the CTA's threads
+    auto block_scan = [&](u64 v) {
+        v = warp_scan(v);
+        __syncthreads();
+        if (lane == 31) sm.part[warp] = v;
+        __syncthreads();
+        u64 before = lane < warp ? sm.part[lane] : 0;
+#pragma unroll
+        for (int o = 16; o; o >>= 1) before += __shfl_xor_sync(~0u, before, o);
+        return v + before;
+    };
+    int turn = 1;
+    auto cluster_sum = [&](u64 v) {   // of a number every thread of a CTA has
+        tell(turn, v);
         u64 s = 0;
-        for (int w = 0; w < warp; ++w) s += part[w].mass;
+        for (int c = 0; c < C; ++c) s += sm.from[turn][c];
+        turn = 3 - turn;
         return s;
     };
-    int id_cut = V;
-    if (ties < all.count - above.count) {
-        u64 n = 0;
-        for (int i = v0 + lane; i < v1; i += 32) n += key_of(load<T>(row, i)) == cut;
-        n = warp_sum(n);
-        u64 at = before_warp(n);
-        if (at < ties && ties <= at + n)
-            for (int i0 = v0; i0 < v1; i0 += 32) {
-                const unsigned is = __ballot_sync(~0u, i0 + lane < v1 && key_of(load<T>(row, min(i0 + lane, V - 1))) == cut);
-                if (at < ties && at + __popc(is) >= ties) {
-                    unsigned k = is;
-                    for (u64 j = at + 1; j < ties; ++j) k &= k - 1;
-                    if (lane == 0) found_s = i0 + __ffs(k) - 1;
-                }
-                at += __popc(is);
-            }
+    // mass or number of the tokens up to `last` in the order
+    auto upto = [&](u64 last, bool masses) {
+        u64 s = 0;
+        groups([&](int, const float (&x)[4], int id) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (order_of(key_of(x[e]), id + e) <= last && x[e] > -INFINITY) s += masses ? weight(x[e]) : 1;
+        });
+        return cluster_sum(block_sum(s));
+    };
+    // The last token of the shortest start that reaches `want` (mass or number), within the tokens up to cut, by bisection:
+    // for rows with thousands of equal or nearly equal values at the cut.
+    auto bisect = [&](u64 want, bool masses) {
+        u64 lo = order_of(key_top, 0), hi = cut;   // sum(lo - 1) < want <= sum(hi)
+        while (lo < hi) {
+            const u64 m = lo + (hi - lo) / 2;
+            if (upto(m, masses) >= want) hi = m;
+            else lo = m + 1;
+        }
+        return lo;
+    };
+    // The histogram's bin, by bins from 0 down in value, that the sum of `want` falls into: before (the sum ahead of it)
+    // and its own sum, for every thread. Bins are a thread's; what every CTA of the cluster counted is added.
+    auto find_bin = [&](u64 want, u64 &before, u64 &own) {
+        sync();
+        u64 v = 0;
+        for (int c = 0; c < C; ++c) {
+            const Shared &o = *cluster.map_shared_rank(&sm, c);
+            v += ((u64)o.hi[tid] << 32) + o.lo[tid];
+        }
+        const u64 run = block_scan(v);
+        if (tid == 0) sm.at = -1;
         __syncthreads();
-        id_cut = found_s;
-    }
-    auto kept = [&](float x, int i) { const uint32_t k = key_of(x); return k > cut || (k == cut && i <= id_cut); };
-    const u64 S = above.mass + ties * wt;
-    if (a.token) {
-        // the first id at which the running sum is above u S; with none, the last of any mass
-        const u64 want = min((u64)floor((double)u * (double)S), S - 1);
-        u64 m = 0;
-        for (int i = v0 + lane; i < v1; i += 32) {
-            const float x = load<T>(row, i);
-            if (kept(x, i)) m += weight(x);
+        if (run - v < want && want <= run) sm.at = tid, sm.above = run - v, sm.part[0] = v;
+        __syncthreads();
+        before = sm.above, own = sm.part[0];
+        return sm.at;
+    };
+    auto push = [&](uint32_t key, int id) {
+        Shared &o = *cluster.map_shared_rank(&sm, 0);
+        const int i = atomicAdd(&o.n_list, 1);
+        if (i < kList) o.list[i] = order_of(key, id);
+    };
+    // The first CTA sorts the list; f(its n entries) says which is the last kept; everyone gets it.
+    auto decide = [&](auto f) {
+        sync();
+        if (rank == 0) {
+            const int n = sm.n_list;
+            int n2 = 32;
+            while (n2 < n) n2 *= 2;
+            for (int i = tid + n; i < n2; i += kThreads) sm.list[i] = ~0ull;
+            __syncthreads();
+            for (int size = 2; size <= n2; size *= 2)
+                for (int half = size / 2; half; half /= 2) {
+                    if (tid < n2 / 2) {
+                        const int i = 2 * tid - (tid & (half - 1)), j = i + half;
+                        const u64 x = sm.list[i], y = sm.list[j];
+                        if ((x > y) == ((i & size) == 0)) sm.list[i] = y, sm.list[j] = x;
+                    }
+                    __syncthreads();
+                }
+            const u64 last = f(n);
+            if (tid < C) *cluster.map_shared_rank(&sm.cut, tid) = last;
         }
-        m = warp_sum(m);
-        u64 at = before_warp(m);
-        if (at <= want && want < at + m)
-            for (int i0 = v0; i0 < v1; i0 += 32) {
-                const int i = i0 + lane;
-                const float x = load<T>(row, min(i, V - 1));
-                u64 w = i < v1 && kept(x, i) ? weight(x) : 0;
-                for (int o = 1; o < 32; o <<= 1) {
-                    const u64 y = __shfl_up_sync(~0u, w, o);
-                    if (lane >= o) w += y;
-                }
-                const unsigned over = __ballot_sync(~0u, at + w > want);
-                if (over) {
-                    if (lane == 0) a.token[r] = i0 + __ffs(over) - 1;
-                    break;
-                }
-                at += __shfl_sync(~0u, w, 31);
+        sync();
+        return sm.cut;
+    };
+    // how many of the list's first n entries, whose sum of weights is cut at P, are kept: by the thread of each entry
+    auto list_cut = [&](int n, u64 ahead, auto threshold) {
+        const u64 w = tid < n ? weight(value_of(~(uint32_t)(sm.list[tid] >> kIdBits))) : 0;
+        const u64 run = block_scan(w);
+        if (tid == n - 1) sm.above = run;
+        __syncthreads();
+        const u64 P = threshold(sm.above);
+        const int kept = __syncthreads_count(tid < n && ahead + run - w < P);
+        return max(kept, 1);
+    };
+
+    // a token is kept by top-p where the mass before it is below this
+    auto threshold = [&](u64 S) { return max(1ull, (u64)ceil((double)fmaxf(top_p, 0.f) * (double)S)); };
+    bool p_left = top_p < 1.f && !greedy;
+    if (greedy) {
+        u64 first = ~0ull;
+        groups([&](int, const float (&x)[4], int id) {
+#pragma unroll
+            for (int e = 3; e >= 0; --e)
+                if (x[e] == top) first = min(first, order_of(key_top, id + e));
+        });
+#pragma unroll
+        for (int o = 16; o; o >>= 1) first = min(first, __shfl_xor_sync(~0u, first, o));
+        if (lane == 0) sm.part[warp] = first;
+        __syncthreads();
+        for (int w = 0; w < kWarps; ++w) first = min(first, sm.part[w]);
+        tell(turn, first);
+        for (int c = 0; c < C; ++c) first = min(first, sm.from[turn][c]);
+        turn = 3 - turn;
+        cut = first;
+    } else if (top_k > 0 && top_k < V) {
+        // ---- top-k: values from the top down to the lowest that may be needed in equal bins; the k-th value's bin, and
+        // all above it where they fit, go into the list
+        const float low = value_of(floor_key), span = top - fmaxf(low, top - 64.f * fmaxf(temp, 0.25f));
+        const float scale = span > 0.f ? (kBins - 1) / span : 0.f;
+        auto bin = [&](float x) { return (int)fminf((top - x) * scale, (float)(kBins - 1)); };
+        auto eligible = [&](float x) { return key_of(x) >= floor_key; };
+        groups([&](int, const float (&x)[4], int) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (eligible(x[e])) atomicAdd(&sm.lo[bin(x[e])], 1u);
+        });
+        u64 before, own;
+        const int b = find_bin(top_k, before, own);
+        if (b >= 0) {   // (fewer than k tokens: all are kept)
+            if (own > kList) cut = bisect(top_k, false);
+            else {
+                const bool all = before + own <= kList;
+                groups([&](int, const float (&x)[4], int id) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (eligible(x[e]) && (all ? bin(x[e]) <= b : bin(x[e]) == b)) push(key_of(x[e]), id + e);
+                });
+                cut = decide([&](int) {
+                    int n = top_k - (all ? 0 : (int)before);
+                    if (all && p_left) n = list_cut(n, 0, threshold);
+                    return sm.list[n - 1];
+                });
+                if (all) p_left = false;
             }
-    }
-    if (a.probs || a.kept) {
-        const float inv = (float)(1099511627776.0 / (double)S);
-        __syncthreads();   // kept may be the logits
-        for (int i = tid; i < V; i += kThreads) {
-            const float x = load<T>(row, i);
-            const bool k = kept(x, i);
-            if (a.probs) a.probs[(size_t)r * V + i] = k ? weight.real(x) * inv : 0.f;
-            if (a.kept) a.kept[(size_t)r * V + i] = k ? x : TS_DROPPED_LOGIT;
+        }
+        if (p_left) {   // the histogram again
+            sync();
+            sm.lo[tid] = 0;
+            if (tid == 0) sm.n_list = 0;
+            __syncthreads();
         }
     }
+    if (p_left) {
+        // ---- top-p: exact sums of weights in equal bins of the exponent; tokens so light that all of them together make
+        // less than 1 - top_p of the largest alone are only added up
+        const float least = fmaxf(-41.f, log2f(fmaxf(1.f - top_p, 1e-9f)) - log2f((float)V) - 0.01f), scale = (kBins - 1) / -least;
+        auto bin = [&](float x) { return (int)fminf((x - top) * weight.ch * -scale, (float)(kBins - 1)); };
+        auto kept = [&](float x, int id) { return order_of(key_of(x), id) <= cut; };
+        u64 rest = 0;
+        groups([&](int, const float (&x)[4], int id) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (kept(x[e], id + e)) {
+                    const u64 w = weight(x[e]);
+                    const int b = bin(x[e]);
+                    if (b == kBins - 1) rest += w;
+                    else {
+                        const uint32_t lo = (uint32_t)w, old = atomicAdd(&sm.lo[b], lo), hi = (uint32_t)(w >> 32) + (old + lo < old);
+                        if (hi) atomicAdd(&sm.hi[b], hi);
+                    }
+                }
+        });
+        rest = block_sum(rest);
+        if (tid == 0) {
+            sm.lo[kBins - 1] = (uint32_t)rest;
+            sm.hi[kBins - 1] = (uint32_t)(rest >> 32);
+        }
+        // the whole mass, then the bin
+        sync();
+        u64 all = 0;
+        for (int c = 0; c < C; ++c) {
+            const Shared &o = *cluster.map_shared_rank(&sm, c);
+            all += ((u64)o.hi[tid] << 32) + o.lo[tid];
+        }
+        all = block_sum(all);
+        const u64 P = threshold(all);
+        u64 before, own;
+        const int b = find_bin(P, before, own);
+        groups([&](int, const float (&x)[4], int id) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (kept(x[e], id + e) && bin(x[e]) == b) push(key_of(x[e]), id + e);
+        });
+        sync();
+        if (cluster.map_shared_rank(&sm, 0)->n_list > kList) cut = bisect(P, true);
+        else
+            cut = decide([&](int n) {
+                n = list_cut(n, before, [&](u64) { return P; });
+                return sm.list[n - 1];
+            });
+    }
+
+    // ---- kept weights, group by group; the group and the token that u falls on
+    auto kept = [&](float x, int id) { return order_of(key_of(x), id) <= cut && x > -INFINITY; };
+    groups([&](int g, const float (&x)[4], int id) {
+        u64 w = 0;
+        bool any = false;
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if (kept(x[e], id + e)) w += weight(x[e]), any = true;
+        if (__any_sync(~0u, any)) w = warp_sum(w);
+        if (lane == 0) sm.sums[g] = w;
+    });
+    __syncthreads();
+    const int G = SL / kGroup;
+    const u64 mine = tid < G ? sm.sums[tid] : 0, run = block_scan(mine);
+    __syncthreads();
+    if (tid == kThreads - 1) sm.above = run;
+    __syncthreads();
+    tell(turn, sm.above);
+    u64 S = 0, first = 0;
+    for (int c = 0; c < C; ++c) {
+        if (c < rank) first += sm.from[turn][c];
+        S += sm.from[turn][c];
+    }
+    if (a.token) {
+        // the first id at which the running sum is above u S
+        const u64 want = min((u64)floor((double)u * (double)S), S - 1);
+        if (first + run - mine <= want && want < first + run) {   // this thread's group
+            sm.at = tid;
+            sm.above = first + run - mine;
+        }
+        const bool here = first <= want && want < first + sm.from[turn][rank];
+        __syncthreads();
+        if (here && warp == 0) {
+            const int g = sm.at, id = base + g * kGroup + lane * 4 - lead;
+            float x[4];
+            u64 w[4], sum = 0;
+            load4(seg + g * kGroup + lane * 4, x);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                w[e] = kept(x[e], id + e) ? weight(x[e]) : 0;
+                sum += w[e];
+            }
+            u64 at = sm.above + warp_scan(sum) - sum;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                if (at <= want && want < at + w[e]) a.token[r] = id + e;
+                at += w[e];
+            }
+        }
+    }
+    const float inv = (float)(1099511627776.0 / (double)S);
+    out_rows([&](float x, int id) { return kept(x, id) ? weight.real(x) * inv : 0.f; },
+             [&](float x, int id) { return kept(x, id) ? x : TS_DROPPED_LOGIT; });
+    if (C > 1) cluster.sync();   // shared memory that others may still read
 }
 
 }  // namespace
 
 cudaError_t launch_sample(const SampleArgs &a, ts_dtype dt, cudaStream_t s) {
-    return dt == TS_BF16 ? launch(k_sample<__nv_bfloat16>, dim3(a.R), dim3(kThreads), 0, s, a)
-                         : launch(k_sample<float>, dim3(a.R), dim3(kThreads), 0, s, a);
+    const int es = dt == TS_BF16 ? 2 : 4;
+    auto seg = [&](int C) { return ((a.V + 16 / es - 1 + C - 1) / C + kGroup - 1) / kGroup * kGroup; };
+    // The fewest CTAs a row whose segments let two of them share an SM; more where there are few rows.
+    int C = 1;
+    while (C < 8 && seg(C) * es > 101000) C *= 2;
+    while (C < 8 && (long long)a.R * C <= num_sms() && seg(2 * C) >= 2048) C *= 2;
+    const int SL = seg(C);
+    const size_t smem = (sizeof(Shared) + 15) / 16 * 16 + (size_t)SL * es;
+    auto go = [&](auto kern) {
+        cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        if (e != cudaSuccess) return e;
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3((unsigned)a.R * C);
+        cfg.blockDim = dim3(kThreads);
+        cfg.dynamicSmemBytes = smem;
+        cfg.stream = s;
+        cudaLaunchAttribute attr[2];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = C;
+        attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+        attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[1].val.programmaticStreamSerializationAllowed = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = pdl_enabled() ? 2 : 1;
+        return cudaLaunchKernelEx(&cfg, kern, a, SL);
+    };
+    return dt == TS_BF16 ? go(k_sample<__nv_bfloat16>) : go(k_sample<float>);
 }
 
 }  // namespace ts
