@@ -33,7 +33,6 @@ constexpr int kThreads = 512, kWarps = kThreads / 32;
 constexpr int kGroup = 128;                    // elements of a warp's turn: a sum of weights is kept for each
 constexpr int kMaxSeg = 32896;                 // elements of a segment: 2^18 + 7 over 8 CTAs, in whole groups
 constexpr int kBins = kThreads, kList = 512;   // a thread a bin, a thread a candidate
-constexpr uint32_t kKeyLowest = 0x00800000u;   // key of the lowest finite number
 typedef unsigned long long u64;
 
 // Whole numbers in the order of the floats (-0 counts as 0).
@@ -44,6 +43,9 @@ __device__ __forceinline__ uint32_t key_of(float x) {
 __device__ __forceinline__ float value_of(uint32_t k) {
     return __uint_as_float(k & 0x80000000u ? k & 0x7fffffffu : ~k);
 }
+
+// A number from [0, 1) in units of 2^-64.
+__device__ __forceinline__ u64 part64(float x) { return __float2ull_rz(x * 18446744073709551616.f); }
 
 // A token's place in the order as one rising number.
 constexpr int kIdBits = 18;
@@ -132,7 +134,8 @@ struct Shared {
     float top[kWarps];
     u64 cut;                         // the last token kept, as in list
     int n_list, at;
-    u64 above;
+    u64 above, total;
+    float ch, cl, mh, ml;            // log2(e) / T and T ln(min_p), as sums of two floats
 };
 
 // A cluster a row, segment SL elements. Positions count from the 16-byte boundary at or before the row's first element
@@ -157,41 +160,56 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(SampleArgs a, int SL) {
     const float temp = a.temperature ? a.temperature[r] : 1.f, top_p = a.top_p ? a.top_p[r] : 1.f,
                 min_p = a.min_p ? a.min_p[r] : 0.f, u = a.u ? a.u[r] : 0.f;
     const int top_k = a.top_k ? a.top_k[r] : 0;
+    const bool greedy = temp < 7.888609052210118e-31f;   // 2^-100
+    if (tid == kThreads - 1) {   // (64-bit arithmetic is slow enough here that one thread does it for all)
+        const double c = 1.4426950408889634 / (greedy ? 1.0 : (double)temp);
+        sm.ch = (float)c, sm.cl = (float)(c - (double)sm.ch);
+        if (min_p > 0.f) {
+            const double m = (double)temp * log((double)fminf(min_p, 1.f));
+            sm.mh = (float)m, sm.ml = (float)(m - (double)sm.mh);
+        }
+    }
 
     // ---- the segment into shared memory; its maximum
     constexpr int VE = 16 / sizeof(T);
     float top = -INFINITY;
     bool bad = false;
+    auto look = [&](const T *p) {
+        float f[4];
+        load4(p, f);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            bad |= !(f[e] < INFINITY);
+            top = fmaxf(top, f[e]);
+        }
+    };
     {
-        const int nv = SL / VE;
-        for (int v0 = tid; v0 < nv; v0 += 4 * kThreads) {
+        // 16-byte pieces that lie within the row; what is left at the segment's ends, one by one
+        const int v_lo = min(SL, max(0, lead - base + VE - 1)) / VE, v_hi = max(v_lo, min(SL, max(0, V + lead - base)) / VE);
+        const uint4 *const from = reinterpret_cast<const uint4 *>(row - lead) + base / VE;
+        for (int v0 = v_lo + tid; v0 < v_hi; v0 += 4 * kThreads) {
             uint4 x[4];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const int v = v0 + k * kThreads, p = base + v * VE - lead;   // p: id of the first of VE
-                T *e = reinterpret_cast<T *>(&x[k]);
-                if (v < nv && p >= 0 && p + VE <= V) x[k] = __ldcs(reinterpret_cast<const uint4 *>(row + p));
-                else
+            for (int k = 0; k < 4; ++k)
+                if (v0 + k * kThreads < v_hi) x[k] = __ldcs(from + v0 + k * kThreads);
 #pragma unroll
-                    for (int i = 0; i < VE; ++i) e[i] = v < nv && p + i >= 0 && p + i < V ? row[p + i] : (T)(-INFINITY);
-            }
+            for (int k = 0; k < 4; ++k)
+                if (v0 + k * kThreads < v_hi) {
+                    reinterpret_cast<uint4 *>(seg)[v0 + k * kThreads] = x[k];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const int v = v0 + k * kThreads;
-                if (v < nv) *reinterpret_cast<uint4 *>(seg + v * VE) = x[k];
-#pragma unroll
-                for (int i = 0; i < VE; i += 4) {
-                    float f[4];
-                    load4(reinterpret_cast<const T *>(&x[k]) + i, f);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        bad |= !(f[e] < INFINITY);
-                        top = fmaxf(top, f[e]);
-                    }
+                    for (int i = 0; i < VE; i += 4) look(reinterpret_cast<const T *>(&x[k]) + i);
                 }
-            }
+        }
+        for (int i = tid; i < SL - (v_hi - v_lo) * VE; i += kThreads) {
+            const int pos = i < v_lo * VE ? i : i + (v_hi - v_lo) * VE, p = base + pos - lead;
+            const T x = p >= 0 && p < V ? row[p] : (T)(-INFINITY);
+            seg[pos] = x;
+            const float f = (float)x;
+            bad |= !(f < INFINITY);
+            top = fmaxf(top, f);
         }
     }
+    const float own_top = top;   // of the thread's elements
     for (int b = tid; b < kBins; b += kThreads) sm.lo[b] = 0, sm.hi[b] = 0;
     if (tid == 0) sm.n_list = 0;
 #pragma unroll
@@ -246,15 +264,21 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(SampleArgs a, int SL) {
         sync();
         return;
     }
-    const bool greedy = temp < 7.888609052210118e-31f;   // 2^-100
-    const double c = 1.4426950408889634 / (greedy ? 1.0 : (double)temp);
-    const Weights weight{top, (float)c, (float)(c - (double)(float)c)};
+    const Weights weight{top, sm.ch, sm.cl};
     const uint32_t key_top = key_of(top);
-    // tokens of a lower key are not kept: min-p, and -inf
-    uint32_t floor_key = kKeyLowest;
-    if (min_p > 0.f && !greedy)
-        floor_key = max(floor_key, key_of(__double2float_ru((double)top + (double)temp * log((double)fminf(min_p, 1.f)))));
-    u64 cut = order_of(floor_key, (1 << kIdBits) - 1);   // kept: order_of(key, id) <= cut
+    // tokens below this are not kept: min-p (the sum rounded up), and -inf
+    float low = -3.402823466e38f;
+    if (min_p > 0.f && !greedy) {
+        const float s = top + sm.mh, bb = s - top, e = (top - (s - bb)) + (sm.mh - bb);
+        low = fmaxf(low, __fadd_ru(s, e + sm.ml));
+    }
+    float cut = low;               // kept: above this value, or this value and an id up to cut_id
+    int cut_id = 1 << kIdBits;
+    auto kept = [&](float x, int id) { return x > cut || (x == cut && id <= cut_id); };
+    auto cut_at = [&](u64 last) {
+        cut = value_of(~(uint32_t)(last >> kIdBits));
+        cut_id = (int)(last & ((1 << kIdBits) - 1));
+    };
 
     // every element of the segment, by groups: f(group, x[4], id of x[0])
     auto groups = [&](auto f) {
@@ -301,14 +325,14 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(SampleArgs a, int SL) {
         groups([&](int, const float (&x)[4], int id) {
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-                if (order_of(key_of(x[e]), id + e) <= last && x[e] > -INFINITY) s += masses ? weight(x[e]) : 1;
+                if (kept(x[e], id + e) && order_of(key_of(x[e]), id + e) <= last) s += masses ? weight(x[e]) : 1;
         });
         return cluster_sum(block_sum(s));
     };
     // The last token of the shortest start that reaches `want` (mass or number), within the tokens up to cut, by bisection:
     // for rows with thousands of equal or nearly equal values at the cut.
     auto bisect = [&](u64 want, bool masses) {
-        u64 lo = order_of(key_top, 0), hi = cut;   // sum(lo - 1) < want <= sum(hi)
+        u64 lo = order_of(key_top, 0), hi = order_of(key_of(cut), min(cut_id, (1 << kIdBits) - 1));   // sum(lo - 1) < want <= sum(hi)
         while (lo < hi) {
             const u64 m = lo + (hi - lo) / 2;
             if (upto(m, masses) >= want) hi = m;
@@ -316,9 +340,9 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(SampleArgs a, int SL) {
         }
         return lo;
     };
-    // The histogram's bin, by bins from 0 down in value, that the sum of `want` falls into: before (the sum ahead of it)
-    // and its own sum, for every thread. Bins are a thread's; what every CTA of the cluster counted is added.
-    auto find_bin = [&](u64 want, u64 &before, u64 &own) {
+    // The histogram's bin, by bins from 0 down in value, that a sum of want(total) falls into: before (the sum ahead of
+    // it) and its own sum, for every thread. Bins are a thread's; what every CTA of the cluster counted is added.
+    auto find_bin = [&](auto want_of, u64 &want, u64 &before, u64 &own) {
         sync();
         u64 v = 0;
         for (int c = 0; c < C; ++c) {
@@ -327,7 +351,9 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(SampleArgs a, int SL) {
         }
         const u64 run = block_scan(v);
         if (tid == 0) sm.at = -1;
+        if (tid == kThreads - 1) sm.total = run;
         __syncthreads();
+        want = want_of(sm.total);
         if (run - v < want && want <= run) sm.at = tid, sm.above = run - v, sm.part[0] = v;
         __syncthreads();
         before = sm.above, own = sm.part[0];
@@ -366,15 +392,18 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(SampleArgs a, int SL) {
     auto list_cut = [&](int n, u64 ahead, auto threshold) {
         const u64 w = tid < n ? weight(value_of(~(uint32_t)(sm.list[tid] >> kIdBits))) : 0;
         const u64 run = block_scan(w);
-        if (tid == n - 1) sm.above = run;
+        if (tid == n - 1) sm.total = run;
         __syncthreads();
-        const u64 P = threshold(sm.above);
+        const u64 P = threshold(sm.total);
         const int kept = __syncthreads_count(tid < n && ahead + run - w < P);
         return max(kept, 1);
     };
 
     // a token is kept by top-p where the mass before it is below this
-    auto threshold = [&](u64 S) { return max(1ull, (u64)ceil((double)fmaxf(top_p, 0.f) * (double)S)); };
+    auto threshold = [&](u64 S) {   // ceil(top_p S)
+        const u64 p = part64(fminf(fmaxf(top_p, 0.f), 0.99999994f));
+        return max(1ull, __umul64hi(p, S) + (p * S != 0));
+    };
     bool p_left = top_p < 1.f && !greedy;
     if (greedy) {
         u64 first = ~0ull;
@@ -391,37 +420,61 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(SampleArgs a, int SL) {
         tell(turn, first);
         for (int c = 0; c < C; ++c) first = min(first, sm.from[turn][c]);
         turn = 3 - turn;
-        cut = first;
+        cut_at(first);
     } else if (top_k > 0 && top_k < V) {
-        // ---- top-k: values from the top down to the lowest that may be needed in equal bins; the k-th value's bin, and
-        // all above it where they fit, go into the list
-        const float low = value_of(floor_key), span = top - fmaxf(low, top - 64.f * fmaxf(temp, 0.25f));
-        const float scale = span > 0.f ? (kBins - 1) / span : 0.f;
+        // ---- top-k, by equal bins of value from the top down. First of each thread's largest only: where k of these are
+        // counted, at least k tokens are, and few more. If all of those are not candidates enough for the list, of every
+        // token, and of the k-th one's bin all are candidates, with the bins above it where they fit.
+        const float span = top - fmaxf(low, top - 64.f * fmaxf(temp, 0.25f)), scale = span > 0.f ? (kBins - 1) / span : 0.f;
         auto bin = [&](float x) { return (int)fminf((top - x) * scale, (float)(kBins - 1)); };
-        auto eligible = [&](float x) { return key_of(x) >= floor_key; };
-        groups([&](int, const float (&x)[4], int) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                if (eligible(x[e])) atomicAdd(&sm.lo[bin(x[e])], 1u);
-        });
-        u64 before, own;
-        const int b = find_bin(top_k, before, own);
-        if (b >= 0) {   // (fewer than k tokens: all are kept)
-            if (own > kList) cut = bisect(top_k, false);
-            else {
-                const bool all = before + own <= kList;
+        auto want_k = [&](u64) { return (u64)top_k; };
+        u64 want, before = 0, own = 0;
+        int b = -1;
+        bool all = false, listed = false;
+        if (top_k <= kThreads * C / 2 && top_k < kList) {
+            if (own_top >= low) atomicAdd(&sm.lo[bin(own_top)], 1u);
+            b = find_bin(want_k, want, before, own);
+            if (b >= 0 && b < kBins - 1) {
                 groups([&](int, const float (&x)[4], int id) {
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
-                        if (eligible(x[e]) && (all ? bin(x[e]) <= b : bin(x[e]) == b)) push(key_of(x[e]), id + e);
+                        if (x[e] >= low && bin(x[e]) <= b) push(key_of(x[e]), id + e);
                 });
-                cut = decide([&](int) {
-                    int n = top_k - (all ? 0 : (int)before);
-                    if (all && p_left) n = list_cut(n, 0, threshold);
-                    return sm.list[n - 1];
-                });
-                if (all) p_left = false;
+                sync();
+                listed = all = cluster.map_shared_rank(&sm, 0)->n_list <= kList;
             }
+            if (!listed) {
+                sync();
+                sm.lo[tid] = 0;
+                if (tid == 0) sm.n_list = 0;
+                __syncthreads();
+            }
+        }
+        if (!listed) {
+            groups([&](int, const float (&x)[4], int) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (x[e] >= low) atomicAdd(&sm.lo[bin(x[e])], 1u);
+            });
+            b = find_bin(want_k, want, before, own);
+            if (b >= 0 && own <= kList) {
+                listed = true, all = before + own <= kList;
+                groups([&](int, const float (&x)[4], int id) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (x[e] >= low && (all ? bin(x[e]) <= b : bin(x[e]) == b)) push(key_of(x[e]), id + e);
+                });
+            }
+        }
+        if (listed) {
+            cut_at(decide([&](int) {
+                int n = top_k - (all ? 0 : (int)before);
+                if (all && p_left) n = list_cut(n, 0, threshold);
+                return sm.list[n - 1];
+            }));
+            if (all) p_left = false;
+        } else if (b >= 0) {   // (fewer than k tokens: all are kept)
+            cut_at(bisect(top_k, false));
         }
         if (p_left) {   // the histogram again
             sync();
@@ -435,7 +488,6 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(SampleArgs a, int SL) {
         // less than 1 - top_p of the largest alone are only added up
         const float least = fmaxf(-41.f, log2f(fmaxf(1.f - top_p, 1e-9f)) - log2f((float)V) - 0.01f), scale = (kBins - 1) / -least;
         auto bin = [&](float x) { return (int)fminf((x - top) * weight.ch * -scale, (float)(kBins - 1)); };
-        auto kept = [&](float x, int id) { return order_of(key_of(x), id) <= cut; };
         u64 rest = 0;
         groups([&](int, const float (&x)[4], int id) {
 #pragma unroll
@@ -455,33 +507,23 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(SampleArgs a, int SL) {
             sm.lo[kBins - 1] = (uint32_t)rest;
             sm.hi[kBins - 1] = (uint32_t)(rest >> 32);
         }
-        // the whole mass, then the bin
-        sync();
-        u64 all = 0;
-        for (int c = 0; c < C; ++c) {
-            const Shared &o = *cluster.map_shared_rank(&sm, c);
-            all += ((u64)o.hi[tid] << 32) + o.lo[tid];
-        }
-        all = block_sum(all);
-        const u64 P = threshold(all);
-        u64 before, own;
-        const int b = find_bin(P, before, own);
+        u64 P, before, own;
+        const int b = find_bin(threshold, P, before, own);
         groups([&](int, const float (&x)[4], int id) {
 #pragma unroll
             for (int e = 0; e < 4; ++e)
                 if (kept(x[e], id + e) && bin(x[e]) == b) push(key_of(x[e]), id + e);
         });
         sync();
-        if (cluster.map_shared_rank(&sm, 0)->n_list > kList) cut = bisect(P, true);
+        if (cluster.map_shared_rank(&sm, 0)->n_list > kList) cut_at(bisect(P, true));
         else
-            cut = decide([&](int n) {
+            cut_at(decide([&](int n) {
                 n = list_cut(n, before, [&](u64) { return P; });
                 return sm.list[n - 1];
-            });
+            }));
     }
 
     // ---- kept weights, group by group; the group and the token that u falls on
-    auto kept = [&](float x, int id) { return order_of(key_of(x), id) <= cut && x > -INFINITY; };
     groups([&](int g, const float (&x)[4], int id) {
         u64 w = 0;
         bool any = false;
@@ -505,7 +547,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(SampleArgs a, int SL) {
     }
     if (a.token) {
         // the first id at which the running sum is above u S
-        const u64 want = min((u64)floor((double)u * (double)S), S - 1);
+        const u64 want = __umul64hi(part64(u), S);
         if (first + run - mine <= want && want < first + run) {   // this thread's group
             sm.at = tid;
             sm.above = first + run - mine;
@@ -530,7 +572,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(SampleArgs a, int SL) {
             }
         }
     }
-    const float inv = (float)(1099511627776.0 / (double)S);
+    const float inv = 1099511627776.f / __ull2float_rn(S);
     out_rows([&](float x, int id) { return kept(x, id) ? weight.real(x) * inv : 0.f; },
              [&](float x, int id) { return kept(x, id) ? x : TS_DROPPED_LOGIT; });
     if (C > 1) cluster.sync();   // shared memory that others may still read
