@@ -126,17 +126,21 @@ __device__ __forceinline__ u64 warp_scan(u64 v) {   // inclusive
 }
 
 struct Shared {
-    uint32_t lo[kBins], hi[kBins];   // the segment's histogram: 64-bit sums in two halves (lo alone: counts)
-    u64 list[kList];                 // the cluster's candidates, in its first CTA: ~key and id, so that order is rising
+    uint32_t h[3][kBins];            // the segment's histogram: counts in h[0], or sums by 16 bits each
+    u64 list[kList];                 // the cluster's candidates, in its first CTA, by their place in the order
     u64 sums[kMaxSeg / kGroup];      // kept weights of each group of the segment
     u64 part[kWarps];
     u64 from[3][8];                  // what the cluster's CTAs tell one another, in turn
-    float top[kWarps];
-    u64 cut;                         // the last token kept, as in list
-    int n_list, at;
+    u64 cut, kept;                   // the last token kept, the sum of all kept weights
     u64 above, total;
+    float top[kWarps];
     float ch, cl, mh, ml;            // log2(e) / T and T ln(min_p), as sums of two floats
+    int n_list, at;
 };
+
+__device__ __forceinline__ void copy16(void *to, const void *from) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(to)), "l"(from) : "memory");
+}
 
 // A cluster a row, segment SL elements. Positions count from the 16-byte boundary at or before the row's first element
 // (lead elements before it); those outside the row hold -inf.
@@ -155,63 +159,57 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(SampleArgs a, int SL) {
     if (C > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");   // the cluster's CTAs are there:
     pdl_wait();
     pdl_trigger();
+
+    // ---- the segment into shared memory
+    constexpr int VE = 16 / sizeof(T);
     const T *const row = reinterpret_cast<const T *>(a.logits) + (size_t)r * a.stride;
     const int lead = (int)(((uintptr_t)row & 15) / sizeof(T)), base = rank * SL;
+    // 16-byte pieces that lie within the row; what is left at the segment's ends, one by one
+    const int v_lo = min(SL, max(0, lead - base + VE - 1)) / VE, v_hi = max(v_lo, min(SL, max(0, V + lead - base)) / VE);
+    {
+        const uint4 *const from = reinterpret_cast<const uint4 *>(row - lead) + base / VE;
+        for (int v = v_lo + tid; v < v_hi; v += kThreads) copy16(seg + v * VE, from + v);
+    }
     const float temp = a.temperature ? a.temperature[r] : 1.f, top_p = a.top_p ? a.top_p[r] : 1.f,
                 min_p = a.min_p ? a.min_p[r] : 0.f, u = a.u ? a.u[r] : 0.f;
     const int top_k = a.top_k ? a.top_k[r] : 0;
     const bool greedy = temp < 7.888609052210118e-31f;   // 2^-100
-    if (tid == kThreads - 1) {   // (64-bit arithmetic is slow enough here that one thread does it for all)
+    if (tid == 0) {   // (64-bit arithmetic is slow enough here that one thread does it for all)
         const double c = 1.4426950408889634 / (greedy ? 1.0 : (double)temp);
         sm.ch = (float)c, sm.cl = (float)(c - (double)sm.ch);
         if (min_p > 0.f) {
             const double m = (double)temp * log((double)fminf(min_p, 1.f));
             sm.mh = (float)m, sm.ml = (float)(m - (double)sm.mh);
         }
+        sm.n_list = 0;
     }
-
-    // ---- the segment into shared memory; its maximum
-    constexpr int VE = 16 / sizeof(T);
+#pragma unroll
+    for (int k = 0; k < 3; ++k) sm.h[k][tid] = 0;
     float top = -INFINITY;
     bool bad = false;
-    auto look = [&](const T *p) {
-        float f[4];
-        load4(p, f);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            bad |= !(f[e] < INFINITY);
-            top = fmaxf(top, f[e]);
-        }
-    };
-    {
-        // 16-byte pieces that lie within the row; what is left at the segment's ends, one by one
-        const int v_lo = min(SL, max(0, lead - base + VE - 1)) / VE, v_hi = max(v_lo, min(SL, max(0, V + lead - base)) / VE);
-        const uint4 *const from = reinterpret_cast<const uint4 *>(row - lead) + base / VE;
-        for (int v0 = v_lo + tid; v0 < v_hi; v0 += 4 * kThreads) {
-            uint4 x[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-                if (v0 + k * kThreads < v_hi) x[k] = __ldcs(from + v0 + k * kThreads);
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-                if (v0 + k * kThreads < v_hi) {
-                    reinterpret_cast<uint4 *>(seg)[v0 + k * kThreads] = x[k];
-#pragma unroll
-                    for (int i = 0; i < VE; i += 4) look(reinterpret_cast<const T *>(&x[k]) + i);
-                }
-        }
-        for (int i = tid; i < SL - (v_hi - v_lo) * VE; i += kThreads) {
-            const int pos = i < v_lo * VE ? i : i + (v_hi - v_lo) * VE, p = base + pos - lead;
-            const T x = p >= 0 && p < V ? row[p] : (T)(-INFINITY);
-            seg[pos] = x;
-            const float f = (float)x;
-            bad |= !(f < INFINITY);
-            top = fmaxf(top, f);
-        }
+    for (int i = tid; i < SL - (v_hi - v_lo) * VE; i += kThreads) {
+        const int pos = i < v_lo * VE ? i : i + (v_hi - v_lo) * VE, p = base + pos - lead;
+        const T x = p >= 0 && p < V ? row[p] : (T)(-INFINITY);
+        seg[pos] = x;
+        bad |= !((float)x < INFINITY);
+        top = fmaxf(top, (float)x);
     }
-    const float own_top = top;   // of the thread's elements
-    for (int b = tid; b < kBins; b += kThreads) sm.lo[b] = 0, sm.hi[b] = 0;
-    if (tid == 0) sm.n_list = 0;
+    asm volatile("cp.async.wait_all;" ::: "memory");
+#pragma unroll 2
+    for (int v = v_lo + tid; v < v_hi; v += kThreads)   // the pieces that this thread has copied
+#pragma unroll
+        for (int i = 0; i < VE; i += 4) {
+            float f[4];
+            load4(seg + v * VE + i, f);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                bad |= !(f[e] < INFINITY);
+                top = fmaxf(top, f[e]);
+            }
+        }
+
+    // ---- the row's maximum, and a lower bound of its sum of weights (that of the threads' largest)
+    const float own_top = top;
 #pragma unroll
     for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
     if (lane == 0) sm.top[warp] = top;
@@ -219,24 +217,40 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(SampleArgs a, int SL) {
     top = sm.top[lane % kWarps];
 #pragma unroll
     for (int o = kWarps / 2; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
+    const float ch = sm.ch;
+    float some = 1.f;
+    const bool bound = top_p < 1.f && top_k == 0 && !(min_p > 0.f);
+    if (bound) {
+        some = own_top > -INFINITY ? ex2((own_top - top) * ch) : 0.f;
+#pragma unroll
+        for (int o = 16; o; o >>= 1) some += __shfl_xor_sync(~0u, some, o);
+        __syncthreads();
+        if (lane == 0) sm.top[warp] = some;
+        __syncthreads();
+        some = sm.top[lane % kWarps];
+#pragma unroll
+        for (int o = kWarps / 2; o; o >>= 1) some += __shfl_xor_sync(~0u, some, o);
+    }
     // one word to every CTA of the cluster, and all of theirs
     auto tell = [&](int turn, u64 word) {
         if (tid < C) *cluster.map_shared_rank(&sm.from[turn][rank], tid) = word;
         sync();
     };
     if (C > 1) asm volatile("barrier.cluster.wait.aligned;" ::: "memory");             // before anything is written to them
-    tell(0, (u64)__float_as_uint(top) | (u64)bad << 32);
-    bad = false;
+    tell(0, (u64)__float_as_uint(top) | (u64)__float_as_uint(bad ? NAN : some) << 32);
+    for (int c = 0; c < C; ++c) top = fmaxf(top, __uint_as_float((uint32_t)sm.from[0][c]));
+    some = 0.f;
     for (int c = 0; c < C; ++c) {
-        top = fmaxf(top, __uint_as_float((uint32_t)sm.from[0][c]));
-        bad |= sm.from[0][c] >> 32 != 0;
+        const float t = __uint_as_float((uint32_t)sm.from[0][c]), x = __uint_as_float((uint32_t)(sm.from[0][c] >> 32));
+        bad |= isnan(x);
+        if (t > -INFINITY) some += x * ex2((t - top) * ch);
     }
     bad |= top == -INFINITY;
     const bool wrong =
         !(temp >= 0.f && temp < INFINITY) || isnan(top_p) || isnan(min_p) || top_k < 0 || !(u >= 0.f && u < 1.f);
     auto out_rows = [&](auto prob, auto kept) {   // the segment's part of the output rows
-        if (!a.probs && !a.kept) return;
         float *const rows[2] = {a.probs ? a.probs + (size_t)r * V : nullptr, a.kept ? a.kept + (size_t)r * V : nullptr};
+#pragma unroll
         for (int k = 0; k < 2; ++k) {
             float *const to = rows[k];
             if (!to) continue;
@@ -264,8 +278,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(SampleArgs a, int SL) {
         sync();
         return;
     }
-    const Weights weight{top, sm.ch, sm.cl};
-    const uint32_t key_top = key_of(top);
+    const Weights weight{top, ch, sm.cl};
     // tokens below this are not kept: min-p (the sum rounded up), and -inf
     float low = -3.402823466e38f;
     if (min_p > 0.f && !greedy) {
@@ -312,14 +325,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(SampleArgs a, int SL) {
         return v + before;
     };
     int turn = 1;
-    auto cluster_sum = [&](u64 v) {   // of a number every thread of a CTA has
-        tell(turn, v);
-        u64 s = 0;
-        for (int c = 0; c < C; ++c) s += sm.from[turn][c];
-        turn = 3 - turn;
-        return s;
-    };
-    // mass or number of the tokens up to `last` in the order
+    // mass or number of the kept tokens up to `last` in the order, in the whole row
     auto upto = [&](u64 last, bool masses) {
         u64 s = 0;
         groups([&](int, const float (&x)[4], int id) {
@@ -327,12 +333,16 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(SampleArgs a, int SL) {
             for (int e = 0; e < 4; ++e)
                 if (kept(x[e], id + e) && order_of(key_of(x[e]), id + e) <= last) s += masses ? weight(x[e]) : 1;
         });
-        return cluster_sum(block_sum(s));
+        tell(turn, block_sum(s));
+        s = 0;
+        for (int c = 0; c < C; ++c) s += sm.from[turn][c];
+        turn = 3 - turn;
+        return s;
     };
-    // The last token of the shortest start that reaches `want` (mass or number), within the tokens up to cut, by bisection:
-    // for rows with thousands of equal or nearly equal values at the cut.
+    // The last token of the shortest start of the kept ones that reaches `want` (mass or number), by bisection: for rows with
+    // more candidates than the list takes, of equal or nearly equal values at the cut.
     auto bisect = [&](u64 want, bool masses) {
-        u64 lo = order_of(key_top, 0), hi = order_of(key_of(cut), min(cut_id, (1 << kIdBits) - 1));   // sum(lo - 1) < want <= sum(hi)
+        u64 lo = order_of(key_of(top), 0), hi = order_of(key_of(cut), min(cut_id, (1 << kIdBits) - 1));   // sum(lo - 1) < want <= sum(hi)
         while (lo < hi) {
             const u64 m = lo + (hi - lo) / 2;
             if (upto(m, masses) >= want) hi = m;
@@ -347,7 +357,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(SampleArgs a, int SL) {
         u64 v = 0;
         for (int c = 0; c < C; ++c) {
             const Shared &o = *cluster.map_shared_rank(&sm, c);
-            v += ((u64)o.hi[tid] << 32) + o.lo[tid];
+            v += o.h[0][tid] + ((u64)o.h[1][tid] << 16) + ((u64)o.h[2][tid] << 32);
         }
         const u64 run = block_scan(v);
         if (tid == 0) sm.at = -1;
@@ -359,58 +369,54 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(SampleArgs a, int SL) {
         before = sm.above, own = sm.part[0];
         return sm.at;
     };
-    auto push = [&](uint32_t key, int id) {
+    auto reset = [&] {   // histogram and list empty again
+        sync();
+#pragma unroll
+        for (int k = 0; k < 3; ++k) sm.h[k][tid] = 0;
+        if (tid == 0) sm.n_list = 0;
+        __syncthreads();
+    };
+    auto push = [&](float x, int id) {
         Shared &o = *cluster.map_shared_rank(&sm, 0);
         const int i = atomicAdd(&o.n_list, 1);
-        if (i < kList) o.list[i] = order_of(key, id);
+        if (i < kList) o.list[i] = order_of(key_of(x), id);
     };
-    // The first CTA sorts the list; f(its n entries) says which is the last kept; everyone gets it.
-    auto decide = [&](auto f) {
+    auto pushed = [&] {   // how many have been, in the whole cluster
         sync();
-        if (rank == 0) {
-            const int n = sm.n_list;
-            int n2 = 32;
-            while (n2 < n) n2 *= 2;
-            for (int i = tid + n; i < n2; i += kThreads) sm.list[i] = ~0ull;
-            __syncthreads();
-            for (int size = 2; size <= n2; size *= 2)
-                for (int half = size / 2; half; half /= 2) {
-                    if (tid < n2 / 2) {
-                        const int i = 2 * tid - (tid & (half - 1)), j = i + half;
-                        const u64 x = sm.list[i], y = sm.list[j];
-                        if ((x > y) == ((i & size) == 0)) sm.list[i] = y, sm.list[j] = x;
-                    }
-                    __syncthreads();
-                }
-            const u64 last = f(n);
-            if (tid < C) *cluster.map_shared_rank(&sm.cut, tid) = last;
-        }
-        sync();
-        return sm.cut;
+        return cluster.map_shared_rank(&sm, 0)->n_list;
     };
-    // how many of the list's first n entries, whose sum of weights is cut at P, are kept: by the thread of each entry
-    auto list_cut = [&](int n, u64 ahead, auto threshold) {
-        const u64 w = tid < n ? weight(value_of(~(uint32_t)(sm.list[tid] >> kIdBits))) : 0;
-        const u64 run = block_scan(w);
-        if (tid == n - 1) sm.total = run;
+    auto sort_list = [&](int n) {
+        int n2 = 32;
+        while (n2 < n) n2 *= 2;
+        for (int i = tid + n; i < n2; i += kThreads) sm.list[i] = ~0ull;
         __syncthreads();
-        const u64 P = threshold(sm.total);
-        const int kept = __syncthreads_count(tid < n && ahead + run - w < P);
-        return max(kept, 1);
+        for (int size = 2; size <= n2; size *= 2)
+            for (int half = size / 2; half; half /= 2) {
+                if (tid < n2 / 2) {
+                    const int i = 2 * tid - (tid & (half - 1)), j = i + half;
+                    const u64 x = sm.list[i], y = sm.list[j];
+                    if ((x > y) == ((i & size) == 0)) sm.list[i] = y, sm.list[j] = x;
+                }
+                __syncthreads();
+            }
     };
-
-    // a token is kept by top-p where the mass before it is below this
-    auto threshold = [&](u64 S) {   // ceil(top_p S)
+    auto id_of = [&](u64 order) { return (int)(order & ((1 << kIdBits) - 1)); };
+    auto weight_of = [&](u64 order) { return weight(value_of(~(uint32_t)(order >> kIdBits))); };
+    auto threshold = [&](u64 S) {   // ceil(top_p S): a token is kept by top-p where the mass before it is below this
         const u64 p = part64(fminf(fmaxf(top_p, 0.f), 0.99999994f));
         return max(1ull, __umul64hi(p, S) + (p * S != 0));
     };
-    bool p_left = top_p < 1.f && !greedy;
+
+    const bool by_p = top_p < 1.f && !greedy, by_k = top_k > 0 && top_k < V && !greedy;
+    u64 S = 0;                // the sum of all kept weights
+    bool listed = false;      // the list has every token that may be kept
+    bool summed = false;      // sm.sums are those of the kept tokens
     if (greedy) {
         u64 first = ~0ull;
         groups([&](int, const float (&x)[4], int id) {
 #pragma unroll
             for (int e = 3; e >= 0; --e)
-                if (x[e] == top) first = min(first, order_of(key_top, id + e));
+                if (x[e] == top) first = min(first, order_of(key_of(top), id + e));
         });
 #pragma unroll
         for (int o = 16; o; o >>= 1) first = min(first, __shfl_xor_sync(~0u, first, o));
@@ -419,75 +425,97 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(SampleArgs a, int SL) {
         for (int w = 0; w < kWarps; ++w) first = min(first, sm.part[w]);
         tell(turn, first);
         for (int c = 0; c < C; ++c) first = min(first, sm.from[turn][c]);
-        turn = 3 - turn;
         cut_at(first);
-    } else if (top_k > 0 && top_k < V) {
-        // ---- top-k, by equal bins of value from the top down. First of each thread's largest only: where k of these are
-        // counted, at least k tokens are, and few more. If all of those are not candidates enough for the list, of every
-        // token, and of the k-th one's bin all are candidates, with the bins above it where they fit.
+        S = 1ull << 40;
+        if (a.token && rank == 0 && tid == 0) a.token[r] = cut_id;
+    } else if (by_k || min_p > 0.f) {
+        // ---- top-k and min-p. Tokens in equal bins of value from the top down, for top-k: first of each thread's largest
+        // only, as where k of these have been counted at least k tokens are, and few more.
         const float span = top - fmaxf(low, top - 64.f * fmaxf(temp, 0.25f)), scale = span > 0.f ? (kBins - 1) / span : 0.f;
         auto bin = [&](float x) { return (int)fminf((top - x) * scale, (float)(kBins - 1)); };
         auto want_k = [&](u64) { return (u64)top_k; };
         u64 want, before = 0, own = 0;
         int b = -1;
-        bool all = false, listed = false;
-        if (top_k <= kThreads * C / 2 && top_k < kList) {
-            if (own_top >= low) atomicAdd(&sm.lo[bin(own_top)], 1u);
+        if (by_k && top_k < kList && top_k <= kThreads * C / 2) {
+            if (own_top >= low) atomicAdd(&sm.h[0][bin(own_top)], 1u);
             b = find_bin(want_k, want, before, own);
-            if (b >= 0 && b < kBins - 1) {
-                groups([&](int, const float (&x)[4], int id) {
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        if (x[e] >= low && bin(x[e]) <= b) push(key_of(x[e]), id + e);
-                });
-                sync();
-                listed = all = cluster.map_shared_rank(&sm, 0)->n_list <= kList;
-            }
-            if (!listed) {
-                sync();
-                sm.lo[tid] = 0;
-                if (tid == 0) sm.n_list = 0;
-                __syncthreads();
-            }
         }
-        if (!listed) {
+        if (b >= 0 ? b < kBins - 1 : min_p > 0.f) {
+            groups([&](int, const float (&x)[4], int id) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (x[e] >= low && (b < 0 || bin(x[e]) <= b)) push(x[e], id + e);
+            });
+            listed = pushed() <= kList;
+        }
+        if (by_k && !listed) {   // of every token: all candidates in the k-th one's bin, with the bins above it where they fit
+            reset();
             groups([&](int, const float (&x)[4], int) {
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
-                    if (x[e] >= low) atomicAdd(&sm.lo[bin(x[e])], 1u);
+                    if (x[e] >= low) atomicAdd(&sm.h[0][bin(x[e])], 1u);
             });
             b = find_bin(want_k, want, before, own);
-            if (b >= 0 && own <= kList) {
-                listed = true, all = before + own <= kList;
+            listed = b >= 0 && before + own <= kList;
+            if (b >= 0 && own > kList) cut_at(bisect(top_k, false));
+            else if (b >= 0) {   // (otherwise fewer than k tokens: all are kept)
                 groups([&](int, const float (&x)[4], int id) {
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
-                        if (x[e] >= low && (all ? bin(x[e]) <= b : bin(x[e]) == b)) push(key_of(x[e]), id + e);
+                        if (x[e] >= low && (listed ? bin(x[e]) <= b : bin(x[e]) == b)) push(x[e], id + e);
                 });
+                const int n = pushed();
+                if (!listed) {
+                    if (rank == 0) {
+                        sort_list(n);
+                        if (tid < C) *cluster.map_shared_rank(&sm.cut, tid) = sm.list[top_k - (int)before - 1];
+                    }
+                    sync();
+                    cut_at(sm.cut);
+                }
             }
         }
         if (listed) {
-            cut_at(decide([&](int) {
-                int n = top_k - (all ? 0 : (int)before);
-                if (all && p_left) n = list_cut(n, 0, threshold);
-                return sm.list[n - 1];
-            }));
-            if (all) p_left = false;
-        } else if (b >= 0) {   // (fewer than k tokens: all are kept)
-            cut_at(bisect(top_k, false));
-        }
-        if (p_left) {   // the histogram again
+            // ---- the rest in the cluster's first CTA: what is kept of the list, and the token, by every entry's thread
+            if (rank == 0) {
+                u64 *const w_s = reinterpret_cast<u64 *>(sm.h);
+                int n = sm.n_list;
+                if (by_k || by_p) sort_list(n);
+                if (by_k) n = min(n, top_k);
+                const u64 e = tid < n ? sm.list[tid] : 0, w = tid < n ? weight_of(e) : 0, run = block_scan(w);
+                if (tid == n - 1) sm.total = run;
+                __syncthreads();
+                if (by_p) {
+                    const u64 P = threshold(sm.total);
+                    n = __syncthreads_count(tid < n && run - w < P);
+                }
+                if (tid < n) w_s[tid] = w;
+                if (tid == n - 1) sm.above = run;
+                __syncthreads();
+                if (a.token && tid < n) {
+                    const u64 want = __umul64hi(part64(u), sm.above);
+                    u64 at = 0;
+                    for (int i = 0; i < n; ++i) at += id_of(sm.list[i]) < id_of(e) ? w_s[i] : 0;
+                    if (at <= want && want < at + w) a.token[r] = id_of(e);
+                }
+                if (tid < C) {
+                    Shared &o = *cluster.map_shared_rank(&sm, tid);
+                    o.cut = sm.list[n - 1], o.kept = sm.above;
+                }
+            }
             sync();
-            sm.lo[tid] = 0;
-            if (tid == 0) sm.n_list = 0;
-            __syncthreads();
+            S = sm.kept;
+            if (by_k || by_p) cut_at(sm.cut);
         }
     }
-    if (p_left) {
+    if (by_p && !listed) {
+        if (by_k || min_p > 0.f) reset();
         // ---- top-p: exact sums of weights in equal bins of the exponent; tokens so light that all of them together make
-        // less than 1 - top_p of the largest alone are only added up
-        const float least = fmaxf(-41.f, log2f(fmaxf(1.f - top_p, 1e-9f)) - log2f((float)V) - 0.01f), scale = (kBins - 1) / -least;
-        auto bin = [&](float x) { return (int)fminf((x - top) * weight.ch * -scale, (float)(kBins - 1)); };
+        // less than 1 - top_p of the whole are only added up
+        const float least =
+            fminf(-0.01f, fmaxf(-41.f, log2f(fmaxf(1.f - top_p, 1e-9f)) + (bound ? log2f(some) : 0.f) - log2f((float)V) - 0.02f));
+        const float scale = (kBins - 1) / least;
+        auto bin = [&](float x) { return (int)fminf((x - top) * ch * scale, (float)(kBins - 1)); };
         u64 rest = 0;
         groups([&](int, const float (&x)[4], int id) {
 #pragma unroll
@@ -497,78 +525,94 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(SampleArgs a, int SL) {
                     const int b = bin(x[e]);
                     if (b == kBins - 1) rest += w;
                     else {
-                        const uint32_t lo = (uint32_t)w, old = atomicAdd(&sm.lo[b], lo), hi = (uint32_t)(w >> 32) + (old + lo < old);
-                        if (hi) atomicAdd(&sm.hi[b], hi);
+                        atomicAdd(&sm.h[0][b], (uint32_t)w & 0xffffu);
+                        atomicAdd(&sm.h[1][b], (uint32_t)w >> 16);
+                        if (w >> 32) atomicAdd(&sm.h[2][b], (uint32_t)(w >> 32));
                     }
                 }
         });
         rest = block_sum(rest);
-        if (tid == 0) {
-            sm.lo[kBins - 1] = (uint32_t)rest;
-            sm.hi[kBins - 1] = (uint32_t)(rest >> 32);
-        }
+        if (tid < 3) sm.h[tid][kBins - 1] = tid == 0 ? (uint32_t)rest & 0xffffu : tid == 1 ? (uint32_t)rest >> 16 : (uint32_t)(rest >> 32);
         u64 P, before, own;
         const int b = find_bin(threshold, P, before, own);
-        groups([&](int, const float (&x)[4], int id) {
+        // sums of what is kept in the bins before, candidates of the bin itself
+        groups([&](int g, const float (&x)[4], int id) {
+            u64 w = 0;
+            bool any = false;
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-                if (kept(x[e], id + e) && bin(x[e]) == b) push(key_of(x[e]), id + e);
+                if (kept(x[e], id + e)) {
+                    const int at = bin(x[e]);
+                    if (at < b) w += weight(x[e]), any = true;
+                    else if (at == b) push(x[e], id + e);
+                }
+            if (__any_sync(~0u, any)) w = warp_sum(w);
+            if (lane == 0) sm.sums[g] = w;
         });
-        sync();
-        if (cluster.map_shared_rank(&sm, 0)->n_list > kList) cut_at(bisect(P, true));
-        else
-            cut_at(decide([&](int n) {
-                n = list_cut(n, before, [&](u64) { return P; });
-                return sm.list[n - 1];
-            }));
-    }
-
-    // ---- kept weights, group by group; the group and the token that u falls on
-    groups([&](int g, const float (&x)[4], int id) {
-        u64 w = 0;
-        bool any = false;
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-            if (kept(x[e], id + e)) w += weight(x[e]), any = true;
-        if (__any_sync(~0u, any)) w = warp_sum(w);
-        if (lane == 0) sm.sums[g] = w;
-    });
-    __syncthreads();
-    const int G = SL / kGroup;
-    const u64 mine = tid < G ? sm.sums[tid] : 0, run = block_scan(mine);
-    __syncthreads();
-    if (tid == kThreads - 1) sm.above = run;
-    __syncthreads();
-    tell(turn, sm.above);
-    u64 S = 0, first = 0;
-    for (int c = 0; c < C; ++c) {
-        if (c < rank) first += sm.from[turn][c];
-        S += sm.from[turn][c];
-    }
-    if (a.token) {
-        // the first id at which the running sum is above u S
-        const u64 want = __umul64hi(part64(u), S);
-        if (first + run - mine <= want && want < first + run) {   // this thread's group
-            sm.at = tid;
-            sm.above = first + run - mine;
-        }
-        const bool here = first <= want && want < first + sm.from[turn][rank];
-        __syncthreads();
-        if (here && warp == 0) {
-            const int g = sm.at, id = base + g * kGroup + lane * 4 - lead;
-            float x[4];
-            u64 w[4], sum = 0;
-            load4(seg + g * kGroup + lane * 4, x);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                w[e] = kept(x[e], id + e) ? weight(x[e]) : 0;
-                sum += w[e];
+        if (pushed() > kList) cut_at(bisect(P, true));
+        else {
+            if (rank == 0) {
+                const int n = sm.n_list;
+                sort_list(n);
+                const u64 w = tid < n ? weight_of(sm.list[tid]) : 0, run = block_scan(w);
+                const int m = __syncthreads_count(tid < n && before + run - w < P);
+                if (tid < C) *cluster.map_shared_rank(&sm.cut, tid) = sm.list[m - 1];
             }
-            u64 at = sm.above + warp_scan(sum) - sum;
+            sync();
+            const u64 last = sm.cut;
+            cut_at(last);
+            const Shared &o = *cluster.map_shared_rank(&sm, 0);
+            if (tid < o.n_list && o.list[tid] <= last) {   // the segment's share of them
+                const int pos = id_of(o.list[tid]) + lead - base;
+                if (pos >= 0 && pos < SL) atomicAdd(&sm.sums[pos / kGroup], weight_of(o.list[tid]));
+            }
+            summed = true;
+        }
+    }
+    if (!listed && !greedy) {
+        // ---- kept weights, group by group; the group and the token that u falls on
+        if (!summed)
+            groups([&](int g, const float (&x)[4], int id) {
+                u64 w = 0;
+                bool any = false;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                if (at <= want && want < at + w[e]) a.token[r] = id + e;
-                at += w[e];
+                for (int e = 0; e < 4; ++e)
+                    if (kept(x[e], id + e)) w += weight(x[e]), any = true;
+                if (__any_sync(~0u, any)) w = warp_sum(w);
+                if (lane == 0) sm.sums[g] = w;
+            });
+        __syncthreads();
+        const u64 mine = tid < SL / kGroup ? sm.sums[tid] : 0, run = block_scan(mine);
+        if (tid == kThreads - 1) sm.total = run;
+        __syncthreads();
+        tell(turn, sm.total);
+        u64 first = 0;
+        for (int c = 0; c < C; ++c) {
+            if (c < rank) first += sm.from[turn][c];
+            S += sm.from[turn][c];
+        }
+        if (a.token) {
+            // the first id at which the running sum is above u S
+            const u64 want = __umul64hi(part64(u), S);
+            if (first + run - mine <= want && want < first + run) sm.at = tid, sm.above = first + run - mine;
+            const bool here = first <= want && want < first + sm.from[turn][rank];
+            __syncthreads();
+            if (here && warp == 0) {
+                const int g = sm.at, id = base + g * kGroup + lane * 4 - lead;
+                float x[4];
+                u64 w[4], sum = 0;
+                load4(seg + g * kGroup + lane * 4, x);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    w[e] = kept(x[e], id + e) ? weight(x[e]) : 0;
+                    sum += w[e];
+                }
+                u64 at = sm.above + warp_scan(sum) - sum;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    if (at <= want && want < at + w[e]) a.token[r] = id + e;
+                    at += w[e];
+                }
             }
         }
     }
