@@ -119,8 +119,10 @@ def check_attention(cache, q, out, lens, scale=None):
         assert worst <= 1.0, f"request {b}: error {worst:.2f} of its tolerance"
 
 
-# Whole-number weights are off by 2^-41 of the largest each, and by 2^-23 of themselves at most: sums over a row by less
-# than this share of the row's sum.
+# Whole-number weights are off by 2^-41 of the largest each. Large ones (from 2^-8 of the largest on) by 2^-38 of themselves;
+# small ones by up to 2^-20 (roundings of an exponent of some 16 and of 2^x), as often up as down: their sum by a standard
+# deviation of 2^-20 sqrt(sum w^2) <= 2^-20 sqrt(2^-8 sum w), and as the whole sum is 1 at least, by less than 2^-22 of that
+# within four of these.
 SUM_OFF = 2.0 ** -22
 
 

@@ -33,6 +33,7 @@ constexpr int kThreads = 512, kWarps = kThreads / 32;
 constexpr int kGroup = 128;                    // elements of a warp's turn: a sum of weights is kept for each
 constexpr int kMaxSeg = 32896;                 // elements of a segment: 2^18 + 7 over 8 CTAs, in whole groups
 constexpr int kBins = kThreads, kList = 512;   // a thread a bin, a thread a candidate
+constexpr int kLarges = 64;                    // places of large weights that a warp puts off
 typedef unsigned long long u64;
 
 // Whole numbers in the order of the floats (-0 counts as 0).
@@ -57,19 +58,30 @@ __constant__ float kRootHi[8] = {0x1.0000000000000p+0f, 0x1.172b840000000p+0f, 0
 __constant__ float kRootLo[8] = {0x0.0p+0f, -0x1.c157420000000p-27f, 0x1.4636e20000000p-25f, -0x1.593abc0000000p-25f,
                                  0x1.9fcef40000000p-26f, 0x1.15506e0000000p-27f, -0x1.a94b140000000p-26f, -0x1.822dbc0000000p-27f};
 
-// exp((x - top) / T) in units of 2^-40: y = (x - top) log2(e) / T as a sum of two floats (the difference and the products
-// by their exact errors).
-//  - Weights below 2^-8: ex2 and a correction, to some 2^-22 of themselves.
-//  - From 2^-8 on to the unit and some 2^-38 of themselves: y = n + j / 8 + g, and 2^y = 2^n 2^(j/8) (1 + t + t^2 / 2 + ..),
-//    t = g ln 2, |t| < 0.0434: the first two terms as sums of two floats, the rest (below 2^-16) in one.
+// exp((x - top) / T) in units of 2^-40, y = (x - top) log2(e) / T.
+//  - Weights below 2^-8: y rounded to nearest once (the difference before it once more) and ex2, together to some 2^-20 of
+//    themselves, as often up as down: the errors of thousands of them add up to little.
+//  - From 2^-8 on to the unit and some 2^-38 of themselves: y as a sum of two floats (the difference and the products by
+//    their exact errors), y = n + j / 8 + g, and 2^y = 2^n 2^(j/8) (1 + t + t^2 / 2 + ..), t = g ln 2, |t| < 0.0434: the
+//    first two terms as sums of two floats, the rest (below 2^-16) in one.
+constexpr float kLarge = -8.f;
 struct Weights {
     float top, ch, cl;   // log2(e) / T = ch + cl
+    __device__ __forceinline__ float exponent(float x) const {
+        const float d = x - top;
+        return fmaf(d, ch, d * cl);
+    }
+    // (ex2 is low by 5.06e-8 of its value on the average of an octave, measured)
+    __device__ __forceinline__ static uint32_t light(float y) {
+        const float e = ex2(y);
+        return __float2uint_rn(fmaf(e, 1099511627776.f, e * 55635.f));
+    }
     __device__ __forceinline__ void exponent(float x, float &yh, float &yl) const {
         const float dh = x - top, bb = dh - x, dl = (x - (dh - bb)) - (top + bb);
         yh = dh * ch;
         yl = fmaf(dh, ch, -yh) + fmaf(dh, cl, dl * ch);
     }
-    __device__ __noinline__ static u64 heavy(float yh, float yl) {
+    __device__ __forceinline__ static u64 heavy(float yh, float yl) {
         const float n8 = rintf(yh * 8.f), f = fmaf(n8, -0.125f, yh);
         const float gh = f + yl, gl = yl - (gh - f);
         const float L = 0.693147182464599609375f, Ll = -1.904654299957767e-09f;   // ln 2
@@ -85,12 +97,15 @@ struct Weights {
         const int sft = 2 - n;
         return (u64)((v + (1ll << (sft - 1))) >> sft);
     }
-    __device__ __forceinline__ u64 operator()(float x) const {
-        float yh, yl;
-        exponent(x, yh, yl);
+    __device__ __noinline__ static u64 large(float x, float top, float ch, float cl) {
         if (x == top) return 1ull << 40;
-        if (yh >= -8.f) return heavy(yh, yl);
-        return yh > -44.f ? __float2uint_rn(ex2(yh) * fmaf(yl, 762123384786.22f, 1099511627776.f)) : 0u;   // 2^40 (1 + yl ln 2)
+        float yh, yl;
+        Weights{top, ch, cl}.exponent(x, yh, yl);
+        return heavy(yh, yl);
+    }
+    __device__ __forceinline__ u64 operator()(float x) const {
+        const float y = exponent(x);
+        return y >= kLarge ? large(x, top, ch, cl) : light(y);
     }
     // The same as a float, to some 2^-21 of itself.
     __device__ __forceinline__ float real(float x) const {
@@ -131,6 +146,7 @@ struct Shared {
     u64 sums[kMaxSeg / kGroup];      // kept weights of each group of the segment
     u64 part[kWarps];
     u64 from[3][8];                  // what the cluster's CTAs tell one another, in turn
+    uint16_t larges[kWarps][kLarges];
     u64 cut, kept;                   // the last token kept, the sum of all kept weights
     u64 above, total;
     float top[kWarps];
@@ -301,6 +317,60 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(SampleArgs a, int SL) {
             f(g, x, base + g * kGroup + lane * 4 - lead);
         }
     };
+    // Weights by groups: small(y, weight) of the elements that take(value, id, y) says, but large(place, y, weight) of those
+    // with large weights, which a warp puts off until it has 32 of them or no more groups: one such element among 32 takes as
+    // long as 32. before(group) and after(group) frame a group.
+    auto weigh = [&](auto before, auto take, auto small, auto large, auto after) {
+        uint16_t *const put_off = sm.larges[warp];
+        int n = 0;
+        auto settle = [&](int from) {
+            __syncwarp();
+            if (from + lane < n) {
+                const int pos = put_off[from + lane];
+                const float x = (float)seg[pos];
+                large(pos, weight.exponent(x), weight(x));
+            }
+            n = from;
+            __syncwarp();
+        };
+        groups([&](int g, const float (&x)[4], int id) {
+            float y[4];
+            before(g);
+            bool some = false;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                y[e] = weight.exponent(x[e]);
+                if (!take(x[e], id + e, y[e])) y[e] = -INFINITY;
+                some |= y[e] >= kLarge;
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (y[e] < kLarge) small(y[e], (u64)Weights::light(y[e]));
+            if (__any_sync(~0u, some))
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const unsigned is = __ballot_sync(~0u, y[e] >= kLarge);
+                    if (n + __popc(is) > kLarges) settle(n - 32);
+                    if (y[e] >= kLarge) put_off[n + __popc(is & ((1u << lane) - 1))] = (uint16_t)(id + e + lead - base);
+                    n += __popc(is);
+                }
+            after(g);
+        });
+        if (n > 32) settle(n - 32);
+        if (n) settle(0);
+    };
+    // the sums of the groups' weights
+    auto sum_groups = [&](auto take) {
+        u64 w = 0;
+        weigh([&](int g) {
+            w = 0;
+            if (lane == 0) sm.sums[g] = 0;
+        }, take, [&](float, u64 one) { w += one; }, [&](int pos, float, u64 one) { atomicAdd(&sm.sums[pos / kGroup], one); },
+              [&](int g) {
+            if (__any_sync(~0u, w != 0)) w = warp_sum(w);
+            if (lane == 0) sm.sums[g] += w;
+        });
+    };
     // the CTA's sum, for every thread
     auto block_sum = [&](u64 v) {
 #pragma unroll
@@ -355,10 +425,12 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(SampleArgs a, int SL) {
     auto find_bin = [&](auto want_of, u64 &want, u64 &before, u64 &own) {
         sync();
         u64 v = 0;
-        for (int c = 0; c < C; ++c) {
-            const Shared &o = *cluster.map_shared_rank(&sm, c);
-            v += o.h[0][tid] + ((u64)o.h[1][tid] << 16) + ((u64)o.h[2][tid] << 32);
-        }
+#pragma unroll
+        for (int c = 0; c < 8; ++c)
+            if (c < C) {
+                const Shared &o = *cluster.map_shared_rank(&sm, c);
+                v += o.h[0][tid] + ((u64)o.h[1][tid] << 16) + ((u64)o.h[2][tid] << 32);
+            }
         const u64 run = block_scan(v);
         if (tid == 0) sm.at = -1;
         if (tid == kThreads - 1) sm.total = run;
@@ -376,18 +448,41 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(SampleArgs a, int SL) {
         if (tid == 0) sm.n_list = 0;
         __syncthreads();
     };
+    // A candidate into the CTA's list; then all of them into that of the cluster's first CTA, if they fit: their number.
     auto push = [&](float x, int id) {
-        Shared &o = *cluster.map_shared_rank(&sm, 0);
-        const int i = atomicAdd(&o.n_list, 1);
-        if (i < kList) o.list[i] = order_of(key_of(x), id);
+        const int i = atomicAdd(&sm.n_list, 1);
+        if (i < kList) sm.list[i] = order_of(key_of(x), id);
     };
-    auto pushed = [&] {   // how many have been, in the whole cluster
+    auto pushed = [&] {
         sync();
-        return cluster.map_shared_rank(&sm, 0)->n_list;
+        if (C == 1) return sm.n_list;
+        int all = 0, at = 0;
+#pragma unroll
+        for (int c = 0; c < 8; ++c)
+            if (c < C) {
+                const int n = cluster.map_shared_rank(&sm, c)->n_list;
+                all += n;
+                if (c < rank) at += n;
+            }
+        if (rank && all <= kList)
+            for (int i = tid; i < sm.n_list; i += kThreads) cluster.map_shared_rank(&sm, 0)->list[at + i] = sm.list[i];
+        cluster.sync();
+        return all;
     };
     auto sort_list = [&](int n) {
-        int n2 = 32;
+        int n2 = 16;
         while (n2 < n) n2 *= 2;
+        if (n2 < kThreads) {   // short: an entry's place is how many are before it, counted by several threads
+            const int share = kThreads / n2, lanes = min(share, 32), i = tid / lanes, k0 = tid % lanes;
+            const u64 e = i < n ? sm.list[i] : ~0ull;
+            int at = 0;
+            for (int k = k0; k < n; k += lanes) at += sm.list[k] < e;
+            for (int o = lanes / 2; o; o >>= 1) at += __shfl_xor_sync(~0u, at, o);
+            __syncthreads();
+            if (i < n && k0 == 0) sm.list[at] = e;
+            __syncthreads();
+            return;
+        }
         for (int i = tid + n; i < n2; i += kThreads) sm.list[i] = ~0ull;
         __syncthreads();
         for (int size = 2; size <= n2; size *= 2)
@@ -435,7 +530,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(SampleArgs a, int SL) {
         auto bin = [&](float x) { return (int)fminf((top - x) * scale, (float)(kBins - 1)); };
         auto want_k = [&](u64) { return (u64)top_k; };
         u64 want, before = 0, own = 0;
-        int b = -1;
+        int b = -1, n_list = 0;
         if (by_k && top_k < kList && top_k <= kThreads * C / 2) {
             if (own_top >= low) atomicAdd(&sm.h[0][bin(own_top)], 1u);
             b = find_bin(want_k, want, before, own);
@@ -444,9 +539,10 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(SampleArgs a, int SL) {
             groups([&](int, const float (&x)[4], int id) {
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
-                    if (x[e] >= low && (b < 0 || bin(x[e]) <= b)) push(x[e], id + e);
+                    if (x[e] >= low && (b < 0 || (top - x[e]) * scale < b + 1)) push(x[e], id + e);
             });
-            listed = pushed() <= kList;
+            n_list = pushed();
+            listed = n_list <= kList;
         }
         if (by_k && !listed) {   // of every token: all candidates in the k-th one's bin, with the bins above it where they fit
             reset();
@@ -464,10 +560,10 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(SampleArgs a, int SL) {
                     for (int e = 0; e < 4; ++e)
                         if (x[e] >= low && (listed ? bin(x[e]) <= b : bin(x[e]) == b)) push(x[e], id + e);
                 });
-                const int n = pushed();
+                n_list = pushed();
                 if (!listed) {
                     if (rank == 0) {
-                        sort_list(n);
+                        sort_list(n_list);
                         if (tid < C) *cluster.map_shared_rank(&sm.cut, tid) = sm.list[top_k - (int)before - 1];
                     }
                     sync();
@@ -479,7 +575,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(SampleArgs a, int SL) {
             // ---- the rest in the cluster's first CTA: what is kept of the list, and the token, by every entry's thread
             if (rank == 0) {
                 u64 *const w_s = reinterpret_cast<u64 *>(sm.h);
-                int n = sm.n_list;
+                int n = n_list;
                 if (by_k || by_p) sort_list(n);
                 if (by_k) n = min(n, top_k);
                 const u64 e = tid < n ? sm.list[tid] : 0, w = tid < n ? weight_of(e) : 0, run = block_scan(w);
@@ -515,44 +611,34 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(SampleArgs a, int SL) {
         const float least =
             fminf(-0.01f, fmaxf(-41.f, log2f(fmaxf(1.f - top_p, 1e-9f)) + (bound ? log2f(some) : 0.f) - log2f((float)V) - 0.02f));
         const float scale = (kBins - 1) / least;
-        auto bin = [&](float x) { return (int)fminf((x - top) * ch * scale, (float)(kBins - 1)); };
+        auto bin = [&](float y) { return (int)fminf(y * scale, (float)(kBins - 1)); };
         u64 rest = 0;
-        groups([&](int, const float (&x)[4], int id) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                if (kept(x[e], id + e)) {
-                    const u64 w = weight(x[e]);
-                    const int b = bin(x[e]);
-                    if (b == kBins - 1) rest += w;
-                    else {
-                        atomicAdd(&sm.h[0][b], (uint32_t)w & 0xffffu);
-                        atomicAdd(&sm.h[1][b], (uint32_t)w >> 16);
-                        if (w >> 32) atomicAdd(&sm.h[2][b], (uint32_t)(w >> 32));
-                    }
-                }
-        });
+        auto count = [&](float y, u64 w) {
+            const int b = bin(y);
+            if (b == kBins - 1) rest += w;
+            else {
+                atomicAdd(&sm.h[0][b], (uint32_t)w & 0xffffu);
+                atomicAdd(&sm.h[1][b], (uint32_t)w >> 16);
+                if (w >> 32) atomicAdd(&sm.h[2][b], (uint32_t)(w >> 32));
+            }
+        };
+        weigh([](int) {}, [&](float v, int i, float) { return kept(v, i); }, count, [&](int, float y, u64 w) { count(y, w); }, [](int) {});
         rest = block_sum(rest);
         if (tid < 3) sm.h[tid][kBins - 1] = tid == 0 ? (uint32_t)rest & 0xffffu : tid == 1 ? (uint32_t)rest >> 16 : (uint32_t)(rest >> 32);
         u64 P, before, own;
         const int b = find_bin(threshold, P, before, own);
         // sums of what is kept in the bins before, candidates of the bin itself
-        groups([&](int g, const float (&x)[4], int id) {
-            u64 w = 0;
-            bool any = false;
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                if (kept(x[e], id + e)) {
-                    const int at = bin(x[e]);
-                    if (at < b) w += weight(x[e]), any = true;
-                    else if (at == b) push(x[e], id + e);
-                }
-            if (__any_sync(~0u, any)) w = warp_sum(w);
-            if (lane == 0) sm.sums[g] = w;
+        sum_groups([&](float v, int i, float y) {
+            if (!kept(v, i)) return false;
+            const int at = bin(y);
+            if (at == b) push(v, i);
+            return at < b;
         });
-        if (pushed() > kList) cut_at(bisect(P, true));
+        const int n_list = pushed();
+        if (n_list > kList) cut_at(bisect(P, true));
         else {
             if (rank == 0) {
-                const int n = sm.n_list;
+                const int n = n_list;
                 sort_list(n);
                 const u64 w = tid < n ? weight_of(sm.list[tid]) : 0, run = block_scan(w);
                 const int m = __syncthreads_count(tid < n && before + run - w < P);
@@ -562,7 +648,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(SampleArgs a, int SL) {
             const u64 last = sm.cut;
             cut_at(last);
             const Shared &o = *cluster.map_shared_rank(&sm, 0);
-            if (tid < o.n_list && o.list[tid] <= last) {   // the segment's share of them
+            if (tid < n_list && o.list[tid] <= last) {   // the segment's share of them
                 const int pos = id_of(o.list[tid]) + lead - base;
                 if (pos >= 0 && pos < SL) atomicAdd(&sm.sums[pos / kGroup], weight_of(o.list[tid]));
             }
@@ -571,16 +657,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(SampleArgs a, int SL) {
     }
     if (!listed && !greedy) {
         // ---- kept weights, group by group; the group and the token that u falls on
-        if (!summed)
-            groups([&](int g, const float (&x)[4], int id) {
-                u64 w = 0;
-                bool any = false;
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    if (kept(x[e], id + e)) w += weight(x[e]), any = true;
-                if (__any_sync(~0u, any)) w = warp_sum(w);
-                if (lane == 0) sm.sums[g] = w;
-            });
+        if (!summed) sum_groups([&](float v, int i, float) { return kept(v, i); });
         __syncthreads();
         const u64 mine = tid < SL / kGroup ? sm.sums[tid] : 0, run = block_scan(mine);
         if (tid == kThreads - 1) sm.total = run;
