@@ -9,17 +9,18 @@
 // Whether a token is kept, and which token a uniform number falls on, are
 // comparisons of sums over a vocabulary: in fp32 a row of 50k tokens is decided
 // wrongly about once in a thousand draws. So weights are whole numbers, the
-// largest 2^40 (weight): their sums are exact, whatever the order, up to 2^18
-// tokens.
+// largest 2^36 (Weights): their sums are exact, whatever the order.
 //
-// A row stays on the chip: a cluster of CTAs reads it once, each keeps a segment
-// in shared memory, and the passes over it (maximum, a histogram where a filter
-// needs one, kept weights, output rows) run there.
+// Passes over a row: maximum; where a filter needs it a histogram, and the
+// candidates for its last token; kept weights; output rows. Where there are few
+// rows a cluster of CTAs has one, each a segment in shared memory; where there
+// are many a CTA has a row of its own and reads it again from L2 (STREAM).
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <math.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "attn_common.cuh"
 #include "decode.cuh"
@@ -31,8 +32,8 @@ namespace cg = cooperative_groups;
 
 constexpr int kThreads = 512, kWarps = kThreads / 32;
 constexpr int kGroup = 128;                    // elements of a warp's turn: a sum of weights is kept for each
-constexpr int kMaxSeg = 32896;                 // elements of a segment: 2^18 + 7 over 8 CTAs, in whole groups
 constexpr int kBins = kThreads, kList = 512;   // a thread a bin, a thread a candidate
+constexpr int kManyRows = 100;
 constexpr int kLarges = 64;                    // places of large weights that a warp puts off
 typedef unsigned long long u64;
 
@@ -58,30 +59,66 @@ __constant__ float kRootHi[8] = {0x1.0000000000000p+0f, 0x1.172b840000000p+0f, 0
 __constant__ float kRootLo[8] = {0x0.0p+0f, -0x1.c157420000000p-27f, 0x1.4636e20000000p-25f, -0x1.593abc0000000p-25f,
                                  0x1.9fcef40000000p-26f, 0x1.15506e0000000p-27f, -0x1.a94b140000000p-26f, -0x1.822dbc0000000p-27f};
 
-// exp((x - top) / T) in units of 2^-40, y = (x - top) log2(e) / T.
-//  - Weights below 2^-8: y rounded to nearest once (the difference before it once more) and ex2, together to some 2^-20 of
+// Two floats in one register pair, worked on at once.
+__device__ __forceinline__ u64 two(float a, float b) {
+    u64 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ void one_each(u64 v, float &a, float &b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
+__device__ __forceinline__ u64 add2(u64 a, u64 b) {
+    u64 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ u64 mul2(u64 a, u64 b) {
+    u64 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ u64 fma2(u64 a, u64 b, u64 c) {
+    u64 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+
+// exp((x - top) / T) in units of 2^-36, y = (x - top) log2(e) / T.
+//  - Weights below 2^-6: y rounded to nearest once (the difference before it once more) and ex2, together to some 2^-20 of
 //    themselves, as often up as down: the errors of thousands of them add up to little.
-//  - From 2^-8 on to the unit and some 2^-38 of themselves: y as a sum of two floats (the difference and the products by
+//  - From 2^-6 on to the unit and some 2^-38 of themselves: y as a sum of two floats (the difference and the products by
 //    their exact errors), y = n + j / 8 + g, and 2^y = 2^n 2^(j/8) (1 + t + t^2 / 2 + ..), t = g ln 2, |t| < 0.0434: the
 //    first two terms as sums of two floats, the rest (below 2^-16) in one.
-constexpr float kLarge = -8.f;
+constexpr float kLarge = -6.f, kUnits = 68719476736.f;
 struct Weights {
-    float top, ch, cl;   // log2(e) / T = ch + cl
+    float top, ch, cl;   // log2(e) / T = ch + cl, 0 < cl < 2^-22 ch: -inf stays -inf in both products
     __device__ __forceinline__ float exponent(float x) const {
         const float d = x - top;
         return fmaf(d, ch, d * cl);
     }
+    __device__ __forceinline__ void exponents(const float (&x)[4], float (&y)[4]) const {   // the same of four
+        const u64 t = two(-top, -top), h = two(ch, ch), l = two(cl, cl);
+#pragma unroll
+        for (int e = 0; e < 4; e += 2) {
+            const u64 d = add2(two(x[e], x[e + 1]), t);
+            one_each(fma2(d, h, mul2(d, l)), y[e], y[e + 1]);
+        }
+    }
     // (ex2 is low by 5.06e-8 of its value on the average of an octave, measured)
-    __device__ __forceinline__ static uint32_t light(float y) {
-        const float e = ex2(y);
-        return __float2uint_rn(fmaf(e, 1099511627776.f, e * 55635.f));
+    __device__ __forceinline__ static uint32_t whole(float e) { return __float2uint_rn(fmaf(e, kUnits, e * 3477.f)); }
+    __device__ __forceinline__ static uint32_t light(float y) { return whole(ex2(y)); }
+    // of four light ones: below 2^-4, so 32 bits
+    __device__ __forceinline__ static uint32_t light4(const float (&y)[4]) {
+        return whole((ex2(y[0]) + ex2(y[1])) + (ex2(y[2]) + ex2(y[3])));
     }
     __device__ __forceinline__ void exponent(float x, float &yh, float &yl) const {
         const float dh = x - top, bb = dh - x, dl = (x - (dh - bb)) - (top + bb);
         yh = dh * ch;
         yl = fmaf(dh, ch, -yh) + fmaf(dh, cl, dl * ch);
     }
-    __device__ __forceinline__ static u64 heavy(float yh, float yl) {
+    __device__ __noinline__ static u64 large(float x, float top, float ch, float cl) {   // (not inlined: it is for few)
+        if (x == top) return 1ull << 36;
+        float yh, yl;
+        Weights{top, ch, cl}.exponent(x, yh, yl);
         const float n8 = rintf(yh * 8.f), f = fmaf(n8, -0.125f, yh);
         const float gh = f + yl, gl = yl - (gh - f);
         const float L = 0.693147182464599609375f, Ll = -1.904654299957767e-09f;   // ln 2
@@ -92,22 +129,16 @@ struct Weights {
         const int m = (int)n8, j = m & 7, n = m >> 3;   // m = 8 n + j
         const float Rh = kRootHi[j], Rl = kRootLo[j];
         const float z = Rh * ph, hi = Rh + z, lo = (z - (hi - Rh)) + (fmaf(Rh, ph, -z) + fmaf(Rh, pl, fmaf(Rl, ph, Rl)));
-        // hi in [0.95, 2.1): a whole number of 2^-24; in units of 2^-42, then 2^(n - 40)
+        // hi in [0.95, 2.1): a whole number of 2^-24; in units of 2^-42, then 2^(n - 36)
         const long long v = ((long long)(int)(hi * 16777216.f) << 18) + __float2int_rn(lo * 4398046511104.f);
-        const int sft = 2 - n;
+        const int sft = 6 - n;
         return (u64)((v + (1ll << (sft - 1))) >> sft);
-    }
-    __device__ __noinline__ static u64 large(float x, float top, float ch, float cl) {
-        if (x == top) return 1ull << 40;
-        float yh, yl;
-        Weights{top, ch, cl}.exponent(x, yh, yl);
-        return heavy(yh, yl);
     }
     __device__ __forceinline__ u64 operator()(float x) const {
         const float y = exponent(x);
         return y >= kLarge ? large(x, top, ch, cl) : light(y);
     }
-    // The same as a float, to some 2^-21 of itself.
+    // The same as a float, the largest 1, to some 2^-21 of itself.
     __device__ __forceinline__ float real(float x) const {
         float yh, yl;
         exponent(x, yh, yl);
@@ -115,7 +146,7 @@ struct Weights {
     }
 };
 
-// Four elements of a row's segment as floats.
+// Four elements of a row as floats.
 __device__ __forceinline__ void load4(const float *p, float (&x)[4]) {
     const float4 v = *reinterpret_cast<const float4 *>(p);
     x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w;
@@ -126,10 +157,8 @@ __device__ __forceinline__ void load4(const __nv_bfloat16 *p, float (&x)[4]) {
     x[2] = __uint_as_float(v.y << 16), x[3] = __uint_as_float(v.y & 0xffff0000u);
 }
 
-// The sum over the warp of numbers below 2^43.
-__device__ __forceinline__ u64 warp_sum(u64 v) {
-    const uint32_t lo = __reduce_add_sync(~0u, (uint32_t)v & 0xffffffu), hi = __reduce_add_sync(~0u, (uint32_t)(v >> 24));
-    return ((u64)hi << 24) + lo;
+__device__ __forceinline__ u64 warp_sum(uint32_t v) {
+    return ((u64)__reduce_add_sync(~0u, v >> 16) << 16) + __reduce_add_sync(~0u, v & 0xffffu);
 }
 __device__ __forceinline__ u64 warp_scan(u64 v) {   // inclusive
 #pragma unroll
@@ -140,91 +169,120 @@ __device__ __forceinline__ u64 warp_scan(u64 v) {   // inclusive
     return v;
 }
 
+template <bool STREAM>
 struct Shared {
-    uint32_t h[3][kBins];            // the segment's histogram: counts in h[0], or sums by 16 bits each
+    static constexpr int REP = STREAM ? 4 : 1;   // of the histogram, so that none counts more than 2^16 + 2^10 elements
+    uint32_t h[REP][3][kBins];       // the segment's histogram: counts in [0], or sums by 15, 15 and the rest of the bits
     u64 list[kList];                 // the cluster's candidates, in its first CTA, by their place in the order
-    u64 sums[kMaxSeg / kGroup];      // kept weights of each group of the segment
     u64 part[kWarps];
     u64 from[3][8];                  // what the cluster's CTAs tell one another, in turn
-    uint16_t larges[kWarps][kLarges];
+    std::conditional_t<STREAM, uint32_t, uint16_t> larges[kWarps][kLarges];
     u64 cut, kept;                   // the last token kept, the sum of all kept weights
+    int n_kept;                      // how many of the list are, from its start
     u64 above, total;
     float top[kWarps];
     float ch, cl, mh, ml;            // log2(e) / T and T ln(min_p), as sums of two floats
     int n_list, at;
 };
+template <bool STREAM>
+constexpr size_t kFixed = (sizeof(Shared<STREAM>) + 15) / 16 * 16;   // then a sum a group, then the segment
 
 __device__ __forceinline__ void copy16(void *to, const void *from) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(to)), "l"(from) : "memory");
 }
 
-// A cluster a row, segment SL elements. Positions count from the 16-byte boundary at or before the row's first element
-// (lead elements before it); those outside the row hold -inf.
-template <typename T>
+// A cluster a row, segment SL elements; STREAM: a CTA a row, its segment the row. Positions count from the 16-byte boundary
+// at or before the row's first element (lead elements before it); those outside the row count as -inf.
+template <typename T, bool STREAM>
 __global__ void __launch_bounds__(kThreads, 2) k_sample(SampleArgs a, int SL) {
     extern __shared__ uint4 smem[];
-    Shared &sm = *reinterpret_cast<Shared *>(smem);
-    T *const seg = reinterpret_cast<T *>(reinterpret_cast<char *>(smem) + (sizeof(Shared) + 15) / 16 * 16);
+    using Sh = Shared<STREAM>;
+    Sh &sm = *reinterpret_cast<Sh *>(smem);
+    const int NG = SL / kGroup;
+    u64 *const sums = reinterpret_cast<u64 *>(reinterpret_cast<char *>(smem) + kFixed<STREAM>);   // kept weights of each group
+    T *const seg = reinterpret_cast<T *>(sums + (NG + 1) / 2 * 2);
     const cg::cluster_group cluster = cg::this_cluster();
-    const int C = cluster.num_blocks(), rank = cluster.block_rank();
+    const int C = STREAM ? 1 : cluster.num_blocks(), rank = STREAM ? 0 : cluster.block_rank();
     const int r = blockIdx.x / C, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, V = a.V;
     auto sync = [&] {
-        if (C == 1) __syncthreads();
+        if (STREAM || C == 1) __syncthreads();
         else cluster.sync();
     };
-    if (C > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");   // the cluster's CTAs are there:
+    auto peer = [&](int c) -> Sh & {
+        if constexpr (STREAM) return sm;
+        else return *cluster.map_shared_rank(&sm, c);
+    };
+    if (!STREAM && C > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");   // the cluster's CTAs are there:
     pdl_wait();
     pdl_trigger();
 
-    // ---- the segment into shared memory
-    constexpr int VE = 16 / sizeof(T);
     const T *const row = reinterpret_cast<const T *>(a.logits) + (size_t)r * a.stride;
     const int lead = (int)(((uintptr_t)row & 15) / sizeof(T)), base = rank * SL;
+    constexpr int VE = 16 / sizeof(T);
     // 16-byte pieces that lie within the row; what is left at the segment's ends, one by one
     const int v_lo = min(SL, max(0, lead - base + VE - 1)) / VE, v_hi = max(v_lo, min(SL, max(0, V + lead - base)) / VE);
-    {
-        const uint4 *const from = reinterpret_cast<const uint4 *>(row - lead) + base / VE;
-        for (int v = v_lo + tid; v < v_hi; v += kThreads) copy16(seg + v * VE, from + v);
-    }
+    const uint4 *const pieces = reinterpret_cast<const uint4 *>(row - lead) + base / VE;
+    if constexpr (!STREAM)
+        for (int v = v_lo + tid; v < v_hi; v += kThreads) copy16(seg + v * VE, pieces + v);
     const float temp = a.temperature ? a.temperature[r] : 1.f, top_p = a.top_p ? a.top_p[r] : 1.f,
                 min_p = a.min_p ? a.min_p[r] : 0.f, u = a.u ? a.u[r] : 0.f;
     const int top_k = a.top_k ? a.top_k[r] : 0;
     const bool greedy = temp < 7.888609052210118e-31f;   // 2^-100
     if (tid == 0) {   // (64-bit arithmetic is slow enough here that one thread does it for all)
         const double c = 1.4426950408889634 / (greedy ? 1.0 : (double)temp);
-        sm.ch = (float)c, sm.cl = (float)(c - (double)sm.ch);
+        sm.ch = __double2float_rd(c);
+        sm.cl = fmaxf((float)(c - (double)sm.ch), fmaxf(sm.ch * 9.3132257e-10f, 1.4e-45f));
         if (min_p > 0.f) {
             const double m = (double)temp * log((double)fminf(min_p, 1.f));
             sm.mh = (float)m, sm.ml = (float)(m - (double)sm.mh);
         }
         sm.n_list = 0;
     }
+    auto empty = [&] {
 #pragma unroll
-    for (int k = 0; k < 3; ++k) sm.h[k][tid] = 0;
+        for (int k = 0; k < 3 * Sh::REP; ++k) sm.h[k / 3][k % 3][tid] = 0;
+    };
+    empty();
+
+    // ---- the row's maximum, and a lower bound of its sum of weights (that of the threads' largest)
     float top = -INFINITY;
     bool bad = false;
-    for (int i = tid; i < SL - (v_hi - v_lo) * VE; i += kThreads) {
+    auto look = [&](const T *p) {
+        float f[4];
+        load4(p, f);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            bad |= !(f[e] < INFINITY);
+            top = fmaxf(top, f[e]);
+        }
+    };
+    const int odd = STREAM ? (v_lo > 0 ? v_lo * VE : 0) + max(0, V + lead - v_hi * VE) : SL - (v_hi - v_lo) * VE;
+    for (int i = tid; i < odd; i += kThreads) {
         const int pos = i < v_lo * VE ? i : i + (v_hi - v_lo) * VE, p = base + pos - lead;
         const T x = p >= 0 && p < V ? row[p] : (T)(-INFINITY);
-        seg[pos] = x;
+        if constexpr (!STREAM) seg[pos] = x;
         bad |= !((float)x < INFINITY);
         top = fmaxf(top, (float)x);
     }
-    asm volatile("cp.async.wait_all;" ::: "memory");
-#pragma unroll 2
-    for (int v = v_lo + tid; v < v_hi; v += kThreads)   // the pieces that this thread has copied
+    if constexpr (STREAM) {
+        for (int v0 = v_lo + tid; v0 < v_hi; v0 += 4 * kThreads) {
+            uint4 x[4];
 #pragma unroll
-        for (int i = 0; i < VE; i += 4) {
-            float f[4];
-            load4(seg + v * VE + i, f);
+            for (int k = 0; k < 4; ++k)
+                if (v0 + k * kThreads < v_hi) x[k] = pieces[v0 + k * kThreads];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                bad |= !(f[e] < INFINITY);
-                top = fmaxf(top, f[e]);
-            }
+            for (int k = 0; k < 4; ++k)
+                if (v0 + k * kThreads < v_hi)
+#pragma unroll
+                    for (int i = 0; i < VE; i += 4) look(reinterpret_cast<const T *>(&x[k]) + i);
         }
-
-    // ---- the row's maximum, and a lower bound of its sum of weights (that of the threads' largest)
+    } else {
+        asm volatile("cp.async.wait_all;" ::: "memory");
+#pragma unroll 2
+        for (int v = v_lo + tid; v < v_hi; v += kThreads)   // the pieces that this thread has copied
+#pragma unroll
+            for (int i = 0; i < VE; i += 4) look(seg + v * VE + i);
+    }
     const float own_top = top;
 #pragma unroll
     for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
@@ -249,10 +307,10 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(SampleArgs a, int SL) {
     }
     // one word to every CTA of the cluster, and all of theirs
     auto tell = [&](int turn, u64 word) {
-        if (tid < C) *cluster.map_shared_rank(&sm.from[turn][rank], tid) = word;
+        if (tid < C) peer(tid).from[turn][rank] = word;
         sync();
     };
-    if (C > 1) asm volatile("barrier.cluster.wait.aligned;" ::: "memory");             // before anything is written to them
+    if (!STREAM && C > 1) asm volatile("barrier.cluster.wait.aligned;" ::: "memory");   // before anything is written to them
     tell(0, (u64)__float_as_uint(top) | (u64)__float_as_uint(bad ? NAN : some) << 32);
     for (int c = 0; c < C; ++c) top = fmaxf(top, __uint_as_float((uint32_t)sm.from[0][c]));
     some = 0.f;
@@ -264,25 +322,34 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(SampleArgs a, int SL) {
     bad |= top == -INFINITY;
     const bool wrong =
         !(temp >= 0.f && temp < INFINITY) || isnan(top_p) || isnan(min_p) || top_k < 0 || !(u >= 0.f && u < 1.f);
-    auto out_rows = [&](auto prob, auto kept) {   // the segment's part of the output rows
-        float *const rows[2] = {a.probs ? a.probs + (size_t)r * V : nullptr, a.kept ? a.kept + (size_t)r * V : nullptr};
+
+    // four elements of the segment from position pos on, a multiple of 4
+    auto get4 = [&](int pos, float (&x)[4]) {
+        if constexpr (STREAM) {
+            const int p = pos - lead;
+            if (p >= 0 && p + 4 <= V) load4(row + p, x);
+            else
 #pragma unroll
+                for (int e = 0; e < 4; ++e) x[e] = p + e >= 0 && p + e < V ? (float)row[p + e] : -INFINITY;
+        } else {
+            load4(seg + pos, x);
+        }
+    };
+    float *const p_to = a.probs ? a.probs + (size_t)r * V : nullptr, *const k_to = a.kept ? a.kept + (size_t)r * V : nullptr;
+    auto put4 = [&](float *to, int p, const float (&y)[4]) {   // ids p .. p + 3 of an output row
+        if ((((uintptr_t)to - (uintptr_t)lead * 4) & 15) == 0 && p >= 0 && p + 4 <= V)
+            __stcs(reinterpret_cast<float4 *>(to + p), make_float4(y[0], y[1], y[2], y[3]));
+        else
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (p + e >= 0 && p + e < V) to[p + e] = y[e];
+    };
+    auto fill_rows = [&](float prob, float logit) {   // the segment's part of them with one number
         for (int k = 0; k < 2; ++k) {
-            float *const to = rows[k];
-            if (!to) continue;
-            const bool vec = (((uintptr_t)to - (uintptr_t)lead * 4) & 15) == 0;
-            for (int v = tid; v < SL / 4; v += kThreads) {
-                float x[4], y[4];
-                load4(seg + 4 * v, x);
-                const int p = base + 4 * v - lead;
-#pragma unroll
-                for (int e = 0; e < 4; ++e) y[e] = k ? kept(x[e], p + e) : prob(x[e], p + e);
-                if (vec && p >= 0 && p + 4 <= V) __stcs(reinterpret_cast<float4 *>(to + p), make_float4(y[0], y[1], y[2], y[3]));
-                else
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        if (p + e >= 0 && p + e < V) to[p + e] = y[e];
-            }
+            float *const to = k ? k_to : p_to;
+            const float v = k ? logit : prob, y[4] = {v, v, v, v};
+            if (to)
+                for (int i = tid; i < SL / 4; i += kThreads) put4(to, base + 4 * i - lead, y);
         }
     };
     if (bad || wrong) {
@@ -290,7 +357,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(SampleArgs a, int SL) {
             flag(a.status, (bad ? TS_STATUS_NONFINITE : 0u) | (wrong ? TS_STATUS_INDEX : 0u));
             if (a.token) a.token[r] = -1;
         }
-        out_rows([](float, int) { return NAN; }, [](float, int) { return NAN; });
+        fill_rows(NAN, NAN);
         sync();
         return;
     }
@@ -309,25 +376,36 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(SampleArgs a, int SL) {
         cut_id = (int)(last & ((1 << kIdBits) - 1));
     };
 
-    // every element of the segment, by groups: f(group, x[4], id of x[0])
+    // every element of the segment, by groups, AHEAD turns ahead of their use: f(group, x[4], id of x[0])
     auto groups = [&](auto f) {
-        for (int g = warp; g < SL / kGroup; g += kWarps) {
-            float x[4];
-            load4(seg + g * kGroup + lane * 4, x);
+        constexpr int AHEAD = STREAM ? 3 : 1;
+        float next[AHEAD][4], x[4];
+#pragma unroll
+        for (int k = 0; k < AHEAD; ++k)
+            if (warp + k * kWarps < NG) get4((warp + k * kWarps) * kGroup + lane * 4, next[k]);
+#pragma unroll 1
+        for (int g = warp; g < NG; g += kWarps) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                x[e] = next[0][e];
+#pragma unroll
+                for (int k = 1; k < AHEAD; ++k) next[k - 1][e] = next[k][e];
+            }
+            if (g + AHEAD * kWarps < NG) get4((g + AHEAD * kWarps) * kGroup + lane * 4, next[AHEAD - 1]);
             f(g, x, base + g * kGroup + lane * 4 - lead);
         }
     };
-    // Weights by groups: small(y, weight) of the elements that take(value, id, y) says, but large(place, y, weight) of those
-    // with large weights, which a warp puts off until it has 32 of them or no more groups: one such element among 32 takes as
-    // long as 32. before(group) and after(group) frame a group.
+    // Weights by groups, of the elements that take(value, id, y) says: small(y[4]) has those below kLarge and -inf for the
+    // others; large(place, y, weight) those that a warp puts off until it has 32 or no more groups, as one such element
+    // among 32 takes as long as 32. before(group) and after(group) frame a group.
     auto weigh = [&](auto before, auto take, auto small, auto large, auto after) {
-        uint16_t *const put_off = sm.larges[warp];
+        auto *const put_off = sm.larges[warp];
         int n = 0;
         auto settle = [&](int from) {
             __syncwarp();
             if (from + lane < n) {
                 const int pos = put_off[from + lane];
-                const float x = (float)seg[pos];
+                const float x = STREAM ? (float)row[pos - lead] : (float)seg[pos];
                 large(pos, weight.exponent(x), weight(x));
             }
             n = from;
@@ -336,24 +414,22 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(SampleArgs a, int SL) {
         groups([&](int g, const float (&x)[4], int id) {
             float y[4];
             before(g);
-            bool some = false;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                y[e] = weight.exponent(x[e]);
-                if (!take(x[e], id + e, y[e])) y[e] = -INFINITY;
-                some |= y[e] >= kLarge;
-            }
+            weight.exponents(x, y);
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-                if (y[e] < kLarge) small(y[e], (u64)Weights::light(y[e]));
-            if (__any_sync(~0u, some))
+                if (!take(x[e], id + e, y[e])) y[e] = -INFINITY;
+            if (__any_sync(~0u, fmaxf(fmaxf(y[0], y[1]), fmaxf(y[2], y[3])) >= kLarge))
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     const unsigned is = __ballot_sync(~0u, y[e] >= kLarge);
                     if (n + __popc(is) > kLarges) settle(n - 32);
-                    if (y[e] >= kLarge) put_off[n + __popc(is & ((1u << lane) - 1))] = (uint16_t)(id + e + lead - base);
+                    if (y[e] >= kLarge) {
+                        put_off[n + __popc(is & ((1u << lane) - 1))] = id + e + lead - base;
+                        y[e] = -INFINITY;
+                    }
                     n += __popc(is);
                 }
+            small(y);
             after(g);
         });
         if (n > 32) settle(n - 32);
@@ -361,14 +437,14 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(SampleArgs a, int SL) {
     };
     // the sums of the groups' weights
     auto sum_groups = [&](auto take) {
-        u64 w = 0;
-        weigh([&](int g) {
-            w = 0;
-            if (lane == 0) sm.sums[g] = 0;
-        }, take, [&](float, u64 one) { w += one; }, [&](int pos, float, u64 one) { atomicAdd(&sm.sums[pos / kGroup], one); },
+        uint32_t w = 0;
+        weigh([&](int g) { if (lane == 0) sums[g] = 0; }, take, [&](const float (&y)[4]) { w = Weights::light4(y); },
+              [&](int pos, float, u64 one) { atomicAdd(&sums[pos / kGroup], one); },
               [&](int g) {
-            if (__any_sync(~0u, w != 0)) w = warp_sum(w);
-            if (lane == 0) sm.sums[g] += w;
+            if (!__any_sync(~0u, w != 0)) return;
+            const u64 all = warp_sum(w);
+            __syncwarp();
+            if (lane == 0) sums[g] += all;
         });
     };
     // the CTA's sum, for every thread
@@ -426,10 +502,11 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(SampleArgs a, int SL) {
         sync();
         u64 v = 0;
 #pragma unroll
-        for (int c = 0; c < 8; ++c)
+        for (int c = 0; c < (STREAM ? 1 : 8); ++c)
             if (c < C) {
-                const Shared &o = *cluster.map_shared_rank(&sm, c);
-                v += o.h[0][tid] + ((u64)o.h[1][tid] << 16) + ((u64)o.h[2][tid] << 32);
+                const Sh &o = peer(c);
+#pragma unroll
+                for (int k = 0; k < Sh::REP; ++k) v += o.h[k][0][tid] + ((u64)o.h[k][1][tid] << 15) + ((u64)o.h[k][2][tid] << 30);
             }
         const u64 run = block_scan(v);
         if (tid == 0) sm.at = -1;
@@ -443,8 +520,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(SampleArgs a, int SL) {
     };
     auto reset = [&] {   // histogram and list empty again
         sync();
-#pragma unroll
-        for (int k = 0; k < 3; ++k) sm.h[k][tid] = 0;
+        empty();
         if (tid == 0) sm.n_list = 0;
         __syncthreads();
     };
@@ -455,25 +531,25 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(SampleArgs a, int SL) {
     };
     auto pushed = [&] {
         sync();
-        if (C == 1) return sm.n_list;
+        if (STREAM || C == 1) return sm.n_list;
         int all = 0, at = 0;
 #pragma unroll
         for (int c = 0; c < 8; ++c)
             if (c < C) {
-                const int n = cluster.map_shared_rank(&sm, c)->n_list;
+                const int n = peer(c).n_list;
                 all += n;
                 if (c < rank) at += n;
             }
         if (rank && all <= kList)
-            for (int i = tid; i < sm.n_list; i += kThreads) cluster.map_shared_rank(&sm, 0)->list[at + i] = sm.list[i];
-        cluster.sync();
+            for (int i = tid; i < sm.n_list; i += kThreads) peer(0).list[at + i] = sm.list[i];
+        sync();
         return all;
     };
     auto sort_list = [&](int n) {
         int n2 = 16;
         while (n2 < n) n2 *= 2;
         if (n2 < kThreads) {   // short: an entry's place is how many are before it, counted by several threads
-            const int share = kThreads / n2, lanes = min(share, 32), i = tid / lanes, k0 = tid % lanes;
+            const int lanes = min(kThreads / n2, 32), i = tid / lanes, k0 = tid % lanes;
             const u64 e = i < n ? sm.list[i] : ~0ull;
             int at = 0;
             for (int k = k0; k < n; k += lanes) at += sm.list[k] < e;
@@ -505,7 +581,8 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(SampleArgs a, int SL) {
     const bool by_p = top_p < 1.f && !greedy, by_k = top_k > 0 && top_k < V && !greedy;
     u64 S = 0;                // the sum of all kept weights
     bool listed = false;      // the list has every token that may be kept
-    bool summed = false;      // sm.sums are those of the kept tokens
+    bool summed = false;      // sums are those of the kept tokens
+    int n_kept = 0;           // of the list
     if (greedy) {
         u64 first = ~0ull;
         groups([&](int, const float (&x)[4], int id) {
@@ -521,7 +598,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(SampleArgs a, int SL) {
         tell(turn, first);
         for (int c = 0; c < C; ++c) first = min(first, sm.from[turn][c]);
         cut_at(first);
-        S = 1ull << 40;
+        S = 1ull << 36;
         if (a.token && rank == 0 && tid == 0) a.token[r] = cut_id;
     } else if (by_k || min_p > 0.f) {
         // ---- top-k and min-p. Tokens in equal bins of value from the top down, for top-k: first of each thread's largest
@@ -532,14 +609,17 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(SampleArgs a, int SL) {
         u64 want, before = 0, own = 0;
         int b = -1, n_list = 0;
         if (by_k && top_k < kList && top_k <= kThreads * C / 2) {
-            if (own_top >= low) atomicAdd(&sm.h[0][bin(own_top)], 1u);
+            if (own_top >= low) atomicAdd(&sm.h[0][0][bin(own_top)], 1u);
             b = find_bin(want_k, want, before, own);
         }
         if (b >= 0 ? b < kBins - 1 : min_p > 0.f) {
+            // no lower than any value of the bins up to b
+            const float from = b < 0 || scale == 0.f ? low : fmaxf(low, top - (b + 1) / scale * 1.00001f - fabsf(top) * 1e-6f);
             groups([&](int, const float (&x)[4], int id) {
+                if (fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])) >= from)
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    if (x[e] >= low && (b < 0 || (top - x[e]) * scale < b + 1)) push(x[e], id + e);
+                    for (int e = 0; e < 4; ++e)
+                        if (x[e] >= low && (b < 0 || (top - x[e]) * scale < b + 1)) push(x[e], id + e);
             });
             n_list = pushed();
             listed = n_list <= kList;
@@ -549,7 +629,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(SampleArgs a, int SL) {
             groups([&](int, const float (&x)[4], int) {
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
-                    if (x[e] >= low) atomicAdd(&sm.h[0][bin(x[e])], 1u);
+                    if (x[e] >= low) atomicAdd(&sm.h[0][0][bin(x[e])], 1u);
             });
             b = find_bin(want_k, want, before, own);
             listed = b >= 0 && before + own <= kList;
@@ -564,7 +644,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(SampleArgs a, int SL) {
                 if (!listed) {
                     if (rank == 0) {
                         sort_list(n_list);
-                        if (tid < C) *cluster.map_shared_rank(&sm.cut, tid) = sm.list[top_k - (int)before - 1];
+                        if (tid < C) peer(tid).cut = sm.list[top_k - (int)before - 1];
                     }
                     sync();
                     cut_at(sm.cut);
@@ -591,17 +671,17 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(SampleArgs a, int SL) {
                 if (a.token && tid < n) {
                     const u64 want = __umul64hi(part64(u), sm.above);
                     u64 at = 0;
+#pragma unroll 4
                     for (int i = 0; i < n; ++i) at += id_of(sm.list[i]) < id_of(e) ? w_s[i] : 0;
                     if (at <= want && want < at + w) a.token[r] = id_of(e);
                 }
                 if (tid < C) {
-                    Shared &o = *cluster.map_shared_rank(&sm, tid);
-                    o.cut = sm.list[n - 1], o.kept = sm.above;
+                    Sh &o = peer(tid);
+                    o.n_kept = n, o.kept = sm.above;
                 }
             }
             sync();
-            S = sm.kept;
-            if (by_k || by_p) cut_at(sm.cut);
+            S = sm.kept, n_kept = sm.n_kept;
         }
     }
     if (by_p && !listed) {
@@ -611,20 +691,39 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(SampleArgs a, int SL) {
         const float least =
             fminf(-0.01f, fmaxf(-41.f, log2f(fmaxf(1.f - top_p, 1e-9f)) + (bound ? log2f(some) : 0.f) - log2f((float)V) - 0.02f));
         const float scale = (kBins - 1) / least;
-        auto bin = [&](float y) { return (int)fminf(y * scale, (float)(kBins - 1)); };
+        // bin kBins - 1: from least down. (The sum with 1.5 * 2^23 is a whole number in its lower bits.)
+        auto bin = [&](float y) {
+            return y <= least ? kBins - 1 : min(kBins - 2, __float_as_int(fmaf(y, scale, 12582912.f)) & (2 * kBins - 1));
+        };
         u64 rest = 0;
+        uint32_t(*const h)[kBins] = sm.h[warp % Sh::REP];
         auto count = [&](float y, u64 w) {
             const int b = bin(y);
             if (b == kBins - 1) rest += w;
             else {
-                atomicAdd(&sm.h[0][b], (uint32_t)w & 0xffffu);
-                atomicAdd(&sm.h[1][b], (uint32_t)w >> 16);
-                if (w >> 32) atomicAdd(&sm.h[2][b], (uint32_t)(w >> 32));
+                atomicAdd(&h[0][b], (uint32_t)w & 0x7fffu);
+                atomicAdd(&h[1][b], (uint32_t)(w >> 15) & 0x7fffu);
+                if (w >> 30) atomicAdd(&h[2][b], (uint32_t)(w >> 30));
             }
         };
-        weigh([](int) {}, [&](float v, int i, float) { return kept(v, i); }, count, [&](int, float y, u64 w) { count(y, w); }, [](int) {});
+        auto count4 = [&](const float (&y)[4]) {
+            float z[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                z[e] = y[e];
+                if (y[e] > least) {
+                    count(y[e], Weights::light(y[e]));
+                    z[e] = -INFINITY;
+                }
+            }
+            rest += Weights::light4(z);
+        };
+        auto count1 = [&](int, float y, u64 w) { count(y, w); };
+        auto nothing = [](int) {};
+        if (bound) weigh(nothing, [](float, int, float) { return true; }, count4, count1, nothing);
+        else weigh(nothing, [&](float v, int i, float) { return kept(v, i); }, count4, count1, nothing);
         rest = block_sum(rest);
-        if (tid < 3) sm.h[tid][kBins - 1] = tid == 0 ? (uint32_t)rest & 0xffffu : tid == 1 ? (uint32_t)rest >> 16 : (uint32_t)(rest >> 32);
+        if (tid < 3) sm.h[0][tid][kBins - 1] = tid == 0 ? (uint32_t)rest & 0x7fffu : tid == 1 ? (uint32_t)(rest >> 15) & 0x7fffu : (uint32_t)(rest >> 30);
         u64 P, before, own;
         const int b = find_bin(threshold, P, before, own);
         // sums of what is kept in the bins before, candidates of the bin itself
@@ -642,24 +741,30 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(SampleArgs a, int SL) {
                 sort_list(n);
                 const u64 w = tid < n ? weight_of(sm.list[tid]) : 0, run = block_scan(w);
                 const int m = __syncthreads_count(tid < n && before + run - w < P);
-                if (tid < C) *cluster.map_shared_rank(&sm.cut, tid) = sm.list[m - 1];
+                if (tid < C) peer(tid).cut = sm.list[m - 1];
             }
             sync();
             const u64 last = sm.cut;
             cut_at(last);
-            const Shared &o = *cluster.map_shared_rank(&sm, 0);
+            const Sh &o = peer(0);
             if (tid < n_list && o.list[tid] <= last) {   // the segment's share of them
                 const int pos = id_of(o.list[tid]) + lead - base;
-                if (pos >= 0 && pos < SL) atomicAdd(&sm.sums[pos / kGroup], weight_of(o.list[tid]));
+                if (pos >= 0 && pos < SL) atomicAdd(&sums[pos / kGroup], weight_of(o.list[tid]));
             }
             summed = true;
         }
     }
     if (!listed && !greedy) {
         // ---- kept weights, group by group; the group and the token that u falls on
-        if (!summed) sum_groups([&](float v, int i, float) { return kept(v, i); });
+        if (!summed) {
+            if (cut_id == 1 << kIdBits && low == -3.402823466e38f) sum_groups([](float, int, float) { return true; });
+            else sum_groups([&](float v, int i, float) { return kept(v, i); });
+        }
         __syncthreads();
-        const u64 mine = tid < SL / kGroup ? sm.sums[tid] : 0, run = block_scan(mine);
+        const int share = (NG + kThreads - 1) / kThreads, g0 = min(NG, tid * share), g1 = min(NG, g0 + share);   // a thread's groups
+        u64 mine = 0;
+        for (int g = g0; g < g1; ++g) mine += sums[g];
+        const u64 run = block_scan(mine);
         if (tid == kThreads - 1) sm.total = run;
         __syncthreads();
         tell(turn, sm.total);
@@ -671,32 +776,76 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(SampleArgs a, int SL) {
         if (a.token) {
             // the first id at which the running sum is above u S
             const u64 want = __umul64hi(part64(u), S);
-            if (first + run - mine <= want && want < first + run) sm.at = tid, sm.above = first + run - mine;
+            if (first + run - mine <= want && want < first + run) {
+                u64 at = first + run - mine;
+                int g = g0;
+                while (want >= at + sums[g]) at += sums[g++];
+                sm.at = g, sm.above = at;
+            }
             const bool here = first <= want && want < first + sm.from[turn][rank];
             __syncthreads();
-            if (here && warp == 0) {
+            if (here && warp == 0) {   // as sum_groups has added them
                 const int g = sm.at, id = base + g * kGroup + lane * 4 - lead;
-                float x[4];
-                u64 w[4], sum = 0;
-                load4(seg + g * kGroup + lane * 4, x);
+                float x[4], y[4];
+                u64 w[4], large = 0;
+                get4(g * kGroup + lane * 4, x);
+                weight.exponents(x, y);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     w[e] = kept(x[e], id + e) ? weight(x[e]) : 0;
-                    sum += w[e];
+                    if (!kept(x[e], id + e) || y[e] >= kLarge) y[e] = -INFINITY, large += w[e];
                 }
-                u64 at = sm.above + warp_scan(sum) - sum;
+                const u64 sum = large + Weights::light4(y), at = sm.above + warp_scan(sum) - sum;
+                bool mine = at <= want && want < at + sum;
+                if (!__any_sync(~0u, mine)) mine = __ffs(__brev(__ballot_sync(~0u, sum != 0))) - 1 == 31 - lane;
+                if (mine) {   // (the last of any weight, where roundings leave none)
+                    u64 left = want - at;
+                    int t = -1;
+                    bool found = false;
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    if (at <= want && want < at + w[e]) a.token[r] = id + e;
-                    at += w[e];
+                    for (int e = 0; e < 4; ++e) {
+                        if (w[e] && !found) t = id + e;
+                        found |= left < w[e];
+                        left -= w[e];
+                    }
+                    a.token[r] = t;
                 }
             }
         }
     }
-    const float inv = 1099511627776.f / __ull2float_rn(S);
-    out_rows([&](float x, int id) { return kept(x, id) ? weight.real(x) * inv : 0.f; },
-             [&](float x, int id) { return kept(x, id) ? x : TS_DROPPED_LOGIT; });
-    if (C > 1) cluster.sync();   // shared memory that others may still read
+    const float inv = kUnits / __ull2float_rn(S);
+    if (p_to || k_to) {
+        if (listed || greedy) {   // few tokens
+            fill_rows(0.f, TS_DROPPED_LOGIT);
+            __syncthreads();
+            const Sh &o = peer(0);
+            for (int i = tid; i < (greedy ? 1 : n_kept); i += kThreads) {
+                const int id = greedy ? cut_id : id_of(o.list[i]), pos = id + lead - base;
+                if (pos < 0 || pos >= SL) continue;
+                const float x = greedy ? top : value_of(~(uint32_t)(o.list[i] >> kIdBits));   // (the row may be filled by now)
+                if (p_to) p_to[id] = greedy ? 1.f : weight.real(x) * inv;
+                if (k_to) k_to[id] = x;
+            }
+        } else {
+#pragma unroll 4
+            for (int v = tid; v < SL / 4; v += kThreads) {
+                float x[4], y[4];
+                get4(4 * v, x);
+                const int p = base + 4 * v - lead;
+                if (p_to) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) y[e] = kept(x[e], p + e) ? weight.real(x[e]) * inv : 0.f;
+                    put4(p_to, p, y);
+                }
+                if (k_to) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) y[e] = kept(x[e], p + e) ? x[e] : TS_DROPPED_LOGIT;
+                    put4(k_to, p, y);
+                }
+            }
+        }
+    }
+    if (!STREAM && C > 1) cluster.sync();   // shared memory that others may still read
 }
 
 }  // namespace
@@ -704,12 +853,19 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(SampleArgs a, int SL) {
 cudaError_t launch_sample(const SampleArgs &a, ts_dtype dt, cudaStream_t s) {
     const int es = dt == TS_BF16 ? 2 : 4;
     auto seg = [&](int C) { return ((a.V + 16 / es - 1 + C - 1) / C + kGroup - 1) / kGroup * kGroup; };
+    auto need = [&](int C, bool stream) {
+        const size_t sums = (size_t)(seg(C) / kGroup + 1) / 2 * 16;
+        return stream ? kFixed<true> + sums : kFixed<false> + sums + (size_t)seg(C) * es;
+    };
     // The fewest CTAs a row whose segments let two of them share an SM; more where there are few rows.
     int C = 1;
-    while (C < 8 && seg(C) * es > 101000) C *= 2;
-    while (C < 8 && (long long)a.R * C <= num_sms() && seg(2 * C) >= 2048) C *= 2;
+    while (C < 8 && need(C, false) > 115000) C *= 2;
+    const bool stream = C > 1 && a.R >= kManyRows;
+    if (stream) C = 1;
+    else
+        while (C < 8 && (long long)a.R * C <= num_sms() && seg(2 * C) >= 2048) C *= 2;
     const int SL = seg(C);
-    const size_t smem = (sizeof(Shared) + 15) / 16 * 16 + (size_t)SL * es;
+    const size_t smem = need(C, stream);
     auto go = [&](auto kern) {
         cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
         if (e != cudaSuccess) return e;
@@ -728,7 +884,8 @@ cudaError_t launch_sample(const SampleArgs &a, ts_dtype dt, cudaStream_t s) {
         cfg.numAttrs = pdl_enabled() ? 2 : 1;
         return cudaLaunchKernelEx(&cfg, kern, a, SL);
     };
-    return dt == TS_BF16 ? go(k_sample<__nv_bfloat16>) : go(k_sample<float>);
+    if (stream) return dt == TS_BF16 ? go(k_sample<__nv_bfloat16, true>) : go(k_sample<float, true>);
+    return dt == TS_BF16 ? go(k_sample<__nv_bfloat16, false>) : go(k_sample<float, false>);
 }
 
 }  // namespace ts
