@@ -14,7 +14,8 @@
 // Passes over a row: maximum; where a filter needs it a histogram, and the
 // candidates for its last token; kept weights; output rows. Where there are few
 // rows a cluster of CTAs has one, each a segment in shared memory; where there
-// are many a CTA has a row of its own and reads it again from L2 (STREAM).
+// are many long ones a CTA has a row of its own and reads it again from L2, and
+// short ones are a small CTA's.
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <math.h>
@@ -30,12 +31,21 @@ namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr int kThreads = 512, kWarps = kThreads / 32;
-constexpr int kGroup = 128;                    // elements of a warp's turn: a sum of weights is kept for each
-constexpr int kBins = kThreads, kList = 512;   // a thread a bin, a thread a candidate
-constexpr int kManyRows = 100;
-constexpr int kLarges = 64;                    // places of large weights that a warp puts off
 typedef unsigned long long u64;
+enum Mode { kCluster, kStream, kSmall };
+template <Mode M>
+struct Cfg {
+    static constexpr int NT = M == kSmall ? 128 : 512, W = NT / 32;
+    static constexpr int BINS = M == kSmall ? 256 : 512;
+    static constexpr int LIST = M == kStream ? 4096 : 512;   // candidates
+    static constexpr int REP = M == kStream ? 4 : 1;         // histograms, so that none counts more than 2^16 + 2^10 elements
+    static constexpr int PER_SM = M == kSmall ? 8 : 2;       // CTAs
+};
+constexpr int kGroup = 128;       // elements of a warp's turn: a sum of weights is kept for each
+constexpr int kLarges = 64;       // places of large weights that a warp puts off
+constexpr int kManyRows = 100;    // from which rows that no one CTA holds are read again from L2
+constexpr int kSmallV = 4096;
+constexpr int kRing = 5;           // groups of a warp in shared memory or on their way there, where rows are read again
 
 // Whole numbers in the order of the floats (-0 counts as 0).
 __device__ __forceinline__ uint32_t key_of(float x) {
@@ -169,50 +179,53 @@ __device__ __forceinline__ u64 warp_scan(u64 v) {   // inclusive
     return v;
 }
 
-template <bool STREAM>
+template <Mode M>
 struct Shared {
-    static constexpr int REP = STREAM ? 4 : 1;   // of the histogram, so that none counts more than 2^16 + 2^10 elements
-    uint32_t h[REP][3][kBins];       // the segment's histogram: counts in [0], or sums by 15, 15 and the rest of the bits
-    u64 list[kList];                 // the cluster's candidates, in its first CTA, by their place in the order
-    u64 part[kWarps];
-    u64 from[3][8];                  // what the cluster's CTAs tell one another, in turn
-    std::conditional_t<STREAM, uint32_t, uint16_t> larges[kWarps][kLarges];
-    u64 cut, kept;                   // the last token kept, the sum of all kept weights
-    int n_kept;                      // how many of the list are, from its start
+    using F = Cfg<M>;
+    uint32_t h[F::REP][3][F::BINS];   // the segment's histogram: counts in [0], or sums by 15, 15 and the rest of the bits
+    u64 list[F::LIST];                // the cluster's candidates, in its first CTA, by their place in the order
+    u64 part[F::W];
+    u64 from[3][8];                   // what the cluster's CTAs tell one another, in turn
+    std::conditional_t<M == kStream, uint32_t, uint16_t> larges[F::W][kLarges];
+    u64 cut, kept;                    // the last token kept, the sum of all kept weights
     u64 above, total;
-    float top[kWarps];
-    float ch, cl, mh, ml;            // log2(e) / T and T ln(min_p), as sums of two floats
-    int n_list, at;
+    uint4 ring[M == kStream ? F::W * kRing * 32 : 1];   // groups on their way, the warps' own
+    float top[F::W];
+    float ch, cl, mh, ml;             // log2(e) / T and T ln(min_p), as sums of two floats
+    int n_list, n_kept, at;
 };
-template <bool STREAM>
-constexpr size_t kFixed = (sizeof(Shared<STREAM>) + 15) / 16 * 16;   // then a sum a group, then the segment
+template <Mode M>
+constexpr size_t kFixed = (sizeof(Shared<M>) + 15) / 16 * 16;   // then a sum a group, then the segment
 
 __device__ __forceinline__ void copy16(void *to, const void *from) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(to)), "l"(from) : "memory");
 }
 
-// A cluster a row, segment SL elements; STREAM: a CTA a row, its segment the row. Positions count from the 16-byte boundary
-// at or before the row's first element (lead elements before it); those outside the row count as -inf.
-template <typename T, bool STREAM>
-__global__ void __launch_bounds__(kThreads, 2) k_sample(SampleArgs a, int SL) {
+// A cluster a row, segment SL elements; but for kCluster a CTA a row, its segment the row. Positions count from the 16-byte
+// boundary at or before the row's first element (lead elements before it); those outside the row count as -inf.
+template <typename T, Mode M>
+__global__ void __launch_bounds__(Cfg<M>::NT, Cfg<M>::PER_SM) k_sample(SampleArgs a, int SL) {
     extern __shared__ uint4 smem[];
-    using Sh = Shared<STREAM>;
+    using F = Cfg<M>;
+    using Sh = Shared<M>;
+    constexpr int NT = F::NT, W = F::W, BINS = F::BINS, LIST = F::LIST;
+    constexpr bool STREAM = M == kStream, ONE = M != kCluster;
     Sh &sm = *reinterpret_cast<Sh *>(smem);
     const int NG = SL / kGroup;
-    u64 *const sums = reinterpret_cast<u64 *>(reinterpret_cast<char *>(smem) + kFixed<STREAM>);   // kept weights of each group
+    u64 *const sums = reinterpret_cast<u64 *>(reinterpret_cast<char *>(smem) + kFixed<M>);   // kept weights of each group
     T *const seg = reinterpret_cast<T *>(sums + (NG + 1) / 2 * 2);
     const cg::cluster_group cluster = cg::this_cluster();
-    const int C = STREAM ? 1 : cluster.num_blocks(), rank = STREAM ? 0 : cluster.block_rank();
+    const int C = ONE ? 1 : cluster.num_blocks(), rank = ONE ? 0 : cluster.block_rank();
     const int r = blockIdx.x / C, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, V = a.V;
     auto sync = [&] {
-        if (STREAM || C == 1) __syncthreads();
+        if (ONE || C == 1) __syncthreads();
         else cluster.sync();
     };
     auto peer = [&](int c) -> Sh & {
-        if constexpr (STREAM) return sm;
+        if constexpr (ONE) return sm;
         else return *cluster.map_shared_rank(&sm, c);
     };
-    if (!STREAM && C > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");   // the cluster's CTAs are there:
+    if (!ONE && C > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");   // the cluster's CTAs are there:
     pdl_wait();
     pdl_trigger();
 
@@ -223,7 +236,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(SampleArgs a, int SL) {
     const int v_lo = min(SL, max(0, lead - base + VE - 1)) / VE, v_hi = max(v_lo, min(SL, max(0, V + lead - base)) / VE);
     const uint4 *const pieces = reinterpret_cast<const uint4 *>(row - lead) + base / VE;
     if constexpr (!STREAM)
-        for (int v = v_lo + tid; v < v_hi; v += kThreads) copy16(seg + v * VE, pieces + v);
+        for (int v = v_lo + tid; v < v_hi; v += NT) copy16(seg + v * VE, pieces + v);
     const float temp = a.temperature ? a.temperature[r] : 1.f, top_p = a.top_p ? a.top_p[r] : 1.f,
                 min_p = a.min_p ? a.min_p[r] : 0.f, u = a.u ? a.u[r] : 0.f;
     const int top_k = a.top_k ? a.top_k[r] : 0;
@@ -239,13 +252,14 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(SampleArgs a, int SL) {
         sm.n_list = 0;
     }
     auto empty = [&] {
+        uint32_t *const h = &sm.h[0][0][0];
 #pragma unroll
-        for (int k = 0; k < 3 * Sh::REP; ++k) sm.h[k / 3][k % 3][tid] = 0;
+        for (int i = 0; i < F::REP * 3 * BINS; i += NT) h[i + tid] = 0;
     };
     empty();
 
-    // ---- the row's maximum, and a lower bound of its sum of weights (that of the threads' largest)
-    float top = -INFINITY;
+    // ---- the row's maximum; of each thread's elements four, of every fourth one
+    float own[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
     bool bad = false;
     auto look = [&](const T *p) {
         float f[4];
@@ -253,64 +267,67 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(SampleArgs a, int SL) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             bad |= !(f[e] < INFINITY);
-            top = fmaxf(top, f[e]);
+            own[e] = fmaxf(own[e], f[e]);
         }
     };
-    const int odd = STREAM ? (v_lo > 0 ? v_lo * VE : 0) + max(0, V + lead - v_hi * VE) : SL - (v_hi - v_lo) * VE;
-    for (int i = tid; i < odd; i += kThreads) {
+    const int odd = STREAM ? v_lo * VE + max(0, V + lead - v_hi * VE) : SL - (v_hi - v_lo) * VE;
+    for (int i = tid; i < odd; i += NT) {
         const int pos = i < v_lo * VE ? i : i + (v_hi - v_lo) * VE, p = base + pos - lead;
         const T x = p >= 0 && p < V ? row[p] : (T)(-INFINITY);
         if constexpr (!STREAM) seg[pos] = x;
         bad |= !((float)x < INFINITY);
-        top = fmaxf(top, (float)x);
+        own[0] = fmaxf(own[0], (float)x);
     }
     if constexpr (STREAM) {
-        for (int v0 = v_lo + tid; v0 < v_hi; v0 += 4 * kThreads) {
+        for (int v0 = v_lo + tid; v0 < v_hi; v0 += 4 * NT) {
             uint4 x[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k)
-                if (v0 + k * kThreads < v_hi) x[k] = pieces[v0 + k * kThreads];
+                if (v0 + k * NT < v_hi) x[k] = pieces[v0 + k * NT];
 #pragma unroll
             for (int k = 0; k < 4; ++k)
-                if (v0 + k * kThreads < v_hi)
+                if (v0 + k * NT < v_hi)
 #pragma unroll
                     for (int i = 0; i < VE; i += 4) look(reinterpret_cast<const T *>(&x[k]) + i);
         }
     } else {
         asm volatile("cp.async.wait_all;" ::: "memory");
 #pragma unroll 2
-        for (int v = v_lo + tid; v < v_hi; v += kThreads)   // the pieces that this thread has copied
+        for (int v = v_lo + tid; v < v_hi; v += NT)   // the pieces that this thread has copied
 #pragma unroll
             for (int i = 0; i < VE; i += 4) look(seg + v * VE + i);
     }
-    const float own_top = top;
+    float top = fmaxf(fmaxf(own[0], own[1]), fmaxf(own[2], own[3]));
 #pragma unroll
     for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
     if (lane == 0) sm.top[warp] = top;
     bad = __syncthreads_or(bad);
-    top = sm.top[lane % kWarps];
+    top = sm.top[lane % W];
 #pragma unroll
-    for (int o = kWarps / 2; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
+    for (int o = W / 2; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
     const float ch = sm.ch;
+    // a lower bound of the row's sum of weights: these tokens'
     float some = 1.f;
     const bool bound = top_p < 1.f && top_k == 0 && !(min_p > 0.f);
     if (bound) {
-        some = own_top > -INFINITY ? ex2((own_top - top) * ch) : 0.f;
+        some = 0.f;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) some += own[e] > -INFINITY ? ex2((own[e] - top) * ch) : 0.f;
 #pragma unroll
         for (int o = 16; o; o >>= 1) some += __shfl_xor_sync(~0u, some, o);
         __syncthreads();
         if (lane == 0) sm.top[warp] = some;
         __syncthreads();
-        some = sm.top[lane % kWarps];
+        some = sm.top[lane % W];
 #pragma unroll
-        for (int o = kWarps / 2; o; o >>= 1) some += __shfl_xor_sync(~0u, some, o);
+        for (int o = W / 2; o; o >>= 1) some += __shfl_xor_sync(~0u, some, o);
     }
     // one word to every CTA of the cluster, and all of theirs
     auto tell = [&](int turn, u64 word) {
         if (tid < C) peer(tid).from[turn][rank] = word;
         sync();
     };
-    if (!STREAM && C > 1) asm volatile("barrier.cluster.wait.aligned;" ::: "memory");   // before anything is written to them
+    if (!ONE && C > 1) asm volatile("barrier.cluster.wait.aligned;" ::: "memory");   // before anything is written to them
     tell(0, (u64)__float_as_uint(top) | (u64)__float_as_uint(bad ? NAN : some) << 32);
     for (int c = 0; c < C; ++c) top = fmaxf(top, __uint_as_float((uint32_t)sm.from[0][c]));
     some = 0.f;
@@ -349,7 +366,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(SampleArgs a, int SL) {
             float *const to = k ? k_to : p_to;
             const float v = k ? logit : prob, y[4] = {v, v, v, v};
             if (to)
-                for (int i = tid; i < SL / 4; i += kThreads) put4(to, base + 4 * i - lead, y);
+                for (int i = tid; i < SL / 4; i += NT) put4(to, base + 4 * i - lead, y);
         }
     };
     if (bad || wrong) {
@@ -375,24 +392,47 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(SampleArgs a, int SL) {
         cut = value_of(~(uint32_t)(last >> kIdBits));
         cut_id = (int)(last & ((1 << kIdBits) - 1));
     };
+    auto all_of_them = [](float, int, float) { return true; };
+    auto kept_of_them = [&](float v, int i, float) { return kept(v, i); };
 
-    // every element of the segment, by groups, AHEAD turns ahead of their use: f(group, x[4], id of x[0])
+    // every element of the segment, by groups: f(group, x[4], id of x[0]). What comes from L2 is on its way through shared
+    // memory kRing - 1 turns before its use, each lane's part by itself.
     auto groups = [&](auto f) {
-        constexpr int AHEAD = STREAM ? 3 : 1;
-        float next[AHEAD][4], x[4];
+        float x[4];
+        if constexpr (STREAM) {
+            T *const ring = reinterpret_cast<T *>(sm.ring) + warp * kRing * kGroup + lane * 4;
+            auto fetch = [&](int g, int stage) {
+                const int p = g * kGroup + lane * 4 - lead;
+                if (g < NG && p >= 0 && p + 4 <= V)
+                    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(smem_u32(ring + stage * kGroup)), "l"(row + p),
+                                 "n"(4 * sizeof(T))
+                                 : "memory");
+                asm volatile("cp.async.commit_group;" ::: "memory");
+            };
 #pragma unroll
-        for (int k = 0; k < AHEAD; ++k)
-            if (warp + k * kWarps < NG) get4((warp + k * kWarps) * kGroup + lane * 4, next[k]);
+            for (int k = 0; k < kRing - 1; ++k) fetch(warp + k * W, k);
+            int stage = 0;
 #pragma unroll 1
-        for (int g = warp; g < NG; g += kWarps) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                x[e] = next[0][e];
-#pragma unroll
-                for (int k = 1; k < AHEAD; ++k) next[k - 1][e] = next[k][e];
+            for (int g = warp; g < NG; g += W) {
+                fetch(g + (kRing - 1) * W, stage ? stage - 1 : kRing - 1);   // where the last turn's was
+                asm volatile("cp.async.wait_group %0;" ::"n"(kRing - 1) : "memory");
+                const int p = g * kGroup + lane * 4 - lead;
+                if (p >= 0 && p + 4 <= V) load4(ring + stage * kGroup, x);
+                else get4(g * kGroup + lane * 4, x);
+                f(g, x, p);
+                stage = stage == kRing - 1 ? 0 : stage + 1;
             }
-            if (g + AHEAD * kWarps < NG) get4((g + AHEAD * kWarps) * kGroup + lane * 4, next[AHEAD - 1]);
-            f(g, x, base + g * kGroup + lane * 4 - lead);
+            asm volatile("cp.async.wait_all;" ::: "memory");
+        } else {
+            float next[4];
+            if (warp < NG) get4(warp * kGroup + lane * 4, next);
+#pragma unroll 1
+            for (int g = warp; g < NG; g += W) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) x[e] = next[e];
+                if (g + W < NG) get4((g + W) * kGroup + lane * 4, next);
+                f(g, x, base + g * kGroup + lane * 4 - lead);
+            }
         }
     };
     // Weights by groups, of the elements that take(value, id, y) says: small(y[4]) has those below kLarge and -inf for the
@@ -454,9 +494,9 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(SampleArgs a, int SL) {
         __syncthreads();
         if (lane == 0) sm.part[warp] = v;
         __syncthreads();
-        v = sm.part[lane % kWarps];
+        v = sm.part[lane % W];
 #pragma unroll
-        for (int o = kWarps / 2; o; o >>= 1) v += __shfl_xor_sync(~0u, v, o);
+        for (int o = W / 2; o; o >>= 1) v += __shfl_xor_sync(~0u, v, o);
         return v;
     };
     // inclusive running sum over the CTA's threads
@@ -496,26 +536,40 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(SampleArgs a, int SL) {
         }
         return lo;
     };
-    // The histogram's bin, by bins from 0 down in value, that a sum of want(total) falls into: before (the sum ahead of
-    // it) and its own sum, for every thread. Bins are a thread's; what every CTA of the cluster counted is added.
-    auto find_bin = [&](auto want_of, u64 &want, u64 &before, u64 &own) {
+    // The histogram's bin, by bins from 0 down in value, that `want` falls into: before (the sum ahead of it) and its own
+    // sum, for every thread; -1 where the sum of all is less. What every CTA of the cluster counted is added.
+    auto find_bin = [&](auto want_of, u64 &want, u64 &before, u64 &own_sum) {
         sync();
-        u64 v = 0;
+        constexpr int Q = BINS / NT;
+        u64 v[Q] = {};
 #pragma unroll
-        for (int c = 0; c < (STREAM ? 1 : 8); ++c)
+        for (int c = 0; c < (ONE ? 1 : 8); ++c)
             if (c < C) {
                 const Sh &o = peer(c);
 #pragma unroll
-                for (int k = 0; k < Sh::REP; ++k) v += o.h[k][0][tid] + ((u64)o.h[k][1][tid] << 15) + ((u64)o.h[k][2][tid] << 30);
+                for (int k = 0; k < F::REP; ++k)
+#pragma unroll
+                    for (int q = 0; q < Q; ++q) {
+                        const int b = tid * Q + q;
+                        v[q] += o.h[k][0][b] + ((u64)o.h[k][1][b] << 15) + ((u64)o.h[k][2][b] << 30);
+                    }
             }
-        const u64 run = block_scan(v);
+        u64 mine = 0;
+#pragma unroll
+        for (int q = 0; q < Q; ++q) mine += v[q];
+        const u64 run = block_scan(mine);
         if (tid == 0) sm.at = -1;
-        if (tid == kThreads - 1) sm.total = run;
+        if (tid == NT - 1) sm.total = run;
         __syncthreads();
         want = want_of(sm.total);
-        if (run - v < want && want <= run) sm.at = tid, sm.above = run - v, sm.part[0] = v;
+        u64 at = run - mine;
+#pragma unroll
+        for (int q = 0; q < Q; ++q) {
+            if (at < want && want <= at + v[q]) sm.at = tid * Q + q, sm.above = at, sm.part[0] = v[q];
+            at += v[q];
+        }
         __syncthreads();
-        before = sm.above, own = sm.part[0];
+        before = sm.above, own_sum = sm.part[0];
         return sm.at;
     };
     auto reset = [&] {   // histogram and list empty again
@@ -524,14 +578,34 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(SampleArgs a, int SL) {
         if (tid == 0) sm.n_list = 0;
         __syncthreads();
     };
-    // A candidate into the CTA's list; then all of them into that of the cluster's first CTA, if they fit: their number.
-    auto push = [&](float x, int id) {
+    // Candidates of a group, those that take(value) says, into the CTA's list, a place for the whole warp at once; then all of
+    // them into that of the cluster's first CTA, if they fit: their number.
+    auto push4 = [&](const float (&x)[4], int id, auto take) {
+        unsigned is[4];
+        int n = 0;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            is[e] = __ballot_sync(~0u, take(e));
+            n += __popc(is[e]);
+        }
+        if (n == 0) return;
+        int at = 0;
+        if (lane == 0) at = atomicAdd(&sm.n_list, n);
+        at = __shfl_sync(~0u, at, 0);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int i = at + __popc(is[e] & ((1u << lane) - 1));
+            if ((is[e] >> lane & 1) && i < LIST) sm.list[i] = order_of(key_of(x[e]), id + e);
+            at += __popc(is[e]);
+        }
+    };
+    auto push = [&](float x, int id) {   // (one)
         const int i = atomicAdd(&sm.n_list, 1);
-        if (i < kList) sm.list[i] = order_of(key_of(x), id);
+        if (i < LIST) sm.list[i] = order_of(key_of(x), id);
     };
     auto pushed = [&] {
         sync();
-        if (STREAM || C == 1) return sm.n_list;
+        if (ONE || C == 1) return sm.n_list;
         int all = 0, at = 0;
 #pragma unroll
         for (int c = 0; c < 8; ++c)
@@ -540,49 +614,92 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(SampleArgs a, int SL) {
                 all += n;
                 if (c < rank) at += n;
             }
-        if (rank && all <= kList)
-            for (int i = tid; i < sm.n_list; i += kThreads) peer(0).list[at + i] = sm.list[i];
+        if (rank && all <= LIST)
+            for (int i = tid; i < sm.n_list; i += NT) peer(0).list[at + i] = sm.list[i];
         sync();
         return all;
     };
-    auto sort_list = [&](int n) {
+    auto sort = [&](u64 *list, int n) {   // room for a power of two
         int n2 = 16;
         while (n2 < n) n2 *= 2;
-        if (n2 < kThreads) {   // short: an entry's place is how many are before it, counted by several threads
-            const int lanes = min(kThreads / n2, 32), i = tid / lanes, k0 = tid % lanes;
-            const u64 e = i < n ? sm.list[i] : ~0ull;
+        if (n2 <= NT / 2) {   // short: an entry's place is how many are before it, counted by several threads
+            const int lanes = min(NT / n2, 32), i = tid / lanes, k0 = tid % lanes;
+            const u64 e = i < n ? list[i] : ~0ull;
             int at = 0;
-            for (int k = k0; k < n; k += lanes) at += sm.list[k] < e;
+            for (int k = k0; k < n; k += lanes) at += list[k] < e;
             for (int o = lanes / 2; o; o >>= 1) at += __shfl_xor_sync(~0u, at, o);
             __syncthreads();
-            if (i < n && k0 == 0) sm.list[at] = e;
+            if (i < n && k0 == 0) list[at] = e;
             __syncthreads();
             return;
         }
-        for (int i = tid + n; i < n2; i += kThreads) sm.list[i] = ~0ull;
+        for (int i = tid + n; i < n2; i += NT) list[i] = ~0ull;
         __syncthreads();
         for (int size = 2; size <= n2; size *= 2)
             for (int half = size / 2; half; half /= 2) {
-                if (tid < n2 / 2) {
-                    const int i = 2 * tid - (tid & (half - 1)), j = i + half;
-                    const u64 x = sm.list[i], y = sm.list[j];
-                    if ((x > y) == ((i & size) == 0)) sm.list[i] = y, sm.list[j] = x;
+                for (int k = tid; k < n2 / 2; k += NT) {
+                    const int i = 2 * k - (k & (half - 1)), j = i + half;
+                    const u64 x = list[i], y = list[j];
+                    if ((x > y) == ((i & size) == 0)) list[i] = y, list[j] = x;
                 }
                 __syncthreads();
             }
     };
     auto id_of = [&](u64 order) { return (int)(order & ((1 << kIdBits) - 1)); };
-    auto weight_of = [&](u64 order) { return weight(value_of(~(uint32_t)(order >> kIdBits))); };
+    auto value_at = [&](u64 order) { return value_of(~(uint32_t)(order >> kIdBits)); };
     auto threshold = [&](u64 S) {   // ceil(top_p S): a token is kept by top-p where the mass before it is below this
         const u64 p = part64(fminf(fmaxf(top_p, 0.f), 0.99999994f));
         return max(1ull, __umul64hi(p, S) + (p * S != 0));
     };
+    // Of a sorted list's first n entries, whose sum comes after `ahead`: how many are kept where a token is that has less than
+    // P(their sum) before it; and their sum.
+    auto kept_of = [&](const u64 *list, int n, u64 ahead, auto P_of, u64 &sum) {
+        const int q = (n + NT - 1) / NT, i0 = min(n, tid * q), i1 = min(n, i0 + q);   // a thread's entries
+        u64 mine = 0;
+        for (int i = i0; i < i1; ++i) mine += weight(value_at(list[i]));
+        const u64 run = block_scan(mine);
+        if (tid == NT - 1) sm.total = run;
+        if (tid == 0) sm.n_kept = 0;
+        __syncthreads();
+        const u64 P = P_of(sm.total);
+        u64 at = ahead + run - mine;
+        for (int i = i0; i < i1; ++i) {
+            if (at >= P) break;
+            at += weight(value_at(list[i]));
+            if (i == n - 1 || at >= P) sm.n_kept = i + 1, sm.kept = at - ahead;
+        }
+        __syncthreads();
+        sum = sm.kept;
+        return sm.n_kept;
+    };
+    // the segment's share of a list's entries up to `last` added to the groups' sums
+    auto add_listed = [&](const u64 *list, int n, u64 last) {
+        for (int i = tid; i < n; i += NT) {
+            const u64 e = list[i];
+            const int pos = id_of(e) + lead - base;
+            if (e <= last && pos >= 0 && pos < SL) atomicAdd(&sums[pos / kGroup], weight(value_at(e)));
+        }
+    };
 
     const bool by_p = top_p < 1.f && !greedy, by_k = top_k > 0 && top_k < V && !greedy;
     u64 S = 0;                // the sum of all kept weights
-    bool listed = false;      // the list has every token that may be kept
+    bool listed = false;      // all kept tokens are in the list,
+    int n_list = 0;           // of this length: those up to
+    u64 last = ~0ull;         // this place in the order
     bool summed = false;      // sums are those of the kept tokens
-    int n_kept = 0;           // of the list
+    bool drawn = false;
+    // Values in equal bins from the top down: how far down the threads' largest of a number `want` lie. At least as many
+    // tokens do, and few more.
+    const float span = top - fmaxf(low, top - 64.f * fmaxf(temp, 0.25f)), vscale = span > 0.f ? (BINS - 1) / span : 0.f;
+    auto vbin = [&](float x) { return (int)fminf((top - x) * vscale, (float)(BINS - 1)); };
+    auto sample_bin = [&](u64 number) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if (own[e] >= low) atomicAdd(&sm.h[0][0][vbin(own[e])], 1u);
+        u64 want, before, own_sum;
+        const int b = find_bin([&](u64) { return number; }, want, before, own_sum);
+        return b < BINS - 1 ? b : -1;
+    };
     if (greedy) {
         u64 first = ~0ull;
         groups([&](int, const float (&x)[4], int id) {
@@ -594,56 +711,46 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(SampleArgs a, int SL) {
         for (int o = 16; o; o >>= 1) first = min(first, __shfl_xor_sync(~0u, first, o));
         if (lane == 0) sm.part[warp] = first;
         __syncthreads();
-        for (int w = 0; w < kWarps; ++w) first = min(first, sm.part[w]);
+        for (int w = 0; w < W; ++w) first = min(first, sm.part[w]);
         tell(turn, first);
         for (int c = 0; c < C; ++c) first = min(first, sm.from[turn][c]);
         cut_at(first);
         S = 1ull << 36;
+        drawn = true;
         if (a.token && rank == 0 && tid == 0) a.token[r] = cut_id;
     } else if (by_k || min_p > 0.f) {
-        // ---- top-k and min-p. Tokens in equal bins of value from the top down, for top-k: first of each thread's largest
-        // only, as where k of these have been counted at least k tokens are, and few more.
-        const float span = top - fmaxf(low, top - 64.f * fmaxf(temp, 0.25f)), scale = span > 0.f ? (kBins - 1) / span : 0.f;
-        auto bin = [&](float x) { return (int)fminf((top - x) * scale, (float)(kBins - 1)); };
-        auto want_k = [&](u64) { return (u64)top_k; };
-        u64 want, before = 0, own = 0;
-        int b = -1, n_list = 0;
-        if (by_k && top_k < kList && top_k <= kThreads * C / 2) {
-            if (own_top >= low) atomicAdd(&sm.h[0][0][bin(own_top)], 1u);
-            b = find_bin(want_k, want, before, own);
-        }
-        if (b >= 0 ? b < kBins - 1 : min_p > 0.f) {
+        // ---- top-k and min-p
+        u64 want, before = 0, own_sum = 0;
+        int b = -1;
+        if (by_k && top_k < LIST && top_k <= 2 * NT * C) b = sample_bin(top_k);
+        if (b >= 0 || min_p > 0.f) {
             // no lower than any value of the bins up to b
-            const float from = b < 0 || scale == 0.f ? low : fmaxf(low, top - (b + 1) / scale * 1.00001f - fabsf(top) * 1e-6f);
+            const float from = b < 0 || vscale == 0.f ? low : fmaxf(low, top - (b + 1) / vscale * 1.00001f - fabsf(top) * 1e-6f);
             groups([&](int, const float (&x)[4], int id) {
-                if (fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])) >= from)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        if (x[e] >= low && (b < 0 || (top - x[e]) * scale < b + 1)) push(x[e], id + e);
+                if (__any_sync(~0u, fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])) >= from))
+                    push4(x, id, [&](int e) { return x[e] >= low && (b < 0 || (top - x[e]) * vscale < b + 1); });
             });
             n_list = pushed();
-            listed = n_list <= kList;
+            listed = n_list <= LIST;
         }
-        if (by_k && !listed) {   // of every token: all candidates in the k-th one's bin, with the bins above it where they fit
+        if (by_k && !listed) {   // bins of every token: all candidates in the k-th one's, with the bins above it where they fit
             reset();
             groups([&](int, const float (&x)[4], int) {
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
-                    if (x[e] >= low) atomicAdd(&sm.h[0][0][bin(x[e])], 1u);
+                    if (x[e] >= low) atomicAdd(&sm.h[0][0][vbin(x[e])], 1u);
             });
-            b = find_bin(want_k, want, before, own);
-            listed = b >= 0 && before + own <= kList;
-            if (b >= 0 && own > kList) cut_at(bisect(top_k, false));
+            b = find_bin([&](u64) { return (u64)top_k; }, want, before, own_sum);
+            listed = b >= 0 && before + own_sum <= LIST;
+            if (b >= 0 && own_sum > LIST) cut_at(bisect(top_k, false));
             else if (b >= 0) {   // (otherwise fewer than k tokens: all are kept)
                 groups([&](int, const float (&x)[4], int id) {
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        if (x[e] >= low && (listed ? bin(x[e]) <= b : bin(x[e]) == b)) push(x[e], id + e);
+                    push4(x, id, [&](int e) { return x[e] >= low && (listed ? vbin(x[e]) <= b : vbin(x[e]) == b); });
                 });
                 n_list = pushed();
                 if (!listed) {
                     if (rank == 0) {
-                        sort_list(n_list);
+                        sort(sm.list, n_list);
                         if (tid < C) peer(tid).cut = sm.list[top_k - (int)before - 1];
                     }
                     sync();
@@ -652,54 +759,121 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(SampleArgs a, int SL) {
             }
         }
         if (listed) {
-            // ---- the rest in the cluster's first CTA: what is kept of the list, and the token, by every entry's thread
+            // ---- the list's kept entries, in the cluster's first CTA; and the token, if they are few, by every entry's thread
             if (rank == 0) {
-                u64 *const w_s = reinterpret_cast<u64 *>(sm.h);
                 int n = n_list;
-                if (by_k || by_p) sort_list(n);
+                if (by_k || by_p) sort(sm.list, n);
                 if (by_k) n = min(n, top_k);
-                const u64 e = tid < n ? sm.list[tid] : 0, w = tid < n ? weight_of(e) : 0, run = block_scan(w);
-                if (tid == n - 1) sm.total = run;
-                __syncthreads();
-                if (by_p) {
-                    const u64 P = threshold(sm.total);
-                    n = __syncthreads_count(tid < n && run - w < P);
-                }
-                if (tid < n) w_s[tid] = w;
-                if (tid == n - 1) sm.above = run;
-                __syncthreads();
-                if (a.token && tid < n) {
-                    const u64 want = __umul64hi(part64(u), sm.above);
-                    u64 at = 0;
+                u64 sum;
+                n = kept_of(sm.list, n, 0, [&](u64 all) { return by_p ? threshold(all) : ~0ull; }, sum);
+                if (n <= NT / 4) {
+                    u64 *const w_s = reinterpret_cast<u64 *>(sm.h);
+                    const u64 e = tid < n ? sm.list[tid] : 0, w = tid < n ? weight(value_at(e)) : 0;
+                    if (tid < n) w_s[tid] = w;
+                    __syncthreads();
+                    if (a.token && tid < n) {
+                        const u64 place = __umul64hi(part64(u), sum);
+                        u64 at = 0;
 #pragma unroll 4
-                    for (int i = 0; i < n; ++i) at += id_of(sm.list[i]) < id_of(e) ? w_s[i] : 0;
-                    if (at <= want && want < at + w) a.token[r] = id_of(e);
+                        for (int i = 0; i < n; ++i) at += id_of(sm.list[i]) < id_of(e) ? w_s[i] : 0;
+                        if (at <= place && place < at + w) a.token[r] = id_of(e);
+                    }
                 }
                 if (tid < C) {
                     Sh &o = peer(tid);
-                    o.n_kept = n, o.kept = sm.above;
+                    o.n_kept = n, o.kept = sum, o.cut = by_k || by_p ? sm.list[n - 1] : ~0ull;
                 }
             }
             sync();
-            S = sm.kept, n_kept = sm.n_kept;
+            S = sm.kept, last = sm.cut;
+            if (by_k || by_p) cut_at(last);
+            if (sm.n_kept <= NT / 4) drawn = true;
+            else {
+                for (int g = tid; g < NG; g += NT) sums[g] = 0;
+                __syncthreads();
+                add_listed(peer(0).list, n_list, last);
+                summed = true;
+            }
         }
     }
+    if constexpr (STREAM)
+        if (bound && by_p) {
+            // ---- top-p alone: a few thousand largest in the list, the others' sum; where they reach top_p, the rest is done on them
+            const int b = sample_bin(3 * NT);   // (of 4 NT: about 2700 tokens of 50000 that are alike)
+            u64 rest = 0;
+            const float from = top - (b + 1) / vscale;
+            if (b >= 0 && vscale > 0.f) {
+                groups([&](int, const float (&x)[4], int id) {
+                    float y[4];
+                    weight.exponents(x, y);
+                    push4(x, id, [&](int e) { return x[e] >= from || y[e] >= kLarge; });
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (x[e] >= from || y[e] >= kLarge) y[e] = -INFINITY;
+                    rest += Weights::light4(y);
+                });
+                n_list = pushed();
+            }
+            if (b >= 0 && vscale > 0.f && n_list <= LIST) {
+                reset();   // (the list stays)
+                const float bottom = fminf(kLarge, weight.exponent(from)) - 0.01f, scale = (BINS - 1) / bottom;
+                auto bin = [&](float y) { return min(BINS - 1, __float_as_int(fmaf(y, scale, 12582912.f)) & (2 * BINS - 1)); };
+                uint32_t(*const h)[BINS] = sm.h[warp % F::REP];
+                u64 mass = 0;
+                for (int i = tid; i < n_list; i += NT) {
+                    const float x = value_at(sm.list[i]);
+                    const u64 w = weight(x);
+                    const int at = bin(weight.exponent(x));
+                    mass += w;
+                    atomicAdd(&h[0][at], (uint32_t)w & 0x7fffu);
+                    atomicAdd(&h[1][at], (uint32_t)(w >> 15) & 0x7fffu);
+                    if (w >> 30) atomicAdd(&h[2][at], (uint32_t)(w >> 30));
+                }
+                mass = block_sum(mass);
+                const u64 P = threshold(mass + block_sum(rest));
+                if (P <= mass) {
+                    u64 want, before, own_sum, sum;
+                    const int at = find_bin([&](u64) { return P; }, want, before, own_sum);
+                    u64 *const some_of = reinterpret_cast<u64 *>(sm.h);   // the bin's entries
+                    constexpr int ROOM = F::REP * 3 * BINS / 2 >= 2048 ? 2048 : 512;
+                    for (int g = tid; g < NG; g += NT) sums[g] = 0;
+                    for (int i = tid; i < n_list; i += NT)
+                        if (bin(weight.exponent(value_at(sm.list[i]))) == at) {
+                            const int k = atomicAdd(&sm.n_list, 1);
+                            if (k < ROOM) some_of[k] = sm.list[i];
+                        }
+                    __syncthreads();
+                    const int n = sm.n_list;
+                    if (n <= ROOM) {
+                        sort(some_of, n);
+                        last = some_of[kept_of(some_of, n, before, [&](u64) { return P; }, sum) - 1];
+                    } else {
+                        last = bisect(P, true);
+                    }
+                    cut_at(last);
+                    for (int i = tid; i < n_list; i += NT)
+                        if (sm.list[i] <= last) atomicAdd(&sums[(id_of(sm.list[i]) + lead) / kGroup], weight(value_at(sm.list[i])));
+                    listed = summed = true;
+                }
+            }
+            if (!listed) reset();
+        }
     if (by_p && !listed) {
         if (by_k || min_p > 0.f) reset();
         // ---- top-p: exact sums of weights in equal bins of the exponent; tokens so light that all of them together make
         // less than 1 - top_p of the whole are only added up
         const float least =
             fminf(-0.01f, fmaxf(-41.f, log2f(fmaxf(1.f - top_p, 1e-9f)) + (bound ? log2f(some) : 0.f) - log2f((float)V) - 0.02f));
-        const float scale = (kBins - 1) / least;
-        // bin kBins - 1: from least down. (The sum with 1.5 * 2^23 is a whole number in its lower bits.)
+        const float scale = (BINS - 1) / least;
+        // bin BINS - 1: from least down. (The sum with 1.5 * 2^23 is a whole number in its lower bits.)
         auto bin = [&](float y) {
-            return y <= least ? kBins - 1 : min(kBins - 2, __float_as_int(fmaf(y, scale, 12582912.f)) & (2 * kBins - 1));
+            return y <= least ? BINS - 1 : min(BINS - 2, __float_as_int(fmaf(y, scale, 12582912.f)) & (2 * BINS - 1));
         };
         u64 rest = 0;
-        uint32_t(*const h)[kBins] = sm.h[warp % Sh::REP];
+        uint32_t(*const h)[BINS] = sm.h[warp % F::REP];
         auto count = [&](float y, u64 w) {
             const int b = bin(y);
-            if (b == kBins - 1) rest += w;
+            if (b == BINS - 1) rest += w;
             else {
                 atomicAdd(&h[0][b], (uint32_t)w & 0x7fffu);
                 atomicAdd(&h[1][b], (uint32_t)(w >> 15) & 0x7fffu);
@@ -720,55 +894,49 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(SampleArgs a, int SL) {
         };
         auto count1 = [&](int, float y, u64 w) { count(y, w); };
         auto nothing = [](int) {};
-        if (bound) weigh(nothing, [](float, int, float) { return true; }, count4, count1, nothing);
-        else weigh(nothing, [&](float v, int i, float) { return kept(v, i); }, count4, count1, nothing);
+        if (bound) weigh(nothing, all_of_them, count4, count1, nothing);
+        else weigh(nothing, kept_of_them, count4, count1, nothing);
         rest = block_sum(rest);
-        if (tid < 3) sm.h[0][tid][kBins - 1] = tid == 0 ? (uint32_t)rest & 0x7fffu : tid == 1 ? (uint32_t)(rest >> 15) & 0x7fffu : (uint32_t)(rest >> 30);
-        u64 P, before, own;
-        const int b = find_bin(threshold, P, before, own);
+        if (tid < 3) sm.h[0][tid][BINS - 1] = tid == 0 ? (uint32_t)rest & 0x7fffu : tid == 1 ? (uint32_t)(rest >> 15) & 0x7fffu : (uint32_t)(rest >> 30);
+        u64 P, before, own_sum;
+        const int b = find_bin(threshold, P, before, own_sum);
         // sums of what is kept in the bins before, candidates of the bin itself
         sum_groups([&](float v, int i, float y) {
-            if (!kept(v, i)) return false;
-            const int at = bin(y);
+            const int at = kept(v, i) ? bin(y) : BINS;
             if (at == b) push(v, i);
             return at < b;
         });
-        const int n_list = pushed();
-        if (n_list > kList) cut_at(bisect(P, true));
+        n_list = pushed();
+        if (n_list > LIST) cut_at(bisect(P, true));
         else {
             if (rank == 0) {
-                const int n = n_list;
-                sort_list(n);
-                const u64 w = tid < n ? weight_of(sm.list[tid]) : 0, run = block_scan(w);
-                const int m = __syncthreads_count(tid < n && before + run - w < P);
+                u64 sum;
+                sort(sm.list, n_list);
+                const int m = kept_of(sm.list, n_list, before, [&](u64) { return P; }, sum);
                 if (tid < C) peer(tid).cut = sm.list[m - 1];
             }
             sync();
-            const u64 last = sm.cut;
-            cut_at(last);
-            const Sh &o = peer(0);
-            if (tid < n_list && o.list[tid] <= last) {   // the segment's share of them
-                const int pos = id_of(o.list[tid]) + lead - base;
-                if (pos >= 0 && pos < SL) atomicAdd(&sums[pos / kGroup], weight_of(o.list[tid]));
-            }
+            cut_at(sm.cut);
+            add_listed(peer(0).list, n_list, sm.cut);
             summed = true;
         }
     }
-    if (!listed && !greedy) {
+    if (!drawn) {
         // ---- kept weights, group by group; the group and the token that u falls on
         if (!summed) {
-            if (cut_id == 1 << kIdBits && low == -3.402823466e38f) sum_groups([](float, int, float) { return true; });
-            else sum_groups([&](float v, int i, float) { return kept(v, i); });
+            if (cut_id == 1 << kIdBits && low == -3.402823466e38f) sum_groups(all_of_them);
+            else sum_groups(kept_of_them);
         }
         __syncthreads();
-        const int share = (NG + kThreads - 1) / kThreads, g0 = min(NG, tid * share), g1 = min(NG, g0 + share);   // a thread's groups
+        const int share = (NG + NT - 1) / NT, g0 = min(NG, tid * share), g1 = min(NG, g0 + share);   // a thread's groups
         u64 mine = 0;
         for (int g = g0; g < g1; ++g) mine += sums[g];
         const u64 run = block_scan(mine);
-        if (tid == kThreads - 1) sm.total = run;
+        if (tid == NT - 1) sm.total = run;
         __syncthreads();
         tell(turn, sm.total);
         u64 first = 0;
+        S = 0;
         for (int c = 0; c < C; ++c) {
             if (c < rank) first += sm.from[turn][c];
             S += sm.from[turn][c];
@@ -797,7 +965,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(SampleArgs a, int SL) {
                 }
                 const u64 sum = large + Weights::light4(y), at = sm.above + warp_scan(sum) - sum;
                 bool mine = at <= want && want < at + sum;
-                if (!__any_sync(~0u, mine)) mine = __ffs(__brev(__ballot_sync(~0u, sum != 0))) - 1 == 31 - lane;
+                if (!__any_sync(~0u, mine)) mine = __clz(__ballot_sync(~0u, sum != 0)) == 31 - lane;
                 if (mine) {   // (the last of any weight, where roundings leave none)
                     u64 left = want - at;
                     int t = -1;
@@ -816,19 +984,21 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(SampleArgs a, int SL) {
     const float inv = kUnits / __ull2float_rn(S);
     if (p_to || k_to) {
         if (listed || greedy) {   // few tokens
+            __syncthreads();      // (the row may be where they go, and is read no more)
             fill_rows(0.f, TS_DROPPED_LOGIT);
             __syncthreads();
             const Sh &o = peer(0);
-            for (int i = tid; i < (greedy ? 1 : n_kept); i += kThreads) {
+            for (int i = tid; i < (greedy ? 1 : n_list); i += NT) {
+                if (!greedy && o.list[i] > last) continue;
                 const int id = greedy ? cut_id : id_of(o.list[i]), pos = id + lead - base;
                 if (pos < 0 || pos >= SL) continue;
-                const float x = greedy ? top : value_of(~(uint32_t)(o.list[i] >> kIdBits));   // (the row may be filled by now)
+                const float x = greedy ? top : value_at(o.list[i]);
                 if (p_to) p_to[id] = greedy ? 1.f : weight.real(x) * inv;
                 if (k_to) k_to[id] = x;
             }
         } else {
 #pragma unroll 4
-            for (int v = tid; v < SL / 4; v += kThreads) {
+            for (int v = tid; v < SL / 4; v += NT) {
                 float x[4], y[4];
                 get4(4 * v, x);
                 const int p = base + 4 * v - lead;
@@ -845,47 +1015,53 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(SampleArgs a, int SL) {
             }
         }
     }
-    if (!STREAM && C > 1) cluster.sync();   // shared memory that others may still read
+    if (!ONE && C > 1) cluster.sync();   // shared memory that others may still read
+}
+
+template <Mode M>
+size_t smem_of(int SL, int es) {
+    return kFixed<M> + (size_t)(SL / kGroup + 1) / 2 * 16 + (M == kStream ? 0 : (size_t)SL * es);
+}
+
+template <typename T, Mode M>
+cudaError_t launch_as(const SampleArgs &a, int C, int SL, cudaStream_t s) {
+    constexpr auto kern = k_sample<T, M>;
+    const size_t smem = smem_of<M>(SL, sizeof(T));
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)a.R * C);
+    cfg.blockDim = dim3(Cfg<M>::NT);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = C;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    const int pdl = pdl_enabled();
+    cfg.attrs = attr + !pdl;
+    cfg.numAttrs = pdl + (M == kCluster);
+    return cudaLaunchKernelEx(&cfg, kern, a, SL);
+}
+
+template <typename T>
+cudaError_t launch_rows(const SampleArgs &a, cudaStream_t s) {
+    auto seg = [&](int C) { return ((a.V + 16 / (int)sizeof(T) - 1 + C - 1) / C + kGroup - 1) / kGroup * kGroup; };
+    // The fewest CTAs a row whose segments let two of them share an SM; more where there are few rows.
+    int C = 1;
+    while (C < 8 && smem_of<kCluster>(seg(C), sizeof(T)) > 115000) C *= 2;
+    if (C > 1 && a.R >= kManyRows) return launch_as<T, kStream>(a, 1, seg(1), s);
+    while (C < 8 && (long long)a.R * C <= num_sms() && seg(2 * C) >= 2048) C *= 2;
+    if (C == 1 && a.V <= kSmallV) return launch_as<T, kSmall>(a, 1, seg(1), s);
+    return launch_as<T, kCluster>(a, C, seg(C), s);
 }
 
 }  // namespace
 
 cudaError_t launch_sample(const SampleArgs &a, ts_dtype dt, cudaStream_t s) {
-    const int es = dt == TS_BF16 ? 2 : 4;
-    auto seg = [&](int C) { return ((a.V + 16 / es - 1 + C - 1) / C + kGroup - 1) / kGroup * kGroup; };
-    auto need = [&](int C, bool stream) {
-        const size_t sums = (size_t)(seg(C) / kGroup + 1) / 2 * 16;
-        return stream ? kFixed<true> + sums : kFixed<false> + sums + (size_t)seg(C) * es;
-    };
-    // The fewest CTAs a row whose segments let two of them share an SM; more where there are few rows.
-    int C = 1;
-    while (C < 8 && need(C, false) > 115000) C *= 2;
-    const bool stream = C > 1 && a.R >= kManyRows;
-    if (stream) C = 1;
-    else
-        while (C < 8 && (long long)a.R * C <= num_sms() && seg(2 * C) >= 2048) C *= 2;
-    const int SL = seg(C);
-    const size_t smem = need(C, stream);
-    auto go = [&](auto kern) {
-        cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-        if (e != cudaSuccess) return e;
-        cudaLaunchConfig_t cfg = {};
-        cfg.gridDim = dim3((unsigned)a.R * C);
-        cfg.blockDim = dim3(kThreads);
-        cfg.dynamicSmemBytes = smem;
-        cfg.stream = s;
-        cudaLaunchAttribute attr[2];
-        attr[0].id = cudaLaunchAttributeClusterDimension;
-        attr[0].val.clusterDim.x = C;
-        attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-        attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-        attr[1].val.programmaticStreamSerializationAllowed = 1;
-        cfg.attrs = attr;
-        cfg.numAttrs = pdl_enabled() ? 2 : 1;
-        return cudaLaunchKernelEx(&cfg, kern, a, SL);
-    };
-    if (stream) return dt == TS_BF16 ? go(k_sample<__nv_bfloat16, true>) : go(k_sample<float, true>);
-    return dt == TS_BF16 ? go(k_sample<__nv_bfloat16, false>) : go(k_sample<float, false>);
+    return dt == TS_BF16 ? launch_rows<__nv_bfloat16>(a, s) : launch_rows<float>(a, s);
 }
 
 }  // namespace ts
