@@ -37,7 +37,7 @@ template <Mode M>
 struct Cfg {
     static constexpr int NT = M == kSmall ? 128 : 512, W = NT / 32;
     static constexpr int BINS = M == kSmall ? 256 : 512;
-    static constexpr int LIST = M == kStream ? 4096 : 512;   // candidates
+    static constexpr int LIST = M == kStream ? 6144 : 512, SORT = M == kStream ? 4096 : 512;   // candidates, and how many can be sorted
     static constexpr int REP = M == kStream ? 4 : 1;         // histograms, so that none counts more than 2^16 + 2^10 elements
     static constexpr int PER_SM = M == kSmall ? 8 : 2;       // CTAs
 };
@@ -45,7 +45,7 @@ constexpr int kGroup = 128;       // elements of a warp's turn: a sum of weights
 constexpr int kLarges = 64;       // places of large weights that a warp puts off
 constexpr int kManyRows = 100;    // from which rows that no one CTA holds are read again from L2
 constexpr int kSmallV = 4096;
-constexpr int kRing = 5;           // groups of a warp in shared memory or on their way there, where rows are read again
+constexpr int kRing = 3;           // groups of a warp in shared memory or on their way there, where rows are read again
 
 // Whole numbers in the order of the floats (-0 counts as 0).
 __device__ __forceinline__ uint32_t key_of(float x) {
@@ -148,11 +148,24 @@ struct Weights {
         const float y = exponent(x);
         return y >= kLarge ? large(x, top, ch, cl) : light(y);
     }
-    // The same as a float, the largest 1, to some 2^-21 of itself.
-    __device__ __forceinline__ float real(float x) const {
+    // Weights as floats, the largest `one`, to some 2^-21 of themselves.
+    __device__ __forceinline__ float real(float x, float one) const {
         float yh, yl;
         exponent(x, yh, yl);
-        return yh > -150.f ? exp2f(yh) * fmaf(yl, 0.693147182f, 1.f) : 0.f;
+        return yh > -150.f ? ex2(yh) * fmaf(yl, 0.693147182f, 1.f) * one : 0.f;
+    }
+    __device__ __forceinline__ void real4(const float (&x)[4], float one, float (&p)[4]) const {
+        const u64 t = two(-top, -top), h = two(ch, ch), l = two(cl, cl), minus = two(-1.f, -1.f);
+#pragma unroll
+        for (int e = 0; e < 4; e += 2) {
+            const u64 v = two(x[e], x[e + 1]), d = add2(v, t), bb = fma2(v, minus, d),
+                      low = add2(fma2(fma2(bb, minus, d), minus, v), fma2(bb, minus, t));   // d + low = x - top
+            const u64 y = mul2(d, h), yl = add2(fma2(d, h, mul2(y, minus)), fma2(d, l, mul2(low, h)));
+            float y0, y1, f0, f1;
+            one_each(y, y0, y1);
+            one_each(fma2(yl, two(0.693147182f, 0.693147182f), two(1.f, 1.f)), f0, f1);
+            p[e] = y0 > -150.f ? ex2(y0) * f0 * one : 0.f, p[e + 1] = y1 > -150.f ? ex2(y1) * f1 * one : 0.f;
+        }
     }
 };
 
@@ -208,7 +221,7 @@ __global__ void __launch_bounds__(Cfg<M>::NT, Cfg<M>::PER_SM) k_sample(SampleArg
     extern __shared__ uint4 smem[];
     using F = Cfg<M>;
     using Sh = Shared<M>;
-    constexpr int NT = F::NT, W = F::W, BINS = F::BINS, LIST = F::LIST;
+    constexpr int NT = F::NT, W = F::W, BINS = F::BINS, LIST = F::LIST, SORT = F::SORT;
     constexpr bool STREAM = M == kStream, ONE = M != kCluster;
     Sh &sm = *reinterpret_cast<Sh *>(smem);
     const int NG = SL / kGroup;
@@ -619,6 +632,44 @@ __global__ void __launch_bounds__(Cfg<M>::NT, Cfg<M>::PER_SM) k_sample(SampleArg
         sync();
         return all;
     };
+    // All tokens from a value on into the list: their number, above LIST where they do not fit. others(x) sees every four.
+    // A long row's threads note each their own by place, and then put them in one line.
+    auto gather = [&](float from, auto others) {
+        if constexpr (STREAM)
+            if (NG <= 64 * W) {
+                constexpr int MOST = sizeof(sm.h) / NT;
+                uint8_t *const notes = reinterpret_cast<uint8_t *>(sm.h) + tid;   // (the histogram is empty after reset())
+                int n = 0, turn_no = 0;
+                groups([&](int, const float (&x)[4], int) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (x[e] >= from) {
+                            if (n < MOST) notes[n * NT] = (uint8_t)(turn_no * 4 + e);
+                            ++n;
+                        }
+                    ++turn_no;
+                    others(x);
+                });
+                const bool over = __syncthreads_or(n > MOST);
+                const int end = (int)block_scan(n), at = end - n;
+                if (tid == NT - 1) sm.n_list = end;
+                __syncthreads();
+                const int all = sm.n_list;
+                if (over || all > LIST) return LIST + 1;
+#pragma unroll 4
+                for (int k = 0; k < n; ++k) {
+                    const int note = notes[k * NT], id = (warp + (note >> 2) * W) * kGroup + lane * 4 + (note & 3) - lead;
+                    sm.list[at + k] = order_of(key_of((float)row[id]), id);
+                }
+                __syncthreads();
+                return all;
+            }
+        groups([&](int, const float (&x)[4], int id) {
+            if (__any_sync(~0u, fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])) >= from)) push4(x, id, [&](int e) { return x[e] >= from; });
+            others(x);
+        });
+        return pushed();
+    };
     auto sort = [&](u64 *list, int n) {   // room for a power of two
         int n2 = 16;
         while (n2 < n) n2 *= 2;
@@ -642,8 +693,11 @@ __global__ void __launch_bounds__(Cfg<M>::NT, Cfg<M>::PER_SM) k_sample(SampleArg
                     const u64 x = list[i], y = list[j];
                     if ((x > y) == ((i & size) == 0)) list[i] = y, list[j] = x;
                 }
-                __syncthreads();
+                // (32 pairs half 32 or less apart are a warp's own 64 entries)
+                if (half > 32 || (half == 1 && size >= 64)) __syncthreads();
+                else __syncwarp();
             }
+        __syncthreads();
     };
     auto id_of = [&](u64 order) { return (int)(order & ((1 << kIdBits) - 1)); };
     auto value_at = [&](u64 order) { return value_of(~(uint32_t)(order >> kIdBits)); };
@@ -722,16 +776,12 @@ __global__ void __launch_bounds__(Cfg<M>::NT, Cfg<M>::PER_SM) k_sample(SampleArg
         // ---- top-k and min-p
         u64 want, before = 0, own_sum = 0;
         int b = -1;
-        if (by_k && top_k < LIST && top_k <= 2 * NT * C) b = sample_bin(top_k);
+        if (by_k && top_k < SORT && top_k <= 2 * NT * C) b = sample_bin(top_k);
         if (b >= 0 || min_p > 0.f) {
             // no lower than any value of the bins up to b
             const float from = b < 0 || vscale == 0.f ? low : fmaxf(low, top - (b + 1) / vscale * 1.00001f - fabsf(top) * 1e-6f);
-            groups([&](int, const float (&x)[4], int id) {
-                if (__any_sync(~0u, fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])) >= from))
-                    push4(x, id, [&](int e) { return x[e] >= low && (b < 0 || (top - x[e]) * vscale < b + 1); });
-            });
-            n_list = pushed();
-            listed = n_list <= LIST;
+            n_list = gather(from, [](const float (&)[4]) {});
+            listed = n_list <= SORT;
         }
         if (by_k && !listed) {   // bins of every token: all candidates in the k-th one's, with the bins above it where they fit
             reset();
@@ -741,8 +791,8 @@ __global__ void __launch_bounds__(Cfg<M>::NT, Cfg<M>::PER_SM) k_sample(SampleArg
                     if (x[e] >= low) atomicAdd(&sm.h[0][0][vbin(x[e])], 1u);
             });
             b = find_bin([&](u64) { return (u64)top_k; }, want, before, own_sum);
-            listed = b >= 0 && before + own_sum <= LIST;
-            if (b >= 0 && own_sum > LIST) cut_at(bisect(top_k, false));
+            listed = b >= 0 && before + own_sum <= SORT;
+            if (b >= 0 && own_sum > SORT) cut_at(bisect(top_k, false));
             else if (b >= 0) {   // (otherwise fewer than k tokens: all are kept)
                 groups([&](int, const float (&x)[4], int id) {
                     push4(x, id, [&](int e) { return x[e] >= low && (listed ? vbin(x[e]) <= b : vbin(x[e]) == b); });
@@ -799,24 +849,22 @@ __global__ void __launch_bounds__(Cfg<M>::NT, Cfg<M>::PER_SM) k_sample(SampleArg
     if constexpr (STREAM)
         if (bound && by_p) {
             // ---- top-p alone: a few thousand largest in the list, the others' sum; where they reach top_p, the rest is done on them
-            const int b = sample_bin(3 * NT);   // (of 4 NT: about 2700 tokens of 50000 that are alike)
+            // (of 50000 tokens that are alike, some 5300)
+            const int b = sample_bin(4 * NT * 37 / 40);
             u64 rest = 0;
-            const float from = top - (b + 1) / vscale;
-            if (b >= 0 && vscale > 0.f) {
-                groups([&](int, const float (&x)[4], int id) {
+            const float from = fminf(top - (b + 1) / vscale, top + (kLarge - 0.01f) / ch);   // (no large ones are left out)
+            if (b >= 0 && vscale > 0.f)
+                n_list = gather(from, [&](const float (&x)[4]) {
                     float y[4];
                     weight.exponents(x, y);
-                    push4(x, id, [&](int e) { return x[e] >= from || y[e] >= kLarge; });
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
-                        if (x[e] >= from || y[e] >= kLarge) y[e] = -INFINITY;
+                        if (x[e] >= from) y[e] = -INFINITY;
                     rest += Weights::light4(y);
                 });
-                n_list = pushed();
-            }
             if (b >= 0 && vscale > 0.f && n_list <= LIST) {
                 reset();   // (the list stays)
-                const float bottom = fminf(kLarge, weight.exponent(from)) - 0.01f, scale = (BINS - 1) / bottom;
+                const float bottom = weight.exponent(from) - 0.01f, scale = (BINS - 1) / bottom;
                 auto bin = [&](float y) { return min(BINS - 1, __float_as_int(fmaf(y, scale, 12582912.f)) & (2 * BINS - 1)); };
                 uint32_t(*const h)[BINS] = sm.h[warp % F::REP];
                 u64 mass = 0;
@@ -907,7 +955,7 @@ __global__ void __launch_bounds__(Cfg<M>::NT, Cfg<M>::PER_SM) k_sample(SampleArg
             return at < b;
         });
         n_list = pushed();
-        if (n_list > LIST) cut_at(bisect(P, true));
+        if (n_list > SORT) cut_at(bisect(P, true));
         else {
             if (rank == 0) {
                 u64 sum;
@@ -993,23 +1041,29 @@ __global__ void __launch_bounds__(Cfg<M>::NT, Cfg<M>::PER_SM) k_sample(SampleArg
                 const int id = greedy ? cut_id : id_of(o.list[i]), pos = id + lead - base;
                 if (pos < 0 || pos >= SL) continue;
                 const float x = greedy ? top : value_at(o.list[i]);
-                if (p_to) p_to[id] = greedy ? 1.f : weight.real(x) * inv;
+                if (p_to) p_to[id] = greedy ? 1.f : weight.real(x, inv);
                 if (k_to) k_to[id] = x;
             }
         } else {
 #pragma unroll 4
             for (int v = tid; v < SL / 4; v += NT) {
                 float x[4], y[4];
+                bool in[4];
                 get4(4 * v, x);
                 const int p = base + 4 * v - lead;
-                if (p_to) {
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) y[e] = kept(x[e], p + e) ? weight.real(x[e]) * inv : 0.f;
+                for (int e = 0; e < 4; ++e) in[e] = kept(x[e], p + e), y[e] = 0.f;
+                if (p_to) {
+                    if (in[0] | in[1] | in[2] | in[3]) {
+                        weight.real4(x, inv, y);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) y[e] = in[e] ? y[e] : 0.f;
+                    }
                     put4(p_to, p, y);
                 }
                 if (k_to) {
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) y[e] = kept(x[e], p + e) ? x[e] : TS_DROPPED_LOGIT;
+                    for (int e = 0; e < 4; ++e) y[e] = in[e] ? x[e] : TS_DROPPED_LOGIT;
                     put4(k_to, p, y);
                 }
             }
