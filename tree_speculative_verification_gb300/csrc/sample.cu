@@ -551,7 +551,7 @@ __global__ void __launch_bounds__(Cfg<M>::NT, Cfg<M>::PER_SM) k_sample(SampleArg
     };
     // The histogram's bin, by bins from 0 down in value, that `want` falls into: before (the sum ahead of it) and its own
     // sum, for every thread; -1 where the sum of all is less. What every CTA of the cluster counted is added.
-    auto find_bin = [&](auto want_of, u64 &want, u64 &before, u64 &own_sum) {
+    auto find_bin = [&](auto masses, auto want_of, u64 &want, u64 &before, u64 &own_sum) {
         sync();
         constexpr int Q = BINS / NT;
         u64 v[Q] = {};
@@ -560,11 +560,12 @@ __global__ void __launch_bounds__(Cfg<M>::NT, Cfg<M>::PER_SM) k_sample(SampleArg
             if (c < C) {
                 const Sh &o = peer(c);
 #pragma unroll
-                for (int k = 0; k < F::REP; ++k)
+                for (int k = 0; k < (masses ? F::REP : 1); ++k)
 #pragma unroll
                     for (int q = 0; q < Q; ++q) {
                         const int b = tid * Q + q;
-                        v[q] += o.h[k][0][b] + ((u64)o.h[k][1][b] << 15) + ((u64)o.h[k][2][b] << 30);
+                        v[q] += o.h[k][0][b];
+                        if constexpr (masses) v[q] += ((u64)o.h[k][1][b] << 15) + ((u64)o.h[k][2][b] << 30);
                     }
             }
         u64 mine = 0;
@@ -708,6 +709,17 @@ __global__ void __launch_bounds__(Cfg<M>::NT, Cfg<M>::PER_SM) k_sample(SampleArg
     // Of a sorted list's first n entries, whose sum comes after `ahead`: how many are kept where a token is that has less than
     // P(their sum) before it; and their sum.
     auto kept_of = [&](const u64 *list, int n, u64 ahead, auto P_of, u64 &sum) {
+        if (n <= NT) {
+            const u64 w = tid < n ? weight(value_at(list[tid])) : 0, run = block_scan(w);
+            if (tid == NT - 1) sm.total = run;
+            __syncthreads();
+            const u64 P = P_of(sm.total);
+            const int m = __syncthreads_count(tid < n && ahead + run - w < P);
+            if (tid == m - 1) sm.kept = run;
+            __syncthreads();
+            sum = sm.kept;
+            return m;
+        }
         const int q = (n + NT - 1) / NT, i0 = min(n, tid * q), i1 = min(n, i0 + q);   // a thread's entries
         u64 mine = 0;
         for (int i = i0; i < i1; ++i) mine += weight(value_at(list[i]));
@@ -747,11 +759,15 @@ __global__ void __launch_bounds__(Cfg<M>::NT, Cfg<M>::PER_SM) k_sample(SampleArg
     const float span = top - fmaxf(low, top - 64.f * fmaxf(temp, 0.25f)), vscale = span > 0.f ? (BINS - 1) / span : 0.f;
     auto vbin = [&](float x) { return (int)fminf((top - x) * vscale, (float)(BINS - 1)); };
     auto sample_bin = [&](u64 number) {
+        if (number <= NT * C / 2) {   // one a thread is enough
+            own[0] = fmaxf(fmaxf(own[0], own[1]), fmaxf(own[2], own[3]));
+            own[1] = own[2] = own[3] = -INFINITY;
+        }
 #pragma unroll
         for (int e = 0; e < 4; ++e)
             if (own[e] >= low) atomicAdd(&sm.h[0][0][vbin(own[e])], 1u);
         u64 want, before, own_sum;
-        const int b = find_bin([&](u64) { return number; }, want, before, own_sum);
+        const int b = find_bin(std::false_type(), [&](u64) { return number; }, want, before, own_sum);
         return b < BINS - 1 ? b : -1;
     };
     if (greedy) {
@@ -790,7 +806,7 @@ __global__ void __launch_bounds__(Cfg<M>::NT, Cfg<M>::PER_SM) k_sample(SampleArg
                 for (int e = 0; e < 4; ++e)
                     if (x[e] >= low) atomicAdd(&sm.h[0][0][vbin(x[e])], 1u);
             });
-            b = find_bin([&](u64) { return (u64)top_k; }, want, before, own_sum);
+            b = find_bin(std::false_type(), [&](u64) { return (u64)top_k; }, want, before, own_sum);
             listed = b >= 0 && before + own_sum <= SORT;
             if (b >= 0 && own_sum > SORT) cut_at(bisect(top_k, false));
             else if (b >= 0) {   // (otherwise fewer than k tokens: all are kept)
@@ -881,7 +897,7 @@ __global__ void __launch_bounds__(Cfg<M>::NT, Cfg<M>::PER_SM) k_sample(SampleArg
                 const u64 P = threshold(mass + block_sum(rest));
                 if (P <= mass) {
                     u64 want, before, own_sum, sum;
-                    const int at = find_bin([&](u64) { return P; }, want, before, own_sum);
+                    const int at = find_bin(std::true_type(), [&](u64) { return P; }, want, before, own_sum);
                     u64 *const some_of = reinterpret_cast<u64 *>(sm.h);   // the bin's entries
                     constexpr int ROOM = F::REP * 3 * BINS / 2 >= 2048 ? 2048 : 512;
                     for (int g = tid; g < NG; g += NT) sums[g] = 0;
@@ -947,7 +963,7 @@ __global__ void __launch_bounds__(Cfg<M>::NT, Cfg<M>::PER_SM) k_sample(SampleArg
         rest = block_sum(rest);
         if (tid < 3) sm.h[0][tid][BINS - 1] = tid == 0 ? (uint32_t)rest & 0x7fffu : tid == 1 ? (uint32_t)(rest >> 15) & 0x7fffu : (uint32_t)(rest >> 30);
         u64 P, before, own_sum;
-        const int b = find_bin(threshold, P, before, own_sum);
+        const int b = find_bin(std::true_type(), threshold, P, before, own_sum);
         // sums of what is kept in the bins before, candidates of the bin itself
         sum_groups([&](float v, int i, float y) {
             const int at = kept(v, i) ? bin(y) : BINS;
@@ -1105,7 +1121,7 @@ cudaError_t launch_rows(const SampleArgs &a, cudaStream_t s) {
     auto seg = [&](int C) { return ((a.V + 16 / (int)sizeof(T) - 1 + C - 1) / C + kGroup - 1) / kGroup * kGroup; };
     // The fewest CTAs a row whose segments let two of them share an SM; more where there are few rows.
     int C = 1;
-    while (C < 8 && smem_of<kCluster>(seg(C), sizeof(T)) > 115000) C *= 2;
+    while (C < 8 && smem_of<kCluster>(seg(C), sizeof(T)) > 115600) C *= 2;
     if (C > 1 && a.R >= kManyRows) return launch_as<T, kStream>(a, 1, seg(1), s);
     while (C < 8 && (long long)a.R * C <= num_sms() && seg(2 * C) >= 2048) C *= 2;
     if (C == 1 && a.V <= kSmallV) return launch_as<T, kSmall>(a, 1, seg(1), s);
