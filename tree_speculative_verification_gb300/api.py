@@ -340,12 +340,14 @@ class PagedKV:
         self.H, self.d, self.device = k_pages.shape[1], k_pages.shape[3], k_pages.get_device()
         self._whole = k_pages.is_cuda and all(x.is_contiguous() and x.device == k_pages.device
                                               for x in (k_pages, v_pages, block_table)) and block_table.dim() == 2
+        self.B = block_table.shape[0]
         self._c = ts_paged_kv(k_pages.data_ptr(), v_pages.data_ptr(), block_table.data_ptr(), k_pages.shape[0],
                               block_table.shape[1])
+        self._ref = C.byref(self._c)
 
     @property
     def c(self):
-        return C.byref(self._c)
+        return self._ref
 
     @property
     def L_max(self) -> int:
@@ -657,7 +659,7 @@ def kv_pages_build(pool: PagePool, row_end, row_begin=None, slot=None, slot_offs
 def _whole_pages(kv: PagedKV):
     if not kv._whole:
         raise TreespecError("pages and block table must be contiguous on one CUDA device")
-    return kv.c
+    return kv._ref
 
 
 def _token_rows(t, H, d, name, dtype, device):
@@ -695,7 +697,7 @@ def decode_workspace(B: int, Hq: int, Hkv: int, d: int, device="cuda"):
 def decode_attention_paged(out, q, kv: PagedKV, kv_len, scale: float = 0.0, ws=None, status=None, stream=None):
     """Attention of one new token a request to the first kv_len[b] rows of its pages; q, out [B][Hq][d] bfloat16, Hq a
     multiple of kv.H, the rows of q Hq * d apart or more."""
-    ref, dev, d, B = _whole_pages(kv), kv.device, kv.d, kv.block_table.shape[0]
+    ref, dev, d, B = _whole_pages(kv), kv.device, kv.d, kv.B
     if q.dim() != 3 or q.shape[0] != B:
         raise TreespecError(f"q must be [{B}][Hq][{d}]")
     Hq = q.shape[1]

@@ -71,159 +71,183 @@ __device__ Request request(const PageArgs &a, int b) {
 }
 
 // Entry k of the ring, k counted from its start and below three times round.
-__device__ __forceinline__ int ring_at(long long k, int num) {
+__device__ __forceinline__ int ring_at(int k, int num) {
     k -= k >= num ? num : 0;
-    return (int)(k - (k >= num ? num : 0));
+    return k - (k >= num ? num : 0);
 }
 
-// n ids from one place to another, by a warp: four loads under way a lane.
-template <typename From, typename To>
-__device__ __forceinline__ void move_ids(int n, From from, To to) {
-    for (int i = threadIdx.x & 31; i < n; i += 128) {
-        int id[4];
+// Of kPageThreads rising numbers the last one that is i or less (the first is).
+__device__ __forceinline__ int last_upto(const int *s, int i) {
+    int x = 0;
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-            if (i + 32 * k < n) id[k] = *from(i + 32 * k);
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-            if (i + 32 * k < n) *to(i + 32 * k) = id[k];
-    }
+    for (int step = kPageThreads / 2; step; step /= 2)
+        if (s[x + step] <= i) x += step;
+    return x;
 }
 
-__global__ void __launch_bounds__(kPageThreads) k_pages_build(PageArgs a) {
-    __shared__ Sums part[kPageThreads / 32];
-    __shared__ long long off_s[kPageThreads + 1];   // first slots of the tile's requests, and the tile's end
-    __shared__ int begin_s[kPageThreads], held_s[kPageThreads], want_s[kPageThreads], from_s[kPageThreads];
+__device__ __forceinline__ int clamped(long long v) { return (int)min(v, (long long)INT32_MAX); }
+
+// Rows, pages taken and pages given back each stand in one line, the requests' one after the other; every CTA takes an equal
+// stretch of each line and finds a stretch's requests by the running sums.
+__global__ void __launch_bounds__(kPageThreads, 2) k_pages_build(PageArgs a) {
+    __shared__ Sums part[kPageThreads / 32], all_s, tile_s;
+    __shared__ int row_s[kPageThreads + 1], take_s[kPageThreads + 1], back_s[kPageThreads + 1];   // a tile's requests' first ones
+    __shared__ int begin_s[kPageThreads], held_s[kPageThreads], want_s[kPageThreads];
     __shared__ bool ok_s[kPageThreads];
-    __shared__ unsigned long long taken_s;
-    __shared__ int last_s;
+    __shared__ int taken_s, last_s;
     const int tid = threadIdx.x, B = a.pool.B, num = a.pool.num_pages, width = a.pool.max_pages;
     int32_t *const ring = a.pool.ring, *const table = a.pool.block_table;
     pdl_wait();
     pdl_trigger();
     const int head = a.pool.ring_state[0], count = a.pool.ring_state[1];
-    // what comes back in all: with it the ring must not hold more than the pool's pages
     Request r = request(a, tid);
-    Sums all = r.own;
-    for (int b = tid + kPageThreads; b < B; b += kPageThreads) {
-        const Request x = request(a, b);
-        all.n += x.own.n, all.take += x.own.take, all.back += x.own.back;
-    }
     if (tid == 0) taken_s = 0;
-    all = block_sums(all, part);
+    // running sums over the first tile; of all requests (what comes back must not fill the ring beyond the pool's pages)
+    Sums run = block_sums(r.own, part), all = run;
+    if (B > kPageThreads) {
+        Sums more = r.own;
+        for (int b = tid + kPageThreads; b < B; b += kPageThreads) {
+            const Request x = request(a, b);
+            more.n += x.own.n, more.take += x.own.take, more.back += x.own.back;
+        }
+        all = block_sums(more, part);
+    }
+    if (tid == kPageThreads - 1) all_s = all;
     __syncthreads();
-    if (tid == kPageThreads - 1) part[0] = all;
-    __syncthreads();
-    all = part[0];
+    all = all_s;
     const bool pool_ok = head >= 0 && head < num && count >= 0 && count + all.back <= num;
-    const long long s0 = min((long long)blockIdx.x * a.per_cta, (long long)a.max_slots),
-                    s1 = min(s0 + a.per_cta, (long long)a.max_slots);
     uint32_t bits = 0;
     if (!pool_ok || (a.slot && all.n > a.max_slots)) bits |= TS_STATUS_INDEX;
+    // the CTA's stretches
+    const int c = blockIdx.x, ctas = gridDim.x;
+    const int s0 = (int)min((long long)c * a.per_cta, (long long)a.max_slots), s1 = (int)min((long long)s0 + a.per_cta, (long long)a.max_slots);
+    const int takes = (int)min(all.take, (long long)max(count, 0)), t_per = (takes + ctas - 1) / ctas, b_per = ((int)min(all.back, (long long)num) + ctas - 1) / ctas;
 
     Sums at = {};
+    bool ok = false;
     for (int base = 0; base < B; base += kPageThreads) {   // a tile of requests, a thread each
         const int b = base + tid;
-        if (base) r = request(a, b);
-        const Sums run = block_sums(r.own, part);
+        if (base) {
+            r = request(a, b);
+            run = block_sums(r.own, part);
+        }
         const long long first = at.n + run.n - r.own.n, from = at.take + run.take - r.own.take;
-        const bool ok = b < B && pool_ok && r.sound && (r.own.take == 0 || from + r.own.take <= count);
+        ok = b < B && pool_ok && r.sound && (r.own.take == 0 || from + r.own.take <= count);
         if (b < B && !r.sound) bits |= TS_STATUS_INDEX;
         if (b < B && pool_ok && r.sound && !ok) bits |= TS_STATUS_NO_PAGES;
-        if (ok && r.own.take) atomicMax(&taken_s, (unsigned long long)(from + r.own.take));
-        off_s[tid] = first, begin_s[tid] = r.begin, held_s[tid] = r.held, ok_s[tid] = ok;
-        want_s[tid] = r.sound ? (int)r.want : r.held;
-        // a request takes or gives back: where its first page comes from, or goes behind the ring's free part
-        from_s[tid] = !ok ? 0 : ring_at(head + (r.own.take ? from : count + at.back + run.back - r.own.back), num);
-        if (tid == kPageThreads - 1) off_s[kPageThreads] = first + r.own.n;
-        if (blockIdx.x == 0 && b < B && a.slot_offset) {
-            a.slot_offset[b] = (int)min(first, (long long)INT32_MAX);
-            if (b == B - 1) a.slot_offset[B] = (int)min(first + r.own.n, (long long)INT32_MAX);
+        if (ok && r.own.take) atomicMax(&taken_s, (int)(from + r.own.take));
+        row_s[tid] = clamped(first), take_s[tid] = clamped(from), back_s[tid] = clamped(at.back + run.back - r.own.back);
+        begin_s[tid] = r.begin, held_s[tid] = r.held, want_s[tid] = r.sound ? (int)r.want : r.held, ok_s[tid] = ok;
+        if (tid == kPageThreads - 1) {
+            row_s[kPageThreads] = clamped(first + r.own.n), take_s[kPageThreads] = clamped(from + r.own.take);
+            back_s[kPageThreads] = clamped(at.back + run.back);
+            tile_s = run;
+        }
+        if (c == 0 && b < B && a.slot_offset) {
+            a.slot_offset[b] = clamped(first);
+            if (b == B - 1) a.slot_offset[B] = clamped(first + r.own.n);
         }
         __syncthreads();
-        for (int i = tid >> 5; i < min(kPageThreads, B - base); i += kPageThreads / 32) {   // a warp a request
-            if ((base + i) % gridDim.x != blockIdx.x || !ok_s[i]) continue;
-            const int held = held_s[i], want = want_s[i], from_i = from_s[i];
-            int32_t *const row = table + (size_t)(base + i) * width;
-            auto in_ring = [&](int k) { return ring + ring_at((long long)from_i + k, num); };
-            move_ids(want - held, in_ring, [&](int k) { return row + held + k; });
-            move_ids(held - want, [&](int k) { return row + want + k; }, in_ring);
-        }
-        if (a.slot) {   // the tile's slots in this CTA's range, four a thread
-            const long long lo = max(s0, off_s[0]), hi = min(s1, off_s[kPageThreads]);
-            for (long long i0 = (lo & ~3LL) + 4 * tid; i0 < hi; i0 += 4 * kPageThreads) {
-                const long long i1 = max(i0, lo);
-                int x = 0, y = kPageThreads - 1, v[4];   // the last request whose first slot is not behind i1
-                while (x < y) {
-                    const int m = (x + y + 1) >> 1;
-                    if (off_s[m] <= i1) x = m;
-                    else y = m - 1;
-                }
-                int page = -1, p_now = -1;
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const long long i = i0 + e;
-                    v[e] = -1;
-                    if (i < lo || i >= hi) continue;
-                    while (off_s[x + 1] <= i) ++x, p_now = -1;
-                    if (!ok_s[x]) continue;
-                    const int j = begin_s[x] + (int)(i - off_s[x]), p = j / TS_PAGE_KEYS;
-                    if (p != p_now) {
-                        p_now = p;
-                        page = p < held_s[x] ? table[(size_t)(base + x) * width + p]
-                                             : ring[ring_at((long long)from_s[x] + (p - held_s[x]), num)];
-                        if (page < 0 || page >= num) page = -1, bits |= TS_STATUS_INDEX;
-                    }
-                    if (page >= 0) v[e] = page * TS_PAGE_KEYS + j % TS_PAGE_KEYS;
-                }
-                if (a.slot_vec && i0 >= lo && i0 + 4 <= hi)
-                    *reinterpret_cast<int4 *>(a.slot + i0) = make_int4(v[0], v[1], v[2], v[3]);
-                else
-                    for (int e = 0; e < 4; ++e)
-                        if (i0 + e >= lo && i0 + e < hi) a.slot[i0 + e] = v[e];
+        const Sums tile = tile_s;
+        if (pool_ok) {
+            // pages taken: as many of the line as are served, which are whole requests
+            const int t1 = min(min(take_s[kPageThreads], taken_s), (c + 1) * t_per);
+            for (int i = max(take_s[0], c * t_per) + tid; i < t1; i += kPageThreads) {
+                const int x = last_upto(take_s, i);
+                table[(size_t)(base + x) * width + held_s[x] + (i - take_s[x])] = ring[ring_at(head + i, num)];
+            }
+            // pages given back, behind the ring's free part
+            const int b1 = min(back_s[kPageThreads], (c + 1) * b_per);
+            for (int i = max(back_s[0], c * b_per) + tid; i < b1; i += kPageThreads) {
+                const int x = last_upto(back_s, i);
+                ring[ring_at(head + count + i, num)] = table[(size_t)(base + x) * width + want_s[x] + (i - back_s[x])];
             }
         }
-        __syncthreads();
-        if (tid == kPageThreads - 1) part[0] = run;
-        __syncthreads();
-        at.n += part[0].n, at.take += part[0].take, at.back += part[0].back;
+        if (a.slot) {   // slots, four a thread and two of these at once
+            const int lo = max(s0, row_s[0]), hi = min(s1, row_s[kPageThreads]);
+            // page p of the tile's request x: its own, or the ring's where it is taken only now
+            auto page_of = [&](int x, int p) {
+                return p < held_s[x] ? table[(size_t)(base + x) * width + p] : ring[ring_at(head + take_s[x] + (p - held_s[x]), num)];
+            };
+            for (long long j0 = (lo & ~3) + 4 * tid; j0 < hi; j0 += 8 * kPageThreads) {
+                int x[2], page[2], p_now[2];
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {   // the first slot's request and page
+                    const long long i0 = j0 + 4 * k * kPageThreads;
+                    x[k] = 0, p_now[k] = -1, page[k] = -1;
+                    if (i0 >= hi) continue;
+                    const int i = max((int)i0, lo);
+                    x[k] = last_upto(row_s, i);
+                    if (!ok_s[x[k]]) continue;
+                    p_now[k] = (begin_s[x[k]] + (i - row_s[x[k]])) / TS_PAGE_KEYS;
+                    page[k] = page_of(x[k], p_now[k]);
+                }
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const long long i0 = j0 + 4 * k * kPageThreads;
+                    if (i0 >= hi) continue;
+                    int v[4], y = x[k], p_y = p_now[k], page_y = page[k];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        v[e] = -1;
+                        const long long i = i0 + e;
+                        if (i < lo || i >= hi) continue;
+                        while (row_s[y + 1] <= i) ++y, p_y = -1;
+                        if (!ok_s[y]) continue;
+                        const int j = begin_s[y] + ((int)i - row_s[y]);
+                        if (j / TS_PAGE_KEYS != p_y) {
+                            p_y = j / TS_PAGE_KEYS;
+                            page_y = page_of(y, p_y);
+                        }
+                        if (page_y >= 0 && page_y < num) v[e] = page_y * TS_PAGE_KEYS + j % TS_PAGE_KEYS;
+                        else bits |= TS_STATUS_INDEX;
+                    }
+                    if (a.slot_vec && i0 >= lo && i0 + 4 <= hi)
+                        *reinterpret_cast<int4 *>(a.slot + i0) = make_int4(v[0], v[1], v[2], v[3]);
+                    else
+                        for (int e = 0; e < 4; ++e)
+                            if (i0 + e >= lo && i0 + e < hi) a.slot[i0 + e] = v[e];
+                }
+            }
+        }
+        at.n += tile.n, at.take += tile.take, at.back += tile.back;
+        if (base + kPageThreads < B) __syncthreads();   // shared memory is the next tile's
     }
     if (a.slot)
-        for (long long i = max(s0, at.n) + tid; i < s1; i += kPageThreads) a.slot[i] = -1;
+        for (long long i = max((long long)s0, at.n) + tid; i < s1; i += kPageThreads) a.slot[i] = -1;
     if (bits) flag(a.status, bits);
 
     // the last CTA to come here: every other one has read what is now written
     __syncthreads();
-    if (tid == 0) {
-        last_s = gridDim.x == 1;
-        if (gridDim.x > 1) {
+    if (ctas > 1) {
+        if (tid == 0) {
             __threadfence();
             unsigned *done = (unsigned *)a.pool.ring_state + 2;
-            last_s = atomicAdd(done, 1u) == gridDim.x - 1;
+            last_s = atomicAdd(done, 1u) == ctas - 1;
             if (last_s) *done = 0;
             __threadfence();
         }
+        __syncthreads();
+        if (!last_s) return;
     }
-    __syncthreads();
-    if (!last_s) return;
     long long take = 0;
     for (int base = 0; base < B; base += kPageThreads) {
         const int b = base + tid;
-        if (B > kPageThreads) r = request(a, b);
-        const Sums run = block_sums(r.own, part);
-        if (b < B) {
-            const bool ok = pool_ok && r.sound && (r.own.take == 0 || take + run.take <= count);
-            a.new_held[b] = ok ? (int)r.want : r.held;
+        if (B > kPageThreads) {
+            r = request(a, b);
+            run = block_sums(r.own, part);
+            ok = b < B && pool_ok && r.sound && (r.own.take == 0 || take + run.take <= count);
         }
-        __syncthreads();
-        if (tid == kPageThreads - 1) part[0] = run;
-        __syncthreads();
-        take += part[0].take;
+        if (b < B) a.new_held[b] = ok ? (int)r.want : r.held;
+        if (B > kPageThreads) {
+            if (tid == kPageThreads - 1) tile_s = run;
+            __syncthreads();
+            take += tile_s.take;
+        }
     }
     if (tid == 0) {
-        const long long taken = (long long)taken_s;
-        a.new_state[0] = pool_ok ? (int)((head + taken) % num) : head;
-        a.new_state[1] = pool_ok ? (int)(count - taken + all.back) : count;
+        a.new_state[0] = pool_ok ? ring_at(head + taken_s, num) : head;
+        a.new_state[1] = pool_ok ? (int)(count - taken_s + all.back) : count;
     }
 }
 
