@@ -1066,7 +1066,16 @@ __global__ void __launch_bounds__(kWalkThreads, 1) k_walk(int32_t *out_tokens, i
         const float Mw = mx * a2;
         const int x_first = (!NAIVE && c_first >= 0) ? sm.tok[c_first] : -1;
         float s = 0.f, cc = 0.f;
-        if (landed && !nf)
+        if (landed && !nf && fabsf(Mw) > 65536.f) {
+            // a range of masked tokens (-1e30, the lowest finite number): Mw's rounding, or its overflow, would be the exponent
+            for (int g = g0 + lane; g < g1; g += 32) {
+                float4 a = R4[g];
+                a.x = ex2((a.x - mx) * a2); a.y = ex2((a.y - mx) * a2);
+                a.z = ex2((a.z - mx) * a2); a.w = ex2((a.w - mx) * a2);
+                kahan(s, cc, (a.x + a.y) + (a.z + a.w));
+                R4[g] = a;
+            }
+        } else if (landed && !nf) {
             for (int g = g0 + lane; g < g1; g += 32) {
                 float4 a = R4[g];
                 a.x = ex2(__fmaf_rn(a.x, a2, -Mw)); a.y = ex2(__fmaf_rn(a.y, a2, -Mw));
@@ -1074,6 +1083,7 @@ __global__ void __launch_bounds__(kWalkThreads, 1) k_walk(int32_t *out_tokens, i
                 kahan(s, cc, (a.x + a.y) + (a.z + a.w));
                 R4[g] = a;
             }
+        }
         __syncwarp();
         if (lane == 0 && x_first >= 0 && (x_first >> 2) >= g0 && (x_first >> 2) < g1) sm.rx = R[x_first];
         if (tchild) {
