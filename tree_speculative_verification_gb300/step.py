@@ -5,6 +5,9 @@ logits, drafter probabilities, uniforms) and the output buffers, and runs the
 hot path: tree_build -> kv_append -> tree_attention -> verify (greedy and/or
 MSS, or naive sampling) -> kv_commit. kv_commit writes the new prefix lengths into a separate
 array, so repeating a step on the same inputs is idempotent.
+
+DecodeStep runs a step of one new token a request on a paged cache, from a pool
+of pages that it hands out and takes back.
 """
 from __future__ import annotations
 
@@ -297,3 +300,64 @@ class DeviceStep:
             append_rides = self._append_in_attention or (self._fused and kind == "greedy" and not self.serial_verify)
             n += len(name.split("+")) + 1 + (0 if append_rides else 1)
         return n
+
+
+class DecodeStep:
+    """Steps of one new token a request: kv_pages_build -> kv_append_slots -> decode_attention_paged -> sample_tokens, over a
+    pool of num_pages pages that B requests share (max_pages each at most).
+
+    len [B] is how many rows of each request are in the cache; a request of none takes no part in a step. begin() and end()
+    admit and drop requests, run() is a step and may be captured (its inputs stay where they are). A request for which the
+    pool has no page stays as long as it is, and attends without its new row (api.STATUS_NO_PAGES in status): drop another
+    and repeat it. temperature, top_k, top_p, min_p: tensors [B] or None, as for api.sample_tokens."""
+
+    def __init__(self, B: int, Hq: int, Hk: int, d: int, num_pages: int, max_pages: int, device="cuda", temperature=None,
+                 top_k=None, top_p=None, min_p=None):
+        z = lambda *s, t=torch.int32: torch.zeros(s, dtype=t, device=device)
+        pages = lambda: z(num_pages, Hk, api.PAGE_KEYS, d, t=torch.bfloat16)
+        self.pool = api.PagePool.empty(B, max_pages, num_pages, device)
+        self.kv = api.PagedKV(pages(), pages(), self.pool.block_table)
+        self.len, self.status = z(B), z(1)
+        self.temperature, self.top_k, self.top_p, self.min_p = temperature, top_k, top_p, min_p
+        self.out, self.token = z(B, Hq, d, t=torch.bfloat16), z(B)
+        self.slot, self._packed, self._offset = z(B), z(B), z(B + 1)
+        self.ws = api.decode_workspace(B, Hq, Hk, d, device)
+        self._end, self._room, self._none = z(B), z(B), z(B) - 1
+        self._part, self._served = z(B, t=torch.bool), z(B, t=torch.bool)
+
+    def _grow(self, end, slot, offset, stream):
+        """Pages and slots for rows len .. end - 1; len becomes end where the pool had the pages."""
+        api.kv_pages_build(self.pool, end, self.len, slot, offset, status=self.status, stream=stream)
+        torch.mul(self.pool.held, api.PAGE_KEYS, out=self._room)
+        torch.le(end, self._room, out=self._served)
+        torch.where(self._served, end, self.len, out=self.len)
+
+    def begin(self, lengths, k, v, stream=None):
+        """Rows k, v [T][Hk][d] of prompts, one request's after the other: lengths [B] of them, 0 for requests that stay as
+        they are."""
+        with torch.cuda.stream(stream or torch.cuda.current_stream(self.len.device)):
+            slot = torch.empty(k.shape[0], dtype=torch.int32, device=self.len.device)
+            self._grow(self.len + lengths, slot, None, stream)
+            api.kv_append_slots(self.kv, k, v, slot, self.status, stream)
+
+    def end(self, which, stream=None):
+        """Requests that are done, which [B] bool: their pages go back."""
+        with torch.cuda.stream(stream or torch.cuda.current_stream(self.len.device)):
+            self.len.masked_fill_(which, 0)
+            api.kv_pages_build(self.pool, self.len, status=self.status, stream=stream)
+
+    def run(self, q, k, v, logits, u, probs=None, kept=None, stream=None):
+        """A step: q [B][Hq][d], k and v [B][Hk][d] of the new tokens (bfloat16; slices of a projection's output), logits
+        [B][V], u [B] uniform numbers. out [B][Hq][d] is the attention's output, token [B] the next tokens; probs, kept
+        [B][V]: as for api.sample_tokens."""
+        with torch.cuda.stream(stream or torch.cuda.current_stream(self.len.device)):
+            torch.gt(self.len, 0, out=self._part)
+            torch.add(self.len, self._part, out=self._end)
+            self._grow(self._end, self._packed, self._offset, stream)
+            # slots stand one after the other; a request's own is where its first one is, if it takes part
+            torch.index_select(self._packed, 0, self._offset[:-1], out=self.slot)
+            torch.where(self._part, self.slot, self._none, out=self.slot)
+            api.kv_append_slots(self.kv, k, v, self.slot, self.status, stream)
+            api.decode_attention_paged(self.out, q, self.kv, self.len, ws=self.ws, status=self.status, stream=stream)
+            api.sample_tokens(self.token, logits, u, self.temperature, self.top_k, self.top_p, self.min_p, probs, kept,
+                              self.status, stream)
