@@ -530,7 +530,8 @@ typedef struct ts_page_pool {
  * A request with lengths that do not fit (row_begin < 0 or above row_end, more
  * than max_pages pages, held outside 0 .. max_pages) is left as it is, with slots
  * -1; so is every request where the ring's state does not fit num_pages, and rows
- * past max_slots get no slot (TS_STATUS_INDEX).
+ * past max_slots get no slot (TS_STATUS_INDEX). Calls on one pool must not overlap
+ * on the GPU, two captured graphs that hold them included.
  */
 ts_status kv_pages_build(const ts_page_pool *pool, int32_t *new_held, int32_t *new_state, int32_t *slot,
                          int max_slots, int32_t *slot_offset, const int32_t *row_begin, const int32_t *row_end,
@@ -543,7 +544,8 @@ ts_status kv_pages_build(const ts_page_pool *pool, int32_t *new_held, int32_t *n
  * k_stride / v_stride elements from one token to the next (at least H * d, a
  * multiple of 16 bytes). A slot of -1 is left out; any other that is not in the
  * pages too (TS_STATUS_INDEX). Slots are distinct: of a slot that stands twice,
- * each 16 bytes come from one of its rows, not said which. kv->block_table is not read.
+ * each 16 bytes come from one of its rows, not said which. The new rows must not
+ * overlap the pages. kv->block_table is not read.
  */
 ts_status kv_append_slots(const ts_paged_kv *kv, const void *k_new, const void *v_new, long long k_stride,
                           long long v_stride, const int32_t *slot, int T, int H, int d, uint32_t *status,
@@ -556,13 +558,16 @@ ts_status kv_append_slots(const ts_paged_kv *kv, const void *k_new, const void *
  * among the kv_len[b]. q [B] rows of Hq heads, q_stride elements apart (as for
  * tree_qk_norm_rope), out [B][Hq][d]; bf16, Hq a multiple of Hkv. Softmax and
  * sums are fp32. scale <= 0 selects 1/sqrt(d).
- * kv_len 0 gives zeros. A request with kv_len outside 0 .. max_pages *
- * TS_PAGE_KEYS keeps its rows of out (TS_STATUS_INDEX); a page id outside
- * [0, num_pages) reads as zeros (TS_STATUS_INDEX). Rows from kv_len on may hold
- * anything. ws: at least treespec_decode_workspace_size(...) bytes, zero-filled
- * before its first use (treespec_workspace_init); calls leave what must be zero
- * so, and may be of several sizes. Calls that share one ws must not overlap on
- * the GPU, two captured graphs that hold them included.
+ * out must not overlap q. kv_len 0 gives zeros. A request with kv_len outside
+ * 0 .. max_pages * TS_PAGE_KEYS keeps its rows of out (TS_STATUS_INDEX); a page id
+ * outside [0, num_pages) reads as zeros (TS_STATUS_INDEX). Rows from kv_len on may
+ * hold anything. Where the requests' pages, times Hkv and blocks of 16 query heads
+ * a key/value head (of 8 where these are 8 or fewer), are 2^31 or more in all, only
+ * the zeros of kv_len 0 are written (TS_STATUS_INDEX). ws: at least
+ * treespec_decode_workspace_size(...) bytes, zero-filled before its first use
+ * (treespec_workspace_init); calls leave what must be zero so, and may be of several
+ * sizes. Calls that share one ws must not overlap on the GPU, two captured graphs
+ * that hold them included.
  */
 ts_status decode_attention_paged(void *out, const void *q, long long q_stride, const ts_paged_kv *kv,
                                  const int32_t *kv_len, int B, int Hq, int Hkv, int d, float scale, void *ws,
@@ -591,7 +596,8 @@ size_t treespec_decode_workspace_size(int B, int Hq, int Hkv, int d);
  *   kept   [R][V] fp32 (may be NULL; may be the logits where these are fp32, V
  *          apart): the logits of the kept tokens, TS_DROPPED_LOGIT elsewhere; target
  *          rows for verify_mss at the same temperature
- * Weights are counted in units of 2^-40 of the largest, and summed exactly.
+ * Weights are counted in units of 2^-36 of the largest (a token below 2^-37 of it
+ * may have none), and summed exactly.
  * A row with NaN or +inf, or with nothing but -inf (TS_STATUS_NONFINITE), or with
  * u or a setting out of its range (NaN, T negative or infinite, top_k negative;
  * TS_STATUS_INDEX) gets token -1 and its rows of probs and kept NaN, which a

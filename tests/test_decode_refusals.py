@@ -34,7 +34,8 @@ def pages(**kw):
     (dict(pool=pool(B=0)), b"B="), (dict(pool=pool(B=65536)), b"B="), (dict(pool=pool(num_pages=0)), b"num_pages"),
     (dict(pool=pool(num_pages=1 << 25)), b"num_pages"), (dict(pool=pool(max_pages=0)), b"max_pages"),
     (dict(end=None), b"NULL"), (dict(new_held=None), b"NULL"), (dict(new_state=None), b"NULL"), (dict(begin=None), b"row_begin"),
-    (dict(n=0), b"max_slots"), (dict(slot=None), b"slot_offset"),
+    (dict(n=0), b"max_slots"), (dict(slot=None), b"slot_offset"), (dict(slot=P(0x10002)), b"4-byte"),
+    (dict(pool=pool(held=0x10001)), b"4-byte"), (dict(end=P(0x10002)), b"4-byte"),
 ])
 def test_pages_refusals(lib, kw, word):
     a = {**dict(pool=pool(), new_held=OK, new_state=OK, slot=OK, n=8, off=OK, begin=OK, end=OK), **kw}
@@ -49,7 +50,7 @@ BAD_PAGES = [(dict(kv=None), 1, b"NULL"), (dict(kv=pages(k_pages=None)), 1, b"NU
 @pytest.mark.parametrize("kw,rc,word", BAD_PAGES + [
     (dict(kv=pages(num_pages=1 << 25)), 1, b"num_pages"), (dict(T=0), 1, b"T="), (dict(slot=None), 1, b"slot"), (dict(k=None), 1, b"k_new"),
     (dict(v=BAD), 1, b"v_new"), (dict(ks=511), 1, b"stride"), (dict(vs=504), 1, b"stride"), (dict(ks=516), 1, b"stride"),
-    (dict(vs=(1 << 31) + 8), 1, b"stride")])
+    (dict(vs=(1 << 31) + 8), 1, b"stride"), (dict(slot=P(0x10002)), 1, b"4-byte")])
 def test_append_refusals(lib, kw, rc, word):
     a = {**dict(kv=pages(), k=OK, v=OK, ks=512, vs=512, slot=OK, T=3, H=4, d=128), **kw}
     got = lib.kv_append_slots(a["kv"], a["k"], a["v"], a["ks"], a["vs"], a["slot"], a["T"], a["H"], a["d"], None, None)
@@ -61,9 +62,10 @@ def test_append_refusals(lib, kw, rc, word):
     (dict(n=None), 1, b"NULL"), (dict(out=BAD), 1, b"out"), (dict(q=BAD), 1, b"q must"), (dict(q=None), 1, b"q is NULL"),
     (dict(Hq=6), 1, b"multiple"), (dict(Hq=0), 1, b"multiple"), (dict(B=0), 1, b"B="), (dict(B=65536), 1, b"B="), (dict(qs=1000), 1, b"stride"),
     (dict(qs=1028), 1, b"stride"), (dict(scale=float("inf")), 1, b"scale"), (dict(scale=3e38), 1, b"scale"), (dict(ws=None), 1, b"workspace"),
-    (dict(wn=16), 1, b"workspace"), (dict(ws=BAD), 1, b"workspace")])
+    (dict(wn=16), 1, b"workspace"), (dict(ws=BAD), 1, b"workspace"), (dict(out=OK), 1, b"place of its own"),
+    (dict(n=P(0x10001)), 1, b"4-byte")])
 def test_attention_refusals(lib, kw, rc, word):
-    a = {**dict(out=OK, q=OK, qs=1024, kv=pages(), n=OK, B=2, Hq=8, H=4, d=128, scale=0.0, ws=OK, wn=1 << 40), **kw}
+    a = {**dict(out=P(0x20000), q=OK, qs=1024, kv=pages(), n=OK, B=2, Hq=8, H=4, d=128, scale=0.0, ws=OK, wn=1 << 40), **kw}
     got = lib.decode_attention_paged(a["out"], a["q"], a["qs"], a["kv"], a["n"], a["B"], a["Hq"], a["H"], a["d"], a["scale"], a["ws"],
                                      a["wn"], None, None)
     assert got == rc and word in lib.treespec_last_error() and b"decode_attention_paged" in lib.treespec_last_error()
@@ -74,7 +76,8 @@ def test_attention_refusals(lib, kw, rc, word):
     (dict(R=0), b"R="), (dict(V=0), b"V="), (dict(V=(1 << 18) + 1, stride=1 << 20), b"V="), (dict(stride=99), b"stride"),
     (dict(stride=(1 << 31) + 1), b"stride"), (dict(token=None), b"no output"), (dict(u=None), b"needs u"),
     (dict(probs=OK), b"place of its own"), (dict(probs=P(0x30000), kept=P(0x30000)), b"place of its own"),
-    (dict(kept=OK, dt=1), b"place"), (dict(kept=OK, stride=101), b"place")])
+    (dict(kept=OK, dt=1), b"place"), (dict(kept=OK, stride=101), b"place"), (dict(probs=P(0x30002)), b"4-byte"),
+    (dict(u=P(0x30001)), b"4-byte"), (dict(token=P(0x30002)), b"4-byte")])
 def test_sample_refusals(lib, kw, word):
     a = {**dict(token=P(0x20000), probs=None, kept=None, logits=OK, stride=100, dt=0, u=OK, R=2, V=100), **kw}
     rc = lib.sample_tokens(a["token"], a["probs"], a["kept"], a["logits"], a["stride"], a["dt"], a["u"], None, None, None, None, a["R"],
@@ -111,7 +114,7 @@ def test_calls_that_pass_without_a_device(lib):
         for T in (1, 2000):
             assert lib.kv_append_slots(pages(), OK, OK, 1024, 1024, OK, T, 4, d, None, None) == api.TS_ERR_CUDA
         for Hq in (4, 32, 64, 128):
-            assert lib.decode_attention_paged(OK, OK, 128 * Hq, pages(), OK, 2, Hq, 4, d, 0.0, OK, 1 << 40, None, None) == api.TS_ERR_CUDA
+            assert lib.decode_attention_paged(X, OK, 128 * Hq, pages(), OK, 2, Hq, 4, d, 0.0, OK, 1 << 40, None, None) == api.TS_ERR_CUDA
     for dt in (0, 1):
         for V in (1, 300, 32001, 50272, 1 << 18):
             for R in (1, 100, 5000):

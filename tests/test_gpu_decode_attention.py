@@ -218,3 +218,18 @@ def test_agrees_with_tree_attention_of_one_node():
     api.tree_attention_paged(ref, q[:, None].contiguous(), c.kv, cu([n - 1 for n in lens]), t,
                              ws=api.workspace(api.TS_OP_ATTENTION, 3, 4, 1, 128, L, 1))
     assert (out.float() - ref[:, 0].float()).abs().max() < 2e-2
+
+
+def test_more_tiles_than_32_bits_count():
+    """2^31 tiles in all: told, and only the rows without a key are written (no page is read)."""
+    B, H, d, pages = 16385, 256, 64, 512
+    kv = api.PagedKV(torch.zeros(1, H, PK, d, dtype=torch.bfloat16, device="cuda"), torch.zeros(1, H, PK, d, dtype=torch.bfloat16, device="cuda"),
+                     torch.zeros(B, pages, dtype=torch.int32, device="cuda"))
+    lens = torch.full((B,), pages * PK, dtype=torch.int32, device="cuda")
+    lens[77] = 0
+    q = torch.zeros(B, H, d, dtype=torch.bfloat16, device="cuda")
+    out = torch.ones_like(q)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    api.decode_attention_paged(out, q, kv, lens, 0.0, api.decode_workspace(B, H, H, d), status)
+    assert status.item() == api.STATUS_INDEX
+    assert not out[77].any() and (out[:77] == 1).all() and (out[78:] == 1).all()

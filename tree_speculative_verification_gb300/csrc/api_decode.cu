@@ -16,6 +16,13 @@ ts_status done(cudaError_t e, const char *who) {
 
 bool aligned(const void *p, unsigned n) { return ((uintptr_t)p & (n - 1)) == 0; }
 
+// Arrays of 32-bit numbers; a NULL one is as good as aligned.
+template <typename... P>
+ts_status check_words(const char *who, P... p) {
+    if ((... && aligned(p, 4))) return TS_OK;
+    return set_error(TS_ERR_INVALID_ARG, "%s: an array of 32-bit numbers is not 4-byte aligned", who);
+}
+
 ts_status check_pages(const ts_paged_kv *kv, int H, int d, const char *who) {
     if (!kv) return set_error(TS_ERR_INVALID_ARG, "%s: cache is NULL", who);
     if (!kv->k_pages || !kv->v_pages) return set_error(TS_ERR_INVALID_ARG, "%s: pages are NULL", who);
@@ -58,6 +65,9 @@ ts_status kv_pages_build(const ts_page_pool *pool, int32_t *new_held, int32_t *n
     if (slot && (max_slots < 1 || !row_begin))
         return set_error(TS_ERR_INVALID_ARG, "%s: slots need row_begin and max_slots >= 1 (%d)", who, max_slots);
     if (slot_offset && !slot) return set_error(TS_ERR_INVALID_ARG, "%s: slot_offset without slots", who);
+    const ts_status st = check_words(who, pool->block_table, pool->held, pool->ring, pool->ring_state, new_held, new_state,
+                                     slot, slot_offset, row_begin, row_end, status);
+    if (st) return st;
     return done(ts::launch_pages_build(*pool, new_held, new_state, slot, slot ? max_slots : 0, slot_offset,
                                        slot ? row_begin : nullptr, row_end, status, stream),
                 who);
@@ -73,7 +83,7 @@ ts_status kv_append_slots(const ts_paged_kv *kv, const void *k_new, const void *
     if (T < 1) return set_error(TS_ERR_INVALID_ARG, "%s: T=%d must be >= 1", who, T);
     if (!slot) return set_error(TS_ERR_INVALID_ARG, "%s: slot is NULL", who);
     if ((st = check_stride(k_new, (long long)H * d, k_stride, "k_new", who)) ||
-        (st = check_stride(v_new, (long long)H * d, v_stride, "v_new", who)))
+        (st = check_stride(v_new, (long long)H * d, v_stride, "v_new", who)) || (st = check_words(who, slot, status)))
         return st;
     return done(ts::launch_append_slots(*kv, k_new, v_new, k_stride, v_stride, slot, T, H, d, status, stream), who);
 }
@@ -90,7 +100,10 @@ ts_status decode_attention_paged(void *out, const void *q, long long q_stride, c
     if (!aligned(out, 16)) return set_error(TS_ERR_INVALID_ARG, "%s: out must be 16-byte aligned", who);
     if (!decode_sizes_ok(B, Hq, Hkv, d))
         return set_error(TS_ERR_INVALID_ARG, "%s: B=%d, Hq=%d (a multiple of Hkv=%d), B * Hq below 2^31", who, B, Hq, Hkv);
-    if ((st = check_stride(q, (long long)Hq * d, q_stride, "q", who))) return st;
+    if ((st = check_stride(q, (long long)Hq * d, q_stride, "q", who)) ||
+        (st = check_words(who, kv_len, kv->block_table, status)))
+        return st;
+    if (out == q) return set_error(TS_ERR_INVALID_ARG, "%s: out needs a place of its own", who);
     if (!(scale > 0.f)) scale = 1.0f / sqrtf((float)d);
     if (!(scale * 1.4426950408889634f < INFINITY))   // scores are exponents of 2
         return set_error(TS_ERR_INVALID_ARG, "%s: scale is not finite, or its product with log2(e) is not", who);
@@ -124,6 +137,8 @@ ts_status sample_tokens(int32_t *token, float *probs, float *kept, const void *l
         return set_error(TS_ERR_INVALID_ARG, "%s: probs needs a place of its own", who);
     if ((const void *)kept == logits && (dtype != TS_F32 || row_stride != V))
         return set_error(TS_ERR_INVALID_ARG, "%s: kept in the logits' place only where these are fp32, V apart", who);
+    const ts_status st = check_words(who, token, probs, kept, u, temperature, top_k, top_p, min_p, status);
+    if (st) return st;
     const ts::SampleArgs a{token, probs, kept,  logits, row_stride, u, temperature,
                            top_k, top_p, min_p, R,      V,          status};
     return done(ts::launch_sample(a, dtype, stream), who);
