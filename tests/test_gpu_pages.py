@@ -192,3 +192,16 @@ def test_rows_past_32_bits():
     for p in (kv.k_pages, kv.v_pages):
         assert torch.equal(p[-1, :, 63], x[0]) and torch.equal(p[0, :, 1], x[1])
         assert not p[-1, :, :63].any() and not p[0, :, 2:].any() and not p[0, :, 0].any()
+
+
+def test_most_slots_there_can_be():
+    """A slot array of 2^31 - 1 entries: the last request's rows, and -1 on to the end."""
+    n, B = 2 ** 31 - 1, 3
+    pool = device_pool(Pages(np.zeros((B, 4), dtype=np.int64), [0] * B, [3, 1, 2, 0], 4))
+    slot = torch.full((n,), -9, dtype=torch.int32, device="cuda")
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    api.kv_pages_build(pool, cu([64, 1, 2]), cu([0, 0, 0]), slot, None, status=status)
+    assert status.item() == 0
+    assert slot[:64].tolist() == list(range(192, 256)) and slot[64:67].tolist() == [64, 128, 129]
+    for at in range(67, n, 1 << 28):
+        assert int(slot[at:at + (1 << 28)].max()) == -1 and int(slot[at:at + (1 << 28)].min()) == -1

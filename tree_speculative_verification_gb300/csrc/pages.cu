@@ -169,7 +169,7 @@ __global__ void __launch_bounds__(kPageThreads, 2) k_pages_build(PageArgs a) {
             auto page_of = [&](int x, int p) {
                 return p < held_s[x] ? table[(size_t)(base + x) * width + p] : ring[ring_at(head + take_s[x] + (p - held_s[x]), num)];
             };
-            for (long long j0 = (lo & ~3) + 4 * tid; j0 < hi; j0 += 8 * kPageThreads) {
+            for (long long j0 = (lo & ~3LL) + 4 * tid; j0 < hi; j0 += 8 * kPageThreads) {
                 int x[2], page[2], p_now[2];
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {   // the first slot's request and page
@@ -269,7 +269,7 @@ __global__ void __launch_bounds__(kSlotThreads) k_append_slots(uint4 *k_pages, u
         int at[TB];
 #pragma unroll
         for (int i = 0; i < TB; ++i)
-            if (t0 + i < T) {
+            if (i < T - t0) {
                 at[i] = slot[t0 + i];
                 k[i] = __ldcs(k_new + (t0 + i) * k_stride + p);
                 v[i] = __ldcs(v_new + (t0 + i) * v_stride + p);
@@ -277,8 +277,8 @@ __global__ void __launch_bounds__(kSlotThreads) k_append_slots(uint4 *k_pages, u
         const int h = p >> vec_log2, c = p & ((1 << vec_log2) - 1);
 #pragma unroll
         for (int i = 0; i < TB; ++i) {
-            if (t0 + i >= T || at[i] < 0) {
-                if (t0 + i < T && at[i] < -1 && p == 0) flag(status, TS_STATUS_INDEX);
+            if (i >= T - t0 || at[i] < 0) {
+                if (i < T - t0 && at[i] < -1 && p == 0) flag(status, TS_STATUS_INDEX);
                 continue;
             }
             const int page = at[i] / TS_PAGE_KEYS, row = at[i] % TS_PAGE_KEYS;
@@ -301,7 +301,7 @@ cudaError_t launch_pages_build(const ts_page_pool &pool, int32_t *new_held, int3
     PageArgs a{pool, new_held, new_state, slot, slot_offset, row_begin, row_end, slot ? max_slots : 0, 0,
                ((uintptr_t)slot & 15) == 0, status};
     const int ctas = (int)std::min<long long>(2LL * num_sms(), 1 + (long long)a.max_slots / (8 * kPageThreads));
-    a.per_cta = ((a.max_slots + ctas - 1) / ctas + 3) / 4 * 4;
+    a.per_cta = (int)(((long long)a.max_slots + ctas - 1) / ctas + 3) / 4 * 4;
     return launch(k_pages_build, dim3(ctas), dim3(kPageThreads), 0, s, a);
 }
 
@@ -310,7 +310,7 @@ cudaError_t launch_append_slots(const ts_paged_kv &kv, const void *k_new, const 
                                 cudaStream_t s) {
     const int vec_log2 = d == 128 ? 4 : 3;
     auto go = [&](auto kern, int tb) {
-        return launch(kern, dim3((T + tb - 1) / tb), dim3(kSlotThreads), 0, s, (uint4 *)kv.k_pages, (uint4 *)kv.v_pages,
+        return launch(kern, dim3(T / tb + (T % tb != 0)), dim3(kSlotThreads), 0, s, (uint4 *)kv.k_pages, (uint4 *)kv.v_pages,
                       (const uint4 *)k_new, (const uint4 *)v_new, k_stride / 8, v_stride / 8, slot, T, H, vec_log2,
                       (int)kv.num_pages, status);
     };
