@@ -119,10 +119,10 @@ def check_attention(cache, q, out, lens, scale=None):
         assert worst <= 1.0, f"request {b}: error {worst:.2f} of its tolerance"
 
 
-# Whole-number weights are off by 2^-41 of the largest each. Large ones (from 2^-8 of the largest on) by 2^-38 of themselves;
-# small ones by up to 2^-20 (roundings of an exponent of some 16 and of 2^x), as often up as down: their sum by a standard
-# deviation of 2^-20 sqrt(sum w^2) <= 2^-20 sqrt(2^-8 sum w), and as the whole sum is 1 at least, by less than 2^-22 of that
-# within four of these.
+# Weights are whole numbers of 2^-36 of the largest, so off by 2^-37 each, as often up as down: 2^18 of them by 2^-26 of the
+# largest within four standard deviations. Large ones (from 2^-6 of the largest on) by 2^-38 of themselves more; small ones
+# by up to 2^-20 (roundings of an exponent of some 16 and of 2^x), as often up as down: their sum by a standard deviation of
+# 2^-21 sqrt(sum w^2) <= 2^-21 sqrt(2^-6 sum w), and as the whole sum is 1 at least, by 2^-22 of that within four of these.
 SUM_OFF = 2.0 ** -22
 
 
@@ -157,7 +157,7 @@ def check_sample(logits, u, T, k, p, m, token, probs=None, kept=None):
         got_n = None
         if probs is not None:
             got_n = int((probs[r] > 0).sum())
-            # what underflows fp32 or has no weight in 2^-40 may be kept and read 0
+            # what underflows fp32 or has no weight in 2^-36 may be kept and read 0
             if not lo <= got_n <= hi:
                 q = w[:hi] / w[:hi].sum()
                 assert lo > got_n >= int((q > 1e-35).sum()), f"row {r}: {got_n} kept, {lo}..{hi} expected"

@@ -101,15 +101,16 @@ __device__ __forceinline__ u64 fma2(u64 a, u64 b, u64 c) {
 constexpr float kLarge = -6.f, kUnits = 68719476736.f;
 struct Weights {
     float top, ch, cl;   // log2(e) / T = ch + cl, 0 < cl < 2^-22 ch: -inf stays -inf in both products
+    float by;            // of x, top and T: 1, or 2^-64 where T is above 2^100, so that no difference that counts overflows
     __device__ __forceinline__ float exponent(float x) const {
-        const float d = x - top;
+        const float d = fmaf(x, by, -top);
         return fmaf(d, ch, d * cl);
     }
     __device__ __forceinline__ void exponents(const float (&x)[4], float (&y)[4]) const {   // the same of four
-        const u64 t = two(-top, -top), h = two(ch, ch), l = two(cl, cl);
+        const u64 b = two(by, by), t = two(-top, -top), h = two(ch, ch), l = two(cl, cl);
 #pragma unroll
         for (int e = 0; e < 4; e += 2) {
-            const u64 d = add2(two(x[e], x[e + 1]), t);
+            const u64 d = fma2(two(x[e], x[e + 1]), b, t);
             one_each(fma2(d, h, mul2(d, l)), y[e], y[e + 1]);
         }
     }
@@ -121,14 +122,15 @@ struct Weights {
         return whole((ex2(y[0]) + ex2(y[1])) + (ex2(y[2]) + ex2(y[3])));
     }
     __device__ __forceinline__ void exponent(float x, float &yh, float &yl) const {
+        x *= by;
         const float dh = x - top, bb = dh - x, dl = (x - (dh - bb)) - (top + bb);
         yh = dh * ch;
         yl = fmaf(dh, ch, -yh) + fmaf(dh, cl, dl * ch);
     }
-    __device__ __noinline__ static u64 large(float x, float top, float ch, float cl) {   // (not inlined: it is for few)
+    __device__ __noinline__ static u64 large(float x, float top, float ch, float cl) {   // of x times by (not inlined: it is for few)
         if (x == top) return 1ull << 36;
         float yh, yl;
-        Weights{top, ch, cl}.exponent(x, yh, yl);
+        Weights{top, ch, cl, 1.f}.exponent(x, yh, yl);
         const float n8 = rintf(yh * 8.f), f = fmaf(n8, -0.125f, yh);
         const float gh = f + yl, gl = yl - (gh - f);
         const float L = 0.693147182464599609375f, Ll = -1.904654299957767e-09f;   // ln 2
@@ -146,7 +148,7 @@ struct Weights {
     }
     __device__ __forceinline__ u64 operator()(float x) const {
         const float y = exponent(x);
-        return y >= kLarge ? large(x, top, ch, cl) : light(y);
+        return y >= kLarge ? large(x * by, top, ch, cl) : light(y);
     }
     // Weights as floats, the largest `one`, to some 2^-21 of themselves.
     __device__ __forceinline__ float real(float x, float one) const {
@@ -155,10 +157,10 @@ struct Weights {
         return yh > -150.f ? ex2(yh) * fmaf(yl, 0.693147182f, 1.f) * one : 0.f;
     }
     __device__ __forceinline__ void real4(const float (&x)[4], float one, float (&p)[4]) const {
-        const u64 t = two(-top, -top), h = two(ch, ch), l = two(cl, cl), minus = two(-1.f, -1.f);
+        const u64 b = two(by, by), t = two(-top, -top), h = two(ch, ch), l = two(cl, cl), minus = two(-1.f, -1.f);
 #pragma unroll
         for (int e = 0; e < 4; e += 2) {
-            const u64 v = two(x[e], x[e + 1]), d = add2(v, t), bb = fma2(v, minus, d),
+            const u64 v = mul2(two(x[e], x[e + 1]), b), d = add2(v, t), bb = fma2(v, minus, d),
                       low = add2(fma2(fma2(bb, minus, d), minus, v), fma2(bb, minus, t));   // d + low = x - top
             const u64 y = mul2(d, h), yl = add2(fma2(d, h, mul2(y, minus)), fma2(d, l, mul2(low, h)));
             float y0, y1, f0, f1;
@@ -254,8 +256,9 @@ __global__ void __launch_bounds__(Cfg<M>::NT, Cfg<M>::PER_SM) k_sample(SampleArg
                 min_p = a.min_p ? a.min_p[r] : 0.f, u = a.u ? a.u[r] : 0.f;
     const int top_k = a.top_k ? a.top_k[r] : 0;
     const bool greedy = temp < 7.888609052210118e-31f;   // 2^-100
+    const float by = temp > 1.2676506002282294e30f ? 5.421010862427522e-20f : 1.f;   // 2^-64 above 2^100
     if (tid == 0) {   // (64-bit arithmetic is slow enough here that one thread does it for all)
-        const double c = 1.4426950408889634 / (greedy ? 1.0 : (double)temp);
+        const double c = 1.4426950408889634 / (greedy ? 1.0 : (double)(temp * by));
         sm.ch = __double2float_rd(c);
         sm.cl = fmaxf((float)(c - (double)sm.ch), fmaxf(sm.ch * 9.3132257e-10f, 1.4e-45f));
         if (min_p > 0.f) {
@@ -325,7 +328,7 @@ __global__ void __launch_bounds__(Cfg<M>::NT, Cfg<M>::PER_SM) k_sample(SampleArg
     if (bound) {
         some = 0.f;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) some += own[e] > -INFINITY ? ex2((own[e] - top) * ch) : 0.f;
+        for (int e = 0; e < 4; ++e) some += own[e] > -INFINITY ? ex2((own[e] - top) * by * ch) : 0.f;
 #pragma unroll
         for (int o = 16; o; o >>= 1) some += __shfl_xor_sync(~0u, some, o);
         __syncthreads();
@@ -347,7 +350,7 @@ __global__ void __launch_bounds__(Cfg<M>::NT, Cfg<M>::PER_SM) k_sample(SampleArg
     for (int c = 0; c < C; ++c) {
         const float t = __uint_as_float((uint32_t)sm.from[0][c]), x = __uint_as_float((uint32_t)(sm.from[0][c] >> 32));
         bad |= isnan(x);
-        if (t > -INFINITY) some += x * ex2((t - top) * ch);
+        if (t > -INFINITY) some += x * ex2((t - top) * by * ch);
     }
     bad |= top == -INFINITY;
     const bool wrong =
@@ -391,7 +394,7 @@ __global__ void __launch_bounds__(Cfg<M>::NT, Cfg<M>::PER_SM) k_sample(SampleArg
         sync();
         return;
     }
-    const Weights weight{top, ch, sm.cl};
+    const Weights weight{top * by, ch, sm.cl, by};
     // tokens below this are not kept: min-p (the sum rounded up), and -inf
     float low = -3.402823466e38f;
     if (min_p > 0.f && !greedy) {
@@ -868,7 +871,8 @@ __global__ void __launch_bounds__(Cfg<M>::NT, Cfg<M>::PER_SM) k_sample(SampleArg
             // (of 50000 tokens that are alike, some 5300)
             const int b = sample_bin(4 * NT * 37 / 40);
             u64 rest = 0;
-            const float from = fminf(top - (b + 1) / vscale, top + (kLarge - 0.01f) / ch);   // (no large ones are left out)
+            // (no large ones are left out, and what is no token is not in it)
+            const float from = fmaxf(low, fminf(top - (b + 1) / vscale, top + (kLarge - 0.01f) / (by * ch)));
             if (b >= 0 && vscale > 0.f)
                 n_list = gather(from, [&](const float (&x)[4]) {
                     float y[4];
@@ -1061,6 +1065,7 @@ __global__ void __launch_bounds__(Cfg<M>::NT, Cfg<M>::PER_SM) k_sample(SampleArg
                 if (k_to) k_to[id] = x;
             }
         } else {
+            if (STREAM) __syncthreads();   // (the same: the token's group may still be read)
 #pragma unroll 4
             for (int v = tid; v < SL / 4; v += NT) {
                 float x[4], y[4];
