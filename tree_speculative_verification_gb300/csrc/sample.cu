@@ -285,6 +285,7 @@ __global__ void __launch_bounds__(Cfg<M>::NT, Cfg<M>::PER_SM) k_sample(SampleArg
             bad |= !(f[e] < INFINITY);
             own[e] = fmaxf(own[e], f[e]);
         }
+        return fmaxf(fmaxf(f[0], f[1]), fmaxf(f[2], f[3]));
     };
     const int odd = STREAM ? v_lo * VE + max(0, V + lead - v_hi * VE) : SL - (v_hi - v_lo) * VE;
     for (int i = tid; i < odd; i += NT) {
@@ -294,17 +295,31 @@ __global__ void __launch_bounds__(Cfg<M>::NT, Cfg<M>::PER_SM) k_sample(SampleArg
         bad |= !((float)x < INFINITY);
         own[0] = fmaxf(own[0], (float)x);
     }
+    // the largest of every 32 pieces (as key_of); the ends of the row, which are not all pieces, count as the largest there is
+    uint32_t *const most_of = reinterpret_cast<uint32_t *>(sums);
+    constexpr int CG = 32 * VE / kGroup;   // groups that one stands for
     if constexpr (STREAM) {
-        for (int v0 = v_lo + tid; v0 < v_hi; v0 += 4 * NT) {
+        const int chunks = (NG + CG - 1) / CG;
+        for (int c0 = warp; c0 < chunks; c0 += 4 * W) {
             uint4 x[4];
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-                if (v0 + k * NT < v_hi) x[k] = pieces[v0 + k * NT];
+            for (int k = 0; k < 4; ++k) {
+                const int v = (c0 + k * W) * 32 + lane;
+                if (v >= v_lo && v < v_hi) x[k] = pieces[v];
+            }
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-                if (v0 + k * NT < v_hi)
+            for (int k = 0; k < 4; ++k) {
+                const int chunk = c0 + k * W, v = chunk * 32 + lane;
+                if (chunk >= chunks) break;
+                float most = INFINITY;
+                if (v >= v_lo && v < v_hi) {
+                    most = -INFINITY;
 #pragma unroll
-                    for (int i = 0; i < VE; i += 4) look(reinterpret_cast<const T *>(&x[k]) + i);
+                    for (int i = 0; i < VE; i += 4) most = fmaxf(most, look(reinterpret_cast<const T *>(&x[k]) + i));
+                }
+                const uint32_t key = __reduce_max_sync(~0u, key_of(most));
+                if (lane == 0) most_of[chunk] = key;
+            }
         }
     } else {
         asm volatile("cp.async.wait_all;" ::: "memory");
@@ -449,6 +464,39 @@ __global__ void __launch_bounds__(Cfg<M>::NT, Cfg<M>::PER_SM) k_sample(SampleArg
                 if (g + W < NG) get4((g + W) * kGroup + lane * 4, next);
                 f(g, x, base + g * kGroup + lane * 4 - lead);
             }
+        }
+    };
+    // The groups that may have a value from `from` on, where the largest ones are known and tell few.
+    auto high_groups = [&](float from, auto f) {
+        if constexpr (STREAM) {
+            const uint32_t key = key_of(from);
+            auto high = [&](int j0) {   // of the warp's groups warp + j W those of j0 .. j0 + 31
+                const int g = warp + (j0 + lane) * W;
+                return __ballot_sync(~0u, g < NG && most_of[g / CG] >= key);
+            };
+            int n = 0;
+            for (int j0 = 0; warp + j0 * W < NG; j0 += 32) n += __popc(high(j0));
+            if (2 * n * W <= NG)
+                for (int j0 = 0; warp + j0 * W < NG; j0 += 32)
+                    for (unsigned m = high(j0); m;) {
+                        constexpr int U = 4;   // at once
+                        float x[U][4];
+                        int g[U];
+#pragma unroll
+                        for (int q = 0; q < U; ++q) {
+                            g[q] = -1;
+                            if (!m) continue;
+                            g[q] = warp + (j0 + __ffs(m) - 1) * W;
+                            m &= m - 1;
+                            get4(g[q] * kGroup + lane * 4, x[q]);
+                        }
+#pragma unroll
+                        for (int q = 0; q < U; ++q)
+                            if (g[q] >= 0) f(g[q], x[q], g[q] * kGroup + lane * 4 - lead);
+                    }
+            else groups(f);
+        } else {
+            groups(f);
         }
     };
     // Weights by groups, of the elements that take(value, id, y) says: small(y[4]) has those below kLarge and -inf for the
@@ -636,22 +684,22 @@ __global__ void __launch_bounds__(Cfg<M>::NT, Cfg<M>::PER_SM) k_sample(SampleArg
         sync();
         return all;
     };
-    // All tokens from a value on into the list: their number, above LIST where they do not fit. others(x) sees every four.
-    // A long row's threads note each their own by place, and then put them in one line.
-    auto gather = [&](float from, auto others) {
+    // All tokens from a value on into the list, by way of every four or the high groups' (each): their number, above LIST where
+    // they do not fit. others(x) sees what is visited. A long row's threads note each their own by place, and then put them
+    // in one line.
+    auto gather = [&](float from, auto each, auto others) {
         if constexpr (STREAM)
             if (NG <= 64 * W) {
                 constexpr int MOST = sizeof(sm.h) / NT;
                 uint8_t *const notes = reinterpret_cast<uint8_t *>(sm.h) + tid;   // (the histogram is empty after reset())
-                int n = 0, turn_no = 0;
-                groups([&](int, const float (&x)[4], int) {
+                int n = 0;
+                each([&](int g, const float (&x)[4], int) {
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
                         if (x[e] >= from) {
-                            if (n < MOST) notes[n * NT] = (uint8_t)(turn_no * 4 + e);
+                            if (n < MOST) notes[n * NT] = (uint8_t)(g / W * 4 + e);
                             ++n;
                         }
-                    ++turn_no;
                     others(x);
                 });
                 const bool over = __syncthreads_or(n > MOST);
@@ -668,7 +716,7 @@ __global__ void __launch_bounds__(Cfg<M>::NT, Cfg<M>::PER_SM) k_sample(SampleArg
                 __syncthreads();
                 return all;
             }
-        groups([&](int, const float (&x)[4], int id) {
+        each([&](int, const float (&x)[4], int id) {
             if (__any_sync(~0u, fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])) >= from)) push4(x, id, [&](int e) { return x[e] >= from; });
             others(x);
         });
@@ -750,6 +798,53 @@ __global__ void __launch_bounds__(Cfg<M>::NT, Cfg<M>::PER_SM) k_sample(SampleArg
         }
     };
 
+    // Of the list's n entries up to `most` in the order, all from a value on: the last one of the shortest start that reaches
+    // want_of(their number or mass); 0 where none does. A histogram and its bin's entries, so that a long list is not sorted.
+    auto choose = [&](int n, u64 most, float from, auto masses, auto want_of) {
+        reset();   // (the list stays)
+        const float bottom = weight.exponent(from) - 0.01f, scale = (BINS - 1) / bottom;
+        auto bin = [&](float x) {
+            return min(BINS - 1, __float_as_int(fmaf(weight.exponent(x), scale, 12582912.f)) & (2 * BINS - 1));
+        };
+        uint32_t(*const h)[BINS] = sm.h[masses ? warp % F::REP : 0];
+        for (int i = tid; i < n; i += NT) {
+            const u64 e = sm.list[i];
+            if (e > most) continue;
+            const float x = value_at(e);
+            const int at = bin(x);
+            if constexpr (masses) {
+                const u64 w = weight(x);
+                atomicAdd(&h[0][at], (uint32_t)w & 0x7fffu);
+                atomicAdd(&h[1][at], (uint32_t)(w >> 15) & 0x7fffu);
+                if (w >> 30) atomicAdd(&h[2][at], (uint32_t)(w >> 30));
+            } else {
+                atomicAdd(&h[0][at], 1u);
+            }
+        }
+        u64 want, before, own_sum, sum;
+        const int at = find_bin(masses, want_of, want, before, own_sum);
+        if (at < 0) return 0ull;
+        u64 *const some_of = reinterpret_cast<u64 *>(sm.h);   // the bin's entries
+        constexpr int ROOM = 2048;
+        static_assert(ROOM * 8 <= sizeof(sm.h) || !STREAM);
+        for (int i = tid; i < n; i += NT) {
+            const u64 e = sm.list[i];
+            if (e <= most && bin(value_at(e)) == at) {
+                const int k = atomicAdd(&sm.n_list, 1);
+                if (k < ROOM) some_of[k] = e;
+            }
+        }
+        __syncthreads();
+        const int m = sm.n_list;
+        if (m > ROOM) {
+            cut_at(min(most, order_of(key_of(from), (1 << kIdBits) - 1)));
+            return bisect(want, masses);
+        }
+        sort(some_of, m);
+        if constexpr (masses) return some_of[kept_of(some_of, m, before, [&](u64) { return want; }, sum) - 1];
+        else return some_of[(int)(want - before) - 1];
+    };
+
     const bool by_p = top_p < 1.f && !greedy, by_k = top_k > 0 && top_k < V && !greedy;
     u64 S = 0;                // the sum of all kept weights
     bool listed = false;      // all kept tokens are in the list,
@@ -775,7 +870,7 @@ __global__ void __launch_bounds__(Cfg<M>::NT, Cfg<M>::PER_SM) k_sample(SampleArg
     };
     if (greedy) {
         u64 first = ~0ull;
-        groups([&](int, const float (&x)[4], int id) {
+        high_groups(top, [&](int, const float (&x)[4], int id) {
 #pragma unroll
             for (int e = 3; e >= 0; --e)
                 if (x[e] == top) first = min(first, order_of(key_of(top), id + e));
@@ -794,13 +889,15 @@ __global__ void __launch_bounds__(Cfg<M>::NT, Cfg<M>::PER_SM) k_sample(SampleArg
     } else if (by_k || min_p > 0.f) {
         // ---- top-k and min-p
         u64 want, before = 0, own_sum = 0;
+        float list_from = low;
         int b = -1;
         if (by_k && top_k < SORT && top_k <= 2 * NT * C) b = sample_bin(top_k);
         if (b >= 0 || min_p > 0.f) {
             // no lower than any value of the bins up to b
             const float from = b < 0 || vscale == 0.f ? low : fmaxf(low, top - (b + 1) / vscale * 1.00001f - fabsf(top) * 1e-6f);
-            n_list = gather(from, [](const float (&)[4]) {});
-            listed = n_list <= SORT;
+            n_list = gather(from, [&](auto f) { high_groups(from, f); }, [](const float (&)[4]) {});
+            listed = n_list <= LIST;
+            list_from = from;
         }
         if (by_k && !listed) {   // bins of every token: all candidates in the k-th one's, with the bins above it where they fit
             reset();
@@ -811,6 +908,7 @@ __global__ void __launch_bounds__(Cfg<M>::NT, Cfg<M>::PER_SM) k_sample(SampleArg
             });
             b = find_bin(std::false_type(), [&](u64) { return (u64)top_k; }, want, before, own_sum);
             listed = b >= 0 && before + own_sum <= SORT;
+            if (listed) list_from = vscale == 0.f ? low : fmaxf(low, top - (b + 1) / vscale * 1.00001f - fabsf(top) * 1e-6f);
             if (b >= 0 && own_sum > SORT) cut_at(bisect(top_k, false));
             else if (b >= 0) {   // (otherwise fewer than k tokens: all are kept)
                 groups([&](int, const float (&x)[4], int id) {
@@ -827,7 +925,19 @@ __global__ void __launch_bounds__(Cfg<M>::NT, Cfg<M>::PER_SM) k_sample(SampleArg
                 }
             }
         }
-        if (listed) {
+        if (STREAM && listed && n_list > NT) {
+            // ---- a long list's
+            last = ~0ull;
+            if (by_k && n_list > top_k) last = choose(n_list, last, list_from, std::false_type(), [&](u64) { return (u64)top_k; });
+            if (last == 0) last = ~0ull;   // (min-p keeps fewer)
+            if (by_p) last = choose(n_list, last, list_from, std::true_type(), threshold);
+            if (by_k || by_p) cut_at(last);
+            __syncthreads();
+            for (int g = tid; g < NG; g += NT) sums[g] = 0;
+            __syncthreads();
+            add_listed(sm.list, n_list, last);
+            summed = true;
+        } else if (listed) {
             // ---- the list's kept entries, in the cluster's first CTA; and the token, if they are few, by every entry's thread
             if (rank == 0) {
                 int n = n_list;
@@ -874,7 +984,7 @@ __global__ void __launch_bounds__(Cfg<M>::NT, Cfg<M>::PER_SM) k_sample(SampleArg
             // (no large ones are left out, and what is no token is not in it)
             const float from = fmaxf(low, fminf(top - (b + 1) / vscale, top + (kLarge - 0.01f) / (by * ch)));
             if (b >= 0 && vscale > 0.f)
-                n_list = gather(from, [&](const float (&x)[4]) {
+                n_list = gather(from, groups, [&](const float (&x)[4]) {
                     float y[4];
                     weight.exponents(x, y);
 #pragma unroll
@@ -882,47 +992,17 @@ __global__ void __launch_bounds__(Cfg<M>::NT, Cfg<M>::PER_SM) k_sample(SampleArg
                         if (x[e] >= from) y[e] = -INFINITY;
                     rest += Weights::light4(y);
                 });
+            rest = block_sum(rest);
             if (b >= 0 && vscale > 0.f && n_list <= LIST) {
-                reset();   // (the list stays)
-                const float bottom = weight.exponent(from) - 0.01f, scale = (BINS - 1) / bottom;
-                auto bin = [&](float y) { return min(BINS - 1, __float_as_int(fmaf(y, scale, 12582912.f)) & (2 * BINS - 1)); };
-                uint32_t(*const h)[BINS] = sm.h[warp % F::REP];
-                u64 mass = 0;
-                for (int i = tid; i < n_list; i += NT) {
-                    const float x = value_at(sm.list[i]);
-                    const u64 w = weight(x);
-                    const int at = bin(weight.exponent(x));
-                    mass += w;
-                    atomicAdd(&h[0][at], (uint32_t)w & 0x7fffu);
-                    atomicAdd(&h[1][at], (uint32_t)(w >> 15) & 0x7fffu);
-                    if (w >> 30) atomicAdd(&h[2][at], (uint32_t)(w >> 30));
-                }
-                mass = block_sum(mass);
-                const u64 P = threshold(mass + block_sum(rest));
-                if (P <= mass) {
-                    u64 want, before, own_sum, sum;
-                    const int at = find_bin(std::true_type(), [&](u64) { return P; }, want, before, own_sum);
-                    u64 *const some_of = reinterpret_cast<u64 *>(sm.h);   // the bin's entries
-                    constexpr int ROOM = F::REP * 3 * BINS / 2 >= 2048 ? 2048 : 512;
-                    for (int g = tid; g < NG; g += NT) sums[g] = 0;
-                    for (int i = tid; i < n_list; i += NT)
-                        if (bin(weight.exponent(value_at(sm.list[i]))) == at) {
-                            const int k = atomicAdd(&sm.n_list, 1);
-                            if (k < ROOM) some_of[k] = sm.list[i];
-                        }
-                    __syncthreads();
-                    const int n = sm.n_list;
-                    if (n <= ROOM) {
-                        sort(some_of, n);
-                        last = some_of[kept_of(some_of, n, before, [&](u64) { return P; }, sum) - 1];
-                    } else {
-                        last = bisect(P, true);
-                    }
-                    cut_at(last);
-                    for (int i = tid; i < n_list; i += NT)
-                        if (sm.list[i] <= last) atomicAdd(&sums[(id_of(sm.list[i]) + lead) / kGroup], weight(value_at(sm.list[i])));
-                    listed = summed = true;
-                }
+                last = choose(n_list, ~0ull, from, std::true_type(), [&](u64 mass) { return threshold(mass + rest); });
+                listed = last != 0;
+            }
+            if (listed) {
+                cut_at(last);
+                for (int g = tid; g < NG; g += NT) sums[g] = 0;
+                __syncthreads();
+                add_listed(sm.list, n_list, last);
+                summed = true;
             }
             if (!listed) reset();
         }
