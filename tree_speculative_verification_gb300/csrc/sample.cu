@@ -501,7 +501,7 @@ __global__ void __launch_bounds__(Cfg<M>::NT, Cfg<M>::PER_SM) k_sample(SampleArg
     };
     // Weights by groups, of the elements that take(value, id, y) says: small(y[4]) has those below kLarge and -inf for the
     // others; large(place, y, weight) those that a warp puts off until it has 32 or no more groups, as one such element
-    // among 32 takes as long as 32. before(group) and after(group) frame a group.
+    // among 32 takes as long as 32. before(group, x[4], y[4]) and after(group) frame a group.
     auto weigh = [&](auto before, auto take, auto small, auto large, auto after) {
         auto *const put_off = sm.larges[warp];
         int n = 0;
@@ -517,8 +517,8 @@ __global__ void __launch_bounds__(Cfg<M>::NT, Cfg<M>::PER_SM) k_sample(SampleArg
         };
         groups([&](int g, const float (&x)[4], int id) {
             float y[4];
-            before(g);
             weight.exponents(x, y);
+            before(g, x, y);
 #pragma unroll
             for (int e = 0; e < 4; ++e)
                 if (!take(x[e], id + e, y[e])) y[e] = -INFINITY;
@@ -539,10 +539,13 @@ __global__ void __launch_bounds__(Cfg<M>::NT, Cfg<M>::PER_SM) k_sample(SampleArg
         if (n > 32) settle(n - 32);
         if (n) settle(0);
     };
-    // the sums of the groups' weights
-    auto sum_groups = [&](auto take) {
+    // the sums of the groups' weights; see(group, x[4], y[4]) looks at all
+    auto sum_groups_and = [&](auto see, auto take) {
         uint32_t w = 0;
-        weigh([&](int g) { if (lane == 0) sums[g] = 0; }, take, [&](const float (&y)[4]) { w = Weights::light4(y); },
+        weigh([&](int g, const float (&x)[4], const float (&y)[4]) {
+            if (lane == 0) sums[g] = 0;
+            see(g, x, y);
+        }, take, [&](const float (&y)[4]) { w = Weights::light4(y); },
               [&](int pos, float, u64 one) { atomicAdd(&sums[pos / kGroup], one); },
               [&](int g) {
             if (!__any_sync(~0u, w != 0)) return;
@@ -551,6 +554,7 @@ __global__ void __launch_bounds__(Cfg<M>::NT, Cfg<M>::PER_SM) k_sample(SampleArg
             if (lane == 0) sums[g] += all;
         });
     };
+    auto sum_groups = [&](auto take) { sum_groups_and([](int, const float (&)[4], const float (&)[4]) {}, take); };
     // the CTA's sum, for every thread
     auto block_sum = [&](u64 v) {
 #pragma unroll
@@ -684,37 +688,42 @@ __global__ void __launch_bounds__(Cfg<M>::NT, Cfg<M>::PER_SM) k_sample(SampleArg
         sync();
         return all;
     };
+    // A long row's threads note the candidates each their own by place, and then put them in one line.
+    constexpr int MOST = sizeof(sm.h) / NT;   // a thread's
+    const bool by_notes = STREAM && NG <= 64 * W;
+    uint8_t *const notes = reinterpret_cast<uint8_t *>(sm.h) + tid;   // (no histogram is in use meanwhile)
+    int n_notes = 0;
+    auto note = [&](int g, int e) {
+        if (n_notes < MOST) notes[n_notes * NT] = (uint8_t)(g / W * 4 + e);
+        ++n_notes;
+    };
+    auto noted = [&] {
+        const bool over = __syncthreads_or(n_notes > MOST);
+        const int end = (int)block_scan(n_notes), at = end - n_notes;
+        if (tid == NT - 1) sm.n_list = end;
+        __syncthreads();
+        const int all = sm.n_list;
+        if (over || all > LIST) return LIST + 1;
+#pragma unroll 4
+        for (int k = 0; k < n_notes; ++k) {
+            const int one = notes[k * NT], id = (warp + (one >> 2) * W) * kGroup + lane * 4 + (one & 3) - lead;
+            sm.list[at + k] = order_of(key_of((float)row[id]), id);
+        }
+        __syncthreads();
+        return all;
+    };
     // All tokens from a value on into the list, by way of every four or the high groups' (each): their number, above LIST where
-    // they do not fit. others(x) sees what is visited. A long row's threads note each their own by place, and then put them
-    // in one line.
+    // they do not fit. others(x) sees what is visited.
     auto gather = [&](float from, auto each, auto others) {
         if constexpr (STREAM)
-            if (NG <= 64 * W) {
-                constexpr int MOST = sizeof(sm.h) / NT;
-                uint8_t *const notes = reinterpret_cast<uint8_t *>(sm.h) + tid;   // (the histogram is empty after reset())
-                int n = 0;
+            if (by_notes) {
                 each([&](int g, const float (&x)[4], int) {
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
-                        if (x[e] >= from) {
-                            if (n < MOST) notes[n * NT] = (uint8_t)(g / W * 4 + e);
-                            ++n;
-                        }
+                        if (x[e] >= from) note(g, e);
                     others(x);
                 });
-                const bool over = __syncthreads_or(n > MOST);
-                const int end = (int)block_scan(n), at = end - n;
-                if (tid == NT - 1) sm.n_list = end;
-                __syncthreads();
-                const int all = sm.n_list;
-                if (over || all > LIST) return LIST + 1;
-#pragma unroll 4
-                for (int k = 0; k < n; ++k) {
-                    const int note = notes[k * NT], id = (warp + (note >> 2) * W) * kGroup + lane * 4 + (note & 3) - lead;
-                    sm.list[at + k] = order_of(key_of((float)row[id]), id);
-                }
-                __syncthreads();
-                return all;
+                return noted();
             }
         each([&](int, const float (&x)[4], int id) {
             if (__any_sync(~0u, fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])) >= from)) push4(x, id, [&](int e) { return x[e] >= from; });
@@ -798,13 +807,14 @@ __global__ void __launch_bounds__(Cfg<M>::NT, Cfg<M>::PER_SM) k_sample(SampleArg
         }
     };
 
-    // Of the list's n entries up to `most` in the order, all from a value on: the last one of the shortest start that reaches
-    // want_of(their number or mass); 0 where none does. A histogram and its bin's entries, so that a long list is not sorted.
-    auto choose = [&](int n, u64 most, float from, auto masses, auto want_of) {
+    // Of the list's n entries up to `most` in the order, all from one value down to another (`ahead` of them the tokens of more
+    // than that): the last one of the shortest start that reaches want_of(their number or mass); 0 where none does. A histogram
+    // and its bin's entries, so that a long list is not sorted.
+    auto choose = [&](int n, u64 most, float to, float from, u64 ahead, auto masses, auto want_of) {
         reset();   // (the list stays)
-        const float bottom = weight.exponent(from) - 0.01f, scale = (BINS - 1) / bottom;
+        const float y0 = weight.exponent(to), scale = (BINS - 1) / (weight.exponent(from) - y0 - 0.01f);
         auto bin = [&](float x) {
-            return min(BINS - 1, __float_as_int(fmaf(weight.exponent(x), scale, 12582912.f)) & (2 * BINS - 1));
+            return min(BINS - 1, __float_as_int(fmaf(weight.exponent(x) - y0, scale, 12582912.f)) & (2 * BINS - 1));
         };
         uint32_t(*const h)[BINS] = sm.h[masses ? warp % F::REP : 0];
         for (int i = tid; i < n; i += NT) {
@@ -838,7 +848,7 @@ __global__ void __launch_bounds__(Cfg<M>::NT, Cfg<M>::PER_SM) k_sample(SampleArg
         const int m = sm.n_list;
         if (m > ROOM) {
             cut_at(min(most, order_of(key_of(from), (1 << kIdBits) - 1)));
-            return bisect(want, masses);
+            return bisect(ahead + want, masses);
         }
         sort(some_of, m);
         if constexpr (masses) return some_of[kept_of(some_of, m, before, [&](u64) { return want; }, sum) - 1];
@@ -868,6 +878,62 @@ __global__ void __launch_bounds__(Cfg<M>::NT, Cfg<M>::PER_SM) k_sample(SampleArg
         const int b = find_bin(std::false_type(), [&](u64) { return number; }, want, before, own_sum);
         return b < BINS - 1 ? b : -1;
     };
+    // Values between which the last token kept by top-p alone lies, most likely: from the largest of each quarter of a thread's
+    // elements, which tell the number of tokens above a value where that is small (of n, none is with (1 - f)^n), and from a
+    // sample of all where it is not. Right is what is then counted; an estimate that is off costs time. Counts of the tokens
+    // from lo on and from hi on.
+    struct Range {
+        float lo, hi;
+        int n_lo, n_hi;
+    };
+    auto estimate = [&] {
+        Range z{low, top, 1 << 30, 0};
+        if constexpr (STREAM) {
+            constexpr float FIX = 65536.f, EIGHTHS = 8.f;
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (own[e] >= low) atomicAdd(&sm.h[0][0][vbin(own[e])], 1u);
+            const int chunks = (v_hi + 31) / 32;
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const int v = (4 * warp + 2 * k + 1) * chunks / (4 * W) * 32 + lane;
+                if (v < v_lo || v >= v_hi) continue;
+                const uint4 x = pieces[v];
+#pragma unroll
+                for (int i = 0; i < VE; i += 4) {
+                    float f[4];
+                    load4(reinterpret_cast<const T *>(&x) + i, f);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) atomicAdd(&sm.h[0][1][vbin(f[e])], 1u);
+                }
+            }
+            __syncthreads();
+            const u64 both = sm.h[0][0][tid] | (u64)sm.h[0][1][tid] << 32, run = block_scan(both);   // (a bin a thread)
+            if (tid == NT - 1) sm.total = run;
+            if (tid == 0) sm.at = -1, sm.n_kept = 0;
+            __syncthreads();
+            const float samples = fmaxf(1.f, (float)(uint32_t)(sm.total >> 32));
+            auto share = [&](u64 r) { return 1.f - ex2(__log2f(fmaxf(1.f - (float)(uint32_t)r / (4 * NT), 1e-6f)) * (4.f * NT) / V); };
+            const float f = (uint32_t)run < 3 * NT ? share(run) - share(run - both) : (float)(uint32_t)(both >> 32) / samples;
+            const float n = f * V, mass = n * ex2(-(tid + 0.5f) / vscale * by * ch);
+            // mass and number in one sum
+            const u64 mine = (u64)(mass * FIX) << 24 | (u64)(n * EIGHTHS), upto = block_scan(mine), ahead = upto - mine;
+            if (tid == NT - 1) sm.total = upto;
+            __syncthreads();
+            const float S = (float)(sm.total >> 24), p = fminf(fmaxf(top_p, 0.f), 1.f), off = fminf(0.02f, 0.15f * fminf(p, 1.f - p));
+            const float m0 = (float)(ahead >> 24), m1 = (float)(upto >> 24);
+            if (m0 < (p + off) * S && (p + off) * S <= m1) sm.at = tid, sm.above = upto & 0xffffff;
+            if (m0 < (p - off) * S && (p - off) * S <= m1) sm.n_kept = tid, sm.kept = ahead & 0xffffff;
+            __syncthreads();
+            if (sm.at >= 0) {
+                z.lo = top - (sm.at + 1) / vscale, z.n_lo = (int)sm.above / 8;
+                z.hi = top - sm.n_kept / vscale, z.n_hi = sm.n_kept ? (int)sm.kept / 8 : 0;
+            }
+            __syncthreads();
+        }
+        return z;
+    };
+    bool cut_found = false;
     if (greedy) {
         u64 first = ~0ull;
         high_groups(top, [&](int, const float (&x)[4], int id) {
@@ -928,9 +994,9 @@ __global__ void __launch_bounds__(Cfg<M>::NT, Cfg<M>::PER_SM) k_sample(SampleArg
         if (STREAM && listed && n_list > NT) {
             // ---- a long list's
             last = ~0ull;
-            if (by_k && n_list > top_k) last = choose(n_list, last, list_from, std::false_type(), [&](u64) { return (u64)top_k; });
+            if (by_k && n_list > top_k) last = choose(n_list, last, top, list_from, 0, std::false_type(), [&](u64) { return (u64)top_k; });
             if (last == 0) last = ~0ull;   // (min-p keeps fewer)
-            if (by_p) last = choose(n_list, last, list_from, std::true_type(), threshold);
+            if (by_p) last = choose(n_list, last, top, list_from, 0, std::true_type(), threshold);
             if (by_k || by_p) cut_at(last);
             __syncthreads();
             for (int g = tid; g < NG; g += NT) sums[g] = 0;
@@ -977,36 +1043,65 @@ __global__ void __launch_bounds__(Cfg<M>::NT, Cfg<M>::PER_SM) k_sample(SampleArg
     }
     if constexpr (STREAM)
         if (bound && by_p) {
-            // ---- top-p alone: a few thousand largest in the list, the others' sum; where they reach top_p, the rest is done on them
-            // (of 50000 tokens that are alike, some 5300)
-            const int b = sample_bin(4 * NT * 37 / 40);
+            // ---- top-p alone, where the cut lies between two values: the list has the tokens between them, or all from the lower
+            // one on where these fit too; what is above and below is only summed
+            constexpr int FITS = LIST * 4 / 5;
+            Range z = vscale > 0.f ? estimate() : Range{low, top, 1 << 30, 0};
+            z.lo = fmaxf(low, fminf(z.lo, top + (kLarge - 0.01f) / (by * ch)));   // (no large ones are left out, and only tokens are in)
             u64 rest = 0;
-            // (no large ones are left out, and what is no token is not in it)
-            const float from = fmaxf(low, fminf(top - (b + 1) / vscale, top + (kLarge - 0.01f) / (by * ch)));
-            if (b >= 0 && vscale > 0.f)
-                n_list = gather(from, groups, [&](const float (&x)[4]) {
+            auto rest_of = [&](const float (&x)[4], const float (&y)[4]) {
+                float w[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) w[e] = x[e] >= z.lo ? -INFINITY : y[e];
+                rest += Weights::light4(w);
+            };
+            if (z.n_lo <= FITS) {
+                n_list = gather(z.lo, groups, [&](const float (&x)[4]) {
                     float y[4];
                     weight.exponents(x, y);
+                    rest_of(x, y);
+                });
+                rest = block_sum(rest);
+                if (n_list <= LIST) {
+                    last = choose(n_list, ~0ull, top, z.lo, 0, std::true_type(), [&](u64 mass) { return threshold(mass + rest); });
+                    listed = cut_found = last != 0;
+                }
+                if (listed) {
+                    for (int g = tid; g < NG; g += NT) sums[g] = 0;
+                    __syncthreads();
+                }
+            } else if (z.n_lo - z.n_hi <= FITS) {
+                sum_groups_and([&](int g, const float (&x)[4], const float (&y)[4]) {
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
-                        if (x[e] >= from) y[e] = -INFINITY;
-                    rest += Weights::light4(y);
-                });
-            rest = block_sum(rest);
-            if (b >= 0 && vscale > 0.f && n_list <= LIST) {
-                last = choose(n_list, ~0ull, from, std::true_type(), [&](u64 mass) { return threshold(mass + rest); });
-                listed = last != 0;
+                        if (x[e] >= z.lo && x[e] <= z.hi) {
+                            if (by_notes) note(g, e);
+                            else push(x[e], g * kGroup + lane * 4 + e - lead);
+                        }
+                    rest_of(x, y);
+                }, [&](float v, int, float) { return v > z.hi; });
+                rest = block_sum(rest);
+                u64 above = 0;
+                for (int g = tid; g < NG; g += NT) above += sums[g];
+                above = block_sum(above);
+                n_list = by_notes ? noted() : sm.n_list;
+                if (n_list <= LIST) {
+                    last = choose(n_list, ~0ull, z.hi, z.lo, above, std::true_type(), [&](u64 mass) {
+                        const u64 P = threshold(above + mass + rest);
+                        return P > above ? P - above : ~0ull;
+                    });
+                    cut_found = last != 0;
+                }
             }
-            if (listed) {
+            if (cut_found) {
                 cut_at(last);
-                for (int g = tid; g < NG; g += NT) sums[g] = 0;
-                __syncthreads();
                 add_listed(sm.list, n_list, last);
                 summed = true;
+            } else {
+                reset();
             }
-            if (!listed) reset();
         }
-    if (by_p && !listed) {
+    if (by_p && !listed && !cut_found) {
         if (by_k || min_p > 0.f) reset();
         // ---- top-p: exact sums of weights in equal bins of the exponent; tokens so light that all of them together make
         // less than 1 - top_p of the whole are only added up
@@ -1041,9 +1136,9 @@ __global__ void __launch_bounds__(Cfg<M>::NT, Cfg<M>::PER_SM) k_sample(SampleArg
             rest += Weights::light4(z);
         };
         auto count1 = [&](int, float y, u64 w) { count(y, w); };
-        auto nothing = [](int) {};
-        if (bound) weigh(nothing, all_of_them, count4, count1, nothing);
-        else weigh(nothing, kept_of_them, count4, count1, nothing);
+        auto nothing = [](int, const float (&)[4], const float (&)[4]) {};
+        if (bound) weigh(nothing, all_of_them, count4, count1, [](int) {});
+        else weigh(nothing, kept_of_them, count4, count1, [](int) {});
         rest = block_sum(rest);
         if (tid < 3) sm.h[0][tid][BINS - 1] = tid == 0 ? (uint32_t)rest & 0x7fffu : tid == 1 ? (uint32_t)(rest >> 15) & 0x7fffu : (uint32_t)(rest >> 30);
         u64 P, before, own_sum;
