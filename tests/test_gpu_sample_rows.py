@@ -187,3 +187,22 @@ def test_outputs_alone(dtype, V):
         got, status = run(x, u, want=name, **kw)
         assert status == 0 and torch.equal(got[name], all_of[name])
     check_some(x, u, list(range(20)), want="token", **kw)
+
+
+def test_rows_do_not_depend_on_one_another():
+    """A row's results are the same whatever rows stand beside it: settings in other orders, more rows than are put in order."""
+    R, V = 2100, 30001
+    x, u = logits(R, V, 6), uniforms(R)
+    rng = np.random.default_rng(3)
+    kw = dict(T=rng.choice([0.0, 0.7, 1.0, 1.3], R), k=rng.choice([0, 0, 1, 50, 1000, 5000, V], R), p=rng.choice([0.5, 0.9, 0.99, 1.0], R),
+              m=rng.choice([0.0, 0.0, 0.05], R))
+    whole, status = run(x, u, **kw)
+    assert status == 0
+    for rows in (slice(0, 700), slice(700, 2100), slice(5, 108)):
+        got, _ = run(x[rows], u[rows], **{n: v[rows] for n, v in kw.items()})
+        for n in whole:
+            assert torch.equal(got[n], whole[n][rows])
+    back = np.arange(699, -1, -1)
+    got, _ = run(x[:700].flip(0), u[back], **{n: v[back] for n, v in kw.items()})
+    for n in whole:
+        assert torch.equal(got[n].flip(0), whole[n][:700])

@@ -45,7 +45,8 @@ constexpr int kGroup = 128;       // elements of a warp's turn: a sum of weights
 constexpr int kLarges = 64;       // places of large weights that a warp puts off
 constexpr int kManyRows = 100;    // from which rows that no one CTA holds are read again from L2
 constexpr int kSmallV = 4096;
-constexpr int kRing = 3;           // groups of a warp in shared memory or on their way there, where rows are read again
+constexpr int kOrderedRows = 2048;   // up to so many rows are taken in an order of their settings
+constexpr int kRing = 4;           // groups of a warp in shared memory or on their way there, where rows are read again
 
 // Whole numbers in the order of the floats (-0 counts as 0).
 __device__ __forceinline__ uint32_t key_of(float x) {
@@ -185,6 +186,12 @@ __device__ __forceinline__ void load4(const __nv_bfloat16 *p, float (&x)[4]) {
 __device__ __forceinline__ u64 warp_sum(uint32_t v) {
     return ((u64)__reduce_add_sync(~0u, v >> 16) << 16) + __reduce_add_sync(~0u, v & 0xffffu);
 }
+// An atomic sum in shared memory by halves, as there is no 64-bit one but by comparing and trying again.
+__device__ __forceinline__ void add64(u64 *p, u64 v) {
+    uint32_t *const q = reinterpret_cast<uint32_t *>(p);
+    const uint32_t lo = (uint32_t)v, hi = (uint32_t)(v >> 32) + (atomicAdd(q, lo) + lo < lo);
+    if (hi) atomicAdd(q + 1, hi);
+}
 __device__ __forceinline__ u64 warp_scan(u64 v) {   // inclusive
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -231,7 +238,8 @@ __global__ void __launch_bounds__(Cfg<M>::NT, Cfg<M>::PER_SM) k_sample(SampleArg
     T *const seg = reinterpret_cast<T *>(sums + (NG + 1) / 2 * 2);
     const cg::cluster_group cluster = cg::this_cluster();
     const int C = ONE ? 1 : cluster.num_blocks(), rank = ONE ? 0 : cluster.block_rank();
-    const int r = blockIdx.x / C, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, V = a.V;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, V = a.V;
+    int r = blockIdx.x / C;
     auto sync = [&] {
         if (ONE || C == 1) __syncthreads();
         else cluster.sync();
@@ -243,6 +251,41 @@ __global__ void __launch_bounds__(Cfg<M>::NT, Cfg<M>::PER_SM) k_sample(SampleArg
     if (!ONE && C > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");   // the cluster's CTAs are there:
     pdl_wait();
     pdl_trigger();
+    // Rows of unlike settings are taken the long ones first, so that none of these is all that is left at the end: top-p alone,
+    // then nothing or a large k, then the others. Every CTA counts for itself which is its.
+    if constexpr (STREAM)
+        if (a.R <= kOrderedRows && a.top_p && (a.top_k || a.min_p)) {
+            constexpr int Q = kOrderedRows / NT;
+            u64 mine = 0;
+            int kind[Q];
+#pragma unroll
+            for (int q = 0; q < Q; ++q) {
+                const int i = tid * Q + q;
+                kind[q] = -1;
+                if (i >= a.R) continue;
+                const int k = a.top_k ? a.top_k[i] : 0;
+                const bool few = (a.min_p && a.min_p[i] > 0.f) || (k > 0 && k <= NT) || (a.temperature && a.temperature[i] == 0.f);
+                kind[q] = few ? 2 : (k > 0 && k <= LIST) || a.top_p[i] >= 1.f;
+                mine += 1ull << 20 * kind[q];
+            }
+            u64 upto = warp_scan(mine);
+            if (lane == 31) sm.part[warp] = upto;
+            __syncthreads();
+            u64 all = 0;
+            for (int w = 0; w < W; ++w) {
+                if (w < warp) upto += sm.part[w];
+                all += sm.part[w];
+            }
+            constexpr int ONES = (1 << 20) - 1;
+            const int n0 = (int)(all & ONES), n1 = (int)(all >> 20 & ONES), which = r < n0 ? 0 : r < n0 + n1 ? 1 : 2;
+            int at = (int)(upto - mine >> 20 * which & ONES) + (which == 0 ? 0 : which == 1 ? n0 : n0 + n1);
+#pragma unroll
+            for (int q = 0; q < Q; ++q)
+                if (kind[q] == which && at++ == r) sm.at = tid * Q + q;
+            __syncthreads();
+            r = sm.at;
+            __syncthreads();
+        }
 
     const T *const row = reinterpret_cast<const T *>(a.logits) + (size_t)r * a.stride;
     const int lead = (int)(((uintptr_t)row & 15) / sizeof(T)), base = rank * SL;
@@ -375,7 +418,7 @@ __global__ void __launch_bounds__(Cfg<M>::NT, Cfg<M>::PER_SM) k_sample(SampleArg
     auto get4 = [&](int pos, float (&x)[4]) {
         if constexpr (STREAM) {
             const int p = pos - lead;
-            if (p >= 0 && p + 4 <= V) load4(row + p, x);
+            if ((unsigned)p <= (unsigned)(V - 4)) load4(row + p, x);   // (V is large)
             else
 #pragma unroll
                 for (int e = 0; e < 4; ++e) x[e] = p + e >= 0 && p + e < V ? (float)row[p + e] : -INFINITY;
@@ -426,44 +469,51 @@ __global__ void __launch_bounds__(Cfg<M>::NT, Cfg<M>::PER_SM) k_sample(SampleArg
     auto all_of_them = [](float, int, float) { return true; };
     auto kept_of_them = [&](float v, int i, float) { return kept(v, i); };
 
-    // every element of the segment, by groups: f(group, x[4], id of x[0]). What comes from L2 is on its way through shared
-    // memory kRing - 1 turns before its use, each lane's part by itself.
+    // every element of the segment, by groups: f(group, x[4], id of x[0])
     auto groups = [&](auto f) {
-        float x[4];
+        float x[4], next[4];
+        if (warp < NG) get4(warp * kGroup + lane * 4, next);
+#pragma unroll 1
+        for (int g = warp; g < NG; g += W) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) x[e] = next[e];
+            if (g + W < NG) get4((g + W) * kGroup + lane * 4, next);
+            f(g, x, base + g * kGroup + lane * 4 - lead);
+        }
+    };
+    // The same where f is short: what comes from L2 is on its way through shared memory kRing - 1 turns before its use, each
+    // lane's part by itself. (1024 rows of 50272, top-k 1000: 158 us and 168; with a longer f that costs registers, top-p 0.95:
+    // 270 and 252.)
+    auto groups_ahead = [&](auto f) {
         if constexpr (STREAM) {
-            T *const ring = reinterpret_cast<T *>(sm.ring) + warp * kRing * kGroup + lane * 4;
-            auto fetch = [&](int g, int stage) {
-                const int p = g * kGroup + lane * 4 - lead;
-                if (g < NG && p >= 0 && p + 4 <= V)
-                    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(smem_u32(ring + stage * kGroup)), "l"(row + p),
-                                 "n"(4 * sizeof(T))
-                                 : "memory");
+            constexpr unsigned STAGE = kGroup * sizeof(T), RING = kRing * STAGE;
+            const T *const mine = reinterpret_cast<const T *>(sm.ring) + warp * kRing * kGroup + lane * 4;
+            const uint32_t ring = smem_u32(mine);
+            const unsigned last = V - 4;                              // the last place of four tokens; others are none or fewer
+            const T *from = row + (warp * kGroup + lane * 4 - lead);
+            unsigned p = warp * kGroup + lane * 4 - lead, p_from = p, stage = 0;
+            auto fetch = [&](unsigned to) {
+                if (p_from <= last)
+                    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(ring + to), "l"(from), "n"(4 * sizeof(T)) : "memory");
                 asm volatile("cp.async.commit_group;" ::: "memory");
+                from += W * kGroup, p_from += W * kGroup;
             };
 #pragma unroll
-            for (int k = 0; k < kRing - 1; ++k) fetch(warp + k * W, k);
-            int stage = 0;
+            for (int k = 0; k < kRing - 1; ++k) fetch(k * STAGE);
+            float x[4];
 #pragma unroll 1
             for (int g = warp; g < NG; g += W) {
-                fetch(g + (kRing - 1) * W, stage ? stage - 1 : kRing - 1);   // where the last turn's was
+                fetch((stage + (kRing - 1) * STAGE) % RING);         // where the last turn's was
                 asm volatile("cp.async.wait_group %0;" ::"n"(kRing - 1) : "memory");
-                const int p = g * kGroup + lane * 4 - lead;
-                if (p >= 0 && p + 4 <= V) load4(ring + stage * kGroup, x);
-                else get4(g * kGroup + lane * 4, x);
+                if (p <= last) load4(mine + stage / sizeof(T), x);
+                else get4(p + lead, x);
                 f(g, x, p);
-                stage = stage == kRing - 1 ? 0 : stage + 1;
+                p += W * kGroup;
+                stage = (stage + STAGE) % RING;
             }
             asm volatile("cp.async.wait_all;" ::: "memory");
         } else {
-            float next[4];
-            if (warp < NG) get4(warp * kGroup + lane * 4, next);
-#pragma unroll 1
-            for (int g = warp; g < NG; g += W) {
-#pragma unroll
-                for (int e = 0; e < 4; ++e) x[e] = next[e];
-                if (g + W < NG) get4((g + W) * kGroup + lane * 4, next);
-                f(g, x, base + g * kGroup + lane * 4 - lead);
-            }
+            groups(f);
         }
     };
     // The groups that may have a value from `from` on, where the largest ones are known and tell few.
@@ -494,7 +544,7 @@ __global__ void __launch_bounds__(Cfg<M>::NT, Cfg<M>::PER_SM) k_sample(SampleArg
                         for (int q = 0; q < U; ++q)
                             if (g[q] >= 0) f(g[q], x[q], g[q] * kGroup + lane * 4 - lead);
                     }
-            else groups(f);
+            else groups_ahead(f);
         } else {
             groups(f);
         }
@@ -502,7 +552,7 @@ __global__ void __launch_bounds__(Cfg<M>::NT, Cfg<M>::PER_SM) k_sample(SampleArg
     // Weights by groups, of the elements that take(value, id, y) says: small(y[4]) has those below kLarge and -inf for the
     // others; large(place, y, weight) those that a warp puts off until it has 32 or no more groups, as one such element
     // among 32 takes as long as 32. before(group, x[4], y[4]) and after(group) frame a group.
-    auto weigh = [&](auto before, auto take, auto small, auto large, auto after) {
+    auto weigh = [&](auto each, auto before, auto take, auto small, auto large, auto after) {
         auto *const put_off = sm.larges[warp];
         int n = 0;
         auto settle = [&](int from) {
@@ -515,7 +565,7 @@ __global__ void __launch_bounds__(Cfg<M>::NT, Cfg<M>::PER_SM) k_sample(SampleArg
             n = from;
             __syncwarp();
         };
-        groups([&](int g, const float (&x)[4], int id) {
+        each([&](int g, const float (&x)[4], int id) {
             float y[4];
             weight.exponents(x, y);
             before(g, x, y);
@@ -540,13 +590,13 @@ __global__ void __launch_bounds__(Cfg<M>::NT, Cfg<M>::PER_SM) k_sample(SampleArg
         if (n) settle(0);
     };
     // the sums of the groups' weights; see(group, x[4], y[4]) looks at all
-    auto sum_groups_and = [&](auto see, auto take) {
+    auto sum_groups_and = [&](auto each, auto see, auto take) {
         uint32_t w = 0;
-        weigh([&](int g, const float (&x)[4], const float (&y)[4]) {
+        weigh(each, [&](int g, const float (&x)[4], const float (&y)[4]) {
             if (lane == 0) sums[g] = 0;
             see(g, x, y);
         }, take, [&](const float (&y)[4]) { w = Weights::light4(y); },
-              [&](int pos, float, u64 one) { atomicAdd(&sums[pos / kGroup], one); },
+              [&](int pos, float, u64 one) { add64(&sums[pos / kGroup], one); },
               [&](int g) {
             if (!__any_sync(~0u, w != 0)) return;
             const u64 all = warp_sum(w);
@@ -554,7 +604,7 @@ __global__ void __launch_bounds__(Cfg<M>::NT, Cfg<M>::PER_SM) k_sample(SampleArg
             if (lane == 0) sums[g] += all;
         });
     };
-    auto sum_groups = [&](auto take) { sum_groups_and([](int, const float (&)[4], const float (&)[4]) {}, take); };
+    auto sum_groups = [&](auto take) { sum_groups_and(groups_ahead, [](int, const float (&)[4], const float (&)[4]) {}, take); };
     // the CTA's sum, for every thread
     auto block_sum = [&](u64 v) {
 #pragma unroll
@@ -803,7 +853,7 @@ __global__ void __launch_bounds__(Cfg<M>::NT, Cfg<M>::PER_SM) k_sample(SampleArg
         for (int i = tid; i < n; i += NT) {
             const u64 e = list[i];
             const int pos = id_of(e) + lead - base;
-            if (e <= last && pos >= 0 && pos < SL) atomicAdd(&sums[pos / kGroup], weight(value_at(e)));
+            if (e <= last && pos >= 0 && pos < SL) add64(&sums[pos / kGroup], weight(value_at(e)));
         }
     };
 
@@ -1056,7 +1106,7 @@ __global__ void __launch_bounds__(Cfg<M>::NT, Cfg<M>::PER_SM) k_sample(SampleArg
                 rest += Weights::light4(w);
             };
             if (z.n_lo <= FITS) {
-                n_list = gather(z.lo, groups, [&](const float (&x)[4]) {
+                n_list = gather(z.lo, groups_ahead, [&](const float (&x)[4]) {
                     float y[4];
                     weight.exponents(x, y);
                     rest_of(x, y);
@@ -1071,7 +1121,7 @@ __global__ void __launch_bounds__(Cfg<M>::NT, Cfg<M>::PER_SM) k_sample(SampleArg
                     __syncthreads();
                 }
             } else if (z.n_lo - z.n_hi <= FITS) {
-                sum_groups_and([&](int g, const float (&x)[4], const float (&y)[4]) {
+                sum_groups_and(groups, [&](int g, const float (&x)[4], const float (&y)[4]) {
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
                         if (x[e] >= z.lo && x[e] <= z.hi) {
@@ -1137,8 +1187,8 @@ __global__ void __launch_bounds__(Cfg<M>::NT, Cfg<M>::PER_SM) k_sample(SampleArg
         };
         auto count1 = [&](int, float y, u64 w) { count(y, w); };
         auto nothing = [](int, const float (&)[4], const float (&)[4]) {};
-        if (bound) weigh(nothing, all_of_them, count4, count1, [](int) {});
-        else weigh(nothing, kept_of_them, count4, count1, [](int) {});
+        if (bound) weigh(groups, nothing, all_of_them, count4, count1, [](int) {});
+        else weigh(groups, nothing, kept_of_them, count4, count1, [](int) {});
         rest = block_sum(rest);
         if (tid < 3) sm.h[0][tid][BINS - 1] = tid == 0 ? (uint32_t)rest & 0x7fffu : tid == 1 ? (uint32_t)(rest >> 15) & 0x7fffu : (uint32_t)(rest >> 30);
         u64 P, before, own_sum;
