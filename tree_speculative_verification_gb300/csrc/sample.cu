@@ -1216,14 +1216,48 @@ __global__ void __launch_bounds__(Cfg<M>::NT, Cfg<M>::PER_SM) k_sample(SampleArg
     }
     if (!drawn) {
         // ---- kept weights, group by group; the group and the token that u falls on
-        if (!summed) {
-            if (cut_id == 1 << kIdBits && low == -3.402823466e38f) sum_groups(all_of_them);
+        const bool whole_row = !summed && cut_id == 1 << kIdBits && low == -3.402823466e38f;
+        // (of a row in shared memory all kept: each thread sums a stretch of an odd number of elements, four at a time)
+        const bool by_stretch = !STREAM && whole_row;
+        const int stretch = (SL + NT - 1) / NT | 1;
+        if (!summed && !by_stretch) {
+            if (whole_row) sum_groups(all_of_them);
             else sum_groups(kept_of_them);
         }
         __syncthreads();
         const int share = (NG + NT - 1) / NT, g0 = min(NG, tid * share), g1 = min(NG, g0 + share);   // a thread's groups
         u64 mine = 0;
-        for (int g = g0; g < g1; ++g) mine += sums[g];
+        // four of a stretch from position i on
+        auto four_at = [&](int i, int end, float (&x)[4]) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) x[e] = i + e < end ? (float)seg[i + e] : -INFINITY;
+        };
+        auto larges_of = [&](float (&y)[4]) {
+            unsigned is = 0;
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (y[e] >= kLarge) is |= 1u << e, y[e] = -INFINITY;
+            return is;
+        };
+        if (by_stretch) {
+            const int i0 = min(SL, tid * stretch), i1 = min(SL, i0 + stretch);
+#pragma unroll 1
+            for (int i = i0; i < i1; i += 32) {
+                unsigned larges = 0;
+#pragma unroll
+                for (int k = 0; k < 32; k += 4) {
+                    if (i + k >= i1) break;
+                    float x[4], y[4];
+                    four_at(i + k, i1, x);
+                    weight.exponents(x, y);
+                    larges |= larges_of(y) << k;
+                    mine += Weights::light4(y);
+                }
+                for (; larges; larges &= larges - 1) mine += weight((float)seg[i + __ffs(larges) - 1]);
+            }
+        } else {
+            for (int g = g0; g < g1; ++g) mine += sums[g];
+        }
         const u64 run = block_scan(mine);
         if (tid == NT - 1) sm.total = run;
         __syncthreads();
@@ -1239,17 +1273,19 @@ __global__ void __launch_bounds__(Cfg<M>::NT, Cfg<M>::PER_SM) k_sample(SampleArg
             const u64 want = __umul64hi(part64(u), S);
             if (first + run - mine <= want && want < first + run) {
                 u64 at = first + run - mine;
-                int g = g0;
-                while (want >= at + sums[g]) at += sums[g++];
+                int g = by_stretch ? tid : g0;
+                if (!by_stretch)
+                    while (want >= at + sums[g]) at += sums[g++];
                 sm.at = g, sm.above = at;
             }
             const bool here = first <= want && want < first + sm.from[turn][rank];
             __syncthreads();
-            if (here && warp == 0) {   // as sum_groups has added them
-                const int g = sm.at, id = base + g * kGroup + lane * 4 - lead;
+            if (here && warp == 0) {   // as they have been added
+                const int from = sm.at * (by_stretch ? stretch : kGroup) + lane * 4, id = base + from - lead;
                 float x[4], y[4];
                 u64 w[4], large = 0;
-                get4(g * kGroup + lane * 4, x);
+                if (by_stretch) four_at(from, min(SL, (sm.at + 1) * stretch), x);
+                else get4(from, x);
                 weight.exponents(x, y);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
