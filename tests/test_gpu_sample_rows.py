@@ -13,6 +13,7 @@ from test_gpu_sample import BF16, F32, check, logits, run, uniforms
 
 pytestmark = pytest.mark.gpu
 LONG = [(F32, 30001), (BF16, 60002)]
+MANY = 168     # rows, more than there are SMs
 
 
 def check_some(x, u, rows, T=None, k=None, p=None, m=None, want="token probs kept"):
@@ -31,43 +32,43 @@ def check_some(x, u, rows, T=None, k=None, p=None, m=None, want="token probs kep
 def test_settings_by_row(dtype, V):
     grid = [(T, k, p, m) for T in (0.0, 0.7, 1.0, 2.0) for k in (0, 1, 50, V + 3) for p in (1.0, 0.9, 0.99) for m in (0.0, 0.05)]
     grid += [(1.3, 5, 0.5, 0.3), (1.0, 4095, 0.97, 0.0), (1.0, 4096, 1.0, 0.0), (1.0, 9000, 0.999, 0.001), (2.0, 3, 1.0, 1.0), (1.0, 0, 0.0, 0.0)]
+    grid += grid[:MANY - len(grid)]
     T, k, p, m = zip(*grid)
-    assert len(grid) >= 100
     check(logits(len(grid), V, V, dtype), uniforms(len(grid), V), T, k, p, m)
 
 
 @pytest.mark.parametrize("V", [131072, 131075, 2 ** 18])
 @pytest.mark.parametrize("dtype", [F32, BF16])
 def test_longest_rows(dtype, V):
-    R = 104
+    R = MANY
     grid = [(0.8, 0, 1.0, 0.0), (1.0, 50, 0.9, 0.0), (1.0, 0, 0.9, 0.0), (1.0, 0, 0.995, 0.0), (0.5, 3000, 0.99, 0.0), (1.0, 0, 1.0, 0.02),
             (0.0, 0, 1.0, 0.0), (1.0, 20000, 0.999, 0.0)]
     T, k, p, m = zip(*(grid * (R // len(grid))))
-    rows = list(range(8)) + list(range(96, 104))
+    rows = list(range(8)) + list(range(R - 8, R))
     check_some(logits(R, V, V, dtype), uniforms(R, V), rows, T, k, p, m)
 
 
 @pytest.mark.parametrize("dtype,V", LONG)
 @pytest.mark.parametrize("sigma", [0.01, 3.0, 30.0])
 def test_top_p_alone(dtype, V, sigma):
-    R = 102
-    check_some(logits(R, V, 2, dtype, sigma), uniforms(R), list(range(0, R, 3)), p=[0.1, 0.6, 0.95, 0.99, 0.999, 0.9999999, 0.3, 0.8] * 12 + [0.5] * 6)
+    R = MANY
+    check_some(logits(R, V, 2, dtype, sigma), uniforms(R), list(range(0, R, 3)), p=[0.1, 0.6, 0.95, 0.99, 0.999, 0.9999999, 0.3, 0.8] * (R // 8))
 
 
 @pytest.mark.parametrize("dtype,V", LONG)
 def test_top_k_alone(dtype, V):
-    R = 112
+    R = MANY
     k = [1, 2, 64, 1000, 4095, 4096, 6144, 6145, 20000, V - 1, V, 300, 1500, 2049]
     rows = list(range(28))
-    check_some(logits(R, V, 3, dtype), uniforms(R), rows, k=k * 8)
-    check_some(logits(R, V, 3, dtype), uniforms(R), rows, k=k * 8, p=[0.8] * R)
+    check_some(logits(R, V, 3, dtype), uniforms(R), rows, k=k * 12)
+    check_some(logits(R, V, 3, dtype), uniforms(R), rows, k=k * 12, p=[0.8] * R)
 
 
 def test_equal_values():
-    R, V = 108, 33333
+    R, V = 180, 33333
     x, u = torch.full((R, V), -7.25, device="cuda"), np.arange(R, dtype=np.float32) / R
-    k = [0, 0, 3, 1000, V, 1, 0, 0, 17] * 12
-    p = [1.0, 0.5, 1.0, 0.25, 0.75, 0.9, 1e-6, 0.999, 0.5] * 12
+    k = [0, 0, 3, 1000, V, 1, 0, 0, 17] * 20
+    p = [1.0, 0.5, 1.0, 0.25, 0.75, 0.9, 1e-6, 0.999, 0.5] * 20
     got, status = run(x, u, k=k, p=p)
     assert status == 0
     for r in range(R):
@@ -78,7 +79,7 @@ def test_equal_values():
 
 
 def test_few_values():
-    R, V = 100, 40000
+    R, V = MANY, 40000
     g = torch.Generator("cuda").manual_seed(1)
     x = torch.randint(0, 4, (R, V), generator=g, device="cuda").float()
     for kw in ({"p": [0.3] * R}, {"k": [15000] * R}, {"k": [9000] * R, "p": [0.5] * R}, {"m": [0.3] * R}, {"k": [30000] * R, "p": [0.99] * R}):
@@ -87,7 +88,7 @@ def test_few_values():
 
 @pytest.mark.parametrize("dtype,V", LONG)
 def test_masked_tokens(dtype, V):
-    R = 100
+    R = MANY
     x = logits(R, V, 4, dtype)
     x[0, 1:] = -math.inf
     x[1, :-1] = -math.inf
@@ -123,20 +124,20 @@ def test_rows_that_cannot_be_drawn(dtype, V):
                                               (F32, 777, 3, 781), (BF16, 4095, 1, 4097)])
 def test_strided_rows(dtype, V, off, wide):
     """Rows at every alignment; what stands around them is not read."""
-    R = 160
+    R = MANY
     buf = torch.full((R, wide), math.nan, dtype=dtype, device="cuda")
     x = buf[:, off:off + V]
     x.copy_(logits(R, V, 11, dtype))
-    check_some(x, uniforms(R), list(range(16)), k=[0, 5, 0, 40, 0, 0, 700, 0] * 20, p=[1.0, 0.9, 0.9, 1.0, 0.5, 0.999, 0.9, 0.99] * 20)
+    check_some(x, uniforms(R), list(range(16)), k=[0, 5, 0, 40, 0, 0, 700, 0] * (R // 8), p=[1.0, 0.9, 0.9, 1.0, 0.5, 0.999, 0.9, 0.99] * (R // 8))
 
 
 @pytest.mark.parametrize("V", [30001, 4093, 4096])
 def test_kept_in_the_logits_place(V):
     """Each kind of row: nothing dropped, few kept, many kept, one kept, some tokens masked."""
-    R = 160
+    R = MANY
     x = logits(R, V, 5)
     x[::16, 7:900] = -math.inf
-    k, p, T = [0, 30, 0, 0, 20000, 0, 1, 0] * 20, [1.0, 0.9, 0.9, 0.9999, 0.99, 0.5, 1.0, 0.999] * 20, [1.0, 1.0, 1.0, 1.0, 1.0, 0.0, 1.0, 1e30] * 20
+    k, p, T = [0, 30, 0, 0, 20000, 0, 1, 0] * (R // 8), [1.0, 0.9, 0.9, 0.9999, 0.99, 0.5, 1.0, 0.999] * (R // 8), [1.0, 1.0, 1.0, 1.0, 1.0, 0.0, 1.0, 1e30] * (R // 8)
     want, _ = run(x, uniforms(R), T, k, p)
     for again in range(3):
         y, token = x.clone(), torch.zeros(R, dtype=torch.int32, device="cuda")
@@ -145,7 +146,7 @@ def test_kept_in_the_logits_place(V):
         assert torch.equal(y, want["kept"]) and torch.equal(probs, want["probs"]) and torch.equal(token, want["token"])
 
 
-@pytest.mark.parametrize("R,V", [(100, 30001), (6, 30001), (200, 1000)])
+@pytest.mark.parametrize("R,V", [(MANY, 30001), (6, 30001), (200, 1000)])
 def test_hottest_temperatures(R, V):
     """Temperatures up to the largest number, over logits as far apart as they can be."""
     top = torch.finfo(F32).max
@@ -160,7 +161,7 @@ def test_hottest_temperatures(R, V):
     check_some(x, u, list(range(6)), T=T[:R], m=[0.5] * R)
 
 
-@pytest.mark.parametrize("R,V", [(128, 30001), (300, 2000)])
+@pytest.mark.parametrize("R,V", [(MANY, 30001), (300, 2000)])
 def test_same_results_again_and_in_a_graph(R, V):
     x = logits(R, V, 5)
     u, p, k = cu(uniforms(R), np.float32), cu([0.9, 0.99] * (R // 2), np.float32), cu([0, 0, 400, 5000] * (R // 4))
@@ -179,9 +180,9 @@ def test_same_results_again_and_in_a_graph(R, V):
 @pytest.mark.parametrize("dtype,V", LONG + [(F32, 3999), (BF16, 4096)])
 def test_outputs_alone(dtype, V):
     """Each output asked for alone is the one of all three; token alone is checked against the definition too."""
-    R = 160
+    R = MANY
     x, u = logits(R, V, 9, dtype), uniforms(R, 3)
-    kw = dict(T=[0.8, 1.0] * 80, k=[0, 0, 40, 5000] * 40, p=[1.0, 0.9, 0.9, 0.99, 0.97] * 32)
+    kw = dict(T=[0.8, 1.0] * (R // 2), k=[0, 0, 40, 5000] * (R // 4), p=([1.0, 0.9, 0.9, 0.99, 0.97] * R)[:R])
     all_of, _ = run(x, u, **kw)
     for name in all_of:
         got, status = run(x, u, want=name, **kw)
@@ -198,7 +199,7 @@ def test_rows_do_not_depend_on_one_another():
               m=rng.choice([0.0, 0.0, 0.05], R))
     whole, status = run(x, u, **kw)
     assert status == 0
-    for rows in (slice(0, 700), slice(700, 2100), slice(5, 108)):
+    for rows in (slice(0, 700), slice(700, 2100), slice(5, 200), slice(40, 90)):
         got, _ = run(x[rows], u[rows], **{n: v[rows] for n, v in kw.items()})
         for n in whole:
             assert torch.equal(got[n], whole[n][rows])

@@ -43,7 +43,6 @@ struct Cfg {
 };
 constexpr int kGroup = 128;       // elements of a warp's turn: a sum of weights is kept for each
 constexpr int kLarges = 64;       // places of large weights that a warp puts off
-constexpr int kManyRows = 100;    // from which rows that no one CTA holds are read again from L2
 constexpr int kSmallV = 4096;
 constexpr int kOrderedRows = 2048;   // up to so many rows are taken in an order of their settings
 constexpr int kRing = 4;           // groups of a warp in shared memory or on their way there, where rows are read again
@@ -265,7 +264,7 @@ __global__ void __launch_bounds__(Cfg<M>::NT, Cfg<M>::PER_SM) k_sample(SampleArg
                 if (i >= a.R) continue;
                 const int k = a.top_k ? a.top_k[i] : 0;
                 const bool few = (a.min_p && a.min_p[i] > 0.f) || (k > 0 && k <= NT) || (a.temperature && a.temperature[i] == 0.f);
-                kind[q] = few ? 2 : (k > 0 && k <= LIST) || a.top_p[i] >= 1.f;
+                kind[q] = few ? 2 : (k > 0 && k < V) || a.top_p[i] >= 1.f;
                 mine += 1ull << 20 * kind[q];
             }
             u64 upto = warp_scan(mine);
@@ -382,7 +381,7 @@ __global__ void __launch_bounds__(Cfg<M>::NT, Cfg<M>::PER_SM) k_sample(SampleArg
     const float ch = sm.ch;
     // a lower bound of the row's sum of weights: these tokens'
     float some = 1.f;
-    const bool bound = top_p < 1.f && top_k == 0 && !(min_p > 0.f);
+    const bool bound = top_p < 1.f && (top_k <= 0 || top_k >= V) && !(min_p > 0.f);
     if (bound) {
         some = 0.f;
 #pragma unroll
@@ -1388,7 +1387,11 @@ cudaError_t launch_rows(const SampleArgs &a, cudaStream_t s) {
     // The fewest CTAs a row whose segments let two of them share an SM; more where there are few rows.
     int C = 1;
     while (C < 8 && smem_of<kCluster>(seg(C), sizeof(T)) > 115600) C *= 2;
-    if (C > 1 && a.R >= kManyRows) return launch_as<T, kStream>(a, 1, seg(1), s);
+    // Filtered rows, more than there are SMs: a CTA a row, from L2 (cluster and CTA: 160 rows of 50272 with top-k 50 26 and 22
+    // us, top-p 0.9 59 and 47, settings by row and distributions 57 and 70; 300 rows 33 and 24, 78 and 50, 77 and 77; 1024 rows
+    // 100 and 78, 234 and 143, 179 and 136; 100 rows 16 and 17, 40 and 37, 52 and 63). Not filtered, a row is read from shared
+    // memory (1024 rows 77 and 95 us).
+    if (C > 1 && a.R > num_sms() && (a.top_k || a.top_p || a.min_p)) return launch_as<T, kStream>(a, 1, seg(1), s);
     while (C < 8 && (long long)a.R * C <= num_sms() && seg(2 * C) >= 2048) C *= 2;
     if (C == 1 && a.V <= kSmallV) return launch_as<T, kSmall>(a, 1, seg(1), s);
     return launch_as<T, kCluster>(a, C, seg(C), s);
