@@ -207,7 +207,7 @@ struct Shared {
     u64 list[F::LIST];                // the cluster's candidates, in its first CTA, by their place in the order
     u64 part[F::W];
     u64 from[3][8];                   // what the cluster's CTAs tell one another, in turn
-    std::conditional_t<M == kStream, uint32_t, uint16_t> larges[F::W][kLarges];
+    uint32_t larges[M == kStream ? F::W : 1][M == kStream ? kLarges : 1];
     u64 cut, kept;                    // the last token kept, the sum of all kept weights
     u64 above, total;
     uint4 ring[M == kStream ? F::W * kRing * 32 : 1];   // groups on their way, the warps' own
@@ -216,7 +216,7 @@ struct Shared {
     int n_list, n_kept, at;
 };
 template <Mode M>
-constexpr size_t kFixed = (sizeof(Shared<M>) + 15) / 16 * 16;   // then a sum a group, then the segment
+constexpr size_t kFixed = (sizeof(Shared<M>) + 15) / 16 * 16;   // then a sum a unit, then the segment
 
 __device__ __forceinline__ void copy16(void *to, const void *from) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(to)), "l"(from) : "memory");
@@ -233,8 +233,8 @@ __global__ void __launch_bounds__(Cfg<M>::NT, Cfg<M>::PER_SM) k_sample(SampleArg
     constexpr bool STREAM = M == kStream, ONE = M != kCluster;
     Sh &sm = *reinterpret_cast<Sh *>(smem);
     const int NG = SL / kGroup;
-    u64 *const sums = reinterpret_cast<u64 *>(reinterpret_cast<char *>(smem) + kFixed<M>);   // kept weights of each group
-    T *const seg = reinterpret_cast<T *>(sums + (NG + 1) / 2 * 2);
+    u64 *const sums = reinterpret_cast<u64 *>(reinterpret_cast<char *>(smem) + kFixed<M>);   // kept weights of each unit
+    T *const seg = reinterpret_cast<T *>(sums + (STREAM ? (NG + 1) / 2 * 2 : NT));
     const cg::cluster_group cluster = cg::this_cluster();
     const int C = ONE ? 1 : cluster.num_blocks(), rank = ONE ? 0 : cluster.block_rank();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, V = a.V;
@@ -548,6 +548,40 @@ __global__ void __launch_bounds__(Cfg<M>::NT, Cfg<M>::PER_SM) k_sample(SampleArg
             groups(f);
         }
     };
+    // Sums of kept weights are held by units: a group of kGroup, or, where the row is in shared memory, a thread's stretch of an
+    // odd number of elements (read without conflicts of banks, and its sum needs no other thread's).
+    const int unit = STREAM ? kGroup : (SL + NT - 1) / NT | 1, units = STREAM ? NG : NT;
+    // four elements of a stretch from position i on
+    auto four_at = [&](int i, int end, float (&x)[4]) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[e] = i + e < end ? (float)seg[i + e] : -INFINITY;
+    };
+    // The same as weigh() by stretches: the large ones are noted in bits, and follow every 32 elements.
+    auto weigh_stretch = [&](auto take, auto small, auto large) {
+        const int i0 = min(SL, tid * unit), i1 = min(SL, i0 + unit);
+#pragma unroll 1
+        for (int i = i0; i < i1; i += 32) {
+            unsigned larges = 0;
+#pragma unroll
+            for (int k = 0; k < 32; k += 4) {
+                if (i + k >= i1) break;
+                float x[4], y[4];
+                four_at(i + k, i1, x);
+                weight.exponents(x, y);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const bool in = take(x[e], base + i + k + e - lead, y[e]);
+                    if (in && y[e] >= kLarge) larges |= 1u << (k + e);
+                    if (!in || y[e] >= kLarge) y[e] = -INFINITY;
+                }
+                small(y);
+            }
+            for (; larges; larges &= larges - 1) {
+                const float x = (float)seg[i + __ffs(larges) - 1];
+                large(weight.exponent(x), weight(x));
+            }
+        }
+    };
     // Weights by groups, of the elements that take(value, id, y) says: small(y[4]) has those below kLarge and -inf for the
     // others; large(place, y, weight) those that a warp puts off until it has 32 or no more groups, as one such element
     // among 32 takes as long as 32. before(group, x[4], y[4]) and after(group) frame a group.
@@ -558,7 +592,7 @@ __global__ void __launch_bounds__(Cfg<M>::NT, Cfg<M>::PER_SM) k_sample(SampleArg
             __syncwarp();
             if (from + lane < n) {
                 const int pos = put_off[from + lane];
-                const float x = STREAM ? (float)row[pos - lead] : (float)seg[pos];
+                const float x = (float)row[pos - lead];
                 large(pos, weight.exponent(x), weight(x));
             }
             n = from;
@@ -577,7 +611,7 @@ __global__ void __launch_bounds__(Cfg<M>::NT, Cfg<M>::PER_SM) k_sample(SampleArg
                     const unsigned is = __ballot_sync(~0u, y[e] >= kLarge);
                     if (n + __popc(is) > kLarges) settle(n - 32);
                     if (y[e] >= kLarge) {
-                        put_off[n + __popc(is & ((1u << lane) - 1))] = id + e + lead - base;
+                        put_off[n + __popc(is & ((1u << lane) - 1))] = id + e + lead;
                         y[e] = -INFINITY;
                     }
                     n += __popc(is);
@@ -603,7 +637,20 @@ __global__ void __launch_bounds__(Cfg<M>::NT, Cfg<M>::PER_SM) k_sample(SampleArg
             if (lane == 0) sums[g] += all;
         });
     };
-    auto sum_groups = [&](auto take) { sum_groups_and(groups_ahead, [](int, const float (&)[4], const float (&)[4]) {}, take); };
+    // the sums of the units' weights
+    auto sum_units = [&](auto take) {
+        if constexpr (STREAM) {
+            sum_groups_and(groups_ahead, [](int, const float (&)[4], const float (&)[4]) {}, take);
+        } else {
+            u64 mine = 0;
+            weigh_stretch(take, [&](const float (&y)[4]) { mine += Weights::light4(y); }, [&](float, u64 w) { mine += w; });
+            sums[tid] = mine;
+        }
+    };
+    auto clear_units = [&] {
+        for (int g = tid; g < units; g += NT) sums[g] = 0;
+        __syncthreads();
+    };
     // the CTA's sum, for every thread
     auto block_sum = [&](u64 v) {
 #pragma unroll
@@ -852,7 +899,7 @@ __global__ void __launch_bounds__(Cfg<M>::NT, Cfg<M>::PER_SM) k_sample(SampleArg
         for (int i = tid; i < n; i += NT) {
             const u64 e = list[i];
             const int pos = id_of(e) + lead - base;
-            if (e <= last && pos >= 0 && pos < SL) add64(&sums[pos / kGroup], weight(value_at(e)));
+            if (e <= last && pos >= 0 && pos < SL) add64(&sums[pos / unit], weight(value_at(e)));
         }
     };
 
@@ -1048,8 +1095,7 @@ __global__ void __launch_bounds__(Cfg<M>::NT, Cfg<M>::PER_SM) k_sample(SampleArg
             if (by_p) last = choose(n_list, last, top, list_from, 0, std::true_type(), threshold);
             if (by_k || by_p) cut_at(last);
             __syncthreads();
-            for (int g = tid; g < NG; g += NT) sums[g] = 0;
-            __syncthreads();
+            clear_units();
             add_listed(sm.list, n_list, last);
             summed = true;
         } else if (listed) {
@@ -1083,8 +1129,7 @@ __global__ void __launch_bounds__(Cfg<M>::NT, Cfg<M>::PER_SM) k_sample(SampleArg
             if (by_k || by_p) cut_at(last);
             if (sm.n_kept <= NT / 4) drawn = true;
             else {
-                for (int g = tid; g < NG; g += NT) sums[g] = 0;
-                __syncthreads();
+                clear_units();
                 add_listed(peer(0).list, n_list, last);
                 summed = true;
             }
@@ -1115,10 +1160,7 @@ __global__ void __launch_bounds__(Cfg<M>::NT, Cfg<M>::PER_SM) k_sample(SampleArg
                     last = choose(n_list, ~0ull, top, z.lo, 0, std::true_type(), [&](u64 mass) { return threshold(mass + rest); });
                     listed = cut_found = last != 0;
                 }
-                if (listed) {
-                    for (int g = tid; g < NG; g += NT) sums[g] = 0;
-                    __syncthreads();
-                }
+                if (listed) clear_units();
             } else if (z.n_lo - z.n_hi <= FITS) {
                 sum_groups_and(groups, [&](int g, const float (&x)[4], const float (&y)[4]) {
 #pragma unroll
@@ -1186,14 +1228,19 @@ __global__ void __launch_bounds__(Cfg<M>::NT, Cfg<M>::PER_SM) k_sample(SampleArg
         };
         auto count1 = [&](int, float y, u64 w) { count(y, w); };
         auto nothing = [](int, const float (&)[4], const float (&)[4]) {};
-        if (bound) weigh(groups, nothing, all_of_them, count4, count1, [](int) {});
-        else weigh(groups, nothing, kept_of_them, count4, count1, [](int) {});
+        if constexpr (STREAM) {
+            if (bound) weigh(groups, nothing, all_of_them, count4, count1, [](int) {});
+            else weigh(groups, nothing, kept_of_them, count4, count1, [](int) {});
+        } else {
+            if (bound) weigh_stretch(all_of_them, count4, count);
+            else weigh_stretch(kept_of_them, count4, count);
+        }
         rest = block_sum(rest);
         if (tid < 3) sm.h[0][tid][BINS - 1] = tid == 0 ? (uint32_t)rest & 0x7fffu : tid == 1 ? (uint32_t)(rest >> 15) & 0x7fffu : (uint32_t)(rest >> 30);
         u64 P, before, own_sum;
         const int b = find_bin(std::true_type(), threshold, P, before, own_sum);
         // sums of what is kept in the bins before, candidates of the bin itself
-        sum_groups([&](float v, int i, float y) {
+        sum_units([&](float v, int i, float y) {
             const int at = kept(v, i) ? bin(y) : BINS;
             if (at == b) push(v, i);
             return at < b;
@@ -1215,48 +1262,14 @@ __global__ void __launch_bounds__(Cfg<M>::NT, Cfg<M>::PER_SM) k_sample(SampleArg
     }
     if (!drawn) {
         // ---- kept weights, group by group; the group and the token that u falls on
-        const bool whole_row = !summed && cut_id == 1 << kIdBits && low == -3.402823466e38f;
-        // (of a row in shared memory all kept: each thread sums a stretch of an odd number of elements, four at a time)
-        const bool by_stretch = !STREAM && whole_row;
-        const int stretch = (SL + NT - 1) / NT | 1;
-        if (!summed && !by_stretch) {
-            if (whole_row) sum_groups(all_of_them);
-            else sum_groups(kept_of_them);
+        if (!summed) {
+            if (cut_id == 1 << kIdBits && low == -3.402823466e38f) sum_units(all_of_them);
+            else sum_units(kept_of_them);
         }
         __syncthreads();
-        const int share = (NG + NT - 1) / NT, g0 = min(NG, tid * share), g1 = min(NG, g0 + share);   // a thread's groups
+        const int share = (units + NT - 1) / NT, g0 = min(units, tid * share), g1 = min(units, g0 + share);   // a thread's units
         u64 mine = 0;
-        // four of a stretch from position i on
-        auto four_at = [&](int i, int end, float (&x)[4]) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) x[e] = i + e < end ? (float)seg[i + e] : -INFINITY;
-        };
-        auto larges_of = [&](float (&y)[4]) {
-            unsigned is = 0;
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                if (y[e] >= kLarge) is |= 1u << e, y[e] = -INFINITY;
-            return is;
-        };
-        if (by_stretch) {
-            const int i0 = min(SL, tid * stretch), i1 = min(SL, i0 + stretch);
-#pragma unroll 1
-            for (int i = i0; i < i1; i += 32) {
-                unsigned larges = 0;
-#pragma unroll
-                for (int k = 0; k < 32; k += 4) {
-                    if (i + k >= i1) break;
-                    float x[4], y[4];
-                    four_at(i + k, i1, x);
-                    weight.exponents(x, y);
-                    larges |= larges_of(y) << k;
-                    mine += Weights::light4(y);
-                }
-                for (; larges; larges &= larges - 1) mine += weight((float)seg[i + __ffs(larges) - 1]);
-            }
-        } else {
-            for (int g = g0; g < g1; ++g) mine += sums[g];
-        }
+        for (int g = g0; g < g1; ++g) mine += sums[g];
         const u64 run = block_scan(mine);
         if (tid == NT - 1) sm.total = run;
         __syncthreads();
@@ -1272,19 +1285,18 @@ __global__ void __launch_bounds__(Cfg<M>::NT, Cfg<M>::PER_SM) k_sample(SampleArg
             const u64 want = __umul64hi(part64(u), S);
             if (first + run - mine <= want && want < first + run) {
                 u64 at = first + run - mine;
-                int g = by_stretch ? tid : g0;
-                if (!by_stretch)
-                    while (want >= at + sums[g]) at += sums[g++];
+                int g = g0;
+                while (want >= at + sums[g]) at += sums[g++];
                 sm.at = g, sm.above = at;
             }
             const bool here = first <= want && want < first + sm.from[turn][rank];
             __syncthreads();
             if (here && warp == 0) {   // as they have been added
-                const int from = sm.at * (by_stretch ? stretch : kGroup) + lane * 4, id = base + from - lead;
+                const int from = sm.at * unit + lane * 4, id = base + from - lead;
                 float x[4], y[4];
                 u64 w[4], large = 0;
-                if (by_stretch) four_at(from, min(SL, (sm.at + 1) * stretch), x);
-                else get4(from, x);
+                if constexpr (STREAM) get4(from, x);
+                else four_at(from, min(SL, (sm.at + 1) * unit), x);
                 weight.exponents(x, y);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
@@ -1355,7 +1367,8 @@ __global__ void __launch_bounds__(Cfg<M>::NT, Cfg<M>::PER_SM) k_sample(SampleArg
 
 template <Mode M>
 size_t smem_of(int SL, int es) {
-    return kFixed<M> + (size_t)(SL / kGroup + 1) / 2 * 16 + (M == kStream ? 0 : (size_t)SL * es);
+    const int units = M == kStream ? SL / kGroup : Cfg<M>::NT;
+    return kFixed<M> + (size_t)(units + 1) / 2 * 16 + (M == kStream ? 0 : (size_t)SL * es);
 }
 
 template <typename T, Mode M>
@@ -1384,9 +1397,11 @@ cudaError_t launch_as(const SampleArgs &a, int C, int SL, cudaStream_t s) {
 template <typename T>
 cudaError_t launch_rows(const SampleArgs &a, cudaStream_t s) {
     auto seg = [&](int C) { return ((a.V + 16 / (int)sizeof(T) - 1 + C - 1) / C + kGroup - 1) / kGroup * kGroup; };
-    // The fewest CTAs a row whose segments let two of them share an SM; more where there are few rows.
+    // The fewest CTAs a row whose segments let two of them share an SM (228 KB, of which each takes one for itself); more where
+    // there are few rows.
+    constexpr size_t kHalf = (228 / 2 - 1) * 1024;
     int C = 1;
-    while (C < 8 && smem_of<kCluster>(seg(C), sizeof(T)) > 115600) C *= 2;
+    while (C < 8 && smem_of<kCluster>(seg(C), sizeof(T)) > kHalf) C *= 2;
     // Filtered rows, more than there are SMs: a CTA a row, from L2 (cluster and CTA: 160 rows of 50272 with top-k 50 26 and 22
     // us, top-p 0.9 59 and 47, settings by row and distributions 57 and 70; 300 rows 33 and 24, 78 and 50, 77 and 77; 1024 rows
     // 100 and 78, 234 and 143, 179 and 136; 100 rows 16 and 17, 40 and 37, 52 and 63). Not filtered, a row is read from shared
