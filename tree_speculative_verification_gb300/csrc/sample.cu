@@ -43,8 +43,9 @@ struct Cfg {
 };
 constexpr int kGroup = 128;       // elements of a warp's turn: a sum of weights is kept for each
 constexpr int kLarges = 64;       // places of large weights that a warp puts off
-constexpr int kSmallV = 4096;
-constexpr int kOrderedRows = 2048;   // up to so many rows are taken in an order of their settings
+// Up to so many rows are taken in an order of their settings (1024 rows of 50272, settings by row and distributions: 136 us and
+// 150; all with top-k 50: 78 and 74).
+constexpr int kOrderedRows = 2048;
 constexpr int kRing = 4;           // groups of a warp in shared memory or on their way there, where rows are read again
 
 // Whole numbers in the order of the floats (-0 counts as 0).
@@ -1408,7 +1409,10 @@ cudaError_t launch_rows(const SampleArgs &a, cudaStream_t s) {
     // memory (1024 rows 77 and 95 us).
     if (C > 1 && a.R > num_sms() && (a.top_k || a.top_p || a.min_p)) return launch_as<T, kStream>(a, 1, seg(1), s);
     while (C < 8 && (long long)a.R * C <= num_sms() && seg(2 * C) >= 2048) C *= 2;
-    if (C == 1 && a.V <= kSmallV) return launch_as<T, kSmall>(a, 1, seg(1), s);
+    // Short rows, where there are more than the SMs hold at once in large CTAs (small CTAs and large: settings by row and
+    // distributions, 1000 tokens, 300 rows 12.7 and 12.8 us, 1200 rows 16.5 and 41; 4000 tokens, 450 rows 35 and 28, 1200 rows
+    // 45 and 57).
+    if (C == 1 && a.V <= 4096 && (a.V <= 512 || a.R >= num_sms() + a.V / 8)) return launch_as<T, kSmall>(a, 1, seg(1), s);
     return launch_as<T, kCluster>(a, C, seg(C), s);
 }
 
