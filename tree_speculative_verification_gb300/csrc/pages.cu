@@ -76,11 +76,10 @@ __device__ __forceinline__ int ring_at(int k, int num) {
     return k - (k >= num ? num : 0);
 }
 
-// Of kPageThreads rising numbers the last one that is i or less (the first is).
-__device__ __forceinline__ int last_upto(const int *s, int i) {
+// Of 2 `most` rising numbers (a power of two) the last one that is i or less (the first is).
+__device__ __forceinline__ int last_upto(const int *s, int most, int i) {
     int x = 0;
-#pragma unroll
-    for (int step = kPageThreads / 2; step; step /= 2)
+    for (int step = most; step; step /= 2)
         if (s[x + step] <= i) x += step;
     return x;
 }
@@ -135,7 +134,8 @@ __global__ void __launch_bounds__(kPageThreads, 2) k_pages_build(PageArgs a) {
         ok = b < B && pool_ok && r.sound && (r.own.take == 0 || from + r.own.take <= count);
         if (b < B && !r.sound) bits |= TS_STATUS_INDEX;
         if (b < B && pool_ok && r.sound && !ok) bits |= TS_STATUS_NO_PAGES;
-        if (ok && r.own.take) atomicMax(&taken_s, (int)(from + r.own.take));
+        const int served = __reduce_max_sync(~0u, ok && r.own.take ? (int)(from + r.own.take) : 0);   // of the line; rises from warp to warp
+        if ((tid & 31) == 0 && served) atomicMax(&taken_s, served);
         row_s[tid] = clamped(first), take_s[tid] = clamped(from), back_s[tid] = clamped(at.back + run.back - r.own.back);
         begin_s[tid] = r.begin, held_s[tid] = r.held, want_s[tid] = r.sound ? (int)r.want : r.held, ok_s[tid] = ok;
         if (tid == kPageThreads - 1) {
@@ -149,67 +149,79 @@ __global__ void __launch_bounds__(kPageThreads, 2) k_pages_build(PageArgs a) {
         }
         __syncthreads();
         const Sums tile = tile_s;
-        if (pool_ok) {
-            // pages taken: as many of the line as are served, which are whole requests
-            const int t1 = min(min(take_s[kPageThreads], taken_s), (c + 1) * t_per);
-            for (int i = max(take_s[0], c * t_per) + tid; i < t1; i += kPageThreads) {
-                const int x = last_upto(take_s, i);
-                table[(size_t)(base + x) * width + held_s[x] + (i - take_s[x])] = ring[ring_at(head + i, num)];
+        const int most = B - base > 1 ? 1 << (31 - __clz(min(B - base, kPageThreads) - 1)) : 1;   // half of the tile's requests' number, rounded up
+        // Pages taken: as many of the line as are served, which are whole requests; and pages given back, behind the ring's free
+        // part. A thread's first ones are read before anything is written.
+        const int t1 = pool_ok ? min(min(take_s[kPageThreads], taken_s), (c + 1) * t_per) : 0,
+                  b1 = pool_ok ? min(back_s[kPageThreads], (c + 1) * b_per) : 0;
+        int ti = max(take_s[0], c * t_per) + tid, bi = max(back_s[0], c * b_per) + tid;
+        auto move = [&] {
+            while (ti < t1 || bi < b1) {
+                int t_page = 0, b_page = 0, *t_to = nullptr;
+                if (ti < t1) {
+                    const int x = last_upto(take_s, most, ti);
+                    t_page = ring[ring_at(head + ti, num)];
+                    t_to = &table[(size_t)(base + x) * width + held_s[x] + (ti - take_s[x])];
+                }
+                if (bi < b1) {
+                    const int x = last_upto(back_s, most, bi);
+                    b_page = table[(size_t)(base + x) * width + want_s[x] + (bi - back_s[x])];
+                }
+                if (ti < t1) *t_to = t_page;
+                if (bi < b1) ring[ring_at(head + count + bi, num)] = b_page;
+                ti += kPageThreads, bi += kPageThreads;
             }
-            // pages given back, behind the ring's free part
-            const int b1 = min(back_s[kPageThreads], (c + 1) * b_per);
-            for (int i = max(back_s[0], c * b_per) + tid; i < b1; i += kPageThreads) {
-                const int x = last_upto(back_s, i);
-                ring[ring_at(head + count + i, num)] = table[(size_t)(base + x) * width + want_s[x] + (i - back_s[x])];
-            }
-        }
-        if (a.slot) {   // slots, four a thread and two of these at once
+        };
+        if (a.slot) {   // slots, four a thread
             const int lo = max(s0, row_s[0]), hi = min(s1, row_s[kPageThreads]);
             // page p of the tile's request x: its own, or the ring's where it is taken only now
             auto page_of = [&](int x, int p) {
                 return p < held_s[x] ? table[(size_t)(base + x) * width + p] : ring[ring_at(head + take_s[x] + (p - held_s[x]), num)];
             };
-            for (long long j0 = (lo & ~3LL) + 4 * tid; j0 < hi; j0 += 8 * kPageThreads) {
-                int x[2], page[2], p_now[2];
-#pragma unroll
-                for (int k = 0; k < 2; ++k) {   // the first slot's request and page
-                    const long long i0 = j0 + 4 * k * kPageThreads;
-                    x[k] = 0, p_now[k] = -1, page[k] = -1;
-                    if (i0 >= hi) continue;
-                    const int i = max((int)i0, lo);
-                    x[k] = last_upto(row_s, i);
-                    if (!ok_s[x[k]]) continue;
-                    p_now[k] = (begin_s[x[k]] + (i - row_s[x[k]])) / TS_PAGE_KEYS;
-                    page[k] = page_of(x[k], p_now[k]);
-                }
-#pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    const long long i0 = j0 + 4 * k * kPageThreads;
-                    if (i0 >= hi) continue;
-                    int v[4], y = x[k], p_y = p_now[k], page_y = page[k];
+            int now = -1;   // the request of the slots before: the next ones' are mostly its
+            for (long long i0 = (lo & ~3LL) + 4 * tid; i0 < hi; i0 += 4 * kPageThreads) {
+                // Four rows of one request are in one page or two, and their first one's place is enough; of several requests
+                // every row has a page of its own (-1: there is none to read).
+                int at[4] = {-1, -1, -1, -1}, page[4] = {}, v[4];
+                const int i = max((int)i0, lo);
+                if (now < 0 || i >= row_s[now + 1]) now = last_upto(row_s, most, i);
+                const bool one = i0 >= lo && i0 + 4 <= min(hi, row_s[now + 1]);
+                if (one) {
+                    if (ok_s[now]) {
+                        const int j = begin_s[now] + (i - row_s[now]);
+                        at[0] = j % TS_PAGE_KEYS;
+                        page[0] = page_of(now, j / TS_PAGE_KEYS);
+                        if (at[0] > TS_PAGE_KEYS - 4) page[1] = page_of(now, j / TS_PAGE_KEYS + 1);
+                    }
+                } else {
+                    int y = now;
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        v[e] = -1;
-                        const long long i = i0 + e;
-                        if (i < lo || i >= hi) continue;
-                        while (row_s[y + 1] <= i) ++y, p_y = -1;
+                        if (i0 + e < lo || i0 + e >= hi) continue;
+                        while (row_s[y + 1] <= i0 + e) ++y;
                         if (!ok_s[y]) continue;
-                        const int j = begin_s[y] + ((int)i - row_s[y]);
-                        if (j / TS_PAGE_KEYS != p_y) {
-                            p_y = j / TS_PAGE_KEYS;
-                            page_y = page_of(y, p_y);
-                        }
-                        if (page_y >= 0 && page_y < num) v[e] = page_y * TS_PAGE_KEYS + j % TS_PAGE_KEYS;
-                        else bits |= TS_STATUS_INDEX;
+                        const int j = begin_s[y] + ((int)i0 + e - row_s[y]);
+                        at[e] = j % TS_PAGE_KEYS;
+                        page[e] = page_of(y, j / TS_PAGE_KEYS);
                     }
-                    if (a.slot_vec && i0 >= lo && i0 + 4 <= hi)
-                        *reinterpret_cast<int4 *>(a.slot + i0) = make_int4(v[0], v[1], v[2], v[3]);
-                    else
-                        for (int e = 0; e < 4; ++e)
-                            if (i0 + e >= lo && i0 + e < hi) a.slot[i0 + e] = v[e];
                 }
+                move();
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int r = one && at[0] >= 0 ? at[0] + e : at[e], in = one ? (r < TS_PAGE_KEYS ? page[0] : page[1]) : page[e];
+                    const bool good = (unsigned)in < (unsigned)num;
+                    if (r >= 0 && !good) bits |= TS_STATUS_INDEX;
+                    v[e] = r >= 0 && good ? in * TS_PAGE_KEYS + r % TS_PAGE_KEYS : -1;
+                }
+                if (a.slot_vec && i0 >= lo && i0 + 4 <= hi)
+                    *reinterpret_cast<int4 *>(a.slot + i0) = make_int4(v[0], v[1], v[2], v[3]);
+                else
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (i0 + e >= lo && i0 + e < hi) a.slot[i0 + e] = v[e];
             }
         }
+        move();
         at.n += tile.n, at.take += tile.take, at.back += tile.back;
         if (base + kPageThreads < B) __syncthreads();   // shared memory is the next tile's
     }
