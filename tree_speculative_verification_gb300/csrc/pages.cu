@@ -17,8 +17,10 @@ namespace {
 // no entry is both read and written. What the call changes in place (pages
 // held, the ring's head and count) is written by the CTA that ends last.
 //
-// Integers; bound by the chain of loads (lengths, then table or ring entries)
-// up to some 100k rows, then by the 4 bytes a row.
+// Integers; bound by the chain of loads (lengths, then table or ring entries):
+// 8 requests 4.6 us. 2.1 M rows of 256 requests take 12 us, where a write of their
+// slots alone would take 1.4: the sums and searches that every CTA makes for
+// itself (issue slots 60%), and the last CTA's turn.
 constexpr int kPageThreads = 512;
 
 struct PageArgs {
