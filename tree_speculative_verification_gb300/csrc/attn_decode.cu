@@ -107,6 +107,7 @@ struct Shared {
 
 constexpr int kGroup = 16, kGroupFrom = 33;   // parts are joined in two levels, kGroup at a time, from kGroupFrom on
 constexpr int kWholeSteps = 4, kLeastSteps = 1;
+constexpr int kFewParts = 8;
 constexpr int kMostParts = 64, kMostCtas = kMostParts * kGroup - 1;   // parts, or groups, in one join; CTAs that allows
 
 // Adds one to a counter: what the CTA has written before (behind a barrier) is seen by whoever finds it counted and
@@ -278,6 +279,18 @@ __global__ void __launch_bounds__(32 * kWarps<D, NT, ONE>, kPerSm<D, NT, ONE>) k
             for (int i = 0; i < KC; ++i) qr[j][i] = h < a.G ? __ldg(p + 4 * i) : zero;
         }
     };
+    // Four dims of a head, from dd on: where they are final into out, else into a part, with the head's maximum and sum.
+    auto put = [&](int b, int kvh, int h0, int h, int dd, const float4 &acc, float top, float sum, float *part) {
+        if (part) {
+            *reinterpret_cast<float4 *>(part + h * D + dd) = acc;
+            if (dd == 0) part[HB * D + h] = top, part[HB * (D + 1) + h] = sum;
+        } else {
+            const float f = 1.f / sum;
+            const __nv_bfloat162 r0 = __floats2bfloat162_rn(acc.x * f, acc.y * f), r1 = __floats2bfloat162_rn(acc.z * f, acc.w * f);
+            *reinterpret_cast<uint2 *>(a.out + ((size_t)b * a.Hq + kvh * a.G + h0 + h) * D + dd) =
+                make_uint2(*reinterpret_cast<const uint32_t *>(&r0), *reinterpret_cast<const uint32_t *>(&r1));
+        }
+    };
     // The warps' O, maxima and sums in shared memory as one: the item's rows of out, or a part.
     auto join_warps = [&](int b, int kvh, int h0, float *part) {
         __syncthreads();
@@ -295,15 +308,7 @@ __global__ void __launch_bounds__(32 * kWarps<D, NT, ONE>, kPerSm<D, NT, ONE>) k
                 sum = fmaf(l_s[w][h], f, sum);
                 acc.x = fmaf(y.x, f, acc.x), acc.y = fmaf(y.y, f, acc.y), acc.z = fmaf(y.z, f, acc.z), acc.w = fmaf(y.w, f, acc.w);
             }
-            if (part) {
-                *reinterpret_cast<float4 *>(part + h * D + dd) = acc;
-                if (dd == 0) part[HB * D + h] = top, part[HB * (D + 1) + h] = sum;
-            } else {
-                const float f = 1.f / sum;
-                const __nv_bfloat162 r0 = __floats2bfloat162_rn(acc.x * f, acc.y * f), r1 = __floats2bfloat162_rn(acc.z * f, acc.w * f);
-                *reinterpret_cast<uint2 *>(a.out + ((size_t)b * a.Hq + kvh * a.G + h0 + h) * D + dd) =
-                    make_uint2(*reinterpret_cast<const uint32_t *>(&r0), *reinterpret_cast<const uint32_t *>(&r1));
-            }
+            put(b, kvh, h0, h, dd, acc, top, sum, part);
         }
         __syncthreads();
     };
@@ -492,6 +497,34 @@ __global__ void __launch_bounds__(32 * kWarps<D, NT, ONE>, kPerSm<D, NT, ONE>) k
                 const int k = k0 + i * step;
                 return a.parts + (size_t)(2 * k + (k == sh.c0)) * PART;
             };
+            // Few parts: a thread reads its dims of all of them at once.
+            if (n <= kFewParts) {
+                for (int q = tid; q < HB * D / 4; q += kThreads) {
+                    const int h = q / (D / 4), dd = q % (D / 4) * 4;
+                    if (sh.h0 + h >= a.G) break;
+                    float4 y[kFewParts], sum_y = make_float4(0.f, 0.f, 0.f, 0.f);
+                    float mk[kFewParts], lk[kFewParts], top = -INFINITY, sum = 0.f;
+#pragma unroll
+                    for (int k = 0; k < kFewParts; ++k) {
+                        const float *p = part_at(min(k, n - 1));
+                        y[k] = __ldcg(reinterpret_cast<const float4 *>(p + h * D + dd));
+                        mk[k] = __ldcg(p + HB * D + h), lk[k] = __ldcg(p + HB * (D + 1) + h);
+                    }
+#pragma unroll
+                    for (int k = 0; k < kFewParts; ++k) top = fmaxf(top, mk[k]);
+#pragma unroll
+                    for (int k = 0; k < kFewParts; ++k)
+                        if (k < n) {
+                            const float f = ex2(mk[k] - guarded(top));
+                            sum = fmaf(lk[k], f, sum);
+                            sum_y.x = fmaf(y[k].x, f, sum_y.x), sum_y.y = fmaf(y[k].y, f, sum_y.y);
+                            sum_y.z = fmaf(y[k].z, f, sum_y.z), sum_y.w = fmaf(y[k].w, f, sum_y.w);
+                        }
+                    put(sh.b, sh.kvh, sh.h0, h, dd, sum_y, top, sum, part);
+                }
+                __syncthreads();
+                return;
+            }
             float4 acc[NV], v[NV];
             auto load = [&](int k) {
 #pragma unroll
