@@ -19,7 +19,7 @@
 //
 // 64 requests of 1024 keys, 56 heads: 277 us, the copy rate; 4 of 16384 keys,
 // 64 heads over 8: 48 us, of which the stream takes 38 (the copy rate again), launch
-// and plan 4, the join 5; 8 of 2048 keys, 32 over 8: 18 us, of which the stream
+// and plan 4, the join 5; 8 of 2048 keys, 32 over 8: 17 us, of which the stream
 // takes 9.5. One request's start is plan, loads, join: 4.6 us.
 #include <cuda_bf16.h>
 #include <math.h>
@@ -79,8 +79,8 @@ __device__ __forceinline__ float guarded(float m) { return m == -INFINITY ? 0.f 
 
 // As many warps an SM as the registers allow, in CTAs of four, or all in one CTA where there are few items: the more warps
 // share an item, the fewer parts of it are joined through the workspace, but the more of them wait for one another at its
-// end. In fours and in one: one request of 16384 keys, 8 heads 22.0 and 17.5 us; 8 requests of 2048 keys, 8 heads 18.0 and
-// 19.6; 64 requests of 1024 keys, 56 heads 278 and 295.
+// end. In fours and in one: one request of 16384 keys, 8 heads 21.4 and 17.6 us; 8 requests of 2048 keys, 8 heads 16.8 and
+// 19.0; 64 requests of 1024 keys, 56 heads 276 and 296.
 template <int D, int NT>
 constexpr int kFours = D == 64 ? (NT == 1 ? 4 : 3) : (NT == 1 ? 3 : 2);
 template <int D, int NT, bool ONE>
@@ -106,7 +106,6 @@ struct Shared {
 };
 
 constexpr int kGroup = 16, kGroupFrom = 33;   // parts are joined in two levels, kGroup at a time, from kGroupFrom on
-constexpr int kWholeSteps = 4, kLeastSteps = 1;
 constexpr int kFewParts = 8;
 constexpr int kMostParts = 64, kMostCtas = kMostParts * kGroup - 1;   // parts, or groups, in one join; CTAs that allows
 
@@ -187,11 +186,13 @@ __global__ void __launch_bounds__(32 * kWarps<D, NT, ONE>, kPerSm<D, NT, ONE>) k
     }
     const int T = (int)all_tiles, c = blockIdx.x;
     live_items *= items;
-    // As many CTAs as the GPU holds. A part that has to be joined costs 3 us, a step of every warp 0.8 us: items of up to
-    // kWhole tiles are not cut, and none into parts of less than kLeast. Where there are enough CTAs they are a whole number
-    // an item, unless that leaves out more than a tenth of them: equal requests are then cut alike, no CTA's stretch holds
-    // parts of two items, and no item has one part more.
-    constexpr int kWhole = kWholeSteps * W / 4, kLeast = kLeastSteps * W / 4;
+    // As many CTAs as the GPU holds. A part that has to be joined costs 2 to 3 us, a step of every warp 0.8 us: items of up to
+    // kWhole tiles are not cut, and none into parts of less than a step of every warp. (Whole up to 3 steps of all twelve warps
+    // or 4: one request of 768 keys, 8 heads 8.1 and 9.6 us; up to 2: of 512 keys 8.7 and 8.0. Up to 4 of four or 5: 8 requests
+    // of 300 keys, 8 heads 9.1 and 10.8, 16 of these 13.8 and 11.3.) Where there are enough CTAs they are a whole number an
+    // item, unless that leaves out more than a tenth of them: equal requests are then cut alike, no CTA's stretch holds parts
+    // of two items, and no item has one part more.
+    constexpr int kWhole = (ONE ? 3 : 4) * W / 4, kLeast = W / 4;
     int ctas = gridDim.x;
     if (live_items <= ctas) {
         const int pages = T / live_items, most = pages <= kWhole ? 1 : pages / kLeast, fit = ctas / live_items;
@@ -497,7 +498,8 @@ __global__ void __launch_bounds__(32 * kWarps<D, NT, ONE>, kPerSm<D, NT, ONE>) k
                 const int k = k0 + i * step;
                 return a.parts + (size_t)(2 * k + (k == sh.c0)) * PART;
             };
-            // Few parts: a thread reads its dims of all of them at once.
+            // Few parts: a thread reads its dims of all of them at once (8 requests of 2048 keys, 7 parts: 16.8 us, and 17.8 by
+            // warps and shared memory as below).
             if (n <= kFewParts) {
                 for (int q = tid; q < HB * D / 4; q += kThreads) {
                     const int h = q / (D / 4), dd = q % (D / 4) * 4;
