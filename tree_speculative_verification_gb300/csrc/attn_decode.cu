@@ -161,25 +161,45 @@ __global__ void __launch_bounds__(32 * kWarps<D, NT, ONE>, kPerSm<D, NT, ONE>) k
         return all;
     };
     const int items = a.Hkv * a.blocks;   // of a request
-    long long mine = 0, before = 0;
-    int live = 0, mine_first = 0;
-    for (int b = tid; b < a.B; b += kThreads) {
-        const int n = a.kv_len[b], p = pages_of(n);
-        if (b < kThreads) len_s[b] = n, mine_first = p;
-        mine += p;
-        live += p > 0;
-        if (p == 0 && n != 0 && blockIdx.x == 0) flag(a.status, TS_STATUS_INDEX);
-    }
-    for (int b = blockIdx.x; b < a.B; b += gridDim.x)   // no key: zeros
-        if (a.kv_len[b] == 0)
-            for (int i = tid; i < a.Hq * VEC; i += kThreads)
-                ((uint4 *)a.out)[(size_t)b * a.Hq * VEC + i] = make_uint4(0, 0, 0, 0);
-    live = __reduce_add_sync(~0u, live);
-    if (lane == 0) items_s[warp] = live;
-    const long long all_tiles = block_sum(mine, before) * items;
-    int live_items = 0;
+    auto no_keys = [&](int b) {           // zeros
+        for (int i = tid; i < a.Hq * VEC; i += kThreads)
+            ((uint4 *)a.out)[(size_t)b * a.Hq * VEC + i] = make_uint4(0, 0, 0, 0);
+    };
+    // Up to 32 requests every warp plans for itself, a lane a request, without a barrier (one request of 4096 keys 11.0 us, and
+    // 11.4 by all warps together).
+    const bool few = a.B <= 32;
+    int lane_n = 0, lane_p = 0, lane_to = 0;   // keys, pages, and pages up to and with this request
+    long long mine = 0, before = 0, all_tiles;
+    int live = 0, live_items = 0, mine_first = 0;
+    if (few) {
+        if (lane < a.B) lane_n = a.kv_len[lane];
+        lane_p = lane_to = pages_of(lane_n);
 #pragma unroll
-    for (int w = 0; w < W; ++w) live_items += items_s[w];
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(~0u, lane_to, o);
+            if (lane >= o) lane_to += y;
+        }
+        live_items = __popc(__ballot_sync(~0u, lane_p > 0));
+        all_tiles = (long long)__shfl_sync(~0u, lane_to, 31) * items;
+        if (blockIdx.x == 0 && warp == 0 && lane_p == 0 && lane_n != 0) flag(a.status, TS_STATUS_INDEX);
+        for (int b = blockIdx.x; b < a.B; b += gridDim.x)
+            if (__shfl_sync(~0u, lane_n, b) == 0) no_keys(b);
+    } else {
+        for (int b = tid; b < a.B; b += kThreads) {
+            const int n = a.kv_len[b], p = pages_of(n);
+            if (b < kThreads) len_s[b] = n, mine_first = p;
+            mine += p;
+            live += p > 0;
+            if (p == 0 && n != 0 && blockIdx.x == 0) flag(a.status, TS_STATUS_INDEX);
+        }
+        for (int b = blockIdx.x; b < a.B; b += gridDim.x)
+            if (a.kv_len[b] == 0) no_keys(b);
+        live = __reduce_add_sync(~0u, live);
+        if (lane == 0) items_s[warp] = live;
+        all_tiles = block_sum(mine, before) * items;
+#pragma unroll
+        for (int w = 0; w < W; ++w) live_items += items_s[w];
+    }
     if (all_tiles == 0 || all_tiles > INT32_MAX) {
         if (all_tiles && blockIdx.x == 0 && tid == 0) flag(a.status, TS_STATUS_INDEX);
         return;
@@ -203,7 +223,12 @@ __global__ void __launch_bounds__(32 * kWarps<D, NT, ONE>, kPerSm<D, NT, ONE>) k
     auto stretch = [&](int c) { return q0 * c + (unsigned)(r0 * c) / (unsigned)ctas; };   // floor(T c / ctas)
     int x = stretch(c);
     const int x_end = stretch(c + 1);
-    if (a.B <= kThreads) {
+    int req, first;                        // a request, and the line's tile at which it starts
+    if (few) {
+        const int lo = (lane_to - lane_p) * items;
+        req = __ffs(__ballot_sync(~0u, lo <= x && x < lo + lane_p * items)) - 1;
+        first = __shfl_sync(~0u, lo, req);
+    } else if (a.B <= kThreads) {
         const int lo = (int)before * items;
         if (lo <= x && x < lo + mine_first * items) req_s = tid, first_s = lo;
         __syncthreads();
@@ -219,12 +244,12 @@ __global__ void __launch_bounds__(32 * kWarps<D, NT, ONE>, kPerSm<D, NT, ONE>) k
         }
         __syncthreads();
     }
-    int req = req_s, first = first_s;      // a request, and the line's tile at which it starts
+    if (!few) req = req_s, first = first_s;
     auto segment = [&](int x) {            // the one that starts at tile x, below x_end
         Segment z;
         int n, pages;
         while (true) {
-            n = req < kThreads ? len_s[req] : a.kv_len[req], pages = pages_of(n);
+            n = few ? __shfl_sync(~0u, lane_n, req) : req < kThreads ? len_s[req] : a.kv_len[req], pages = pages_of(n);
             if (x < first + pages * items) break;
             first += pages * items;
             ++req;
