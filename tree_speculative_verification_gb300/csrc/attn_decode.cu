@@ -130,7 +130,7 @@ __global__ void __launch_bounds__(32 * kWarps<D, NT, ONE>, kPerSm<D, NT, ONE>) k
     float(*o_s)[HB][ROW] = reinterpret_cast<float(*)[HB][ROW]>(smem);   // [W]
     __shared__ float m_s[W][HB], l_s[W][HB], f_s[kMostParts][HB];
     __shared__ long long sum_s[W];
-    __shared__ int len_s[kThreads], req_s, first_s, items_s[W], last_s;
+    __shared__ int len_s[kThreads], req_s, first_s, items_s[W], most_s[W], last_s;
     __shared__ Shared shared_s[2];   // of the CTA's first segment, of its last
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
     pdl_wait();
@@ -171,6 +171,8 @@ __global__ void __launch_bounds__(32 * kWarps<D, NT, ONE>, kPerSm<D, NT, ONE>) k
     int lane_n = 0, lane_p = 0, lane_to = 0;   // keys, pages, and pages up to and with this request
     long long mine = 0, before = 0, all_tiles;
     int live = 0, live_items = 0, mine_first = 0;
+    int most_p = 0;
+    bool alike;                                // all requests with keys have as many pages
     if (few) {
         if (lane < a.B) lane_n = a.kv_len[lane];
         lane_p = lane_to = pages_of(lane_n);
@@ -180,6 +182,8 @@ __global__ void __launch_bounds__(32 * kWarps<D, NT, ONE>, kPerSm<D, NT, ONE>) k
             if (lane >= o) lane_to += y;
         }
         live_items = __popc(__ballot_sync(~0u, lane_p > 0));
+        most_p = __reduce_max_sync(~0u, lane_p);
+        alike = __all_sync(~0u, lane_p == 0 || lane_p == most_p);
         all_tiles = (long long)__shfl_sync(~0u, lane_to, 31) * items;
         if (blockIdx.x == 0 && warp == 0 && lane_p == 0 && lane_n != 0) flag(a.status, TS_STATUS_INDEX);
         for (int b = blockIdx.x; b < a.B; b += gridDim.x)
@@ -190,15 +194,19 @@ __global__ void __launch_bounds__(32 * kWarps<D, NT, ONE>, kPerSm<D, NT, ONE>) k
             if (b < kThreads) len_s[b] = n, mine_first = p;
             mine += p;
             live += p > 0;
+            most_p = max(most_p, p);
             if (p == 0 && n != 0 && blockIdx.x == 0) flag(a.status, TS_STATUS_INDEX);
         }
         for (int b = blockIdx.x; b < a.B; b += gridDim.x)
             if (a.kv_len[b] == 0) no_keys(b);
         live = __reduce_add_sync(~0u, live);
-        if (lane == 0) items_s[warp] = live;
-        all_tiles = block_sum(mine, before) * items;
+        most_p = __reduce_max_sync(~0u, most_p);
+        if (lane == 0) items_s[warp] = live, most_s[warp] = most_p;
+        all_tiles = block_sum(mine, before);
 #pragma unroll
-        for (int w = 0; w < W; ++w) live_items += items_s[w];
+        for (int w = 0; w < W; ++w) live_items += items_s[w], most_p = max(most_p, most_s[w]);
+        alike = all_tiles == (long long)live_items * most_p;
+        all_tiles *= items;
     }
     if (all_tiles == 0 || all_tiles > INT32_MAX) {
         if (all_tiles && blockIdx.x == 0 && tid == 0) flag(a.status, TS_STATUS_INDEX);
@@ -209,14 +217,17 @@ __global__ void __launch_bounds__(32 * kWarps<D, NT, ONE>, kPerSm<D, NT, ONE>) k
     // As many CTAs as the GPU holds. A part that has to be joined costs 2 to 3 us, a step of every warp 0.8 us: items of up to
     // kWhole tiles are not cut, and none into parts of less than a step of every warp. (Whole up to 3 steps of all twelve warps
     // or 4: one request of 768 keys, 8 heads 8.1 and 9.6 us; up to 2: of 512 keys 8.7 and 8.0. Up to 4 of four or 5: 8 requests
-    // of 300 keys, 8 heads 9.1 and 10.8, 16 of these 13.8 and 11.3.) Where there are enough CTAs they are a whole number an
-    // item, unless that leaves out more than a tenth of them: equal requests are then cut alike, no CTA's stretch holds parts
-    // of two items, and no item has one part more.
-    constexpr int kWhole = (ONE ? 3 : 4) * W / 4, kLeast = W / 4;
+    // of 300 keys, 8 heads 9.1 and 10.8.) Where there are enough CTAs they are a whole number an item, unless that leaves out
+    // more than a tenth of them: no CTA's stretch of equal requests then holds parts of two items, and no item has one part
+    // more. With more of them left out too, where all requests are alike and a CTA's stretch grows by less than kJoin (16
+    // requests, 8 heads: of 300 keys 13.9 and 10.8 us, of 1500 23.4 and 21.6; 4 requests of 16384 keys, 8 heads 48 and 46; by 20
+    // steps of every warp it is too much: 29 requests of 2500 keys 51 and 60).
+    constexpr int kWhole = (ONE ? 3 : 4) * W / 4, kLeast = W / 4, kJoin = 8 * W / 4;
     int ctas = gridDim.x;
     if (live_items <= ctas) {
         const int pages = T / live_items, most = pages <= kWhole ? 1 : pages / kLeast, fit = ctas / live_items;
-        if (most <= fit || ctas % live_items <= ctas / 10) ctas = min(most, fit) * live_items;
+        if (most <= fit || ctas % live_items <= ctas / 10 || (alike && (pages + fit - 1) / fit <= T / ctas + kJoin))
+            ctas = min(most, fit) * live_items;
     }
     if (c >= ctas) return;
     const int q0 = T / ctas, r0 = T - q0 * ctas;
