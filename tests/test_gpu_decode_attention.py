@@ -233,3 +233,19 @@ def test_more_tiles_than_32_bits_count():
     api.decode_attention_paged(out, q, kv, lens, 0.0, api.decode_workspace(B, H, H, d), status)
     assert status.item() == api.STATUS_INDEX
     assert not out[77].any() and (out[:77] == 1).all() and (out[78:] == 1).all()
+
+
+@pytest.mark.parametrize("B,Hk,G,d,n", [(3, 8, 4, 128, 600), (7, 4, 1, 64, 900), (11, 8, 2, 128, 3000), (32, 1, 8, 128, 2000), (31, 12, 1, 64, 300),
+                                        (33, 8, 1, 128, 700), (2, 2, 9, 128, 8000), (1, 5, 3, 64, 12000)])
+def test_unlike_lengths(B, Hk, G, d, n):
+    """Batches of all lengths, some empty, cut into parts of their items."""
+    g = torch.Generator().manual_seed(B)
+    for again in range(3):
+        lens = torch.randint(0, n + 1, (B,), generator=g).tolist()
+        if again == 1:
+            lens[B // 2] = 0
+        if again == 2:
+            lens = [n - n // 50 * (b % 2) for b in range(B)]
+        c = Cache(lens, Hk, d, seed=again)
+        q = queries(B, Hk * G, d, again)
+        check_attention(c, q, attend(c, q, lens), lens)

@@ -12,15 +12,16 @@
 //
 // The work is cut evenly: the tiles (64 keys, a page) of all (request, key/value
 // head, block of query heads) items stand in one line, and every CTA takes an
-// equal stretch of it, found from the lengths on the GPU. An item that lies in
+// equal stretch of it, found from the lengths on the GPU (or, where there are more
+// CTAs than items, one part of one item). An item that lies in
 // several CTAs' stretches leaves a part (O, maximum, sum) of each in the
 // workspace, and the CTA that finds by a counter that it is the item's last one
 // joins them, in their order, so that results do not depend on which that is.
 //
 // 64 requests of 1024 keys, 56 heads: 277 us, the copy rate; 4 of 16384 keys,
-// 64 heads over 8: 48 us, of which the stream takes 38 (the copy rate again), launch
-// and plan 4, the join 5; 8 of 2048 keys, 32 over 8: 17 us, of which the stream
-// takes 9.5. One request's start is plan, loads, join: 4.6 us.
+// 64 heads over 8: 46 us, of which the stream takes 38 (the copy rate again), launch
+// and plan 4, the join 4; 8 of 2048 keys, 32 over 8: 17 us, of which the stream
+// takes 9.5. One request's start is plan, loads, sums: 4.4 us.
 #include <cuda_bf16.h>
 #include <math.h>
 
@@ -130,7 +131,7 @@ __global__ void __launch_bounds__(32 * kWarps<D, NT, ONE>, kPerSm<D, NT, ONE>) k
     float(*o_s)[HB][ROW] = reinterpret_cast<float(*)[HB][ROW]>(smem);   // [W]
     __shared__ float m_s[W][HB], l_s[W][HB], f_s[kMostParts][HB];
     __shared__ long long sum_s[W];
-    __shared__ int len_s[kThreads], req_s, first_s, items_s[W], most_s[W], last_s;
+    __shared__ int len_s[kThreads], req_s, first_s, items_s[W], most_s[W], last_s, part_s[2];
     __shared__ Shared shared_s[2];   // of the CTA's first segment, of its last
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
     pdl_wait();
@@ -165,14 +166,14 @@ __global__ void __launch_bounds__(32 * kWarps<D, NT, ONE>, kPerSm<D, NT, ONE>) k
         for (int i = tid; i < a.Hq * VEC; i += kThreads)
             ((uint4 *)a.out)[(size_t)b * a.Hq * VEC + i] = make_uint4(0, 0, 0, 0);
     };
-    // Up to 32 requests every warp plans for itself, a lane a request, without a barrier (one request of 4096 keys 11.0 us, and
-    // 11.4 by all warps together).
+    // Up to 32 requests every warp plans for itself, a lane a request, without a barrier (one request of 100 keys 4.2 us, and 4.6
+    // by all warps together).
     const bool few = a.B <= 32;
     int lane_n = 0, lane_p = 0, lane_to = 0;   // keys, pages, and pages up to and with this request
     long long mine = 0, before = 0, all_tiles;
     int live = 0, live_items = 0, mine_first = 0;
     int most_p = 0;
-    bool alike;                                // all requests with keys have as many pages
+    bool alike = false;                        // all requests with keys have as many pages (more than 32 of them)
     if (few) {
         if (lane < a.B) lane_n = a.kv_len[lane];
         lane_p = lane_to = pages_of(lane_n);
@@ -183,7 +184,6 @@ __global__ void __launch_bounds__(32 * kWarps<D, NT, ONE>, kPerSm<D, NT, ONE>) k
         }
         live_items = __popc(__ballot_sync(~0u, lane_p > 0));
         most_p = __reduce_max_sync(~0u, lane_p);
-        alike = __all_sync(~0u, lane_p == 0 || lane_p == most_p);
         all_tiles = (long long)__shfl_sync(~0u, lane_to, 31) * items;
         if (blockIdx.x == 0 && warp == 0 && lane_p == 0 && lane_n != 0) flag(a.status, TS_STATUS_INDEX);
         for (int b = blockIdx.x; b < a.B; b += gridDim.x)
@@ -217,45 +217,91 @@ __global__ void __launch_bounds__(32 * kWarps<D, NT, ONE>, kPerSm<D, NT, ONE>) k
     // As many CTAs as the GPU holds. A part that has to be joined costs 2 to 3 us, a step of every warp 0.8 us: items of up to
     // kWhole tiles are not cut, and none into parts of less than a step of every warp. (Whole up to 3 steps of all twelve warps
     // or 4: one request of 768 keys, 8 heads 8.1 and 9.6 us; up to 2: of 512 keys 8.7 and 8.0. Up to 4 of four or 5: 8 requests
-    // of 300 keys, 8 heads 9.1 and 10.8.) Where there are enough CTAs they are a whole number an item, unless that leaves out
-    // more than a tenth of them: no CTA's stretch of equal requests then holds parts of two items, and no item has one part
-    // more. With more of them left out too, where all requests are alike and a CTA's stretch grows by less than kJoin (16
-    // requests, 8 heads: of 300 keys 13.9 and 10.8 us, of 1500 23.4 and 21.6; 4 requests of 16384 keys, 8 heads 48 and 46; by 20
-    // steps of every warp it is too much: 29 requests of 2500 keys 51 and 60).
+    // of 300 keys, 8 heads 9.1 and 10.8.)
+    // Where there are enough CTAs each gets one part of one item, of at most so many tiles that the parts are no more than the
+    // CTAs, unless that is kJoin, or a tenth, above an equal stretch of the line: no CTA then has parts of two items to leave.
+    // (Such parts and equal stretches: 16 requests, 8 heads, of 300 keys 10.9 and 13.9 us, of 1500 21.6 and 23.4; 4 requests of
+    // 16384 keys, 8 heads 46 and 48; 8 of 100 to 600 keys, 8 heads 9.5 and 14.0, 16 of 300 to 3000 25.2 and 26.1. By 20 steps of
+    // every warp above it is too much: 29 requests of 2500 keys 60 and 51.) That is found by a lane a request; more requests
+    // than a warp has lanes are cut into parts where they are all alike, or where that leaves out a tenth of the CTAs at most.
     constexpr int kWhole = (ONE ? 3 : 4) * W / 4, kLeast = W / 4, kJoin = 8 * W / 4;
-    int ctas = gridDim.x;
-    if (live_items <= ctas) {
-        const int pages = T / live_items, most = pages <= kWhole ? 1 : pages / kLeast, fit = ctas / live_items;
-        if (most <= fit || ctas % live_items <= ctas / 10 || (alike && (pages + fit - 1) / fit <= T / ctas + kJoin))
-            ctas = min(most, fit) * live_items;
-    }
-    if (c >= ctas) return;
-    const int q0 = T / ctas, r0 = T - q0 * ctas;
-    auto stretch = [&](int c) { return q0 * c + (unsigned)(r0 * c) / (unsigned)ctas; };   // floor(T c / ctas)
-    int x = stretch(c);
-    const int x_end = stretch(c + 1);
-    int req, first;                        // a request, and the line's tile at which it starts
-    if (few) {
-        const int lo = (lane_to - lane_p) * items;
-        req = __ffs(__ballot_sync(~0u, lo <= x && x < lo + lane_p * items)) - 1;
-        first = __shfl_sync(~0u, lo, req);
-    } else if (a.B <= kThreads) {
-        const int lo = (int)before * items;
-        if (lo <= x && x < lo + mine_first * items) req_s = tid, first_s = lo;
-        __syncthreads();
-    } else {
-        int done = 0;
-        for (int base = 0; base < a.B; base += kThreads) {
-            const int b = base + tid, p = b < a.B ? pages_of(a.kv_len[b]) : 0;
-            __syncthreads();
-            const int all = (int)block_sum(p, before), lo = (done + (int)before) * items;
-            if (lo <= x && x < lo + p * items) req_s = b, first_s = lo;
-            done += all;
-            if (x < done * items) break;
+    const int grid = gridDim.x;
+    int ctas = grid, x = 0, x_end = 0, req = 0, first = 0;   // a request, and the line's tile at which it starts
+    int parts = 0;                                           // of the CTA's one item (0: a stretch of the line)
+    if (few && live_items <= grid) {
+        auto parts_of = [&](int s) { return lane_p <= kWhole ? (lane_p > 0) : (int)((unsigned)(lane_p + s - 1) / (unsigned)s); };
+        auto number = [&](int s) { return items * (int)__reduce_add_sync(~0u, parts_of(s)); };
+        const bool same = __all_sync(~0u, lane_p == 0 || lane_p == most_p);
+        const int share = T / grid;
+        int s = share + max(kJoin, share / 10);
+        bool fits = most_p <= kWhole;
+        if (!fits && same) {
+            const int fit = grid / live_items, need = max(kLeast, (most_p + fit - 1) / fit);
+            fits = need <= s, s = need;
+        } else if (!fits) {
+            int lo = max(kLeast, share + (share * grid < T));
+            // (a part more an item than its share of the line are CTAs enough)
+            const int enough = grid > live_items ? (int)((unsigned)T / (unsigned)(grid - live_items)) + 1 : most_p;
+            fits = enough <= s || number(s) <= grid;
+            s = max(lo, min(s, enough));
+#pragma unroll 1
+            for (int i = 0; i < 3 && fits && lo < s; ++i) {
+                const int m = (lo + s) / 2;
+                if (number(m) <= grid) s = m;
+                else lo = m + 1;
+            }
         }
-        __syncthreads();
+        if (fits) {
+            const int own = parts_of(s);
+            int to = own * items;                            // CTAs up to and with this request's
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int y = __shfl_up_sync(~0u, to, o);
+                if (lane >= o) to += y;
+            }
+            if (c >= __shfl_sync(~0u, to, 31)) return;
+            req = __ffs(__ballot_sync(~0u, to - own * items <= c && c < to)) - 1;
+            const int at = c - __shfl_sync(~0u, to - own * items, req), pages = __shfl_sync(~0u, lane_p, req);
+            parts = __shfl_sync(~0u, own, req), first = __shfl_sync(~0u, (lane_to - lane_p) * items, req);
+            const int item = (unsigned)at / (unsigned)parts, k = at - item * parts, each = pages / parts, over = pages - each * parts;
+            if (tid == 0) part_s[0] = c - k;                 // the first one's CTA
+            x = first + item * pages + each * k + over * k / parts;
+            x_end = first + item * pages + each * (k + 1) + over * (k + 1) / parts;
+        }
     }
-    if (!few) req = req_s, first = first_s;
+    if (!parts) {
+        if (!few && live_items <= grid) {
+            const int pages = T / live_items, most = pages <= kWhole ? 1 : pages / kLeast, fit = grid / live_items;
+            if (most <= fit || grid % live_items <= grid / 10 || (alike && (pages + fit - 1) / fit <= T / grid + kJoin))
+                ctas = min(most, fit) * live_items;
+        }
+        if (c >= ctas) return;
+        const int q0 = T / ctas, r0 = T - q0 * ctas;
+        auto stretch = [&](int c) { return q0 * c + (unsigned)(r0 * c) / (unsigned)ctas; };   // floor(T c / ctas)
+        x = stretch(c), x_end = stretch(c + 1);
+        if (few) {
+            const int lo = (lane_to - lane_p) * items;
+            req = __ffs(__ballot_sync(~0u, lo <= x && x < lo + lane_p * items)) - 1;
+            first = __shfl_sync(~0u, lo, req);
+        } else if (a.B <= kThreads) {
+            const int lo = (int)before * items;
+            if (lo <= x && x < lo + mine_first * items) req_s = tid, first_s = lo;
+            __syncthreads();
+        } else {
+            int done = 0;
+            for (int base = 0; base < a.B; base += kThreads) {
+                const int b = base + tid, p = b < a.B ? pages_of(a.kv_len[b]) : 0;
+                __syncthreads();
+                const int all = (int)block_sum(p, before), lo = (done + (int)before) * items;
+                if (lo <= x && x < lo + p * items) req_s = b, first_s = lo;
+                done += all;
+                if (x < done * items) break;
+            }
+            __syncthreads();
+        }
+        if (!few) req = req_s, first = first_s;
+    }
+    if (tid == 0) part_s[1] = parts;
     auto segment = [&](int x) {            // the one that starts at tile x, below x_end
         Segment z;
         int n, pages;
@@ -356,9 +402,13 @@ __global__ void __launch_bounds__(32 * kWarps<D, NT, ONE>, kPerSm<D, NT, ONE>) k
     // use).
     auto shared_of = [&](const Segment &w) {
         Shared sh{w.b, w.kvh, w.h0};
-        const int c1 = (int)(((long long)w.i1 * ctas - 1) / T);
-        sh.c0 = sh.k0 = (int)(((long long)(w.i0 + 1) * ctas - 1) / T);
-        sh.n = c1 - sh.c0 + 1;
+        if (part_s[1]) {   // (the same thread's)
+            sh.c0 = part_s[0], sh.n = part_s[1];
+        } else {
+            sh.c0 = (int)(((long long)(w.i0 + 1) * ctas - 1) / T);
+            sh.n = (int)(((long long)w.i1 * ctas - 1) / T) - sh.c0 + 1;
+        }
+        sh.k0 = sh.c0;
         sh.groups = sh.n >= kGroupFrom ? sh.n / kGroup : 0;
         if (sh.groups) {
             const int at = min((c - sh.c0) / kGroup, sh.groups - 1);
