@@ -1406,8 +1406,9 @@ template <typename T>
 cudaError_t launch_rows(const SampleArgs &a, cudaStream_t s) {
     auto seg = [&](int C) { return ((a.V + 16 / (int)sizeof(T) - 1 + C - 1) / C + kGroup - 1) / kGroup * kGroup; };
     // The fewest CTAs a row whose segments let two of them share an SM (228 KB, of which each takes one for itself); more where
-    // there are few rows, but no more than SMs (twice as many and not, top-k 50: 20 rows of 32000 13.0 and 10.8 us, 38 rows of
-    // 50272 22.9 and 13.2, 64 rows 13.8 and 13.3; top-p 0.9: 22.5 and 20.4 of 20 rows, 24.8 and 27.1 of 64).
+    // there are few rows: four while nearly all clusters run at once, eight while every CTA has an SM. (With twice as many CTAs
+    // and not, top-k 50: 38 rows of 50272 22.9 and 13.2 us, 76 rows 23.5 and 14.3, 20 rows of 32000 13.0 and 10.8; but 64 rows
+    // of 50272 from the whole distribution, launched one by one, 10.2 and 12.5, with top-p 0.9 24.8 and 27.1.)
     constexpr size_t kHalf = (228 / 2 - 1) * 1024;
     int C = 1;
     while (C < 8 && smem_of<kCluster>(seg(C), sizeof(T)) > kHalf) C *= 2;
@@ -1416,7 +1417,7 @@ cudaError_t launch_rows(const SampleArgs &a, cudaStream_t s) {
     // 100 and 78, 234 and 143, 179 and 136; 100 rows 16 and 17, 40 and 37, 52 and 63). Not filtered, a row is read from shared
     // memory (1024 rows 77 and 95 us).
     if (C > 1 && a.R > num_sms() && (a.top_k || a.top_p || a.min_p)) return launch_as<T, kStream>(a, 1, seg(1), s);
-    while (C < 8 && 2LL * a.R * C <= num_sms() && seg(2 * C) >= 2048) C *= 2;
+    while (C < 8 && 2LL * a.R * C <= (C < 4 ? num_sms() * 17 / 10 : num_sms()) && seg(2 * C) >= 2048) C *= 2;
     // Short rows, where there are more than the SMs hold at once in large CTAs (small CTAs and large: settings by row and
     // distributions, 1000 tokens, 300 rows 12.7 and 12.8 us, 1200 rows 16.5 and 41; 4000 tokens, 450 rows 35 and 28, 1200 rows
     // 45 and 57).
