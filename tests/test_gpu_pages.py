@@ -205,3 +205,20 @@ def test_most_slots_there_can_be():
     assert slot[:64].tolist() == list(range(192, 256)) and slot[64:67].tolist() == [64, 128, 129]
     for at in range(67, n, 1 << 28):
         assert int(slot[at:at + (1 << 28)].max()) == -1 and int(slot[at:at + (1 << 28)].min()) == -1
+
+
+def test_ring_after_a_request_that_is_not_served():
+    """What the pool cannot serve takes nothing from the ring, also where requests that need no pages follow: the start and the
+    count are those of the pages that were handed out (none here, one in the second call)."""
+    i32 = lambda *a: cu(list(a))
+    pool = api.PagePool(cu([[-1, -1, -1], [2, -1, -1], [-1, -1, -1]]), i32(0, 1, 0), i32(0, 1, 3, 0), i32(2, 1, 0))
+    slot, status = torch.full((104,), -9, dtype=torch.int32, device="cuda"), torch.zeros(1, dtype=torch.int32, device="cuda")
+    api.kv_pages_build(pool, i32(100, 11, 0), i32(0, 10, 0), slot, None, status=status)
+    assert status.item() == api.STATUS_NO_PAGES
+    assert pool.state.tolist() == [2, 1, 0] and pool.held.tolist() == [0, 1, 0]
+    assert slot.tolist() == [-1] * 100 + [2 * PK + 10] + [-1] * 3
+    status.zero_()
+    api.kv_pages_build(pool, i32(60, 100, 0), i32(0, 100, 0), slot, None, status=status)   # the first takes it, the second gets none
+    assert status.item() == api.STATUS_NO_PAGES
+    assert pool.state.tolist() == [3, 0, 0] and pool.held.tolist() == [1, 1, 0] and int(pool.block_table[0, 0]) == 3
+    assert slot[:60].tolist() == list(range(3 * PK, 3 * PK + 60)) and slot[60:].max() == -1
