@@ -77,7 +77,8 @@ def test_attention_refusals(lib, kw, rc, word):
     (dict(stride=(1 << 31) + 1), b"stride"), (dict(token=None), b"no output"), (dict(u=None), b"needs u"),
     (dict(probs=OK), b"place of its own"), (dict(probs=P(0x30000), kept=P(0x30000)), b"place of its own"),
     (dict(kept=OK, dt=1), b"place"), (dict(kept=OK, stride=101), b"place"), (dict(probs=P(0x30002)), b"4-byte"),
-    (dict(u=P(0x30001)), b"4-byte"), (dict(token=P(0x30002)), b"4-byte")])
+    (dict(u=P(0x30001)), b"4-byte"), (dict(token=P(0x30002)), b"4-byte"),
+    (dict(token=P(0x30000), u=P(0x30000)), b"place of its own"), (dict(token=OK), b"place of its own")])
 def test_sample_refusals(lib, kw, word):
     a = {**dict(token=P(0x20000), probs=None, kept=None, logits=OK, stride=100, dt=0, u=OK, R=2, V=100), **kw}
     rc = lib.sample_tokens(a["token"], a["probs"], a["kept"], a["logits"], a["stride"], a["dt"], a["u"], None, None, None, None, a["R"],

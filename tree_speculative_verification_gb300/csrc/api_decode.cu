@@ -137,6 +137,8 @@ ts_status sample_tokens(int32_t *token, float *probs, float *kept, const void *l
         return set_error(TS_ERR_INVALID_ARG, "%s: probs needs a place of its own", who);
     if ((const void *)kept == logits && (dtype != TS_F32 || row_stride != V))
         return set_error(TS_ERR_INVALID_ARG, "%s: kept in the logits' place only where these are fp32, V apart", who);
+    if (token && (token == top_k || (const void *)token == u || (const void *)token == logits))
+        return set_error(TS_ERR_INVALID_ARG, "%s: token needs a place of its own", who);
     const ts_status st = check_words(who, token, probs, kept, u, temperature, top_k, top_p, min_p, status);
     if (st) return st;
     const ts::SampleArgs a{token, probs, kept,  logits, row_stride, u, temperature,
