@@ -1098,10 +1098,10 @@ __global__ void __launch_bounds__(Cfg<M>::NT, Cfg<M>::PER_SM) k_sample(SampleArg
         if (STREAM && listed && n_list > NT) {
             // ---- a long list's
             last = ~0ull;
-            if (by_k && n_list > top_k) last = choose(n_list, last, top, list_from, 0, std::false_type(), [&](u64) { return (u64)top_k; });
-            if (last == 0) last = ~0ull;   // (min-p keeps fewer)
+            // (fewer than top_k where min-p keeps fewer: then all of them, and the cut stays at its bound)
+            if (by_k && n_list >= top_k) last = choose(n_list, last, top, list_from, 0, std::false_type(), [&](u64) { return (u64)top_k; });
             if (by_p) last = choose(n_list, last, top, list_from, 0, std::true_type(), threshold);
-            if (by_k || by_p) cut_at(last);
+            if (last != ~0ull) cut_at(last);
             __syncthreads();
             clear_units();
             add_listed(sm.list, n_list, last);
