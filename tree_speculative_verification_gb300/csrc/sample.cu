@@ -917,8 +917,9 @@ __global__ void __launch_bounds__(Cfg<M>::NT, Cfg<M>::PER_SM) k_sample(SampleArg
     auto choose = [&](int n, u64 most, float to, float from, u64 ahead, auto masses, auto want_of) {
         reset();   // (the list stays)
         const float y0 = weight.exponent(to), scale = (BINS - 1) / (weight.exponent(from) - y0 - 0.01f);
+        // (held in float to the last bin, whatever the distance: the sum with 1.5 * 2^23 is a whole number in its lower bits)
         auto bin = [&](float x) {
-            return min(BINS - 1, __float_as_int(fmaf(weight.exponent(x) - y0, scale, 12582912.f)) & (2 * BINS - 1));
+            return __float_as_int(fminf((weight.exponent(x) - y0) * scale, (float)(BINS - 1)) + 12582912.f) & (2 * BINS - 1);
         };
         uint32_t(*const h)[BINS] = sm.h[masses ? warp % F::REP : 0];
         for (int i = tid; i < n; i += NT) {
@@ -1078,7 +1079,9 @@ __global__ void __launch_bounds__(Cfg<M>::NT, Cfg<M>::PER_SM) k_sample(SampleArg
             });
             b = find_bin(std::false_type(), [&](u64) { return (u64)top_k; }, want, before, own_sum);
             listed = b >= 0 && before + own_sum <= SORT;
-            if (listed) list_from = vscale == 0.f ? low : fmaxf(low, top - (b + 1) / vscale * 1.00001f - fabsf(top) * 1e-6f);
+            // (the last bin has whatever is below it)
+            if (listed)
+                list_from = vscale == 0.f || b == BINS - 1 ? low : fmaxf(low, top - (b + 1) / vscale * 1.00001f - fabsf(top) * 1e-6f);
             if (b >= 0 && own_sum > SORT) cut_at(bisect(top_k, false));
             else if (b >= 0) {   // (otherwise fewer than k tokens: all are kept)
                 groups([&](int, const float (&x)[4], int id) {
