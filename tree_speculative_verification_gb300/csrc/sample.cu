@@ -1318,16 +1318,19 @@ __global__ void __launch_bounds__(Cfg<M>::NT, Cfg<M>::PER_SM) k_sample(SampleArg
                 bool mine = at <= want && want < at + sum;
                 if (!__any_sync(~0u, mine)) mine = __clz(__ballot_sync(~0u, sum != 0)) == 31 - lane;
                 if (mine) {   // (the last of any weight, where roundings leave none)
+                    // (four light ones may have a weight together where none has one by itself: the largest kept one, then)
                     u64 left = want - at;
-                    int t = -1;
+                    int t = -1, best = -1;
+                    float most = -INFINITY;
                     bool found = false;
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
                         if (w[e] && !found) t = id + e;
+                        if (kept(x[e], id + e) && x[e] > most) best = id + e, most = x[e];
                         found |= left < w[e];
                         left -= w[e];
                     }
-                    a.token[r] = t;
+                    a.token[r] = t < 0 ? best : t;
                 }
             }
         }
