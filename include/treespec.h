@@ -601,7 +601,8 @@ size_t treespec_decode_workspace_size(int B, int Hq, int Hkv, int d);
  * A row with NaN or +inf, or with nothing but -inf (TS_STATUS_NONFINITE), or with
  * u or a setting out of its range (NaN, T negative or infinite, top_k negative;
  * TS_STATUS_INDEX) gets token -1 and its rows of probs and kept NaN, which a
- * verifier refuses in turn. V <= 2^18. Outputs overlap nothing but as said of kept.
+ * verifier refuses in turn. V <= 2^18. Outputs overlap nothing but as said of kept; one on u
+ * or on a setting, in part even, is refused.
  */
 #define TS_DROPPED_LOGIT (-1e30f)
 ts_status sample_tokens(int32_t *token, float *probs, float *kept, const void *logits, long long row_stride,

@@ -23,6 +23,11 @@ ts_status check_words(const char *who, P... p) {
     return set_error(TS_ERR_INVALID_ARG, "%s: an array of 32-bit numbers is not 4-byte aligned", who);
 }
 
+// Whether two arrays of so many 32-bit numbers share any (NULL: none).
+bool overlap(const void *p, long long n, const void *q, long long m) {
+    return p && q && (uintptr_t)p < (uintptr_t)q + 4 * m && (uintptr_t)q < (uintptr_t)p + 4 * n;
+}
+
 ts_status check_pages(const ts_paged_kv *kv, int H, int d, const char *who) {
     if (!kv) return set_error(TS_ERR_INVALID_ARG, "%s: cache is NULL", who);
     if (!kv->k_pages || !kv->v_pages) return set_error(TS_ERR_INVALID_ARG, "%s: pages are NULL", who);
@@ -137,10 +142,20 @@ ts_status sample_tokens(int32_t *token, float *probs, float *kept, const void *l
         return set_error(TS_ERR_INVALID_ARG, "%s: probs needs a place of its own", who);
     if ((const void *)kept == logits && (dtype != TS_F32 || row_stride != V))
         return set_error(TS_ERR_INVALID_ARG, "%s: kept in the logits' place only where these are fp32, V apart", who);
-    if (token && (token == top_k || (const void *)token == u || (const void *)token == logits))
+    if (token && (const void *)token == logits)
         return set_error(TS_ERR_INVALID_ARG, "%s: token needs a place of its own", who);
     const ts_status st = check_words(who, token, probs, kept, u, temperature, top_k, top_p, min_p, status);
     if (st) return st;
+    // a row's CTAs read other rows' settings too, whose CTAs may already write
+    const void *const set[] = {u, temperature, top_k, top_p, min_p};
+    for (const void *p : set) {
+        const char *const what = overlap(token, R, p, R)                    ? "token"
+                                 : overlap(probs, (long long)R * V, p, R) ? "probs"
+                                 : overlap(kept, (long long)R * V, p, R)  ? "kept"
+                                                                          : nullptr;
+        if (what)
+            return set_error(TS_ERR_INVALID_ARG, "%s: %s needs a place of its own, apart from u and the settings", who, what);
+    }
     const ts::SampleArgs a{token, probs, kept,  logits, row_stride, u, temperature,
                            top_k, top_p, min_p, R,      V,          status};
     return done(ts::launch_sample(a, dtype, stream), who);
