@@ -305,6 +305,8 @@ __global__ void __launch_bounds__(Cfg<M>::NT, Cfg<M>::PER_SM) k_sample(SampleArg
     const float temp = a.temperature ? a.temperature[r] : 1.f, top_p = a.top_p ? a.top_p[r] : 1.f,
                 min_p = a.min_p ? a.min_p[r] : 0.f, u = a.u ? a.u[r] : 0.f;
     const int top_k = a.top_k ? a.top_k[r] : 0;
+    const bool wrong =
+        !(temp >= 0.f && temp < INFINITY) || isnan(top_p) || isnan(min_p) || top_k < 0 || !(u >= 0.f && u < 1.f);
     const bool greedy = temp < 7.888609052210118e-31f;   // 2^-100
     const float by = temp > 1.2676506002282294e30f ? 5.421010862427522e-20f : 1.f;   // 2^-64 above 2^100
     if (tid == 0) {   // (64-bit arithmetic is slow enough here that one thread does it for all)
@@ -387,9 +389,9 @@ __global__ void __launch_bounds__(Cfg<M>::NT, Cfg<M>::PER_SM) k_sample(SampleArg
 #pragma unroll
     for (int o = W / 2; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
     const float ch = sm.ch;
-    // a lower bound of the row's sum of weights: these tokens'
+    // a lower bound of the row's sum of weights: these tokens' (a number, whatever the settings: NaN says that logits are bad)
     float some = 1.f;
-    const bool bound = top_p < 1.f && (top_k <= 0 || top_k >= V) && !(min_p > 0.f);
+    const bool bound = !wrong && top_p < 1.f && (top_k <= 0 || top_k >= V) && !(min_p > 0.f);
     if (bound) {
         some = 0.f;
 #pragma unroll
@@ -418,8 +420,6 @@ __global__ void __launch_bounds__(Cfg<M>::NT, Cfg<M>::PER_SM) k_sample(SampleArg
         if (t > -INFINITY) some += x * ex2((t - top) * by * ch);
     }
     bad |= top == -INFINITY;
-    const bool wrong =
-        !(temp >= 0.f && temp < INFINITY) || isnan(top_p) || isnan(min_p) || top_k < 0 || !(u >= 0.f && u < 1.f);
 
     // four elements of the segment from position pos on, a multiple of 4
     auto get4 = [&](int pos, float (&x)[4]) {
