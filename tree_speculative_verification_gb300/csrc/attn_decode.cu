@@ -507,8 +507,8 @@ __global__ void __launch_bounds__(32 * kWarps<D, NT, ONE>, kPerSm<D, NT, ONE>) k
                     }
             }
             // P^T as the second factor, in two bf16 numbers: the upper half of the fp32 number, and what is left, rounded
-            // (in all 16 bits of each weight). What is left counts as 2^-126 at least, so that an infinite value comes
-            // through as one
+            // (in all 16 bits of each weight). Where nothing is left it counts as 2^-24 of the weight (2^-133 at least, the lowest
+            // number there is), so that an infinite value comes through as one; a weight of 0 has neither half
             uint32_t hi[NT][2], lo[NT][2];
 #pragma unroll
             for (int j = 0; j < NT; ++j) {
@@ -522,9 +522,10 @@ __global__ void __launch_bounds__(32 * kWarps<D, NT, ONE>, kPerSm<D, NT, ONE>) k
                     const float p0 = p[j][2 * r], p1 = p[j][2 * r + 1];
                     const uint32_t u0 = __float_as_uint(p0), u1 = __float_as_uint(p1);
                     hi[j][r] = transposed(__byte_perm(u0, u1, 0x7632));
-                    const __nv_bfloat162 rest =
-                        __floats2bfloat162_rn(fmaxf(p0 - __uint_as_float(u0 & 0xffff0000u), 1.17549435e-38f),
-                                              fmaxf(p1 - __uint_as_float(u1 & 0xffff0000u), 1.17549435e-38f));
+                    auto left = [](float w, uint32_t u) {
+                        return fminf(w, fmaxf(w - __uint_as_float(u & 0xffff0000u), fmaxf(w * 0x1p-24f, 0x1p-133f)));
+                    };
+                    const __nv_bfloat162 rest = __floats2bfloat162_rn(left(p0, u0), left(p1, u1));
                     lo[j][r] = transposed(*reinterpret_cast<const uint32_t *>(&rest));
                 }
             }
