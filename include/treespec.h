@@ -596,8 +596,10 @@ size_t treespec_decode_workspace_size(int B, int Hq, int Hkv, int d);
  *   kept   [R][V] fp32 (may be NULL; may be the logits where these are fp32, V
  *          apart): the logits of the kept tokens, TS_DROPPED_LOGIT elsewhere; target
  *          rows for verify_mss at the same temperature
- * Weights are counted in units of 2^-36 of the largest (a token below 2^-37 of it
- * may have none), and summed exactly.
+ * Where top_p's cut and the token fall is decided as in 64-bit arithmetic: by sums
+ * that do not depend on their order, right to 2^-42 of each weight, so that only what
+ * is nearer to a border than some 1e-13 of the whole sum is open. A token below 2^-60
+ * of the sum may have no weight. probs are right to 2^-20 of each number.
  * A row with NaN or +inf, or with nothing but -inf (TS_STATUS_NONFINITE), or with
  * u or a setting out of its range (NaN, T negative or infinite, top_k negative;
  * TS_STATUS_INDEX) gets token -1 and its rows of probs and kept NaN, which a

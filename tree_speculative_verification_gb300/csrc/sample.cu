@@ -8,8 +8,12 @@
 //
 // Whether a token is kept, and which token a uniform number falls on, are
 // comparisons of sums over a vocabulary: in fp32 a row of 50k tokens is decided
-// wrongly about once in a thousand draws. So weights are whole numbers, the
-// largest 2^36 (Weights): their sums are exact, whatever the order.
+// wrongly about once in a thousand draws. So sums are whole numbers, whose order
+// does not matter, of weights that are right to 2^-23 of themselves (Weights), and
+// so off by a bound that is known. Where u or top_p falls within that bound of a
+// border (one row of 50k tokens in some four hundred), it is weighed once more, to
+// 2^-43 (exact_sum), and decided by that: as in 64-bit floating point, but for what
+// that itself leaves open.
 //
 // Passes over a row: maximum; where a filter needs it a bound of the candidates
 // for the last token kept, and these; kept weights; output rows. Three layouts:
@@ -48,7 +52,6 @@ struct Cfg {
     static constexpr int PER_SM = M == kSmall ? 8 : 2;       // CTAs
 };
 constexpr int kGroup = 128;       // elements of a warp's turn
-constexpr int kLarges = 64;       // places of large weights that a warp puts off
 // Up to so many rows are taken in an order of their settings (1024 rows of 50272, settings by row and distributions: 136 us and
 // 150; all with top-k 50: 78 and 74).
 constexpr int kOrderedRows = 2048;
@@ -70,11 +73,15 @@ __device__ __forceinline__ u64 part64(float x) { return __float2ull_rz(x * 18446
 constexpr int kIdBits = 18;
 __device__ __forceinline__ u64 order_of(uint32_t key, int id) { return (u64)(uint32_t)~key << kIdBits | (uint32_t)id; }
 
-// 2^(j / 8) as two floats each.
-__constant__ float kRootHi[8] = {0x1.0000000000000p+0f, 0x1.172b840000000p+0f, 0x1.306fe00000000p+0f, 0x1.4bfdae0000000p+0f,
-                                 0x1.6a09e60000000p+0f, 0x1.8ace540000000p+0f, 0x1.ae89fa0000000p+0f, 0x1.d5818e0000000p+0f};
-__constant__ float kRootLo[8] = {0x0.0p+0f, -0x1.c157420000000p-27f, 0x1.4636e20000000p-25f, -0x1.593abc0000000p-25f,
-                                 0x1.9fcef40000000p-26f, 0x1.15506e0000000p-27f, -0x1.a94b140000000p-26f, -0x1.822dbc0000000p-27f};
+// 2^(j / 32) in units of 2^-62.
+__device__ const u64 kRoot[32] = {
+    0x4000000000000000ull, 0x4166c34c5615d0ecull, 0x42d561b3e6243d8aull, 0x444c0740496d4294ull, 0x45cae0f1f545eb73ull,
+    0x47521cc5a2e6a9e0ull, 0x48e1e9b9d588e19bull, 0x4a7a77d47f7b84b1ull, 0x4c1bf828c6dc54b8ull, 0x4dc69cdceaa72a9cull,
+    0x4f7a993048d088d7ull, 0x513821818624b40cull, 0x52ff6b54d8a89c75ull, 0x54d0ad5a753e077cull, 0x56ac1f752150a563ull,
+    0x5891fac0e95612c8ull, 0x5a827999fcef3242ull, 0x5c7dd7a3b17dcf75ull, 0x5e8451cfac061b5full, 0x6096266533384a2bull,
+    0x62b39508aa836d6full, 0x64dcdec3371793d1ull, 0x6712460a8fc24072ull, 0x69540ec8f895722dull, 0x6ba27e656b4eb57aull,
+    0x6dfddbcbed791babull, 0x70666f76154a7089ull, 0x72dc8373be41a454ull, 0x75606373ee921c97ull, 0x77f25ccdee6d7ae6ull,
+    0x7a92be8a92436616ull, 0x7d41d96db915019dull};
 
 // Two floats in one register pair, worked on at once.
 __device__ __forceinline__ u64 two(float a, float b) {
@@ -99,69 +106,109 @@ __device__ __forceinline__ u64 fma2(u64 a, u64 b, u64 c) {
     return r;
 }
 
-// exp((x - top) / T) in units of 2^-36, y = (x - top) log2(e) / T. (In these units four light ones, below 2^-6 each, add up in 32
-// bits.)
-//  - Weights below 2^-6: y rounded to nearest once (the difference before it once more) and ex2, together to some 2^-20 of
-//    themselves, as often up as down: the errors of thousands of them add up to little.
-//  - From 2^-6 on to the unit and some 2^-38 of themselves: y as a sum of two floats (the difference and the products by
-//    their exact errors), y = n + j / 8 + g, and 2^y = 2^n 2^(j/8) (1 + t + t^2 / 2 + ..), t = g ln 2, |t| < 0.0434: the
-//    first two terms as sums of two floats, the rest (below 2^-16) in one.
-constexpr float kLarge = -6.f, kUnits = 68719476736.f;
+__device__ __forceinline__ u64 shifted(u64 v, int by) {   // 0 from 64 on
+    u64 r;
+    asm("shr.u64 %0, %1, %2;" : "=l"(r) : "l"(v), "r"(by));
+    return r;
+}
+
+// exp((x - top) / T) = 2^y to some 2^-43 of itself (near the top 2^-44), in units of 2^(drop - 62). y = (x - top) c,
+// c = log2(e) / T = ch + cl; by of x and top: 1, or 2^-64 where T is above 2^100, so that no difference that counts overflows.
+// The difference and the products with their errors: y = Y - r, Y = n + j / 32 + g; t = (g - r) ln 2 and its square as sums of two
+// floats, 2^(g - r) = 1 + t + t^2 / 2 + .. in whole numbers of 2^-62 where it is large. (-inf: 0)
+__device__ __forceinline__ u64 exact_of(float x, float top, float ch, float cl, float by, int drop) {
+    const float v = __fmul_rn(x, -by), d = __fadd_rn(v, top), b = __fsub_rn(d, v);
+    const float low = __fadd_rn(__fsub_rn(v, __fsub_rn(d, b)), __fsub_rn(top, b));   // d + low = top - x
+    const float Y = __fmul_rn(d, -ch), r = __fmaf_rn(low, ch, __fmaf_rn(d, cl, __fmaf_rn(d, ch, Y)));
+    const int m = __float2int_rn(fmaxf(Y, -100.f) * 32.f);
+    const float g = __fmaf_rn((float)m, -0.03125f, Y);
+    const float L = 0.693147182464599609375f, Ll = -1.904654299957767e-09f;   // ln 2
+    const float t = __fmul_rn(g, L), tl = __fmaf_rn(r, -L, __fmaf_rn(g, Ll, __fmaf_rn(g, L, -t)));
+    const float q = __fmul_rn(t, t), ql = __fmaf_rn(tl, tl, __fmaf_rn(t, 2.f * tl, __fmaf_rn(t, t, -q)));
+    const float rest = tl + fmaf(0.5f, ql, fmaf(q * 0.5f, fmaf(t * (1.f / 3), tl, tl), t * q * fmaf(t, fmaf(t, 1.f / 120, 1.f / 24), 1.f / 6)));
+    // (conversions to 64 bits are several times slower than these four)
+    const int t31 = __float2int_rn(t * 0x1p31f);
+    const long long p = ((long long)t31 << 31) + __float2int_rn(__fmaf_rn((float)t31, -0x1p-31f, t) * 0x1p62f) +
+                        ((long long)__float2int_rn(q * 0x1p43f) << 18) + ((long long)__float2int_rn(rest * 0x1p47f) << 15);
+    const u64 R = kRoot[m & 31];
+    return Y > -100.f ? shifted(R + (u64)__mul64hi((long long)R, p << 2), drop - (m >> 5)) : 0;
+}
+// (not inlined: for rows that are weighed once more, and the tokens at their borders)
+__device__ __noinline__ u64 exact_one(float x, float top, float ch, float cl, float by, int drop) {
+    return exact_of(x, top, ch, cl, by, drop);
+}
+__device__ __noinline__ u64 exact_sum(float x0, float x1, float x2, float x3, float top, float ch, float cl, float by, int drop) {
+    return exact_of(x0, top, ch, cl, by, drop) + exact_of(x1, top, ch, cl, by, drop) + exact_of(x2, top, ch, cl, by, drop) +
+           exact_of(x3, top, ch, cl, by, drop);
+}
+
+// 2^(x c - N), c = log2(e) / T = ch + cl and N the whole number next to top c: the weights of all tokens times one number from
+// [0.7, 1.42], which no comparison of their sums sees. x c = n + f, n whole and |f| <= 1/2 (the difference of x ch and n is rounded
+// once, whatever they are), 2^f by a polynomial (interpolated at Chebyshev's points, 2^-26.7 of itself), n in the exponent: to
+// 2^-23.3 of itself. Then as whole numbers of 2^-42, the nearest.
+constexpr float kUnits = 4398046511104.f;    // 2^42
+constexpr int kUnitBits = 42;
+constexpr float kOff = 0x1p-23f;
+constexpr float kMagic = 12582912.f;         // 1.5 * 2^23: a sum with it is a whole number in its lower bits
+// Numbers from [0, 2) as a 2^-20 + b 2^-42, a and b whole, |b| <= 2^21, in the lower bits of sums with these:
+constexpr float kHigh = 0x1.8p3f, kLow = 0x1.8p-19f;
+constexpr uint32_t kHighBits = 0x41400000u, kLowBits = 0x36400000u;
 struct Weights {
-    float top, ch, cl;   // log2(e) / T = ch + cl, 0 < cl < 2^-22 ch: -inf stays -inf in both products
-    float by;            // of x, top and T: 1, or 2^-64 where T is above 2^100, so that no difference that counts overflows
-    __device__ __forceinline__ float exponent(float x) const {
-        const float d = fmaf(x, by, -top);
-        return fmaf(d, ch, d * cl);
+    float top, ch, cl, by;   // (top times by: for exact weights, and distributions)
+    float floor, magic;      // what is below the former weighs as that, less than a unit; kMagic - N
+    bool slow;               // x c are too large numbers for this: every weight by exact_one
+    // (x - top) c, rounded; falls with x, or stays
+    __device__ __forceinline__ float exponent(float x) const { return __fmul_rn(__fadd_rn(__fmul_rn(x, -by), top), -ch); }
+    __device__ __forceinline__ u64 exact(float x0, float x1, float x2, float x3, int drop) const {
+        return exact_sum(x0, x1, x2, x3, top, ch, cl, by, drop);
     }
-    __device__ __forceinline__ void exponents(const float (&x)[4], float (&y)[4]) const {   // the same of four
-        const u64 b = two(by, by), t = two(-top, -top), h = two(ch, ch), l = two(cl, cl);
+    __device__ __forceinline__ u64 exact(float x, int drop) const { return exact_one(x, top, ch, cl, by, drop); }
+    __device__ __forceinline__ void four(const float (&x)[4], float (&w)[4]) const {
+        if (slow) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) w[e] = __ull2float_rn(exact(x[e], 62 - kUnitBits)) * (1.f / kUnits);
+            return;
+        }
+        const u64 h = two(ch, ch), l = two(cl, cl), minus = two(-1.f, -1.f), c = two(magic, magic);
 #pragma unroll
         for (int e = 0; e < 4; e += 2) {
-            const u64 d = fma2(two(x[e], x[e + 1]), b, t);
-            one_each(fma2(d, h, mul2(d, l)), y[e], y[e + 1]);
+            const u64 v = two(fmaxf(x[e], floor), fmaxf(x[e + 1], floor)), k = fma2(v, h, c);
+            const u64 f = fma2(v, l, fma2(v, h, fma2(k, minus, c)));
+            u64 q = fma2(f, two(0x1.4413dcp-13f, 0x1.4413dcp-13f), two(0x1.5f0906p-10f, 0x1.5f0906p-10f));
+            q = fma2(f, q, two(0x1.3b2a52p-7f, 0x1.3b2a52p-7f));
+            q = fma2(f, q, two(0x1.c6af6cp-5f, 0x1.c6af6cp-5f));
+            q = fma2(f, q, two(0x1.ebfbe0p-3f, 0x1.ebfbe0p-3f));
+            q = fma2(f, q, two(0x1.62e430p-1f, 0x1.62e430p-1f));
+            float k0, k1, p0, p1;
+            one_each(k, k0, k1);
+            one_each(fma2(f, q, two(1.f, 1.f)), p0, p1);
+            w[e] = __int_as_float(__float_as_int(p0) + (int)((uint32_t)__float_as_int(k0) << 23));   // (kMagic's bits are above 2^9)
+            w[e + 1] = __int_as_float(__float_as_int(p1) + (int)((uint32_t)__float_as_int(k1) << 23));
         }
     }
-    // (ex2 is low by 5.06e-8 of its value on the average of an octave, measured)
-    __device__ __forceinline__ static uint32_t whole(float e) { return __float2uint_rn(fmaf(e, kUnits, e * 3477.f)); }
-    __device__ __forceinline__ static uint32_t light(float y) { return whole(ex2(y)); }
-    // of four light ones: below 2^-4, so 32 bits
-    __device__ __forceinline__ static uint32_t light4(const float (&y)[4]) {
-        return whole((ex2(y[0]) + ex2(y[1])) + (ex2(y[2]) + ex2(y[3])));
+    __device__ __forceinline__ static u64 whole(float w) {
+        const float a = __fadd_rn(w, kHigh), b = __fadd_rn(__fsub_rn(w, __fsub_rn(a, kHigh)), kLow);
+        return ((u64)(__float_as_uint(a) - kHighBits) << 22) + (long long)(int)(__float_as_uint(b) - kLowBits);
     }
-    __device__ __forceinline__ void exponent(float x, float &yh, float &yl) const {
-        x *= by;
-        const float dh = x - top, bb = dh - x, dl = (x - (dh - bb)) - (top + bb);
-        yh = dh * ch;
-        yl = fmaf(dh, ch, -yh) + fmaf(dh, cl, dl * ch);
-    }
-    __device__ __noinline__ static u64 large(float x, float top, float ch, float cl) {   // of x times by (not inlined: it is for few)
-        if (x == top) return 1ull << 36;
-        float yh, yl;
-        Weights{top, ch, cl, 1.f}.exponent(x, yh, yl);
-        const float n8 = rintf(yh * 8.f), f = fmaf(n8, -0.125f, yh);
-        const float gh = f + yl, gl = yl - (gh - f);
-        const float L = 0.693147182464599609375f, Ll = -1.904654299957767e-09f;   // ln 2
-        const float th = gh * L, tl = fmaf(gh, L, -th) + fmaf(gh, Ll, gl * L);
-        const float hh = 0.5f * th, sh = hh * th, sl = fmaf(hh, th, -sh) + th * tl;
-        const float r = th * th * th * fmaf(th, fmaf(th, fmaf(th, 1.f / 720, 1.f / 120), 1.f / 24), 1.f / 6);
-        const float ph = th + sh, pl = (sh - (ph - th)) + ((tl + sl) + r);
-        const int m = (int)n8, j = m & 7, n = m >> 3;   // m = 8 n + j
-        const float Rh = kRootHi[j], Rl = kRootLo[j];
-        const float z = Rh * ph, hi = Rh + z, lo = (z - (hi - Rh)) + (fmaf(Rh, ph, -z) + fmaf(Rh, pl, fmaf(Rl, ph, Rl)));
-        // hi in [0.95, 2.1): a whole number of 2^-24; in units of 2^-42, then 2^(n - 36)
-        const long long v = ((long long)(int)(hi * 16777216.f) << 18) + __float2int_rn(lo * 4398046511104.f);
-        const int sft = 6 - n;
-        return (u64)((v + (1ll << (sft - 1))) >> sft);
+    // (not inlined: it is for few)
+    __device__ __noinline__ static u64 one(float x, float ch, float cl, float floor, float magic) {
+        x = fmaxf(x, floor);
+        const float k = __fmaf_rn(x, ch, magic), f = __fmaf_rn(x, cl, __fmaf_rn(x, ch, __fsub_rn(magic, k)));
+        float q = __fmaf_rn(f, 0x1.4413dcp-13f, 0x1.5f0906p-10f);
+        q = __fmaf_rn(f, q, 0x1.3b2a52p-7f);
+        q = __fmaf_rn(f, q, 0x1.c6af6cp-5f);
+        q = __fmaf_rn(f, q, 0x1.ebfbe0p-3f);
+        q = __fmaf_rn(f, __fmaf_rn(f, q, 0x1.62e430p-1f), 1.f);
+        return whole(__int_as_float(__float_as_int(q) + (int)((uint32_t)__float_as_int(k) << 23)));
     }
     __device__ __forceinline__ u64 operator()(float x) const {
-        const float y = exponent(x);
-        return y >= kLarge ? large(x * by, top, ch, cl) : light(y);
+        return slow ? whole(__ull2float_rn(exact(x, 62 - kUnitBits)) * (1.f / kUnits)) : one(x, ch, cl, floor, magic);
     }
     // Weights as floats, the largest `one`, to some 2^-21 of themselves.
     __device__ __forceinline__ float real(float x, float one) const {
-        float yh, yl;
-        exponent(x, yh, yl);
+        x *= by;
+        const float dh = x - top, bb = dh - x, dl = (x - (dh - bb)) - (top + bb), yh = dh * ch;
+        const float yl = fmaf(dh, ch, -yh) + fmaf(dh, cl, dl * ch);
         return yh > -150.f ? ex2(yh) * fmaf(yl, 0.693147182f, 1.f) * one : 0.f;
     }
     __device__ __forceinline__ void real4(const float (&x)[4], float one, float (&p)[4]) const {
@@ -179,6 +226,28 @@ struct Weights {
     }
 };
 
+// The sum of weights as whole numbers, below 2^10 of them, in two 32-bit sums.
+struct WeightSum {
+    uint32_t a = 0, b = 0;
+    __device__ __forceinline__ void add(const float (&w)[4]) {
+        const u64 high = two(kHigh, kHigh), minus = two(-kHigh, -kHigh), low = two(kLow, kLow);
+#pragma unroll
+        for (int e = 0; e < 4; e += 2) {
+            const u64 v = two(w[e], w[e + 1]), s = add2(v, high);
+            const u64 t = add2(fma2(add2(s, minus), two(-1.f, -1.f), v), low);
+            float s0, s1, t0, t1;
+            one_each(s, s0, s1);
+            one_each(t, t0, t1);
+            a += __float_as_uint(s0) + __float_as_uint(s1) - 2 * kHighBits;
+            b += __float_as_uint(t0) + __float_as_uint(t1) - 2 * kLowBits;
+        }
+    }
+    __device__ __forceinline__ u64 sum() const { return ((u64)a << 22) + (long long)(int)b; }
+    __device__ __forceinline__ u64 warp_sum() const {   // of four each
+        return ((u64)__reduce_add_sync(~0u, a) << 22) + (long long)__reduce_add_sync(~0u, (int)b);
+    }
+};
+
 // Four elements of a row as floats.
 __device__ __forceinline__ void load4(const float *p, float (&x)[4]) {
     const float4 v = *reinterpret_cast<const float4 *>(p);
@@ -190,8 +259,10 @@ __device__ __forceinline__ void load4(const __nv_bfloat16 *p, float (&x)[4]) {
     x[2] = __uint_as_float(v.y << 16), x[3] = __uint_as_float(v.y & 0xffff0000u);
 }
 
-__device__ __forceinline__ u64 warp_sum(uint32_t v) {
-    return ((u64)__reduce_add_sync(~0u, v >> 16) << 16) + __reduce_add_sync(~0u, v & 0xffffu);
+__device__ __forceinline__ u64 warp_sum(u64 v) {
+#pragma unroll
+    for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(~0u, v, o);
+    return v;
 }
 // An atomic sum in shared memory by halves, as there is no 64-bit one but by comparing and trying again.
 __device__ __forceinline__ void add64(u64 *p, u64 v) {
@@ -213,16 +284,20 @@ struct Shared {
     using F = Cfg<M>;
     uint32_t h[F::REP][3][F::BINS];   // the segment's histogram: counts in [0], or sums by 15, 15 and the rest of the bits
     u64 list[F::LIST];                // the cluster's candidates, in its first CTA, by their place in the order
-    u64 part[F::W];
-    u64 from[3][8];                   // what the cluster's CTAs tell one another, in turn
-    uint32_t larges[M == kStream ? F::W : 1][M == kStream ? kLarges : 1];
+    union {
+        u64 part[F::W];
+        float top[F::W];
+    };
+    u64 from[2][8];                   // what the cluster's CTAs tell one another, in turn
     u64 cut, kept;                    // the last token kept, the sum of all kept weights
+    u64 most;                         // the last one that top-k alone leaves
     u64 above, total;
     uint4 ring[M == kStream ? F::W * kRing * 32 : 1];   // groups on their way, the warps' own
-    float top[F::W];
     float ch, cl, mh, ml;             // log2(e) / T and T ln(min_p), as sums of two floats
     int n_list, n_kept, at;
+    bool cut_unsure, draw_unsure;     // by less than the sums may be off
 };
+static_assert(sizeof(Shared<kCluster>) <= 10752, "two CTAs an SM with 25216 fp32 elements each");
 template <Mode M>
 constexpr size_t kFixed = (sizeof(Shared<M>) + 15) / 16 * 16;   // then a sum a unit, then the segment
 
@@ -311,13 +386,14 @@ __global__ void __launch_bounds__(Cfg<M>::NT, Cfg<M>::PER_SM) k_sample(SampleArg
     const float by = temp > 1.2676506002282294e30f ? 5.421010862427522e-20f : 1.f;   // 2^-64 above 2^100
     if (tid == 0) {   // (64-bit arithmetic is slow enough here that one thread does it for all)
         const double c = 1.4426950408889634 / (greedy ? 1.0 : (double)(temp * by));
-        sm.ch = __double2float_rd(c);
-        sm.cl = fmaxf((float)(c - (double)sm.ch), fmaxf(sm.ch * 9.3132257e-10f, 1.4e-45f));
+        sm.ch = (float)c;
+        sm.cl = (float)(c - (double)sm.ch);
         if (min_p > 0.f) {
             const double m = (double)temp * log((double)fminf(min_p, 1.f));
             sm.mh = (float)m, sm.ml = (float)(m - (double)sm.mh);
         }
         sm.n_list = 0;
+        sm.draw_unsure = false;
     }
     auto empty = [&] {
         uint32_t *const h = &sm.h[0][0][0];
@@ -405,17 +481,21 @@ __global__ void __launch_bounds__(Cfg<M>::NT, Cfg<M>::PER_SM) k_sample(SampleArg
 #pragma unroll
         for (int o = W / 2; o; o >>= 1) some += __shfl_xor_sync(~0u, some, o);
     }
-    // one word to every CTA of the cluster, and all of theirs
-    auto tell = [&](int turn, u64 word) {
+    // one word to every CTA of the cluster; all of theirs, in the cluster's order
+    int turn = 0;
+    auto tell = [&](u64 word) {
+        u64 *const mine = sm.from[turn];
         if (tid < C) peer(tid).from[turn][rank] = word;
+        turn ^= 1;
         sync();
+        return mine;
     };
     if (!ONE && C > 1) asm volatile("barrier.cluster.wait.aligned;" ::: "memory");   // before anything is written to them
-    tell(0, (u64)__float_as_uint(top) | (u64)__float_as_uint(bad ? NAN : some) << 32);
-    for (int c = 0; c < C; ++c) top = fmaxf(top, __uint_as_float((uint32_t)sm.from[0][c]));
+    const u64 *const tops = tell((u64)__float_as_uint(top) | (u64)__float_as_uint(bad ? NAN : some) << 32);
+    for (int c = 0; c < C; ++c) top = fmaxf(top, __uint_as_float((uint32_t)tops[c]));
     some = 0.f;
     for (int c = 0; c < C; ++c) {
-        const float t = __uint_as_float((uint32_t)sm.from[0][c]), x = __uint_as_float((uint32_t)(sm.from[0][c] >> 32));
+        const float t = __uint_as_float((uint32_t)tops[c]), x = __uint_as_float((uint32_t)(tops[c] >> 32));
         bad |= isnan(x);
         if (t > -INFINITY) some += x * ex2((t - top) * by * ch);
     }
@@ -459,7 +539,9 @@ __global__ void __launch_bounds__(Cfg<M>::NT, Cfg<M>::PER_SM) k_sample(SampleArg
         sync();
         return;
     }
-    const Weights weight{top * by, ch, sm.cl, by};
+    // (4.0e6 is below 2^22: sums with kMagic - N are exact)
+    const bool slow = by != 1.f || !(fabsf(top * ch) < 4.0e6f);
+    const Weights weight{top * by, ch, sm.cl, by, top - 60.f / ch, kMagic - rintf(top * ch), slow};
     // tokens below this are not kept: min-p (the sum rounded up), and -inf
     float low = -3.402823466e38f;
     if (min_p > 0.f && !greedy) {
@@ -564,85 +646,33 @@ __global__ void __launch_bounds__(Cfg<M>::NT, Cfg<M>::PER_SM) k_sample(SampleArg
 #pragma unroll
         for (int e = 0; e < 4; ++e) x[e] = i + e < end ? (float)seg[i + e] : -INFINITY;
     };
-    // The same as weigh() by stretches: the large ones are noted in bits, and follow every 32 elements.
-    auto weigh_stretch = [&](auto take, auto small, auto large) {
+    // The weights of a thread's stretch, four at a time: add(x[4], w[4], id of x[0]).
+    auto weigh_stretch = [&](auto add) {
         const int i0 = min(SL, tid * unit), i1 = min(SL, i0 + unit);
 #pragma unroll 1
-        for (int i = i0; i < i1; i += 32) {
-            unsigned larges = 0;
-#pragma unroll
-            for (int k = 0; k < 32; k += 4) {
-                if (i + k >= i1) break;
-                float x[4], y[4];
-                four_at(i + k, i1, x);
-                weight.exponents(x, y);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const bool in = take(x[e], base + i + k + e - lead, y[e]);
-                    if (in && y[e] >= kLarge) larges |= 1u << (k + e);
-                    if (!in || y[e] >= kLarge) y[e] = -INFINITY;
-                }
-                small(y);
-            }
-            for (; larges; larges &= larges - 1) {
-                const float x = (float)seg[i + __ffs(larges) - 1];
-                large(weight.exponent(x), weight(x));
-            }
+        for (int i = i0; i < i1; i += 4) {
+            float x[4], w[4];
+            four_at(i, i1, x);
+            weight.four(x, w);
+            add(x, w, base + i - lead);
         }
     };
-    // Weights by groups, of the elements that take(value, id, y) says: small(y[4]) has those below kLarge and -inf for the
-    // others; large(place, y, weight) those that a warp puts off until it has 32 or no more groups, as one such element
-    // among 32 takes as long as 32. before(group, x[4], y[4]) and after(group) frame a group.
-    auto weigh = [&](auto each, auto before, auto take, auto small, auto large, auto after) {
-        auto *const put_off = sm.larges[warp];
-        int n = 0;
-        auto settle = [&](int from) {
-            __syncwarp();
-            if (from + lane < n) {
-                const int pos = put_off[from + lane];
-                const float x = (float)row[pos - lead];
-                large(pos, weight.exponent(x), weight(x));
-            }
-            n = from;
-            __syncwarp();
-        };
-        each([&](int g, const float (&x)[4], int id) {
-            float y[4];
-            weight.exponents(x, y);
-            before(g, x, y);
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                if (!take(x[e], id + e, y[e])) y[e] = -INFINITY;
-            if (__any_sync(~0u, fmaxf(fmaxf(y[0], y[1]), fmaxf(y[2], y[3])) >= kLarge))
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const unsigned is = __ballot_sync(~0u, y[e] >= kLarge);
-                    if (n + __popc(is) > kLarges) settle(n - 32);
-                    if (y[e] >= kLarge) {
-                        put_off[n + __popc(is & ((1u << lane) - 1))] = id + e + lead;
-                        y[e] = -INFINITY;
-                    }
-                    n += __popc(is);
-                }
-            small(y);
-            after(g);
-        });
-        if (n > 32) settle(n - 32);
-        if (n) settle(0);
-    };
-    // the sums of the groups' weights; see(group, x[4], y[4]) looks at all
+    // The sums of the groups' weights, of the elements that take(value, id, Y) says; see(group, x[4], w[4]) looks at all.
     auto sum_groups_and = [&](auto each, auto see, auto take) {
-        uint32_t w = 0;
-        weigh(each, [&](int g, const float (&x)[4], const float (&y)[4]) {
-            if (lane == 0) sums[g] = 0;
-            see(g, x, y);
-        }, take, [&](const float (&y)[4]) { w = Weights::light4(y); },
-              [&](int pos, float, u64 one) { add64(&sums[pos / kGroup], one); },
-              [&](int g) {
-            if (!__any_sync(~0u, w != 0)) return;
-            const u64 all = warp_sum(w);
-            __syncwarp();
-            if (lane == 0) sums[g] += all;
+        each([&](int g, const float (&x)[4], int id) {
+            float w[4];
+            weight.four(x, w);
+            see(g, x, w);
+            bool any = false;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const bool in = take(x[e], id + e, weight.exponent(x[e]));
+                any |= in, w[e] = in ? w[e] : 0.f;
+            }
+            WeightSum of;
+            of.add(w);
+            const u64 sum = __any_sync(~0u, any) ? of.warp_sum() : 0;
+            if (lane == 0) sums[g] = sum;
         });
     };
     // the sums of the units' weights
@@ -650,9 +680,13 @@ __global__ void __launch_bounds__(Cfg<M>::NT, Cfg<M>::PER_SM) k_sample(SampleArg
         if constexpr (STREAM) {
             sum_groups_and(groups_ahead, [](int, const float (&)[4], const float (&)[4]) {}, take);
         } else {
-            u64 mine = 0;
-            weigh_stretch(take, [&](const float (&y)[4]) { mine += Weights::light4(y); }, [&](float, u64 w) { mine += w; });
-            sums[tid] = mine;
+            WeightSum mine;
+            weigh_stretch([&](const float (&x)[4], float (&w)[4], int id) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) w[e] = take(x[e], id + e, weight.exponent(x[e])) ? w[e] : 0.f;
+                mine.add(w);
+            });
+            sums[tid] = mine.sum();
         }
     };
     auto clear_units = [&] {
@@ -682,28 +716,32 @@ __global__ void __launch_bounds__(Cfg<M>::NT, Cfg<M>::PER_SM) k_sample(SampleArg
         for (int o = 16; o; o >>= 1) before += __shfl_xor_sync(~0u, before, o);
         return v + before;
     };
-    int turn = 1;
-    // mass or number of the kept tokens up to `last` in the order, in the whole row
-    auto upto = [&](u64 last, bool masses) {
+    // a sum over the cluster's threads, for all of them
+    auto whole_sum = [&](u64 v) {
+        const u64 *const all = tell(block_sum(v));
+        v = 0;
+        for (int c = 0; c < C; ++c) v += all[c];
+        return v;
+    };
+    // sum of what is told of the kept tokens up to `last` in the order, in the whole row
+    auto upto = [&](u64 last, auto of) {
         u64 s = 0;
         groups([&](int, const float (&x)[4], int id) {
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-                if (kept(x[e], id + e) && order_of(key_of(x[e]), id + e) <= last) s += masses ? weight(x[e]) : 1;
+                if (kept(x[e], id + e) && order_of(key_of(x[e]), id + e) <= last) s += of(x[e]);
         });
-        tell(turn, block_sum(s));
-        s = 0;
-        for (int c = 0; c < C; ++c) s += sm.from[turn][c];
-        turn = 3 - turn;
-        return s;
+        return whole_sum(s);
     };
+    auto one_of = [](float) { return (u64)1; };
+    auto weight_of = [&](float x) { return weight(x); };
     // The last token of the shortest start of the kept ones that reaches `want` (mass or number), by bisection: for rows with
     // more candidates than the list takes, of equal or nearly equal values at the cut.
-    auto bisect = [&](u64 want, bool masses) {
+    auto bisect = [&](u64 want, auto of) {
         u64 lo = order_of(key_of(top), 0), hi = order_of(key_of(cut), min(cut_id, (1 << kIdBits) - 1));   // sum(lo - 1) < want <= sum(hi)
         while (lo < hi) {
             const u64 m = lo + (hi - lo) / 2;
-            if (upto(m, masses) >= want) hi = m;
+            if (upto(m, of) >= want) hi = m;
             else lo = m + 1;
         }
         return lo;
@@ -866,20 +904,33 @@ __global__ void __launch_bounds__(Cfg<M>::NT, Cfg<M>::PER_SM) k_sample(SampleArg
     };
     auto id_of = [&](u64 order) { return (int)(order & ((1 << kIdBits) - 1)); };
     auto value_at = [&](u64 order) { return value_of(~(uint32_t)(order >> kIdBits)); };
+    const bool by_p = top_p < 1.f && !greedy, by_k = top_k > 0 && top_k < V && !greedy;
+    // How far a difference between a sum of weights and f times all of them, near 0, may be off: S the latter. (Of a part A and
+    // the rest B, A - f (A + B) = (1 - f) A - f B, and both are f (1 - f) S there; and what is cut off below the units.)
+    auto slack = [&](u64 S, float f) { return (u64)(__ull2float_rn(S) * (2.f * kOff * f * (1.f - f))) + V; };
+    u64 mass = 0;             // of all that top-p takes its part of
+    bool cut_unsure = false;  // whether its cut is one by less than that
     auto threshold = [&](u64 S) {   // ceil(top_p S): a token is kept by top-p where the mass before it is below this
+        mass = S;
         const u64 p = part64(fminf(fmaxf(top_p, 0.f), 0.99999994f));
         return max(1ull, __umul64hi(p, S) + (p * S != 0));
     };
-    // Of a sorted list's first n entries, whose sum comes after `ahead`: how many are kept where a token is that has less than
-    // P(their sum) before it; and their sum.
-    auto kept_of = [&](const u64 *list, int n, u64 ahead, auto P_of, u64 &sum) {
+    // whether a cut is: w the last kept token's weight, upto the sum with it, both in units that P and so the threshold is in
+    // (ahead: what they leave out)
+    auto near_cut = [&](u64 w, u64 upto, u64 P, u64 ahead) {
+        const u64 E = slack(mass, fminf(fmaxf(top_p, 0.f), 1.f));
+        return (ahead + upto > w && upto - w + E >= P) || upto < P + E;
+    };
+    // Of a sorted list's first n entries, whose sum comes after `ahead` (and after `above`, which P leaves out): how many are kept
+    // where a token is that has less than P(their sum) before it; their sum, and whether that is near.
+    auto kept_of = [&](const u64 *list, int n, u64 ahead, u64 above, auto P_of, u64 &sum) {
         if (n <= NT) {
             const u64 w = tid < n ? weight(value_at(list[tid])) : 0, run = block_scan(w);
             if (tid == NT - 1) sm.total = run;
             __syncthreads();
             const u64 P = P_of(sm.total);
             const int m = __syncthreads_count(tid < n && ahead + run - w < P);
-            if (tid == m - 1) sm.kept = run;
+            if (tid == m - 1) sm.kept = run, sm.cut_unsure = by_p && near_cut(w, ahead + run, P, above);
             __syncthreads();
             sum = sm.kept;
             return m;
@@ -895,8 +946,9 @@ __global__ void __launch_bounds__(Cfg<M>::NT, Cfg<M>::PER_SM) k_sample(SampleArg
         u64 at = ahead + run - mine;
         for (int i = i0; i < i1; ++i) {
             if (at >= P) break;
-            at += weight(value_at(list[i]));
-            if (i == n - 1 || at >= P) sm.n_kept = i + 1, sm.kept = at - ahead;
+            const u64 w = weight(value_at(list[i]));
+            at += w;
+            if (i == n - 1 || at >= P) sm.n_kept = i + 1, sm.kept = at - ahead, sm.cut_unsure = by_p && near_cut(w, at, P, above);
         }
         __syncthreads();
         sum = sm.kept;
@@ -953,20 +1005,93 @@ __global__ void __launch_bounds__(Cfg<M>::NT, Cfg<M>::PER_SM) k_sample(SampleArg
         const int m = sm.n_list;
         if (m > ROOM) {
             cut_at(min(most, order_of(key_of(from), (1 << kIdBits) - 1)));
-            return bisect(ahead + want, masses);
+            if constexpr (masses) cut_unsure = true;   // (how near it is is not known)
+            if constexpr (masses) return bisect(ahead + want, weight_of);
+            else return bisect(ahead + want, one_of);
         }
         sort(some_of, m);
-        if constexpr (masses) return some_of[kept_of(some_of, m, before, [&](u64) { return want; }, sum) - 1];
-        else return some_of[(int)(want - before) - 1];
+        if constexpr (masses) {
+            const u64 last = some_of[kept_of(some_of, m, before, ahead, [&](u64) { return want; }, sum) - 1];
+            cut_unsure = sm.cut_unsure;
+            return last;
+        } else return some_of[(int)(want - before) - 1];
     };
 
-    const bool by_p = top_p < 1.f && !greedy, by_k = top_k > 0 && top_k < V && !greedy;
+    // What exact sums are asked for, where all weights sum to S: their exact ones, up to 1.42 times as much, fit 64 bits.
+    auto drop_of = [&](u64 S) { return max(0, 64 - __clzll(S) - kUnitBits - 1); };
+    // The cut of top-p among the tokens that are kept so far, by exact weights, from one that is off by a few tokens at most: their
+    // sum and that of those before the cut once, and then from token to token; where these are many, by bisection.
+    auto exact_cut = [&](u64 last) {
+        const int drop = drop_of(mass);
+        auto of = [&](float x) { return weight.exact(x, drop); };
+        u64 S = 0, before = 0;
+        groups([&](int, const float (&x)[4], int id) {
+            float all[4], some[4];
+            bool any = false, each = true;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                all[e] = kept(x[e], id + e) ? x[e] : -INFINITY;
+                const bool is = order_of(key_of(x[e]), id + e) < last;
+                some[e] = is ? all[e] : -INFINITY;
+                any |= some[e] > -INFINITY, each &= some[e] == all[e];
+            }
+            const u64 w = weight.exact(all[0], all[1], all[2], all[3], drop);
+            S += w;
+            if (each) before += w;
+            else if (any) before += weight.exact(some[0], some[1], some[2], some[3], drop);
+        });
+        S = whole_sum(S), before = whole_sum(before);
+        const u64 P = threshold(S);
+        // the kept token next to `at` in the order, before or after it (~0: there is none)
+        auto next_to = [&](u64 at, bool after) {
+            u64 best = after ? ~0ull : 0;
+            groups([&](int, const float (&x)[4], int id) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const u64 o = order_of(key_of(x[e]), id + e);
+                    if (kept(x[e], id + e) && (after ? o > at && o < best : o < at && o >= best)) best = o;
+                }
+            });
+#pragma unroll
+            for (int o = 16; o; o >>= 1) {
+                const u64 y = __shfl_xor_sync(~0u, best, o);
+                best = after ? min(best, y) : max(best, y);
+            }
+            __syncthreads();
+            if (lane == 0) sm.part[warp] = best;
+            __syncthreads();
+            for (int w = 0; w < W; ++w) best = after ? min(best, sm.part[w]) : max(best, sm.part[w]);
+            const u64 *const all = tell(best);
+            for (int c = 0; c < C; ++c) best = after ? min(best, all[c]) : max(best, all[c]);
+            return best;
+        };
+        constexpr int MANY = 32;
+        int steps = 0;
+        while (before >= P && ++steps <= MANY) {
+            last = next_to(last, false);
+            before -= of(value_at(last));
+        }
+        while (before < P && ++steps <= MANY) {
+            const u64 with = before + of(value_at(last));
+            if (with >= P) return last;
+            const u64 next = next_to(last, true);
+            if (next == ~0ull) return last;
+            before = with, last = next;
+        }
+        return bisect(P, of);
+    };
+
     u64 S = 0;                // the sum of all kept weights
     bool listed = false;      // all kept tokens are in the list,
     int n_list = 0;           // of this length: those up to
     u64 last = ~0ull;         // this place in the order
     bool summed = false;      // sums are those of the kept tokens
     bool drawn = false;
+    // ~0: all that are kept so far
+    auto cut_again = [&](u64 most) {
+        if (most != ~0ull) cut_at(most);
+        else cut = low, cut_id = 1 << kIdBits;
+    };
     // Values in equal bins from the top down: how far down the threads' largest of a number `want` lie. At least as many
     // tokens do, and few more.
     const float span = top - fmaxf(low, top - 64.f * fmaxf(temp, 0.25f)), vscale = span > 0.f ? (BINS - 1) / span : 0.f;
@@ -1051,10 +1176,10 @@ __global__ void __launch_bounds__(Cfg<M>::NT, Cfg<M>::PER_SM) k_sample(SampleArg
         if (lane == 0) sm.part[warp] = first;
         __syncthreads();
         for (int w = 0; w < W; ++w) first = min(first, sm.part[w]);
-        tell(turn, first);
-        for (int c = 0; c < C; ++c) first = min(first, sm.from[turn][c]);
+        const u64 *const all = tell(first);
+        for (int c = 0; c < C; ++c) first = min(first, all[c]);
         cut_at(first);
-        S = 1ull << 36;
+        S = 1ull << kUnitBits;
         drawn = true;
         if (a.token && rank == 0 && tid == 0) a.token[r] = cut_id;
     } else if (by_k || min_p > 0.f) {
@@ -1082,7 +1207,7 @@ __global__ void __launch_bounds__(Cfg<M>::NT, Cfg<M>::PER_SM) k_sample(SampleArg
             // (the last bin has whatever is below it)
             if (listed)
                 list_from = vscale == 0.f || b == BINS - 1 ? low : fmaxf(low, top - (b + 1) / vscale * 1.00001f - fabsf(top) * 1e-6f);
-            if (b >= 0 && own_sum > SORT) cut_at(bisect(top_k, false));
+            if (b >= 0 && own_sum > SORT) cut_at(bisect(top_k, one_of));
             else if (b >= 0) {   // (otherwise fewer than k tokens: all are kept)
                 groups([&](int, const float (&x)[4], int id) {
                     push4(x, id, [&](int e) { return x[e] >= low && (listed ? vbin(x[e]) <= b : vbin(x[e]) == b); });
@@ -1103,20 +1228,26 @@ __global__ void __launch_bounds__(Cfg<M>::NT, Cfg<M>::PER_SM) k_sample(SampleArg
             last = ~0ull;
             // (fewer than top_k where min-p keeps fewer: then all of them, and the cut stays at its bound)
             if (by_k && n_list >= top_k) last = choose(n_list, last, top, list_from, 0, std::false_type(), [&](u64) { return (u64)top_k; });
+            const u64 most = last;
             if (by_p) last = choose(n_list, last, top, list_from, 0, std::true_type(), threshold);
-            if (last != ~0ull) cut_at(last);
-            __syncthreads();
-            clear_units();
-            add_listed(sm.list, n_list, last);
-            summed = true;
+            if (cut_unsure) {
+                cut_again(most);
+            } else {
+                if (last != ~0ull) cut_at(last);
+                __syncthreads();
+                clear_units();
+                add_listed(sm.list, n_list, last);
+                summed = true;
+            }
         } else if (listed) {
             // ---- the list's kept entries, in the cluster's first CTA; and the token, if they are few, by every entry's thread
             if (rank == 0) {
                 int n = n_list;
                 if (by_k || by_p) sort(sm.list, n);
                 if (by_k) n = min(n, top_k);
+                const u64 most = n < n_list ? sm.list[n - 1] : ~0ull;
                 u64 sum;
-                n = kept_of(sm.list, n, 0, [&](u64 all) { return by_p ? threshold(all) : ~0ull; }, sum);
+                n = kept_of(sm.list, n, 0, 0, [&](u64 all) { return by_p ? threshold(all) : (mass = all, ~0ull); }, sum);
                 if (n <= NT / 4) {
                     u64 *const w_s = reinterpret_cast<u64 *>(sm.h);
                     const u64 e = tid < n ? sm.list[tid] : 0, w = tid < n ? weight(value_at(e)) : 0;
@@ -1127,22 +1258,33 @@ __global__ void __launch_bounds__(Cfg<M>::NT, Cfg<M>::PER_SM) k_sample(SampleArg
                         u64 at = 0;
 #pragma unroll 4
                         for (int i = 0; i < n; ++i) at += id_of(sm.list[i]) < id_of(e) ? w_s[i] : 0;
-                        if (at <= place && place < at + w) a.token[r] = id_of(e);
+                        if (at <= place && place < at + w) {
+                            const u64 E = slack(sum, u);
+                            a.token[r] = id_of(e);
+                            if (place - at < E || at + w - place <= E)
+                                for (int c = 0; c < C; ++c) peer(c).draw_unsure = true;
+                        }
                     }
                 }
                 if (tid < C) {
                     Sh &o = peer(tid);
                     o.n_kept = n, o.kept = sum, o.cut = by_k || by_p ? sm.list[n - 1] : ~0ull;
+                    o.most = most, o.total = mass, o.cut_unsure = sm.cut_unsure;
                 }
             }
             sync();
-            S = sm.kept, last = sm.cut;
-            if (by_k || by_p) cut_at(last);
-            if (sm.n_kept <= NT / 4) drawn = true;
-            else {
-                clear_units();
-                add_listed(peer(0).list, n_list, last);
-                summed = true;
+            S = sm.kept, last = sm.cut, mass = sm.total;
+            cut_unsure = sm.cut_unsure;
+            if (cut_unsure) {
+                cut_again(sm.most);
+            } else {
+                if (by_k || by_p) cut_at(last);
+                if (sm.n_kept <= NT / 4 && !sm.draw_unsure) drawn = true;
+                else {
+                    clear_units();
+                    add_listed(peer(0).list, n_list, last);
+                    summed = true;
+                }
             }
         }
     }
@@ -1152,37 +1294,38 @@ __global__ void __launch_bounds__(Cfg<M>::NT, Cfg<M>::PER_SM) k_sample(SampleArg
             // one on where these fit too; what is above and below is only summed
             constexpr int FITS = LIST * 4 / 5;
             Range z = vscale > 0.f ? estimate() : Range{low, top, 1 << 30, 0};
-            z.lo = fmaxf(low, fminf(z.lo, top + (kLarge - 0.01f) / (by * ch)));   // (no large ones are left out, and only tokens are in)
+            z.lo = fmaxf(low, z.lo);   // (only tokens are in)
+            WeightSum below;
             u64 rest = 0;
-            auto rest_of = [&](const float (&x)[4], const float (&y)[4]) {
-                float w[4];
+            auto rest_of = [&](const float (&x)[4], const float (&w)[4]) {
+                float of[4];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) w[e] = x[e] >= z.lo ? -INFINITY : y[e];
-                rest += Weights::light4(w);
+                for (int e = 0; e < 4; ++e) of[e] = x[e] >= z.lo ? 0.f : w[e];
+                below.add(of);
             };
             if (z.n_lo <= FITS) {
                 n_list = gather(z.lo, groups_ahead, [&](const float (&x)[4]) {
-                    float y[4];
-                    weight.exponents(x, y);
-                    rest_of(x, y);
+                    float w[4];
+                    weight.four(x, w);
+                    rest_of(x, w);
                 });
-                rest = block_sum(rest);
+                rest = block_sum(below.sum());
                 if (n_list <= LIST) {
                     last = choose(n_list, ~0ull, top, z.lo, 0, std::true_type(), [&](u64 mass) { return threshold(mass + rest); });
                     listed = cut_found = last != 0;
                 }
                 if (listed) clear_units();
             } else if (z.n_lo - z.n_hi <= FITS) {
-                sum_groups_and(groups, [&](int g, const float (&x)[4], const float (&y)[4]) {
+                sum_groups_and(groups, [&](int g, const float (&x)[4], const float (&w)[4]) {
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
                         if (x[e] >= z.lo && x[e] <= z.hi) {
                             if (by_notes) note(g, e);
                             else push(x[e], g * kGroup + lane * 4 + e - lead);
                         }
-                    rest_of(x, y);
+                    rest_of(x, w);
                 }, [&](float v, int, float) { return v > z.hi; });
-                rest = block_sum(rest);
+                rest = block_sum(below.sum());
                 u64 above = 0;
                 for (int g = tid; g < NG; g += NT) above += sums[g];
                 above = block_sum(above);
@@ -1195,7 +1338,9 @@ __global__ void __launch_bounds__(Cfg<M>::NT, Cfg<M>::PER_SM) k_sample(SampleArg
                     cut_found = last != 0;
                 }
             }
-            if (cut_found) {
+            if (cut_unsure) {
+                cut_again(~0ull);
+            } else if (cut_found) {
                 cut_at(last);
                 add_listed(sm.list, n_list, last);
                 summed = true;
@@ -1203,7 +1348,7 @@ __global__ void __launch_bounds__(Cfg<M>::NT, Cfg<M>::PER_SM) k_sample(SampleArg
                 reset();
             }
         }
-    if (by_p && !listed && !cut_found) {
+    if (by_p && !listed && !cut_found && !cut_unsure) {
         if (by_k || min_p > 0.f) reset();
         // ---- top-p: exact sums of weights in equal bins of the exponent; tokens so light that all of them together make
         // less than 1 - top_p of the whole are only added up
@@ -1225,27 +1370,24 @@ __global__ void __launch_bounds__(Cfg<M>::NT, Cfg<M>::PER_SM) k_sample(SampleArg
                 if (w >> 30) atomicAdd(&h[2][b], (uint32_t)(w >> 30));
             }
         };
-        auto count4 = [&](const float (&y)[4]) {
-            float z[4];
+        auto spread = [&](auto take) {
+            auto count4 = [&](const float (&x)[4], const float (&w)[4], int id) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                z[e] = y[e];
-                if (y[e] > least) {
-                    count(y[e], Weights::light(y[e]));
-                    z[e] = -INFINITY;
-                }
+                for (int e = 0; e < 4; ++e)
+                    if (take(x[e], id + e, 0.f)) count(weight.exponent(x[e]), Weights::whole(w[e]));
+            };
+            if constexpr (STREAM) {
+                groups([&](int, const float (&x)[4], int id) {
+                    float w[4];
+                    weight.four(x, w);
+                    count4(x, w, id);
+                });
+            } else {
+                weigh_stretch(count4);
             }
-            rest += Weights::light4(z);
         };
-        auto count1 = [&](int, float y, u64 w) { count(y, w); };
-        auto nothing = [](int, const float (&)[4], const float (&)[4]) {};
-        if constexpr (STREAM) {
-            if (bound) weigh(groups, nothing, all_of_them, count4, count1, [](int) {});
-            else weigh(groups, nothing, kept_of_them, count4, count1, [](int) {});
-        } else {
-            if (bound) weigh_stretch(all_of_them, count4, count);
-            else weigh_stretch(kept_of_them, count4, count);
-        }
+        if (bound) spread(all_of_them);
+        else spread(kept_of_them);
         rest = block_sum(rest);
         if (tid < 3) sm.h[0][tid][BINS - 1] = tid == 0 ? (uint32_t)rest & 0x7fffu : tid == 1 ? (uint32_t)(rest >> 15) & 0x7fffu : (uint32_t)(rest >> 30);
         u64 P, before, own_sum;
@@ -1257,26 +1399,30 @@ __global__ void __launch_bounds__(Cfg<M>::NT, Cfg<M>::PER_SM) k_sample(SampleArg
             return at < b;
         });
         n_list = pushed();
-        if (n_list > SORT) cut_at(bisect(P, true));
-        else {
+        if (n_list > SORT) {
+            last = bisect(P, weight_of), cut_unsure = true;   // (how near it is is not known)
+        } else {
             if (rank == 0) {
                 u64 sum;
                 sort(sm.list, n_list);
-                const int m = kept_of(sm.list, n_list, before, [&](u64) { return P; }, sum);
-                if (tid < C) peer(tid).cut = sm.list[m - 1];
+                const int m = kept_of(sm.list, n_list, before, 0, [&](u64) { return P; }, sum);
+                if (tid < C) peer(tid).cut = sm.list[m - 1], peer(tid).cut_unsure = sm.cut_unsure;
             }
             sync();
-            cut_at(sm.cut);
-            add_listed(peer(0).list, n_list, sm.cut);
-            summed = true;
+            last = sm.cut, cut_unsure = sm.cut_unsure;
+            if (!cut_unsure) {
+                cut_at(last);
+                add_listed(peer(0).list, n_list, last);
+                summed = true;
+            }
         }
     }
-    if (!drawn) {
-        // ---- kept weights, group by group; the group and the token that u falls on
-        if (!summed) {
-            if (cut_id == 1 << kIdBits && low == -3.402823466e38f) sum_units(all_of_them);
-            else sum_units(kept_of_them);
-        }
+    if (cut_unsure) {
+        cut_at(exact_cut(last));
+        listed = false;
+    }
+    // The group and the token that u falls on, from the sums of the units and the weights that they are of; the sum of all.
+    auto draw = [&](auto of, auto E_of) {
         __syncthreads();
         const int share = (units + NT - 1) / NT, g0 = min(units, tid * share), g1 = min(units, g0 + share);   // a thread's units
         u64 mine = 0;
@@ -1284,58 +1430,88 @@ __global__ void __launch_bounds__(Cfg<M>::NT, Cfg<M>::PER_SM) k_sample(SampleArg
         const u64 run = block_scan(mine);
         if (tid == NT - 1) sm.total = run;
         __syncthreads();
-        tell(turn, sm.total);
-        u64 first = 0;
-        S = 0;
+        const u64 *const all = tell(sm.total);
+        u64 first = 0, S = 0;
         for (int c = 0; c < C; ++c) {
-            if (c < rank) first += sm.from[turn][c];
-            S += sm.from[turn][c];
+            if (c < rank) first += all[c];
+            S += all[c];
         }
-        if (a.token) {
-            // the first id at which the running sum is above u S
-            const u64 want = __umul64hi(part64(u), S);
-            if (first + run - mine <= want && want < first + run) {
-                u64 at = first + run - mine;
-                int g = g0;
-                while (want >= at + sums[g]) at += sums[g++];
-                sm.at = g, sm.above = at;
-            }
-            const bool here = first <= want && want < first + sm.from[turn][rank];
-            __syncthreads();
-            if (here && warp == 0) {   // as they have been added
-                const int from = sm.at * unit + lane * 4, id = base + from - lead;
-                float x[4], y[4];
-                u64 w[4], large = 0;
-                if constexpr (STREAM) get4(from, x);
-                else four_at(from, min(SL, (sm.at + 1) * unit), x);
-                weight.exponents(x, y);
+        if (!a.token) return S;
+        // the first id at which the running sum is above u S
+        const u64 want = __umul64hi(part64(u), S);
+        if (first + run - mine <= want && want < first + run) {
+            u64 at = first + run - mine;
+            int g = g0;
+            while (want >= at + sums[g]) at += sums[g++];
+            sm.at = g, sm.above = at;
+        }
+        const bool here = first <= want && want < first + all[rank];
+        __syncthreads();
+        if (here && warp == 0) {
+            const int from = sm.at * unit + lane * 4, id = base + from - lead;
+            float x[4];
+            u64 w[4], sum = 0;
+            if constexpr (STREAM) get4(from, x);
+            else four_at(from, min(SL, (sm.at + 1) * unit), x);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) sum += w[e] = kept(x[e], id + e) ? of(x[e]) : 0;
+            u64 at = sm.above + warp_scan(sum) - sum;
+            if (at <= want && want < at + sum) {
+                const u64 E = E_of(S);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    w[e] = kept(x[e], id + e) ? weight(x[e]) : 0;
-                    if (!kept(x[e], id + e) || y[e] >= kLarge) y[e] = -INFINITY, large += w[e];
-                }
-                const u64 sum = large + Weights::light4(y), at = sm.above + warp_scan(sum) - sum;
-                bool mine = at <= want && want < at + sum;
-                if (!__any_sync(~0u, mine)) mine = __clz(__ballot_sync(~0u, sum != 0)) == 31 - lane;
-                if (mine) {   // (the last of any weight, where roundings leave none)
-                    // (four light ones may have a weight together where none has one by itself: the largest kept one, then)
-                    u64 left = want - at;
-                    int t = -1, best = -1;
-                    float most = -INFINITY;
-                    bool found = false;
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        if (w[e] && !found) t = id + e;
-                        if (kept(x[e], id + e) && x[e] > most) best = id + e, most = x[e];
-                        found |= left < w[e];
-                        left -= w[e];
+                    if (at <= want && want < at + w[e]) {
+                        a.token[r] = id + e;
+                        if (want - at < E || at + w[e] - want <= E)
+                            for (int c = 0; c < C; ++c) peer(c).draw_unsure = true;
                     }
-                    a.token[r] = t < 0 ? best : t;
+                    at += w[e];
                 }
             }
         }
+        return S;
+    };
+    // The same by exact weights, where the first ones leave it open.
+    auto draw_exactly = [&] {
+        const int drop = drop_of(S);
+        auto of = [&](float x) { return weight.exact(x, drop); };
+        auto four_of = [&](const float (&x)[4], int id) {
+            float y[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) y[e] = kept(x[e], id + e) ? x[e] : -INFINITY;
+            return weight.exact(y[0], y[1], y[2], y[3], drop);
+        };
+        if constexpr (STREAM) {
+            groups([&](int g, const float (&x)[4], int id) {
+                const u64 sum = warp_sum(four_of(x, id));
+                if (lane == 0) sums[g] = sum;
+            });
+        } else {
+            u64 mine = 0;
+            const int i0 = min(SL, tid * unit), i1 = min(SL, i0 + unit);
+#pragma unroll 1
+            for (int i = i0; i < i1; i += 4) {
+                float x[4];
+                four_at(i, i1, x);
+                mine += four_of(x, base + i - lead);
+            }
+            sums[tid] = mine;
+        }
+        draw(of, [](u64) { return (u64)0; });
+    };
+    if (!drawn) {
+        // ---- kept weights, group by group
+        if (!summed) {
+            if (cut_id == 1 << kIdBits && low == -3.402823466e38f) sum_units(all_of_them);
+            else sum_units(kept_of_them);
+        }
+        S = draw(weight_of, [&](u64 S) { return slack(S, u); });
+        if (ONE || C == 1) {   // (a cluster does it at the end, at its last barrier: its rows are in shared memory)
+            __syncthreads();
+            if (sm.draw_unsure) draw_exactly();
+        }
     }
-    const float inv = kUnits / __ull2float_rn(S);
+    const float inv = (greedy ? kUnits : __ull2float_rn(weight(top))) / __ull2float_rn(S);
     if (p_to || k_to) {
         if (listed || greedy) {   // few tokens
             __syncthreads();      // (the row may be where they go, and is read no more)
@@ -1376,7 +1552,13 @@ __global__ void __launch_bounds__(Cfg<M>::NT, Cfg<M>::PER_SM) k_sample(SampleArg
             }
         }
     }
-    if (!ONE && C > 1) cluster.sync();   // shared memory that others may still read
+    if (!ONE && C > 1) {
+        cluster.sync();   // shared memory that others may still read
+        if (!drawn && sm.draw_unsure) {
+            draw_exactly();
+            cluster.sync();
+        }
+    }
 }
 
 template <Mode M>
