@@ -325,19 +325,24 @@ class DecodeStep:
         self._end, self._room, self._none = z(B), z(B), z(B) - 1
         self._part, self._served = z(B, t=torch.bool), z(B, t=torch.bool)
 
-    def _grow(self, end, slot, offset, stream):
-        """Pages and slots for rows len .. end - 1; len becomes end where the pool had the pages."""
+    def _grow(self, end, slot, offset, stream, rows=None):
+        """Pages and slots for rows len .. end - 1; len becomes end where the pool had the pages (and, with rows, where the request
+        does not shrink and its rows are among the first so many)."""
         api.kv_pages_build(self.pool, end, self.len, slot, offset, status=self.status, stream=stream)
         torch.mul(self.pool.held, api.PAGE_KEYS, out=self._room)
         torch.le(end, self._room, out=self._served)
+        if rows is not None:
+            self._served &= (end >= self.len) & (offset[1:] <= rows)
         torch.where(self._served, end, self.len, out=self.len)
 
     def begin(self, lengths, k, v, stream=None):
         """Rows k, v [T][Hk][d] of prompts, one request's after the other: lengths [B] of them, 0 for requests that stay as
-        they are."""
+        they are. A request whose length is negative, or whose rows are not all among the T, stays as it is too
+        (api.STATUS_INDEX in status)."""
         with torch.cuda.stream(stream or torch.cuda.current_stream(self.len.device)):
             slot = torch.empty(k.shape[0], dtype=torch.int32, device=self.len.device)
-            self._grow(self.len + lengths, slot, None, stream)
+            offset = torch.empty(self.len.numel() + 1, dtype=torch.int32, device=self.len.device)
+            self._grow(self.len + lengths, slot, offset, stream, rows=k.shape[0])
             api.kv_append_slots(self.kv, k, v, slot, self.status, stream)
 
     def end(self, which, stream=None):
