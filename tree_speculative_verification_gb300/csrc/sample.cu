@@ -22,10 +22,11 @@
 //  kStream   a CTA a row, read again from L2, for many filtered long rows: none of
 //            a cluster's barriers, and room for thousands of candidates
 //  kSmall    a small CTA a row, for many short rows
-// One row is a chain of latencies (32000 bf16, top-k and top-p: 10.3 us, of which
+// One row is a chain of latencies (32000 bf16, top-k and top-p: 10.2 us, of which
 // launch and row 4, the cluster's barriers 4); 64 rows of 50272 drawn from the whole
-// distribution 10.3 us; 1024 filtered rows with their distributions 136 us, 45% of
-// the copy rate: issue slots 43%, memory 35%, the passes' latencies in between.
+// distribution 10.9 us; 1024 filtered rows with their distributions 138 us, 44% of
+// the copy rate: the passes' latencies, and issue slots. A row of 50272 that is
+// weighed once more takes some 12 us for it.
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <math.h>
@@ -52,8 +53,8 @@ struct Cfg {
     static constexpr int PER_SM = M == kSmall ? 8 : 2;       // CTAs
 };
 constexpr int kGroup = 128;       // elements of a warp's turn
-// Up to so many rows are taken in an order of their settings (1024 rows of 50272, settings by row and distributions: 136 us and
-// 150; all with top-k 50: 78 and 74).
+// Up to so many rows are taken in an order of their settings (in order and not: settings by row and distributions, 1024 rows of
+// 50272 139 us and 158, 2048 rows 253 and 261; all with top-k 50 80 and 76, 145 and 137).
 constexpr int kOrderedRows = 2048;
 constexpr int kRing = 4;           // groups of a warp in shared memory or on their way there, where rows are read again
 
@@ -1594,21 +1595,21 @@ template <typename T>
 cudaError_t launch_rows(const SampleArgs &a, cudaStream_t s) {
     auto seg = [&](int C) { return ((a.V + 16 / (int)sizeof(T) - 1 + C - 1) / C + kGroup - 1) / kGroup * kGroup; };
     // The fewest CTAs a row whose segments let two of them share an SM (228 KB, of which each takes one for itself); more where
-    // there are few rows: four while nearly all clusters run at once, eight while every CTA has an SM. (With twice as many CTAs
-    // and not, top-k 50: 38 rows of 50272 22.9 and 13.2 us, 76 rows 23.5 and 14.3, 20 rows of 32000 13.0 and 10.8; but 64 rows
-    // of 50272 from the whole distribution, launched one by one, 10.2 and 12.5, with top-p 0.9 24.8 and 27.1.)
+    // there are few rows, while every CTA has an SM. (Two CTAs a row and four, 39 to 65 rows of 50272, from the whole distribution
+    // 10.2 to 11.0 and 10.8 to 11.6 us, top-k 50 13.0 to 13.8 and 13.6 to 14.5, top-p 0.9 30.5 to 31.1 and 29.1 to 30.0, min-p 13.4
+    // to 14.2 and 13.1 to 13.9; 76 rows 16.6 and 19.7, 14.5 and 24.0, 31.9 and 49.1, 15.1 and 21.6; 32000 alike.)
     constexpr size_t kHalf = (228 / 2 - 1) * 1024;
     int C = 1;
     while (C < 8 && smem_of<kCluster>(seg(C), sizeof(T)) > kHalf) C *= 2;
-    // Filtered rows, more than there are SMs: a CTA a row, from L2 (cluster and CTA: 160 rows of 50272 with top-k 50 26 and 22
-    // us, top-p 0.9 59 and 47, settings by row and distributions 57 and 70; 300 rows 33 and 24, 78 and 50, 77 and 77; 1024 rows
-    // 100 and 78, 234 and 143, 179 and 136; 100 rows 16 and 17, 40 and 37, 52 and 63). Not filtered, a row is read from shared
-    // memory (1024 rows 77 and 95 us).
+    // Filtered rows, more than there are SMs: a CTA a row, from L2 (cluster and CTA: 160 rows of 50272 with top-k 50 28 and 23
+    // us, top-p 0.9 65 and 53, settings by row and distributions 58 and 68; 300 rows 35 and 25, 87 and 63, 89 and 93; 1024 rows
+    // 109 and 80, 259 and 163, 190 and 139; 100 rows 17.5 and 18, 42 and 38, 52 and 61). Not filtered, a row is read from shared
+    // memory (300 rows 42 and 54 us, 1024 rows 98 and 102).
     if (C > 1 && a.R > num_sms() && (a.top_k || a.top_p || a.min_p)) return launch_as<T, kStream>(a, 1, seg(1), s);
-    while (C < 8 && 2LL * a.R * C <= (C < 4 ? num_sms() * 17 / 10 : num_sms()) && seg(2 * C) >= 2048) C *= 2;
+    while (C < 8 && 2LL * a.R * C <= num_sms() && seg(2 * C) >= 2048) C *= 2;
     // Short rows, where there are more than the SMs hold at once in large CTAs (small CTAs and large: settings by row and
-    // distributions, 1000 tokens, 300 rows 12.7 and 12.8 us, 1200 rows 16.5 and 41; 4000 tokens, 450 rows 35 and 28, 1200 rows
-    // 45 and 57).
+    // distributions, 1000 tokens, 300 rows 12.3 and 13.0 us, 1200 rows 17 and 46; 4000 tokens, 300 rows 30 and 21.5, 450 rows 31
+    // and 30, 1200 rows 41 and 60).
     if (C == 1 && a.V <= 4096 && (a.V <= 512 || a.R >= num_sms() + a.V / 8)) return launch_as<T, kSmall>(a, 1, seg(1), s);
     return launch_as<T, kCluster>(a, C, seg(C), s);
 }
