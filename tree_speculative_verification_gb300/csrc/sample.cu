@@ -9,7 +9,7 @@
 // Whether a token is kept, and which token a uniform number falls on, are
 // comparisons of sums over a vocabulary: in fp32 a row of 50k tokens is decided
 // wrongly about once in a thousand draws. So sums are whole numbers, whose order
-// does not matter, of weights that are right to 2^-23 of themselves (Weights), and
+// does not matter, of weights that are right to 2^-23.2 of themselves (Weights), and
 // so off by a bound that is known. Where u or top_p falls within that bound of a
 // border (one row of 50k tokens in some four hundred), it is weighed once more, to
 // 2^-43 (exact_sum), and decided by that: as in 64-bit floating point, but for what
@@ -26,7 +26,7 @@
 // launch and row 4, the cluster's barriers 4); 64 rows of 50272 drawn from the whole
 // distribution 10.9 us; 1024 filtered rows with their distributions 138 us, 44% of
 // the copy rate: the passes' latencies, and issue slots. A row of 50272 that is
-// weighed once more takes some 12 us for it.
+// weighed once more takes 8 (alone) to 19 us (with 63 others) for it.
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <math.h>
@@ -145,11 +145,12 @@ __device__ __noinline__ u64 exact_sum(float x0, float x1, float x2, float x3, fl
 
 // 2^(x c - N), c = log2(e) / T = ch + cl and N the whole number next to top c: the weights of all tokens times one number from
 // [0.7, 1.42], which no comparison of their sums sees. x c = n + f, n whole and |f| <= 1/2 (the difference of x ch and n is rounded
-// once, whatever they are), 2^f by a polynomial (interpolated at Chebyshev's points, 2^-26.7 of itself), n in the exponent: to
-// 2^-23.3 of itself. Then as whole numbers of 2^-42, the nearest.
+// once, whatever they are), 2^f by a polynomial (interpolated at Chebyshev's points, 2^-26.7 of itself), n in the exponent. Off by
+// at most: the polynomial and its roundings 2^-23.69 (at every fp32 number), the two roundings of f 2^-25.5, c - ch - cl 2^-28 (at
+// |x c| = 2^22): kOff. Then as whole numbers of 2^-42, the nearest.
 constexpr float kUnits = 4398046511104.f;    // 2^42
 constexpr int kUnitBits = 42;
-constexpr float kOff = 0x1p-23f;
+constexpr float kOff = 0x1.bp-24f;
 constexpr float kMagic = 12582912.f;         // 1.5 * 2^23: a sum with it is a whole number in its lower bits
 // Numbers from [0, 2) as a 2^-20 + b 2^-42, a and b whole, |b| <= 2^21, in the lower bits of sums with these:
 constexpr float kHigh = 0x1.8p3f, kLow = 0x1.8p-19f;
