@@ -153,3 +153,32 @@ def test_cut_in_a_flat_tail(R, V, none, low):
     count = (got["kept"] != -1e30).sum(1).cpu().numpy()
     open_ = math.ceil(2.0 ** -43 * S / w)      # tokens by which 64 bits may be off
     assert (np.abs(count - np.asarray(n)) <= open_).all(), (count[:6], n[:6])
+
+
+@pytest.mark.parametrize("R,V,none", [(3, 50272, {}), (200, 30001, {"m": 0.0}), (700, 1000, {}), (40, 3000, {})])
+@pytest.mark.parametrize("T,low,high", [(1e-6, 9.9999, 10.0), (1e-7, 3.0, 3.000002), (1e-4, -512.0, -511.99), (1e-30, 1.0, 1.0), (3e4, -1e5, 3e5),
+                                        (1e30, -3e30, 2e30), (2e31, -1e32, 3e31), (1e37, -3e38, 3e38), (3e38, -3e38, 3e38)])
+def test_coldest_and_hottest_temperatures(R, V, none, T, low, high):
+    """Temperatures that logits are millions of times, and those near the largest number."""
+    rng = np.random.default_rng(V)
+    x = torch.from_numpy(rng.uniform(low, high, V).astype(np.float32)).cuda()
+    x[V // 2] = high
+    T = np.float32(T)
+    order, w, upto = definition(x, T, 0, 0.0)
+    w = w[w > 0]                                             # (what 64 bits have no weight for)
+    u = near(np.cumsum(np.bincount(order[:len(w)], weights=w.astype(np.float64), minlength=V)) / float(w.sum()), R, rng)
+    want, sure = drawn(order, w, V, u)
+    X, full = x.expand(R, V).contiguous(), {name: [v] * R for name, v in none.items()}
+    got, status = run(X, u, T=[T] * R, **full, want="token")
+    token = got["token"].cpu().numpy()
+    assert status == 0 and (token[sure] == want[sure]).all(), f"{(token != want)[sure].sum()} of {sure.sum()} rows"
+    share = np.concatenate(([0.0], np.cumsum(w)[:-1])) / w.sum()
+    p = np.maximum(near(share, R, rng), np.float32(1e-7))
+    before = np.searchsorted(share, p.astype(np.longdouble), side="left")
+    gap = np.minimum(np.abs(share[np.minimum(before, len(share) - 1)] - p), np.abs(share[before - 1] - p))
+    told = (gap > OPEN) | (before == len(share))
+    got, status = run(X, rng.random(R, dtype=np.float32), T=[T] * R, p=p, **full, want="kept")
+    count = (got["kept"] != -1e30).sum(1).cpu().numpy()
+    # (where the border is the last one that has a weight in 64 bits, tokens without one are kept or not)
+    told &= before < len(share)
+    assert status == 0 and (count[told] == np.maximum(before, 1)[told]).all()

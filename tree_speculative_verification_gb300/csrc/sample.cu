@@ -147,7 +147,8 @@ __device__ __noinline__ u64 exact_sum(float x0, float x1, float x2, float x3, fl
 // [0.7, 1.42], which no comparison of their sums sees. x c = n + f, n whole and |f| <= 1/2 (the difference of x ch and n is rounded
 // once, whatever they are), 2^f by a polynomial (interpolated at Chebyshev's points, 2^-26.7 of itself), n in the exponent. Off by
 // at most: the polynomial and its roundings 2^-23.69 (at every fp32 number), the two roundings of f 2^-25.5, c - ch - cl 2^-28 (at
-// |x c| = 2^22): kOff. Then as whole numbers of 2^-42, the nearest.
+// |x c| = 2^22): kOff. Then as whole numbers of 2^-42, the nearest. Where top c is above that limit, x and top are their distances
+// from top before, exact where they are less than 100 / c; where T is above 2^100, both are times `by` before.
 constexpr float kUnits = 4398046511104.f;    // 2^42
 constexpr int kUnitBits = 42;
 constexpr float kOff = 0x1.bp-24f;
@@ -158,7 +159,7 @@ constexpr uint32_t kHighBits = 0x41400000u, kLowBits = 0x36400000u;
 struct Weights {
     float top, ch, cl, by;   // (top times by: for exact weights, and distributions)
     float floor, magic;      // what is below the former weighs as that, less than a unit; kMagic - N
-    bool slow;               // x c are too large numbers for this: every weight by exact_one
+    float pivot;             // x counts as x by - pivot
     // (x - top) c, rounded; falls with x, or stays
     __device__ __forceinline__ float exponent(float x) const { return __fmul_rn(__fadd_rn(__fmul_rn(x, -by), top), -ch); }
     __device__ __forceinline__ u64 exact(float x0, float x1, float x2, float x3, int drop) const {
@@ -166,15 +167,12 @@ struct Weights {
     }
     __device__ __forceinline__ u64 exact(float x, int drop) const { return exact_one(x, top, ch, cl, by, drop); }
     __device__ __forceinline__ void four(const float (&x)[4], float (&w)[4]) const {
-        if (slow) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) w[e] = __ull2float_rn(exact(x[e], 62 - kUnitBits)) * (1.f / kUnits);
-            return;
-        }
         const u64 h = two(ch, ch), l = two(cl, cl), minus = two(-1.f, -1.f), c = two(magic, magic);
 #pragma unroll
         for (int e = 0; e < 4; e += 2) {
-            const u64 v = two(fmaxf(x[e], floor), fmaxf(x[e + 1], floor)), k = fma2(v, h, c);
+            float y0, y1;
+            one_each(fma2(two(x[e], x[e + 1]), two(by, by), two(-pivot, -pivot)), y0, y1);
+            const u64 v = two(fmaxf(y0, floor), fmaxf(y1, floor)), k = fma2(v, h, c);
             const u64 f = fma2(v, l, fma2(v, h, fma2(k, minus, c)));
             u64 q = fma2(f, two(0x1.4413dcp-13f, 0x1.4413dcp-13f), two(0x1.5f0906p-10f, 0x1.5f0906p-10f));
             q = fma2(f, q, two(0x1.3b2a52p-7f, 0x1.3b2a52p-7f));
@@ -204,7 +202,7 @@ struct Weights {
         return whole(__int_as_float(__float_as_int(q) + (int)((uint32_t)__float_as_int(k) << 23)));
     }
     __device__ __forceinline__ u64 operator()(float x) const {
-        return slow ? whole(__ull2float_rn(exact(x, 62 - kUnitBits)) * (1.f / kUnits)) : one(x, ch, cl, floor, magic);
+        return one(__fmaf_rn(x, by, -pivot), ch, cl, floor, magic);
     }
     // Weights as floats, the largest `one`, to some 2^-21 of themselves.
     __device__ __forceinline__ float real(float x, float one) const {
@@ -542,8 +540,9 @@ __global__ void __launch_bounds__(Cfg<M>::NT, Cfg<M>::PER_SM) k_sample(SampleArg
         return;
     }
     // (4.0e6 is below 2^22: sums with kMagic - N are exact)
-    const bool slow = by != 1.f || !(fabsf(top * ch) < 4.0e6f);
-    const Weights weight{top * by, ch, sm.cl, by, top - 60.f / ch, kMagic - rintf(top * ch), slow};
+    const bool far = !(fabsf(top * by * ch) < 4.0e6f);
+    const float pivot = far ? top * by : 0.f, highest = top * by - pivot;
+    const Weights weight{top * by, ch, sm.cl, by, highest - 100.f / ch, kMagic - rintf(highest * ch), pivot};
     // tokens below this are not kept: min-p (the sum rounded up), and -inf
     float low = -3.402823466e38f;
     if (min_p > 0.f && !greedy) {
