@@ -24,7 +24,7 @@
 //  kSmall    a small CTA a row, for many short rows
 // One row is a chain of latencies (32000 bf16, top-k and top-p: 10.2 us, of which
 // launch and row 4, the cluster's barriers 4); 64 rows of 50272 drawn from the whole
-// distribution 10.9 us; 1024 filtered rows with their distributions 138 us, 44% of
+// distribution 10.9 us; 1024 filtered rows with their distributions 137 us, 44% of
 // the copy rate: the passes' latencies, and issue slots. A row of 50272 that is
 // weighed once more takes 8 (alone) to 19 us (with 63 others) for it.
 #include <cooperative_groups.h>
@@ -1603,8 +1603,8 @@ cudaError_t launch_rows(const SampleArgs &a, cudaStream_t s) {
     while (C < 8 && smem_of<kCluster>(seg(C), sizeof(T)) > kHalf) C *= 2;
     // Filtered rows, more than there are SMs: a CTA a row, from L2 (cluster and CTA: 160 rows of 50272 with top-k 50 28 and 23
     // us, top-p 0.9 65 and 53, settings by row and distributions 58 and 68; 300 rows 35 and 25, 87 and 63, 89 and 93; 1024 rows
-    // 109 and 80, 259 and 163, 190 and 139; 100 rows 17.5 and 18, 42 and 38, 52 and 61). Not filtered, a row is read from shared
-    // memory (300 rows 42 and 54 us, 1024 rows 98 and 102).
+    // 109 and 80, 259 and 163, 190 and 138; 100 rows 17.5 and 18, 42 and 40, 53 and 61). Not filtered, a row is read from shared
+    // memory (100 rows 21 and 27 us, 300 rows 42 and 53, 1024 rows 101 and 100).
     if (C > 1 && a.R > num_sms() && (a.top_k || a.top_p || a.min_p)) return launch_as<T, kStream>(a, 1, seg(1), s);
     while (C < 8 && 2LL * a.R * C <= num_sms() && seg(2 * C) >= 2048) C *= 2;
     // Short rows, where there are more than the SMs hold at once in large CTAs (small CTAs and large: settings by row and
