@@ -6,6 +6,9 @@ import numpy as np
 import pytest
 import torch
 
+from tree_speculative_verification_gb300 import api
+
+from _decode import cu
 from test_gpu_sample import BF16, F32, run
 
 pytestmark = pytest.mark.gpu
@@ -182,3 +185,46 @@ def test_coldest_and_hottest_temperatures(R, V, none, T, low, high):
     # (where the border is the last one that has a weight in 64 bits, tokens without one are kept or not)
     told &= before < len(share)
     assert status == 0 and (count[told] == np.maximum(before, 1)[told]).all()
+
+
+@pytest.mark.parametrize("R,V,dtype,none", LAYOUTS)
+def test_all_outputs_of_rows_at_a_border(R, V, dtype, none):
+    """u and top_p next to borders: distributions and kept logits are those of the cut that is kept, each output alone too."""
+    x, rng = row_of(V, dtype, "normal", V + 3), np.random.default_rng(V)
+    order, w, upto = definition(x, np.float32(1.0), 0, 0.0)
+    share = upto[:-1] / upto[-1]
+    p = np.maximum(near(share[1:], R, rng), np.float32(1e-7))
+    by_id = np.zeros(V, np.longdouble)
+    by_id[order] = w
+    u = near(np.cumsum(by_id) / upto[-1], R, rng)
+    X, kw = x.expand(R, V).contiguous(), {"p": p, **{name: [v] * R for name, v in none.items()}}
+    got, status = run(X, u, **kw)
+    assert status == 0
+    kept = (got["kept"] != -1e30).cpu().numpy()
+    count, probs = kept.sum(1), got["probs"].cpu().numpy().astype(np.float64)
+    for r in range(0, R, max(1, R // 40)):
+        ref = np.zeros(V)
+        ref[order[:count[r]]] = w[:count[r]] / upto[count[r]]
+        assert kept[r, order[:count[r]]].all() and (np.abs(probs[r] - ref) <= 2.0 ** -20 * ref + 1e-37).all()
+        assert kept[r, int(got["token"][r])]
+    for name in got:
+        alone, _ = run(X, u, want=name, **kw)
+        assert torch.equal(alone[name], got[name])
+
+
+@pytest.mark.parametrize("R,V,none", [(60, 50272, {}), (320, 30001, {"m": 0.0}), (2000, 2000, {})])
+def test_kept_in_the_logits_place_at_a_border(R, V, none):
+    """The row is weighed once more although the kept logits go where it was."""
+    x, rng = row_of(V, F32, "normal", V + 4), np.random.default_rng(V)
+    order, w, upto = definition(x, np.float32(1.0), 0, 0.0)
+    share = upto[:-1] / upto[-1]
+    by_id = np.zeros(V, np.longdouble)
+    by_id[order] = w
+    X, u = x.expand(R, V).contiguous(), near(np.cumsum(by_id) / upto[-1], R, rng)
+    for p in (np.full(R, 1.0, np.float32), np.maximum(near(share[1:], R, rng), np.float32(1e-7))):
+        f = lambda a: cu(a, np.float32)
+        m = f([0.0] * R) if none else None
+        want, _ = run(X, u, p=p, m=[0.0] * R if none else None)
+        y, token = X.clone(), torch.zeros(R, dtype=torch.int32, device="cuda")
+        api.sample_tokens(token, y, f(u), top_p=f(p), min_p=m, kept=y)
+        assert torch.equal(y, want["kept"]) and torch.equal(token, want["token"])
