@@ -18,7 +18,7 @@
 // Passes over a row: maximum; where a filter needs it a bound of the candidates
 // for the last token kept, and these; kept weights; output rows. Three layouts:
 //  kCluster  a cluster of CTAs a row, each a segment in shared memory: the row is
-//            read once, the passes cost instructions (some ten an element)
+//            read once, the passes cost instructions (some twenty an element)
 //  kStream   a CTA a row, read again from L2, for many filtered long rows: none of
 //            a cluster's barriers, and room for thousands of candidates
 //  kSmall    a small CTA a row, for many short rows
